@@ -341,6 +341,142 @@ ra_status_t ra_allreduce_bulk_noalloc(const void* const* sendbufs, void* const* 
                                       ra_dtype_t dtype, ra_op_t op, int nranks, int max_sms, int* chunk_status,
                                       void* stream);
 
+/* ==== operators on either side of the gradient all-reduce ====================
+ *
+ * A data-parallel step fills the gradient buffer (backward), reduces it (the
+ * calls above), measures and clips it, and steps the optimiser. The calls
+ * below are the parts of that step that stream memory: layer norm with the
+ * reduction of its weight gradient, the global gradient norm, and AdamW.
+ *
+ * Common rules: as for the collectives. Arguments are checked on the host
+ * before any launch and nothing is enqueued on an error; the library allocates
+ * nothing and keeps no state; work is enqueued on `stream` (NULL = the legacy
+ * default stream) as programmatic dependent launches and can be captured in a
+ * graph. Scratch comes from the caller. dtypes: RA_FLOAT32, RA_FLOAT16,
+ * RA_BFLOAT16 (RA_INT32: RA_ERR_UNSUPPORTED). All arithmetic is fp32, rounded
+ * to nearest even once where a result is stored. Results do not depend on
+ * timing: no sum is taken in an order that varies from run to run on a device.
+ * Pointers must be aligned to their element size; wider alignment is faster.
+ */
+
+/*
+ * Layer norm of `rows` rows of `cols` elements:
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * x, y: dtype, row r at x + r * x_stride elements (strides >= cols).
+ * weight, bias: `cols` elements of weight_dtype (dtype itself or RA_FLOAT32);
+ * NULL weight = ones, NULL bias = zeros. mean, rstd: `rows` floats, kept for
+ * the backward pass; either may be NULL. y may be x (same stride); any other
+ * overlap of an output with another buffer is RA_ERR_ALIAS.
+ * rows == 0 or cols == 0 enqueues nothing.
+ * HBM traffic: reads and writes rows*cols*e.
+ */
+ra_status_t ra_layernorm_forward(const void* x, size_t x_stride, const void* weight, const void* bias, void* y,
+                                 size_t y_stride, float* mean, float* rstd, size_t rows, size_t cols, double eps,
+                                 ra_dtype_t dtype, ra_dtype_t weight_dtype, void* stream);
+
+/*
+ * Its backward pass. With xhat = (x - mean) * rstd and a = dy * weight,
+ *   dx      = rstd * (a - avg_row(a) - xhat * avg_row(a * xhat)),
+ *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy.
+ * mean, rstd: as ra_layernorm_forward stored them. dx: dtype; it may be dy or
+ * x (same stride). dweight, dbias: `cols` elements of weight_dtype, anywhere
+ * (slices of a flat gradient buffer); either may be NULL. accumulate != 0 adds
+ * to what they hold (in fp32, rounded once), 0 overwrites. rows == 0 gives
+ * zero sums. workspace: at least ra_layernorm_workspace(rows, cols) bytes of
+ * device memory, 16-byte aligned, contents irrelevant before and after; only
+ * read or written when dweight or dbias is given, and may be NULL otherwise.
+ * HBM traffic: reads 2*rows*cols*e, writes rows*cols*e.
+ */
+ra_status_t ra_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size_t x_stride,
+                                  const void* weight, const float* mean, const float* rstd, void* dx,
+                                  size_t dx_stride, void* dweight, void* dbias, int accumulate, size_t rows,
+                                  size_t cols, ra_dtype_t dtype, ra_dtype_t weight_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ra_layernorm_backward needs for this shape. Host only. */
+size_t ra_layernorm_workspace(size_t rows, size_t cols);
+
+/*
+ * Global norm of `ntensors` gradient tensors and the factor that clips it:
+ *   out[0] = norm  = sqrt(sum over all elements of (prescale * g)^2),
+ *   out[1] = scale = prescale * min(1, max_norm / (norm + 1e-6)),
+ * or NaN in out[1] if the norm is not finite, which makes ra_adamw leave
+ * everything as it is. prescale undoes a loss scale (1 otherwise); max_norm
+ * may be infinity (no clipping). Squares and sums are fp32 (a |prescale * g|
+ * above 1.8e19 overflows to an infinite norm). out: 2 device floats.
+ * workspace: ra_grad_norm_workspace() bytes of device memory, 16-byte aligned,
+ * set to zero before its first use; every call leaves it ready for the next.
+ * Two calls that may run at once need one each. Tensors of count 0 may be
+ * NULL; no elements at all give norm 0. HBM traffic: reads count*e.
+ */
+ra_status_t ra_grad_norm(const void* const* grads, const size_t* counts, int ntensors, ra_dtype_t dtype,
+                         double prescale, double max_norm, float* out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Bytes of workspace ra_grad_norm needs. Host only. */
+size_t ra_grad_norm_workspace(void);
+
+/* How the two moments of AdamW are held. */
+typedef enum {
+  RA_STATE_F32 = 0, /* exp_avg = m and exp_avg_sq = v, fp32 */
+  RA_STATE_E4M3 = 1 /* 8 bits: exp_avg = m and exp_avg_sq = sqrt(v) as e4m3 values, one byte each, times one
+                       fp32 scale per RA_ADAMW_BLOCK elements (counted from the tensor's start). The
+                       square root halves the dynamic range v would need */
+} ra_state_t;
+#define RA_ADAMW_BLOCK 256
+
+/* One tensor of an AdamW step. */
+typedef struct {
+  void* param;             /* count elements of param_dtype, updated in place */
+  const void* grad;        /* count elements of grad_dtype */
+  void* exp_avg;           /* count floats, or count e4m3 bytes; updated */
+  void* exp_avg_sq;        /* the same */
+  float* exp_avg_scale;    /* RA_STATE_E4M3: ceil(count / RA_ADAMW_BLOCK) floats; ignored otherwise */
+  float* exp_avg_sq_scale; /* the same */
+  void* copy;              /* the updated parameter once more in copy_dtype (NULL: none) */
+  size_t count;            /* 0: the tensor is skipped and its pointers may be NULL */
+  double weight_decay;     /* decoupled, per tensor */
+} ra_adamw_tensor_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;            /* 1 for the first step: the bias corrections are 1 - beta^step */
+  const float* grad_scale; /* device float the gradients are multiplied by (ra_grad_norm's out + 1); NULL = 1.
+                              If it is not finite the step is skipped: nothing is written */
+  ra_state_t state;
+  ra_dtype_t copy_dtype;   /* type of the copies; ignored where there are none */
+  uint64_t seed;           /* RA_STATE_E4M3: seeds the stochastic rounding of the moments */
+} ra_adamw_options_t;
+
+/*
+ * One AdamW step over `ntensors` tensors. Per element, every operation fp32:
+ *   g = grad * grad_scale
+ *   m = beta1 * m + (1 - beta1) * g,   v = beta2 * v + (1 - beta2) * g * g
+ *   param = param * (1 - lr * weight_decay)
+ *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * param is rounded to param_dtype and to copy_dtype from the same fp32 value.
+ * The step uses the fresh fp32 moments; only what is stored of them is 8 bits.
+ *
+ * RA_STATE_E4M3 stores a block's values x as round(x * (448 * (1 / amax))) with
+ * scale amax * (1 / 448), amax the block's largest magnitude (a block whose amax is not
+ * above 2^-100 is stored as zeros with scale 0). Rounding is stochastic: with
+ * nearest rounding a second moment that changes by 0.1% a step would never
+ * leave its 8-bit value. The random bits are a hash of (seed, step, place of
+ * the tensor in the list, place of the element in the tensor), 16 for each
+ * moment, so a step can be repeated exactly. Below e4m3's normal range (2^-15
+ * of the block's amax) rounding is to nearest, and a v that is not zero is not
+ * stored as zero. A NaN or infinity in a block's moments makes the whole block
+ * NaN (nearest what fp32 moments would do; grad_scale avoids it).
+ *
+ * Written buffers must not overlap each other or a gradient (RA_ERR_ALIAS);
+ * gradients may overlap each other. RA_ERR_INVALID_ARG: step < 1, betas
+ * outside [0, 1), eps or lr or weight_decay negative or not finite.
+ * HBM traffic per element: param and moments read and written, grad read.
+ */
+ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, ra_dtype_t param_dtype, ra_dtype_t grad_dtype,
+                     const ra_adamw_options_t* options, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,6 +39,8 @@ def _nvcc() -> str:
 
 SLICE_SOURCE = "ra_launch_op.cu"  # compiled once per (dtype id, op id)
 SLICES = [(dt, op) for dt in range(4) for op in range(5)]
+ADAMW_SLICE_SOURCE = "ra_adamw_slice.cu"  # compiled once per (parameter dtype id, gradient dtype id)
+ADAMW_SLICES = [(p, g) for p in range(3) for g in range(3)]
 
 
 def sources() -> list[tuple[str, str, list[str]]]:
@@ -51,6 +53,9 @@ def sources() -> list[tuple[str, str, list[str]]]:
         if f == SLICE_SOURCE:
             for dt, op in SLICES:
                 out.append((src, f"ra_launch_op_{dt}_{op}.o", [f"-DRA_SLICE_DT={dt}", f"-DRA_SLICE_OP={op}"]))
+        elif f == ADAMW_SLICE_SOURCE:
+            for p, g in ADAMW_SLICES:
+                out.append((src, f"ra_adamw_{p}_{g}.o", [f"-DRA_SLICE_P={p}", f"-DRA_SLICE_G={g}"]))
         else:
             out.append((src, f[:-3] + ".o", []))
     return out

@@ -1,0 +1,182 @@
+// AdamW over many tensors in one launch, moments in fp32 or in 8 bits.
+//
+// Per element (g the scaled gradient, all fp32, every product and sum rounded):
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+// It touches every byte once, so HBM bounds it: 4 + 4 + 2 + 8 + 8 + 2 = 28
+// bytes per element for fp32 parameters and moments with bf16 gradients and
+// copies, 10 for bf16 parameters with 8-bit moments.
+//
+// Work: a warp takes chunks of 256 consecutive elements, 8 per lane. With 8-bit
+// moments a chunk is one block of the scales, so the block's largest magnitude
+// is one warp reduction and the moments never leave registers between being
+// read and being stored again. The tensors' table travels in the kernel's
+// parameters; a CTA finds its tensor by bisection over the tensors' first CTAs.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "ra_kernels.cuh"
+#include "ra_ops.cuh"
+
+namespace ra {
+
+constexpr int kAdamBlock = 256;  // elements per chunk, and per scale of an 8-bit moment
+constexpr int kAdamThreads = 256;
+constexpr int kAdamWarps = kAdamThreads / 32;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
+
+struct AdamTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  void* copy;
+  uint64_t count;
+  float keep;       // 1 - lr * weight_decay
+  uint32_t layout;  // kAdamVec: all buffers can be read in vectors of 8 elements at 8 k - shift; low bits: shift
+};
+constexpr uint32_t kAdamVec = 8;
+
+// Kernel parameters hold at most 32,764 bytes; the small table keeps short lists' launches short.
+constexpr int kAdamSmall = 16;
+constexpr int kAdamLarge = 416;
+
+struct AdamScalars {
+  float b1, one_minus_b1, b2, one_minus_b2, inv_sqrt_bc2, eps, step_size;
+  int n;              // tensors in the table
+  uint32_t key;       // of the random bits
+  uint32_t ordinal0;  // place of table entry 0 in the caller's list
+  int copy_dtype;
+  const float* scale;
+};
+template <int CAP>
+struct AdamArgs {
+  AdamScalars s;
+  uint32_t cta0[CAP];  // first CTA of each tensor
+  AdamTensor t[CAP];
+};
+
+// A 32-bit mix: xor-shifts and multiplications by odd constants (the fractions of e and of the golden ratio).
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0xB7E15163u;
+  x ^= x >> 15;
+  x *= 0x9E3779B9u;
+  return x ^ (x >> 16);
+}
+
+template <int DT>
+__device__ __forceinline__ float load_as_f32(const void* base, uint64_t i) {
+  if constexpr (DT == DT_F32) return __ldcs(static_cast<const float*>(base) + i);
+  else return widen16<DT>(ld_elem<DT>(base, i));
+}
+template <int DT>
+__device__ __forceinline__ void store_f32_as(void* base, uint64_t i, float x) {
+  if constexpr (DT == DT_F32) __stcs(static_cast<float*>(base) + i, x);
+  else st_elem<DT>(base, i, round16<DT>(x));
+}
+__device__ __forceinline__ float load_e4m3(const void* base, uint64_t i) {
+  const __nv_fp8_storage_t b = __ldcs(static_cast<const unsigned char*>(base) + i);
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+}
+
+// |x| * 448 / amax rounded up or down in e4m3's normal range by 16 random bits:
+// the bits below the 3 kept ones of the mantissa decide with their own weight.
+__device__ __forceinline__ float round_e4m3(float x, float inv, uint32_t rand16) {
+  const float t = fminf(fmaxf(__fmul_rn(x, inv), -kE4m3Max), kE4m3Max);
+  return __uint_as_float((__float_as_uint(t) + (rand16 << 4)) & 0xfff00000u);
+}
+
+template <int P, int G, bool S8, int CAP>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
+  pdl_enter();
+  const AdamScalars& s = a.s;
+  float scale = 1.0f;
+  if (s.scale != nullptr) {
+    scale = *s.scale;
+    if (!(fabsf(scale) < __int_as_float(0x7f800000))) return;  // not finite: the step is skipped
+  }
+  int lo = 0, hi = s.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cta0[mid] <= blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const AdamTensor& t = a.t[lo];
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t chunk = (uint64_t)(blockIdx.x - a.cta0[lo]) * kAdamWarps + threadIdx.x / 32;
+  const uint64_t base = chunk * kAdamBlock;
+  if (base >= t.count) return;
+  const uint32_t key = S8 ? mix32(s.key + (s.ordinal0 + (uint32_t)lo) * 0xB7E15163u) : 0;
+
+  float m[8], r[8];
+  float m_scale = 0.0f, r_scale = 0.0f;
+  if (S8) m_scale = t.ms[chunk], r_scale = t.vs[chunk];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint64_t i = base + lane + 32 * j;
+    m[j] = r[j] = 0.0f;
+    if (i >= t.count) continue;
+    const float g = load_as_f32<G>(t.g, i) * scale;
+    float v;
+    if constexpr (S8) {
+      m[j] = load_e4m3(t.m, i) * m_scale;
+      const float root = load_e4m3(t.v, i) * r_scale;
+      v = root * root;
+    } else {
+      m[j] = load_as_f32<DT_F32>(t.m, i);
+      v = load_as_f32<DT_F32>(t.v, i);
+    }
+    m[j] = m[j] * s.b1 + g * s.one_minus_b1;
+    v = v * s.b2 + (g * s.one_minus_b2) * g;
+    r[j] = __fsqrt_rn(v);
+    const float u = __fdiv_rn(m[j], r[j] * s.inv_sqrt_bc2 + s.eps);
+    const float p = load_as_f32<P>(t.p, i) * t.keep - u * s.step_size;
+    store_f32_as<P>(t.p, i, p);
+    if (t.copy != nullptr) {
+      if (s.copy_dtype == DT_F32) store_f32_as<DT_F32>(t.copy, i, p);
+      else if (s.copy_dtype == DT_F16) store_f32_as<DT_F16>(t.copy, i, p);
+      else store_f32_as<DT_BF16>(t.copy, i, p);
+    }
+    if constexpr (!S8) {
+      store_f32_as<DT_F32>(t.m, i, m[j]);
+      store_f32_as<DT_F32>(t.v, i, v);
+    }
+  }
+  if constexpr (S8) {
+    uint32_t m_top = 0, r_top = 0;  // magnitudes as bits: they order as the values do, NaN on top
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m_top = max(m_top, __float_as_uint(m[j]) & 0x7fffffffu);
+      r_top = max(r_top, __float_as_uint(r[j]) & 0x7fffffffu);
+    }
+    const float m_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m_top));
+    const float r_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, r_top));
+    const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
+    const bool m_some = m_amax > kMinAmax, r_some = r_amax > kMinAmax;
+    const bool m_bad = !(m_amax < inf), r_bad = !(r_amax < inf);
+    const float m_inv = m_some ? __frcp_rn(m_amax) * kE4m3Max : 0.0f;
+    const float r_inv = r_some ? __frcp_rn(r_amax) * kE4m3Max : 0.0f;
+    if (lane == 0) {
+      t.ms[chunk] = m_bad ? nan : m_some ? m_amax * (1.0f / kE4m3Max) : 0.0f;
+      t.vs[chunk] = r_bad ? nan : r_some ? r_amax * (1.0f / kE4m3Max) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint64_t i = base + lane + 32 * j;
+      if (i >= t.count) continue;
+      const uint32_t rand = mix32((uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0xB7E15163u + key);
+      const float mq = round_e4m3(m[j], m_inv, rand & 0xffffu);
+      float rq = round_e4m3(r[j], r_inv, rand >> 16);
+      if (r_some && r[j] > 0.0f) rq = fmaxf(rq, 0.001953125f);  // 2^-9, the smallest value above zero
+      static_cast<unsigned char*>(t.m)[i] = m_bad ? 0x7f : __nv_cvt_float_to_fp8(mq, __NV_SATFINITE, __NV_E4M3);
+      static_cast<unsigned char*>(t.v)[i] = r_bad ? 0x7f : __nv_cvt_float_to_fp8(rq, __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+}
+
+}  // namespace ra

@@ -9,6 +9,7 @@
 #include "../../include/ra.h"
 #include "ra_ag.cuh"
 #include "ra_bulk.cuh"
+#include "ra_host.h"
 #include "ra_kernels.cuh"
 #include "ra_order.cuh"
 #include "ra_steps.cuh"
@@ -25,6 +26,17 @@ namespace {
 
 thread_local int g_last_cuda_error = 0;
 
+}  // namespace
+
+ra_status_t ra::cuda_failed(cudaError_t err) {
+  g_last_cuda_error = (int)err;
+  return RA_ERR_CUDA;
+}
+
+namespace {
+
+using ra::cuda_failed;
+
 int elem_size(int dtype) {
   switch (dtype) {
     case RA_FLOAT32: return 4;
@@ -35,17 +47,8 @@ int elem_size(int dtype) {
   }
 }
 
-ra_status_t cuda_failed(cudaError_t err) {
-  g_last_cuda_error = (int)err;
-  return RA_ERR_CUDA;
-}
-
-struct Range {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi) in bytes; empty if lo == hi
-};
-bool overlaps(const Range& a, const Range& b) {
-  return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
+using ra::overlaps;
+using ra::Range;
 
 // ---- launch shapes of the fused kernels ------------------------------------
 // The fused shape for a call, from sweeps on GB300 (fraction of the copy

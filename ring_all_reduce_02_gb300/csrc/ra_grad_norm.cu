@@ -1,0 +1,180 @@
+// ra_grad_norm: the global 2-norm of many gradient tensors and the factor that
+// clips it, in one launch.
+//
+// One read of every element, two operations each: HBM bounds it. Every thread
+// sums squares in fp32 over its share of the tiles, a CTA folds its threads'
+// sums in a fixed tree and writes one partial; the CTA that takes the last
+// ticket adds the partials in a fixed order in fp64, so the result does not
+// depend on the order in which CTAs finish.
+#include <math.h>
+
+#include "ra_host.h"
+#include "ra_kernels.cuh"
+#include "ra_ops.cuh"
+
+namespace ra {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormTile = 4096;       // elements a CTA takes at a time
+constexpr int kNormCtas = 1216;       // CTAs at most, a partial each: 8 on each of 152 SMs
+constexpr int kNormSmall = 32;        // tensors in the small and the large table: kernel parameters hold 32,764 bytes
+constexpr int kNormLarge = 1280;
+
+struct NormWorkspace {
+  uint32_t ticket;  // CTAs that have written their partial; 0 between calls
+  uint32_t pad[3];
+  float partial[kNormCtas];
+};
+
+struct NormScalars {
+  int n;
+  uint32_t tiles;
+  uint32_t written;  // partials that the launches before this one (a longer list of tensors) have written
+  int last;          // this launch writes the result
+  float prescale, max_norm;
+  float* out;
+  NormWorkspace* ws;
+};
+template <int CAP>
+struct NormArgs {
+  NormScalars s;
+  const void* g[CAP];
+  uint64_t count[CAP];
+  uint32_t tile0[CAP];
+};
+
+// The sum over the CTA of one value per thread, in thread 0; the same tree every time.
+template <typename T>
+__device__ __forceinline__ T cta_sum(T x, T* smem) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x / 32] = x;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < kNormThreads / 32; ++w) x += smem[w];
+  return x;
+}
+
+template <int DT, int CAP>
+__global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ NormArgs<CAP> a) {
+  pdl_enter();
+  const NormScalars& s = a.s;
+  __shared__ double sums[kNormThreads / 32];
+  __shared__ bool finish;
+  float acc = 0.0f;
+  for (uint32_t tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
+    int lo = 0, hi = s.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.tile0[mid] <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    const uint64_t begin = (uint64_t)(tile - a.tile0[lo]) * kNormTile;
+    const uint64_t end = min(begin + kNormTile, a.count[lo]);
+    for (uint64_t i = begin + threadIdx.x; i < end; i += kNormThreads) {
+      float x;
+      if constexpr (DT == DT_F32) x = __uint_as_float(ld_elem<DT>(a.g[lo], i));
+      else x = widen16<DT>(ld_elem<DT>(a.g[lo], i));
+      x *= s.prescale;
+      acc = __fmaf_rn(x, x, acc);
+    }
+  }
+  const double mine = cta_sum((double)acc, sums);
+  if (threadIdx.x == 0) {
+    float* slot = &s.ws->partial[blockIdx.x];
+    *slot = (float)(blockIdx.x < s.written ? mine + (double)*slot : mine);
+    finish = false;
+    if (s.last) {
+      __threadfence();
+      finish = atomicAdd(&s.ws->ticket, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!finish) return;
+  __threadfence();
+  double sum = 0.0;
+  for (uint32_t k = threadIdx.x; k < max(s.written, gridDim.x); k += kNormThreads) sum += (double)__ldcg(&s.ws->partial[k]);
+  sum = cta_sum(sum, sums);
+  if (threadIdx.x == 0) {
+    const float norm = (float)sqrt(sum);
+    const float inf = __int_as_float(0x7f800000);
+    s.out[0] = norm;
+    s.out[1] = norm < inf ? s.prescale * fminf(__fdiv_rn(s.max_norm, norm + 1e-6f), 1.0f) : __int_as_float(0x7fffffff);
+    s.ws->ticket = 0;
+  }
+}
+
+}  // namespace ra
+
+namespace {
+
+template <int CAP>
+ra_status_t launch_all(const void* const* grads, const size_t* counts, int ntensors, int dtype, ra::NormScalars s,
+                       cudaStream_t stream) {
+  ra::NormArgs<CAP> a;
+  int i = 0;
+  s.written = 0;
+  do {
+    uint64_t tiles = 0;
+    s.n = 0;
+    for (; i < ntensors && s.n < CAP; ++i) {
+      if (counts[i] == 0) continue;
+      const uint64_t more = ((uint64_t)counts[i] + ra::kNormTile - 1) / ra::kNormTile;
+      if (tiles + more > 0x7fffffffull) {
+        if (s.n == 0) return RA_ERR_UNSUPPORTED;
+        break;
+      }
+      a.g[s.n] = grads[i], a.count[s.n] = counts[i], a.tile0[s.n++] = (uint32_t)tiles;
+      tiles += more;
+    }
+    s.tiles = (uint32_t)tiles;
+    s.last = i == ntensors;
+    const uint64_t ctas = tiles < (uint64_t)ra::kNormCtas ? (tiles ? tiles : 1) : (uint64_t)ra::kNormCtas;
+    a.s = s;
+    cudaError_t err;
+    if (dtype == RA_FLOAT32)
+      err = ra::launch_programmatic(ra::grad_norm_kernel<ra::DT_F32, CAP>, dim3((unsigned)ctas), ra::kNormThreads, 0, stream, a);
+    else if (dtype == RA_FLOAT16)
+      err = ra::launch_programmatic(ra::grad_norm_kernel<ra::DT_F16, CAP>, dim3((unsigned)ctas), ra::kNormThreads, 0, stream, a);
+    else
+      err = ra::launch_programmatic(ra::grad_norm_kernel<ra::DT_BF16, CAP>, dim3((unsigned)ctas), ra::kNormThreads, 0, stream, a);
+    if (err != cudaSuccess) return ra::cuda_failed(err);
+    if (ctas > s.written) s.written = (uint32_t)ctas;
+  } while (i < ntensors);
+  return RA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ra_grad_norm_workspace(void) { return sizeof(ra::NormWorkspace); }
+
+ra_status_t ra_grad_norm(const void* const* grads, const size_t* counts, int ntensors, ra_dtype_t dtype,
+                         double prescale, double max_norm, float* out, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  const ra_status_t st = ra::check_float(dtype);
+  if (st != RA_SUCCESS) return st;
+  if (ntensors < 0 || (ntensors > 0 && (grads == nullptr || counts == nullptr))) return RA_ERR_INVALID_ARG;
+  if (!(max_norm >= 0.0) || !(fabs(prescale) < INFINITY)) return RA_ERR_INVALID_ARG;
+  const uintptr_t w = reinterpret_cast<uintptr_t>(workspace), d = reinterpret_cast<uintptr_t>(out);
+  if (w == 0 || w % 16 || workspace_bytes < sizeof(ra::NormWorkspace) || d == 0 || d % 4) return RA_ERR_INVALID_ARG;
+  const ra::Range ws{w, w + sizeof(ra::NormWorkspace)}, result{d, d + 8};
+  if (ra::overlaps(ws, result)) return RA_ERR_ALIAS;
+  const uint64_t es = (uint64_t)ra::float_size(dtype);
+  for (int i = 0; i < ntensors; ++i) {
+    if (counts[i] == 0) continue;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(grads[i]);
+    if ((uint64_t)counts[i] > RA_MAX_COUNT || p == 0 || p % es || p + counts[i] * es < p) return RA_ERR_INVALID_ARG;
+    const ra::Range g{p, p + (uintptr_t)(counts[i] * es)};
+    if (ra::overlaps(g, ws) || ra::overlaps(g, result)) return RA_ERR_ALIAS;
+  }
+  ra::NormScalars s{};
+  s.prescale = (float)prescale, s.max_norm = (float)max_norm;
+  s.out = out, s.ws = static_cast<ra::NormWorkspace*>(workspace);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return ntensors <= ra::kNormSmall ? launch_all<ra::kNormSmall>(grads, counts, ntensors, dtype, s, cs)
+                                    : launch_all<ra::kNormLarge>(grads, counts, ntensors, dtype, s, cs);
+}
+
+}  // extern "C"

@@ -28,8 +28,11 @@ RA_MAX_RANKS = 64
 EXPORTS = ("ra_allreduce", "ra_reduce_scatter", "ra_allgather", "ra_allreduce_ex", "ra_reduce_scatter_ex",
            "ra_bucket_plan", "ra_allreduce_buckets", "ra_allreduce_ringsteps", "ra_chunk_range", "ra_plan_chunk",
            "ra_status_string", "ra_last_cuda_error", "ra_vector_bytes", "ra_selftest_bulk_timeout",
-           "ra_allreduce_bulk_noalloc")
+           "ra_allreduce_bulk_noalloc", "ra_layernorm_forward", "ra_layernorm_backward", "ra_layernorm_workspace",
+           "ra_grad_norm", "ra_grad_norm_workspace", "ra_adamw")
 ENGINE_CODES = {"registers": 0, "bulk": 1}
+RA_STATE_F32, RA_STATE_E4M3 = 0, 1
+RA_ADAMW_BLOCK = 256  # elements per scale of an 8-bit moment
 
 
 class Options(ctypes.Structure):
@@ -37,6 +40,23 @@ class Options(ctypes.Structure):
 
     _fields_ = [("order", ctypes.c_int), ("accum", ctypes.c_int), ("max_sms", ctypes.c_int),
                 ("engine", ctypes.c_int), ("status", ctypes.c_void_p)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """ra_adamw_tensor_t."""
+
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("count", ctypes.c_size_t),
+                ("weight_decay", ctypes.c_double)]
+
+
+class AdamwOptions(ctypes.Structure):
+    """ra_adamw_options_t."""
+
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("grad_scale", ctypes.c_void_p),
+                ("state", ctypes.c_int), ("copy_dtype", ctypes.c_int), ("seed", ctypes.c_uint64)]
 
 
 def options(order: str = "ring", accum: str = "dtype", max_sms: int = 0, engine: str = "registers",
@@ -99,6 +119,19 @@ def lib() -> ctypes.CDLL:
             L.ra_selftest_bulk_timeout.restype = I
             L.ra_allreduce_bulk_noalloc.argtypes = [PP, PP, SZ, I, I, I, I, VP, VP]
             L.ra_allreduce_bulk_noalloc.restype = I
+            L.ra_layernorm_forward.argtypes = [VP, SZ, VP, VP, VP, SZ, VP, VP, SZ, SZ, ctypes.c_double, I, I, VP]
+            L.ra_layernorm_forward.restype = I
+            L.ra_layernorm_backward.argtypes = [VP, SZ, VP, SZ, VP, VP, VP, VP, SZ, VP, VP, I, SZ, SZ, I, I, VP, SZ,
+                                                VP]
+            L.ra_layernorm_backward.restype = I
+            L.ra_layernorm_workspace.argtypes = [SZ, SZ]
+            L.ra_layernorm_workspace.restype = SZ
+            L.ra_grad_norm.argtypes = [PP, PSZ, I, I, ctypes.c_double, ctypes.c_double, VP, VP, SZ, VP]
+            L.ra_grad_norm.restype = I
+            L.ra_grad_norm_workspace.argtypes = []
+            L.ra_grad_norm_workspace.restype = SZ
+            L.ra_adamw.argtypes = [ctypes.POINTER(AdamwTensor), I, I, I, ctypes.POINTER(AdamwOptions), VP]
+            L.ra_adamw.restype = I
             _lib = L
     return _lib
 
@@ -335,3 +368,216 @@ def ra_allreduce_bulk_noalloc(sendbufs, recvbufs, op: str = "sum", max_sms: int 
                                          ctypes.c_void_p(cs), ctypes.c_void_p(_stream_ptr(stream) or None))
     if st:
         raise RaError(st, "ra_allreduce_bulk_noalloc")
+
+
+# ---- layer norm, gradient norm, AdamW ---------------------------------------
+
+
+def _float_code(t, what: str) -> int:
+    import torch
+
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _matrix(t, what: str, shape=None) -> int:
+    """The row stride of a 2-D CUDA tensor with unit column stride."""
+    if not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be a 2-D CUDA tensor whose rows are contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have the shape {tuple(shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, what: str, n: int, dtype=None) -> int:
+    """The address of a contiguous CUDA tensor of n elements, or 0 for None."""
+    if t is None:
+        return 0
+    if not t.is_cuda or t.numel() != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of {n} elements" +
+                         (f" and type {dtype}" if dtype is not None else ""))
+    return t.data_ptr()
+
+
+def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """Layer norm of the rows of x [rows, cols] into y (which may be x); weight and bias ([cols], of x's type
+    or float32, or None), mean and rstd ([rows] float32, kept for the backward pass, or None)."""
+    import torch
+
+    what = "ra_layernorm_forward"
+    xs, ys = _matrix(x, f"{what}: x"), _matrix(y, f"{what}: y", x.shape)
+    rows, cols = x.shape
+    if y.dtype != x.dtype:
+        raise ValueError(f"{what}: x and y must share one dtype")
+    w = weight if weight is not None else bias
+    wdt = w.dtype if w is not None else x.dtype
+    st = lib().ra_layernorm_forward(x.data_ptr(), xs, _vector(weight, f"{what}: weight", cols, wdt),
+                                    _vector(bias, f"{what}: bias", cols, wdt), y.data_ptr(), ys,
+                                    _vector(mean, f"{what}: mean", rows, torch.float32),
+                                    _vector(rstd, f"{what}: rstd", rows, torch.float32), rows, cols, eps,
+                                    _float_code(x, what), _float_code(w if w is not None else x, what),
+                                    _stream_ptr(stream))
+    if st:
+        raise RaError(st, what)
+
+
+def ra_layernorm_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace ra_layernorm_backward needs."""
+    return lib().ra_layernorm_workspace(rows, cols)
+
+
+def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
+                          accumulate: bool = False, stream=None) -> None:
+    """Gradients of layer norm: dx [rows, cols] (may be dy or x), and the sums over the rows dweight and dbias
+    ([cols], of weight's type; None: not wanted), added to what they hold with ``accumulate``. ``workspace``: a
+    contiguous CUDA tensor of ra_layernorm_workspace(rows, cols) bytes, needed for the sums."""
+    import torch
+
+    what = "ra_layernorm_backward"
+    ds, xs = _matrix(dy, f"{what}: dy", x.shape), _matrix(x, f"{what}: x")
+    gs = _matrix(dx, f"{what}: dx", x.shape)
+    rows, cols = x.shape
+    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+        raise ValueError(f"{what}: x, dy and dx must share one dtype")
+    w = next((t for t in (weight, dweight, dbias) if t is not None), x)
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws, ws_bytes = _vector(workspace, f"{what}: workspace", workspace.numel()), workspace.nbytes
+    st = lib().ra_layernorm_backward(dy.data_ptr(), ds, x.data_ptr(), xs,
+                                     _vector(weight, f"{what}: weight", cols, w.dtype),
+                                     _vector(mean, f"{what}: mean", rows, torch.float32),
+                                     _vector(rstd, f"{what}: rstd", rows, torch.float32), dx.data_ptr(), gs,
+                                     _vector(dweight, f"{what}: dweight", cols, w.dtype),
+                                     _vector(dbias, f"{what}: dbias", cols, w.dtype), int(accumulate), rows, cols,
+                                     _float_code(x, what), _float_code(w, what), ws, ws_bytes, _stream_ptr(stream))
+    if st:
+        raise RaError(st, what)
+
+
+def _same_type(tensors, what: str):
+    dt = tensors[0].dtype if tensors else None
+    for t in tensors:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what}: every tensor must be a contiguous CUDA tensor")
+        if t.dtype != dt:
+            raise ValueError(f"{what}: all tensors must share one dtype")
+
+
+class GradTensors:
+    """A list of gradient tensors, checked once: their addresses and counts, and the tensors themselves (kept
+    alive). Its values are read at every call; the list itself is fixed."""
+
+    def __init__(self, grads):
+        self.tensors = list(grads)
+        _same_type(self.tensors, "grad_tensors")
+        self.dtype = _float_code(self.tensors[0], "grad_tensors") if self.tensors else 0
+        n = len(self.tensors)
+        self.addresses = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.tensors])
+        self.counts = (ctypes.c_size_t * max(n, 1))(*[t.numel() for t in self.tensors])
+
+
+def grad_tensors(grads) -> GradTensors:
+    """The list that ra_grad_norm takes, checked once."""
+    return GradTensors(grads)
+
+
+def ra_grad_norm_workspace() -> int:
+    """Bytes of workspace ra_grad_norm needs (zeroed before its first use)."""
+    return lib().ra_grad_norm_workspace()
+
+
+def ra_grad_norm(grads, max_norm: float, out, workspace, prescale: float = 1.0, stream=None) -> None:
+    """The 2-norm of all gradients (a grad_tensors() list, or tensors of one dtype) into out[0], and the factor
+    that clips it to max_norm into out[1]: out[1:] is ra_adamw's grad_scale. ``workspace``: a CUDA tensor of
+    ra_grad_norm_workspace() bytes, zeroed once."""
+    import torch
+
+    what = "ra_grad_norm"
+    g = grads if isinstance(grads, GradTensors) else GradTensors(grads)
+    st = lib().ra_grad_norm(g.addresses, g.counts, len(g.tensors), g.dtype, prescale, max_norm,
+                            _vector(out, f"{what}: out", 2, torch.float32),
+                            _vector(workspace, f"{what}: workspace", workspace.numel()), workspace.nbytes,
+                            _stream_ptr(stream))
+    if st:
+        raise RaError(st, what)
+
+
+class AdamwTensors:
+    """The tensors of an AdamW step, checked once: the C table of their addresses, counts and weight decays,
+    and the tensors themselves (kept alive)."""
+
+    def __init__(self, params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None,
+                 weight_decay=0.0, copies=None):
+        import torch
+
+        what = "adamw_tensors"
+        params = list(params)
+        n = len(params)
+        lists = {"params": params, "grads": list(grads), "exp_avgs": list(exp_avgs),
+                 "exp_avg_sqs": list(exp_avg_sqs)}
+        eight = exp_avg_scales is not None or exp_avg_sq_scales is not None
+        if eight:
+            if exp_avg_scales is None or exp_avg_sq_scales is None:
+                raise ValueError(f"{what}: 8-bit moments need both lists of scales")
+            lists["exp_avg_scales"], lists["exp_avg_sq_scales"] = list(exp_avg_scales), list(exp_avg_sq_scales)
+        if copies is not None:
+            lists["copies"] = list(copies)
+        decay = list(weight_decay) if hasattr(weight_decay, "__iter__") else [weight_decay] * n
+        if len(decay) != n or any(len(v) != n for v in lists.values()):
+            raise ValueError(f"{what}: every list must have one entry per parameter")
+        for name, tensors in lists.items():
+            _same_type(tensors, f"{what}: {name}")
+            for t, p in zip(tensors, params):
+                want = -(-p.numel() // RA_ADAMW_BLOCK) if name.endswith("scales") else p.numel()
+                if t.numel() != want:
+                    raise ValueError(f"{what}: {name} must match the parameters' sizes")
+        for name in ("exp_avgs", "exp_avg_sqs"):
+            for t in lists[name][:1]:
+                if t.dtype not in ((torch.float8_e4m3fn, torch.uint8) if eight else (torch.float32,)):
+                    raise TypeError(f"{what}: {name} must be " +
+                                    ("float8_e4m3fn or uint8" if eight else "float32") + f", not {t.dtype}")
+        for name in ("exp_avg_scales", "exp_avg_sq_scales"):
+            for t in lists.get(name, [])[:1]:
+                if t.dtype != torch.float32:
+                    raise TypeError(f"{what}: {name} must be float32")
+        self.lists = lists
+        self.state = RA_STATE_E4M3 if eight else RA_STATE_F32
+        self.param_dtype = _float_code(params[0], what) if n else 0
+        self.grad_dtype = _float_code(lists["grads"][0], what) if n else 0
+        self.copy_dtype = _float_code(lists["copies"][0], what) if n and copies is not None else 0
+        self.table = (AdamwTensor * max(n, 1))()
+        fields = (("param", "params"), ("grad", "grads"), ("exp_avg", "exp_avgs"), ("exp_avg_sq", "exp_avg_sqs"),
+                  ("exp_avg_scale", "exp_avg_scales"), ("exp_avg_sq_scale", "exp_avg_sq_scales"), ("copy", "copies"))
+        for field, name in fields:
+            for entry, t in zip(self.table, lists.get(name, ())):
+                setattr(entry, field, t.data_ptr() or None)
+        for entry, p, wd in zip(self.table, params, decay):
+            entry.count, entry.weight_decay = p.numel(), wd
+
+
+def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None,
+                  weight_decay=0.0, copies=None) -> AdamwTensors:
+    """The list that ra_adamw takes, checked once. Moments: float32, or, with both lists of scales
+    (ceil(n / RA_ADAMW_BLOCK) float32 for a tensor of n), float8_e4m3fn (exp_avg_sqs then hold square roots).
+    ``weight_decay``: one number or one per parameter. ``copies``: low-precision copies of the parameters to
+    write along."""
+    return AdamwTensors(params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, weight_decay,
+                        copies)
+
+
+def ra_adamw(tensors: AdamwTensors, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999,
+             eps: float = 1e-8, grad_scale=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over an adamw_tensors() list. ``step`` counts from 1. ``grad_scale``: a float32 CUDA
+    tensor of one element the gradients are multiplied by (out[1:] of ra_grad_norm); not finite: nothing is
+    written. ``seed``: of the stochastic rounding of 8-bit moments."""
+    import torch
+
+    what = "ra_adamw"
+    opts = AdamwOptions(lr, beta1, beta2, eps, step, _vector(grad_scale, f"{what}: grad_scale", 1, torch.float32),
+                        tensors.state, tensors.copy_dtype, seed)
+    st = lib().ra_adamw(tensors.table, len(tensors.lists["params"]), tensors.param_dtype, tensors.grad_dtype,
+                        ctypes.byref(opts), _stream_ptr(stream))
+    if st:
+        raise RaError(st, what)

@@ -41,6 +41,8 @@ SLICE_SOURCE = "ra_launch_op.cu"  # compiled once per (dtype id, op id)
 SLICES = [(dt, op) for dt in range(4) for op in range(5)]
 ADAMW_SLICE_SOURCE = "ra_adamw_slice.cu"  # compiled once per (parameter dtype id, gradient dtype id)
 ADAMW_SLICES = [(p, g) for p in range(3) for g in range(3)]
+LN_SLICE_SOURCE = "ra_layernorm_slice.cu"  # compiled once per (row dtype id, weight dtype id)
+LN_SLICES = [(0, 0), (1, 0), (1, 1), (2, 0), (2, 2)]
 
 
 def sources() -> list[tuple[str, str, list[str]]]:
@@ -56,6 +58,9 @@ def sources() -> list[tuple[str, str, list[str]]]:
         elif f == ADAMW_SLICE_SOURCE:
             for p, g in ADAMW_SLICES:
                 out.append((src, f"ra_adamw_{p}_{g}.o", [f"-DRA_SLICE_P={p}", f"-DRA_SLICE_G={g}"]))
+        elif f == LN_SLICE_SOURCE:
+            for dt, w in LN_SLICES:
+                out.append((src, f"ra_layernorm_{dt}_{w}.o", [f"-DRA_SLICE_DT={dt}", f"-DRA_SLICE_W={w}"]))
         else:
             out.append((src, f[:-3] + ".o", []))
     return out

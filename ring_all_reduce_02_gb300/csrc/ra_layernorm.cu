@@ -4,6 +4,17 @@
 #include "ra_host.h"
 #include "ra_layernorm.cuh"
 
+namespace ra {
+#define RA_DECLARE_LN(DT, W)                                        \
+  cudaError_t ln_forward_##DT##_##W(LnForward a, cudaStream_t s);   \
+  cudaError_t ln_backward_##DT##_##W(LnBackward a, cudaStream_t s);
+RA_DECLARE_LN(0, 0)
+RA_DECLARE_LN(1, 0)
+RA_DECLARE_LN(1, 1)
+RA_DECLARE_LN(2, 0)
+RA_DECLARE_LN(2, 2)
+}  // namespace ra
+
 namespace {
 
 using ra::Range;
@@ -43,28 +54,6 @@ ra_status_t check_types(int dtype, int weight_dtype) {
   if (st == RA_SUCCESS && weight_dtype != dtype && weight_dtype != RA_FLOAT32) st = RA_ERR_UNSUPPORTED;
   return st;
 }
-unsigned row_ctas(uint64_t rows) { return (unsigned)(rows < 152 * 8 ? rows : 152 * 8); }
-
-template <int DT, int WDT>
-cudaError_t forward(const ra::LnForward& a, cudaStream_t s) {
-  return ra::launch_programmatic(ra::ln_forward_rows<DT, WDT>, dim3(row_ctas(a.rows)), ra::kLnThreads, 0, s, a);
-}
-template <int DT, int WDT>
-cudaError_t backward(const ra::LnBackward& a, cudaStream_t s) {
-  const unsigned slices = (unsigned)((a.cols + 31) / 32);
-  if (a.dw || a.db) {  // before dx, which may be x or dy
-    if (a.parts) {
-      const cudaError_t err = ra::launch_programmatic(ra::ln_backward_columns<DT>, dim3(slices, (unsigned)a.parts),
-                                                      ra::kLnThreads, 0, s, a);
-      if (err != cudaSuccess) return err;
-    }
-    const cudaError_t err = ra::launch_programmatic(ra::ln_backward_finish<WDT>, dim3(slices), ra::kLnThreads, 0, s, a);
-    if (err != cudaSuccess) return err;
-  }
-  if (a.rows == 0) return cudaSuccess;
-  return ra::launch_programmatic(ra::ln_backward_rows<DT, WDT>, dim3(row_ctas(a.rows)), ra::kLnThreads, 0, s, a);
-}
-
 }  // namespace
 
 extern "C" {
@@ -95,14 +84,12 @@ ra_status_t ra_layernorm_forward(const void* x, size_t x_stride, const void* wei
     for (int q = 0; q < o; ++q)
       if (overlaps(out[o].at, out[q].at)) return RA_ERR_ALIAS;
   }
-  const ra::LnForward a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, (float)eps};
+  const ra::LnForward a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, (float)eps, 0};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
-  if (dtype == RA_FLOAT32) err = forward<ra::DT_F32, ra::DT_F32>(a, s);
-  else if (dtype == RA_FLOAT16)
-    err = weight_dtype == RA_FLOAT32 ? forward<ra::DT_F16, ra::DT_F32>(a, s) : forward<ra::DT_F16, ra::DT_F16>(a, s);
-  else
-    err = weight_dtype == RA_FLOAT32 ? forward<ra::DT_BF16, ra::DT_F32>(a, s) : forward<ra::DT_BF16, ra::DT_BF16>(a, s);
+  if (dtype == RA_FLOAT32) err = ra::ln_forward_0_0(a, s);
+  else if (dtype == RA_FLOAT16) err = weight_dtype == RA_FLOAT32 ? ra::ln_forward_1_0(a, s) : ra::ln_forward_1_1(a, s);
+  else err = weight_dtype == RA_FLOAT32 ? ra::ln_forward_2_0(a, s) : ra::ln_forward_2_2(a, s);
   return ra::launched(err);
 }
 
@@ -150,15 +137,13 @@ ra_status_t ra_layernorm_backward(const void* dy, size_t dy_stride, const void* 
       if (overlaps(out[o].at, out[q].at)) return RA_ERR_ALIAS;
   }
   ra::LnBackward a{dy, x, weight, mean, rstd, dx, dweight, dbias, static_cast<float*>(workspace), rows, cols,
-                   dy_stride, x_stride, dx_stride, accumulate, 0};
+                   dy_stride, x_stride, dx_stride, accumulate, 0, 0, 0};
   a.parts = (int)(rows < kLnMaxParts ? rows : kLnMaxParts);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
-  if (dtype == RA_FLOAT32) err = backward<ra::DT_F32, ra::DT_F32>(a, s);
-  else if (dtype == RA_FLOAT16)
-    err = weight_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, s) : backward<ra::DT_F16, ra::DT_F16>(a, s);
-  else
-    err = weight_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, s);
+  if (dtype == RA_FLOAT32) err = ra::ln_backward_0_0(a, s);
+  else if (dtype == RA_FLOAT16) err = weight_dtype == RA_FLOAT32 ? ra::ln_backward_1_0(a, s) : ra::ln_backward_1_1(a, s);
+  else err = weight_dtype == RA_FLOAT32 ? ra::ln_backward_2_0(a, s) : ra::ln_backward_2_2(a, s);
   return ra::launched(err);
 }
 

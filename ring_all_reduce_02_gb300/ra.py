@@ -373,54 +373,87 @@ def ra_allreduce_bulk_noalloc(sendbufs, recvbufs, op: str = "sum", max_sms: int 
 # ---- layer norm, gradient norm, AdamW ---------------------------------------
 
 
-def _float_code(t, what: str) -> int:
-    import torch
+_FLOAT_CODES: dict = {}  # torch dtype -> ra_dtype_t, filled by the first call
 
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(t.dtype)
+
+def _float_codes() -> dict:
+    if not _FLOAT_CODES:
+        import torch
+
+        _FLOAT_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    return _FLOAT_CODES
+
+
+def _float_code(t, what: str) -> int:
+    code = _float_codes().get(t.dtype)
     if code is None:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
     return code
 
 
-def _matrix(t, what: str, shape=None) -> int:
-    """The row stride of a 2-D CUDA tensor with unit column stride."""
-    if not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{what} must be a 2-D CUDA tensor whose rows are contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what} must have the shape {tuple(shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _stream_of(t, stream) -> int:
+    """The stream handle a call on tensor t goes to: ``stream``, or torch's current one on t's device (read
+    without building a Stream object, which would cost as much as the launch)."""
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream_ptr(stream)
 
 
-def _vector(t, what: str, n: int, dtype=None) -> int:
-    """The address of a contiguous CUDA tensor of n elements, or 0 for None."""
-    if t is None:
-        return 0
-    if not t.is_cuda or t.numel() != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what} must be a contiguous CUDA tensor of {n} elements" +
-                         (f" and type {dtype}" if dtype is not None else ""))
-    return t.data_ptr()
+def _F32():
+    import torch
+
+    return torch.float32
+
+
+def _is_matrix(t) -> bool:
+    """A 2-D CUDA tensor whose rows are contiguous."""
+    return t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+
+
+def _row_stride(t, cols: int) -> int:
+    return max(t.stride(0), cols) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _is_vector(t, n: int, dtype) -> bool:
+    """A contiguous CUDA tensor of n elements, or None."""
+    return t is None or (t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous())
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_vectors(what: str, **vectors) -> None:
+    """Raises for the first of ``name=(tensor, count, dtype)`` that is not a vector of that kind."""
+    for name, (t, n, dtype) in vectors.items():
+        if not _is_vector(t, n, dtype):
+            raise ValueError(f"{what}: {name} must be a contiguous CUDA tensor of {n} elements of {dtype}")
 
 
 def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
     """Layer norm of the rows of x [rows, cols] into y (which may be x); weight and bias ([cols], of x's type
     or float32, or None), mean and rstd ([rows] float32, kept for the backward pass, or None)."""
-    import torch
-
-    what = "ra_layernorm_forward"
-    xs, ys = _matrix(x, f"{what}: x"), _matrix(y, f"{what}: y", x.shape)
-    rows, cols = x.shape
-    if y.dtype != x.dtype:
-        raise ValueError(f"{what}: x and y must share one dtype")
+    codes = _float_codes()
+    dtype = x.dtype
     w = weight if weight is not None else bias
-    wdt = w.dtype if w is not None else x.dtype
-    st = lib().ra_layernorm_forward(x.data_ptr(), xs, _vector(weight, f"{what}: weight", cols, wdt),
-                                    _vector(bias, f"{what}: bias", cols, wdt), y.data_ptr(), ys,
-                                    _vector(mean, f"{what}: mean", rows, torch.float32),
-                                    _vector(rstd, f"{what}: rstd", rows, torch.float32), rows, cols, eps,
-                                    _float_code(x, what), _float_code(w if w is not None else x, what),
-                                    _stream_ptr(stream))
+    wdtype = dtype if w is None else w.dtype
+    if not (_is_matrix(x) and _is_matrix(y) and x.shape == y.shape and y.dtype is dtype):
+        raise ValueError("ra_layernorm_forward: x and y must be 2-D CUDA tensors of one shape and dtype, rows contiguous")
+    if dtype not in codes or wdtype not in codes:
+        raise TypeError(f"ra_layernorm_forward: unsupported dtype {dtype} with weights of {wdtype}")
+    rows, cols = x.shape
+    f32 = _F32()
+    if not (_is_vector(weight, cols, wdtype) and _is_vector(bias, cols, wdtype) and _is_vector(mean, rows, f32)
+            and _is_vector(rstd, rows, f32)):
+        _check_vectors("ra_layernorm_forward", weight=(weight, cols, wdtype), bias=(bias, cols, wdtype),
+                       mean=(mean, rows, f32), rstd=(rstd, rows, f32))
+    st = (_lib or lib()).ra_layernorm_forward(
+        x.data_ptr(), _row_stride(x, cols), _address(weight), _address(bias), y.data_ptr(), _row_stride(y, cols),
+        _address(mean), _address(rstd), rows, cols, eps, codes[dtype], codes[wdtype], _stream_of(x, stream))
     if st:
-        raise RaError(st, what)
+        raise RaError(st, "ra_layernorm_forward")
 
 
 def ra_layernorm_workspace(rows: int, cols: int) -> int:
@@ -433,27 +466,34 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     """Gradients of layer norm: dx [rows, cols] (may be dy or x), and the sums over the rows dweight and dbias
     ([cols], of weight's type; None: not wanted), added to what they hold with ``accumulate``. ``workspace``: a
     contiguous CUDA tensor of ra_layernorm_workspace(rows, cols) bytes, needed for the sums."""
-    import torch
-
-    what = "ra_layernorm_backward"
-    ds, xs = _matrix(dy, f"{what}: dy", x.shape), _matrix(x, f"{what}: x")
-    gs = _matrix(dx, f"{what}: dx", x.shape)
+    codes = _float_codes()
+    dtype = x.dtype
+    w = weight if weight is not None else dweight if dweight is not None else dbias
+    wdtype = dtype if w is None else w.dtype
+    if not (_is_matrix(x) and _is_matrix(dy) and _is_matrix(dx) and dy.shape == x.shape and dx.shape == x.shape
+            and dy.dtype is dtype and dx.dtype is dtype):
+        raise ValueError("ra_layernorm_backward: x, dy and dx must be 2-D CUDA tensors of one shape and dtype, rows "
+                         "contiguous")
+    if dtype not in codes or wdtype not in codes:
+        raise TypeError(f"ra_layernorm_backward: unsupported dtype {dtype} with weights of {wdtype}")
     rows, cols = x.shape
-    if dy.dtype != x.dtype or dx.dtype != x.dtype:
-        raise ValueError(f"{what}: x, dy and dx must share one dtype")
-    w = next((t for t in (weight, dweight, dbias) if t is not None), x)
-    ws, ws_bytes = 0, 0
-    if workspace is not None:
-        ws, ws_bytes = _vector(workspace, f"{what}: workspace", workspace.numel()), workspace.nbytes
-    st = lib().ra_layernorm_backward(dy.data_ptr(), ds, x.data_ptr(), xs,
-                                     _vector(weight, f"{what}: weight", cols, w.dtype),
-                                     _vector(mean, f"{what}: mean", rows, torch.float32),
-                                     _vector(rstd, f"{what}: rstd", rows, torch.float32), dx.data_ptr(), gs,
-                                     _vector(dweight, f"{what}: dweight", cols, w.dtype),
-                                     _vector(dbias, f"{what}: dbias", cols, w.dtype), int(accumulate), rows, cols,
-                                     _float_code(x, what), _float_code(w, what), ws, ws_bytes, _stream_ptr(stream))
+    f32 = _F32()
+    if mean is None or rstd is None or not (
+            _is_vector(weight, cols, wdtype) and _is_vector(dweight, cols, wdtype) and _is_vector(dbias, cols, wdtype)
+            and _is_vector(mean, rows, f32) and _is_vector(rstd, rows, f32)
+            and (workspace is None or (workspace.is_cuda and workspace.is_contiguous()))):
+        if mean is None or rstd is None:
+            raise ValueError("ra_layernorm_backward: mean and rstd are needed, as ra_layernorm_forward stored them")
+        _check_vectors("ra_layernorm_backward", weight=(weight, cols, wdtype), dweight=(dweight, cols, wdtype),
+                       dbias=(dbias, cols, wdtype), mean=(mean, rows, f32), rstd=(rstd, rows, f32))
+        raise ValueError("ra_layernorm_backward: workspace must be a contiguous CUDA tensor")
+    st = (_lib or lib()).ra_layernorm_backward(
+        dy.data_ptr(), _row_stride(dy, cols), x.data_ptr(), _row_stride(x, cols), _address(weight), mean.data_ptr(),
+        rstd.data_ptr(), dx.data_ptr(), _row_stride(dx, cols), _address(dweight), _address(dbias), accumulate, rows,
+        cols, codes[dtype], codes[wdtype], _address(workspace), 0 if workspace is None else workspace.nbytes,
+        _stream_of(x, stream))
     if st:
-        raise RaError(st, what)
+        raise RaError(st, "ra_layernorm_backward")
 
 
 def _same_type(tensors, what: str):
@@ -492,16 +532,14 @@ def ra_grad_norm(grads, max_norm: float, out, workspace, prescale: float = 1.0, 
     """The 2-norm of all gradients (a grad_tensors() list, or tensors of one dtype) into out[0], and the factor
     that clips it to max_norm into out[1]: out[1:] is ra_adamw's grad_scale. ``workspace``: a CUDA tensor of
     ra_grad_norm_workspace() bytes, zeroed once."""
-    import torch
-
-    what = "ra_grad_norm"
     g = grads if isinstance(grads, GradTensors) else GradTensors(grads)
-    st = lib().ra_grad_norm(g.addresses, g.counts, len(g.tensors), g.dtype, prescale, max_norm,
-                            _vector(out, f"{what}: out", 2, torch.float32),
-                            _vector(workspace, f"{what}: workspace", workspace.numel()), workspace.nbytes,
-                            _stream_ptr(stream))
+    if out is None or not _is_vector(out, 2, _F32()) or not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("ra_grad_norm: out must be a contiguous CUDA tensor of 2 float32, workspace a contiguous CUDA "
+                         "tensor")
+    st = (_lib or lib()).ra_grad_norm(g.addresses, g.counts, len(g.tensors), g.dtype, prescale, max_norm,
+                                      out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_of(out, stream))
     if st:
-        raise RaError(st, what)
+        raise RaError(st, "ra_grad_norm")
 
 
 class AdamwTensors:
@@ -572,12 +610,13 @@ def ra_adamw(tensors: AdamwTensors, lr: float, step: int, beta1: float = 0.9, be
     """One AdamW step over an adamw_tensors() list. ``step`` counts from 1. ``grad_scale``: a float32 CUDA
     tensor of one element the gradients are multiplied by (out[1:] of ra_grad_norm); not finite: nothing is
     written. ``seed``: of the stochastic rounding of 8-bit moments."""
-    import torch
-
-    what = "ra_adamw"
-    opts = AdamwOptions(lr, beta1, beta2, eps, step, _vector(grad_scale, f"{what}: grad_scale", 1, torch.float32),
-                        tensors.state, tensors.copy_dtype, seed)
-    st = lib().ra_adamw(tensors.table, len(tensors.lists["params"]), tensors.param_dtype, tensors.grad_dtype,
-                        ctypes.byref(opts), _stream_ptr(stream))
+    if not _is_vector(grad_scale, 1, _F32()):
+        raise ValueError("ra_adamw: grad_scale must be a CUDA tensor of one float32")
+    params = tensors.lists["params"]
+    if not params:
+        return
+    opts = AdamwOptions(lr, beta1, beta2, eps, step, _address(grad_scale), tensors.state, tensors.copy_dtype, seed)
+    st = (_lib or lib()).ra_adamw(tensors.table, len(params), tensors.param_dtype, tensors.grad_dtype,
+                                  ctypes.byref(opts), _stream_of(params[0], stream))
     if st:
-        raise RaError(st, what)
+        raise RaError(st, "ra_adamw")

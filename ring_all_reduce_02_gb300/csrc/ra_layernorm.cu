@@ -6,7 +6,7 @@
 
 namespace ra {
 #define RA_DECLARE_LN(DT, W)                                        \
-  cudaError_t ln_forward_##DT##_##W(LnForward a, cudaStream_t s);   \
+  cudaError_t ln_forward_##DT##_##W(const LnForward& a, cudaStream_t s);   \
   cudaError_t ln_backward_##DT##_##W(LnBackward a, cudaStream_t s);
 RA_DECLARE_LN(0, 0)
 RA_DECLARE_LN(1, 0)
@@ -19,7 +19,7 @@ namespace {
 
 using ra::Range;
 
-constexpr uint64_t kLnMaxParts = 152;
+using ra::kLnMaxParts;
 
 // Bytes from a matrix's first element to past its last.
 uint64_t extent(uint64_t rows, uint64_t cols, uint64_t stride, uint64_t es) { return ((rows - 1) * stride + cols) * es; }
@@ -84,7 +84,7 @@ ra_status_t ra_layernorm_forward(const void* x, size_t x_stride, const void* wei
     for (int q = 0; q < o; ++q)
       if (overlaps(out[o].at, out[q].at)) return RA_ERR_ALIAS;
   }
-  const ra::LnForward a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, (float)eps, 0};
+  const ra::LnForward a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, (float)eps};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (dtype == RA_FLOAT32) err = ra::ln_forward_0_0(a, s);

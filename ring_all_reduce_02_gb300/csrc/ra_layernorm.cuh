@@ -22,8 +22,10 @@ struct LnForward {
   float* rstd;
   uint64_t rows, cols, x_stride, y_stride;
   float eps;
-  uint32_t group;  // threads per row of the register kernel
 };
+
+// Partial sums of the weight's gradient, at most: one per SM. A multiple of 8, see ln_backward_fused.
+constexpr uint64_t kLnMaxParts = 152;
 
 struct LnBackward {
   const void* dy;
@@ -67,32 +69,62 @@ __device__ __forceinline__ float cta_sum_all(float x, float* smem) {
   return x;
 }
 
-// ---- rows in registers ------------------------------------------------------
-// A group of `group` threads (a power of two from 32) takes a row, each thread
-// E of its columns: vectors of V elements (16 bytes), or single elements where
-// alignment or an odd row length rules vectors out. Thread t's j-th vector is
-// the (j group + t)-th of the row, so a warp's accesses are contiguous.
-// 16 bytes of DT, or one element, as fp32.
-template <int DT, int V>
-__device__ __forceinline__ void widen(const uint4& q, float* f) {
+// ---- pairs of fp32 ------------------------------------------------------------
+// sm_103a adds, multiplies and fuses two fp32 at a time (each rounded as the
+// scalar operation is). At 4 to 6 bytes of HBM traffic per 16-bit element an SM
+// has about 25 to 35 issue slots per element, so pairs are what keeps these
+// kernels bound by memory.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(F2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float fold2(F2 p) {
+  float a, b;
+  split(p, a, b);
+  return a + b;
+}
+
+// 16 bytes of DT as pairs of fp32, and back.
+template <int DT>
+__device__ __forceinline__ void widen(const uint4& q, F2* f) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(w[k]);
+    f[0] = pair(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    f[1] = pair(__uint_as_float(w[2]), __uint_as_float(w[3]));
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if constexpr (DT == DT_F16) {
         const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-        f[2 * k] = p.x, f[2 * k + 1] = p.y;
+        f[k] = pair(p.x, p.y);
       } else {
-        f[2 * k] = __uint_as_float(w[k] << 16), f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        f[k] = pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
       }
     }
   }
 }
 template <int DT>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+__device__ __forceinline__ uint32_t narrow2(F2 p) {
+  float a, b;
+  split(p, a, b);
   if constexpr (DT == DT_F16) {
     const __half2 h = __float22half2_rn(make_float2(a, b));
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -102,25 +134,22 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b) {
   }
 }
 template <int DT>
-__device__ __forceinline__ uint4 narrow(const float* f) {
-  if constexpr (DT == DT_F32)
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  else
-    return make_uint4(narrow2<DT>(f[0], f[1]), narrow2<DT>(f[2], f[3]), narrow2<DT>(f[4], f[5]), narrow2<DT>(f[6], f[7]));
-}
-// V elements at element i of a weight vector, through L1: every row reads them again.
-template <int DT, int V>
-__device__ __forceinline__ void load_weights(const void* base, uint64_t i, float* f) {
-  constexpr int es = Elem<DT>::kSize;
-  const char* p = static_cast<const char*>(base) + i * es;
-  if constexpr (V == 1) {
-    if constexpr (DT == DT_F32) f[0] = __ldg(reinterpret_cast<const float*>(p));
-    else f[0] = widen16<DT>(__ldg(reinterpret_cast<const unsigned short*>(p)));
+__device__ __forceinline__ uint4 narrow(const F2* f) {
+  if constexpr (DT == DT_F32) {
+    float a, b, c, d;
+    split(f[0], a, b), split(f[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   } else {
-    constexpr int per = 16 / es;
-#pragma unroll
-    for (int k = 0; k < V / per; ++k) widen<DT, per>(__ldg(reinterpret_cast<const uint4*>(p) + k), f + k * per);
+    return make_uint4(narrow2<DT>(f[0]), narrow2<DT>(f[1]), narrow2<DT>(f[2]), narrow2<DT>(f[3]));
   }
+}
+// V weights from element i, through L1: every row reads them again.
+template <int DT, int V>
+__device__ __forceinline__ void load_weights(const void* base, uint32_t i, F2* f) {
+  constexpr int es = Elem<DT>::kSize, per = 16 / es;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + (uint64_t)i * es);
+#pragma unroll
+  for (int k = 0; k < V / per; ++k) widen<DT>(__ldg(p + k), f + k * (per / 2));
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -128,82 +157,223 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// All threads of a row's group (a named barrier of its own, or the warp).
-__device__ __forceinline__ void group_sync(uint32_t g, uint32_t size) {
-  if (size == 32) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
-}
-// The sum over a group, in all its threads, in a fixed order. `slots`: one float per warp of the CTA; the
-// caller alternates between two sets, so one barrier is enough.
-__device__ __forceinline__ float group_sum(float x, uint32_t g, uint32_t size, float* slots) {
-  x = warp_sum(x);
-  if (size == 32) return x;
-  const uint32_t warps = size / 32, first = g * warps;
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = x;
-  group_sync(g, size);
-  x = (threadIdx.x & 31) < warps ? slots[first + (threadIdx.x & 31)] : 0.0f;
-  return warp_sum(x);
-}
 
 constexpr uint32_t kLnMaxThreads = 512;
+constexpr uint32_t kLnWarpThreads = 128;  // of a CTA with a row to each warp
 
-template <int DT, int WDT, int E, bool VECTOR>
-__global__ void __launch_bounds__(kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
+// ---- forward, rows in registers ---------------------------------------------------
+// A group of threads takes a row, each of them E of its columns in vectors of
+// 16 bytes: thread t's j-th vector is the (j group + t)-th of the row. WARP: a
+// row to each warp of a CTA; otherwise the CTA is one row's group (named
+// barriers for several groups would hold 16 of an SM's 64 barriers per CTA and
+// so allow only 4 CTAs on it).
+template <int DT, int WDT, int E, bool WARP>
+__global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
   pdl_enter();
-  constexpr int es = Elem<DT>::kSize, V = VECTOR ? 16 / es : 1, NV = E / V;
+  constexpr int es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   __shared__ float slots[2][kLnMaxThreads / 32];
-  const uint32_t g = threadIdx.x / a.group, t = threadIdx.x - g * a.group;
-  const uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / a.group) + g;
+  const uint32_t group = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const uint64_t row = WARP ? (uint64_t)blockIdx.x * (kLnWarpThreads / 32) + threadIdx.x / 32 : blockIdx.x;
   if (row >= a.rows) return;  // a whole group
-  const uint32_t cols = (uint32_t)a.cols, step = a.group * V;
+  const uint32_t cols = (uint32_t)a.cols, step = group * V;
+  const auto group_sum = [&](float v, float* s) {
+    v = warp_sum(v);
+    if constexpr (!WARP) {
+      if ((t & 31) == 0) s[t / 32] = v;
+      __syncthreads();
+      v = warp_sum((t & 31) < group / 32 ? s[t & 31] : 0.0f);
+    }
+    return v;
+  };
   const char* x = static_cast<const char*>(a.x) + row * a.x_stride * es;
   char* y = static_cast<char*>(a.y) + row * a.y_stride * es;
-  float f[E];
-  float sum = 0.0f;
+  uint4 q[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const uint32_t c = j * step + t * V;
-    if (c < cols) {
-      if constexpr (VECTOR) widen<DT, V>(__ldcs(reinterpret_cast<const uint4*>(x + (uint64_t)c * es)), f + j * V);
-      else f[j] = ln_load<DT>(x, c);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[j * V + k] = 0.0f;
-    }
+    q[j] = c < cols ? __ldcs(reinterpret_cast<const uint4*>(x + c * es)) : make_uint4(0, 0, 0, 0);
   }
+  F2 f[E / 2], sum = 0;
 #pragma unroll
-  for (int k = 0; k < E; ++k) sum += f[k];
+  for (int j = 0; j < NV; ++j) {
+    widen<DT>(q[j], f + j * H);
+#pragma unroll
+    for (int k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
+  }
   const float n = (float)cols;
-  const float mean = __fdiv_rn(group_sum(sum, g, a.group, slots[0]), n);  // divided: a constant row's mean is exact
-  float sq = 0.0f;
+  const float mean = __fdiv_rn(group_sum(fold2(sum), slots[0]), n);  // divided: a constant row's mean is exact
+  const F2 minus = pair(-mean, -mean);
+  F2 sq = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const bool in = j * step + t * V < cols;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      f[j * V + k] -= mean;
-      if (in) sq = __fmaf_rn(f[j * V + k], f[j * V + k], sq);
+    for (int k = 0; k < H; ++k) {
+      F2& d = f[j * H + k];
+      d = add2(d, minus);
+      if (in) sq = fma2(d, d, sq);
     }
   }
-  const float var = __fdiv_rn(group_sum(sq, g, a.group, slots[1]), n);
+  const float var = __fdiv_rn(group_sum(fold2(sq), slots[1]), n);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+  const F2 rstd2 = pair(rstd, rstd);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const uint32_t c = j * step + t * V;
     if (c >= cols) continue;
-    float w[V], b[V], out[V];
+    F2 w[H], b[H];
+    if (a.w) {
+      load_weights<WDT, V>(a.w, c, w);
+    } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) w[k] = 1.0f, b[k] = 0.0f;
-    if (a.w) load_weights<WDT, V>(a.w, c, w);
-    if (a.b) load_weights<WDT, V>(a.b, c, b);
+      for (int k = 0; k < H; ++k) w[k] = pair(1.0f, 1.0f);
+    }
+    if (a.b) {
+      load_weights<WDT, V>(a.b, c, b);
+    } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) out[k] = __fmaf_rn(f[j * V + k] * rstd, w[k], b[k]);
-    if constexpr (VECTOR) __stcs(reinterpret_cast<uint4*>(y + (uint64_t)c * es), narrow<DT>(out));
-    else ln_store<DT>(y, c, out[0]);
+      for (int k = 0; k < H; ++k) b[k] = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < H; ++k) w[k] = fma2(mul2(f[j * H + k], rstd2), w[k], b[k]);
+    __stcs(reinterpret_cast<uint4*>(y + c * es), narrow<DT>(w));
   }
   if (t == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
+// ---- rows off the 16-byte grid ---------------------------------------------------------
+// A row of an odd length starts somewhere inside a 16-byte line. Its lines are
+// read and written whole all the same: a thread's k-th line holds the row's
+// elements V k - phase .. V k - phase + V - 1, and what lies outside the row is
+// masked. Only the weights have to be shifted to a row's phase: they stand in
+// shared memory with one gap after every V, where a warp's reads of one
+// position in 32 consecutive lines fall on different banks whatever the phase.
+__device__ __forceinline__ uint32_t line_phase(const void* p, uint32_t es) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / es;
+}
+template <uint32_t V>
+__host__ __device__ constexpr uint32_t gapped(uint32_t i) { return i + i / V; }
+// Elements of the gapped array of `cols` weights: V of them precede column 0.
+template <uint32_t V>
+__host__ __device__ constexpr uint32_t gapped_size(uint32_t cols) { return gapped<V>(cols + 2 * V); }
+
+// Line `at` of the matrix [base, end), element by element where it is not all inside it.
+template <int DT>
+__device__ __forceinline__ uint4 load_line(const char* at, const char* base, const char* end) {
+  if (at >= base && at + 16 <= end) return __ldcs(reinterpret_cast<const uint4*>(at));
+  constexpr uint32_t es = Elem<DT>::kSize;
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (uint32_t k = 0; k < 16 / es; ++k) {
+    const char* p = at + k * es;
+    if (p >= base && p < end) w[k * es / 4] |= ld_elem<DT>(p, 0) << (k * es % 4 * 8);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The first `from` and all from `to` on of a line's V values set to zero.
+template <uint32_t V>
+__device__ __forceinline__ void mask_line(F2* f, int from, int to) {
+#pragma unroll
+  for (int k = 0; k < (int)V / 2; ++k) {
+    float u, v;
+    split(f[k], u, v);
+    f[k] = pair(2 * k >= from && 2 * k < to ? u : 0.0f, 2 * k + 1 >= from && 2 * k + 1 < to ? v : 0.0f);
+  }
+}
+// Values [from, to) of a line, one by one.
+template <int DT>
+__device__ __forceinline__ void store_part(char* at, const uint4& q, int from, int to) {
+  constexpr uint32_t es = Elem<DT>::kSize;
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int k = 0; k < (int)(16 / es); ++k)
+    if (k >= from && k < to) st_elem<DT>(at, k, es == 4 ? w[k] : (w[k / 2] >> (k % 2 * 16)) & 0xffffu);
+}
+
+// Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on.
+template <int DT, int WDT, int E>
+__global__ void __launch_bounds__(kLnMaxThreads) ln_forward_shifted(const __grid_constant__ LnForward a) {
+  pdl_enter();
+  constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float slots[2][2][kLnMaxThreads / 32];
+  float2* wb = reinterpret_cast<float2*>(smem);
+  const uint32_t cols = (uint32_t)a.cols, t = threadIdx.x, group = blockDim.x;
+  const char* base = static_cast<const char*>(a.x);
+  const char* end = base + ((a.rows - 1) * a.x_stride + cols) * es;
+  uint4 q[NV];
+  const auto fetch = [&](uint64_t row) {
+    const char* x = base + row * a.x_stride * es;
+    const uint32_t phase = line_phase(x, es);
+#pragma unroll
+    for (uint32_t j = 0; j < NV; ++j) {
+      const uint32_t k = j * group + t;
+      q[j] = k * V < phase + cols ? load_line<DT>(x + ((int)(k * V) - (int)phase) * (int)es, base, end) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch(blockIdx.x);
+  for (uint32_t c = t; c < cols; c += group)
+    wb[gapped<V>(c + V)] = make_float2(a.w ? ln_load<WDT>(a.w, c) : 1.0f, a.b ? ln_load<WDT>(a.b, c) : 0.0f);
+  __syncthreads();
+  const float n = (float)cols;
+  uint32_t parity = 0;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const uint32_t phase = line_phase(base + row * a.x_stride * es, es);
+    const auto group_sum = [&](float v, float* s) {
+      v = warp_sum(v);
+      if ((t & 31) == 0) s[t / 32] = v;
+      __syncthreads();
+      return warp_sum((t & 31) < group / 32 ? s[t & 31] : 0.0f);
+    };
+    F2 f[E / 2], sum = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < NV; ++j) {
+      const int at = (int)((j * group + t) * V) - (int)phase;  // column of the line's first value
+      widen<DT>(q[j], f + j * H);
+      if (at < 0 || at + (int)V > (int)cols) mask_line<V>(f + j * H, -at, (int)cols - at);
+#pragma unroll
+      for (uint32_t k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
+    }
+    if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+    const float mean = __fdiv_rn(group_sum(fold2(sum), slots[parity][0]), n);
+    const F2 minus = pair(-mean, -mean);
+    F2 sq = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < NV; ++j) {
+      const int at = (int)((j * group + t) * V) - (int)phase;
+#pragma unroll
+      for (uint32_t k = 0; k < H; ++k) f[j * H + k] = add2(f[j * H + k], minus);
+      if (at < 0 || at + (int)V > (int)cols) mask_line<V>(f + j * H, -at, (int)cols - at);
+#pragma unroll
+      for (uint32_t k = 0; k < H; ++k) sq = fma2(f[j * H + k], f[j * H + k], sq);
+    }
+    const float var = __fdiv_rn(group_sum(fold2(sq), slots[parity][1]), n);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+    const F2 rstd2 = pair(rstd, rstd);
+    char* y = static_cast<char*>(a.y) + row * a.y_stride * es;
+#pragma unroll
+    for (uint32_t j = 0; j < NV; ++j) {
+      const uint32_t k0 = j * group + t;
+      const int at = (int)(k0 * V) - (int)phase;
+      if (at >= (int)cols) continue;
+      const float2* near = wb + (V + 1) * k0 + V - phase;  // value e's weights: one further on from e = phase on
+#pragma unroll
+      for (uint32_t k = 0; k < H; ++k) {
+        const float2 u = near[2 * k + (2 * k >= phase)], v = near[2 * k + 1 + (2 * k + 1 >= phase)];
+        f[j * H + k] = fma2(mul2(f[j * H + k], rstd2), pair(u.x, v.x), pair(u.y, v.y));
+      }
+      const uint4 out = narrow<DT>(f + j * H);
+      if (at >= 0 && at + (int)V <= (int)cols) __stcs(reinterpret_cast<uint4*>(y + at * (int)es), out);
+      else store_part<DT>(y + at * (int)es, out, -at, (int)cols - at);
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    parity ^= 1;
   }
 }
 
@@ -213,6 +383,10 @@ __global__ void __launch_bounds__(kLnMaxThreads) ln_forward_registers(const __gr
 // column sums of dy xhat and dy stay in registers over all the rows of a group:
 // x and dy are read once. The CTA folds its groups' sums and writes one partial
 // of each; ln_backward_finish adds the partials.
+//
+// SHIFTED: rows off the 16-byte grid, by whole lines as above. The rows of one
+// group are a multiple of 8 apart, so all of them have the same phase and a
+// register keeps standing for the same column.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // copies `bytes` (0 to 16) and fills up with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -223,55 +397,57 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Bytes of one row's buffer in shared memory: single-element rows keep their offset in a 16-byte line.
-__host__ __device__ constexpr uint32_t ln_row_bytes(uint32_t cols, uint32_t es, bool vector) {
-  return (cols * es + (vector ? 0 : 16) + 15) / 16 * 16;
+// All threads of a row's group: a named barrier of its own, or the warp.
+__device__ __forceinline__ void group_sync(uint32_t g, uint32_t size) {
+  if (size == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
 }
 
-template <int DT, int WDT, int E, bool VECTOR>
+// Bytes of one row's lines, and of the weights, in shared memory.
+__host__ __device__ constexpr uint32_t ln_row_bytes(uint32_t cols, uint32_t es, bool shifted) {
+  return (cols * es + (shifted ? 16 - es : 0) + 15) / 16 * 16;
+}
+__host__ __device__ constexpr uint32_t ln_weight_bytes(uint32_t cols, uint32_t es, bool shifted) {
+  return ((shifted ? (es == 2 ? gapped_size<8>(cols) : gapped_size<4>(cols)) : cols) * 4 + 15) / 16 * 16;
+}
+
+template <int DT, int WDT, int E, bool SHIFTED>
 __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __grid_constant__ LnBackward a) {
   pdl_enter();
-  constexpr uint32_t es = Elem<DT>::kSize, V = VECTOR ? 16 / es : 1, NV = E / V;
+  constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
   __shared__ float slots[2][2][kLnMaxThreads / 32];
   const uint32_t cols = (uint32_t)a.cols, size = a.group, groups = kLnMaxThreads / size, stages = a.stages;
-  const uint32_t g = threadIdx.x / size, t = threadIdx.x - g * size, step = size * V;
-  const uint32_t row_bytes = ln_row_bytes(cols, es, VECTOR);
+  const uint32_t g = threadIdx.x / size, t = threadIdx.x - g * size;
+  const uint32_t row_bytes = ln_row_bytes(cols, es, SHIFTED);
   float* weights = reinterpret_cast<float*>(smem);
-  char* ring = smem + (cols * 4 + 15) / 16 * 16 + (size_t)g * stages * 2 * row_bytes;
+  char* ring = smem + ln_weight_bytes(cols, es, SHIFTED) + (size_t)g * stages * 2 * row_bytes;
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  for (uint32_t c = threadIdx.x; c < cols; c += kLnMaxThreads) weights[c] = a.w ? ln_load<WDT>(a.w, c) : 1.0f;
-  __syncthreads();
 
   const char* xs = static_cast<const char*>(a.x);
   const char* dys = static_cast<const char*>(a.dy);
   // few rows spread over the CTAs first, then over their groups
   const uint64_t first = (uint64_t)g * gridDim.x + blockIdx.x, stride = (uint64_t)gridDim.x * groups;
+  const uint32_t phase = SHIFTED ? line_phase(xs + first * a.x_stride * es, es) : 0;
+  const uint32_t lines = (phase + cols + V - 1) / V;
   const char* x_end = xs + ((a.rows - 1) * a.x_stride + cols) * es;
   const char* dy_end = dys + ((a.rows - 1) * a.dy_stride + cols) * es;
-  // Copies a row into a buffer. Single-element rows: the 16-byte lines that hold it, none read outside the matrix.
   const auto fetch_row = [&](uint32_t dst, const char* base, const char* end, const char* row) {
-    if constexpr (VECTOR) {
+    const char* line0 = row - phase * es;
 #pragma unroll
-      for (uint32_t j = 0; j < NV; ++j) {
-        const uint32_t c = j * step + t * V;
-        if (c < cols) cp_async16(dst + c * es, row + (uint64_t)c * es, 16);
-      }
-    } else {
-      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
-      const char* line0 = row - off;
-      for (uint32_t k = t; k * 16 < off + cols * es; k += size) {
-        const char* line = line0 + k * 16;
-        if (line >= base) {
-          const uint64_t left = (uint64_t)(end - line);
-          cp_async16(dst + k * 16, line, left < 16 ? (uint32_t)left : 16);
-        } else {  // the matrix starts inside this line
-          for (uint32_t b = off; b < 16 && b < off + cols * es; b += es) {
-            const uint32_t bits = ld_elem<DT>(row, (b - off) / es);
-            if constexpr (es == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + b), "r"(bits) : "memory");
-            else asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + b), "h"((unsigned short)bits) : "memory");
-          }
-        }
+    for (uint32_t j = 0; j < NV; ++j) {
+      const uint32_t k = j * size + t;
+      if (k >= lines) continue;
+      const char* line = line0 + k * 16;
+      if constexpr (!SHIFTED) {
+        cp_async16(dst + k * 16, line, 16);
+      } else if (line >= base) {
+        const uint64_t left = (uint64_t)(end - line);
+        cp_async16(dst + k * 16, line, left < 16 ? (uint32_t)left : 16);
+      } else {  // the matrix starts inside this line
+        const uint4 q = load_line<DT>(line, base, end);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + k * 16), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                     : "memory");
       }
     }
   };
@@ -282,66 +458,71 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     }
     cp_async_commit();
   };
-  float dw[E], db[E];
-#pragma unroll
-  for (int k = 0; k < E; ++k) dw[k] = db[k] = 0.0f;
-  const float inv_n = 1.0f / (float)cols;
   for (uint32_t s = 0; s + 1 < stages; ++s) fetch(s, first + s * stride);
   float mean = 0.0f, rstd = 0.0f;
   if (first < a.rows) mean = __ldg(a.mean + first), rstd = __ldg(a.rstd + first);
+  for (uint32_t c = threadIdx.x; c < cols; c += kLnMaxThreads)
+    weights[SHIFTED ? gapped<V>(c + V) : c] = a.w ? ln_load<WDT>(a.w, c) : 1.0f;
+  __syncthreads();
+
+  F2 dw[E / 2], db[E / 2];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) dw[k] = db[k] = 0;
+  const float inv_n = 1.0f / (float)cols;
   uint32_t stage = 0, parity = 0;
   for (uint64_t row = first; row < a.rows; row += stride) {
     if (stages == 2) cp_async_wait<0>();
     else if (stages == 3) cp_async_wait<1>();
     else cp_async_wait<2>();
-    if constexpr (!VECTOR) group_sync(g, size);  // the row was copied by all; and all are done with the one before
+    // every thread reads back the lines it fetched itself, so nothing else has to be waited for
     fetch(stage == 0 ? stages - 1 : stage - 1, row + (stages - 1) * stride);
     float next_mean = 0.0f, next_rstd = 0.0f;
     if (row + stride < a.rows) next_mean = __ldg(a.mean + row + stride), next_rstd = __ldg(a.rstd + row + stride);
 
     const char* sx = ring + stage * 2 * row_bytes;
-    const char* sdy = sx + row_bytes;
-    if constexpr (!VECTOR) {
-      sx += reinterpret_cast<uintptr_t>(xs + row * a.x_stride * es) & 15;
-      sdy += reinterpret_cast<uintptr_t>(dys + row * a.dy_stride * es) & 15;
-    }
-    const auto load = [&](uint32_t c, float* x, float* dy, float* w) {
-      if constexpr (VECTOR) {
-        widen<DT, V>(*reinterpret_cast<const uint4*>(sx + c * es), x);
-        widen<DT, V>(*reinterpret_cast<const uint4*>(sdy + c * es), dy);
+    // xhat and p = dy w of line k, pair by pair; dy itself where it is asked for
+    const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
+    const auto load = [&](uint32_t k, F2* h, F2* dy, F2* w) {
+      widen<DT>(*reinterpret_cast<const uint4*>(sx + k * 16), h);
+      widen<DT>(*reinterpret_cast<const uint4*>(sx + row_bytes + k * 16), dy);
+      if constexpr (SHIFTED) {
+        const int at = (int)(k * V) - (int)phase;
+        if (at < 0 || at + (int)V > (int)cols) mask_line<V>(h, -at, (int)cols - at), mask_line<V>(dy, -at, (int)cols - at);
+        const float* near = weights + (V + 1) * k + V - phase;
 #pragma unroll
-        for (uint32_t k = 0; k < V; k += 4) {
-          const float4 q = *reinterpret_cast<const float4*>(weights + c + k);
-          w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
+        for (uint32_t e = 0; e < H; ++e) {
+          float u = near[2 * e + (2 * e >= phase)], v = near[2 * e + 1 + (2 * e + 1 >= phase)];
+          w[e] = pair(u, v);
         }
+        if (at < 0 || at + (int)V > (int)cols) mask_line<V>(w, -at, (int)cols - at);
       } else {
-        if constexpr (DT == DT_F32) {
-          x[0] = *reinterpret_cast<const float*>(sx + c * es), dy[0] = *reinterpret_cast<const float*>(sdy + c * es);
-        } else {
-          x[0] = widen16<DT>(*reinterpret_cast<const unsigned short*>(sx + c * es));
-          dy[0] = widen16<DT>(*reinterpret_cast<const unsigned short*>(sdy + c * es));
+#pragma unroll
+        for (uint32_t e = 0; e < H; e += 2) {
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(weights + k * V + 2 * e);
+          w[e] = q.x, w[e + 1] = q.y;
         }
-        w[0] = weights[c];
       }
+#pragma unroll
+      for (uint32_t e = 0; e < H; ++e) h[e] = fma2(h[e], rstd2, shift2);
     };
-    float s1 = 0.0f, s2 = 0.0f;
+    F2 sum1 = 0, sum2 = 0;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t c = j * step + t * V;
-      if (c >= cols) continue;
-      float x[V], dy[V], w[V];
-      load(c, x, dy, w);
+      const uint32_t k = j * size + t;
+      if (k >= lines) continue;
+      F2 h[H], dy[H], w[H];
+      load(k, h, dy, w);
 #pragma unroll
-      for (uint32_t k = 0; k < V; ++k) {
-        const float h = (x[k] - mean) * rstd, p = dy[k] * w[k];
-        s1 += p;
-        s2 = __fmaf_rn(p, h, s2);
-        dw[j * V + k] = __fmaf_rn(dy[k], h, dw[j * V + k]);
-        db[j * V + k] += dy[k];
+      for (uint32_t e = 0; e < H; ++e) {
+        const F2 p = mul2(dy[e], w[e]);
+        sum1 = add2(sum1, p);
+        sum2 = fma2(p, h[e], sum2);
+        dw[j * H + e] = fma2(dy[e], h[e], dw[j * H + e]);
+        db[j * H + e] = add2(db[j * H + e], dy[e]);
       }
     }
     // both sums in one exchange
-    s1 = warp_sum(s1), s2 = warp_sum(s2);
+    float s1 = warp_sum(fold2(sum1)), s2 = warp_sum(fold2(sum2));
     if (size > 32) {
       const uint32_t warps = size / 32, lane = threadIdx.x & 31;
       if (lane == 0) slots[parity][0][threadIdx.x / 32] = s1, slots[parity][1][threadIdx.x / 32] = s2;
@@ -350,21 +531,22 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       s2 = warp_sum(lane < warps ? slots[parity][1][g * warps + lane] : 0.0f);
       parity ^= 1;
     }
-    const float c1 = s1 * inv_n, c2 = s2 * inv_n;
-    char* dx = static_cast<char*>(a.dx) + row * a.dx_stride * es;
+    // rstd (p - s1/n - xhat s2/n)
+    const float c1 = -rstd * (s1 * inv_n), c2 = -rstd * (s2 * inv_n);
+    const F2 c1_2 = pair(c1, c1), c2_2 = pair(c2, c2);
+    char* dx = static_cast<char*>(a.dx) + row * a.dx_stride * es - phase * es;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t c = j * step + t * V;
-      if (c >= cols) continue;
-      float x[V], dy[V], w[V], out[V];
-      load(c, x, dy, w);
+      const uint32_t k = j * size + t;
+      if (k >= lines) continue;
+      F2 h[H], dy[H], w[H];
+      load(k, h, dy, w);
 #pragma unroll
-      for (uint32_t k = 0; k < V; ++k) {
-        const float h = (x[k] - mean) * rstd;
-        out[k] = rstd * (__fmaf_rn(dy[k], w[k], -c1) - h * c2);
-      }
-      if constexpr (VECTOR) __stcs(reinterpret_cast<uint4*>(dx + (uint64_t)c * es), narrow<DT>(out));
-      else ln_store<DT>(dx, c, out[0]);
+      for (uint32_t e = 0; e < H; ++e) h[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(h[e], c2_2, c1_2));
+      const uint4 out = narrow<DT>(h);
+      const int at = (int)(k * V) - (int)phase;
+      if (!SHIFTED || (at >= 0 && at + (int)V <= (int)cols)) __stcs(reinterpret_cast<uint4*>(dx + k * 16), out);
+      else store_part<DT>(dx + k * 16, out, -at, (int)cols - at);
     }
     mean = next_mean, rstd = next_rstd;
     stage = stage + 1 == stages ? 0 : stage + 1;
@@ -376,12 +558,15 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (uint32_t j = 0; j < NV; ++j) {
-    const uint32_t c = j * step + t * V;
-    if (c >= cols) continue;
+    const int at = (int)((j * size + t) * V) - (int)phase;
 #pragma unroll
-    for (uint32_t k = 0; k < V; ++k) {
-      sums[(g * 2) * cols + c + k] = dw[j * V + k];
-      sums[(g * 2 + 1) * cols + c + k] = db[j * V + k];
+    for (uint32_t e = 0; e < H; ++e) {
+      float w0, w1, b0, b1;
+      split(dw[j * H + e], w0, w1), split(db[j * H + e], b0, b1);
+      const int c = at + 2 * (int)e;
+      float* s = sums + (int)(2 * g * cols) + c;
+      if (c >= 0 && c < (int)cols) s[0] = w0, s[cols] = b0;
+      if (c + 1 >= 0 && c + 1 < (int)cols) s[1] = w1, s[cols + 1] = b1;
     }
   }
   __syncthreads();
@@ -481,26 +666,35 @@ __global__ void __launch_bounds__(kLnThreads) ln_backward_columns(const __grid_c
   }
 }
 
-// The sums of the partials: CTA x takes 32 columns.
+// The sums of the partials: CTA x takes 32 columns, each warp a share of the parts. All of a thread's reads are
+// independent and there are few of them: the kernel is one trip to L2 and back.
+constexpr int kLnFinishThreads = 1024;
 template <int WDT>
-__global__ void __launch_bounds__(kLnThreads) ln_backward_finish(const __grid_constant__ LnBackward a) {
+__global__ void __launch_bounds__(kLnFinishThreads) ln_backward_finish(const __grid_constant__ LnBackward a) {
   pdl_enter();
-  __shared__ float sw[kLnThreads / 32][33], sb[kLnThreads / 32][33];
-  const uint32_t lane = threadIdx.x & 31, wid = threadIdx.x / 32;
+  constexpr int kWarps = kLnFinishThreads / 32, kReads = ((int)kLnMaxParts + kWarps - 1) / kWarps;
+  __shared__ float sw[kWarps][33], sb[kWarps][33];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x / 32;
   const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
-  float dw = 0.0f, db = 0.0f;
-  if (c < a.cols) {
-    for (int p = wid; p < a.parts; p += kLnThreads / 32) {
-      dw += a.part[(uint64_t)p * 2 * a.cols + c];
-      db += a.part[((uint64_t)p * 2 + 1) * a.cols + c];
-    }
+  float w[kReads], b[kReads];
+#pragma unroll
+  for (int k = 0; k < kReads; ++k) {
+    const int p = k * kWarps + wid;
+    const bool in = p < a.parts && c < a.cols;
+    w[k] = in ? __ldcg(a.part + (uint64_t)p * 2 * a.cols + c) : 0.0f;
+    b[k] = in ? __ldcg(a.part + ((uint64_t)p * 2 + 1) * a.cols + c) : 0.0f;
   }
-  sw[wid][lane] = dw, sb[wid][lane] = db;
+#pragma unroll
+  for (int k = 1; k < kReads; ++k) w[0] += w[k], b[0] += b[k];
+  sw[wid][lane] = w[0], sb[wid][lane] = b[0];
   __syncthreads();
-  if (wid == 0 && c < a.cols) {
-    for (int k = 1; k < kLnThreads / 32; ++k) dw += sw[k][lane], db += sb[k][lane];
-    if (a.dw) ln_store<WDT>(a.dw, c, a.accumulate ? ln_load<WDT>(a.dw, c) + dw : dw);
-    if (a.db) ln_store<WDT>(a.db, c, a.accumulate ? ln_load<WDT>(a.db, c) + db : db);
+  // warp q sums column q of the block's 32: over the warps, in the same tree every time
+  float dw = sw[lane][wid], db = sb[lane][wid];
+  dw = warp_sum(dw), db = warp_sum(db);
+  const uint64_t mine = (uint64_t)blockIdx.x * 32 + wid;
+  if (lane == 0 && mine < a.cols) {
+    if (a.dw) ln_store<WDT>(a.dw, mine, a.accumulate ? ln_load<WDT>(a.dw, mine) + dw : dw);
+    if (a.db) ln_store<WDT>(a.db, mine, a.accumulate ? ln_load<WDT>(a.db, mine) + db : db);
   }
 }
 

@@ -248,17 +248,11 @@ __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forw
 // A row of an odd length starts somewhere inside a 16-byte line. Its lines are
 // read and written whole all the same: a thread's k-th line holds the row's
 // elements V k - phase .. V k - phase + V - 1, and what lies outside the row is
-// masked. Only the weights have to be shifted to a row's phase: they stand in
-// shared memory with one gap after every V, where a warp's reads of one
-// position in 32 consecutive lines fall on different banks whatever the phase.
+// masked. A CTA takes rows that are a multiple of 8 apart, so that all of them
+// have one phase, and keeps the weights in shared memory shifted to it.
 __device__ __forceinline__ uint32_t line_phase(const void* p, uint32_t es) {
   return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / es;
 }
-template <uint32_t V>
-__host__ __device__ constexpr uint32_t gapped(uint32_t i) { return i + i / V; }
-// Elements of the gapped array of `cols` weights: V of them precede column 0.
-template <uint32_t V>
-__host__ __device__ constexpr uint32_t gapped_size(uint32_t cols) { return gapped<V>(cols + 2 * V); }
 
 // Line `at` of the matrix [base, end), element by element where it is not all inside it.
 template <int DT>
@@ -293,35 +287,39 @@ __device__ __forceinline__ void store_part(char* at, const uint4& q, int from, i
     if (k >= from && k < to) st_elem<DT>(at, k, es == 4 ? w[k] : (w[k / 2] >> (k % 2 * 16)) & 0xffffu);
 }
 
-// Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on.
+// Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on. The grid is a
+// multiple of 8 (or has a CTA for every row).
 template <int DT, int WDT, int E>
 __global__ void __launch_bounds__(kLnMaxThreads) ln_forward_shifted(const __grid_constant__ LnForward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
   __shared__ float slots[2][2][kLnMaxThreads / 32];
-  float2* wb = reinterpret_cast<float2*>(smem);
   const uint32_t cols = (uint32_t)a.cols, t = threadIdx.x, group = blockDim.x;
   const char* base = static_cast<const char*>(a.x);
   const char* end = base + ((a.rows - 1) * a.x_stride + cols) * es;
+  const uint32_t phase = line_phase(base + blockIdx.x * a.x_stride * es, es), lines = (phase + cols + V - 1) / V;
   uint4 q[NV];
   const auto fetch = [&](uint64_t row) {
-    const char* x = base + row * a.x_stride * es;
-    const uint32_t phase = line_phase(x, es);
+    const char* line0 = base + row * a.x_stride * es - phase * es;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
       const uint32_t k = j * group + t;
-      q[j] = k * V < phase + cols ? load_line<DT>(x + ((int)(k * V) - (int)phase) * (int)es, base, end) : make_uint4(0, 0, 0, 0);
+      q[j] = k < lines ? load_line<DT>(line0 + k * 16, base, end) : make_uint4(0, 0, 0, 0);
     }
   };
   fetch(blockIdx.x);
-  for (uint32_t c = t; c < cols; c += group)
-    wb[gapped<V>(c + V)] = make_float2(a.w ? ln_load<WDT>(a.w, c) : 1.0f, a.b ? ln_load<WDT>(a.b, c) : 0.0f);
+  float* ws = reinterpret_cast<float*>(smem);
+  float* bs = ws + lines * V;
+  for (uint32_t i = t; i < lines * V; i += group) {
+    const bool in = i >= phase && i - phase < cols;
+    ws[i] = !in ? 0.0f : a.w ? ln_load<WDT>(a.w, i - phase) : 1.0f;
+    bs[i] = in && a.b ? ln_load<WDT>(a.b, i - phase) : 0.0f;
+  }
   __syncthreads();
   const float n = (float)cols;
   uint32_t parity = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const uint32_t phase = line_phase(base + row * a.x_stride * es, es);
     const auto group_sum = [&](float v, float* s) {
       v = warp_sum(v);
       if ((t & 31) == 0) s[t / 32] = v;
@@ -353,21 +351,22 @@ __global__ void __launch_bounds__(kLnMaxThreads) ln_forward_shifted(const __grid
     const float var = __fdiv_rn(group_sum(fold2(sq), slots[parity][1]), n);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
     const F2 rstd2 = pair(rstd, rstd);
-    char* y = static_cast<char*>(a.y) + row * a.y_stride * es;
+    char* y = static_cast<char*>(a.y) + row * a.y_stride * es - phase * es;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t k0 = j * group + t;
-      const int at = (int)(k0 * V) - (int)phase;
-      if (at >= (int)cols) continue;
-      const float2* near = wb + (V + 1) * k0 + V - phase;  // value e's weights: one further on from e = phase on
+      const uint32_t k = j * group + t;
+      if (k >= lines) continue;
 #pragma unroll
-      for (uint32_t k = 0; k < H; ++k) {
-        const float2 u = near[2 * k + (2 * k >= phase)], v = near[2 * k + 1 + (2 * k + 1 >= phase)];
-        f[j * H + k] = fma2(mul2(f[j * H + k], rstd2), pair(u.x, v.x), pair(u.y, v.y));
+      for (uint32_t e = 0; e < H; e += 2) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(ws + k * V + 2 * e);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bs + k * V + 2 * e);
+        f[j * H + e] = fma2(mul2(f[j * H + e], rstd2), w.x, b.x);
+        f[j * H + e + 1] = fma2(mul2(f[j * H + e + 1], rstd2), w.y, b.y);
       }
       const uint4 out = narrow<DT>(f + j * H);
-      if (at >= 0 && at + (int)V <= (int)cols) __stcs(reinterpret_cast<uint4*>(y + at * (int)es), out);
-      else store_part<DT>(y + at * (int)es, out, -at, (int)cols - at);
+      const int at = (int)(k * V) - (int)phase;
+      if (at >= 0 && at + (int)V <= (int)cols) __stcs(reinterpret_cast<uint4*>(y + k * 16), out);
+      else store_part<DT>(y + k * 16, out, -at, (int)cols - at);
     }
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -378,14 +377,17 @@ __global__ void __launch_bounds__(kLnMaxThreads) ln_forward_shifted(const __grid
 }
 
 // ---- the backward pass in one sweep --------------------------------------------
-// One CTA per SM; its groups walk over the rows. The next rows of x and dy are
-// on their way into shared memory (cp.async) while a row is worked on, and the
-// column sums of dy xhat and dy stay in registers over all the rows of a group:
-// x and dy are read once. The CTA folds its groups' sums and writes one partial
-// of each; ln_backward_finish adds the partials.
+// One CTA per SM; its groups of threads walk over the rows. The next rows of x
+// and dy are on their way into shared memory (cp.async, up to 8 rows ahead)
+// while one is worked on, and the column sums of dy xhat and dy stay in
+// registers over all the rows of a group: x and dy are read once. The CTA folds
+// its groups' sums and writes one partial of each; ln_backward_finish adds the
+// partials. KEEP: xhat and dy w of the row stay in registers between their two
+// uses (before and after the row's sums), and its place in shared memory is
+// filled again at once; otherwise they are taken from shared memory twice.
 //
-// SHIFTED: rows off the 16-byte grid, by whole lines as above. The rows of one
-// group are a multiple of 8 apart, so all of them have the same phase and a
+// SHIFTED: rows off the 16-byte grid, by whole lines as above. The rows of a
+// CTA are a multiple of 8 apart, so all of them have the same phase and a
 // register keeps standing for the same column.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // copies `bytes` (0 to 16) and fills up with zeros
@@ -396,6 +398,19 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+constexpr uint32_t kLnMaxStages = 8;
+// Waits until all but the `pending` newest groups of copies have landed.
+__device__ __forceinline__ void cp_async_wait_but(uint32_t pending) {
+  switch (pending) {
+    case 7: cp_async_wait<7>(); break;
+    case 6: cp_async_wait<6>(); break;
+    case 5: cp_async_wait<5>(); break;
+    case 4: cp_async_wait<4>(); break;
+    case 3: cp_async_wait<3>(); break;
+    case 2: cp_async_wait<2>(); break;
+    default: cp_async_wait<1>();
+  }
+}
 
 // All threads of a row's group: a named barrier of its own, or the warp.
 __device__ __forceinline__ void group_sync(uint32_t g, uint32_t size) {
@@ -403,66 +418,68 @@ __device__ __forceinline__ void group_sync(uint32_t g, uint32_t size) {
   else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
 }
 
-// Bytes of one row's lines, and of the weights, in shared memory.
-__host__ __device__ constexpr uint32_t ln_row_bytes(uint32_t cols, uint32_t es, bool shifted) {
-  return (cols * es + (shifted ? 16 - es : 0) + 15) / 16 * 16;
-}
-__host__ __device__ constexpr uint32_t ln_weight_bytes(uint32_t cols, uint32_t es, bool shifted) {
-  return ((shifted ? (es == 2 ? gapped_size<8>(cols) : gapped_size<4>(cols)) : cols) * 4 + 15) / 16 * 16;
+// Elements of one row's lines in shared memory.
+__host__ __device__ constexpr uint32_t ln_row_elems(uint32_t cols, uint32_t es, bool shifted) {
+  return (cols + (shifted ? 16 / es - 1 : 0) + 16 / es - 1) / (16 / es) * (16 / es);
 }
 
-template <int DT, int WDT, int E, bool SHIFTED>
+template <int DT, int WDT, int E, bool KEEP, bool SHIFTED>
 __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __grid_constant__ LnBackward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
-  __shared__ float slots[2][2][kLnMaxThreads / 32];
-  const uint32_t cols = (uint32_t)a.cols, size = a.group, groups = kLnMaxThreads / size, stages = a.stages;
-  const uint32_t g = threadIdx.x / size, t = threadIdx.x - g * size;
-  const uint32_t row_bytes = ln_row_bytes(cols, es, SHIFTED);
+  __shared__ float2 slots[2][kLnMaxThreads / 32];
+  const uint32_t cols = (uint32_t)a.cols, size = a.group, groups = blockDim.x / size, stages = a.stages;
+  const uint32_t g = threadIdx.x / size, t = threadIdx.x - g * size, lane = threadIdx.x & 31;
+  const uint32_t row_elems = ln_row_elems(cols, es, SHIFTED), row_bytes = row_elems * es;
   float* weights = reinterpret_cast<float*>(smem);
-  char* ring = smem + ln_weight_bytes(cols, es, SHIFTED) + (size_t)g * stages * 2 * row_bytes;
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  char* ring = smem + row_elems * 4 + (size_t)g * stages * 2 * row_bytes;
 
-  const char* xs = static_cast<const char*>(a.x);
-  const char* dys = static_cast<const char*>(a.dy);
   // few rows spread over the CTAs first, then over their groups
   const uint64_t first = (uint64_t)g * gridDim.x + blockIdx.x, stride = (uint64_t)gridDim.x * groups;
-  const uint32_t phase = SHIFTED ? line_phase(xs + first * a.x_stride * es, es) : 0;
+  const char* xs = static_cast<const char*>(a.x);
+  const char* dys = static_cast<const char*>(a.dy);
+  const uint32_t phase = SHIFTED ? line_phase(xs + blockIdx.x * a.x_stride * es, es) : 0;
   const uint32_t lines = (phase + cols + V - 1) / V;
   const char* x_end = xs + ((a.rows - 1) * a.x_stride + cols) * es;
   const char* dy_end = dys + ((a.rows - 1) * a.dy_stride + cols) * es;
-  const auto fetch_row = [&](uint32_t dst, const char* base, const char* end, const char* row) {
-    const char* line0 = row - phase * es;
+  // this thread's first lines of the next row to fetch, the row itself, and where they go
+  const char* x_next = xs + first * a.x_stride * es - phase * es + t * 16;
+  const char* dy_next = dys + first * a.dy_stride * es - phase * es + t * 16;
+  const uint64_t x_hop = stride * a.x_stride * es, dy_hop = stride * a.dy_stride * es, dx_hop = stride * a.dx_stride * es;
+  uint64_t row_next = first;
+  const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
+  const auto fetch_lines = [&](uint32_t dst, const char* line, const char* base, const char* end) {
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t k = j * size + t;
-      if (k >= lines) continue;
-      const char* line = line0 + k * 16;
+      if (j * size + t >= lines) continue;
+      const char* at = line + j * size * 16;
+      const uint32_t to = dst + j * size * 16;
       if constexpr (!SHIFTED) {
-        cp_async16(dst + k * 16, line, 16);
-      } else if (line >= base) {
-        const uint64_t left = (uint64_t)(end - line);
-        cp_async16(dst + k * 16, line, left < 16 ? (uint32_t)left : 16);
+        cp_async16(to, at, 16);
+      } else if (at >= base) {
+        const uint64_t left = (uint64_t)(end - at);
+        cp_async16(to, at, left < 16 ? (uint32_t)left : 16);
       } else {  // the matrix starts inside this line
-        const uint4 q = load_line<DT>(line, base, end);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + k * 16), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
-                     : "memory");
+        const uint4 q = load_line<DT>(at, base, end);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
       }
     }
   };
-  const auto fetch = [&](uint32_t stage, uint64_t row) {
-    if (row < a.rows) {
-      fetch_row(ring_at + stage * 2 * row_bytes, xs, x_end, xs + row * a.x_stride * es);
-      fetch_row(ring_at + (stage * 2 + 1) * row_bytes, dys, dy_end, dys + row * a.dy_stride * es);
+  const auto fetch = [&](uint32_t stage) {
+    if (row_next < a.rows) {
+      const uint32_t dst = mine_at + stage * 2 * row_bytes;
+      fetch_lines(dst, x_next, xs, x_end);
+      fetch_lines(dst + row_bytes, dy_next, dys, dy_end);
+      x_next += x_hop, dy_next += dy_hop, row_next += stride;
     }
     cp_async_commit();
   };
-  for (uint32_t s = 0; s + 1 < stages; ++s) fetch(s, first + s * stride);
+  for (uint32_t s = 0; s < stages; ++s) fetch(s);
   float mean = 0.0f, rstd = 0.0f;
   if (first < a.rows) mean = __ldg(a.mean + first), rstd = __ldg(a.rstd + first);
-  for (uint32_t c = threadIdx.x; c < cols; c += kLnMaxThreads)
-    weights[SHIFTED ? gapped<V>(c + V) : c] = a.w ? ln_load<WDT>(a.w, c) : 1.0f;
+  for (uint32_t i = threadIdx.x; i < row_elems; i += blockDim.x)
+    weights[i] = i < phase || i - phase >= cols ? 0.0f : a.w ? ln_load<WDT>(a.w, i - phase) : 1.0f;
   __syncthreads();
 
   F2 dw[E / 2], db[E / 2];
@@ -470,48 +487,36 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   for (int k = 0; k < E / 2; ++k) dw[k] = db[k] = 0;
   const float inv_n = 1.0f / (float)cols;
   uint32_t stage = 0, parity = 0;
-  for (uint64_t row = first; row < a.rows; row += stride) {
-    if (stages == 2) cp_async_wait<0>();
-    else if (stages == 3) cp_async_wait<1>();
-    else cp_async_wait<2>();
-    // every thread reads back the lines it fetched itself, so nothing else has to be waited for
-    fetch(stage == 0 ? stages - 1 : stage - 1, row + (stages - 1) * stride);
+  const char* buffer = ring + t * 16;  // this thread's first line of the row in work
+  const float* w_at = weights + t * V;
+  char* dx = static_cast<char*>(a.dx) + first * a.dx_stride * es - phase * es + t * 16;
+  for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
+    cp_async_wait_but(stages - 1);  // every thread reads back the lines it fetched itself: nothing else to wait for
     float next_mean = 0.0f, next_rstd = 0.0f;
     if (row + stride < a.rows) next_mean = __ldg(a.mean + row + stride), next_rstd = __ldg(a.rstd + row + stride);
-
-    const char* sx = ring + stage * 2 * row_bytes;
-    // xhat and p = dy w of line k, pair by pair; dy itself where it is asked for
     const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
-    const auto load = [&](uint32_t k, F2* h, F2* dy, F2* w) {
-      widen<DT>(*reinterpret_cast<const uint4*>(sx + k * 16), h);
-      widen<DT>(*reinterpret_cast<const uint4*>(sx + row_bytes + k * 16), dy);
+    // xhat, dy and the weights of the thread's j-th line
+    const auto load = [&](uint32_t j, F2* h, F2* dy, F2* w) {
+      widen<DT>(*reinterpret_cast<const uint4*>(buffer + j * size * 16), h);
+      widen<DT>(*reinterpret_cast<const uint4*>(buffer + row_bytes + j * size * 16), dy);
       if constexpr (SHIFTED) {
-        const int at = (int)(k * V) - (int)phase;
+        const int at = (int)((j * size + t) * V) - (int)phase;
         if (at < 0 || at + (int)V > (int)cols) mask_line<V>(h, -at, (int)cols - at), mask_line<V>(dy, -at, (int)cols - at);
-        const float* near = weights + (V + 1) * k + V - phase;
-#pragma unroll
-        for (uint32_t e = 0; e < H; ++e) {
-          float u = near[2 * e + (2 * e >= phase)], v = near[2 * e + 1 + (2 * e + 1 >= phase)];
-          w[e] = pair(u, v);
-        }
-        if (at < 0 || at + (int)V > (int)cols) mask_line<V>(w, -at, (int)cols - at);
-      } else {
-#pragma unroll
-        for (uint32_t e = 0; e < H; e += 2) {
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(weights + k * V + 2 * e);
-          w[e] = q.x, w[e + 1] = q.y;
-        }
       }
 #pragma unroll
       for (uint32_t e = 0; e < H; ++e) h[e] = fma2(h[e], rstd2, shift2);
+#pragma unroll
+      for (uint32_t e = 0; e < H; e += 2) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w_at + j * size * V + 2 * e);
+        w[e] = q.x, w[e + 1] = q.y;
+      }
     };
-    F2 sum1 = 0, sum2 = 0;
+    F2 hs[KEEP ? E / 2 : 1], ps[KEEP ? E / 2 : 1], sum1 = 0, sum2 = 0;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t k = j * size + t;
-      if (k >= lines) continue;
+      if (j * size + t >= lines) continue;
       F2 h[H], dy[H], w[H];
-      load(k, h, dy, w);
+      load(j, h, dy, w);
 #pragma unroll
       for (uint32_t e = 0; e < H; ++e) {
         const F2 p = mul2(dy[e], w[e]);
@@ -519,37 +524,53 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
         sum2 = fma2(p, h[e], sum2);
         dw[j * H + e] = fma2(dy[e], h[e], dw[j * H + e]);
         db[j * H + e] = add2(db[j * H + e], dy[e]);
+        if constexpr (KEEP) hs[j * H + e] = h[e], ps[j * H + e] = p;
       }
     }
-    // both sums in one exchange
-    float s1 = warp_sum(fold2(sum1)), s2 = warp_sum(fold2(sum2));
-    if (size > 32) {
-      const uint32_t warps = size / 32, lane = threadIdx.x & 31;
-      if (lane == 0) slots[parity][0][threadIdx.x / 32] = s1, slots[parity][1][threadIdx.x / 32] = s2;
-      group_sync(g, size);
-      s1 = warp_sum(lane < warps ? slots[parity][0][g * warps + lane] : 0.0f);
-      s2 = warp_sum(lane < warps ? slots[parity][1][g * warps + lane] : 0.0f);
-      parity ^= 1;
+    if constexpr (KEEP) fetch(stage);
+    // both sums in one exchange: the lower half of a warp carries one, the upper the other
+    float s1 = fold2(sum1), s2 = fold2(sum2);
+    {
+      const bool up = lane & 16;
+      float mine = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      if (size > 32) {
+        const uint32_t warps = size / 32, w = lane & 15;
+        if (w == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
+        group_sync(g, size);
+        mine = w < warps ? reinterpret_cast<const float*>(&slots[parity][g * warps + w])[lane / 16] : 0.0f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        parity ^= 1;
+      }
+      s1 = __shfl_sync(0xffffffffu, mine, 0), s2 = __shfl_sync(0xffffffffu, mine, 16);
     }
     // rstd (p - s1/n - xhat s2/n)
     const float c1 = -rstd * (s1 * inv_n), c2 = -rstd * (s2 * inv_n);
     const F2 c1_2 = pair(c1, c1), c2_2 = pair(c2, c2);
-    char* dx = static_cast<char*>(a.dx) + row * a.dx_stride * es - phase * es;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t k = j * size + t;
-      if (k >= lines) continue;
-      F2 h[H], dy[H], w[H];
-      load(k, h, dy, w);
+      if (j * size + t >= lines) continue;
+      F2 out[H];
+      if constexpr (KEEP) {
 #pragma unroll
-      for (uint32_t e = 0; e < H; ++e) h[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(h[e], c2_2, c1_2));
-      const uint4 out = narrow<DT>(h);
-      const int at = (int)(k * V) - (int)phase;
-      if (!SHIFTED || (at >= 0 && at + (int)V <= (int)cols)) __stcs(reinterpret_cast<uint4*>(dx + k * 16), out);
-      else store_part<DT>(dx + k * 16, out, -at, (int)cols - at);
+        for (uint32_t e = 0; e < H; ++e) out[e] = fma2(ps[j * H + e], rstd2, fma2(hs[j * H + e], c2_2, c1_2));
+      } else {
+        F2 dy[H], w[H];
+        load(j, out, dy, w);
+#pragma unroll
+        for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(out[e], c2_2, c1_2));
+      }
+      const uint4 q = narrow<DT>(out);
+      const int at = (int)((j * size + t) * V) - (int)phase;
+      if (!SHIFTED || (at >= 0 && at + (int)V <= (int)cols)) __stcs(reinterpret_cast<uint4*>(dx + j * size * 16), q);
+      else store_part<DT>(dx + j * size * 16, q, -at, (int)cols - at);
     }
+    if constexpr (!KEEP) fetch(stage);
     mean = next_mean, rstd = next_rstd;
-    stage = stage + 1 == stages ? 0 : stage + 1;
+    ++stage, buffer += 2 * row_bytes;
+    if (stage == stages) stage = 0, buffer = ring + t * 16;
   }
   if (a.dw == nullptr && a.db == nullptr) return;
   // fold the groups: every group's sums side by side in shared memory, then column by column
@@ -558,23 +579,24 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (uint32_t j = 0; j < NV; ++j) {
-    const int at = (int)((j * size + t) * V) - (int)phase;
+    const uint32_t k = j * size + t;
+    if (k >= lines) continue;
+    float* to = sums + g * 2 * row_elems + k * V;
 #pragma unroll
-    for (uint32_t e = 0; e < H; ++e) {
-      float w0, w1, b0, b1;
-      split(dw[j * H + e], w0, w1), split(db[j * H + e], b0, b1);
-      const int c = at + 2 * (int)e;
-      float* s = sums + (int)(2 * g * cols) + c;
-      if (c >= 0 && c < (int)cols) s[0] = w0, s[cols] = b0;
-      if (c + 1 >= 0 && c + 1 < (int)cols) s[1] = w1, s[cols + 1] = b1;
+    for (uint32_t e = 0; e < H; e += 2) {
+      *reinterpret_cast<ulonglong2*>(to + 2 * e) = make_ulonglong2(dw[j * H + e], dw[j * H + e + 1]);
+      *reinterpret_cast<ulonglong2*>(to + row_elems + 2 * e) = make_ulonglong2(db[j * H + e], db[j * H + e + 1]);
     }
   }
   __syncthreads();
   float* part = a.part + (uint64_t)blockIdx.x * 2 * cols;
-  for (uint32_t c = threadIdx.x; c < 2 * cols; c += kLnMaxThreads) {
-    float s = sums[c];
-    for (uint32_t k = 1; k < groups; ++k) s += sums[k * 2 * cols + c];
-    part[c] = s;
+  for (uint32_t c = threadIdx.x; c < cols; c += blockDim.x) {
+    float w = 0.0f, b = 0.0f;
+    for (uint32_t k = 0; k < groups; ++k) {
+      w += sums[k * 2 * row_elems + phase + c];
+      b += sums[(k * 2 + 1) * row_elems + phase + c];
+    }
+    part[c] = w, part[cols + c] = b;
   }
 }
 

@@ -23,12 +23,8 @@ uint32_t phase(const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p)
 uint32_t line(uint64_t stride) { return (uint32_t)(stride * es & 15u); }
 unsigned row_ctas(uint64_t rows) { return (unsigned)(rows < 152 * 8 ? rows : 152 * 8); }
 
-// Threads per row: the fewest that hold it in `per` columns each.
-uint32_t group_for(uint64_t cols, uint64_t per, uint32_t least, uint32_t most) {
-  uint32_t group = least;
-  while (group < most && group * per < cols) group *= 2;
-  return group;
-}
+// Threads for a row of `cols` columns, `per` or fewer to each: whole warps.
+uint32_t group_for(uint64_t cols, uint32_t per) { return (uint32_t)((cols + 32 * per - 1) / (32 * per)) * 32; }
 
 template <class K>
 cudaError_t allow_smem(K kernel, size_t smem) {
@@ -46,18 +42,23 @@ template <int E>
 cudaError_t forward_shifted(const LnForward& a, uint32_t group, size_t smem, cudaStream_t s) {
   const cudaError_t err = allow_smem(ln_forward_shifted<DT, WDT, E>, smem);
   if (err != cudaSuccess) return err;
-  uint64_t per_sm = 1024 / group;
+  uint64_t per_sm = (E <= 16 ? 1024 : 512) / group;
   if (per_sm > kLnSmem / (smem + 1280)) per_sm = kLnSmem / (smem + 1280);
   if (per_sm < 1) per_sm = 1;
   const uint64_t ctas = a.rows < 152 * per_sm ? a.rows : 152 * per_sm;
   return launch_programmatic(ln_forward_shifted<DT, WDT, E>, dim3((unsigned)ctas), group, smem, s, a);
 }
 
-template <int E>
-cudaError_t backward_fused(const LnBackward& a, bool shifted, size_t smem, cudaStream_t s) {
-  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, true> : ln_backward_fused<DT, WDT, E, false>;
+template <int E, bool KEEP>
+cudaError_t backward_fused(LnBackward a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
+  const uint32_t groups = kLnMaxThreads / a.group;
+  const size_t stages = (kLnSmem - weights) / (groups * stage);
+  a.stages = stages > kLnMaxStages ? kLnMaxStages : (uint32_t)stages;
+  size_t smem = weights + groups * a.stages * stage;
+  if (smem < groups * 2 * weights) smem = groups * 2 * weights;  // the fold
+  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, KEEP, true> : ln_backward_fused<DT, WDT, E, KEEP, false>;
   const cudaError_t err = allow_smem(kernel, smem);
-  return err != cudaSuccess ? err : launch_programmatic(kernel, dim3((unsigned)a.parts), kLnMaxThreads, smem, s, a);
+  return err != cudaSuccess ? err : launch_programmatic(kernel, dim3((unsigned)a.parts), groups * a.group, smem, s, a);
 }
 
 }  // namespace
@@ -66,25 +67,20 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   const bool aligned = a.cols % V == 0 && !phase(a.x) && !phase(a.y) && !line(a.x_stride) && !line(a.y_stride) &&
                        !phase(a.w) && !phase(a.b);
   if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64) {
-    const uint32_t group = group_for(a.cols, 32, 32, kLnMaxThreads);
-    const uint64_t per = (a.cols + group - 1) / group;
-    if (per <= 8) return forward_registers<8>(a, group, s);
-    if (per <= 16) return forward_registers<16>(a, group, s);
-    if (per <= 24) return forward_registers<24>(a, group, s);
-    if (per <= 32) return forward_registers<32>(a, group, s);
-    return forward_registers<64>(a, group, s);
+    if (a.cols <= 256) return forward_registers<8>(a, 32, s);
+    if (a.cols <= 512) return forward_registers<16>(a, 32, s);
+    if (a.cols <= 16384) return forward_registers<32>(a, group_for(a.cols, 32), s);
+    return forward_registers<64>(a, group_for(a.cols, 64), s);
   }
   // x and y in step: every row of both at the same place in its 16-byte line
-  if (phase(a.x) == phase(a.y) && line(a.x_stride) == line(a.y_stride) && a.cols < 1u << 20) {
-    const uint64_t cols = a.cols + V - 1;  // a line more, at most
-    const size_t smem = gapped_size<V>((uint32_t)a.cols) * sizeof(float2);
-    const uint32_t group = group_for(cols, 16, 64, kLnMaxThreads);
-    const uint64_t per = (cols + group - 1) / group;
-    if (smem <= kLnSmem && per <= 64) {
-      if (per <= 8) return forward_shifted<8>(a, group, smem, s);
-      if (per <= 16) return forward_shifted<16>(a, group, smem, s);
-      if (per <= 32) return forward_shifted<32>(a, group, smem, s);
-      return forward_shifted<64>(a, group, smem, s);
+  const uint64_t reach = a.cols + V - 1;  // a line more, at most
+  if (phase(a.x) == phase(a.y) && line(a.x_stride) == line(a.y_stride) && reach <= (uint64_t)kLnMaxThreads * 64) {
+    const size_t smem = 2 * sizeof(float) * ln_row_elems((uint32_t)a.cols, es, true);
+    if (smem <= kLnSmem) {
+      if (reach <= 512) return forward_shifted<8>(a, group_for(reach, 8), smem, s);
+      if (reach <= 8192) return forward_shifted<16>(a, group_for(reach, 16), smem, s);
+      if (reach <= 16384) return forward_shifted<32>(a, group_for(reach, 32), smem, s);
+      return forward_shifted<64>(a, group_for(reach, 64), smem, s);
     }
   }
   return launch_programmatic(ln_forward_rows<DT, WDT>, dim3(row_ctas(a.rows)), kLnThreads, 0, s, a);
@@ -99,27 +95,20 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
   const bool in_step = phase(a.x) == phase(a.dy) && phase(a.x) == phase(a.dx) && line(a.x_stride) == line(a.dy_stride) &&
                        line(a.x_stride) == line(a.dx_stride);
   const uint64_t reach = a.cols + (aligned ? 0 : V - 1);
-  // the sweep in one kernel wants a row in 32 columns a thread and two rows of x and dy per group in shared memory
+  // the sweep in one kernel: two stages of a row's x and dy for each group have to fit in shared memory
   if (a.rows > 0 && in_step && reach <= (uint64_t)kLnMaxThreads * 32) {
-    const uint32_t cols = (uint32_t)a.cols;
-    const size_t fixed = ln_weight_bytes(cols, es, !aligned), row = 2 * ln_row_bytes(cols, es, !aligned);
-    a.group = group_for(reach, 32, 32, kLnMaxThreads);
-    uint32_t groups = kLnMaxThreads / a.group;
-    size_t stages = (kLnSmem - fixed) / (groups * row);
-    while (stages < 2 && a.group < kLnMaxThreads) {
-      a.group *= 2, groups /= 2;
-      stages = (kLnSmem - fixed) / (groups * row);
-    }
-    if (stages >= 2) {
-      a.stages = stages > 4 ? 4 : (uint32_t)stages;
-      size_t smem = fixed + groups * a.stages * row;
-      const size_t fold = (size_t)groups * 2 * cols * 4;
-      if (fold > smem) smem = fold;
-      const uint64_t per = (reach + a.group - 1) / a.group;
-      if (per <= 8) err = backward_fused<8>(a, !aligned, smem, s);
-      else if (per <= 16) err = backward_fused<16>(a, !aligned, smem, s);
-      else if (per <= 24) err = backward_fused<24>(a, !aligned, smem, s);
-      else err = backward_fused<32>(a, !aligned, smem, s);
+    const uint32_t elems = ln_row_elems((uint32_t)a.cols, es, !aligned);
+    const size_t weights = elems * 4, row = 2 * elems * es;
+    const auto fits = [&](uint32_t per) {
+      a.group = group_for(reach, per);
+      return weights + 2 * (kLnMaxThreads / a.group) * row <= kLnSmem;
+    };
+    bool done = true;
+    if (reach <= 256) a.group = 32, err = backward_fused<8, true>(a, !aligned, weights, row, s);
+    else if (reach <= 8192 && fits(16)) err = backward_fused<16, true>(a, !aligned, weights, row, s);
+    else if (fits(32)) err = backward_fused<32, false>(a, !aligned, weights, row, s);
+    else done = false;
+    if (done) {
       if (err != cudaSuccess || !sums) return err;
       return launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a);
     }

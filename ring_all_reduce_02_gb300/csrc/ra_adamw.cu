@@ -75,9 +75,21 @@ ra_status_t add_span(std::vector<Span>& v, const void* p, uint64_t bytes, uintpt
 bool unit(double x) { return x >= 0.0 && x < 1.0; }
 bool sound(double x) { return x >= 0.0 && x < INFINITY; }
 
+// How the kernel may take a tensor's chunks (AdamTensor::layout): in vectors of 8 elements if every buffer is
+// as many elements past a vector boundary as the others (fp32 moments: the chunks then start that much early;
+// 8-bit blocks start with the tensor, which has to be on a boundary).
+uint32_t layout_of(const ra_adamw_tensor_t& t, uint64_t pe, uint64_t ge, uint64_t se, uint64_t ce) {
+  const auto past = [](const void* p, uint64_t es) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) / es % 8); };
+  const uint32_t shift = past(t.param, pe);
+  if (past(t.grad, ge) != shift || past(t.exp_avg, se) != shift || past(t.exp_avg_sq, se) != shift) return 0;
+  if (t.copy != nullptr && past(t.copy, ce) != shift) return 0;
+  if (se == 1 && shift != 0) return 0;
+  return ra::kAdamVec | shift;
+}
+
 template <int CAP, class Fn>
-ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, const ra_adamw_options_t& o,
-                       ra::AdamScalars s, cudaStream_t stream) {
+ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, const ra_adamw_options_t& o, uint64_t pe,
+                       uint64_t ge, uint64_t ce, ra::AdamScalars s, cudaStream_t stream) {
   ra::AdamArgs<CAP> a;
   int i = 0;
   while (i < ntensors) {
@@ -86,7 +98,8 @@ ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, co
     s.ordinal0 = (uint32_t)i;
     for (; i < ntensors && s.n < CAP; ++i) {
       const ra_adamw_tensor_t& t = tensors[i];
-      const uint64_t chunks = (t.count + ra::kAdamBlock - 1) / ra::kAdamBlock;
+      const uint32_t layout = t.count ? layout_of(t, pe, ge, o.state == RA_STATE_E4M3 ? 1 : 4, ce) : 0;
+      const uint64_t chunks = (t.count + (layout & 7u) + ra::kAdamBlock - 1) / ra::kAdamBlock;
       const uint64_t more = (chunks + ra::kAdamWarps - 1) / ra::kAdamWarps;
       if (ctas + more > 0x7fffffffull) {
         if (s.n == 0) return RA_ERR_UNSUPPORTED;
@@ -97,7 +110,7 @@ ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, co
       e.ms = t.exp_avg_scale, e.vs = t.exp_avg_sq_scale, e.copy = t.copy;
       e.count = t.count;
       e.keep = (float)(1.0 - o.lr * t.weight_decay);
-      e.layout = 0;
+      e.layout = layout;
       a.cta0[s.n++] = (uint32_t)ctas;
       ctas += more;
     }
@@ -174,6 +187,6 @@ extern "C" ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, 
   s.scale = o.grad_scale;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return ntensors <= ra::kAdamSmall
-             ? launch_all<ra::kAdamSmall>(tensors, ntensors, ra::kAdamSmallFns[param_dtype][grad_dtype], o, s, cs)
-             : launch_all<ra::kAdamLarge>(tensors, ntensors, ra::kAdamLargeFns[param_dtype][grad_dtype], o, s, cs);
+             ? launch_all<ra::kAdamSmall>(tensors, ntensors, ra::kAdamSmallFns[param_dtype][grad_dtype], o, pe, ge, ce, s, cs)
+             : launch_all<ra::kAdamLarge>(tensors, ntensors, ra::kAdamLargeFns[param_dtype][grad_dtype], o, pe, ge, ce, s, cs);
 }

@@ -37,7 +37,7 @@ struct AdamTensor {
   void* copy;
   uint64_t count;
   float keep;       // 1 - lr * weight_decay
-  uint32_t layout;  // kAdamVec: all buffers can be read in vectors of 8 elements at 8 k - shift; low bits: shift
+  uint32_t layout;  // kAdamVec: every buffer has vectors of 8 elements at elements 8 k - shift; low 3 bits: shift
 };
 constexpr uint32_t kAdamVec = 8;
 
@@ -84,67 +84,110 @@ __device__ __forceinline__ float load_e4m3(const void* base, uint64_t i) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
 }
 
-// |x| * 448 / amax rounded up or down in e4m3's normal range by 16 random bits:
+// x * 448 / amax rounded up or down in e4m3's normal range by 16 random bits:
 // the bits below the 3 kept ones of the mantissa decide with their own weight.
+// The conversion that follows saturates, so that nothing passes 448.
 __device__ __forceinline__ float round_e4m3(float x, float inv, uint32_t rand16) {
-  const float t = fminf(fmaxf(__fmul_rn(x, inv), -kE4m3Max), kE4m3Max);
-  return __uint_as_float((__float_as_uint(t) + (rand16 << 4)) & 0xfff00000u);
+  return __uint_as_float((__float_as_uint(__fmul_rn(x, inv)) + (rand16 << 4)) & 0xfff00000u);
 }
 
-template <int P, int G, bool S8, int CAP>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
-  pdl_enter();
-  const AdamScalars& s = a.s;
-  float scale = 1.0f;
-  if (s.scale != nullptr) {
-    scale = *s.scale;
-    if (!(fabsf(scale) < __int_as_float(0x7f800000))) return;  // not finite: the step is skipped
+// 8 consecutive elements at element i, as fp32; i and the base are on the 8-element grid.
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, uint64_t i, float* f) {
+  if constexpr (DT == DT_F32) {
+    const VecT<8> v = ld_vec_w<8>(static_cast<const float*>(base) + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v.w[k]);
+  } else {
+    const VecT<4> v = ld_vec_w<4>(static_cast<const unsigned short*>(base) + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = widen16<DT>((v.w[k / 2] >> (k % 2 * 16)) & 0xffffu);
   }
-  int lo = 0, hi = s.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cta0[mid] <= blockIdx.x) lo = mid;
-    else hi = mid - 1;
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* base, uint64_t i, const float* f) {
+  if constexpr (DT == DT_F32) {
+    VecT<8> v;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v.w[k] = __float_as_uint(f[k]);
+    st_vec<8>(static_cast<float*>(base) + i, v);
+  } else {
+    VecT<4> v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v.w[k] = round16<DT>(f[2 * k]) | round16<DT>(f[2 * k + 1]) << 16;
+    st_vec<4>(static_cast<unsigned short*>(base) + i, v);
   }
-  const AdamTensor& t = a.t[lo];
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t chunk = (uint64_t)(blockIdx.x - a.cta0[lo]) * kAdamWarps + threadIdx.x / 32;
-  const uint64_t base = chunk * kAdamBlock;
-  if (base >= t.count) return;
-  const uint32_t key = S8 ? mix32(s.key + (s.ordinal0 + (uint32_t)lo) * 0xB7E15163u) : 0;
+}
+__device__ __forceinline__ void load8_e4m3(const void* base, uint64_t i, float* f) {
+  const uint2 q = __ldcs(reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(base) + i));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((k < 2 ? q.x : q.y) >> (k % 2 * 16));
+    const float2 p = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+    f[2 * k] = p.x, f[2 * k + 1] = p.y;
+  }
+}
+__device__ __forceinline__ uint32_t pack4_e4m3(const float* f) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
 
-  float m[8], r[8];
+// One chunk of a tensor by one warp: elements base .. base + 255, of which [0, count) exist. WHOLE: all of them
+// do, on the 8-element grid of every buffer, and lane l takes 8 l .. 8 l + 7; otherwise lane l takes l, l + 32, ...
+template <int P, int G, bool S8, bool WHOLE>
+__device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTensor& t, int64_t base, uint64_t chunk,
+                                            uint32_t key, float scale) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t i0 = (uint64_t)base + (WHOLE ? 8 * lane : 0);
+  const auto at = [&](int j) { return base + (int64_t)lane + 32 * j; };
+  const auto in = [&](int j) { return (uint64_t)at(j) < t.count; };  // a negative place wraps around
+  float p[8], g[8], m[8], r[8];  // r: v, then its square root
   float m_scale = 0.0f, r_scale = 0.0f;
-  if (S8) m_scale = t.ms[chunk], r_scale = t.vs[chunk];
+  if constexpr (S8) m_scale = t.ms[chunk], r_scale = t.vs[chunk];
+  if constexpr (WHOLE) {
+    load8<G>(t.g, i0, g);
+    load8<P>(t.p, i0, p);
+    if constexpr (S8) load8_e4m3(t.m, i0, m), load8_e4m3(t.v, i0, r);
+    else load8<DT_F32>(t.m, i0, m), load8<DT_F32>(t.v, i0, r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      g[j] = in(j) ? load_as_f32<G>(t.g, at(j)) : 0.0f;
+      p[j] = in(j) ? load_as_f32<P>(t.p, at(j)) : 0.0f;
+      if constexpr (S8) m[j] = in(j) ? load_e4m3(t.m, at(j)) : 0.0f, r[j] = in(j) ? load_e4m3(t.v, at(j)) : 0.0f;
+      else m[j] = in(j) ? load_as_f32<DT_F32>(t.m, at(j)) : 0.0f, r[j] = in(j) ? load_as_f32<DT_F32>(t.v, at(j)) : 0.0f;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint64_t i = base + lane + 32 * j;
-    m[j] = r[j] = 0.0f;
-    if (i >= t.count) continue;
-    const float g = load_as_f32<G>(t.g, i) * scale;
-    float v;
-    if constexpr (S8) {
-      m[j] = load_e4m3(t.m, i) * m_scale;
-      const float root = load_e4m3(t.v, i) * r_scale;
-      v = root * root;
-    } else {
-      m[j] = load_as_f32<DT_F32>(t.m, i);
-      v = load_as_f32<DT_F32>(t.v, i);
-    }
-    m[j] = m[j] * s.b1 + g * s.one_minus_b1;
-    v = v * s.b2 + (g * s.one_minus_b2) * g;
-    r[j] = __fsqrt_rn(v);
-    const float u = __fdiv_rn(m[j], r[j] * s.inv_sqrt_bc2 + s.eps);
-    const float p = load_as_f32<P>(t.p, i) * t.keep - u * s.step_size;
-    store_f32_as<P>(t.p, i, p);
+    g[j] *= scale;
+    if constexpr (S8) m[j] *= m_scale, r[j] *= r_scale, r[j] *= r[j];
+    m[j] = m[j] * s.b1 + g[j] * s.one_minus_b1;
+    r[j] = r[j] * s.b2 + (g[j] * s.one_minus_b2) * g[j];
+    const float root = __fsqrt_rn(r[j]);
+    p[j] = p[j] * t.keep - __fdividef(m[j], root * s.inv_sqrt_bc2 + s.eps) * s.step_size;
+    if constexpr (S8) r[j] = root;
+  }
+  if constexpr (WHOLE) {
+    store8<P>(t.p, i0, p);
+    if constexpr (!S8) store8<DT_F32>(t.m, i0, m), store8<DT_F32>(t.v, i0, r);
     if (t.copy != nullptr) {
-      if (s.copy_dtype == DT_F32) store_f32_as<DT_F32>(t.copy, i, p);
-      else if (s.copy_dtype == DT_F16) store_f32_as<DT_F16>(t.copy, i, p);
-      else store_f32_as<DT_BF16>(t.copy, i, p);
+      if (s.copy_dtype == DT_F32) store8<DT_F32>(t.copy, i0, p);
+      else if (s.copy_dtype == DT_F16) store8<DT_F16>(t.copy, i0, p);
+      else store8<DT_BF16>(t.copy, i0, p);
     }
-    if constexpr (!S8) {
-      store_f32_as<DT_F32>(t.m, i, m[j]);
-      store_f32_as<DT_F32>(t.v, i, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!in(j)) continue;
+      store_f32_as<P>(t.p, at(j), p[j]);
+      if constexpr (!S8) store_f32_as<DT_F32>(t.m, at(j), m[j]), store_f32_as<DT_F32>(t.v, at(j), r[j]);
+      if (t.copy != nullptr) {
+        if (s.copy_dtype == DT_F32) store_f32_as<DT_F32>(t.copy, at(j), p[j]);
+        else if (s.copy_dtype == DT_F16) store_f32_as<DT_F16>(t.copy, at(j), p[j]);
+        else store_f32_as<DT_BF16>(t.copy, at(j), p[j]);
+      }
     }
   }
   if constexpr (S8) {
@@ -165,18 +208,56 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
       t.ms[chunk] = m_bad ? nan : m_some ? m_amax * (1.0f / kE4m3Max) : 0.0f;
       t.vs[chunk] = r_bad ? nan : r_some ? r_amax * (1.0f / kE4m3Max) : 0.0f;
     }
+    const float r_floor = r_some ? 0.001953125f : 0.0f;  // 2^-9, the smallest value above zero
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint64_t i = base + lane + 32 * j;
-      if (i >= t.count) continue;
+      const uint64_t i = WHOLE ? i0 + j : (uint64_t)at(j);
       const uint32_t rand = mix32((uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0xB7E15163u + key);
-      const float mq = round_e4m3(m[j], m_inv, rand & 0xffffu);
-      float rq = round_e4m3(r[j], r_inv, rand >> 16);
-      if (r_some && r[j] > 0.0f) rq = fmaxf(rq, 0.001953125f);  // 2^-9, the smallest value above zero
-      static_cast<unsigned char*>(t.m)[i] = m_bad ? 0x7f : __nv_cvt_float_to_fp8(mq, __NV_SATFINITE, __NV_E4M3);
-      static_cast<unsigned char*>(t.v)[i] = r_bad ? 0x7f : __nv_cvt_float_to_fp8(rq, __NV_SATFINITE, __NV_E4M3);
+      m[j] = round_e4m3(m[j], m_inv, rand & 0xffffu);
+      const float rounded = round_e4m3(r[j], r_inv, rand >> 16);
+      r[j] = r[j] > 0.0f ? fmaxf(rounded, r_floor) : rounded;
+    }
+    if constexpr (WHOLE) {
+      uint2 mq = make_uint2(pack4_e4m3(m), pack4_e4m3(m + 4)), rq = make_uint2(pack4_e4m3(r), pack4_e4m3(r + 4));
+      if (m_bad) mq = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+      if (r_bad) rq = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+      __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(t.m) + i0), mq);
+      __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(t.v) + i0), rq);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!in(j)) continue;
+        static_cast<unsigned char*>(t.m)[at(j)] = m_bad ? 0x7f : __nv_cvt_float_to_fp8(m[j], __NV_SATFINITE, __NV_E4M3);
+        static_cast<unsigned char*>(t.v)[at(j)] = r_bad ? 0x7f : __nv_cvt_float_to_fp8(r[j], __NV_SATFINITE, __NV_E4M3);
+      }
     }
   }
+}
+
+template <int P, int G, bool S8, int CAP>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
+  pdl_enter();
+  const AdamScalars& s = a.s;
+  float scale = 1.0f;
+  if (s.scale != nullptr) {
+    scale = *s.scale;
+    if (!(fabsf(scale) < __int_as_float(0x7f800000))) return;  // not finite: the step is skipped
+  }
+  int lo = 0, hi = s.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cta0[mid] <= blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const AdamTensor& t = a.t[lo];
+  const uint64_t chunk = (uint64_t)(blockIdx.x - a.cta0[lo]) * kAdamWarps + threadIdx.x / 32;
+  const int64_t base = (int64_t)(chunk * kAdamBlock) - (int64_t)(t.layout & 7u);
+  if (base >= (int64_t)t.count) return;
+  const uint32_t key = S8 ? mix32(s.key + (s.ordinal0 + (uint32_t)lo) * 0xB7E15163u) : 0;
+  if ((t.layout & kAdamVec) && base >= 0 && base + kAdamBlock <= (int64_t)t.count)
+    adamw_chunk<P, G, S8, true>(s, t, base, chunk, key, scale);
+  else
+    adamw_chunk<P, G, S8, false>(s, t, base, chunk, key, scale);
 }
 
 }  // namespace ra

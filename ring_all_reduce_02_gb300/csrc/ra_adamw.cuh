@@ -18,6 +18,7 @@
 
 #include "ra_kernels.cuh"
 #include "ra_ops.cuh"
+#include "ra_pairs.cuh"
 
 namespace ra {
 
@@ -61,13 +62,19 @@ struct AdamArgs {
 };
 
 // A 32-bit mix: xor-shifts and multiplications by odd constants (the fractions of e and of the golden ratio).
-__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
+__host__ __device__ __forceinline__ uint32_t mix32_but_last(uint32_t x) {
   x ^= x >> 16;
   x *= 0xB7E15163u;
   x ^= x >> 15;
-  x *= 0x9E3779B9u;
+  return x * 0x9E3779B9u;
+}
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x = mix32_but_last(x);
   return x ^ (x >> 16);
 }
+// The 16 low and the 16 high bits of mix32, each 4 places up, from mix32_but_last.
+__device__ __forceinline__ uint32_t low_bits(uint32_t x) { return ((x << 4) ^ (x >> 12)) & 0xffff0u; }
+__device__ __forceinline__ uint32_t high_bits(uint32_t x) { return (x >> 12) & 0xffff0u; }
 
 template <int DT>
 __device__ __forceinline__ float load_as_f32(const void* base, uint64_t i) {
@@ -84,11 +91,11 @@ __device__ __forceinline__ float load_e4m3(const void* base, uint64_t i) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
 }
 
-// x * 448 / amax rounded up or down in e4m3's normal range by 16 random bits:
-// the bits below the 3 kept ones of the mantissa decide with their own weight.
-// The conversion that follows saturates, so that nothing passes 448.
-__device__ __forceinline__ float round_e4m3(float x, float inv, uint32_t rand16) {
-  return __uint_as_float((__float_as_uint(__fmul_rn(x, inv)) + (rand16 << 4)) & 0xfff00000u);
+// A value scaled to its block (x * 448 / amax), rounded up or down in e4m3's normal range by 16 random bits in
+// places 4 to 19: the bits below the 3 kept ones of the mantissa decide with their own weight. The conversion
+// that follows saturates, so that nothing passes 448.
+__device__ __forceinline__ float round_up_or_down(float x, uint32_t bits) {
+  return __uint_as_float((__float_as_uint(x) + bits) & 0xfff00000u);
 }
 
 // 8 consecutive elements at element i, as fp32; i and the base are on the 8-element grid.
@@ -133,6 +140,12 @@ __device__ __forceinline__ uint32_t pack4_e4m3(const float* f) {
   return lo | hi << 16;
 }
 
+__device__ __forceinline__ void sum_rn(F2 x, F2 y, float& a, float& b) {
+  float x0, x1, y0, y1;
+  split(x, x0, x1), split(y, y0, y1);
+  a = __fadd_rn(x0, y0), b = __fadd_rn(x1, y1);
+}
+
 // One chunk of a tensor by one warp: elements base .. base + 255, of which [0, count) exist. WHOLE: all of them
 // do, on the 8-element grid of every buffer, and lane l takes 8 l .. 8 l + 7; otherwise lane l takes l, l + 32, ...
 template <int P, int G, bool S8, bool WHOLE>
@@ -159,15 +172,23 @@ __device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTens
       else m[j] = in(j) ? load_as_f32<DT_F32>(t.m, at(j)) : 0.0f, r[j] = in(j) ? load_as_f32<DT_F32>(t.v, at(j)) : 0.0f;
     }
   }
+  const F2 scale2 = twice(scale), b1 = twice(s.b1), b1c = twice(s.one_minus_b1), b2 = twice(s.b2), b2c = twice(s.one_minus_b2);
+  const F2 bc = twice(s.inv_sqrt_bc2), eps = twice(s.eps), keep = twice(t.keep), step = twice(-s.step_size);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    g[j] *= scale;
-    if constexpr (S8) m[j] *= m_scale, r[j] *= r_scale, r[j] *= r[j];
-    m[j] = m[j] * s.b1 + g[j] * s.one_minus_b1;
-    r[j] = r[j] * s.b2 + (g[j] * s.one_minus_b2) * g[j];
-    const float root = __fsqrt_rn(r[j]);
-    p[j] = p[j] * t.keep - __fdividef(m[j], root * s.inv_sqrt_bc2 + s.eps) * s.step_size;
-    if constexpr (S8) r[j] = root;
+  for (int j = 0; j < 8; j += 2) {
+    const F2 gg = mul2(pair(g[j], g[j + 1]), scale2);
+    F2 mm = pair(m[j], m[j + 1]), vv = pair(r[j], r[j + 1]);
+    if constexpr (S8) mm = mul2(mm, twice(m_scale)), vv = mul2(vv, twice(r_scale)), vv = mul2(vv, vv);
+    // products and sums rounded one by one: the stored moments are the same bits as the formula's written out
+    // (the sums are scalar: the assembler contracts a mul.f32x2 and an add.f32x2, rounding modifiers or not)
+    sum_rn(mul2(mm, b1), mul2(gg, b1c), m[j], m[j + 1]);
+    sum_rn(mul2(vv, b2), mul2(mul2(gg, b2c), gg), r[j], r[j + 1]);
+    const float r0 = __fsqrt_rn(r[j]), r1 = __fsqrt_rn(r[j + 1]);
+    float d0, d1;
+    split(fma2(pair(r0, r1), bc, eps), d0, d1);
+    const F2 u = pair(__fdividef(m[j], d0), __fdividef(m[j + 1], d1));
+    split(fma2(u, step, mul2(pair(p[j], p[j + 1]), keep)), p[j], p[j + 1]);
+    if constexpr (S8) r[j] = r0, r[j + 1] = r1;
   }
   if constexpr (WHOLE) {
     store8<P>(t.p, i0, p);
@@ -191,14 +212,11 @@ __device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTens
     }
   }
   if constexpr (S8) {
-    uint32_t m_top = 0, r_top = 0;  // magnitudes as bits: they order as the values do, NaN on top
+    float m_top = 0.0f, r_top = 0.0f;  // NaN wins, and its bits are above infinity's
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m_top = max(m_top, __float_as_uint(m[j]) & 0x7fffffffu);
-      r_top = max(r_top, __float_as_uint(r[j]) & 0x7fffffffu);
-    }
-    const float m_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m_top));
-    const float r_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, r_top));
+    for (int j = 0; j < 8; ++j) m_top = fmaximum(m_top, fabsf(m[j])), r_top = fmaximum(r_top, r[j]);
+    const float m_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m_top)));
+    const float r_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r_top)));
     const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
     const bool m_some = m_amax > kMinAmax, r_some = r_amax > kMinAmax;
     const bool m_bad = !(m_amax < inf), r_bad = !(r_amax < inf);
@@ -209,13 +227,24 @@ __device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTens
       t.vs[chunk] = r_bad ? nan : r_some ? r_amax * (1.0f / kE4m3Max) : 0.0f;
     }
     const float r_floor = r_some ? 0.001953125f : 0.0f;  // 2^-9, the smallest value above zero
+    const uint32_t seed0 = (uint32_t)i0 * 0x9E3779B9u + (uint32_t)(i0 >> 32) * 0xB7E15163u + key;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint64_t i = WHOLE ? i0 + j : (uint64_t)at(j);
-      const uint32_t rand = mix32((uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0xB7E15163u + key);
-      m[j] = round_e4m3(m[j], m_inv, rand & 0xffffu);
-      const float rounded = round_e4m3(r[j], r_inv, rand >> 16);
-      r[j] = r[j] > 0.0f ? fmaxf(rounded, r_floor) : rounded;
+    for (int j = 0; j < 8; j += 2) {
+      uint32_t rand[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint64_t i = (uint64_t)at(j + k);
+        rand[k] = mix32_but_last(WHOLE ? seed0 + (j + k) * 0x9E3779B9u  // 8 elements from a multiple of 8 share i >> 32
+                                       : (uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0xB7E15163u + key);
+      }
+      split(mul2(pair(m[j], m[j + 1]), twice(m_inv)), m[j], m[j + 1]);
+      float t0, t1;
+      split(mul2(pair(r[j], r[j + 1]), twice(r_inv)), t0, t1);
+      m[j] = round_up_or_down(m[j], low_bits(rand[0])), m[j + 1] = round_up_or_down(m[j + 1], low_bits(rand[1]));
+      t0 = round_up_or_down(t0, high_bits(rand[0])), t1 = round_up_or_down(t1, high_bits(rand[1]));
+      if (r[j] > 0.0f) t0 = fmaxf(t0, r_floor);
+      if (r[j + 1] > 0.0f) t1 = fmaxf(t1, r_floor);
+      r[j] = t0, r[j + 1] = t1;
     }
     if constexpr (WHOLE) {
       uint2 mq = make_uint2(pack4_e4m3(m), pack4_e4m3(m + 4)), rq = make_uint2(pack4_e4m3(r), pack4_e4m3(r + 4));
@@ -235,7 +264,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTens
 }
 
 template <int P, int G, bool S8, int CAP>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
+__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
   pdl_enter();
   const AdamScalars& s = a.s;
   float scale = 1.0f;

@@ -10,6 +10,7 @@
 
 #include "ra_kernels.cuh"
 #include "ra_ops.cuh"
+#include "ra_pairs.cuh"
 
 namespace ra {
 
@@ -67,39 +68,6 @@ __device__ __forceinline__ float cta_sum_all(float x, float* smem) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
-}
-
-// ---- pairs of fp32 ------------------------------------------------------------
-// sm_103a adds, multiplies and fuses two fp32 at a time (each rounded as the
-// scalar operation is). At 4 to 6 bytes of HBM traffic per 16-bit element an SM
-// has about 25 to 35 issue slots per element, so pairs are what keeps these
-// kernels bound by memory.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pair(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void split(F2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float fold2(F2 p) {
-  float a, b;
-  split(p, a, b);
-  return a + b;
 }
 
 // 16 bytes of DT as pairs of fp32, and back.

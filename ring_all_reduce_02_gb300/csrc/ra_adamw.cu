@@ -89,18 +89,17 @@ uint32_t layout_of(const ra_adamw_tensor_t& t, uint64_t pe, uint64_t ge, uint64_
 
 template <int CAP, class Fn>
 ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, const ra_adamw_options_t& o, uint64_t pe,
-                       uint64_t ge, uint64_t ce, ra::AdamScalars s, cudaStream_t stream) {
+                       uint64_t ge, uint64_t ce, ra::AdamScalars s, uint32_t key, cudaStream_t stream) {
   ra::AdamArgs<CAP> a;
+  const uint64_t per_cta = (uint64_t)ra::kAdamThreads * ra::adam_lane_elems(o.state == RA_STATE_E4M3);
   int i = 0;
   while (i < ntensors) {
     uint64_t ctas = 0;
     s.n = 0;
-    s.ordinal0 = (uint32_t)i;
     for (; i < ntensors && s.n < CAP; ++i) {
       const ra_adamw_tensor_t& t = tensors[i];
       const uint32_t layout = t.count ? layout_of(t, pe, ge, o.state == RA_STATE_E4M3 ? 1 : 4, ce) : 0;
-      const uint64_t chunks = (t.count + (layout & 7u) + ra::kAdamBlock - 1) / ra::kAdamBlock;
-      const uint64_t more = (chunks + ra::kAdamWarps - 1) / ra::kAdamWarps;
+      const uint64_t more = (t.count + (layout & 7u) + per_cta - 1) / per_cta;
       if (ctas + more > 0x7fffffffull) {
         if (s.n == 0) return RA_ERR_UNSUPPORTED;
         break;
@@ -111,6 +110,7 @@ ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, co
       e.count = t.count;
       e.keep = (float)(1.0 - o.lr * t.weight_decay);
       e.layout = layout;
+      e.key = ra::mix32(key + (uint32_t)i * 0xB7E15163u);
       a.cta0[s.n++] = (uint32_t)ctas;
       ctas += more;
     }
@@ -182,11 +182,12 @@ extern "C" ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, 
   s.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow(o.beta2, (double)o.step)));
   s.eps = (float)o.eps;
   s.step_size = (float)(o.lr / (1.0 - pow(o.beta1, (double)o.step)));
-  s.key = ra::mix32((uint32_t)o.seed + ra::mix32((uint32_t)(o.seed >> 32) + (uint32_t)o.step * 0x9E3779B9u));
+  s.one = 1.0f;
+  const uint32_t key = ra::mix32((uint32_t)o.seed + ra::mix32((uint32_t)(o.seed >> 32) + (uint32_t)o.step * 0x9E3779B9u));
   s.copy_dtype = o.copy_dtype;
   s.scale = o.grad_scale;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return ntensors <= ra::kAdamSmall
-             ? launch_all<ra::kAdamSmall>(tensors, ntensors, ra::kAdamSmallFns[param_dtype][grad_dtype], o, pe, ge, ce, s, cs)
-             : launch_all<ra::kAdamLarge>(tensors, ntensors, ra::kAdamLargeFns[param_dtype][grad_dtype], o, pe, ge, ce, s, cs);
+             ? launch_all<ra::kAdamSmall>(tensors, ntensors, ra::kAdamSmallFns[param_dtype][grad_dtype], o, pe, ge, ce, s, key, cs)
+             : launch_all<ra::kAdamLarge>(tensors, ntensors, ra::kAdamLargeFns[param_dtype][grad_dtype], o, pe, ge, ce, s, key, cs);
 }

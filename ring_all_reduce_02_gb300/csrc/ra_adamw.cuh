@@ -23,8 +23,19 @@
 namespace ra {
 
 constexpr int kAdamBlock = 256;  // elements per chunk, and per scale of an 8-bit moment
-constexpr int kAdamThreads = 256;
+#ifndef RA_ADAM_MINB
+#define RA_ADAM_MINB 8
+#endif
+#ifndef RA_ADAM_T
+#define RA_ADAM_T 128
+#endif
+constexpr int kAdamThreads = RA_ADAM_T;
 constexpr int kAdamWarps = kAdamThreads / 32;
+#ifndef RA_ADAM_E
+#define RA_ADAM_E 16
+#endif
+// Consecutive elements of a lane.
+__host__ __device__ constexpr int adam_lane_elems(bool s8) { return s8 ? RA_ADAM_E : 8; }
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 
@@ -38,19 +49,22 @@ struct AdamTensor {
   void* copy;
   uint64_t count;
   float keep;       // 1 - lr * weight_decay
+  uint32_t key;     // of its random bits
   uint32_t layout;  // kAdamVec: every buffer has vectors of 8 elements at elements 8 k - shift; low 3 bits: shift
 };
 constexpr uint32_t kAdamVec = 8;
 
 // Kernel parameters hold at most 32,764 bytes; the small table keeps short lists' launches short.
-constexpr int kAdamSmall = 16;
-constexpr int kAdamLarge = 416;
+#ifndef RA_ADAM_SMALL
+#define RA_ADAM_SMALL 64
+#endif
+constexpr int kAdamSmall = RA_ADAM_SMALL;
+constexpr int kAdamLarge = 384;
 
 struct AdamScalars {
   float b1, one_minus_b1, b2, one_minus_b2, inv_sqrt_bc2, eps, step_size;
+  float one;          // 1.0f, which the assembler must not know
   int n;              // tensors in the table
-  uint32_t key;       // of the random bits
-  uint32_t ordinal0;  // place of table entry 0 in the caller's list
   int copy_dtype;
   const float* scale;
 };
@@ -60,6 +74,17 @@ struct AdamArgs {
   uint32_t cta0[CAP];  // first CTA of each tensor
   AdamTensor t[CAP];
 };
+
+// The last i < n with first[i] <= x, by the whole warp: first[] ascends, first[0] = 0, n <= 1024. Two rounds of
+// 32 probes, against the ten dependent constant loads of a bisection.
+__device__ __forceinline__ int last_not_above(const uint32_t* first, int n, uint32_t x) {
+  if (n == 1) return 0;
+  const int lane = threadIdx.x & 31, step = (n + 31) / 32;
+  int i = lane * step;
+  int lo = (__popc(__ballot_sync(0xffffffffu, i < n && first[i] <= x)) - 1) * step;
+  i = lo + lane;
+  return lo + __popc(__ballot_sync(0xffffffffu, lane < step && i < n && first[i] <= x)) - 1;
+}
 
 // A 32-bit mix: xor-shifts and multiplications by odd constants (the fractions of e and of the golden ratio).
 __host__ __device__ __forceinline__ uint32_t mix32_but_last(uint32_t x) {
@@ -72,10 +97,6 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x = mix32_but_last(x);
   return x ^ (x >> 16);
 }
-// The 16 low and the 16 high bits of mix32, each 4 places up, from mix32_but_last.
-__device__ __forceinline__ uint32_t low_bits(uint32_t x) { return ((x << 4) ^ (x >> 12)) & 0xffff0u; }
-__device__ __forceinline__ uint32_t high_bits(uint32_t x) { return (x >> 12) & 0xffff0u; }
-
 template <int DT>
 __device__ __forceinline__ float load_as_f32(const void* base, uint64_t i) {
   if constexpr (DT == DT_F32) return __ldcs(static_cast<const float*>(base) + i);
@@ -91,24 +112,26 @@ __device__ __forceinline__ float load_e4m3(const void* base, uint64_t i) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
 }
 
-// A value scaled to its block (x * 448 / amax), rounded up or down in e4m3's normal range by 16 random bits in
-// places 4 to 19: the bits below the 3 kept ones of the mantissa decide with their own weight. The conversion
-// that follows saturates, so that nothing passes 448.
-__device__ __forceinline__ float round_up_or_down(float x, uint32_t bits) {
-  return __uint_as_float((__float_as_uint(x) + bits) & 0xfff00000u);
+// A value scaled to its block (x * 448 / amax), rounded up or down in e4m3's normal range by 16 random bits: the
+// bits below the 3 kept ones of the mantissa decide with their own weight. The conversion that follows saturates,
+// so that nothing passes 448.
+__device__ __forceinline__ float round_up_or_down(float x, uint32_t rand16) {
+  return __uint_as_float((__float_as_uint(x) + (rand16 << 4)) & 0xfff00000u);
 }
 
-// 8 consecutive elements at element i, as fp32; i and the base are on the 8-element grid.
+// 8 consecutive elements as they are stored, and as fp32. The base is on the 8-element grid.
 template <int DT>
-__device__ __forceinline__ void load8(const void* base, uint64_t i, float* f) {
-  if constexpr (DT == DT_F32) {
-    const VecT<8> v = ld_vec_w<8>(static_cast<const float*>(base) + i);
+using Raw8 = VecT<DT == DT_F32 ? 8 : 4>;
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const void* base, uint64_t i) {
+  return ld_vec_w<DT == DT_F32 ? 8 : 4>(static_cast<const char*>(base) + i * Elem<DT>::kSize);
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& v, float* f) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v.w[k]);
-  } else {
-    const VecT<4> v = ld_vec_w<4>(static_cast<const unsigned short*>(base) + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = widen16<DT>((v.w[k / 2] >> (k % 2 * 16)) & 0xffffu);
+  for (int k = 0; k < 8; ++k) {
+    if constexpr (DT == DT_F32) f[k] = __uint_as_float(v.w[k]);
+    else f[k] = widen16<DT>((v.w[k / 2] >> (k % 2 * 16)) & 0xffffu);
   }
 }
 template <int DT>
@@ -125,8 +148,10 @@ __device__ __forceinline__ void store8(void* base, uint64_t i, const float* f) {
     st_vec<4>(static_cast<unsigned short*>(base) + i, v);
   }
 }
-__device__ __forceinline__ void load8_e4m3(const void* base, uint64_t i, float* f) {
-  const uint2 q = __ldcs(reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(base) + i));
+__device__ __forceinline__ uint2 load8_bytes(const void* base, uint64_t i) {
+  return __ldcs(reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(base) + i));
+}
+__device__ __forceinline__ void widen8_e4m3(const uint2& q, float* f) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((k < 2 ? q.x : q.y) >> (k % 2 * 16));
@@ -134,73 +159,164 @@ __device__ __forceinline__ void load8_e4m3(const void* base, uint64_t i, float* 
     f[2 * k] = p.x, f[2 * k + 1] = p.y;
   }
 }
+__device__ __forceinline__ float e4m3_byte(uint32_t w, int k) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(w >> (8 * k)), __NV_E4M3)));
+}
 __device__ __forceinline__ uint32_t pack4_e4m3(const float* f) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 
-__device__ __forceinline__ void sum_rn(F2 x, F2 y, float& a, float& b) {
-  float x0, x1, y0, y1;
-  split(x, x0, x1), split(y, y0, y1);
-  a = __fadd_rn(x0, y0), b = __fadd_rn(x1, y1);
+// 1 / d to a few ulp (it only enters the parameter, where the step is a small part): d is sqrt(v) / sqrt(1 - b2^t)
+// + eps with sqrt(v) either zero or above 2^-75, so it is no denormal unless eps is one.
+__device__ __forceinline__ float reciprocal(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+// The largest magnitude and the largest value of three; a NaN wins the first and loses the second.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The negated square roots of two values -v from 2^-96 up, rounded to nearest: with y ~ 1/sqrt(v) and s = v y, the
+// residual s^2 - v is exact in one fused operation and s - (s^2 - v) y/2 is Newton's next step, whose error is far
+// below half an ulp (P. Markstein, IBM J. Res. Dev. 34, 1990). Equal to sqrtf for every significand. Signs are
+// turned so that no operation is spent on them.
+__device__ __forceinline__ F2 minus_sqrt2(F2 minus_v) {
+  float v0, v1, y0, y1;
+  split(minus_v, v0, v1);
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(-v0));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(-v1));
+  const F2 y = pair(y0, y1), s = mul2(minus_v, y);
+  return fma2(fma2(s, s, minus_v), mul2(y, twice(0.5f)), s);
 }
 
-// One chunk of a tensor by one warp: elements base .. base + 255, of which [0, count) exist. WHOLE: all of them
-// do, on the 8-element grid of every buffer, and lane l takes 8 l .. 8 l + 7; otherwise lane l takes l, l + 32, ...
-template <int P, int G, bool S8, bool WHOLE>
-__device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTensor& t, int64_t base, uint64_t chunk,
-                                            uint32_t key, float scale) {
+// What a lane reads of whole chunks: its E consecutive elements.
+template <int P, int G, bool S8, int E>
+struct AdamRaw {
+  Raw8<P> p[E / 8];
+  Raw8<G> g[E / 8];
+  Raw8<DT_F32> m[E / 8], v[E / 8];
+};
+template <int P, int G, int E>
+struct AdamRaw<P, G, true, E> {
+  Raw8<P> p[E / 8];
+  Raw8<G> g[E / 8];
+  uint2 m[E / 8], v[E / 8];
+};
+
+// A warp's elements base .. base + 32 E - 1 of a tensor, E to a lane. WHOLE: all of them exist and are on the
+// 8-element grid of every buffer, and lane l takes base + E l .. base + E l + E - 1; a block of the 8-bit moments
+// is then 8 (E = 32) or 16 or 32 lanes' share. Otherwise E = 8, only [0, count) exist, and lane l takes l, l + 32, ...
+template <int P, int G, bool S8, bool WHOLE, int E>
+__device__ __forceinline__ void adamw_elements(const AdamScalars& s, const AdamTensor& t, int64_t base, float scale) {
+  static_assert(WHOLE || E == 8, "whole warps' shares or one block");
   const uint32_t lane = threadIdx.x & 31;
-  const uint64_t i0 = (uint64_t)base + (WHOLE ? 8 * lane : 0);
-  const auto at = [&](int j) { return base + (int64_t)lane + 32 * j; };
-  const auto in = [&](int j) { return (uint64_t)at(j) < t.count; };  // a negative place wraps around
-  float p[8], g[8], m[8], r[8];  // r: v, then its square root
+  const uint64_t i0 = (uint64_t)base + (WHOLE ? E * lane : 0);
+  const uint64_t block = S8 ? (WHOLE ? i0 : (uint64_t)base) / kAdamBlock : 0;  // 8-bit moments: base is on a block
+  const auto at = [&](int j) { return WHOLE ? i0 + j : (uint64_t)(base + (int64_t)lane + 32 * j); };
+  const auto in = [&](int j) { return WHOLE || at(j) < t.count; };  // a negative place wraps around
+  float p[E], g[E], m[E], r[E];  // r: v; with 8-bit moments sqrt(v), and from then on its negative
   float m_scale = 0.0f, r_scale = 0.0f;
-  if constexpr (S8) m_scale = t.ms[chunk], r_scale = t.vs[chunk];
   if constexpr (WHOLE) {
-    load8<G>(t.g, i0, g);
-    load8<P>(t.p, i0, p);
-    if constexpr (S8) load8_e4m3(t.m, i0, m), load8_e4m3(t.v, i0, r);
-    else load8<DT_F32>(t.m, i0, m), load8<DT_F32>(t.v, i0, r);
-  } else {
+    AdamRaw<P, G, S8, E> raw;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int k = 0; k < E / 8; ++k) {
+      raw.g[k] = load8<G>(t.g, i0 + 8 * k);
+      raw.p[k] = load8<P>(t.p, i0 + 8 * k);
+      if constexpr (S8) raw.m[k] = load8_bytes(t.m, i0 + 8 * k), raw.v[k] = load8_bytes(t.v, i0 + 8 * k);
+      else raw.m[k] = load8<DT_F32>(t.m, i0 + 8 * k), raw.v[k] = load8<DT_F32>(t.v, i0 + 8 * k);
+    }
+    if constexpr (S8) m_scale = t.ms[block], r_scale = t.vs[block];
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      widen8<G>(raw.g[k], g + 8 * k), widen8<P>(raw.p[k], p + 8 * k);
+      if constexpr (S8) widen8_e4m3(raw.m[k], m + 8 * k), widen8_e4m3(raw.v[k], r + 8 * k);
+      else widen8<DT_F32>(raw.m[k], m + 8 * k), widen8<DT_F32>(raw.v[k], r + 8 * k);
+    }
+  } else {
+    if constexpr (S8) m_scale = t.ms[block], r_scale = t.vs[block];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
       g[j] = in(j) ? load_as_f32<G>(t.g, at(j)) : 0.0f;
       p[j] = in(j) ? load_as_f32<P>(t.p, at(j)) : 0.0f;
       if constexpr (S8) m[j] = in(j) ? load_e4m3(t.m, at(j)) : 0.0f, r[j] = in(j) ? load_e4m3(t.v, at(j)) : 0.0f;
       else m[j] = in(j) ? load_as_f32<DT_F32>(t.m, at(j)) : 0.0f, r[j] = in(j) ? load_as_f32<DT_F32>(t.v, at(j)) : 0.0f;
     }
   }
-  const F2 scale2 = twice(scale), b1 = twice(s.b1), b1c = twice(s.one_minus_b1), b2 = twice(s.b2), b2c = twice(s.one_minus_b2);
-  const F2 bc = twice(s.inv_sqrt_bc2), eps = twice(s.eps), keep = twice(t.keep), step = twice(-s.step_size);
+  // the sign of the second moment's coefficients, see minus_sqrt2
+  constexpr float kSign = S8 ? -1.0f : 1.0f;
+  const F2 scale2 = twice(scale), b1 = twice(s.b1), b1c = twice(s.one_minus_b1);
+  const F2 b2 = twice(kSign * s.b2), b2c = twice(kSign * s.one_minus_b2);
+  const F2 one = twice(s.one), m_scale2 = twice(m_scale), r_scale2 = twice(r_scale);
+  float most = -1.0f, r_top = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
+  for (int j = 0; j < E; j += 2) {
     const F2 gg = mul2(pair(g[j], g[j + 1]), scale2);
     F2 mm = pair(m[j], m[j + 1]), vv = pair(r[j], r[j + 1]);
-    if constexpr (S8) mm = mul2(mm, twice(m_scale)), vv = mul2(vv, twice(r_scale)), vv = mul2(vv, vv);
-    // products and sums rounded one by one: the stored moments are the same bits as the formula's written out
-    // (the sums are scalar: the assembler contracts a mul.f32x2 and an add.f32x2, rounding modifiers or not)
-    sum_rn(mul2(mm, b1), mul2(gg, b1c), m[j], m[j + 1]);
-    sum_rn(mul2(vv, b2), mul2(mul2(gg, b2c), gg), r[j], r[j + 1]);
-    const float r0 = __fsqrt_rn(r[j]), r1 = __fsqrt_rn(r[j + 1]);
+    if constexpr (S8) mm = mul2(mm, m_scale2), vv = mul2(vv, r_scale2), vv = mul2(vv, vv);
+    // Products and sums rounded one by one: the stored moments are the same bits as the formula's written out.
+    // (x * 1 + y rather than x + y: the assembler contracts a mul.f32x2 and an add.f32x2, rounding modifiers or not.)
+    mm = fma2(mul2(mm, b1), one, mul2(gg, b1c));
+    vv = fma2(mul2(vv, b2), one, mul2(mul2(gg, b2c), gg));
+    split(mm, m[j], m[j + 1]), split(vv, r[j], r[j + 1]);
+    if constexpr (S8) {
+      most = max3(most, r[j], r[j + 1]);
+      split(minus_sqrt2(vv), r[j], r[j + 1]);
+      r_top = max3_abs_nan(r_top, r[j], r[j + 1]);
+    }
+  }
+  // zeros, values too small for minus_sqrt2, infinities: rare, and again by the book from what is in memory
+  bool plain = true;
+  if constexpr (S8) {
+    plain = most <= -0x1p-96f && r_top < __int_as_float(0x7f800000);
+    if (!plain) {
+      r_top = 0.0f;
+#pragma unroll 1
+      for (int k = 0; k < E; ++k) {
+        float v = 0.0f;
+        if (in(k)) {
+          const float gk = load_as_f32<G>(t.g, at(k)) * scale, root = load_e4m3(t.v, at(k)) * r_scale;
+          v = __fadd_rn(root * root * s.b2, gk * s.one_minus_b2 * gk);
+        }
+        v = __fsqrt_rn(v);
+        r_top = fmaximum(r_top, v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) r[j] = j == k ? -v : r[j];
+      }
+    }
+  }
+  const F2 bc = twice(kSign * s.inv_sqrt_bc2), eps = twice(s.eps), keep = twice(t.keep), step = twice(-s.step_size);
+#pragma unroll
+  for (int j = 0; j < E; j += 2) {
+    const F2 root = S8 ? pair(r[j], r[j + 1]) : pair(__fsqrt_rn(r[j]), __fsqrt_rn(r[j + 1]));
     float d0, d1;
-    split(fma2(pair(r0, r1), bc, eps), d0, d1);
-    const F2 u = pair(__fdividef(m[j], d0), __fdividef(m[j + 1], d1));
+    split(fma2(root, bc, eps), d0, d1);
+    const F2 u = mul2(pair(m[j], m[j + 1]), pair(reciprocal(d0), reciprocal(d1)));
     split(fma2(u, step, mul2(pair(p[j], p[j + 1]), keep)), p[j], p[j + 1]);
-    if constexpr (S8) r[j] = r0, r[j + 1] = r1;
   }
   if constexpr (WHOLE) {
-    store8<P>(t.p, i0, p);
-    if constexpr (!S8) store8<DT_F32>(t.m, i0, m), store8<DT_F32>(t.v, i0, r);
-    if (t.copy != nullptr) {
-      if (s.copy_dtype == DT_F32) store8<DT_F32>(t.copy, i0, p);
-      else if (s.copy_dtype == DT_F16) store8<DT_F16>(t.copy, i0, p);
-      else store8<DT_BF16>(t.copy, i0, p);
+#pragma unroll
+    for (int k = 0; k < E; k += 8) {
+      store8<P>(t.p, i0 + k, p + k);
+      if constexpr (!S8) store8<DT_F32>(t.m, i0 + k, m + k), store8<DT_F32>(t.v, i0 + k, r + k);
+      if (t.copy != nullptr) {
+        if (s.copy_dtype == DT_F32) store8<DT_F32>(t.copy, i0 + k, p + k);
+        else if (s.copy_dtype == DT_F16) store8<DT_F16>(t.copy, i0 + k, p + k);
+        else store8<DT_BF16>(t.copy, i0 + k, p + k);
+      }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < E; ++j) {
       if (!in(j)) continue;
       store_f32_as<P>(t.p, at(j), p[j]);
       if constexpr (!S8) store_f32_as<DT_F32>(t.m, at(j), m[j]), store_f32_as<DT_F32>(t.v, at(j), r[j]);
@@ -212,49 +328,72 @@ __device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTens
     }
   }
   if constexpr (S8) {
-    float m_top = 0.0f, r_top = 0.0f;  // NaN wins, and its bits are above infinity's
+    float m_top = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m_top = fmaximum(m_top, fabsf(m[j])), r_top = fmaximum(r_top, r[j]);
-    const float m_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m_top)));
-    const float r_amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r_top)));
+    for (int j = 0; j < E; j += 2) m_top = max3_abs_nan(m_top, m[j], m[j + 1]);
+    // the largest magnitudes of the block, as bits: they order as the values do, a NaN above infinity
+    uint32_t m_bits = __float_as_uint(m_top), r_bits = __float_as_uint(r_top);
+    constexpr int kLanes = 256 / E;  // of a block
+    if constexpr (kLanes == 32) {
+      m_bits = __reduce_max_sync(0xffffffffu, m_bits), r_bits = __reduce_max_sync(0xffffffffu, r_bits);
+    } else {
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        m_bits = max(m_bits, __shfl_xor_sync(0xffffffffu, m_bits, o));
+        r_bits = max(r_bits, __shfl_xor_sync(0xffffffffu, r_bits, o));
+      }
+    }
+    const float m_amax = __uint_as_float(m_bits), r_amax = __uint_as_float(r_bits);
     const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
     const bool m_some = m_amax > kMinAmax, r_some = r_amax > kMinAmax;
     const bool m_bad = !(m_amax < inf), r_bad = !(r_amax < inf);
     const float m_inv = m_some ? __frcp_rn(m_amax) * kE4m3Max : 0.0f;
     const float r_inv = r_some ? __frcp_rn(r_amax) * kE4m3Max : 0.0f;
-    if (lane == 0) {
-      t.ms[chunk] = m_bad ? nan : m_some ? m_amax * (1.0f / kE4m3Max) : 0.0f;
-      t.vs[chunk] = r_bad ? nan : r_some ? r_amax * (1.0f / kE4m3Max) : 0.0f;
+    if (lane % kLanes == 0) {
+      t.ms[block] = m_bad ? nan : m_some ? m_amax * (1.0f / kE4m3Max) : 0.0f;
+      t.vs[block] = r_bad ? nan : r_some ? r_amax * (1.0f / kE4m3Max) : 0.0f;
     }
     const float r_floor = r_some ? 0.001953125f : 0.0f;  // 2^-9, the smallest value above zero
-    const uint32_t seed0 = (uint32_t)i0 * 0x9E3779B9u + (uint32_t)(i0 >> 32) * 0xB7E15163u + key;
+    const uint32_t seed0 = (uint32_t)i0 * 0x9E3779B9u + (uint32_t)(i0 >> 32) * 0xB7E15163u + t.key;
+    const F2 m_inv2 = twice(m_inv), r_inv2 = twice(-r_inv);
+    uint32_t zeros = 0;  // second moments that are
+    if (!plain) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint32_t rand[2];
+      for (int j = 0; j < E; ++j) zeros |= (r[j] == 0.0f ? 1u : 0u) << j;
+    }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint64_t i = (uint64_t)at(j + k);
-        rand[k] = mix32_but_last(WHOLE ? seed0 + (j + k) * 0x9E3779B9u  // 8 elements from a multiple of 8 share i >> 32
-                                       : (uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0xB7E15163u + key);
+    for (int j = 0; j < E; j += 2) {
+      split(mul2(pair(m[j], m[j + 1]), m_inv2), m[j], m[j + 1]);
+      split(mul2(pair(r[j], r[j + 1]), r_inv2), r[j], r[j + 1]);
+#pragma unroll
+      for (int k = j; k < j + 2; ++k) {
+        const uint64_t i = at(k);
+        const uint32_t x = mix32_but_last(WHOLE ? seed0 + k * 0x9E3779B9u  // a lane's elements share i >> 32
+                                                : (uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0xB7E15163u + t.key);
+        m[k] = round_up_or_down(m[k], (x ^ (x >> 16)) & 0xffffu);
+        r[k] = fmaxf(round_up_or_down(r[k], x >> 16), r_floor);
       }
-      split(mul2(pair(m[j], m[j + 1]), twice(m_inv)), m[j], m[j + 1]);
-      float t0, t1;
-      split(mul2(pair(r[j], r[j + 1]), twice(r_inv)), t0, t1);
-      m[j] = round_up_or_down(m[j], low_bits(rand[0])), m[j + 1] = round_up_or_down(m[j + 1], low_bits(rand[1]));
-      t0 = round_up_or_down(t0, high_bits(rand[0])), t1 = round_up_or_down(t1, high_bits(rand[1]));
-      if (r[j] > 0.0f) t0 = fmaxf(t0, r_floor);
-      if (r[j + 1] > 0.0f) t1 = fmaxf(t1, r_floor);
-      r[j] = t0, r[j + 1] = t1;
+    }
+    if (!plain) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) r[j] = zeros >> j & 1u ? 0.0f : r[j];
     }
     if constexpr (WHOLE) {
-      uint2 mq = make_uint2(pack4_e4m3(m), pack4_e4m3(m + 4)), rq = make_uint2(pack4_e4m3(r), pack4_e4m3(r + 4));
-      if (m_bad) mq = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      if (r_bad) rq = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(t.m) + i0), mq);
-      __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(t.v) + i0), rq);
+      uint32_t mq[E / 4], rq[E / 4];
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) {
+        mq[k] = m_bad ? 0x7f7f7f7fu : pack4_e4m3(m + 4 * k);
+        rq[k] = r_bad ? 0x7f7f7f7fu : pack4_e4m3(r + 4 * k);
+      }
+      unsigned char *to_m = static_cast<unsigned char*>(t.m) + i0, *to_r = static_cast<unsigned char*>(t.v) + i0;
+#pragma unroll
+      for (int k = 0; k < E / 4; k += 2) {
+        __stcs(reinterpret_cast<uint2*>(to_m + 4 * k), make_uint2(mq[k], mq[k + 1]));
+        __stcs(reinterpret_cast<uint2*>(to_r + 4 * k), make_uint2(rq[k], rq[k + 1]));
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < E; ++j) {
         if (!in(j)) continue;
         static_cast<unsigned char*>(t.m)[at(j)] = m_bad ? 0x7f : __nv_cvt_float_to_fp8(m[j], __NV_SATFINITE, __NV_E4M3);
         static_cast<unsigned char*>(t.v)[at(j)] = r_bad ? 0x7f : __nv_cvt_float_to_fp8(r[j], __NV_SATFINITE, __NV_E4M3);
@@ -264,7 +403,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamScalars& s, const AdamTens
 }
 
 template <int P, int G, bool S8, int CAP>
-__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
+__global__ void __launch_bounds__(kAdamThreads, S8 ? RA_ADAM_MINB : 1024 / RA_ADAM_T) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
   pdl_enter();
   const AdamScalars& s = a.s;
   float scale = 1.0f;
@@ -272,21 +411,19 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
     scale = *s.scale;
     if (!(fabsf(scale) < __int_as_float(0x7f800000))) return;  // not finite: the step is skipped
   }
-  int lo = 0, hi = s.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cta0[mid] <= blockIdx.x) lo = mid;
-    else hi = mid - 1;
-  }
+  const int lo = last_not_above(a.cta0, s.n, blockIdx.x);
   const AdamTensor& t = a.t[lo];
-  const uint64_t chunk = (uint64_t)(blockIdx.x - a.cta0[lo]) * kAdamWarps + threadIdx.x / 32;
-  const int64_t base = (int64_t)(chunk * kAdamBlock) - (int64_t)(t.layout & 7u);
-  if (base >= (int64_t)t.count) return;
-  const uint32_t key = S8 ? mix32(s.key + (s.ordinal0 + (uint32_t)lo) * 0xB7E15163u) : 0;
-  if ((t.layout & kAdamVec) && base >= 0 && base + kAdamBlock <= (int64_t)t.count)
-    adamw_chunk<P, G, S8, true>(s, t, base, chunk, key, scale);
-  else
-    adamw_chunk<P, G, S8, false>(s, t, base, chunk, key, scale);
+  constexpr int E = adam_lane_elems(S8);
+  const uint64_t warp = (uint64_t)(blockIdx.x - a.cta0[lo]) * kAdamWarps + threadIdx.x / 32;
+  int64_t base = (int64_t)(warp * (32 * E)) - (int64_t)(t.layout & 7u);
+  const int64_t count = (int64_t)t.count;
+  if ((t.layout & kAdamVec) && base >= 0 && base + 32 * E <= count) {
+    adamw_elements<P, G, S8, true, E>(s, t, base, scale);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < E / 8 && base < count; ++k, base += kAdamBlock)
+      adamw_elements<P, G, S8, false, 8>(s, t, base, scale);
+  }
 }
 
 }  // namespace ra

@@ -19,6 +19,7 @@
 #include "ra_kernels.cuh"
 #include "ra_ops.cuh"
 #include "ra_pairs.cuh"
+#include "ra_tensors.cuh"
 
 namespace ra {
 
@@ -74,17 +75,6 @@ struct AdamArgs {
   uint32_t cta0[CAP];  // first CTA of each tensor
   AdamTensor t[CAP];
 };
-
-// The last i < n with first[i] <= x, by the whole warp: first[] ascends, first[0] = 0, n <= 1024. Two rounds of
-// 32 probes, against the ten dependent constant loads of a bisection.
-__device__ __forceinline__ int last_not_above(const uint32_t* first, int n, uint32_t x) {
-  if (n == 1) return 0;
-  const int lane = threadIdx.x & 31, step = (n + 31) / 32;
-  int i = lane * step;
-  int lo = (__popc(__ballot_sync(0xffffffffu, i < n && first[i] <= x)) - 1) * step;
-  i = lo + lane;
-  return lo + __popc(__ballot_sync(0xffffffffu, lane < step && i < n && first[i] <= x)) - 1;
-}
 
 // A 32-bit mix: xor-shifts and multiplications by odd constants (the fractions of e and of the golden ratio).
 __host__ __device__ __forceinline__ uint32_t mix32_but_last(uint32_t x) {

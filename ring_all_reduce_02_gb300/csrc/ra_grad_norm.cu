@@ -1,24 +1,36 @@
 // ra_grad_norm: the global 2-norm of many gradient tensors and the factor that
 // clips it, in one launch.
 //
-// One read of every element, two operations each: HBM bounds it. Every thread
-// sums squares in fp32 over its share of the tiles, a CTA folds its threads'
-// sums in a fixed tree and writes one partial; the CTA that takes the last
-// ticket adds the partials in a fixed order in fp64, so the result does not
-// depend on the order in which CTAs finish.
+// One read of every element, two operations each: HBM bounds it. Resident CTAs
+// walk over tiles of the tensors; a tile starts on a 32-byte boundary of its
+// tensor's memory, so that all but a tensor's first and last vectors are whole.
+// Every thread sums squares in fp32 over its share of the tiles, a CTA folds
+// its threads' sums in a fixed tree and writes one partial; the CTA that takes
+// the last ticket adds the partials in a fixed order in fp64, so the result
+// does not depend on the order in which CTAs finish.
 #include <math.h>
 
 #include "ra_host.h"
 #include "ra_kernels.cuh"
 #include "ra_ops.cuh"
+#include "ra_pairs.cuh"
+#include "ra_tensors.cuh"
 
 namespace ra {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormTile = 4096;       // elements a CTA takes at a time
-constexpr int kNormCtas = 1216;       // CTAs at most, a partial each: 8 on each of 152 SMs
+#ifndef RA_NORM_U
+#define RA_NORM_U 4
+#endif
+#ifndef RA_NORM_CTAS
+#define RA_NORM_CTAS 456
+#endif
+constexpr int kNormUnroll = RA_NORM_U;        // 32-byte vectors a thread has in flight
+constexpr int kNormCtas = RA_NORM_CTAS;       // CTAs at most, a partial each: 8 on each of 152 SMs
 constexpr int kNormSmall = 32;        // tensors in the small and the large table: kernel parameters hold 32,764 bytes
-constexpr int kNormLarge = 1280;
+constexpr int kNormLarge = 1024;
+// Elements of a tile.
+__host__ __device__ constexpr int norm_tile(int es) { return kNormThreads * kNormUnroll * 32 / es; }
 
 struct NormWorkspace {
   uint32_t ticket;  // CTAs that have written their partial; 0 between calls
@@ -61,25 +73,47 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
   const NormScalars& s = a.s;
   __shared__ double sums[kNormThreads / 32];
   __shared__ bool finish;
-  float acc = 0.0f;
+  constexpr int es = Elem<DT>::kSize, V = 32 / es;
+  const F2 prescale = twice(s.prescale);
+  F2 acc[4] = {0, 0, 0, 0};
   for (uint32_t tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
-    int lo = 0, hi = s.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.tile0[mid] <= tile) lo = mid;
-      else hi = mid - 1;
+    const int lo = last_not_above(a.tile0, s.n, tile);
+    const char* g = static_cast<const char*>(a.g[lo]);
+    const int64_t count = (int64_t)a.count[lo];
+    const int64_t first = (int64_t)(tile - a.tile0[lo]) * norm_tile(es) - (int64_t)((reinterpret_cast<uintptr_t>(g) & 31u) / es) +
+                          (int64_t)threadIdx.x * V;
+    VecT<8> x[kNormUnroll];
+#pragma unroll
+    for (int u = 0; u < kNormUnroll; ++u) {
+      const int64_t i = first + u * (kNormThreads * V);
+      if (i >= 0 && i + V <= count) {
+        x[u] = ld_vec_w<8>(g + i * es);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[u].w[k] = 0;
+        if (i + V > 0 && i < count) {
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (i + k >= 0 && i + k < count) x[u].w[k * es / 4] |= ld_elem<DT>(g, (uint64_t)(i + k)) << (k * es % 4 * 8);
+        }
+      }
     }
-    const uint64_t begin = (uint64_t)(tile - a.tile0[lo]) * kNormTile;
-    const uint64_t end = min(begin + kNormTile, a.count[lo]);
-    for (uint64_t i = begin + threadIdx.x; i < end; i += kNormThreads) {
-      float x;
-      if constexpr (DT == DT_F32) x = __uint_as_float(ld_elem<DT>(a.g[lo], i));
-      else x = widen16<DT>(ld_elem<DT>(a.g[lo], i));
-      x *= s.prescale;
-      acc = __fmaf_rn(x, x, acc);
+#pragma unroll
+    for (int u = 0; u < kNormUnroll; ++u) {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        F2 f;
+        if constexpr (DT == DT_F32) {
+          f = pair(__uint_as_float(x[u].w[k]), __uint_as_float(x[u].w[k + 1]));
+        } else {
+          f = pair(widen16<DT>(x[u].w[k / 2] & 0xffffu), widen16<DT>(x[u].w[k / 2] >> 16));
+        }
+        f = mul2(f, prescale);
+        acc[k / 2 % 4] = fma2(f, f, acc[k / 2 % 4]);
+      }
     }
   }
-  const double mine = cta_sum((double)acc, sums);
+  const double mine = cta_sum((double)fold2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]))), sums);
   if (threadIdx.x == 0) {
     float* slot = &s.ws->partial[blockIdx.x];
     *slot = (float)(blockIdx.x < s.written ? mine + (double)*slot : mine);
@@ -112,6 +146,7 @@ template <int CAP>
 ra_status_t launch_all(const void* const* grads, const size_t* counts, int ntensors, int dtype, ra::NormScalars s,
                        cudaStream_t stream) {
   ra::NormArgs<CAP> a;
+  const int es = ra::float_size(dtype);
   int i = 0;
   s.written = 0;
   do {
@@ -119,7 +154,8 @@ ra_status_t launch_all(const void* const* grads, const size_t* counts, int ntens
     s.n = 0;
     for (; i < ntensors && s.n < CAP; ++i) {
       if (counts[i] == 0) continue;
-      const uint64_t more = ((uint64_t)counts[i] + ra::kNormTile - 1) / ra::kNormTile;
+      const uint64_t past = reinterpret_cast<uintptr_t>(grads[i]) % 32 / es;  // elements past a vector boundary
+      const uint64_t more = (counts[i] + past + ra::norm_tile(es) - 1) / ra::norm_tile(es);
       if (tiles + more > 0x7fffffffull) {
         if (s.n == 0) return RA_ERR_UNSUPPORTED;
         break;

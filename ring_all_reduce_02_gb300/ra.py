@@ -373,19 +373,26 @@ def ra_allreduce_bulk_noalloc(sendbufs, recvbufs, op: str = "sum", max_sms: int 
 # ---- layer norm, gradient norm, AdamW ---------------------------------------
 
 
-_FLOAT_CODES: dict = {}  # torch dtype -> ra_dtype_t, filled by the first call
+class _Torch:
+    """What the calls below need of torch, looked up by the first of them: importing this module does not import
+    torch, and looking names up again would cost a call more than its checks."""
 
+    codes: dict = {}  # torch dtype -> ra_dtype_t
+    f32 = None
+    current_stream = None  # device index -> handle of torch's current stream there
 
-def _float_codes() -> dict:
-    if not _FLOAT_CODES:
+    @classmethod
+    def load(cls):
         import torch
 
-        _FLOAT_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    return _FLOAT_CODES
+        cls.f32 = torch.float32
+        cls.current_stream = torch._C._cuda_getCurrentRawStream
+        cls.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        return cls
 
 
 def _float_code(t, what: str) -> int:
-    code = _float_codes().get(t.dtype)
+    code = (_Torch.codes or _Torch.load().codes).get(t.dtype)
     if code is None:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
     return code
@@ -394,26 +401,16 @@ def _float_code(t, what: str) -> int:
 def _stream_of(t, stream) -> int:
     """The stream handle a call on tensor t goes to: ``stream``, or torch's current one on t's device (read
     without building a Stream object, which would cost as much as the launch)."""
-    if stream is None:
-        import torch
-
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return _stream_ptr(stream)
-
-
-def _F32():
-    import torch
-
-    return torch.float32
+    return _Torch.current_stream(t.get_device()) if stream is None else _stream_ptr(stream)
 
 
 def _is_matrix(t) -> bool:
     """A 2-D CUDA tensor whose rows are contiguous."""
-    return t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+    return t.is_cuda and t.dim() == 2 and (t.is_contiguous() or t.stride(1) == 1 or t.shape[1] <= 1)
 
 
 def _row_stride(t, cols: int) -> int:
-    return max(t.stride(0), cols) if t.shape[0] <= 1 else t.stride(0)
+    return cols if t.is_contiguous() else max(t.stride(0), cols) if t.shape[0] <= 1 else t.stride(0)
 
 
 def _is_vector(t, n: int, dtype) -> bool:
@@ -435,7 +432,7 @@ def _check_vectors(what: str, **vectors) -> None:
 def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
     """Layer norm of the rows of x [rows, cols] into y (which may be x); weight and bias ([cols], of x's type
     or float32, or None), mean and rstd ([rows] float32, kept for the backward pass, or None)."""
-    codes = _float_codes()
+    codes = _Torch.codes or _Torch.load().codes
     dtype = x.dtype
     w = weight if weight is not None else bias
     wdtype = dtype if w is None else w.dtype
@@ -444,7 +441,7 @@ def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_forward: unsupported dtype {dtype} with weights of {wdtype}")
     rows, cols = x.shape
-    f32 = _F32()
+    f32 = _Torch.f32
     if not (_is_vector(weight, cols, wdtype) and _is_vector(bias, cols, wdtype) and _is_vector(mean, rows, f32)
             and _is_vector(rstd, rows, f32)):
         _check_vectors("ra_layernorm_forward", weight=(weight, cols, wdtype), bias=(bias, cols, wdtype),
@@ -466,7 +463,7 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     """Gradients of layer norm: dx [rows, cols] (may be dy or x), and the sums over the rows dweight and dbias
     ([cols], of weight's type; None: not wanted), added to what they hold with ``accumulate``. ``workspace``: a
     contiguous CUDA tensor of ra_layernorm_workspace(rows, cols) bytes, needed for the sums."""
-    codes = _float_codes()
+    codes = _Torch.codes or _Torch.load().codes
     dtype = x.dtype
     w = weight if weight is not None else dweight if dweight is not None else dbias
     wdtype = dtype if w is None else w.dtype
@@ -477,7 +474,7 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_backward: unsupported dtype {dtype} with weights of {wdtype}")
     rows, cols = x.shape
-    f32 = _F32()
+    f32 = _Torch.f32
     if mean is None or rstd is None or not (
             _is_vector(weight, cols, wdtype) and _is_vector(dweight, cols, wdtype) and _is_vector(dbias, cols, wdtype)
             and _is_vector(mean, rows, f32) and _is_vector(rstd, rows, f32)
@@ -533,7 +530,7 @@ def ra_grad_norm(grads, max_norm: float, out, workspace, prescale: float = 1.0, 
     that clips it to max_norm into out[1]: out[1:] is ra_adamw's grad_scale. ``workspace``: a CUDA tensor of
     ra_grad_norm_workspace() bytes, zeroed once."""
     g = grads if isinstance(grads, GradTensors) else GradTensors(grads)
-    if out is None or not _is_vector(out, 2, _F32()) or not (workspace.is_cuda and workspace.is_contiguous()):
+    if out is None or not _is_vector(out, 2, _Torch.f32 or _Torch.load().f32) or not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("ra_grad_norm: out must be a contiguous CUDA tensor of 2 float32, workspace a contiguous CUDA "
                          "tensor")
     st = (_lib or lib()).ra_grad_norm(g.addresses, g.counts, len(g.tensors), g.dtype, prescale, max_norm,
@@ -610,7 +607,7 @@ def ra_adamw(tensors: AdamwTensors, lr: float, step: int, beta1: float = 0.9, be
     """One AdamW step over an adamw_tensors() list. ``step`` counts from 1. ``grad_scale``: a float32 CUDA
     tensor of one element the gradients are multiplied by (out[1:] of ra_grad_norm); not finite: nothing is
     written. ``seed``: of the stochastic rounding of 8-bit moments."""
-    if not _is_vector(grad_scale, 1, _F32()):
+    if not _is_vector(grad_scale, 1, _Torch.f32 or _Torch.load().f32):
         raise ValueError("ra_adamw: grad_scale must be a CUDA tensor of one float32")
     params = tensors.lists["params"]
     if not params:

@@ -10,6 +10,13 @@
 #define RA_CAT3_(a, b, c) a##_##b##_##c
 #define RA_CAT3(a, b, c) RA_CAT3_(a, b, c)
 
+#ifndef RA_LN_F8
+#define RA_LN_F8 256
+#endif
+#ifndef RA_LN_F16
+#define RA_LN_F16 512
+#endif
+
 namespace ra {
 namespace {
 
@@ -53,7 +60,7 @@ template <int E, bool KEEP>
 cudaError_t backward_fused(LnBackward a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
   const uint32_t groups = kLnMaxThreads / a.group;
   const size_t stages = (kLnSmem - weights) / (groups * stage);
-  a.stages = stages > kLnMaxStages ? kLnMaxStages : (uint32_t)stages;
+  a.stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + groups * a.stages * stage;
   if (smem < groups * 2 * weights) smem = groups * 2 * weights;  // the fold
   const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, KEEP, true> : ln_backward_fused<DT, WDT, E, KEEP, false>;
@@ -69,6 +76,8 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64) {
     if (a.cols <= 256) return forward_registers<8>(a, 32, s);
     if (a.cols <= 512) return forward_registers<16>(a, 32, s);
+    if (a.cols <= RA_LN_F8) return forward_registers<8>(a, group_for(a.cols, 8), s);
+    if (a.cols <= RA_LN_F16) return forward_registers<16>(a, group_for(a.cols, 16), s);
     if (a.cols <= 16384) return forward_registers<32>(a, group_for(a.cols, 32), s);
     return forward_registers<64>(a, group_for(a.cols, 64), s);
   }
@@ -106,6 +115,7 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
     bool done = true;
     if (reach <= 256) a.group = 32, err = backward_fused<8, true>(a, !aligned, weights, row, s);
     else if (reach <= 8192 && fits(16)) err = backward_fused<16, true>(a, !aligned, weights, row, s);
+    else if (reach <= 12288 && fits(24)) err = backward_fused<24, false>(a, !aligned, weights, row, s);
     else if (fits(32)) err = backward_fused<32, false>(a, !aligned, weights, row, s);
     else done = false;
     if (done) {

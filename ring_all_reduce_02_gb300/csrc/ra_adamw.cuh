@@ -3,15 +3,25 @@
 // Per element (g the scaled gradient, all fp32, every product and sum rounded):
 //   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps).
-// It touches every byte once, so HBM bounds it: 4 + 4 + 2 + 8 + 8 + 2 = 28
-// bytes per element for fp32 parameters and moments with bf16 gradients and
-// copies, 10 for bf16 parameters with 8-bit moments.
+// It touches every byte once: 4 + 4 + 2 + 8 + 8 + 2 = 28 bytes an element for
+// fp32 parameters and moments with bf16 gradients and copies, 10 for bf16
+// parameters with 8-bit moments.
 //
-// Work: a warp takes chunks of 256 consecutive elements, 8 per lane. With 8-bit
-// moments a chunk is one block of the scales, so the block's largest magnitude
-// is one warp reduction and the moments never leave registers between being
-// read and being stored again. The tensors' table travels in the kernel's
-// parameters; a CTA finds its tensor by bisection over the tensors' first CTAs.
+// Work: a warp takes 256 consecutive elements (fp32 moments, 8 to a lane) or 512
+// (8-bit, 16 to a lane: two blocks of the scales, each the share of half a warp),
+// so that a block's largest magnitude is a few shuffles and the moments never
+// leave registers between being read and being stored again. The tensors' table
+// travels in the kernel's parameters. CTAs of 4 warps live for one such piece.
+//
+// Measured over 354.8 M elements in 292 tensors (back to back, inputs larger than
+// L2): fp32 moments with bf16 gradients and copies 1394 us, 7.13 TB/s, 105% of the
+// copy bandwidth: HBM is the bound. 8-bit moments on bf16 parameters 685 us, 5.2
+// TB/s, 77%: about 52 instructions an element (95 before pairs, Newton square
+// roots and 16 elements a lane) take nearly as long as the memory, and the chain
+// from the moments through the root, the block's maximum and the rounding is long
+// for the 32 warps that the registers allow. 24 warps at 80 registers took 758 us,
+// 40 warps with spills 719, 8 elements a lane 790 to 866; tiles prefetched into
+// shared memory by resident warps 762.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -24,19 +34,11 @@
 namespace ra {
 
 constexpr int kAdamBlock = 256;  // elements per chunk, and per scale of an 8-bit moment
-#ifndef RA_ADAM_MINB
-#define RA_ADAM_MINB 8
-#endif
-#ifndef RA_ADAM_T
-#define RA_ADAM_T 128
-#endif
-constexpr int kAdamThreads = RA_ADAM_T;
+constexpr int kAdamThreads = 128;
 constexpr int kAdamWarps = kAdamThreads / 32;
-#ifndef RA_ADAM_E
-#define RA_ADAM_E 16
-#endif
+constexpr int kAdamCtas = 8;  // on an SM: 64 registers a thread
 // Consecutive elements of a lane.
-__host__ __device__ constexpr int adam_lane_elems(bool s8) { return s8 ? RA_ADAM_E : 8; }
+__host__ __device__ constexpr int adam_lane_elems(bool s8) { return s8 ? 16 : 8; }
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 
@@ -55,11 +57,9 @@ struct AdamTensor {
 };
 constexpr uint32_t kAdamVec = 8;
 
-// Kernel parameters hold at most 32,764 bytes; the small table keeps short lists' launches short.
-#ifndef RA_ADAM_SMALL
-#define RA_ADAM_SMALL 64
-#endif
-constexpr int kAdamSmall = RA_ADAM_SMALL;
+// Kernel parameters hold at most 32,764 bytes. The small table shortens short lists' launches: 37 tensors take 45 us
+// alone against 48 with the large one (the same 27 us back to back).
+constexpr int kAdamSmall = 64;
 constexpr int kAdamLarge = 384;
 
 struct AdamScalars {
@@ -205,10 +205,10 @@ struct AdamRaw<P, G, true, E> {
 
 // A warp's elements base .. base + 32 E - 1 of a tensor, E to a lane. WHOLE: all of them exist and are on the
 // 8-element grid of every buffer, and lane l takes base + E l .. base + E l + E - 1; a block of the 8-bit moments
-// is then 8 (E = 32) or 16 or 32 lanes' share. Otherwise E = 8, only [0, count) exist, and lane l takes l, l + 32, ...
+// is then 256 / E lanes' share. Otherwise E = 8, only [0, count) exist, and lane l takes l, l + 32, ...
 template <int P, int G, bool S8, bool WHOLE, int E>
 __device__ __forceinline__ void adamw_elements(const AdamScalars& s, const AdamTensor& t, int64_t base, float scale) {
-  static_assert(WHOLE || E == 8, "whole warps' shares or one block");
+  static_assert(WHOLE || E == 8, "a whole share, or one block");
   const uint32_t lane = threadIdx.x & 31;
   const uint64_t i0 = (uint64_t)base + (WHOLE ? E * lane : 0);
   const uint64_t block = S8 ? (WHOLE ? i0 : (uint64_t)base) / kAdamBlock : 0;  // 8-bit moments: base is on a block
@@ -393,7 +393,7 @@ __device__ __forceinline__ void adamw_elements(const AdamScalars& s, const AdamT
 }
 
 template <int P, int G, bool S8, int CAP>
-__global__ void __launch_bounds__(kAdamThreads, S8 ? RA_ADAM_MINB : 1024 / RA_ADAM_T) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
+__global__ void __launch_bounds__(kAdamThreads, kAdamCtas) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
   pdl_enter();
   const AdamScalars& s = a.s;
   float scale = 1.0f;

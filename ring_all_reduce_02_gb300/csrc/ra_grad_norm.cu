@@ -19,15 +19,12 @@
 namespace ra {
 
 constexpr int kNormThreads = 256;
-#ifndef RA_NORM_U
-#define RA_NORM_U 4
-#endif
-#ifndef RA_NORM_CTAS
-#define RA_NORM_CTAS 456
-#endif
-constexpr int kNormUnroll = RA_NORM_U;        // 32-byte vectors a thread has in flight
-constexpr int kNormCtas = RA_NORM_CTAS;       // CTAs at most, a partial each: 8 on each of 152 SMs
-constexpr int kNormSmall = 32;        // tensors in the small and the large table: kernel parameters hold 32,764 bytes
+// 456 CTAs (3 on each of 152 SMs) of 256 threads with four 32-byte vectors in flight each. Measured, 354.8 M fp32
+// gradients / one layer's 12.6 M bf16 (back to back): 200 us (7.1 TB/s, 105% of the copy bandwidth) / 7.9 us; two
+// vectors 265 / 8.9, one 445 / 11.7; 1216 CTAs 198 / 11.4 (the last CTA waits for more tickets), 304 CTAs 213 / 7.8.
+constexpr int kNormUnroll = 4;
+constexpr int kNormCtas = 456;
+constexpr int kNormSmall = 32;  // tensors in the small and the large table: kernel parameters hold 32,764 bytes
 constexpr int kNormLarge = 1024;
 // Elements of a tile.
 __host__ __device__ constexpr int norm_tile(int es) { return kNormThreads * kNormUnroll * 32 / es; }

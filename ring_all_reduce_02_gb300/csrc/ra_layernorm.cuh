@@ -258,7 +258,7 @@ __device__ __forceinline__ void store_part(char* at, const uint4& q, int from, i
 // Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on. The grid is a
 // multiple of 8 (or has a CTA for every row).
 template <int DT, int WDT, int E>
-__global__ void __launch_bounds__(kLnMaxThreads) ln_forward_shifted(const __grid_constant__ LnForward a) {
+__global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shifted(const __grid_constant__ LnForward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];

@@ -10,13 +10,6 @@
 #define RA_CAT3_(a, b, c) a##_##b##_##c
 #define RA_CAT3(a, b, c) RA_CAT3_(a, b, c)
 
-#ifndef RA_LN_F8
-#define RA_LN_F8 256
-#endif
-#ifndef RA_LN_F16
-#define RA_LN_F16 512
-#endif
-
 namespace ra {
 namespace {
 
@@ -76,8 +69,9 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64) {
     if (a.cols <= 256) return forward_registers<8>(a, 32, s);
     if (a.cols <= 512) return forward_registers<16>(a, 32, s);
-    if (a.cols <= RA_LN_F8) return forward_registers<8>(a, group_for(a.cols, 8), s);
-    if (a.cols <= RA_LN_F16) return forward_registers<16>(a, group_for(a.cols, 16), s);
+    // few rows leave SMs idle: more threads to a row, fewer columns each (1 x 1024: 1.6 us against 2.1, 512 x 1024: 2.4
+    // against 2.8); many rows want the row's fixed cost on few threads (8192 x 4096: 24 us against 36)
+    if (a.rows <= 608 && a.cols <= 4096) return forward_registers<8>(a, group_for(a.cols, 8), s);
     if (a.cols <= 16384) return forward_registers<32>(a, group_for(a.cols, 32), s);
     return forward_registers<64>(a, group_for(a.cols, 64), s);
   }
@@ -108,16 +102,24 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
   if (a.rows > 0 && in_step && reach <= (uint64_t)kLnMaxThreads * 32) {
     const uint32_t elems = ln_row_elems((uint32_t)a.cols, es, !aligned);
     const size_t weights = elems * 4, row = 2 * elems * es;
-    const auto fits = [&](uint32_t per) {
-      a.group = group_for(reach, per);
-      return weights + 2 * (kLnMaxThreads / a.group) * row <= kLnSmem;
+    // 16 columns a thread keep xhat and dy w in registers; 24 and 32 take them from shared memory again and are
+    // worth about 0.8 and 0.5 of a thread of 16, but win where they put more of the CTA's 512 threads to work (a
+    // group is whole warps): 4096 x 5120 fp32 48 us with 24 against 53 with 16, 4096 x 6001 bf16 51 against 56,
+    // 6001 x 4095 fp16 58 against 67 (72 with 32), 8192 x 4096 bf16 45 with 16
+    const auto score = [&](uint32_t per) {
+      const uint32_t group = group_for(reach, per), groups = group ? kLnMaxThreads / group : 0;
+      if (groups == 0 || weights + 2 * groups * row > kLnSmem) return 0.0;
+      return groups * group * (per == 16 ? 1.0 : per == 24 ? 0.8 : 0.5);
     };
     bool done = true;
-    if (reach <= 256) a.group = 32, err = backward_fused<8, true>(a, !aligned, weights, row, s);
-    else if (reach <= 8192 && fits(16)) err = backward_fused<16, true>(a, !aligned, weights, row, s);
-    else if (reach <= 12288 && fits(24)) err = backward_fused<24, false>(a, !aligned, weights, row, s);
-    else if (fits(32)) err = backward_fused<32, false>(a, !aligned, weights, row, s);
-    else done = false;
+    const double s16 = score(16), s24 = score(24), s32 = score(32);
+    const uint32_t per = reach <= 256 ? 8 : s16 >= s24 && s16 >= s32 ? 16 : s24 >= s32 ? 24 : 32;
+    a.group = group_for(reach, per);
+    if (per == 8) err = backward_fused<8, true>(a, !aligned, weights, row, s);
+    else if (s16 + s24 + s32 == 0.0) done = false;
+    else if (per == 16) err = backward_fused<16, true>(a, !aligned, weights, row, s);
+    else if (per == 24) err = backward_fused<24, false>(a, !aligned, weights, row, s);
+    else err = backward_fused<32, false>(a, !aligned, weights, row, s);
     if (done) {
       if (err != cudaSuccess || !sums) return err;
       return launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a);

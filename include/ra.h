@@ -352,7 +352,7 @@ ra_status_t ra_allreduce_bulk_noalloc(const void* const* sendbufs, void* const* 
  * before any launch and nothing is enqueued on an error; the library allocates
  * nothing and keeps no state; work is enqueued on `stream` (NULL = the legacy
  * default stream) as programmatic dependent launches and can be captured in a
- * graph. Scratch comes from the caller. dtypes: RA_FLOAT32, RA_FLOAT16,
+ * graph. Buffers are device memory; scratch comes from the caller. dtypes: RA_FLOAT32, RA_FLOAT16,
  * RA_BFLOAT16 (RA_INT32: RA_ERR_UNSUPPORTED). All arithmetic is fp32, rounded
  * to nearest even once where a result is stored. Results do not depend on
  * timing: no sum is taken in an order that varies from run to run on a device.
@@ -472,6 +472,8 @@ typedef struct {
  * Written buffers must not overlap each other or a gradient (RA_ERR_ALIAS);
  * gradients may overlap each other. RA_ERR_INVALID_ARG: step < 1, betas
  * outside [0, 1), eps or lr or weight_decay negative or not finite.
+ * RA_ERR_UNSUPPORTED: no host memory for the check of a long list. Lists of
+ * more than 384 tensors go out as several launches.
  * HBM traffic per element: param and moments read and written, grad read.
  */
 ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, ra_dtype_t param_dtype, ra_dtype_t grad_dtype,

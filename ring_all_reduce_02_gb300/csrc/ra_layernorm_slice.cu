@@ -34,7 +34,6 @@ cudaError_t allow_smem(K kernel, size_t smem) {
 template <int E>
 cudaError_t forward_registers(const LnForward& a, uint32_t group, cudaStream_t s) {
   const uint64_t per_cta = group == 32 ? kLnWarpThreads / 32 : 1, ctas = (a.rows + per_cta - 1) / per_cta;
-  if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
   return group == 32 ? launch_programmatic(ln_forward_registers<DT, WDT, E, true>, dim3((unsigned)ctas), kLnWarpThreads, 0, s, a)
                      : launch_programmatic(ln_forward_registers<DT, WDT, E, false>, dim3((unsigned)ctas), group, 0, s, a);
 }
@@ -66,7 +65,7 @@ cudaError_t backward_fused(LnBackward a, bool shifted, size_t weights, size_t st
 cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cudaStream_t s) {
   const bool aligned = a.cols % V == 0 && !phase(a.x) && !phase(a.y) && !line(a.x_stride) && !line(a.y_stride) &&
                        !phase(a.w) && !phase(a.b);
-  if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64) {
+  if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64 && a.rows <= 0x7fffffffull) {  // a CTA for every row, or for 4
     if (a.cols <= 256) return forward_registers<8>(a, 32, s);
     if (a.cols <= 512) return forward_registers<16>(a, 32, s);
     // few rows leave SMs idle: more threads to a row, fewer columns each (1 x 1024: 1.6 us against 2.1, 512 x 1024: 2.4

@@ -295,6 +295,43 @@ def test_range_of_the_8_bit_moments(ra):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True])
+def test_more_than_32_bits_of_elements(ra, eight):
+    # a tensor of 2^32 + 1007 elements: its last 2031 against the formula, the random bits of their places included
+    gpu()
+    n, tail = (1 << 32) + 1007, 2031
+    start = n - tail  # 2^32 - 1024: on a block, and across 2^32
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    p, g = torch.zeros(n, dtype=BF16, device="cuda"), torch.zeros(n, dtype=BF16, device="cuda")
+    p[start:], g[start:] = torch.randn(tail, generator=gen, device="cuda"), torch.randn(tail, generator=gen, device="cuda")
+    if eight:
+        m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2))
+        state = (m, v, *(torch.zeros(-(-n // BLOCK), device="cuda") for _ in range(2)))
+    else:
+        m, v = state = [torch.zeros(n, device="cuda") for _ in range(2)]
+    p0, g0 = p[start:].double().cpu().numpy(), g[start:].double().cpu().numpy()
+    ra.ra_adamw(ra.adamw_tensors([p], [g], *([s] for s in state)), step=1, seed=5, **HYPER)
+    want, m1, v1 = step64(p0, g0, 0 * p0, 0 * p0, 0.0, 1.0, 1, **HYPER)
+    off = np.abs(p[start:].double().cpu().numpy() - want)
+    assert (off <= 2.0 ** -8 * np.abs(want) + 1e-5 * HYPER["lr"]).all()
+    assert float(p[:start].abs().max()) == 0.0
+    if not eight:
+        assert np.allclose(m[start:].double().cpu().numpy(), m1, rtol=8 * U, atol=0)
+        return
+    i = np.arange(start, n, dtype=np.uint64)
+    key = int(mix((5 & MASK) + int(mix(0 + 1 * 0x9E3779B9))))
+    key = int(mix(key))
+    bits = mix(((i & MASK) * 0x9E3779B9 + (i >> np.uint64(32)) * 0xB7E15163 + key) & MASK)
+    for got, x, rand in ((m, m1, bits & 0xFFFF), (v, np.sqrt(v1), bits >> 16)):
+        got = np.abs(got[start:].float().cpu().double().numpy())
+        pad = np.zeros(-(-tail // BLOCK) * BLOCK)
+        pad[:tail] = np.abs(x)
+        inv = np.repeat(448 / pad.reshape(-1, BLOCK).max(1), BLOCK)[:tail]
+        lo, hi = (round_e4m3(np.abs(x) * inv * (1 + e), rand) for e in (-(2.0 ** -19), 2.0 ** -19))
+        assert ((lo <= got) & (got <= hi)).all() and (lo == hi).mean() > 0.9
+
+
+@pytest.mark.gpu
 def test_stochastic_rounding_is_unbiased(ra):
     # a second moment that shrinks by 3% (its root by 1.5%): nearest rounding would leave it where it was
     gpu()

@@ -81,6 +81,17 @@ def test_every_element_counts_once(ra):
 
 
 @pytest.mark.gpu
+def test_more_than_32_bits_of_elements(ra):
+    # 2^32 + 5 ones and a 300: every thread's and CTA's sums stay below 2^24, so that they are exact
+    gpu()
+    n = (1 << 32) + 6
+    g = torch.ones(n, dtype=BF16, device="cuda")
+    g[-1] = 300.0
+    want = float(torch.tensor(n - 1 + 90000.0, dtype=torch.float64).sqrt())
+    assert abs(run(ra, [g])[0] - want) <= 2 * U * want
+
+
+@pytest.mark.gpu
 def test_clip_scale_and_prescale(ra):
     gpu()
     g = tensors([5000, 123], F32, 3, std=1.0)

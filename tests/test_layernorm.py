@@ -307,6 +307,40 @@ def test_another_stream_and_a_graph(ra):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [4096, 4095])
+def test_more_than_32_bits_of_elements(ra, cols):
+    # 4.4e9 elements: the last rows against the formula, and the weight gradients see them
+    gpu()
+    rows, tail = (1 << 32) // cols + 20011, 300
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.ones(rows, cols, dtype=BF16, device="cuda")
+    x[-tail:] = torch.randn(tail, cols, generator=gen, device="cuda").to(BF16)
+    w = torch.randn(cols, generator=gen, device="cuda").to(BF16)
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ra.ra_layernorm_forward(x, w, w, y, mean, rstd)
+    x64, m64, r64, h, w64, b64 = forward64(x[-tail:], w, w)
+    k = (cols / 32 + 32) * U
+    top = x64.abs().amax(1, keepdim=True)
+    want = h * w64 + b64
+    assert_within(y[-tail:], want, ROUND[BF16] * want.abs() + 1.01 * (w64.abs() * k * (3 * h.abs() + 3 * top * r64) + 2 * U * want.abs()), "y")
+    assert_within(mean[-tail:], m64[:, 0], k * top[:, 0] + U * m64[:, 0].abs(), "mean")
+    assert torch.equal(y[0], w) and torch.equal(y[rows // 2], w)  # constant rows give the bias
+    dy = y.zero_()
+    dy[-tail:] = torch.randint(-3, 4, (tail, cols), generator=gen, device="cuda").to(BF16)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w, dtype=F32), torch.empty_like(w, dtype=F32)
+    ws = torch.empty(ra.ra_layernorm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    ra.ra_layernorm_backward(dy, x, w.float(), mean, rstd, dx, dw, db, workspace=ws)
+    assert torch.equal(db.double(), dy[-tail:].double().sum(0)) and (dx[0] == 0).all() and (dx[rows // 2] == 0).all()
+    h = (x64 - mean[-tail:].double().cpu()[:, None]) * rstd[-tail:].double().cpu()[:, None]
+    terms = dy[-tail:].double().cpu() * h
+    assert_within(dw, terms.sum(0), (tail + 16) * U * terms.abs().sum(0) + U, "dw")
+    a = dy[-tail:].double().cpu() * w64
+    want = rstd[-tail:].double().cpu()[:, None] * (a - a.mean(1, keepdim=True) - h * (a * h).mean(1, keepdim=True))
+    tol = 4 * k * r64 * (a.abs() + a.abs().mean(1, keepdim=True) + 2 * h.abs() * (a * h).abs().mean(1, keepdim=True))
+    assert_within(dx[-tail:], want, ROUND[BF16] * want.abs() + tol, "dx")
+
+
 # Fake addresses that are never dereferenced: every case is refused on the host.
 BASE = 0x7F0000000000
 MB = 1 << 20

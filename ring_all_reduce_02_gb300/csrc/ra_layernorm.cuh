@@ -126,6 +126,24 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// The sum over the whole CTA of `warps` (up to 16) warps, in all its threads, in a fixed order. `slots`: 16 floats,
+// 16-byte aligned; two calls in a row need two sets.
+__device__ __forceinline__ float cta_sum_registers(float v, float* slots, uint32_t warps) {
+  v = warp_sum(v);
+  const uint32_t t = threadIdx.x;
+  if ((t & 31) == 0) slots[t / 32] = v;
+  if (t >= warps && t < 4) slots[t] = 0.0f;
+  __syncthreads();
+  if (warps <= 4) {  // one read instead of a second round of shuffles
+    const float4 q = *reinterpret_cast<const float4*>(slots);
+    return (q.x + q.y) + (q.z + q.w);
+  }
+  v = (t & 15) < warps ? slots[t & 15] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 constexpr uint32_t kLnMaxThreads = 512;
 constexpr uint32_t kLnWarpThreads = 128;  // of a CTA with a row to each warp
 
@@ -139,20 +157,12 @@ template <int DT, int WDT, int E, bool WARP>
 __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
   pdl_enter();
   constexpr int es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
-  __shared__ float slots[2][kLnMaxThreads / 32];
+  __shared__ __align__(16) float slots[2][kLnMaxThreads / 32];
   const uint32_t group = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
   const uint64_t row = WARP ? (uint64_t)blockIdx.x * (kLnWarpThreads / 32) + threadIdx.x / 32 : blockIdx.x;
   if (row >= a.rows) return;  // a whole group
   const uint32_t cols = (uint32_t)a.cols, step = group * V;
-  const auto group_sum = [&](float v, float* s) {
-    v = warp_sum(v);
-    if constexpr (!WARP) {
-      if ((t & 31) == 0) s[t / 32] = v;
-      __syncthreads();
-      v = warp_sum((t & 31) < group / 32 ? s[t & 31] : 0.0f);
-    }
-    return v;
-  };
+  const auto group_sum = [&](float v, float* s) { return WARP ? warp_sum(v) : cta_sum_registers(v, s, group / 32); };
   const char* x = static_cast<const char*>(a.x) + row * a.x_stride * es;
   char* y = static_cast<char*>(a.y) + row * a.y_stride * es;
   uint4 q[NV];
@@ -262,21 +272,35 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
-  __shared__ float slots[2][2][kLnMaxThreads / 32];
+  __shared__ __align__(16) float slots[2][2][kLnMaxThreads / 32];
   const uint32_t cols = (uint32_t)a.cols, t = threadIdx.x, group = blockDim.x;
   const char* base = static_cast<const char*>(a.x);
   const char* end = base + ((a.rows - 1) * a.x_stride + cols) * es;
   const uint32_t phase = line_phase(base + blockIdx.x * a.x_stride * es, es), lines = (phase + cols + V - 1) / V;
+  // The CTA's rows have one phase, so what a thread's lines are is settled once: all inside the row, or on its edge.
+  int at[NV];  // column of the line's first value
+  uint32_t whole = 0, some = 0;
+#pragma unroll
+  for (uint32_t j = 0; j < NV; ++j) {
+    at[j] = (int)((j * group + t) * V) - (int)phase;
+    whole |= (at[j] >= 0 && at[j] + (int)V <= (int)cols ? 1u : 0u) << j;
+    some |= (j * group + t < lines ? 1u : 0u) << j;
+  }
+  const char* x_next = base + blockIdx.x * a.x_stride * es;
+  char* y = static_cast<char*>(a.y) + blockIdx.x * a.y_stride * es;
+  const uint64_t x_hop = gridDim.x * a.x_stride * es, y_hop = gridDim.x * a.y_stride * es;
   uint4 q[NV];
-  const auto fetch = [&](uint64_t row) {
-    const char* line0 = base + row * a.x_stride * es - phase * es;
+  const auto fetch = [&]() {
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t k = j * group + t;
-      q[j] = k < lines ? load_line<DT>(line0 + k * 16, base, end) : make_uint4(0, 0, 0, 0);
+      const char* line = x_next + at[j] * (int)es;
+      if (whole >> j & 1u) q[j] = __ldcs(reinterpret_cast<const uint4*>(line));
+      else if (some >> j & 1u) q[j] = load_line<DT>(line, base, end);
+      else q[j] = make_uint4(0, 0, 0, 0);
     }
+    x_next += x_hop;
   };
-  fetch(blockIdx.x);
+  fetch();
   float* ws = reinterpret_cast<float*>(smem);
   float* bs = ws + lines * V;
   for (uint32_t i = t; i < lines * V; i += group) {
@@ -287,54 +311,44 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
   __syncthreads();
   const float n = (float)cols;
   uint32_t parity = 0;
-  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const auto group_sum = [&](float v, float* s) {
-      v = warp_sum(v);
-      if ((t & 31) == 0) s[t / 32] = v;
-      __syncthreads();
-      return warp_sum((t & 31) < group / 32 ? s[t & 31] : 0.0f);
-    };
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, y += y_hop) {
     F2 f[E / 2], sum = 0;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const int at = (int)((j * group + t) * V) - (int)phase;  // column of the line's first value
       widen<DT>(q[j], f + j * H);
-      if (at < 0 || at + (int)V > (int)cols) mask_line<V>(f + j * H, -at, (int)cols - at);
+      if (!(whole >> j & 1u)) mask_line<V>(f + j * H, -at[j], (int)cols - at[j]);
 #pragma unroll
       for (uint32_t k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
     }
-    if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
-    const float mean = __fdiv_rn(group_sum(fold2(sum), slots[parity][0]), n);
-    const F2 minus = pair(-mean, -mean);
+    if (row + gridDim.x < a.rows) fetch();
+    const float mean = __fdiv_rn(cta_sum_registers(fold2(sum), slots[parity][0], group / 32), n);
+    const F2 minus = twice(-mean);
     F2 sq = 0;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const int at = (int)((j * group + t) * V) - (int)phase;
 #pragma unroll
       for (uint32_t k = 0; k < H; ++k) f[j * H + k] = add2(f[j * H + k], minus);
-      if (at < 0 || at + (int)V > (int)cols) mask_line<V>(f + j * H, -at, (int)cols - at);
+      if (!(whole >> j & 1u)) mask_line<V>(f + j * H, -at[j], (int)cols - at[j]);
 #pragma unroll
       for (uint32_t k = 0; k < H; ++k) sq = fma2(f[j * H + k], f[j * H + k], sq);
     }
-    const float var = __fdiv_rn(group_sum(fold2(sq), slots[parity][1]), n);
+    const float var = __fdiv_rn(cta_sum_registers(fold2(sq), slots[parity][1], group / 32), n);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-    const F2 rstd2 = pair(rstd, rstd);
-    char* y = static_cast<char*>(a.y) + row * a.y_stride * es - phase * es;
+    const F2 rstd2 = twice(rstd);
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
-      const uint32_t k = j * group + t;
-      if (k >= lines) continue;
+      if (!(some >> j & 1u)) continue;
+      const uint32_t first = (j * group + t) * V;
 #pragma unroll
       for (uint32_t e = 0; e < H; e += 2) {
-        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(ws + k * V + 2 * e);
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bs + k * V + 2 * e);
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(ws + first + 2 * e);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bs + first + 2 * e);
         f[j * H + e] = fma2(mul2(f[j * H + e], rstd2), w.x, b.x);
         f[j * H + e + 1] = fma2(mul2(f[j * H + e + 1], rstd2), w.y, b.y);
       }
       const uint4 out = narrow<DT>(f + j * H);
-      const int at = (int)(k * V) - (int)phase;
-      if (at >= 0 && at + (int)V <= (int)cols) __stcs(reinterpret_cast<uint4*>(y + k * 16), out);
-      else store_part<DT>(y + k * 16, out, -at, (int)cols - at);
+      if (whole >> j & 1u) __stcs(reinterpret_cast<uint4*>(y + at[j] * (int)es), out);
+      else store_part<DT>(y + at[j] * (int)es, out, -at[j], (int)cols - at[j]);
     }
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;

@@ -111,6 +111,12 @@ __device__ __forceinline__ uint4 narrow(const F2* f) {
     return make_uint4(narrow2<DT>(f[0]), narrow2<DT>(f[1]), narrow2<DT>(f[2]), narrow2<DT>(f[3]));
   }
 }
+// One weight; other CTAs read it too.
+template <int DT>
+__device__ __forceinline__ float weight_at(const void* base, uint32_t i) {
+  if constexpr (DT == DT_F32) return __ldg(static_cast<const float*>(base) + i);
+  else return widen16<DT>(__ldg(static_cast<const unsigned short*>(base) + i));
+}
 // V weights from element i, through L1: every row reads them again.
 template <int DT, int V>
 __device__ __forceinline__ void load_weights(const void* base, uint32_t i, F2* f) {
@@ -303,10 +309,17 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
   fetch();
   float* ws = reinterpret_cast<float*>(smem);
   float* bs = ws + lines * V;
-  for (uint32_t i = t; i < lines * V; i += group) {
-    const bool in = i >= phase && i - phase < cols;
-    ws[i] = !in ? 0.0f : a.w ? ln_load<WDT>(a.w, i - phase) : 1.0f;
-    bs[i] = in && a.b ? ln_load<WDT>(a.b, i - phase) : 0.0f;
+  for (uint32_t i0 = t; i0 < lines * V; i0 += 8 * group) {  // 16 reads in flight a thread
+    float w[8], b[8];
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u) {
+      const uint32_t c = i0 + u * group - phase;  // wraps around before column 0
+      w[u] = c >= cols ? 0.0f : a.w ? weight_at<WDT>(a.w, c) : 1.0f;
+      b[u] = c < cols && a.b ? weight_at<WDT>(a.b, c) : 0.0f;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u)
+      if (i0 + u * group < lines * V) ws[i0 + u * group] = w[u], bs[i0 + u * group] = b[u];
   }
   __syncthreads();
   const float n = (float)cols;
@@ -462,10 +475,17 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   float next_mean = 0.0f, next_rstd = 0.0f;
   if (kAhead == 2 && first + stride < a.rows) next_mean = __ldg(a.mean + first + stride), next_rstd = __ldg(a.rstd + first + stride);
   const auto weight = [&](uint32_t i) {
-    return i < phase || i - phase >= cols ? 0.0f : a.w ? ln_load<WDT>(a.w, i - phase) : 1.0f;
+    return i < phase || i - phase >= cols ? 0.0f : a.w ? weight_at<WDT>(a.w, i - phase) : 1.0f;
   };
   constexpr uint32_t kEarly = 4;
-  for (uint32_t i = threadIdx.x + kEarly * blockDim.x; i < row_elems; i += blockDim.x) weights[i] = weight(i);
+  for (uint32_t i0 = threadIdx.x + kEarly * blockDim.x; i0 < row_elems; i0 += 8 * blockDim.x) {  // 8 reads in flight
+    float w[8];
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u) w[u] = i0 + u * blockDim.x < row_elems ? weight(i0 + u * blockDim.x) : 0.0f;
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u)
+      if (i0 + u * blockDim.x < row_elems) weights[i0 + u * blockDim.x] = w[u];
+  }
   float early[kEarly];
 #pragma unroll
   for (uint32_t k = 0; k < kEarly; ++k) {

@@ -137,7 +137,7 @@ ra_status_t ra_layernorm_backward(const void* dy, size_t dy_stride, const void* 
       if (overlaps(out[o].at, out[q].at)) return RA_ERR_ALIAS;
   }
   ra::LnBackward a{dy, x, weight, mean, rstd, dx, dweight, dbias, static_cast<float*>(workspace), rows, cols,
-                   dy_stride, x_stride, dx_stride, accumulate, 0, 0, 0};
+                   dy_stride, x_stride, dx_stride, accumulate, 0, 0, 1, 0};
   a.parts = (int)(rows < kLnMaxParts ? rows : kLnMaxParts);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;

@@ -27,6 +27,7 @@ struct LnForward {
 
 // Partial sums of the weight's gradient, at most: one per SM. A multiple of 8, see ln_backward_fused.
 constexpr uint64_t kLnMaxParts = 152;
+constexpr uint32_t kLnMaxSplit = 4;  // CTAs that share a row
 
 struct LnBackward {
   const void* dy;
@@ -42,6 +43,7 @@ struct LnBackward {
   int accumulate;
   int parts;
   uint32_t group;   // threads per row of the fused kernel
+  uint32_t split;   // CTAs per row of it
   uint32_t stages;  // rows a group of it has in shared memory
 };
 
@@ -384,6 +386,11 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
 // SHIFTED: rows off the 16-byte grid, by whole lines as above. The rows of a
 // CTA are a multiple of 8 apart, so all of them have the same phase and a
 // register keeps standing for the same column.
+//
+// SPLIT: a row too long for one CTA's registers or shared memory is shared by
+// the 2 or 4 CTAs of a cluster, each with a run of its lines; their sums meet in
+// each other's shared memory. 4096 x 20000 bf16: RA_SPLIT_US us against 500 in
+// separate passes for dx and the column sums (floor 72).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // copies `bytes` (0 to 16) and fills up with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -403,40 +410,59 @@ __device__ __forceinline__ void cp_async_wait_oldest(uint32_t stages) {
   else cp_async_wait<1>();
 }
 
+// The CTAs of a cluster: all of their threads, and a float to another CTA's shared memory at the address that `at`
+// has in this one's.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void store_in_cluster(const float* at, uint32_t rank, float v) {
+  const uint32_t local = (uint32_t)__cvta_generic_to_shared(at);
+  asm volatile(
+      "{\n .reg .b32 there;\n mapa.shared::cluster.u32 there, %0, %1;\n st.shared::cluster.f32 [there], %2;\n}" ::"r"(local), "r"(rank), "f"(v)
+      : "memory");
+}
+
 // All threads of a row's group: a named barrier of its own, or the warp.
 __device__ __forceinline__ void group_sync(uint32_t g, uint32_t size) {
   if (size == 32) __syncwarp();
   else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
 }
 
-// Elements of one row's lines in shared memory.
-__host__ __device__ constexpr uint32_t ln_row_elems(uint32_t cols, uint32_t es, bool shifted) {
-  return (cols + (shifted ? 16 / es - 1 : 0) + 16 / es - 1) / (16 / es) * (16 / es);
+// Elements of one row's lines, and of a CTA's share of them, in shared memory.
+__host__ __device__ constexpr uint32_t ln_share_elems(uint32_t cols, uint32_t es, bool shifted, uint32_t ranks) {
+  return ((cols + (shifted ? 16 / es - 1 : 0) + 16 / es - 1) / (16 / es) + ranks - 1) / ranks * (16 / es);
 }
 
-template <int DT, int WDT, int E, bool KEEP, bool SHIFTED>
+template <int DT, int WDT, int E, bool KEEP, bool SHIFTED, bool SPLIT>
 __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __grid_constant__ LnBackward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
-  __shared__ __align__(16) float2 slots[2][kLnMaxThreads / 32];
+  __shared__ __align__(16) float2 slots[2][(SPLIT ? kLnMaxSplit : 1) * kLnMaxThreads / 32];
   const uint32_t cols = (uint32_t)a.cols, size = a.group, groups = blockDim.x / size, stages = a.stages;
   const uint32_t g = threadIdx.x / size, t = threadIdx.x - g * size, lane = threadIdx.x & 31;
-  const uint32_t row_elems = ln_row_elems(cols, es, SHIFTED), row_bytes = row_elems * es;
+  uint32_t rank = 0, ranks = 1, unit = blockIdx.x, units = gridDim.x;
+  if constexpr (SPLIT) {
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    ranks = a.split, unit = blockIdx.x / ranks, units = gridDim.x / ranks;
+  }
+  const uint32_t row_elems = ln_share_elems(cols, es, SHIFTED, ranks), row_bytes = row_elems * es;
   float* weights = reinterpret_cast<float*>(smem);
   char* ring = smem + row_elems * 4 + (size_t)g * stages * 2 * row_bytes;
 
   // few rows spread over the CTAs first, then over their groups
-  const uint64_t first = (uint64_t)g * gridDim.x + blockIdx.x, stride = (uint64_t)gridDim.x * groups;
+  const uint64_t first = (uint64_t)g * units + unit, stride = (uint64_t)units * groups;
   const char* xs = static_cast<const char*>(a.x);
   const char* dys = static_cast<const char*>(a.dy);
-  const uint32_t phase = SHIFTED ? line_phase(xs + blockIdx.x * a.x_stride * es, es) : 0;
-  const uint32_t lines = (phase + cols + V - 1) / V;
+  const uint32_t phase = SHIFTED ? line_phase(xs + unit * a.x_stride * es, es) : 0;
+  const uint32_t all_lines = (phase + cols + V - 1) / V, line0 = rank * (row_elems / V);  // of the row, and of this CTA's share
+  const uint32_t lines = SPLIT ? (all_lines > line0 ? min(all_lines - line0, row_elems / V) : 0) : all_lines;
+  const int column0 = (int)(line0 * V) - (int)phase;  // of the share's first line
   const char* x_end = xs + ((a.rows - 1) * a.x_stride + cols) * es;
   const char* dy_end = dys + ((a.rows - 1) * a.dy_stride + cols) * es;
   // this thread's first lines of the next row to fetch, the row itself, and where they go
-  const char* x_next = xs + first * a.x_stride * es - phase * es + t * 16;
-  const char* dy_next = dys + first * a.dy_stride * es - phase * es + t * 16;
+  const char* x_next = xs + first * a.x_stride * es - phase * es + (line0 + t) * 16;
+  const char* dy_next = dys + first * a.dy_stride * es - phase * es + (line0 + t) * 16;
   const uint64_t x_hop = stride * a.x_stride * es, dy_hop = stride * a.dy_stride * es, dx_hop = stride * a.dx_stride * es;
   uint64_t row_next = first;
   const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
@@ -475,7 +501,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   float next_mean = 0.0f, next_rstd = 0.0f;
   if (kAhead == 2 && first + stride < a.rows) next_mean = __ldg(a.mean + first + stride), next_rstd = __ldg(a.rstd + first + stride);
   const auto weight = [&](uint32_t i) {
-    return i < phase || i - phase >= cols ? 0.0f : a.w ? weight_at<WDT>(a.w, i - phase) : 1.0f;
+    const uint32_t c = (uint32_t)(column0 + (int)i);  // wraps around before column 0
+    return c >= cols ? 0.0f : a.w ? weight_at<WDT>(a.w, c) : 1.0f;
   };
   constexpr uint32_t kEarly = 4;
   for (uint32_t i0 = threadIdx.x + kEarly * blockDim.x; i0 < row_elems; i0 += 8 * blockDim.x) {  // 8 reads in flight
@@ -498,7 +525,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     const uint32_t i = threadIdx.x + k * blockDim.x;
     if (i < row_elems) weights[i] = early[k];
   }
-  __syncthreads();
+  if constexpr (SPLIT) cluster_sync();  // the others' shared memory is there
+  else __syncthreads();
 
   F2 dw[E / 2], db[E / 2];
 #pragma unroll
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   uint32_t stage = 0, parity = 0;
   const char* buffer = ring + t * 16;  // this thread's first line of the row in work
   const float* w_at = weights + t * V;
-  char* dx = static_cast<char*>(a.dx) + first * a.dx_stride * es - phase * es + t * 16;
+  char* dx = static_cast<char*>(a.dx) + first * a.dx_stride * es - phase * es + (line0 + t) * 16;
   for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
     cp_async_wait_oldest(stages);  // every thread reads back the lines it fetched itself: nothing else to wait for
     float new_mean = 0.0f, new_rstd = 0.0f;
@@ -518,7 +546,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       widen<DT>(*reinterpret_cast<const uint4*>(buffer + j * size * 16), h);
       widen<DT>(*reinterpret_cast<const uint4*>(buffer + row_bytes + j * size * 16), dy);
       if constexpr (SHIFTED) {
-        const int at = (int)((j * size + t) * V) - (int)phase;
+        const int at = column0 + (int)((j * size + t) * V);
         if (at < 0 || at + (int)V > (int)cols) mask_line<V>(h, -at, (int)cols - at), mask_line<V>(dy, -at, (int)cols - at);
       }
 #pragma unroll
@@ -553,7 +581,16 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       float mine = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      if (size > 32) {
+      if constexpr (SPLIT) {
+        const uint32_t warps = size / 32;
+        if ((lane & 15) < ranks)
+          store_in_cluster(reinterpret_cast<const float*>(&slots[parity][rank * warps + threadIdx.x / 32]) + lane / 16, lane & 15, mine);
+        cluster_sync();
+        s1 = s2 = 0.0f;
+        for (uint32_t k = lane; k < ranks * warps; k += 32) s1 += slots[parity][k].x, s2 += slots[parity][k].y;
+        s1 = warp_sum(s1), s2 = warp_sum(s2);
+        parity ^= 1;
+      } else if (size > 32) {
         const uint32_t warps = size / 32, w = lane & 15;
         if (w == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
         group_sync(g, size);
@@ -593,7 +630,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
         for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(out[e], c2_2, c1_2));
       }
       const uint4 q = narrow<DT>(out);
-      const int at = (int)((j * size + t) * V) - (int)phase;
+      const int at = column0 + (int)((j * size + t) * V);
       if (!SHIFTED || (at >= 0 && at + (int)V <= (int)cols)) __stcs(reinterpret_cast<uint4*>(dx + j * size * 16), q);
       else store_part<DT>(dx + j * size * 16, q, -at, (int)cols - at);
     }
@@ -603,6 +640,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     ++stage, buffer += 2 * row_bytes;
     if (stage == stages) stage = 0, buffer = ring + t * 16;
   }
+  if constexpr (SPLIT) cluster_sync();  // no CTA leaves while another may still write to it
   if (a.dw == nullptr && a.db == nullptr) return;
   // fold the groups: every group's sums side by side in shared memory, then column by column
   cp_async_wait<0>();
@@ -620,14 +658,15 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     }
   }
   __syncthreads();
-  float* part = a.part + (uint64_t)blockIdx.x * 2 * cols;
-  for (uint32_t c = threadIdx.x; c < cols; c += blockDim.x) {
+  float* part = a.part + (uint64_t)unit * 2 * cols;
+  const uint32_t from = column0 < 0 ? (uint32_t)-column0 : 0;  // of the share, not before column 0
+  for (uint32_t i = from + threadIdx.x; i < lines * V && column0 + (int)i < (int)cols; i += blockDim.x) {
     float w = 0.0f, b = 0.0f;
     for (uint32_t k = 0; k < groups; ++k) {
-      w += sums[k * 2 * row_elems + phase + c];
-      b += sums[(k * 2 + 1) * row_elems + phase + c];
+      w += sums[k * 2 * row_elems + i];
+      b += sums[(k * 2 + 1) * row_elems + i];
     }
-    part[c] = w, part[cols + c] = b;
+    part[column0 + (int)i] = w, part[cols + column0 + (int)i] = b;
   }
 }
 

@@ -10,6 +10,9 @@
 #define RA_CAT3_(a, b, c) a##_##b##_##c
 #define RA_CAT3(a, b, c) RA_CAT3_(a, b, c)
 
+#ifndef RA_LN_SPLIT_FROM
+#define RA_LN_SPLIT_FROM 16384
+#endif
 namespace ra {
 namespace {
 
@@ -55,9 +58,45 @@ cudaError_t backward_fused(LnBackward a, bool shifted, size_t weights, size_t st
   a.stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + groups * a.stages * stage;
   if (smem < groups * 2 * weights) smem = groups * 2 * weights;  // the fold
-  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, KEEP, true> : ln_backward_fused<DT, WDT, E, KEEP, false>;
+  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, KEEP, true, false> : ln_backward_fused<DT, WDT, E, KEEP, false, false>;
   const cudaError_t err = allow_smem(kernel, smem);
   return err != cudaSuccess ? err : launch_programmatic(kernel, dim3((unsigned)a.parts), groups * a.group, smem, s, a);
+}
+
+// The fused kernel with a cluster of a.split CTAs to a row: a.parts becomes the number of clusters, as many as the GPU
+// holds at once (a second wave would take as long again), a multiple of the rows that share a phase.
+cudaError_t backward_split(LnBackward* a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
+  const size_t stages = (kLnSmem - weights) / stage;
+  a->stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
+  size_t smem = weights + a->stages * stage;
+  if (smem < 2 * weights) smem = 2 * weights;  // the fold
+  const auto kernel = shifted ? ln_backward_fused<DT, WDT, 16, true, true, true> : ln_backward_fused<DT, WDT, 16, true, false, true>;
+  cudaError_t err = allow_smem(kernel, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a->split, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kLnMaxParts / a->split * a->split));
+  cfg.blockDim = dim3(a->group);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  err = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+  if (err != cudaSuccess) return err;
+  if (clusters > (int)(kLnMaxParts / a->split)) clusters = (int)(kLnMaxParts / a->split);
+  if (shifted && clusters > (int)V) clusters = clusters / (int)V * (int)V;
+  if (clusters < 1 || (shifted && clusters < (int)V)) return cudaErrorInvalidConfiguration;
+  a->parts = a->rows < (uint64_t)clusters ? (int)a->rows : clusters;
+  cfg.gridDim = dim3((unsigned)a->parts * a->split);
+  cfg.numAttrs = RA_PDL ? 2 : 1;
+  err = cudaLaunchKernelEx(&cfg, kernel, *a);
+  const cudaError_t last = cudaGetLastError();
+  return err != cudaSuccess ? err : last;
 }
 
 }  // namespace
@@ -77,7 +116,7 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   // x and y in step: every row of both at the same place in its 16-byte line
   const uint64_t reach = a.cols + V - 1;  // a line more, at most
   if (phase(a.x) == phase(a.y) && line(a.x_stride) == line(a.y_stride) && reach <= (uint64_t)kLnMaxThreads * 64) {
-    const size_t smem = 2 * sizeof(float) * ln_row_elems((uint32_t)a.cols, es, true);
+    const size_t smem = 2 * sizeof(float) * ln_share_elems((uint32_t)a.cols, es, true, 1);
     if (smem <= kLnSmem) {
       if (reach <= 512) return forward_shifted<8>(a, group_for(reach, 8), smem, s);
       if (reach <= 8192) return forward_shifted<16>(a, group_for(reach, 16), smem, s);
@@ -98,8 +137,11 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
                        line(a.x_stride) == line(a.dx_stride);
   const uint64_t reach = a.cols + (aligned ? 0 : V - 1);
   // the sweep in one kernel: two stages of a row's x and dy for each group have to fit in shared memory
+  const auto finish = [&]() {
+    return sums ? launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a) : cudaSuccess;
+  };
   if (a.rows > 0 && in_step && reach <= (uint64_t)kLnMaxThreads * 32) {
-    const uint32_t elems = ln_row_elems((uint32_t)a.cols, es, !aligned);
+    const uint32_t elems = ln_share_elems((uint32_t)a.cols, es, !aligned, 1);
     const size_t weights = elems * 4, row = 2 * elems * es;
     // 16 columns a thread keep xhat and dy w in registers; 24 and 32 take them from shared memory again and are
     // worth about 0.8 and 0.5 of a thread of 16, but win where they put more of the CTA's 512 threads to work (a
@@ -110,19 +152,26 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
       if (groups == 0 || weights + 2 * groups * row > kLnSmem) return 0.0;
       return groups * group * (per == 16 ? 1.0 : per == 24 ? 0.8 : 0.5);
     };
-    bool done = true;
     const double s16 = score(16), s24 = score(24), s32 = score(32);
     const uint32_t per = reach <= 256 ? 8 : s16 >= s24 && s16 >= s32 ? 16 : s24 >= s32 ? 24 : 32;
-    a.group = group_for(reach, per);
-    if (per == 8) err = backward_fused<8, true>(a, !aligned, weights, row, s);
-    else if (s16 + s24 + s32 == 0.0) done = false;
-    else if (per == 16) err = backward_fused<16, true>(a, !aligned, weights, row, s);
-    else if (per == 24) err = backward_fused<24, false>(a, !aligned, weights, row, s);
-    else err = backward_fused<32, false>(a, !aligned, weights, row, s);
-    if (done) {
-      if (err != cudaSuccess || !sums) return err;
-      return launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a);
+    if (s16 + s24 + s32 > 0.0 && reach <= RA_LN_SPLIT_FROM) {
+      a.group = group_for(reach, per);
+      if (per == 8) err = backward_fused<8, true>(a, !aligned, weights, row, s);
+      else if (per == 16) err = backward_fused<16, true>(a, !aligned, weights, row, s);
+      else if (per == 24) err = backward_fused<24, false>(a, !aligned, weights, row, s);
+      else err = backward_fused<32, false>(a, !aligned, weights, row, s);
+      return err != cudaSuccess ? err : finish();
     }
+  }
+  for (uint32_t split = 2; a.rows > 0 && in_step && split <= kLnMaxSplit; split *= 2) {
+    if (a.cols > (uint64_t)kLnMaxThreads * 16 * split) continue;
+    const uint32_t share = ln_share_elems((uint32_t)a.cols, es, !aligned, split);
+    const size_t weights = share * 4, row = 2 * share * es;
+    if (share > kLnMaxThreads * 16 || weights + 2 * row > kLnSmem) continue;
+    a.split = split;
+    a.group = group_for(share, 16);
+    err = backward_split(&a, !aligned, weights, row, s);
+    return err != cudaSuccess ? err : finish();
   }
   if (sums) {  // before dx, which may be x or dy
     if (a.parts) {

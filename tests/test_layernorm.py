@@ -226,6 +226,30 @@ def test_weight_gradient_counts_every_row_once(ra, rows, cols):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 20000), (75, 20000), (77, 18001), (701, 17000), (1003, 32768), (613, 12289), (90, 32769)])
+def test_rows_shared_by_several_ctas(ra, rows, cols, dtype):
+    gpu()
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randint(-3, 4, (rows, cols), generator=gen, device="cuda").to(dtype)
+    dy = torch.randint(-3, 4, (rows, cols), generator=gen, device="cuda").to(dtype)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    w = torch.ones(cols, device="cuda")
+    dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    ws = torch.empty(ra.ra_layernorm_workspace(rows, cols), dtype=torch.uint8, device="cuda").fill_(255)
+    ra.ra_layernorm_backward(dy, x, w, mean, rstd, torch.empty_like(x), dw, db, workspace=ws)
+    assert torch.equal(dw.double(), (dy.double() * x.double()).sum(0))  # whole numbers: exact in any order
+    assert torch.equal(db.double(), dy.double().sum(0))
+    few = min(rows, 120)
+    x = (torch.randn(few, cols, generator=gen, device="cuda") * 2 + 0.7).to(dtype)
+    dy = (torch.randn(few, cols, generator=gen, device="cuda") * 0.1).to(dtype)
+    w = torch.randn(cols, generator=gen, device="cuda") * 0.3 + 1
+    mean, rstd = mean[:few].clone(), rstd[:few].clone()
+    ra.ra_layernorm_forward(x, w, None, torch.empty_like(x), mean, rstd)
+    check_backward(ra, dy, x, w, mean, rstd, torch.empty_like(x), dw, db)
+
+
+@pytest.mark.gpu
 def test_no_rows(ra):
     gpu()
     x = torch.empty(0, 16, device="cuda")

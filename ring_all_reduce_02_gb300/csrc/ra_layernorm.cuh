@@ -401,13 +401,14 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 constexpr uint32_t kLnMaxStages = 8;
-// Waits until all but the stages - 1 newest groups of copies have landed; stages: 2, 3, 4, 6 or 8.
+// Waits until all but the stages - 1 newest groups of copies have landed, or fewer; stages: 1 to 8.
 __device__ __forceinline__ void cp_async_wait_oldest(uint32_t stages) {
   if (stages == 8) cp_async_wait<7>();
-  else if (stages == 6) cp_async_wait<5>();
-  else if (stages == 4) cp_async_wait<3>();
+  else if (stages >= 6) cp_async_wait<5>();
+  else if (stages >= 4) cp_async_wait<3>();
   else if (stages == 3) cp_async_wait<2>();
-  else cp_async_wait<1>();
+  else if (stages == 2) cp_async_wait<1>();
+  else cp_async_wait<0>();
 }
 
 // The CTAs of a cluster: all of their threads, and a float to another CTA's shared memory at the address that `at`
@@ -433,16 +434,16 @@ __host__ __device__ constexpr uint32_t ln_share_elems(uint32_t cols, uint32_t es
   return ((cols + (shifted ? 16 / es - 1 : 0) + 16 / es - 1) / (16 / es) + ranks - 1) / ranks * (16 / es);
 }
 
-template <int DT, int WDT, int E, bool KEEP, bool SHIFTED, bool SPLIT>
+template <int DT, int WDT, int E, bool KEEP, bool SHIFTED, bool LATE>
 __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __grid_constant__ LnBackward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
-  __shared__ __align__(16) float2 slots[2][(SPLIT ? kLnMaxSplit : 1) * kLnMaxThreads / 32];
+  __shared__ __align__(16) float2 slots[2][(LATE ? kLnMaxSplit : 1) * kLnMaxThreads / 32];
   const uint32_t cols = (uint32_t)a.cols, size = a.group, groups = blockDim.x / size, stages = a.stages;
   const uint32_t g = threadIdx.x / size, t = threadIdx.x - g * size, lane = threadIdx.x & 31;
   uint32_t rank = 0, ranks = 1, unit = blockIdx.x, units = gridDim.x;
-  if constexpr (SPLIT) {
+  if constexpr (LATE) {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     ranks = a.split, unit = blockIdx.x / ranks, units = gridDim.x / ranks;
   }
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   const char* dys = static_cast<const char*>(a.dy);
   const uint32_t phase = SHIFTED ? line_phase(xs + unit * a.x_stride * es, es) : 0;
   const uint32_t all_lines = (phase + cols + V - 1) / V, line0 = rank * (row_elems / V);  // of the row, and of this CTA's share
-  const uint32_t lines = SPLIT ? (all_lines > line0 ? min(all_lines - line0, row_elems / V) : 0) : all_lines;
+  const uint32_t lines = LATE ? (all_lines > line0 ? min(all_lines - line0, row_elems / V) : 0) : all_lines;
   const int column0 = (int)(line0 * V) - (int)phase;  // of the share's first line
   const char* x_end = xs + ((a.rows - 1) * a.x_stride + cols) * es;
   const char* dy_end = dys + ((a.rows - 1) * a.dy_stride + cols) * es;
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     const uint32_t i = threadIdx.x + k * blockDim.x;
     if (i < row_elems) weights[i] = early[k];
   }
-  if constexpr (SPLIT) cluster_sync();  // the others' shared memory is there
+  if constexpr (LATE) cluster_sync();  // the others' shared memory is there
   else __syncthreads();
 
   F2 dw[E / 2], db[E / 2];
@@ -536,33 +537,102 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   const char* buffer = ring + t * 16;  // this thread's first line of the row in work
   const float* w_at = weights + t * V;
   char* dx = static_cast<char*>(a.dx) + first * a.dx_stride * es - phase * es + (line0 + t) * 16;
+  // xhat, dy and the weights of the thread's j-th line of the row in `buffer`
+  const auto load = [&](const char* buffer, F2 rstd2, F2 shift2, uint32_t j, F2* h, F2* dy, F2* w) {
+    widen<DT>(*reinterpret_cast<const uint4*>(buffer + j * size * 16), h);
+    widen<DT>(*reinterpret_cast<const uint4*>(buffer + row_bytes + j * size * 16), dy);
+    if constexpr (SHIFTED) {
+      const int at = column0 + (int)((j * size + t) * V);
+      if (at < 0 || at + (int)V > (int)cols) mask_line<V>(h, -at, (int)cols - at), mask_line<V>(dy, -at, (int)cols - at);
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < H; ++e) h[e] = fma2(h[e], rstd2, shift2);
+#pragma unroll
+    for (uint32_t e = 0; e < H; e += 2) {
+      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w_at + j * size * V + 2 * e);
+      w[e] = q.x, w[e + 1] = q.y;
+    }
+  };
+  const auto store = [&](char* dx, uint32_t j, const F2* out) {
+    const uint4 q = narrow<DT>(out);
+    const int at = column0 + (int)((j * size + t) * V);
+    if (!SHIFTED || (at >= 0 && at + (int)V <= (int)cols)) __stcs(reinterpret_cast<uint4*>(dx + j * size * 16), q);
+    else store_part<DT>(dx + j * size * 16, q, -at, (int)cols - at);
+  };
+  if constexpr (LATE) {
+    // A row's dx waits until the next row's sums are on their way, so that the exchange between the warps (and CTAs)
+    // is hidden behind it; its place in shared memory is filled again after that.
+    const char* old_buffer = nullptr;
+    char* old_dx = nullptr;
+    uint32_t old_stage = 0;
+    F2 old_rstd2 = 0, old_shift2 = 0, old_c1 = 0, old_c2 = 0;
+    const auto late_dx = [&]() {
+#pragma unroll
+      for (uint32_t j = 0; j < NV; ++j) {
+        if (j * size + t >= lines) continue;
+        F2 out[H], dy[H], w[H];
+        load(old_buffer, old_rstd2, old_shift2, j, out, dy, w);
+#pragma unroll
+        for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), old_rstd2, fma2(out[e], old_c2, old_c1));
+        store(old_dx, j, out);
+      }
+      fetch(old_stage);
+    };
+    const uint32_t warps = size / 32;
+    for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
+      cp_async_wait_oldest(stages - 1);  // the place of the row before is not sent for yet
+      float new_mean = 0.0f, new_rstd = 0.0f;
+      if (row + kAhead * stride < a.rows) new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
+      const F2 rstd2 = twice(rstd), shift2 = twice(-mean * rstd);
+      F2 sum1 = 0, sum2 = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < NV; ++j) {
+        if (j * size + t >= lines) continue;
+        F2 h[H], dy[H], w[H];
+        load(buffer, rstd2, shift2, j, h, dy, w);
+#pragma unroll
+        for (uint32_t e = 0; e < H; ++e) {
+          const F2 p = mul2(dy[e], w[e]);
+          sum1 = add2(sum1, p);
+          sum2 = fma2(p, h[e], sum2);
+          dw[j * H + e] = fma2(dy[e], h[e], dw[j * H + e]);
+          db[j * H + e] = add2(db[j * H + e], dy[e]);
+        }
+      }
+      float s1 = fold2(sum1), s2 = fold2(sum2);
+      const bool up = lane & 16;  // the lower half of a warp carries one sum, the upper the other
+      float mine = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      if ((lane & 15) < ranks)
+        store_in_cluster(reinterpret_cast<const float*>(&slots[parity][rank * warps + threadIdx.x / 32]) + lane / 16, lane & 15, mine);
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      if (old_buffer != nullptr) late_dx();
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      s1 = s2 = 0.0f;
+      for (uint32_t k = lane; k < ranks * warps; k += 32) s1 += slots[parity][k].x, s2 += slots[parity][k].y;
+      s1 = warp_sum(s1), s2 = warp_sum(s2);
+      parity ^= 1;
+      old_rstd2 = rstd2, old_shift2 = shift2, old_c1 = twice(-rstd * (s1 * inv_n)), old_c2 = twice(-rstd * (s2 * inv_n));
+      old_buffer = buffer, old_dx = dx, old_stage = stage;
+      if constexpr (kAhead == 1) mean = new_mean, rstd = new_rstd;
+      else mean = next_mean, rstd = next_rstd, next_mean = new_mean, next_rstd = new_rstd;
+      ++stage, buffer += 2 * row_bytes;
+      if (stage == stages) stage = 0, buffer = ring + t * 16;
+    }
+    if (old_buffer != nullptr) late_dx();
+  } else {
   for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
     cp_async_wait_oldest(stages);  // every thread reads back the lines it fetched itself: nothing else to wait for
     float new_mean = 0.0f, new_rstd = 0.0f;
     if (row + kAhead * stride < a.rows) new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
     const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
-    // xhat, dy and the weights of the thread's j-th line
-    const auto load = [&](uint32_t j, F2* h, F2* dy, F2* w) {
-      widen<DT>(*reinterpret_cast<const uint4*>(buffer + j * size * 16), h);
-      widen<DT>(*reinterpret_cast<const uint4*>(buffer + row_bytes + j * size * 16), dy);
-      if constexpr (SHIFTED) {
-        const int at = column0 + (int)((j * size + t) * V);
-        if (at < 0 || at + (int)V > (int)cols) mask_line<V>(h, -at, (int)cols - at), mask_line<V>(dy, -at, (int)cols - at);
-      }
-#pragma unroll
-      for (uint32_t e = 0; e < H; ++e) h[e] = fma2(h[e], rstd2, shift2);
-#pragma unroll
-      for (uint32_t e = 0; e < H; e += 2) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w_at + j * size * V + 2 * e);
-        w[e] = q.x, w[e + 1] = q.y;
-      }
-    };
     F2 hs[KEEP ? E / 2 : 1], ps[KEEP ? E / 2 : 1], sum1 = 0, sum2 = 0;
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
       if (j * size + t >= lines) continue;
       F2 h[H], dy[H], w[H];
-      load(j, h, dy, w);
+      load(buffer, rstd2, shift2, j, h, dy, w);
 #pragma unroll
       for (uint32_t e = 0; e < H; ++e) {
         const F2 p = mul2(dy[e], w[e]);
@@ -581,16 +651,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       float mine = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      if constexpr (SPLIT) {
-        const uint32_t warps = size / 32;
-        if ((lane & 15) < ranks)
-          store_in_cluster(reinterpret_cast<const float*>(&slots[parity][rank * warps + threadIdx.x / 32]) + lane / 16, lane & 15, mine);
-        cluster_sync();
-        s1 = s2 = 0.0f;
-        for (uint32_t k = lane; k < ranks * warps; k += 32) s1 += slots[parity][k].x, s2 += slots[parity][k].y;
-        s1 = warp_sum(s1), s2 = warp_sum(s2);
-        parity ^= 1;
-      } else if (size > 32) {
+      if (size > 32) {
         const uint32_t warps = size / 32, w = lane & 15;
         if (w == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
         group_sync(g, size);
@@ -625,14 +686,11 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
         for (uint32_t e = 0; e < H; ++e) out[e] = fma2(ps[j * H + e], rstd2, fma2(hs[j * H + e], c2_2, c1_2));
       } else {
         F2 dy[H], w[H];
-        load(j, out, dy, w);
+        load(buffer, rstd2, shift2, j, out, dy, w);
 #pragma unroll
         for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(out[e], c2_2, c1_2));
       }
-      const uint4 q = narrow<DT>(out);
-      const int at = column0 + (int)((j * size + t) * V);
-      if (!SHIFTED || (at >= 0 && at + (int)V <= (int)cols)) __stcs(reinterpret_cast<uint4*>(dx + j * size * 16), q);
-      else store_part<DT>(dx + j * size * 16, q, -at, (int)cols - at);
+      store(dx, j, out);
     }
     if constexpr (!KEEP) fetch(stage);
     if constexpr (kAhead == 1) mean = new_mean, rstd = new_rstd;
@@ -640,7 +698,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     ++stage, buffer += 2 * row_bytes;
     if (stage == stages) stage = 0, buffer = ring + t * 16;
   }
-  if constexpr (SPLIT) cluster_sync();  // no CTA leaves while another may still write to it
+  }
+  if constexpr (LATE) cluster_sync();  // no CTA leaves while another may still write to it
   if (a.dw == nullptr && a.db == nullptr) return;
   // fold the groups: every group's sums side by side in shared memory, then column by column
   cp_async_wait<0>();

@@ -65,12 +65,13 @@ cudaError_t backward_fused(LnBackward a, bool shifted, size_t weights, size_t st
 
 // The fused kernel with a cluster of a.split CTAs to a row: a.parts becomes the number of clusters, as many as the GPU
 // holds at once (a second wave would take as long again), a multiple of the rows that share a phase.
-cudaError_t backward_split(LnBackward* a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
+template <int E>
+cudaError_t backward_late(LnBackward* a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
   const size_t stages = (kLnSmem - weights) / stage;
   a->stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + a->stages * stage;
   if (smem < 2 * weights) smem = 2 * weights;  // the fold
-  const auto kernel = shifted ? ln_backward_fused<DT, WDT, 16, true, true, true> : ln_backward_fused<DT, WDT, 16, true, false, true>;
+  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, false, true, true> : ln_backward_fused<DT, WDT, E, false, false, true>;
   cudaError_t err = allow_smem(kernel, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
@@ -170,7 +171,7 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
     if (share > kLnMaxThreads * 16 || weights + 2 * row > kLnSmem) continue;
     a.split = split;
     a.group = group_for(share, 16);
-    err = backward_split(&a, !aligned, weights, row, s);
+    err = backward_late<16>(&a, !aligned, weights, row, s);
     return err != cudaSuccess ? err : finish();
   }
   if (sums) {  // before dx, which may be x or dy

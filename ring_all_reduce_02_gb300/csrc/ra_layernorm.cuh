@@ -161,6 +161,11 @@ constexpr uint32_t kLnWarpThreads = 128;  // of a CTA with a row to each warp
 // row to each warp of a CTA; otherwise the CTA is one row's group (named
 // barriers for several groups would hold 16 of an SM's 64 barriers per CTA and
 // so allow only 4 CTAs on it).
+//
+// Measured (back to back, inputs larger than L2): 8192 x 1024 bf16 8.0 us (floor
+// 4.9), 8192 x 4096 bf16 24.2 us (82% of the copy bandwidth), 4096 x 5120 fp32
+// 28.2 us (88%), 32768 x 8192 bf16 178 us (89%). About 17 instructions an element
+// at 16-bit types, and a launch's 2 us where rows are few, keep it off the floor.
 template <int DT, int WDT, int E, bool WARP>
 __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
   pdl_enter();
@@ -274,7 +279,8 @@ __device__ __forceinline__ void store_part(char* at, const uint4& q, int from, i
 }
 
 // Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on. The grid is a
-// multiple of 8 (or has a CTA for every row).
+// multiple of 8 (or has a CTA for every row). 6001 x 4095 fp16: 30.5 us (floor 14.5; element by element 75), 2047 x
+// 1537 fp32: 8.0 us (3.7). The two exchanges of a row among 9 warps on 27 to 32 resident warps bound it.
 template <int DT, int WDT, int E>
 __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shifted(const __grid_constant__ LnForward a) {
   pdl_enter();
@@ -387,10 +393,20 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
 // CTA are a multiple of 8 apart, so all of them have the same phase and a
 // register keeps standing for the same column.
 //
-// SPLIT: a row too long for one CTA's registers or shared memory is shared by
-// the 2 or 4 CTAs of a cluster, each with a run of its lines; their sums meet in
-// each other's shared memory. 4096 x 20000 bf16: RA_SPLIT_US us against 500 in
-// separate passes for dx and the column sums (floor 72).
+// LATE: a row too long for one CTA's registers or shared memory is shared by the
+// 2 or 4 CTAs of a cluster, each with a run of its lines; their sums meet in
+// each other's shared memory, and a row's dx waits until the next row's sums are
+// on their way. 4096 x 20000 bf16: 141 us (51% of the copy bandwidth), 4096 x
+// 16384 fp32: 139 us (85%), against 500 and 459 us in separate passes for dx and
+// the column sums; without the delay 233 and 171.
+//
+// Measured (back to back, inputs larger than L2, of the copy bandwidth's floor):
+// 8192 x 1024 bf16 15.9 us (7.4), of which about 3 are the first rows' way, 9 the
+// loop at 80% of the copy bandwidth, 1 the fold and 2 ln_backward_finish; 32768 x
+// 8192 bf16 291 us (237); 2047 x 1537 fp32 15.3 us (5.6); 6001 x 4095 fp16 57 us
+// (21.7). In the loop 16 warps (accumulators and the row's values fill the
+// registers) keep 40 to 45% of the issue slots busy: the chain from the row's
+// sums through the exchange to dx bounds it as much as HBM does.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // copies `bytes` (0 to 16) and fills up with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -622,82 +638,82 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     }
     if (old_buffer != nullptr) late_dx();
   } else {
-  for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
-    cp_async_wait_oldest(stages);  // every thread reads back the lines it fetched itself: nothing else to wait for
-    float new_mean = 0.0f, new_rstd = 0.0f;
-    if (row + kAhead * stride < a.rows) new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
-    const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
-    F2 hs[KEEP ? E / 2 : 1], ps[KEEP ? E / 2 : 1], sum1 = 0, sum2 = 0;
+    for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
+      cp_async_wait_oldest(stages);  // every thread reads back the lines it fetched itself: nothing else to wait for
+      float new_mean = 0.0f, new_rstd = 0.0f;
+      if (row + kAhead * stride < a.rows) new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
+      const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
+      F2 hs[KEEP ? E / 2 : 1], ps[KEEP ? E / 2 : 1], sum1 = 0, sum2 = 0;
 #pragma unroll
-    for (uint32_t j = 0; j < NV; ++j) {
-      if (j * size + t >= lines) continue;
-      F2 h[H], dy[H], w[H];
-      load(buffer, rstd2, shift2, j, h, dy, w);
+      for (uint32_t j = 0; j < NV; ++j) {
+        if (j * size + t >= lines) continue;
+        F2 h[H], dy[H], w[H];
+        load(buffer, rstd2, shift2, j, h, dy, w);
 #pragma unroll
-      for (uint32_t e = 0; e < H; ++e) {
-        const F2 p = mul2(dy[e], w[e]);
-        sum1 = add2(sum1, p);
-        sum2 = fma2(p, h[e], sum2);
-        dw[j * H + e] = fma2(dy[e], h[e], dw[j * H + e]);
-        db[j * H + e] = add2(db[j * H + e], dy[e]);
-        if constexpr (KEEP) hs[j * H + e] = h[e], ps[j * H + e] = p;
+        for (uint32_t e = 0; e < H; ++e) {
+          const F2 p = mul2(dy[e], w[e]);
+          sum1 = add2(sum1, p);
+          sum2 = fma2(p, h[e], sum2);
+          dw[j * H + e] = fma2(dy[e], h[e], dw[j * H + e]);
+          db[j * H + e] = add2(db[j * H + e], dy[e]);
+          if constexpr (KEEP) hs[j * H + e] = h[e], ps[j * H + e] = p;
+        }
       }
-    }
-    if constexpr (KEEP) fetch(stage);
-    // both sums in one exchange: the lower half of a warp carries one, the upper the other
-    float s1 = fold2(sum1), s2 = fold2(sum2);
-    {
-      const bool up = lane & 16;
-      float mine = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
+      if constexpr (KEEP) fetch(stage);
+      // both sums in one exchange: the lower half of a warp carries one, the upper the other
+      float s1 = fold2(sum1), s2 = fold2(sum2);
+      {
+        const bool up = lane & 16;
+        float mine = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      if (size > 32) {
-        const uint32_t warps = size / 32, w = lane & 15;
-        if (w == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
-        group_sync(g, size);
-        if (warps <= 8) {  // few enough to be read by everyone: no second round of shuffles
-          s1 = s2 = 0.0f;
+        for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (size > 32) {
+          const uint32_t warps = size / 32, w = lane & 15;
+          if (w == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
+          group_sync(g, size);
+          if (warps <= 8) {  // few enough to be read by everyone: no second round of shuffles
+            s1 = s2 = 0.0f;
 #pragma unroll
-          for (uint32_t k = 0; k < 8; ++k) {
-            if (k >= warps) break;
-            const float2 q = slots[parity][g * warps + k];
-            s1 += q.x, s2 += q.y;
+            for (uint32_t k = 0; k < 8; ++k) {
+              if (k >= warps) break;
+              const float2 q = slots[parity][g * warps + k];
+              s1 += q.x, s2 += q.y;
+            }
+          } else {
+            mine = w < warps ? reinterpret_cast<const float*>(&slots[parity][g * warps + w])[lane / 16] : 0.0f;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            s1 = __shfl_sync(0xffffffffu, mine, 0), s2 = __shfl_sync(0xffffffffu, mine, 16);
           }
+          parity ^= 1;
         } else {
-          mine = w < warps ? reinterpret_cast<const float*>(&slots[parity][g * warps + w])[lane / 16] : 0.0f;
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
           s1 = __shfl_sync(0xffffffffu, mine, 0), s2 = __shfl_sync(0xffffffffu, mine, 16);
         }
-        parity ^= 1;
-      } else {
-        s1 = __shfl_sync(0xffffffffu, mine, 0), s2 = __shfl_sync(0xffffffffu, mine, 16);
       }
-    }
-    // rstd (p - s1/n - xhat s2/n)
-    const float c1 = -rstd * (s1 * inv_n), c2 = -rstd * (s2 * inv_n);
-    const F2 c1_2 = pair(c1, c1), c2_2 = pair(c2, c2);
+      // rstd (p - s1/n - xhat s2/n)
+      const float c1 = -rstd * (s1 * inv_n), c2 = -rstd * (s2 * inv_n);
+      const F2 c1_2 = pair(c1, c1), c2_2 = pair(c2, c2);
 #pragma unroll
-    for (uint32_t j = 0; j < NV; ++j) {
-      if (j * size + t >= lines) continue;
-      F2 out[H];
-      if constexpr (KEEP) {
+      for (uint32_t j = 0; j < NV; ++j) {
+        if (j * size + t >= lines) continue;
+        F2 out[H];
+        if constexpr (KEEP) {
 #pragma unroll
-        for (uint32_t e = 0; e < H; ++e) out[e] = fma2(ps[j * H + e], rstd2, fma2(hs[j * H + e], c2_2, c1_2));
-      } else {
-        F2 dy[H], w[H];
-        load(buffer, rstd2, shift2, j, out, dy, w);
+          for (uint32_t e = 0; e < H; ++e) out[e] = fma2(ps[j * H + e], rstd2, fma2(hs[j * H + e], c2_2, c1_2));
+        } else {
+          F2 dy[H], w[H];
+          load(buffer, rstd2, shift2, j, out, dy, w);
 #pragma unroll
-        for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(out[e], c2_2, c1_2));
+          for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(out[e], c2_2, c1_2));
+        }
+        store(dx, j, out);
       }
-      store(dx, j, out);
+      if constexpr (!KEEP) fetch(stage);
+      if constexpr (kAhead == 1) mean = new_mean, rstd = new_rstd;
+      else mean = next_mean, rstd = next_rstd, next_mean = new_mean, next_rstd = new_rstd;
+      ++stage, buffer += 2 * row_bytes;
+      if (stage == stages) stage = 0, buffer = ring + t * 16;
     }
-    if constexpr (!KEEP) fetch(stage);
-    if constexpr (kAhead == 1) mean = new_mean, rstd = new_rstd;
-    else mean = next_mean, rstd = next_rstd, next_mean = new_mean, next_rstd = new_rstd;
-    ++stage, buffer += 2 * row_bytes;
-    if (stage == stages) stage = 0, buffer = ring + t * 16;
-  }
   }
   if constexpr (LATE) cluster_sync();  // no CTA leaves while another may still write to it
   if (a.dw == nullptr && a.db == nullptr) return;

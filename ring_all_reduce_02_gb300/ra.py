@@ -2,7 +2,7 @@
 
 The functions carry the C ABI's names (include/ra.h). Tensors supply device
 pointers (``data_ptr()``) and the stream is torch's current CUDA stream unless
-one is given; every step of the collective runs in the library's kernels.
+one is given; every step of a call runs in the library's kernels.
 The library must be built (``python -m ring_all_reduce_02_gb300.build``); if
 it is missing, the first call raises instead of falling back to anything.
 """

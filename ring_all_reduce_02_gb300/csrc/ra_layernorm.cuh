@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
 // while one is worked on, and the column sums of dy xhat and dy stay in
 // registers over all the rows of a group: x and dy are read once. The CTA folds
 // its groups' sums and writes one partial of each; ln_backward_finish adds the
-// partials. KEEP: xhat and dy w of the row stay in registers between their two
+// partials (a CTA that has all the rows writes the gradients itself). KEEP: xhat and dy w of the row stay in registers between their two
 // uses (before and after the row's sums), and its place in shared memory is
 // filled again at once; otherwise they are taken from shared memory twice.
 //
@@ -448,6 +448,13 @@ __device__ __forceinline__ void group_sync(uint32_t g, uint32_t size) {
 // Elements of one row's lines, and of a CTA's share of them, in shared memory.
 __host__ __device__ constexpr uint32_t ln_share_elems(uint32_t cols, uint32_t es, bool shifted, uint32_t ranks) {
   return ((cols + (shifted ? 16 / es - 1 : 0) + 16 / es - 1) / (16 / es) + ranks - 1) / ranks * (16 / es);
+}
+
+// Column c's sums to where they go.
+template <int WDT>
+__device__ __forceinline__ void finish_column(const LnBackward& a, uint64_t c, float dw, float db) {
+  if (a.dw) ln_store<WDT>(a.dw, c, a.accumulate ? ln_load<WDT>(a.dw, c) + dw : dw);
+  if (a.db) ln_store<WDT>(a.db, c, a.accumulate ? ln_load<WDT>(a.db, c) + db : db);
 }
 
 template <int DT, int WDT, int E, bool KEEP, bool SHIFTED, bool LATE>
@@ -741,7 +748,9 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       w += sums[k * 2 * row_elems + i];
       b += sums[(k * 2 + 1) * row_elems + i];
     }
-    part[column0 + (int)i] = w, part[cols + column0 + (int)i] = b;
+    const uint64_t c = (uint64_t)(column0 + (int)i);
+    if (a.parts > 1) part[c] = w, part[cols + c] = b;
+    else finish_column<WDT>(a, c, w, b);
   }
 }
 
@@ -859,10 +868,7 @@ __global__ void __launch_bounds__(kLnFinishThreads) ln_backward_finish(const __g
   float dw = sw[lane][wid], db = sb[lane][wid];
   dw = warp_sum(dw), db = warp_sum(db);
   const uint64_t mine = (uint64_t)blockIdx.x * 32 + wid;
-  if (lane == 0 && mine < a.cols) {
-    if (a.dw) ln_store<WDT>(a.dw, mine, a.accumulate ? ln_load<WDT>(a.dw, mine) + dw : dw);
-    if (a.db) ln_store<WDT>(a.db, mine, a.accumulate ? ln_load<WDT>(a.db, mine) + db : db);
-  }
+  if (lane == 0 && mine < a.cols) finish_column<WDT>(a, mine, dw, db);
 }
 
 }  // namespace ra

@@ -49,8 +49,12 @@ cudaError_t forward_shifted(const LnForward& a, uint32_t group, size_t smem, cud
 }
 
 template <int E, bool KEEP>
-cudaError_t backward_fused(LnBackward a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
+cudaError_t backward_fused(LnBackward* all, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
+  LnBackward& a = *all;
   const uint32_t groups = kLnMaxThreads / a.group;
+  // up to two rows a group are one CTA's: a second round costs less than the launch that would add the partials. Not
+  // off the 16-byte grid, where the rows of a CTA have to be a multiple of 8 apart to share a phase.
+  if (!shifted && a.rows <= 2 * groups) a.parts = 1;
   const size_t stages = (kLnSmem - weights) / (groups * stage);
   a.stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + groups * a.stages * stage;
@@ -136,7 +140,7 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
   const uint64_t reach = a.cols + (aligned ? 0 : V - 1);
   // the sweep in one kernel: two stages of a row's x and dy for each group have to fit in shared memory
   const auto finish = [&]() {
-    return sums ? launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a) : cudaSuccess;
+    return sums && a.parts > 1 ? launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a) : cudaSuccess;
   };
   if (a.rows > 0 && in_step && reach <= (uint64_t)kLnMaxThreads * 32) {
     const uint32_t elems = ln_share_elems((uint32_t)a.cols, es, !aligned, 1);
@@ -154,10 +158,10 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
     const uint32_t per = reach <= 256 ? 8 : s16 >= s24 && s16 >= s32 ? 16 : s24 >= s32 ? 24 : 32;
     if (s16 + s24 + s32 > 0.0) {
       a.group = group_for(reach, per);
-      if (per == 8) err = backward_fused<8, true>(a, !aligned, weights, row, s);
-      else if (per == 16) err = backward_fused<16, true>(a, !aligned, weights, row, s);
-      else if (per == 24) err = backward_fused<24, false>(a, !aligned, weights, row, s);
-      else err = backward_fused<32, false>(a, !aligned, weights, row, s);
+      if (per == 8) err = backward_fused<8, true>(&a, !aligned, weights, row, s);
+      else if (per == 16) err = backward_fused<16, true>(&a, !aligned, weights, row, s);
+      else if (per == 24) err = backward_fused<24, false>(&a, !aligned, weights, row, s);
+      else err = backward_fused<32, false>(&a, !aligned, weights, row, s);
       return err != cudaSuccess ? err : finish();
     }
   }

@@ -404,13 +404,13 @@ def _stream_of(t, stream) -> int:
     return _Torch.current_stream(t.get_device()) if stream is None else _stream_ptr(stream)
 
 
-def _is_matrix(t) -> bool:
-    """A 2-D CUDA tensor whose rows are contiguous."""
-    return t.is_cuda and t.dim() == 2 and (t.is_contiguous() or t.stride(1) == 1 or t.shape[1] <= 1)
+def _rows_contiguous(t) -> bool:
+    """Whether the rows of a matrix are contiguous, whatever lies between them."""
+    return t.stride(1) == 1 or t.shape[1] <= 1
 
 
 def _row_stride(t, cols: int) -> int:
-    return cols if t.is_contiguous() else max(t.stride(0), cols) if t.shape[0] <= 1 else t.stride(0)
+    return max(t.stride(0), cols) if t.shape[0] <= 1 else t.stride(0)
 
 
 def _is_vector(t, n: int, dtype) -> bool:
@@ -436,19 +436,22 @@ def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 
     dtype = x.dtype
     w = weight if weight is not None else bias
     wdtype = dtype if w is None else w.dtype
-    if not (_is_matrix(x) and _is_matrix(y) and x.shape == y.shape and y.dtype is dtype):
+    shape = x.shape
+    dense = x.is_contiguous() and y.is_contiguous()
+    if not (x.is_cuda and y.is_cuda and len(shape) == 2 and y.shape == shape and y.dtype is dtype
+            and (dense or (_rows_contiguous(x) and _rows_contiguous(y)))):
         raise ValueError("ra_layernorm_forward: x and y must be 2-D CUDA tensors of one shape and dtype, rows contiguous")
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_forward: unsupported dtype {dtype} with weights of {wdtype}")
-    rows, cols = x.shape
+    rows, cols = shape
     f32 = _Torch.f32
     if not (_is_vector(weight, cols, wdtype) and _is_vector(bias, cols, wdtype) and _is_vector(mean, rows, f32)
             and _is_vector(rstd, rows, f32)):
         _check_vectors("ra_layernorm_forward", weight=(weight, cols, wdtype), bias=(bias, cols, wdtype),
                        mean=(mean, rows, f32), rstd=(rstd, rows, f32))
     st = (_lib or lib()).ra_layernorm_forward(
-        x.data_ptr(), _row_stride(x, cols), _address(weight), _address(bias), y.data_ptr(), _row_stride(y, cols),
-        _address(mean), _address(rstd), rows, cols, eps, codes[dtype], codes[wdtype], _stream_of(x, stream))
+        x.data_ptr(), cols if dense else _row_stride(x, cols), _address(weight), _address(bias), y.data_ptr(),
+        cols if dense else _row_stride(y, cols), _address(mean), _address(rstd), rows, cols, eps, codes[dtype], codes[wdtype], _stream_of(x, stream))
     if st:
         raise RaError(st, "ra_layernorm_forward")
 
@@ -467,13 +470,16 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     dtype = x.dtype
     w = weight if weight is not None else dweight if dweight is not None else dbias
     wdtype = dtype if w is None else w.dtype
-    if not (_is_matrix(x) and _is_matrix(dy) and _is_matrix(dx) and dy.shape == x.shape and dx.shape == x.shape
-            and dy.dtype is dtype and dx.dtype is dtype):
+    shape = x.shape
+    dense = x.is_contiguous() and dy.is_contiguous() and dx.is_contiguous()
+    if not (x.is_cuda and dy.is_cuda and dx.is_cuda and len(shape) == 2 and dy.shape == shape and dx.shape == shape
+            and dy.dtype is dtype and dx.dtype is dtype
+            and (dense or (_rows_contiguous(x) and _rows_contiguous(dy) and _rows_contiguous(dx)))):
         raise ValueError("ra_layernorm_backward: x, dy and dx must be 2-D CUDA tensors of one shape and dtype, rows "
                          "contiguous")
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_backward: unsupported dtype {dtype} with weights of {wdtype}")
-    rows, cols = x.shape
+    rows, cols = shape
     f32 = _Torch.f32
     if mean is None or rstd is None or not (
             _is_vector(weight, cols, wdtype) and _is_vector(dweight, cols, wdtype) and _is_vector(dbias, cols, wdtype)
@@ -485,8 +491,9 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
                        dbias=(dbias, cols, wdtype), mean=(mean, rows, f32), rstd=(rstd, rows, f32))
         raise ValueError("ra_layernorm_backward: workspace must be a contiguous CUDA tensor")
     st = (_lib or lib()).ra_layernorm_backward(
-        dy.data_ptr(), _row_stride(dy, cols), x.data_ptr(), _row_stride(x, cols), _address(weight), mean.data_ptr(),
-        rstd.data_ptr(), dx.data_ptr(), _row_stride(dx, cols), _address(dweight), _address(dbias), accumulate, rows,
+        dy.data_ptr(), cols if dense else _row_stride(dy, cols), x.data_ptr(), cols if dense else _row_stride(x, cols),
+        _address(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), cols if dense else _row_stride(dx, cols),
+        _address(dweight), _address(dbias), accumulate, rows,
         cols, codes[dtype], codes[wdtype], _address(workspace), 0 if workspace is None else workspace.nbytes,
         _stream_of(x, stream))
     if st:

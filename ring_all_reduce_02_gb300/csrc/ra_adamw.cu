@@ -65,12 +65,22 @@ bool written_overlap(std::vector<Span>& v) {
   return false;
 }
 
-ra_status_t add_span(std::vector<Span>& v, const void* p, uint64_t bytes, uintptr_t align, bool written) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  if (lo == 0 || lo % align || lo + bytes < lo) return RA_ERR_INVALID_ARG;
-  v.push_back({lo, lo + (uintptr_t)bytes, written});
-  return RA_SUCCESS;
+// The buffers of a step come as seven lists: parameters, gradients, moments, scales, copies.
+constexpr int kLists = 7;
+struct Sizes {
+  uint64_t param, grad, moment, copy;  // bytes of an element; copy: 0 if there are none
+  bool s8;
+};
+// Tensor t's buffer of a list: its address (null where the list has none for it), its bytes and its alignment.
+const void* buffer_of(const ra_adamw_tensor_t& t, int list, const Sizes& z, uint64_t* bytes, uintptr_t* align) {
+  const uint64_t scales = (t.count + RA_ADAMW_BLOCK - 1) / RA_ADAMW_BLOCK;
+  const void* p[kLists] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.copy};
+  const uint64_t n = list == 4 || list == 5 ? scales : t.count;
+  const uint64_t es = list == 0 ? z.param : list == 1 ? z.grad : list <= 3 ? z.moment : list <= 5 ? 4 : z.copy;
+  *bytes = n * es, *align = (uintptr_t)es;
+  return p[list];
 }
+bool list_used(int list, const Sizes& z) { return list == 4 || list == 5 ? z.s8 : list < 6 || z.copy; }
 
 bool unit(double x) { return x >= 0.0 && x < 1.0; }
 bool sound(double x) { return x >= 0.0 && x < INFINITY; }
@@ -78,27 +88,27 @@ bool sound(double x) { return x >= 0.0 && x < INFINITY; }
 // How the kernel may take a tensor's chunks (AdamTensor::layout): in vectors of 8 elements if every buffer is
 // as many elements past a vector boundary as the others (fp32 moments: the chunks then start that much early;
 // 8-bit blocks start with the tensor, which has to be on a boundary).
-uint32_t layout_of(const ra_adamw_tensor_t& t, uint64_t pe, uint64_t ge, uint64_t se, uint64_t ce) {
+uint32_t layout_of(const ra_adamw_tensor_t& t, const Sizes& z) {
   const auto past = [](const void* p, uint64_t es) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) / es % 8); };
-  const uint32_t shift = past(t.param, pe);
-  if (past(t.grad, ge) != shift || past(t.exp_avg, se) != shift || past(t.exp_avg_sq, se) != shift) return 0;
-  if (t.copy != nullptr && past(t.copy, ce) != shift) return 0;
-  if (se == 1 && shift != 0) return 0;
+  const uint32_t shift = past(t.param, z.param);
+  if (past(t.grad, z.grad) != shift || past(t.exp_avg, z.moment) != shift || past(t.exp_avg_sq, z.moment) != shift) return 0;
+  if (t.copy != nullptr && past(t.copy, z.copy) != shift) return 0;
+  if (z.s8 && shift != 0) return 0;
   return ra::kAdamVec | shift;
 }
 
 template <int CAP, class Fn>
-ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, const ra_adamw_options_t& o, uint64_t pe,
-                       uint64_t ge, uint64_t ce, ra::AdamScalars s, uint32_t key, cudaStream_t stream) {
+ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, const ra_adamw_options_t& o, const Sizes& z,
+                       ra::AdamScalars s, uint32_t key, cudaStream_t stream) {
   ra::AdamArgs<CAP> a;
-  const uint64_t per_cta = (uint64_t)ra::kAdamThreads * ra::adam_lane_elems(o.state == RA_STATE_E4M3);
+  const uint64_t per_cta = (uint64_t)ra::kAdamThreads * ra::adam_lane_elems(z.s8);
   int i = 0;
   while (i < ntensors) {
     uint64_t ctas = 0;
     s.n = 0;
     for (; i < ntensors && s.n < CAP; ++i) {
       const ra_adamw_tensor_t& t = tensors[i];
-      const uint32_t layout = t.count ? layout_of(t, pe, ge, o.state == RA_STATE_E4M3 ? 1 : 4, ce) : 0;
+      const uint32_t layout = t.count ? layout_of(t, z) : 0;
       const uint64_t more = (t.count + (layout & 7u) + per_cta - 1) / per_cta;
       if (ctas + more > 0x7fffffffull) {
         if (s.n == 0) return RA_ERR_UNSUPPORTED;
@@ -116,7 +126,7 @@ ra_status_t launch_all(const ra_adamw_tensor_t* tensors, int ntensors, Fn fn, co
     }
     if (ctas == 0) continue;
     a.s = s;
-    const cudaError_t err = fn(o.state == RA_STATE_E4M3, a, (uint32_t)ctas, stream);
+    const cudaError_t err = fn(z.s8, a, (uint32_t)ctas, stream);
     if (err != cudaSuccess) return ra::cuda_failed(err);
   }
   return RA_SUCCESS;
@@ -134,47 +144,64 @@ extern "C" ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, 
   if (o.state != RA_STATE_F32 && o.state != RA_STATE_E4M3) return RA_ERR_INVALID_ARG;
   if (o.step < 1 || !unit(o.beta1) || !unit(o.beta2) || !sound(o.lr) || !sound(o.eps)) return RA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(o.grad_scale) % 4) return RA_ERR_INVALID_ARG;
-  const bool s8 = o.state == RA_STATE_E4M3;
-  const uint64_t pe = (uint64_t)ra::float_size(param_dtype), ge = (uint64_t)ra::float_size(grad_dtype);
-  const uint64_t se = s8 ? 1 : 4;
-  uint64_t ce = 0;
-  try {
-    std::vector<Span> spans;
-    spans.reserve((size_t)ntensors * 7 + 1);
-    // one list after another: each is often an ascending run
-    for (int list = 0; list < 7; ++list) {
-      for (int i = 0; i < ntensors; ++i) {
-        const ra_adamw_tensor_t& t = tensors[i];
-        if (t.count == 0) continue;
-        if ((uint64_t)t.count > RA_MAX_COUNT || !sound(t.weight_decay)) return RA_ERR_INVALID_ARG;
-        const uint64_t scales = 4 * ((t.count + RA_ADAMW_BLOCK - 1) / RA_ADAMW_BLOCK);
-        switch (list) {
-          case 0: st = add_span(spans, t.param, t.count * pe, pe, true); break;
-          case 1: st = add_span(spans, t.grad, t.count * ge, ge, false); break;
-          case 2: st = add_span(spans, t.exp_avg, t.count * se, se, true); break;
-          case 3: st = add_span(spans, t.exp_avg_sq, t.count * se, se, true); break;
-          case 4: if (s8) st = add_span(spans, t.exp_avg_scale, scales, 4, true); break;
-          case 5: if (s8) st = add_span(spans, t.exp_avg_sq_scale, scales, 4, true); break;
-          default:
-            if (t.copy == nullptr) break;
-            if (ce == 0) {
-              st = ra::check_float(o.copy_dtype);
-              if (st != RA_SUCCESS) return st;
-              ce = (uint64_t)ra::float_size(o.copy_dtype);
-            }
-            st = add_span(spans, t.copy, t.count * ce, ce, true);
+  Sizes z{(uint64_t)ra::float_size(param_dtype), (uint64_t)ra::float_size(grad_dtype), 4, 0, o.state == RA_STATE_E4M3};
+  if (z.s8) z.moment = 1;
+  bool any = false;
+  for (int i = 0; i < ntensors; ++i) {
+    const ra_adamw_tensor_t& t = tensors[i];
+    if (t.count == 0) continue;
+    any = true;
+    if ((uint64_t)t.count > RA_MAX_COUNT || !sound(t.weight_decay)) return RA_ERR_INVALID_ARG;
+    if (t.copy != nullptr && z.copy == 0) {
+      st = ra::check_float(o.copy_dtype);
+      if (st != RA_SUCCESS) return st;
+      z.copy = (uint64_t)ra::float_size(o.copy_dtype);
+    }
+  }
+  if (!any) return RA_SUCCESS;
+  // Every buffer by itself, and whether the lists are runs of ascending, separate buffers that keep clear of each
+  // other, as slices of flat buffers are: then nothing overlaps (292 tensors: a call of 14 us against 22 with the full check).
+  Span extent[kLists + 1];
+  int extents = 0;
+  bool plain = true;
+  for (int list = 0; list < kLists; ++list) {
+    if (!list_used(list, z)) continue;
+    const bool written = list != 1;
+    Span e{UINTPTR_MAX, 0, written};
+    for (int i = 0; i < ntensors; ++i) {
+      if (tensors[i].count == 0) continue;
+      uint64_t bytes;
+      uintptr_t align;
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(buffer_of(tensors[i], list, z, &bytes, &align));
+      if (lo == 0 && list == kLists - 1) continue;  // no copy of this one
+      if (lo == 0 || lo % align || lo + bytes < lo) return RA_ERR_INVALID_ARG;
+      if (written && lo < e.hi) plain = false;
+      e.lo = std::min(e.lo, lo), e.hi = std::max(e.hi, lo + (uintptr_t)bytes);
+    }
+    extent[extents++] = e;
+  }
+  const uintptr_t scale = reinterpret_cast<uintptr_t>(o.grad_scale);
+  if (scale) extent[extents++] = {scale, scale + 4, false};
+  for (int i = 0; i < extents; ++i)
+    for (int j = 0; j < i; ++j) plain = plain && (extent[i].hi <= extent[j].lo || extent[j].hi <= extent[i].lo);
+  if (!plain) {
+    try {
+      std::vector<Span> spans;
+      spans.reserve((size_t)ntensors * kLists + 1);
+      for (int list = 0; list < kLists; ++list) {  // one list after another: each may still be an ascending run
+        if (!list_used(list, z)) continue;
+        for (int i = 0; i < ntensors; ++i) {
+          uint64_t bytes;
+          uintptr_t align;
+          const uintptr_t lo = reinterpret_cast<uintptr_t>(buffer_of(tensors[i], list, z, &bytes, &align));
+          if (tensors[i].count && lo) spans.push_back({lo, lo + (uintptr_t)bytes, list != 1});
         }
-        if (st != RA_SUCCESS) return st;
       }
+      if (scale) spans.push_back({scale, scale + 4, false});
+      if (written_overlap(spans)) return RA_ERR_ALIAS;
+    } catch (const std::bad_alloc&) {
+      return RA_ERR_UNSUPPORTED;  // the host has no room for the list
     }
-    if (spans.empty()) return RA_SUCCESS;
-    if (o.grad_scale != nullptr) {
-      const uintptr_t p = reinterpret_cast<uintptr_t>(o.grad_scale);
-      spans.push_back({p, p + 4, false});
-    }
-    if (written_overlap(spans)) return RA_ERR_ALIAS;
-  } catch (const std::bad_alloc&) {
-    return RA_ERR_UNSUPPORTED;  // the host has no room for the list
   }
   ra::AdamScalars s{};
   s.b1 = (float)o.beta1, s.one_minus_b1 = (float)(1.0 - o.beta1);
@@ -188,6 +215,6 @@ extern "C" ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, 
   s.scale = o.grad_scale;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return ntensors <= ra::kAdamSmall
-             ? launch_all<ra::kAdamSmall>(tensors, ntensors, ra::kAdamSmallFns[param_dtype][grad_dtype], o, pe, ge, ce, s, key, cs)
-             : launch_all<ra::kAdamLarge>(tensors, ntensors, ra::kAdamLargeFns[param_dtype][grad_dtype], o, pe, ge, ce, s, key, cs);
+             ? launch_all<ra::kAdamSmall>(tensors, ntensors, ra::kAdamSmallFns[param_dtype][grad_dtype], o, z, s, key, cs)
+             : launch_all<ra::kAdamLarge>(tensors, ntensors, ra::kAdamLargeFns[param_dtype][grad_dtype], o, z, s, key, cs);
 }

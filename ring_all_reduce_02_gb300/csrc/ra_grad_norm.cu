@@ -52,15 +52,19 @@ struct NormArgs {
   uint32_t tile0[CAP];
 };
 
-// The sum over the CTA of one value per thread, in thread 0; the same tree every time.
+// The sum over the CTA of one value per thread, in the first warp; the same tree every time.
 template <typename T>
 __device__ __forceinline__ T cta_sum(T x, T* smem) {
+  constexpr int kWarps = kNormThreads / 32;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   if ((threadIdx.x & 31) == 0) smem[threadIdx.x / 32] = x;
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int w = 1; w < kNormThreads / 32; ++w) x += smem[w];
+  if (threadIdx.x < 32) {
+    x = smem[threadIdx.x % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  }
   return x;
 }
 
@@ -68,7 +72,8 @@ template <int DT, int CAP>
 __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ NormArgs<CAP> a) {
   pdl_enter();
   const NormScalars& s = a.s;
-  __shared__ double sums[kNormThreads / 32];
+  __shared__ float sums[kNormThreads / 32];
+  __shared__ double last_sums[kNormThreads / 32];
   __shared__ bool finish;
   constexpr int es = Elem<DT>::kSize, V = 32 / es;
   const F2 prescale = twice(s.prescale);
@@ -110,22 +115,25 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
       }
     }
   }
-  const double mine = cta_sum((double)fold2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]))), sums);
-  if (threadIdx.x == 0) {
-    float* slot = &s.ws->partial[blockIdx.x];
-    *slot = (float)(blockIdx.x < s.written ? mine + (double)*slot : mine);
-    finish = false;
-    if (s.last) {
-      __threadfence();
-      finish = atomicAdd(&s.ws->ticket, 1u) == gridDim.x - 1;
+  const float mine = cta_sum(fold2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]))), sums);
+  double sum = (double)mine;
+  if (gridDim.x > 1 || s.written > 0 || !s.last) {  // one CTA of one launch has it all
+    if (threadIdx.x == 0) {
+      float* slot = &s.ws->partial[blockIdx.x];
+      *slot = blockIdx.x < s.written ? mine + *slot : mine;
+      finish = false;
+      if (s.last) {
+        __threadfence();
+        finish = atomicAdd(&s.ws->ticket, 1u) == gridDim.x - 1;
+      }
     }
+    __syncthreads();
+    if (!finish) return;
+    __threadfence();
+    sum = 0.0;
+    for (uint32_t k = threadIdx.x; k < max(s.written, gridDim.x); k += kNormThreads) sum += (double)__ldcg(&s.ws->partial[k]);
+    sum = cta_sum(sum, last_sums);
   }
-  __syncthreads();
-  if (!finish) return;
-  __threadfence();
-  double sum = 0.0;
-  for (uint32_t k = threadIdx.x; k < max(s.written, gridDim.x); k += kNormThreads) sum += (double)__ldcg(&s.ws->partial[k]);
-  sum = cta_sum(sum, sums);
   if (threadIdx.x == 0) {
     const float norm = (float)sqrt(sum);
     const float inf = __int_as_float(0x7f800000);

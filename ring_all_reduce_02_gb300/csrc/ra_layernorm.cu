@@ -130,7 +130,8 @@ ra_status_t ra_layernorm_backward(const void* dy, size_t dy_stride, const void* 
     if (!sound(b)) return RA_ERR_INVALID_ARG;
   for (int o = 0; o < 4; ++o) {
     for (int i = 0; i < 5; ++i) {
-      const bool same = o == 0 && ((i == 0 && dx == dy && dx_stride == dy_stride) || (i == 1 && dx == x && dx_stride == x_stride));
+      const bool same =
+          o == 0 && ((i == 0 && dx == dy && dx_stride == dy_stride) || (i == 1 && dx == x && dx_stride == x_stride));
       if (overlaps(out[o].at, in[i].at) && !same) return RA_ERR_ALIAS;
     }
     for (int q = 0; q < o; ++q)

@@ -385,9 +385,10 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
 // while one is worked on, and the column sums of dy xhat and dy stay in
 // registers over all the rows of a group: x and dy are read once. The CTA folds
 // its groups' sums and writes one partial of each; ln_backward_finish adds the
-// partials (a CTA that has all the rows writes the gradients itself). KEEP: xhat and dy w of the row stay in registers between their two
-// uses (before and after the row's sums), and its place in shared memory is
-// filled again at once; otherwise they are taken from shared memory twice.
+// partials (a CTA that has all the rows writes the gradients itself). KEEP: xhat
+// and dy w of the row stay in registers between their two uses (before and after
+// the row's sums), and its place in shared memory is filled again at once;
+// otherwise they are taken from shared memory twice.
 //
 // SHIFTED: rows off the 16-byte grid, by whole lines as above. The rows of a
 // CTA are a multiple of 8 apart, so all of them have the same phase and a
@@ -416,7 +417,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr uint32_t kLnMaxStages = 8;
 // Waits until all but the stages - 1 newest groups of copies have landed, or fewer; stages: 1 to 8.
 __device__ __forceinline__ void cp_async_wait_oldest(uint32_t stages) {
   if (stages == 8) cp_async_wait<7>();
@@ -435,7 +435,8 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void store_in_cluster(const float* at, uint32_t rank, float v) {
   const uint32_t local = (uint32_t)__cvta_generic_to_shared(at);
   asm volatile(
-      "{\n .reg .b32 there;\n mapa.shared::cluster.u32 there, %0, %1;\n st.shared::cluster.f32 [there], %2;\n}" ::"r"(local), "r"(rank), "f"(v)
+      "{\n .reg .b32 there;\n mapa.shared::cluster.u32 there, %0, %1;\n st.shared::cluster.f32 [there], %2;\n}" ::"r"(local),
+      "r"(rank), "f"(v)
       : "memory");
 }
 
@@ -523,7 +524,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   // one row ahead, or two where registers allow (4096 x 12288 bf16: 101 -> 78 us; at E = 16 it costs 1%)
   constexpr uint32_t kAhead = E == 16 ? 1 : 2;
   float next_mean = 0.0f, next_rstd = 0.0f;
-  if (kAhead == 2 && first + stride < a.rows) next_mean = __ldg(a.mean + first + stride), next_rstd = __ldg(a.rstd + first + stride);
+  if (kAhead == 2 && first + stride < a.rows)
+    next_mean = __ldg(a.mean + first + stride), next_rstd = __ldg(a.rstd + first + stride);
   const auto weight = [&](uint32_t i) {
     const uint32_t c = (uint32_t)(column0 + (int)i);  // wraps around before column 0
     return c >= cols ? 0.0f : a.w ? weight_at<WDT>(a.w, c) : 1.0f;
@@ -605,7 +607,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
       cp_async_wait_oldest(stages - 1);  // the place of the row before is not sent for yet
       float new_mean = 0.0f, new_rstd = 0.0f;
-      if (row + kAhead * stride < a.rows) new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
+      if (row + kAhead * stride < a.rows)
+        new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
       const F2 rstd2 = twice(rstd), shift2 = twice(-mean * rstd);
       F2 sum1 = 0, sum2 = 0;
 #pragma unroll
@@ -628,7 +631,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
       if ((lane & 15) < ranks)
-        store_in_cluster(reinterpret_cast<const float*>(&slots[parity][rank * warps + threadIdx.x / 32]) + lane / 16, lane & 15, mine);
+        store_in_cluster(reinterpret_cast<const float*>(&slots[parity][rank * warps + threadIdx.x / 32]) + lane / 16,
+                         lane & 15, mine);
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       if (old_buffer != nullptr) late_dx();
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -648,7 +652,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     for (uint64_t row = first; row < a.rows; row += stride, dx += dx_hop) {
       cp_async_wait_oldest(stages);  // every thread reads back the lines it fetched itself: nothing else to wait for
       float new_mean = 0.0f, new_rstd = 0.0f;
-      if (row + kAhead * stride < a.rows) new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
+      if (row + kAhead * stride < a.rows)
+        new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
       const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
       F2 hs[KEEP ? E / 2 : 1], ps[KEEP ? E / 2 : 1], sum1 = 0, sum2 = 0;
 #pragma unroll

@@ -59,7 +59,8 @@ cudaError_t backward_fused(LnBackward* all, bool shifted, size_t weights, size_t
   a.stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + groups * a.stages * stage;
   if (smem < groups * 2 * weights) smem = groups * 2 * weights;  // the fold
-  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, KEEP, true, false> : ln_backward_fused<DT, WDT, E, KEEP, false, false>;
+  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, KEEP, true, false>
+                              : ln_backward_fused<DT, WDT, E, KEEP, false, false>;
   const cudaError_t err = allow_smem(kernel, smem);
   return err != cudaSuccess ? err : launch_programmatic(kernel, dim3((unsigned)a.parts), groups * a.group, smem, s, a);
 }
@@ -72,7 +73,8 @@ cudaError_t backward_late(LnBackward* a, bool shifted, size_t weights, size_t st
   a->stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + a->stages * stage;
   if (smem < 2 * weights) smem = 2 * weights;  // the fold
-  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, false, true, true> : ln_backward_fused<DT, WDT, E, false, false, true>;
+  const auto kernel = shifted ? ln_backward_fused<DT, WDT, E, false, true, true>
+                              : ln_backward_fused<DT, WDT, E, false, false, true>;
   cudaError_t err = allow_smem(kernel, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
@@ -140,7 +142,8 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
   const uint64_t reach = a.cols + (aligned ? 0 : V - 1);
   // the sweep in one kernel: two stages of a row's x and dy for each group have to fit in shared memory
   const auto finish = [&]() {
-    return sums && a.parts > 1 ? launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a) : cudaSuccess;
+    if (!sums || a.parts == 1) return cudaSuccess;
+    return launch_programmatic(ln_backward_finish<WDT>, dim3(slices), kLnFinishThreads, 0, s, a);
   };
   if (a.rows > 0 && in_step && reach <= (uint64_t)kLnMaxThreads * 32) {
     const uint32_t elems = ln_share_elems((uint32_t)a.cols, es, !aligned, 1);

@@ -440,7 +440,8 @@ def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 
     dense = x.is_contiguous() and y.is_contiguous()
     if not (x.is_cuda and y.is_cuda and len(shape) == 2 and y.shape == shape and y.dtype is dtype
             and (dense or (_rows_contiguous(x) and _rows_contiguous(y)))):
-        raise ValueError("ra_layernorm_forward: x and y must be 2-D CUDA tensors of one shape and dtype, rows contiguous")
+        raise ValueError("ra_layernorm_forward: x and y must be 2-D CUDA tensors of one shape and dtype, rows "
+                         "contiguous")
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_forward: unsupported dtype {dtype} with weights of {wdtype}")
     rows, cols = shape
@@ -451,7 +452,8 @@ def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 
                        mean=(mean, rows, f32), rstd=(rstd, rows, f32))
     st = (_lib or lib()).ra_layernorm_forward(
         x.data_ptr(), cols if dense else _row_stride(x, cols), _address(weight), _address(bias), y.data_ptr(),
-        cols if dense else _row_stride(y, cols), _address(mean), _address(rstd), rows, cols, eps, codes[dtype], codes[wdtype], _stream_of(x, stream))
+        cols if dense else _row_stride(y, cols), _address(mean), _address(rstd), rows, cols, eps, codes[dtype],
+        codes[wdtype], _stream_of(x, stream))
     if st:
         raise RaError(st, "ra_layernorm_forward")
 
@@ -493,8 +495,7 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     st = (_lib or lib()).ra_layernorm_backward(
         dy.data_ptr(), cols if dense else _row_stride(dy, cols), x.data_ptr(), cols if dense else _row_stride(x, cols),
         _address(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), cols if dense else _row_stride(dx, cols),
-        _address(dweight), _address(dbias), accumulate, rows,
-        cols, codes[dtype], codes[wdtype], _address(workspace), 0 if workspace is None else workspace.nbytes,
+        _address(dweight), _address(dbias), accumulate, rows, cols, codes[dtype], codes[wdtype], _address(workspace), 0 if workspace is None else workspace.nbytes,
         _stream_of(x, stream))
     if st:
         raise RaError(st, "ra_layernorm_backward")
@@ -537,7 +538,8 @@ def ra_grad_norm(grads, max_norm: float, out, workspace, prescale: float = 1.0, 
     that clips it to max_norm into out[1]: out[1:] is ra_adamw's grad_scale. ``workspace``: a CUDA tensor of
     ra_grad_norm_workspace() bytes, zeroed once."""
     g = grads if isinstance(grads, GradTensors) else GradTensors(grads)
-    if out is None or not _is_vector(out, 2, _Torch.f32 or _Torch.load().f32) or not (workspace.is_cuda and workspace.is_contiguous()):
+    f32 = _Torch.f32 or _Torch.load().f32
+    if out is None or not _is_vector(out, 2, f32) or not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("ra_grad_norm: out must be a contiguous CUDA tensor of 2 float32, workspace a contiguous CUDA "
                          "tensor")
     st = (_lib or lib()).ra_grad_norm(g.addresses, g.counts, len(g.tensors), g.dtype, prescale, max_norm,

@@ -119,6 +119,14 @@ __device__ __forceinline__ float weight_at(const void* base, uint32_t i) {
   if constexpr (DT == DT_F32) return __ldg(static_cast<const float*>(base) + i);
   else return widen16<DT>(__ldg(static_cast<const unsigned short*>(base) + i));
 }
+// Where element i of a row's lines has its weight in shared memory: four of a line's values stand together, a
+// line's second four `half` floats on, so that a warp's 16-byte reads touch every bank equally often (a thread's
+// eight in a row cost two passes: 6001 x 4095 fp16 30.5 us).
+template <uint32_t V>
+__device__ __forceinline__ uint32_t weight_slot(uint32_t i, uint32_t half) {
+  return V == 4 ? i : (i & 4 ? half : 0) + i / 8 * 4 + (i & 3);
+}
+
 // V weights from element i, through L1: every row reads them again.
 template <int DT, int V>
 __device__ __forceinline__ void load_weights(const void* base, uint32_t i, F2* f) {
@@ -327,7 +335,10 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
     }
 #pragma unroll
     for (uint32_t u = 0; u < 8; ++u)
-      if (i0 + u * group < lines * V) ws[i0 + u * group] = w[u], bs[i0 + u * group] = b[u];
+      if (i0 + u * group < lines * V) {
+        const uint32_t slot = weight_slot<V>(i0 + u * group, lines * 4);
+        ws[slot] = w[u], bs[slot] = b[u];
+      }
   }
   __syncthreads();
   const float n = (float)cols;
@@ -359,11 +370,11 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
       if (!(some >> j & 1u)) continue;
-      const uint32_t first = (j * group + t) * V;
+      const uint32_t first = (j * group + t) * 4;
 #pragma unroll
       for (uint32_t e = 0; e < H; e += 2) {
-        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(ws + first + 2 * e);
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bs + first + 2 * e);
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(ws + first + e / 2 * lines * 4);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bs + first + e / 2 * lines * 4);
         f[j * H + e] = fma2(mul2(f[j * H + e], rstd2), w.x, b.x);
         f[j * H + e + 1] = fma2(mul2(f[j * H + e + 1], rstd2), w.y, b.y);
       }
@@ -472,6 +483,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     ranks = a.split, unit = blockIdx.x / ranks, units = gridDim.x / ranks;
   }
   const uint32_t row_elems = ln_share_elems(cols, es, SHIFTED, ranks), row_bytes = row_elems * es;
+  const uint32_t half = row_elems / 2;  // from a line's first four weights to its second four
   float* weights = reinterpret_cast<float*>(smem);
   char* ring = smem + row_elems * 4 + (size_t)g * stages * 2 * row_bytes;
 
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     for (uint32_t u = 0; u < 8; ++u) w[u] = i0 + u * blockDim.x < row_elems ? weight(i0 + u * blockDim.x) : 0.0f;
 #pragma unroll
     for (uint32_t u = 0; u < 8; ++u)
-      if (i0 + u * blockDim.x < row_elems) weights[i0 + u * blockDim.x] = w[u];
+      if (i0 + u * blockDim.x < row_elems) weights[weight_slot<V>(i0 + u * blockDim.x, half)] = w[u];
   }
   float early[kEarly];
 #pragma unroll
@@ -549,7 +561,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
 #pragma unroll
   for (uint32_t k = 0; k < kEarly; ++k) {
     const uint32_t i = threadIdx.x + k * blockDim.x;
-    if (i < row_elems) weights[i] = early[k];
+    if (i < row_elems) weights[weight_slot<V>(i, half)] = early[k];
   }
   if constexpr (LATE) cluster_sync();  // the others' shared memory is there
   else __syncthreads();
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   const float inv_n = 1.0f / (float)cols;
   uint32_t stage = 0, parity = 0;
   const char* buffer = ring + t * 16;  // this thread's first line of the row in work
-  const float* w_at = weights + t * V;
+  const float* w_at = weights + t * 4;
   char* dx = static_cast<char*>(a.dx) + first * a.dx_stride * es - phase * es + (line0 + t) * 16;
   // xhat, dy and the weights of the thread's j-th line of the row in `buffer`
   const auto load = [&](const char* buffer, F2 rstd2, F2 shift2, uint32_t j, F2* h, F2* dy, F2* w) {
@@ -574,7 +586,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     for (uint32_t e = 0; e < H; ++e) h[e] = fma2(h[e], rstd2, shift2);
 #pragma unroll
     for (uint32_t e = 0; e < H; e += 2) {
-      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w_at + j * size * V + 2 * e);
+      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w_at + j * size * 4 + e / 2 * half);
       w[e] = q.x, w[e + 1] = q.y;
     }
   };

@@ -143,25 +143,34 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // The sum over the whole CTA of `warps` (up to 16) warps, in all its threads, in a fixed order. `slots`: 16 floats,
-// 16-byte aligned; two calls in a row need two sets.
+// 16-byte aligned; two calls in a row need two sets. A second round of shuffles for more than 4 warps cost 2% to 4%.
 __device__ __forceinline__ float cta_sum_registers(float v, float* slots, uint32_t warps) {
   v = warp_sum(v);
   const uint32_t t = threadIdx.x;
   if ((t & 31) == 0) slots[t / 32] = v;
-  if (t >= warps && t < 4) slots[t] = 0.0f;
+  if (t >= warps && t < (warps + 3) / 4 * 4) slots[t] = 0.0f;
   __syncthreads();
-  if (warps <= 4) {  // one read instead of a second round of shuffles
-    const float4 q = *reinterpret_cast<const float4*>(slots);
-    return (q.x + q.y) + (q.z + q.w);
-  }
-  v = (t & 15) < warps ? slots[t & 15] : 0.0f;
+  const float4* at = reinterpret_cast<const float4*>(slots);
+  float4 q = at[0];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (uint32_t k = 1; k < 4; ++k) {
+    if (k * 4 >= warps) break;
+    const float4 r = at[k];
+    q.x += r.x, q.y += r.y, q.z += r.z, q.w += r.w;
+  }
+  return (q.x + q.y) + (q.z + q.w);
 }
 
 constexpr uint32_t kLnMaxThreads = 512;
 constexpr uint32_t kLnWarpThreads = 128;  // of a CTA with a row to each warp
+
+// A row's mean from its sum. The product with 1 / n is mended by its remainder, so that a quotient that fp32 holds
+// comes out exactly (a constant row's mean, which leaves deviations of zero); an infinite sum stays as it is. Three
+// divisions and a square root a row, rounded as IEEE has them, cost 4% to 8% of the kernels below.
+__device__ __forceinline__ float row_mean(float sum, float n, float inv_n) {
+  const float q = sum * inv_n, r = __fmaf_rn(__fmaf_rn(-q, n, sum), inv_n, q);
+  return fabsf(q) < INFINITY ? r : q;
+}
 
 // ---- forward, rows in registers ---------------------------------------------------
 // A group of threads takes a row, each of them E of its columns in vectors of
@@ -170,9 +179,9 @@ constexpr uint32_t kLnWarpThreads = 128;  // of a CTA with a row to each warp
 // barriers for several groups would hold 16 of an SM's 64 barriers per CTA and
 // so allow only 4 CTAs on it).
 //
-// Measured (back to back, inputs larger than L2): 8192 x 1024 bf16 8.0 us (floor
-// 4.9), 8192 x 4096 bf16 24.2 us (82% of the copy bandwidth), 4096 x 5120 fp32
-// 28.2 us (88%), 32768 x 8192 bf16 178 us (89%). About 17 instructions an element
+// Measured (back to back, inputs larger than L2): 8192 x 1024 bf16 7.8 us (floor
+// 4.9), 8192 x 4096 bf16 23.3 us (85% of the copy bandwidth), 4096 x 8192 fp32
+// 41.6 us (95%), 32768 x 8192 bf16 178 us (89%). About 17 instructions an element
 // at 16-bit types, and a launch's 2 us where rows are few, keep it off the floor.
 template <int DT, int WDT, int E, bool WARP>
 __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
@@ -199,8 +208,8 @@ __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forw
 #pragma unroll
     for (int k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
   }
-  const float n = (float)cols;
-  const float mean = __fdiv_rn(group_sum(fold2(sum), slots[0]), n);  // divided: a constant row's mean is exact
+  const float n = (float)cols, inv_n = __frcp_rn(n);
+  const float mean = row_mean(group_sum(fold2(sum), slots[0]), n, inv_n);
   const F2 minus = pair(-mean, -mean);
   F2 sq = 0;
 #pragma unroll
@@ -213,8 +222,8 @@ __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forw
       if (in) sq = fma2(d, d, sq);
     }
   }
-  const float var = __fdiv_rn(group_sum(fold2(sq), slots[1]), n);
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+  const float var = group_sum(fold2(sq), slots[1]) * inv_n;
+  const float rstd = rsqrtf(var + a.eps);
   const F2 rstd2 = pair(rstd, rstd);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -287,10 +296,13 @@ __device__ __forceinline__ void store_part(char* at, const uint4& q, int from, i
 }
 
 // Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on. The grid is a
-// multiple of 8 (or has a CTA for every row). 6001 x 4095 fp16: 30.5 us (floor 14.5; element by element 75), 2047 x
-// 1537 fp32: 8.0 us (3.7). The two exchanges of a row among 9 warps on 27 to 32 resident warps bound it.
+// multiple of 8 (or has a CTA for every row). 6001 x 4095 fp16: 23.2 us (floor 14.5; element by element 75), 2047 x
+// 1537 fp32: 7.5 us (3.7). Issue slots, 60% of them in use, and the two exchanges of a row among its warps on 24 to 32
+// resident warps bound it: 2 to 8 rows ahead in shared memory instead of one in registers, or two rows to an
+// exchange, made it slower.
 template <int DT, int WDT, int E>
-__global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shifted(const __grid_constant__ LnForward a) {
+__global__ void __launch_bounds__(E == 24 ? 384 : kLnMaxThreads, E <= 24 ? 2 : 1)
+    ln_forward_shifted(const __grid_constant__ LnForward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
@@ -325,23 +337,23 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
   fetch();
   float* ws = reinterpret_cast<float*>(smem);
   float* bs = ws + lines * V;
-  for (uint32_t i0 = t; i0 < lines * V; i0 += 8 * group) {  // 16 reads in flight a thread
-    float w[8], b[8];
+  for (uint32_t i0 = t; i0 < lines * V; i0 += 4 * group) {  // 8 reads in flight a thread
+    float w[4], b[4];
 #pragma unroll
-    for (uint32_t u = 0; u < 8; ++u) {
+    for (uint32_t u = 0; u < 4; ++u) {
       const uint32_t c = i0 + u * group - phase;  // wraps around before column 0
       w[u] = c >= cols ? 0.0f : a.w ? weight_at<WDT>(a.w, c) : 1.0f;
       b[u] = c < cols && a.b ? weight_at<WDT>(a.b, c) : 0.0f;
     }
 #pragma unroll
-    for (uint32_t u = 0; u < 8; ++u)
+    for (uint32_t u = 0; u < 4; ++u)
       if (i0 + u * group < lines * V) {
         const uint32_t slot = weight_slot<V>(i0 + u * group, lines * 4);
         ws[slot] = w[u], bs[slot] = b[u];
       }
   }
   __syncthreads();
-  const float n = (float)cols;
+  const float n = (float)cols, inv_n = __frcp_rn(n);
   uint32_t parity = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, y += y_hop) {
     F2 f[E / 2], sum = 0;
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
       for (uint32_t k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
     }
     if (row + gridDim.x < a.rows) fetch();
-    const float mean = __fdiv_rn(cta_sum_registers(fold2(sum), slots[parity][0], group / 32), n);
+    const float mean = row_mean(cta_sum_registers(fold2(sum), slots[parity][0], group / 32), n, inv_n);
     const F2 minus = twice(-mean);
     F2 sq = 0;
 #pragma unroll
@@ -364,8 +376,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, E <= 16 ? 2 : 1) ln_forward_shi
 #pragma unroll
       for (uint32_t k = 0; k < H; ++k) sq = fma2(f[j * H + k], f[j * H + k], sq);
     }
-    const float var = __fdiv_rn(cta_sum_registers(fold2(sq), slots[parity][1], group / 32), n);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+    const float var = cta_sum_registers(fold2(sq), slots[parity][1], group / 32) * inv_n;
+    const float rstd = rsqrtf(var + a.eps);
     const F2 rstd2 = twice(rstd);
 #pragma unroll
     for (uint32_t j = 0; j < NV; ++j) {
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_rows(const __grid_const
       sq = __fmaf_rn(d, d, sq);
     }
     const float var = __fdiv_rn(cta_sum_all<kLnThreads>(sq, smem), n);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+    const float rstd = rsqrtf(var + a.eps);
     for (uint64_t i = threadIdx.x; i < a.cols; i += kLnThreads) {
       const float w = a.w ? ln_load<WDT>(a.w, i) : 1.0f, b = a.b ? ln_load<WDT>(a.b, i) : 0.0f;
       ln_store<DT>(y, i, __fmaf_rn((ln_load<DT>(x, i) - mean) * rstd, w, b));

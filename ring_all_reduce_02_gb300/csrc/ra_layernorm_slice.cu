@@ -37,13 +37,20 @@ cudaError_t forward_registers(const LnForward& a, uint32_t group, cudaStream_t s
   return group == 32 ? launch_programmatic(ln_forward_registers<DT, WDT, E, true>, dim3((unsigned)ctas), kLnWarpThreads, 0, s, a)
                      : launch_programmatic(ln_forward_registers<DT, WDT, E, false>, dim3((unsigned)ctas), group, 0, s, a);
 }
+// CTAs, each with a row of `reach` columns, that an SM holds at `per` columns a thread: by registers (64, 85 or 128 a
+// thread) and by the shared memory for the weights.
+uint64_t shifted_rows(uint64_t reach, uint32_t per, size_t smem) {
+  const uint64_t by_registers = (per <= 16 ? 1024 : per == 24 ? 768 : 512) / group_for(reach, per);
+  const uint64_t by_smem = kLnSmem / (smem + 1280);
+  const uint64_t rows = by_registers < by_smem ? by_registers : by_smem;
+  return rows < 1 ? 1 : rows;
+}
+
 template <int E>
 cudaError_t forward_shifted(const LnForward& a, uint32_t group, size_t smem, cudaStream_t s) {
   const cudaError_t err = allow_smem(ln_forward_shifted<DT, WDT, E>, smem);
   if (err != cudaSuccess) return err;
-  uint64_t per_sm = (E <= 16 ? 1024 : 512) / group;
-  if (per_sm > kLnSmem / (smem + 1280)) per_sm = kLnSmem / (smem + 1280);
-  if (per_sm < 1) per_sm = 1;
+  const uint64_t per_sm = shifted_rows((uint64_t)group * E, E, smem);
   const uint64_t ctas = a.rows < 152 * per_sm ? a.rows : 152 * per_sm;
   return launch_programmatic(ln_forward_shifted<DT, WDT, E>, dim3((unsigned)ctas), group, smem, s, a);
 }
@@ -122,10 +129,23 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   if (phase(a.x) == phase(a.y) && line(a.x_stride) == line(a.y_stride) && reach <= (uint64_t)kLnMaxThreads * 64) {
     const size_t smem = 2 * sizeof(float) * ln_share_elems((uint32_t)a.cols, es, true, 1);
     if (smem <= kLnSmem) {
-      if (reach <= 512) return forward_shifted<8>(a, group_for(reach, 8), smem, s);
-      if (reach <= 8192) return forward_shifted<16>(a, group_for(reach, 16), smem, s);
+      if (reach > 8192 && reach <= 9216) return forward_shifted<24>(a, group_for(reach, 24), smem, s);
+      if (reach <= 8192) {
+        // More columns a thread leave fewer warps that are partly empty. Taken where a third more rows are at work on
+        // an SM and there are rows enough for the longer start: 16000 x 4095 bf16 58.4 -> 51.0 us, 16000 x 701 19.2 ->
+        // 14.7, but 1200 x 701 4.9 -> 6.0; with a fifth more rows, 16000 x 1201 21.7 -> 22.7.
+        const bool wider = a.rows > 4096 && 3 * shifted_rows(reach, reach <= 512 ? 16 : 24, smem) >=
+                                                4 * shifted_rows(reach, reach <= 512 ? 8 : 16, smem);
+        if (reach <= 512) {
+          return wider ? forward_shifted<16>(a, group_for(reach, 16), smem, s)
+                       : forward_shifted<8>(a, group_for(reach, 8), smem, s);
+        }
+        return wider ? forward_shifted<24>(a, group_for(reach, 24), smem, s)
+                     : forward_shifted<16>(a, group_for(reach, 16), smem, s);
+      }
       if (reach <= 16384) return forward_shifted<32>(a, group_for(reach, 32), smem, s);
-      return forward_shifted<64>(a, group_for(reach, 64), smem, s);
+      // 64 columns a thread spill; at 4 bytes a column the general kernel is faster (3000 x 23001 fp32: 230 us, not 405)
+      if constexpr (es == 2) return forward_shifted<64>(a, group_for(reach, 64), smem, s);
     }
   }
   return launch_programmatic(ln_forward_rows<DT, WDT>, dim3(row_ctas(a.rows)), kLnThreads, 0, s, a);

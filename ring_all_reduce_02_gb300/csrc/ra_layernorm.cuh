@@ -704,18 +704,21 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
         if (size > 32) {
-          const uint32_t warps = size / 32, w = lane & 15;
-          if (w == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
+          const uint32_t warps = size / 32;
+          if ((lane & 15) == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
           group_sync(g, size);
-          if (warps <= 8) {  // few enough to be read by everyone: no second round of shuffles
-            s1 = s2 = 0.0f;
+          if (warps <= 8) {  // few enough to be read by everyone: no second round of shuffles (for 16 warps it is faster)
+            const F2* all = reinterpret_cast<const F2*>(&slots[parity][g * warps]);
+            F2 even = 0, odd = 0;
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
+            for (uint32_t k = 0; k < 8; k += 2) {
               if (k >= warps) break;
-              const float2 q = slots[parity][g * warps + k];
-              s1 += q.x, s2 += q.y;
+              even = add2(even, all[k]);
+              if (k + 1 < warps) odd = add2(odd, all[k + 1]);
             }
+            split(add2(even, odd), s1, s2);
           } else {
+            const uint32_t w = lane & 15;
             mine = w < warps ? reinterpret_cast<const float*>(&slots[parity][g * warps + w])[lane / 16] : 0.0f;
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);

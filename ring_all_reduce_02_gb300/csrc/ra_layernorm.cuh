@@ -121,7 +121,7 @@ __device__ __forceinline__ float weight_at(const void* base, uint32_t i) {
 }
 // Where element i of a row's lines has its weight in shared memory: four of a line's values stand together, a
 // line's second four `half` floats on, so that a warp's 16-byte reads touch every bank equally often (a thread's
-// eight in a row cost two passes: 6001 x 4095 fp16 30.5 us).
+// eight in a row cost two passes: 6001 x 4095 fp16 30.5 us, not 26.9; backward, 4096 x 12288 bf16 71 us, not 66).
 template <uint32_t V>
 __device__ __forceinline__ uint32_t weight_slot(uint32_t i, uint32_t half) {
   return V == 4 ? i : (i & 4 ? half : 0) + i / 8 * 4 + (i & 3);
@@ -181,7 +181,7 @@ __device__ __forceinline__ float row_mean(float sum, float n, float inv_n) {
 //
 // Measured (back to back, inputs larger than L2): 8192 x 1024 bf16 7.8 us (floor
 // 4.9), 8192 x 4096 bf16 23.3 us (85% of the copy bandwidth), 4096 x 8192 fp32
-// 41.6 us (95%), 32768 x 8192 bf16 178 us (89%). About 17 instructions an element
+// 41.6 us (95%), 32768 x 8192 bf16 171 us (92%). About 16 instructions an element
 // at 16-bit types, and a launch's 2 us where rows are few, keep it off the floor.
 template <int DT, int WDT, int E, bool WARP>
 __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
@@ -420,14 +420,14 @@ __global__ void __launch_bounds__(E == 24 ? 384 : kLnMaxThreads, E <= 24 ? 2 : 1
 // LATE: a row too long for one CTA's registers or shared memory is shared by the
 // 2 or 4 CTAs of a cluster, each with a run of its lines; their sums meet in
 // each other's shared memory, and a row's dx waits until the next row's sums are
-// on their way. 4096 x 20000 bf16: 141 us (51% of the copy bandwidth), 4096 x
+// on their way. 4096 x 20000 bf16: 136 us (53% of the copy bandwidth), 4096 x
 // 16384 fp32: 139 us (85%), against 500 and 459 us in separate passes for dx and
 // the column sums; without the delay 233 and 171.
 //
 // Measured (back to back, inputs larger than L2, of the copy bandwidth's floor):
-// 8192 x 1024 bf16 15.9 us (7.4), of which about 3 are the first rows' way, 9 the
+// 8192 x 1024 bf16 15.8 us (7.4), of which about 3 are the first rows' way, 9 the
 // loop at 80% of the copy bandwidth, 1 the fold and 2 ln_backward_finish; 32768 x
-// 8192 bf16 291 us (237); 2047 x 1537 fp32 15.3 us (5.6); 6001 x 4095 fp16 57 us
+// 8192 bf16 286 us (237); 2047 x 1537 fp32 15.3 us (5.6); 6001 x 4095 fp16 58 us
 // (21.7). In the loop 16 warps (accumulators and the row's values fill the
 // registers) keep 40 to 45% of the issue slots busy: the chain from the row's
 // sums through the exchange to dx bounds it as much as HBM does.
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
           const uint32_t warps = size / 32;
           if ((lane & 15) == 0) reinterpret_cast<float*>(&slots[parity][threadIdx.x / 32])[lane / 16] = mine;
           group_sync(g, size);
-          if (warps <= 8) {  // few enough to be read by everyone: no second round of shuffles (for 16 warps it is faster)
+          if (warps <= 8) {  // all read them: no second round of shuffles (which is faster for 16 warps)
             const F2* all = reinterpret_cast<const F2*>(&slots[parity][g * warps]);
             F2 even = 0, odd = 0;
 #pragma unroll

@@ -586,16 +586,18 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
   const char* buffer = ring + t * 16;  // this thread's first line of the row in work
   const float* w_at = weights + t * 4;
   char* dx = static_cast<char*>(a.dx) + first * a.dx_stride * es - phase * es + (line0 + t) * 16;
-  // xhat, dy and the weights of the thread's j-th line of the row in `buffer`
-  const auto load = [&](const char* buffer, F2 rstd2, F2 shift2, uint32_t j, F2* h, F2* dy, F2* w) {
+  // xhat, dy and the weights of the thread's j-th line of the row in `buffer`. The mean is subtracted before anything
+  // is rounded (x rstd - mean rstd in one fused operation would be off by mean rstd's own rounding: 1e-3 of xhat where
+  // the mean is 10,000 deviations).
+  const auto load = [&](const char* buffer, F2 rstd2, F2 minus_mean2, uint32_t j, F2* h, F2* dy, F2* w) {
     widen<DT>(*reinterpret_cast<const uint4*>(buffer + j * size * 16), h);
     widen<DT>(*reinterpret_cast<const uint4*>(buffer + row_bytes + j * size * 16), dy);
+#pragma unroll
+    for (uint32_t e = 0; e < H; ++e) h[e] = mul2(add2(h[e], minus_mean2), rstd2);
     if constexpr (SHIFTED) {
       const int at = column0 + (int)((j * size + t) * V);
       if (at < 0 || at + (int)V > (int)cols) mask_line<V>(h, -at, (int)cols - at), mask_line<V>(dy, -at, (int)cols - at);
     }
-#pragma unroll
-    for (uint32_t e = 0; e < H; ++e) h[e] = fma2(h[e], rstd2, shift2);
 #pragma unroll
     for (uint32_t e = 0; e < H; e += 2) {
       const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w_at + j * size * 4 + e / 2 * half);
@@ -614,13 +616,13 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
     const char* old_buffer = nullptr;
     char* old_dx = nullptr;
     uint32_t old_stage = 0;
-    F2 old_rstd2 = 0, old_shift2 = 0, old_c1 = 0, old_c2 = 0;
+    F2 old_rstd2 = 0, old_minus_mean2 = 0, old_c1 = 0, old_c2 = 0;
     const auto late_dx = [&]() {
 #pragma unroll
       for (uint32_t j = 0; j < NV; ++j) {
         if (j * size + t >= lines) continue;
         F2 out[H], dy[H], w[H];
-        load(old_buffer, old_rstd2, old_shift2, j, out, dy, w);
+        load(old_buffer, old_rstd2, old_minus_mean2, j, out, dy, w);
 #pragma unroll
         for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), old_rstd2, fma2(out[e], old_c2, old_c1));
         store(old_dx, j, out);
@@ -633,13 +635,13 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       float new_mean = 0.0f, new_rstd = 0.0f;
       if (row + kAhead * stride < a.rows)
         new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
-      const F2 rstd2 = twice(rstd), shift2 = twice(-mean * rstd);
+      const F2 rstd2 = twice(rstd), minus_mean2 = twice(-mean);
       F2 sum1 = 0, sum2 = 0;
 #pragma unroll
       for (uint32_t j = 0; j < NV; ++j) {
         if (j * size + t >= lines) continue;
         F2 h[H], dy[H], w[H];
-        load(buffer, rstd2, shift2, j, h, dy, w);
+        load(buffer, rstd2, minus_mean2, j, h, dy, w);
 #pragma unroll
         for (uint32_t e = 0; e < H; ++e) {
           const F2 p = mul2(dy[e], w[e]);
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       for (uint32_t k = lane; k < ranks * warps; k += 32) s1 += slots[parity][k].x, s2 += slots[parity][k].y;
       s1 = warp_sum(s1), s2 = warp_sum(s2);
       parity ^= 1;
-      old_rstd2 = rstd2, old_shift2 = shift2, old_c1 = twice(-rstd * (s1 * inv_n)), old_c2 = twice(-rstd * (s2 * inv_n));
+      old_rstd2 = rstd2, old_minus_mean2 = minus_mean2, old_c1 = twice(-rstd * (s1 * inv_n)), old_c2 = twice(-rstd * (s2 * inv_n));
       old_buffer = buffer, old_dx = dx, old_stage = stage;
       if constexpr (kAhead == 1) mean = new_mean, rstd = new_rstd;
       else mean = next_mean, rstd = next_rstd, next_mean = new_mean, next_rstd = new_rstd;
@@ -678,13 +680,13 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
       float new_mean = 0.0f, new_rstd = 0.0f;
       if (row + kAhead * stride < a.rows)
         new_mean = __ldg(a.mean + row + kAhead * stride), new_rstd = __ldg(a.rstd + row + kAhead * stride);
-      const F2 rstd2 = pair(rstd, rstd), shift2 = pair(-mean * rstd, -mean * rstd);
+      const F2 rstd2 = twice(rstd), minus_mean2 = twice(-mean);
       F2 hs[KEEP ? E / 2 : 1], ps[KEEP ? E / 2 : 1], sum1 = 0, sum2 = 0;
 #pragma unroll
       for (uint32_t j = 0; j < NV; ++j) {
         if (j * size + t >= lines) continue;
         F2 h[H], dy[H], w[H];
-        load(buffer, rstd2, shift2, j, h, dy, w);
+        load(buffer, rstd2, minus_mean2, j, h, dy, w);
 #pragma unroll
         for (uint32_t e = 0; e < H; ++e) {
           const F2 p = mul2(dy[e], w[e]);
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1) ln_backward_fused(const __gr
           for (uint32_t e = 0; e < H; ++e) out[e] = fma2(ps[j * H + e], rstd2, fma2(hs[j * H + e], c2_2, c1_2));
         } else {
           F2 dy[H], w[H];
-          load(buffer, rstd2, shift2, j, out, dy, w);
+          load(buffer, rstd2, minus_mean2, j, out, dy, w);
 #pragma unroll
           for (uint32_t e = 0; e < H; ++e) out[e] = fma2(mul2(dy[e], w[e]), rstd2, fma2(out[e], c2_2, c1_2));
         }

@@ -165,12 +165,28 @@ constexpr uint32_t kLnMaxThreads = 512;
 constexpr uint32_t kLnWarpThreads = 128;  // of a CTA with a row to each warp
 
 // A row's mean from its sum. The product with 1 / n is mended by its remainder, so that a quotient that fp32 holds
-// comes out exactly (a constant row's mean, which leaves deviations of zero); an infinite sum stays as it is. Three
-// divisions and a square root a row, rounded as IEEE has them, cost 4% to 8% of the kernels below.
+// comes out exactly; an infinite sum stays as it is. Three divisions and a square root a row, rounded as IEEE has
+// them, cost 4% to 8% of the kernels below.
 __device__ __forceinline__ float row_mean(float sum, float n, float inv_n) {
   const float q = sum * inv_n, r = __fmaf_rn(__fmaf_rn(-q, n, sum), inv_n, q);
   return fabsf(q) < INFINITY ? r : q;
 }
+
+// A constant row's mean has to be its value: an ulp of a large mean times 1 / deviation = 1 / sqrt(eps) is not small.
+// The sum of n equal values of s significant bits is exact in fp32 up to 2^(24 - s) of them. Rows of fp32, and of fp16
+// above 8192 columns, can be longer, so there the mean of the deviations from the first mean is added to it: of a
+// constant row these are a few ulp, their sum is as good as exact, and the second deviations are zero. bf16 has 8
+// bits: exact up to 65,536 columns, which only ln_forward_rows passes. The third exchange costs nothing where HBM
+// bounds the row (8192 x 4096 fp32 41.4 -> 41.8 us, 6001 x 4095 fp32 39.6 -> 39.7), up to 15% elsewhere (2047 x 1537
+// fp32 7.6 -> 8.3, 2048 x 16384 fp16 28.3 -> 31.4); ln_forward_rows reads the row once more, 9% to 24% for fp32. Sums of
+// deviations and squares in one exchange, the variance mended by the difference of the means and summed again where
+// that cancels, took 3% to 5% less for fp16 and up to 35% more for odd rows of fp32.
+template <int DT>
+__host__ __device__ __forceinline__ bool second_mean(uint64_t cols) {
+  return DT == DT_F32 || cols > (DT == DT_F16 ? 8192 : 65536);
+}
+// What to add to a mean, from the mean of the deviations from it: nothing where the row is not finite.
+__device__ __forceinline__ float mean_rest(float rest) { return fabsf(rest) < INFINITY ? rest : 0.0f; }
 
 // ---- forward, rows in registers ---------------------------------------------------
 // A group of threads takes a row, each of them E of its columns in vectors of
@@ -183,11 +199,11 @@ __device__ __forceinline__ float row_mean(float sum, float n, float inv_n) {
 // 4.9), 8192 x 4096 bf16 23.3 us (85% of the copy bandwidth), 4096 x 8192 fp32
 // 41.6 us (95%), 32768 x 8192 bf16 171 us (92%). About 16 instructions an element
 // at 16-bit types, and a launch's 2 us where rows are few, keep it off the floor.
-template <int DT, int WDT, int E, bool WARP>
+template <int DT, int WDT, int E, bool WARP, bool SECOND>
 __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
   pdl_enter();
   constexpr int es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
-  __shared__ __align__(16) float slots[2][kLnMaxThreads / 32];
+  __shared__ __align__(16) float slots[SECOND ? 3 : 2][kLnMaxThreads / 32];
   const uint32_t group = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
   const uint64_t row = WARP ? (uint64_t)blockIdx.x * (kLnWarpThreads / 32) + threadIdx.x / 32 : blockIdx.x;
   if (row >= a.rows) return;  // a whole group
@@ -209,8 +225,20 @@ __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forw
     for (int k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
   }
   const float n = (float)cols, inv_n = __frcp_rn(n);
-  const float mean = row_mean(group_sum(fold2(sum), slots[0]), n, inv_n);
-  const F2 minus = pair(-mean, -mean);
+  float mean = row_mean(group_sum(fold2(sum), slots[0]), n, inv_n);
+  if constexpr (SECOND) {
+    const F2 minus = twice(-mean);
+    F2 rest = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = j * step + t * V < cols;
+#pragma unroll
+      for (int k = 0; k < H; ++k)
+        if (in) rest = add2(rest, add2(f[j * H + k], minus));
+    }
+    mean += mean_rest(row_mean(group_sum(fold2(rest), slots[2]), n, inv_n));
+  }
+  const F2 minus = twice(-mean);
   F2 sq = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -224,7 +252,7 @@ __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forw
   }
   const float var = group_sum(fold2(sq), slots[1]) * inv_n;
   const float rstd = rsqrtf(var + a.eps);
-  const F2 rstd2 = pair(rstd, rstd);
+  const F2 rstd2 = twice(rstd);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const uint32_t c = j * step + t * V;
@@ -300,13 +328,13 @@ __device__ __forceinline__ void store_part(char* at, const uint4& q, int from, i
 // 1537 fp32: 7.5 us (3.7). Issue slots, 60% of them in use, and the two exchanges of a row among its warps on 24 to 32
 // resident warps bound it: 2 to 8 rows ahead in shared memory instead of one in registers, or two rows to an
 // exchange, made it slower.
-template <int DT, int WDT, int E>
+template <int DT, int WDT, int E, bool SECOND>
 __global__ void __launch_bounds__(E == 24 ? 384 : kLnMaxThreads, E <= 24 ? 2 : 1)
     ln_forward_shifted(const __grid_constant__ LnForward a) {
   pdl_enter();
   constexpr uint32_t es = Elem<DT>::kSize, V = 16 / es, NV = E / V, H = V / 2;
   extern __shared__ __align__(16) char smem[];
-  __shared__ __align__(16) float slots[2][2][kLnMaxThreads / 32];
+  __shared__ __align__(16) float slots[2][SECOND ? 3 : 2][kLnMaxThreads / 32];
   const uint32_t cols = (uint32_t)a.cols, t = threadIdx.x, group = blockDim.x;
   const char* base = static_cast<const char*>(a.x);
   const char* end = base + ((a.rows - 1) * a.x_stride + cols) * es;
@@ -365,7 +393,21 @@ __global__ void __launch_bounds__(E == 24 ? 384 : kLnMaxThreads, E <= 24 ? 2 : 1
       for (uint32_t k = 0; k < H; ++k) sum = add2(sum, f[j * H + k]);
     }
     if (row + gridDim.x < a.rows) fetch();
-    const float mean = row_mean(cta_sum_registers(fold2(sum), slots[parity][0], group / 32), n, inv_n);
+    float mean = row_mean(cta_sum_registers(fold2(sum), slots[parity][0], group / 32), n, inv_n);
+    if constexpr (SECOND) {
+      const F2 minus = twice(-mean);
+      F2 rest = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < NV; ++j) {
+        F2 d[H];
+#pragma unroll
+        for (uint32_t k = 0; k < H; ++k) d[k] = add2(f[j * H + k], minus);
+        if (!(whole >> j & 1u)) mask_line<V>(d, -at[j], (int)cols - at[j]);
+#pragma unroll
+        for (uint32_t k = 0; k < H; ++k) rest = add2(rest, d[k]);
+      }
+      mean += mean_rest(row_mean(cta_sum_registers(fold2(rest), slots[parity][2], group / 32), n, inv_n));
+    }
     const F2 minus = twice(-mean);
     F2 sq = 0;
 #pragma unroll
@@ -797,12 +839,18 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_rows(const __grid_const
   __shared__ float smem[33];
   constexpr int es = Elem<DT>::kSize;
   const float n = (float)a.cols;
+  const bool second = second_mean<DT>(a.cols);
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const char* x = static_cast<const char*>(a.x) + row * a.x_stride * es;
     char* y = static_cast<char*>(a.y) + row * a.y_stride * es;
     float sum = 0.0f;
     for (uint64_t i = threadIdx.x; i < a.cols; i += kLnThreads) sum += ln_load<DT>(x, i);
-    const float mean = __fdiv_rn(cta_sum_all<kLnThreads>(sum, smem), n);  // divided: a constant row's mean is exact
+    float mean = __fdiv_rn(cta_sum_all<kLnThreads>(sum, smem), n);
+    if (second) {
+      float rest = 0.0f;
+      for (uint64_t i = threadIdx.x; i < a.cols; i += kLnThreads) rest += ln_load<DT>(x, i) - mean;
+      mean += mean_rest(__fdiv_rn(cta_sum_all<kLnThreads>(rest, smem), n));
+    }
     float sq = 0.0f;
     for (uint64_t i = threadIdx.x; i < a.cols; i += kLnThreads) {
       const float d = ln_load<DT>(x, i) - mean;

@@ -1,6 +1,8 @@
 // One (row dtype, weight dtype) slice of the layer norm kernels and their launch
 // shapes. The build compiles this file once per pair, with RA_SLICE_DT and
 // RA_SLICE_W set, so the five slices compile in parallel.
+#include <type_traits>
+
 #include "ra_layernorm.cuh"
 
 #if !defined(RA_SLICE_DT) || !defined(RA_SLICE_W)
@@ -31,11 +33,24 @@ cudaError_t allow_smem(K kernel, size_t smem) {
   return smem <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-template <int E>
+// launch(std::bool_constant): the kernel with a second mean or without, as rows of `cols` columns (LEAST to MOST) have it.
+template <uint64_t LEAST, uint64_t MOST, class F>
+cudaError_t with_second(uint64_t cols, F launch) {
+  constexpr bool never = DT == DT_BF16 || (DT == DT_F16 && MOST <= 8192), always = DT == DT_F32 || (DT == DT_F16 && LEAST > 8192);
+  if constexpr (never) return launch(std::false_type{});
+  else if constexpr (always) return launch(std::true_type{});
+  else return second_mean<DT>(cols) ? launch(std::true_type{}) : launch(std::false_type{});
+}
+
+// E columns a thread: rows of LEAST columns or more.
+template <int E, uint64_t LEAST>
 cudaError_t forward_registers(const LnForward& a, uint32_t group, cudaStream_t s) {
   const uint64_t per_cta = group == 32 ? kLnWarpThreads / 32 : 1, ctas = (a.rows + per_cta - 1) / per_cta;
-  return group == 32 ? launch_programmatic(ln_forward_registers<DT, WDT, E, true>, dim3((unsigned)ctas), kLnWarpThreads, 0, s, a)
-                     : launch_programmatic(ln_forward_registers<DT, WDT, E, false>, dim3((unsigned)ctas), group, 0, s, a);
+  return with_second<LEAST, E * kLnMaxThreads>(a.cols, [&](auto second) {
+    constexpr bool S = decltype(second)::value;
+    return group == 32 ? launch_programmatic(ln_forward_registers<DT, WDT, E, true, S>, dim3((unsigned)ctas), kLnWarpThreads, 0, s, a)
+                       : launch_programmatic(ln_forward_registers<DT, WDT, E, false, S>, dim3((unsigned)ctas), group, 0, s, a);
+  });
 }
 // CTAs, each with a row of `reach` columns, that an SM holds at `per` columns a thread: by registers (64, 85 or 128 a
 // thread) and by the shared memory for the weights.
@@ -46,13 +61,16 @@ uint64_t shifted_rows(uint64_t reach, uint32_t per, size_t smem) {
   return rows < 1 ? 1 : rows;
 }
 
-template <int E>
+template <int E, uint64_t LEAST>
 cudaError_t forward_shifted(const LnForward& a, uint32_t group, size_t smem, cudaStream_t s) {
-  const cudaError_t err = allow_smem(ln_forward_shifted<DT, WDT, E>, smem);
-  if (err != cudaSuccess) return err;
-  const uint64_t per_sm = shifted_rows((uint64_t)group * E, E, smem);
-  const uint64_t ctas = a.rows < 152 * per_sm ? a.rows : 152 * per_sm;
-  return launch_programmatic(ln_forward_shifted<DT, WDT, E>, dim3((unsigned)ctas), group, smem, s, a);
+  return with_second<LEAST, E * kLnMaxThreads>(a.cols, [&](auto second) {
+    const auto kernel = ln_forward_shifted<DT, WDT, E, decltype(second)::value>;
+    const cudaError_t err = allow_smem(kernel, smem);
+    if (err != cudaSuccess) return err;
+    const uint64_t per_sm = shifted_rows((uint64_t)group * E, E, smem);
+    const uint64_t ctas = a.rows < 152 * per_sm ? a.rows : 152 * per_sm;
+    return launch_programmatic(kernel, dim3((unsigned)ctas), group, smem, s, a);
+  });
 }
 
 template <int E, bool KEEP>
@@ -116,20 +134,20 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   const bool aligned = a.cols % V == 0 && !phase(a.x) && !phase(a.y) && !line(a.x_stride) && !line(a.y_stride) &&
                        !phase(a.w) && !phase(a.b);
   if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64 && a.rows <= 0x7fffffffull) {  // a CTA for every row, or for 4
-    if (a.cols <= 256) return forward_registers<8>(a, 32, s);
-    if (a.cols <= 512) return forward_registers<16>(a, 32, s);
+    if (a.cols <= 256) return forward_registers<8, 0>(a, 32, s);
+    if (a.cols <= 512) return forward_registers<16, 0>(a, 32, s);
     // few rows leave SMs idle: more threads to a row, fewer columns each (1 x 1024: 1.6 us against 2.1, 512 x 1024: 2.4
     // against 2.8); many rows want the row's fixed cost on few threads (8192 x 4096: 24 us against 36)
-    if (a.rows <= 608 && a.cols <= 4096) return forward_registers<8>(a, group_for(a.cols, 8), s);
-    if (a.cols <= 16384) return forward_registers<32>(a, group_for(a.cols, 32), s);
-    return forward_registers<64>(a, group_for(a.cols, 64), s);
+    if (a.rows <= 608 && a.cols <= 4096) return forward_registers<8, 0>(a, group_for(a.cols, 8), s);
+    if (a.cols <= 16384) return forward_registers<32, 0>(a, group_for(a.cols, 32), s);
+    return forward_registers<64, 16385>(a, group_for(a.cols, 64), s);
   }
   // x and y in step: every row of both at the same place in its 16-byte line
   const uint64_t reach = a.cols + V - 1;  // a line more, at most
   if (phase(a.x) == phase(a.y) && line(a.x_stride) == line(a.y_stride) && reach <= (uint64_t)kLnMaxThreads * 64) {
     const size_t smem = 2 * sizeof(float) * ln_share_elems((uint32_t)a.cols, es, true, 1);
     if (smem <= kLnSmem) {
-      if (reach > 8192 && reach <= 9216) return forward_shifted<24>(a, group_for(reach, 24), smem, s);
+      if (reach > 8192 && reach <= 9216) return forward_shifted<24, 0>(a, group_for(reach, 24), smem, s);
       if (reach <= 8192) {
         // More columns a thread leave fewer warps that are partly empty. Taken where a third more rows are at work on
         // an SM and there are rows enough for the longer start: 16000 x 4095 bf16 58.4 -> 51.0 us, 16000 x 701 19.2 ->
@@ -137,15 +155,15 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
         const bool wider = a.rows > 4096 && 3 * shifted_rows(reach, reach <= 512 ? 16 : 24, smem) >=
                                                 4 * shifted_rows(reach, reach <= 512 ? 8 : 16, smem);
         if (reach <= 512) {
-          return wider ? forward_shifted<16>(a, group_for(reach, 16), smem, s)
-                       : forward_shifted<8>(a, group_for(reach, 8), smem, s);
+          return wider ? forward_shifted<16, 0>(a, group_for(reach, 16), smem, s)
+                       : forward_shifted<8, 0>(a, group_for(reach, 8), smem, s);
         }
-        return wider ? forward_shifted<24>(a, group_for(reach, 24), smem, s)
-                     : forward_shifted<16>(a, group_for(reach, 16), smem, s);
+        return wider ? forward_shifted<24, 0>(a, group_for(reach, 24), smem, s)
+                     : forward_shifted<16, 0>(a, group_for(reach, 16), smem, s);
       }
-      if (reach <= 16384) return forward_shifted<32>(a, group_for(reach, 32), smem, s);
+      if (reach <= 16384) return forward_shifted<32, 9217 - V>(a, group_for(reach, 32), smem, s);
       // 64 columns a thread spill; at 4 bytes a column the general kernel is faster (3000 x 23001 fp32: 230 us, not 405)
-      if constexpr (es == 2) return forward_shifted<64>(a, group_for(reach, 64), smem, s);
+      if constexpr (es == 2) return forward_shifted<64, 16385 - V>(a, group_for(reach, 64), smem, s);
     }
   }
   return launch_programmatic(ln_forward_rows<DT, WDT>, dim3(row_ctas(a.rows)), kLnThreads, 0, s, a);

@@ -84,3 +84,39 @@ def test_backward_far_from_zero(ra, cols, offset, std):
     mean = x.double().mean(1).float()
     rstd = ((x.double() - mean.double()[:, None]).square().mean(1) + EPS).rsqrt().float()
     check_backward(ra, dy, x, w, mean, rstd)
+
+
+# rows and columns of every way through the forward pass, at few rows and at many
+FORWARD = [(5, 64), (5, 300), (5, 768), (5000, 768), (5, 1000), (5000, 1003), (5, 1537), (5000, 701), (5000, 4095), (5, 5000), (5, 8191),
+           (5, 9001), (5, 12288), (5, 14001), (5, 16384), (5, 20000), (5, 20001), (5, 32768), (3, 33001), (3, 70001)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", FORWARD)
+@pytest.mark.parametrize("dtype,value", [(F32, 12345.678), (F32, 0.1), (F32, -1999.37), (F32, 10000001.0), (F32, 1e30), (F16, 2047.0),
+                                         (F16, 0.33325), (BF16, 255.0)])
+def test_a_constant_row_is_its_own_mean(ra, dtype, value, rows, cols):
+    # its mean is the value to the last bit, so y is the bias and 1 / deviation 1 / sqrt(eps)
+    gpu()
+    for step in (0, 1):  # x and y in step, and one element apart
+        x = torch.full((rows, cols), value, device="cuda").to(dtype)
+        y = torch.empty(rows * cols + 1, device="cuda", dtype=dtype)[step:rows * cols + step].view(rows, cols)
+        b = torch.randn(cols, device="cuda").to(dtype)
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        ra.ra_layernorm_forward(x, None, b, y, mean, rstd)
+        assert torch.equal(mean, x[:, 0].float()), float((mean - x[:, 0].float()).abs().max())
+        assert torch.equal(y, b.expand_as(y))
+        assert ((rstd.double() - CONST_RSTD).abs() <= 4 * U * CONST_RSTD).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [64, 1000, 1537, 9001, 16384, 33001])
+@pytest.mark.parametrize("dtype", [F32, F16])
+def test_rows_that_are_not_finite_keep_their_mean(ra, dtype, cols):
+    gpu()
+    x = torch.zeros(3, cols, device="cuda", dtype=dtype)
+    x[0, 3], x[1, 5], x[2, 7] = float("inf"), -float("inf"), float("nan")
+    y, mean, rstd = torch.empty_like(x), torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+    ra.ra_layernorm_forward(x, None, None, y, mean, rstd)
+    assert float(mean[0]) == float("inf") and float(mean[1]) == -float("inf") and bool(torch.isnan(mean[2]))
+    assert bool(torch.isnan(y).all())

@@ -380,6 +380,7 @@ class _Torch:
     codes: dict = {}  # torch dtype -> ra_dtype_t
     f32 = None
     current_stream = None  # device index -> handle of torch's current stream there
+    current_device = None  # () -> index of torch's current device
 
     @classmethod
     def load(cls):
@@ -387,6 +388,7 @@ class _Torch:
 
         cls.f32 = torch.float32
         cls.current_stream = torch._C._cuda_getCurrentRawStream
+        cls.current_device = torch._C._cuda_getDevice
         cls.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
         return cls
 
@@ -398,10 +400,13 @@ def _float_code(t, what: str) -> int:
     return code
 
 
-def _stream_of(t, stream) -> int:
-    """The stream handle a call on tensor t goes to: ``stream``, or torch's current one on t's device (read
-    without building a Stream object, which would cost as much as the launch)."""
-    return _Torch.current_stream(t.get_device()) if stream is None else _stream_ptr(stream)
+def _stream_on(device: int, stream, what: str) -> int:
+    """The stream handle a call whose tensors are on ``device`` goes to: ``stream``, or torch's current one there
+    (read without building a Stream object, which would cost as much as the launch). The library launches on the
+    current device, so that has to be the tensors'."""
+    if _Torch.current_device() != device:
+        raise ValueError(f"{what}: the tensors are on cuda:{device}, which is not torch's current CUDA device")
+    return _Torch.current_stream(device) if stream is None else _stream_ptr(stream)
 
 
 def _rows_contiguous(t) -> bool:
@@ -413,20 +418,21 @@ def _row_stride(t, cols: int) -> int:
     return max(t.stride(0), cols) if t.shape[0] <= 1 else t.stride(0)
 
 
-def _is_vector(t, n: int, dtype) -> bool:
-    """A contiguous CUDA tensor of n elements, or None."""
-    return t is None or (t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous())
+def _is_vector(t, n: int, dtype, device: int) -> bool:
+    """A contiguous tensor of n elements on CUDA device ``device``, or None."""
+    return t is None or (t.get_device() == device and t.dtype is dtype and t.numel() == n and t.is_contiguous())
 
 
 def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_vectors(what: str, **vectors) -> None:
-    """Raises for the first of ``name=(tensor, count, dtype)`` that is not a vector of that kind."""
+def _check_vectors(what: str, device: int, **vectors) -> None:
+    """Raises for the first of ``name=(tensor, count, dtype)`` that is not a vector of that kind on ``device``."""
     for name, (t, n, dtype) in vectors.items():
-        if not _is_vector(t, n, dtype):
-            raise ValueError(f"{what}: {name} must be a contiguous CUDA tensor of {n} elements of {dtype}")
+        if not _is_vector(t, n, dtype, device):
+            raise ValueError(f"{what}: {name} must be a contiguous CUDA tensor of {n} elements of {dtype}, "
+                             f"on cuda:{device}")
 
 
 def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
@@ -438,22 +444,23 @@ def ra_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 
     wdtype = dtype if w is None else w.dtype
     shape = x.shape
     dense = x.is_contiguous() and y.is_contiguous()
-    if not (x.is_cuda and y.is_cuda and len(shape) == 2 and y.shape == shape and y.dtype is dtype
+    device = x.get_device()
+    if not (device >= 0 and y.get_device() == device and len(shape) == 2 and y.shape == shape and y.dtype is dtype
             and (dense or (_rows_contiguous(x) and _rows_contiguous(y)))):
-        raise ValueError("ra_layernorm_forward: x and y must be 2-D CUDA tensors of one shape and dtype, rows "
-                         "contiguous")
+        raise ValueError("ra_layernorm_forward: x and y must be 2-D CUDA tensors of one shape, dtype and device, "
+                         "rows contiguous")
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_forward: unsupported dtype {dtype} with weights of {wdtype}")
     rows, cols = shape
     f32 = _Torch.f32
-    if not (_is_vector(weight, cols, wdtype) and _is_vector(bias, cols, wdtype) and _is_vector(mean, rows, f32)
-            and _is_vector(rstd, rows, f32)):
-        _check_vectors("ra_layernorm_forward", weight=(weight, cols, wdtype), bias=(bias, cols, wdtype),
+    if not (_is_vector(weight, cols, wdtype, device) and _is_vector(bias, cols, wdtype, device)
+            and _is_vector(mean, rows, f32, device) and _is_vector(rstd, rows, f32, device)):
+        _check_vectors("ra_layernorm_forward", device, weight=(weight, cols, wdtype), bias=(bias, cols, wdtype),
                        mean=(mean, rows, f32), rstd=(rstd, rows, f32))
     st = (_lib or lib()).ra_layernorm_forward(
         x.data_ptr(), cols if dense else _row_stride(x, cols), _address(weight), _address(bias), y.data_ptr(),
         cols if dense else _row_stride(y, cols), _address(mean), _address(rstd), rows, cols, eps, codes[dtype],
-        codes[wdtype], _stream_of(x, stream))
+        codes[wdtype], _stream_on(device, stream, "ra_layernorm_forward"))
     if st:
         raise RaError(st, "ra_layernorm_forward")
 
@@ -474,38 +481,43 @@ def ra_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     wdtype = dtype if w is None else w.dtype
     shape = x.shape
     dense = x.is_contiguous() and dy.is_contiguous() and dx.is_contiguous()
-    if not (x.is_cuda and dy.is_cuda and dx.is_cuda and len(shape) == 2 and dy.shape == shape and dx.shape == shape
-            and dy.dtype is dtype and dx.dtype is dtype
+    device = x.get_device()
+    if not (device >= 0 and dy.get_device() == device and dx.get_device() == device and len(shape) == 2
+            and dy.shape == shape and dx.shape == shape and dy.dtype is dtype and dx.dtype is dtype
             and (dense or (_rows_contiguous(x) and _rows_contiguous(dy) and _rows_contiguous(dx)))):
-        raise ValueError("ra_layernorm_backward: x, dy and dx must be 2-D CUDA tensors of one shape and dtype, rows "
-                         "contiguous")
+        raise ValueError("ra_layernorm_backward: x, dy and dx must be 2-D CUDA tensors of one shape, dtype and "
+                         "device, rows contiguous")
     if dtype not in codes or wdtype not in codes:
         raise TypeError(f"ra_layernorm_backward: unsupported dtype {dtype} with weights of {wdtype}")
     rows, cols = shape
     f32 = _Torch.f32
     if mean is None or rstd is None or not (
-            _is_vector(weight, cols, wdtype) and _is_vector(dweight, cols, wdtype) and _is_vector(dbias, cols, wdtype)
-            and _is_vector(mean, rows, f32) and _is_vector(rstd, rows, f32)
-            and (workspace is None or (workspace.is_cuda and workspace.is_contiguous()))):
+            _is_vector(weight, cols, wdtype, device) and _is_vector(dweight, cols, wdtype, device)
+            and _is_vector(dbias, cols, wdtype, device) and _is_vector(mean, rows, f32, device)
+            and _is_vector(rstd, rows, f32, device)
+            and (workspace is None or (workspace.get_device() == device and workspace.is_contiguous()))):
         if mean is None or rstd is None:
             raise ValueError("ra_layernorm_backward: mean and rstd are needed, as ra_layernorm_forward stored them")
-        _check_vectors("ra_layernorm_backward", weight=(weight, cols, wdtype), dweight=(dweight, cols, wdtype),
+        _check_vectors("ra_layernorm_backward", device, weight=(weight, cols, wdtype), dweight=(dweight, cols, wdtype),
                        dbias=(dbias, cols, wdtype), mean=(mean, rows, f32), rstd=(rstd, rows, f32))
-        raise ValueError("ra_layernorm_backward: workspace must be a contiguous CUDA tensor")
+        raise ValueError(f"ra_layernorm_backward: workspace must be a contiguous CUDA tensor, on cuda:{device}")
     st = (_lib or lib()).ra_layernorm_backward(
         dy.data_ptr(), cols if dense else _row_stride(dy, cols), x.data_ptr(), cols if dense else _row_stride(x, cols),
         _address(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), cols if dense else _row_stride(dx, cols),
-        _address(dweight), _address(dbias), accumulate, rows, cols, codes[dtype], codes[wdtype], _address(workspace), 0 if workspace is None else workspace.nbytes,
-        _stream_of(x, stream))
+        _address(dweight), _address(dbias), accumulate, rows, cols, codes[dtype], codes[wdtype], _address(workspace),
+        0 if workspace is None else workspace.nbytes, _stream_on(device, stream, "ra_layernorm_backward"))
     if st:
         raise RaError(st, "ra_layernorm_backward")
 
 
-def _same_type(tensors, what: str):
+def _same_type(tensors, what: str, device: int):
+    """Raises unless the tensors are contiguous, of one dtype and on CUDA device ``device``."""
     dt = tensors[0].dtype if tensors else None
     for t in tensors:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{what}: every tensor must be a contiguous CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{what}: all tensors must be on one device")
         if t.dtype != dt:
             raise ValueError(f"{what}: all tensors must share one dtype")
 
@@ -516,7 +528,8 @@ class GradTensors:
 
     def __init__(self, grads):
         self.tensors = list(grads)
-        _same_type(self.tensors, "grad_tensors")
+        self.device = self.tensors[0].get_device() if self.tensors else None
+        _same_type(self.tensors, "grad_tensors", self.device)
         self.dtype = _float_code(self.tensors[0], "grad_tensors") if self.tensors else 0
         n = len(self.tensors)
         self.addresses = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.tensors])
@@ -539,11 +552,14 @@ def ra_grad_norm(grads, max_norm: float, out, workspace, prescale: float = 1.0, 
     ra_grad_norm_workspace() bytes, zeroed once."""
     g = grads if isinstance(grads, GradTensors) else GradTensors(grads)
     f32 = _Torch.f32 or _Torch.load().f32
-    if out is None or not _is_vector(out, 2, f32) or not (workspace.is_cuda and workspace.is_contiguous()):
+    device = out.get_device() if g.device is None and out is not None else g.device
+    if (out is None or not (out.is_cuda and _is_vector(out, 2, f32, device))
+            or not (workspace.get_device() == device and workspace.is_contiguous())):
         raise ValueError("ra_grad_norm: out must be a contiguous CUDA tensor of 2 float32, workspace a contiguous CUDA "
-                         "tensor")
+                         "tensor, both on the gradients' device")
     st = (_lib or lib()).ra_grad_norm(g.addresses, g.counts, len(g.tensors), g.dtype, prescale, max_norm,
-                                      out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_of(out, stream))
+                                      out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                      _stream_on(device, stream, "ra_grad_norm"))
     if st:
         raise RaError(st, "ra_grad_norm")
 
@@ -571,8 +587,9 @@ class AdamwTensors:
         decay = list(weight_decay) if hasattr(weight_decay, "__iter__") else [weight_decay] * n
         if len(decay) != n or any(len(v) != n for v in lists.values()):
             raise ValueError(f"{what}: every list must have one entry per parameter")
+        self.device = params[0].get_device() if n else None
         for name, tensors in lists.items():
-            _same_type(tensors, f"{what}: {name}")
+            _same_type(tensors, f"{what}: {name}", self.device)
             for t, p in zip(tensors, params):
                 want = -(-p.numel() // RA_ADAMW_BLOCK) if name.endswith("scales") else p.numel()
                 if t.numel() != want:
@@ -616,13 +633,13 @@ def ra_adamw(tensors: AdamwTensors, lr: float, step: int, beta1: float = 0.9, be
     """One AdamW step over an adamw_tensors() list. ``step`` counts from 1. ``grad_scale``: a float32 CUDA
     tensor of one element the gradients are multiplied by (out[1:] of ra_grad_norm); not finite: nothing is
     written. ``seed``: of the stochastic rounding of 8-bit moments."""
-    if not _is_vector(grad_scale, 1, _Torch.f32 or _Torch.load().f32):
-        raise ValueError("ra_adamw: grad_scale must be a CUDA tensor of one float32")
     params = tensors.lists["params"]
     if not params:
         return
+    if not _is_vector(grad_scale, 1, _Torch.f32 or _Torch.load().f32, tensors.device):
+        raise ValueError("ra_adamw: grad_scale must be a CUDA tensor of one float32, on the parameters' device")
     opts = AdamwOptions(lr, beta1, beta2, eps, step, _address(grad_scale), tensors.state, tensors.copy_dtype, seed)
     st = (_lib or lib()).ra_adamw(tensors.table, len(params), tensors.param_dtype, tensors.grad_dtype,
-                                  ctypes.byref(opts), _stream_of(params[0], stream))
+                                  ctypes.byref(opts), _stream_on(tensors.device, stream, "ra_adamw"))
     if st:
         raise RaError(st, "ra_adamw")

@@ -553,7 +553,7 @@ def ra_grad_norm(grads, max_norm: float, out, workspace, prescale: float = 1.0, 
     g = grads if isinstance(grads, GradTensors) else GradTensors(grads)
     f32 = _Torch.f32 or _Torch.load().f32
     device = out.get_device() if g.device is None and out is not None else g.device
-    if (out is None or not (out.is_cuda and _is_vector(out, 2, f32, device))
+    if (out is None or workspace is None or not (out.is_cuda and _is_vector(out, 2, f32, device))
             or not (workspace.get_device() == device and workspace.is_contiguous())):
         raise ValueError("ra_grad_norm: out must be a contiguous CUDA tensor of 2 float32, workspace a contiguous CUDA "
                          "tensor, both on the gradients' device")

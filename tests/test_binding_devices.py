@@ -121,3 +121,11 @@ def test_no_gradients_at_all(library):
         ra.ra_grad_norm([], 1.0, OnDevice(1, 2), OnDevice(1, 64))
     with pytest.raises(ValueError):
         ra.ra_grad_norm([], 1.0, torch.zeros(2), torch.zeros(64))
+
+
+def test_a_missing_workspace_is_refused(library):
+    with pytest.raises(ValueError, match="workspace"):
+        ra.ra_grad_norm([OnDevice(0, 3)], 1.0, OnDevice(0, 2), None)
+    with pytest.raises(ValueError, match="out"):
+        ra.ra_grad_norm([OnDevice(0, 3)], 1.0, None, OnDevice(0, 64))
+    assert not library.calls

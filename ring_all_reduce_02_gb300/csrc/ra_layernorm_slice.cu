@@ -28,9 +28,12 @@ unsigned row_ctas(uint64_t rows) { return (unsigned)(rows < 152 * 8 ? rows : 152
 // Threads for a row of `cols` columns, `per` or fewer to each: whole warps.
 uint32_t group_for(uint64_t cols, uint32_t per) { return (uint32_t)((cols + 32 * per - 1) / (32 * per)) * 32; }
 
+// Lets a kernel take `smem` bytes. The limit is the function's, not the call's: it is set to the same value by every
+// call, so that none of another thread's lowers it between this and the launch.
 template <class K>
 cudaError_t allow_smem(K kernel, size_t smem) {
-  return smem <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmem);
 }
 
 // launch(std::bool_constant): the kernel with a second mean or without, as rows of `cols` columns (LEAST to MOST) have it.

@@ -302,6 +302,9 @@ constexpr size_t kBulkSmemBudget = (size_t)RA_BULK_SMEM_KB * 1024;
 #define RA_BULK_MAX_STAGES 8
 #endif
 constexpr int kBulkMaxStages = RA_BULK_MAX_STAGES;
+// Bytes of a launch's mbarriers, two for each stage, in whole lines; and the shared memory that no launch passes.
+constexpr size_t bulk_barrier_bytes(size_t stages) { return 128 * ((2 * stages * 8 + 127) / 128); }
+constexpr size_t kBulkMaxSmem = bulk_barrier_bytes(kBulkMaxStages) + kBulkSmemBudget;
 
 // A planned bulk-engine launch: kernel arguments, grid and shared memory.
 struct BulkLaunch {
@@ -310,8 +313,8 @@ struct BulkLaunch {
   size_t smem = 0;
 };
 
-// Plans a bulk-engine launch and raises the kernel's shared-memory limit to
-// what it needs. Enqueues nothing: every error the bulk path can report before
+// Plans a bulk-engine launch and sets the kernel's shared-memory limit.
+// Enqueues nothing: every error the bulk path can report before
 // its launch is reported here.
 ra_status_t plan_bulk(const ra::Args& a, int dtype, int op, int max_sms, BulkLaunch* p) {
   // the bulk engine's loads are TMA bulk copies, which the library issues on device memory only
@@ -346,14 +349,14 @@ ra_status_t plan_bulk(const ra::Args& a, int dtype, int op, int max_sms, BulkLau
   if (stages > (size_t)kBulkMaxStages) stages = kBulkMaxStages;
   if (stages < 2) return RA_ERR_UNSUPPORTED;
   b.stages = (uint32_t)stages;
-  p->smem = 128 * ((2 * stages * 8 + 127) / 128) + stages * stage_bytes;
+  p->smem = bulk_barrier_bytes(stages) + stages * stage_bytes;
   const uint64_t v = (uint64_t)(ra::kVecBytes / elem_size(dtype));
   const uint64_t tiles = ((a.count + n - 1) / n / v) / b.tile_vecs + 1;
   uint64_t gx = (uint64_t)sms / (uint64_t)n;
   if (gx > tiles) gx = tiles;
   if (gx < 1) gx = 1;
   p->grid = dim3((unsigned)gx, (unsigned)n);
-  const cudaError_t err = ra::configure_bulk_kernel(dtype, op, p->smem);
+  const cudaError_t err = ra::configure_bulk_kernel(dtype, op, kBulkMaxSmem);
   return err == cudaSuccess ? RA_SUCCESS : cuda_failed(err);
 }
 

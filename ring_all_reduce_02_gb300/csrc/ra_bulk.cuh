@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(NC + 32, 1) ar_bulk_kernel(const __grid_consta
   }
 }
 
-// Raises both instances' dynamic shared-memory limit to `smem`; enqueues nothing.
+// Sets both instances' dynamic shared-memory limit to `smem`; enqueues nothing. The limit is the kernels', not the
+// call's: `smem` has to be the same in every call, or one of another thread's could lower it before the launch.
 template <int DT, int OP>
 cudaError_t configure_bulk_op(size_t smem) {
   const cudaError_t err = cudaFuncSetAttribute(ar_bulk_kernel<DT, OP, kBulkConsumersWide>,
@@ -210,7 +211,7 @@ cudaError_t configure_bulk_op(size_t smem) {
                               (int)smem);
 }
 
-// Launches the kernel; configure_bulk_op(smem) must have succeeded on this device.
+// Launches the kernel; configure_bulk_op must have succeeded on this device, with `smem` or more.
 template <int DT, int OP>
 cudaError_t launch_bulk_op(const BulkArgs& b, dim3 grid, size_t smem, cudaStream_t s) {
   if (b.consumers == (uint32_t)kBulkConsumersWide)

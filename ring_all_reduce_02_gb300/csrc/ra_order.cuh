@@ -141,8 +141,10 @@ __global__ void __launch_bounds__(kOrdThreads, 6) ordered_kernel(const __grid_co
 template <int DT, int OP, bool IS_RS>
 cudaError_t launch_ordered_kind(const OrderArgs& o, dim3 grid, cudaStream_t s) {
   const size_t smem = (size_t)o.base.nranks * kOrdThreads * kOrdVecBytes;
-  const cudaError_t err =
-      cudaFuncSetAttribute(ordered_kernel<DT, OP, IS_RS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit is the kernel's, not the call's: every call sets it to what the most ranks take, so that none of another
+  // thread's lowers it between this and the launch.
+  const cudaError_t err = cudaFuncSetAttribute(ordered_kernel<DT, OP, IS_RS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               RA_MAX_RANKS * kOrdThreads * kOrdVecBytes);
   if (err != cudaSuccess) return err;
   return launch_programmatic(ordered_kernel<DT, OP, IS_RS>, grid, kOrdThreads, smem, s, o);
 }

@@ -73,3 +73,27 @@ def test_layer_norm(ra, widths):
     torch.cuda.synchronize()
     assert not together(calls, 10000)
     assert all(torch.equal(a, b) for a, b in zip(outputs, want))
+
+
+# rank counts that share a kernel and differ in the shared memory that it takes
+@pytest.mark.parametrize("ranks,how", [((32, 27, 48, 40), dict(order="tree")), ((32, 64), dict(order="rabenseifner")),
+                                       ((8, 11, 13, 16), dict(engine="bulk"))], ids=str)
+def test_all_reduce(ra, ranks, how):
+    calls, outputs, keep = [], [], []
+    for n in ranks:
+        count = n * 1024 + 3
+        gen = torch.Generator(device="cuda").manual_seed(n)
+        sends = [torch.randint(-5, 6, (count,), generator=gen, device="cuda").float() for _ in range(n)]
+        recvs = [torch.zeros(count, device="cuda") for _ in range(n)]
+        status, stream = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+        args = ([t.data_ptr() for t in sends], [t.data_ptr() for t in recvs], count, 0, 0, n,
+                ra.ORDER_CODES[how.get("order", "ring")], 0, stream.cuda_stream, 0, ra.ENGINE_CODES[how.get("engine", "registers")],
+                status.data_ptr())
+        calls.append(lambda a=args: ra.call_ex("ra_allreduce_ex", *a))
+        outputs.append((recvs, sum(sends)))
+        keep += [sends, status, stream]
+    torch.cuda.synchronize()
+    assert not [st for st in (c() for c in calls) if st]
+    assert not together(calls, 5000)
+    for recvs, want in outputs:  # whole numbers: exact in any order
+        assert all(torch.equal(t, want) for t in recvs)

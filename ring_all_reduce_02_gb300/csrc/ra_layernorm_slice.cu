@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "ra_layernorm.cuh"
+#include "ra_layernorm_plan.h"
 
 #if !defined(RA_SLICE_DT) || !defined(RA_SLICE_W)
 #error "compile with -DRA_SLICE_DT=<dtype id> -DRA_SLICE_W=<dtype id>"
@@ -93,10 +94,10 @@ cudaError_t backward_fused(LnBackward* all, bool shifted, size_t weights, size_t
   return err != cudaSuccess ? err : launch_programmatic(kernel, dim3((unsigned)a.parts), groups * a.group, smem, s, a);
 }
 
-// The fused kernel with a cluster of a.split CTAs to a row: a.parts becomes the number of clusters, as many as the GPU
-// holds at once (a second wave would take as long again), a multiple of the rows that share a phase.
+// The fused kernel with a cluster of a.split CTAs to a row; a.parts becomes the number of clusters. Where the device
+// holds too few (it may be shared out), nothing is launched and *fits becomes false.
 template <int E>
-cudaError_t backward_late(LnBackward* a, bool shifted, size_t weights, size_t stage, cudaStream_t s) {
+cudaError_t backward_late(LnBackward* a, bool shifted, size_t weights, size_t stage, cudaStream_t s, bool* fits) {
   const size_t stages = (kLnSmem - weights) / stage;
   a->stages = stages >= 8 ? 8 : stages >= 6 ? 6 : stages >= 4 ? 4 : (uint32_t)stages;
   size_t smem = weights + a->stages * stage;
@@ -121,9 +122,10 @@ cudaError_t backward_late(LnBackward* a, bool shifted, size_t weights, size_t st
   err = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
   if (err != cudaSuccess) return err;
   if (clusters > (int)(kLnMaxParts / a->split)) clusters = (int)(kLnMaxParts / a->split);
-  if (shifted && clusters > (int)V) clusters = clusters / (int)V * (int)V;
-  if (clusters < 1 || (shifted && clusters < (int)V)) return cudaErrorInvalidConfiguration;
-  a->parts = a->rows < (uint64_t)clusters ? (int)a->rows : clusters;
+  const uint64_t parts = late_clusters((uint64_t)clusters, a->rows, shifted ? V : 1);
+  *fits = parts > 0;
+  if (!*fits) return cudaSuccess;
+  a->parts = (int)parts;
   cfg.gridDim = dim3((unsigned)a->parts * a->split);
   cfg.numAttrs = RA_PDL ? 2 : 1;
   err = cudaLaunchKernelEx(&cfg, kernel, *a);
@@ -218,8 +220,10 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
     if (share > kLnMaxThreads * per || weights + 2 * row > kLnSmem) continue;
     a.split = split;
     a.group = group_for(share, per);
-    err = per == 16 ? backward_late<16>(&a, !aligned, weights, row, s) : backward_late<24>(&a, !aligned, weights, row, s);
-    return err != cudaSuccess ? err : finish();
+    bool fits = true;
+    err = per == 16 ? backward_late<16>(&a, !aligned, weights, row, s, &fits)
+                    : backward_late<24>(&a, !aligned, weights, row, s, &fits);
+    if (err != cudaSuccess || fits) return err != cudaSuccess ? err : finish();
   }
   if (sums) {  // before dx, which may be x or dy
     if (a.parts) {

@@ -367,7 +367,8 @@ ra_status_t ra_allreduce_bulk_noalloc(const void* const* sendbufs, void* const* 
  * weight, bias: `cols` elements of weight_dtype (dtype itself or RA_FLOAT32);
  * NULL weight = ones, NULL bias = zeros. mean, rstd: `rows` floats, kept for
  * the backward pass; either may be NULL. y may be x (same stride); any other
- * overlap of an output with another buffer is RA_ERR_ALIAS.
+ * overlap of an output with another buffer is RA_ERR_ALIAS. Column slices of
+ * one matrix (one stride, rows side by side) do not overlap.
  * rows == 0 or cols == 0 enqueues nothing.
  * HBM traffic: reads and writes rows*cols*e.
  */
@@ -380,7 +381,7 @@ ra_status_t ra_layernorm_forward(const void* x, size_t x_stride, const void* wei
  *   dx      = rstd * (a - avg_row(a) - xhat * avg_row(a * xhat)),
  *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy.
  * mean, rstd: as ra_layernorm_forward stored them. dx: dtype; it may be dy or
- * x (same stride). dweight, dbias: `cols` elements of weight_dtype, anywhere
+ * x (same stride), and overlap is as there. dweight, dbias: `cols` elements of weight_dtype, anywhere
  * (slices of a flat gradient buffer); either may be NULL. accumulate != 0 adds
  * to what they hold (in fp32, rounded once), 0 overwrites. rows == 0 gives
  * zero sums. workspace: at least ra_layernorm_workspace(rows, cols) bytes of

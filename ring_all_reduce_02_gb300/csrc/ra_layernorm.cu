@@ -31,6 +31,7 @@ struct Buffer {
   uintptr_t align;
   bool needed;
   Range at;
+  uint64_t stride = 0;  // of a matrix, in bytes
 };
 
 // A span of 2^57 elements at most, not null (unless it may be), aligned, inside the address space.
@@ -41,6 +42,14 @@ bool sound(Buffer& b) {
   if (lo % b.align || lo + b.bytes < lo) return false;
   b.at = {lo, lo + (uintptr_t)b.bytes};
   return true;
+}
+// Whether two buffers share a byte. Matrices of one stride whose rows (of `width` bytes) lie side by side do not, as
+// column slices of one matrix.
+bool shares(const Buffer& a, const Buffer& b, uint64_t width) {
+  if (!ra::overlaps(a.at, b.at)) return false;
+  if (a.stride == 0 || a.stride != b.stride) return true;
+  const uint64_t apart = (a.at.lo < b.at.lo ? b.at.lo - a.at.lo : a.at.lo - b.at.lo) % a.stride;
+  return apart < width || apart + width > a.stride;
 }
 bool shape_ok(uint64_t rows, uint64_t cols) {
   return rows <= RA_MAX_COUNT && cols <= RA_MAX_COUNT && (cols == 0 || rows <= RA_MAX_COUNT / cols);
@@ -68,10 +77,10 @@ ra_status_t ra_layernorm_forward(const void* x, size_t x_stride, const void* wei
     return RA_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return RA_SUCCESS;
   const uint64_t es = ra::float_size(dtype), ws = ra::float_size(weight_dtype);
-  Buffer in[3] = {{x, extent(rows, cols, x_stride, es), es, true, {}},
+  Buffer in[3] = {{x, extent(rows, cols, x_stride, es), es, true, {}, x_stride * es},
                   {weight, cols * ws, ws, false, {}},
                   {bias, cols * ws, ws, false, {}}};
-  Buffer out[3] = {{y, extent(rows, cols, y_stride, es), es, true, {}},
+  Buffer out[3] = {{y, extent(rows, cols, y_stride, es), es, true, {}, y_stride * es},
                    {mean, rows * 4, 4, false, {}},
                    {rstd, rows * 4, 4, false, {}}};
   for (Buffer& b : in)
@@ -80,9 +89,9 @@ ra_status_t ra_layernorm_forward(const void* x, size_t x_stride, const void* wei
     if (!sound(b)) return RA_ERR_INVALID_ARG;
   for (int o = 0; o < 3; ++o) {
     for (int i = 0; i < 3; ++i)
-      if (overlaps(out[o].at, in[i].at) && !(o == 0 && i == 0 && y == x && y_stride == x_stride)) return RA_ERR_ALIAS;
+      if (shares(out[o], in[i], cols * es) && !(o == 0 && i == 0 && y == x && y_stride == x_stride)) return RA_ERR_ALIAS;
     for (int q = 0; q < o; ++q)
-      if (overlaps(out[o].at, out[q].at)) return RA_ERR_ALIAS;
+      if (shares(out[o], out[q], cols * es)) return RA_ERR_ALIAS;
   }
   const ra::LnForward a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, (float)eps};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -115,12 +124,12 @@ ra_status_t ra_layernorm_backward(const void* dy, size_t dy_stride, const void* 
   const uint64_t scratch = sums ? ra_layernorm_workspace(rows, cols) : 0;
   if (workspace_bytes < scratch) return RA_ERR_INVALID_ARG;
   const auto full = [&](size_t stride) { return rows ? extent(rows, cols, stride, es) : 0; };
-  Buffer in[5] = {{dy, full(dy_stride), es, rows > 0, {}},
-                  {x, full(x_stride), es, rows > 0, {}},
+  Buffer in[5] = {{dy, full(dy_stride), es, rows > 0, {}, dy_stride * es},
+                  {x, full(x_stride), es, rows > 0, {}, x_stride * es},
                   {weight, cols * ws, ws, false, {}},
                   {mean, rows * 4, 4, rows > 0, {}},
                   {rstd, rows * 4, 4, rows > 0, {}}};
-  Buffer out[4] = {{dx, full(dx_stride), es, rows > 0, {}},
+  Buffer out[4] = {{dx, full(dx_stride), es, rows > 0, {}, dx_stride * es},
                    {dweight, cols * ws, ws, false, {}},
                    {dbias, cols * ws, ws, false, {}},
                    {scratch ? workspace : nullptr, scratch, 16, scratch > 0, {}}};
@@ -132,10 +141,10 @@ ra_status_t ra_layernorm_backward(const void* dy, size_t dy_stride, const void* 
     for (int i = 0; i < 5; ++i) {
       const bool same =
           o == 0 && ((i == 0 && dx == dy && dx_stride == dy_stride) || (i == 1 && dx == x && dx_stride == x_stride));
-      if (overlaps(out[o].at, in[i].at) && !same) return RA_ERR_ALIAS;
+      if (shares(out[o], in[i], cols * es) && !same) return RA_ERR_ALIAS;
     }
     for (int q = 0; q < o; ++q)
-      if (overlaps(out[o].at, out[q].at)) return RA_ERR_ALIAS;
+      if (shares(out[o], out[q], cols * es)) return RA_ERR_ALIAS;
   }
   ra::LnBackward a{dy, x, weight, mean, rstd, dx, dweight, dbias, static_cast<float*>(workspace), rows, cols,
                    dy_stride, x_stride, dx_stride, accumulate, 0, 0, 1, 0};

@@ -7,6 +7,7 @@ is held to its own two roundings (3 u |xhat|) wherever the row lies: no term in
 import pytest
 import torch
 
+import test_layernorm
 from test_layernorm import BF16, EPS, F16, F32, ROUND, STEP, U, gpu
 
 CONST_RSTD = EPS ** -0.5
@@ -120,3 +121,55 @@ def test_rows_that_are_not_finite_keep_their_mean(ra, dtype, cols):
     ra.ra_layernorm_forward(x, None, None, y, mean, rstd)
     assert float(mean[0]) == float("inf") and float(mean[1]) == -float("inf") and bool(torch.isnan(mean[2]))
     assert bool(torch.isnan(y).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [64, 1000, 1003, 1024, 1537, 6000, 20000, 33001])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_column_slices_of_one_matrix(ra, dtype, cols):
+    # x, y, dy and dx side by side in one buffer: their address ranges overlap, their elements do not
+    gpu()
+    rows = 21
+    gen = torch.Generator().manual_seed(cols)
+    for gap in (0, 3, 8):
+        both = torch.full((rows, 2 * cols + 2 * gap), 7.0, dtype=dtype, device="cuda")
+        left, right = both[:, gap:gap + cols], both[:, cols + 2 * gap:]
+        left.copy_(torch.randn(rows, cols, generator=gen))
+        w, b = torch.randn(cols, generator=gen).cuda(), torch.randn(cols, generator=gen).cuda()
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        x = left.clone()
+        test_layernorm.check_forward(ra, left, w, b, right, mean, rstd)
+        assert torch.equal(left, x)
+        right.copy_(torch.randn(rows, cols, generator=gen))
+        dy = right.clone()
+        other = torch.full((rows, 2 * cols + 2 * gap), 7.0, dtype=dtype, device="cuda")
+        dx = other[:, cols + 2 * gap:]
+        other[:, gap:gap + cols].copy_(dy)
+        dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        test_layernorm.check_backward(ra, other[:, gap:gap + cols], left, w, mean, rstd, dx, dw, db)
+        assert torch.equal(other[:, gap:gap + cols], dy) and torch.equal(left, x)
+        for buffer in (both, other):  # and the gaps are left alone
+            assert (buffer[:, :gap] == 7).all() and (buffer[:, gap + cols:cols + 2 * gap] == 7).all()
+
+
+# Fake addresses that are never dereferenced: every case is refused on the host.
+BASE = 0x7F0000000000
+MB = 1 << 20
+
+
+def test_slices_that_share_columns_are_refused(ra):
+    def forward(y, ys, xs=200):
+        return ra.lib().ra_layernorm_forward(BASE, xs, None, None, y, ys, None, None, 16, 64, 1e-5, 2, 2, None)
+
+    def backward(dx, dxs, dys=200):
+        return ra.lib().ra_layernorm_backward(BASE, dys, BASE + 4 * MB, 64, None, BASE + 5 * MB, BASE + 6 * MB, dx, dxs, None, None, 0, 16,
+                                              64, 2, 2, None, 0, None)
+
+    for call in (forward, backward):
+        for apart in (2, 126, 274, 398, 402, 526):  # columns 1, 63, 137, 199 of 200, and the same a row later
+            assert call(BASE + apart, 200) == ra.RA_ERR_ALIAS
+        assert call(BASE - 126, 200) == call(BASE - 274, 200) == ra.RA_ERR_ALIAS
+        assert call(BASE + 128, 199) == call(BASE + 128, 201) == ra.RA_ERR_ALIAS  # another stride
+    # vectors between a matrix's rows
+    assert ra.lib().ra_layernorm_forward(BASE, 200, BASE + 2 * MB, None, BASE + 4 * MB, 200, BASE + 128, None, 16, 64, 1e-5, 2, 0,
+                                         None) == ra.RA_ERR_ALIAS

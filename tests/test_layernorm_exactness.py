@@ -173,3 +173,61 @@ def test_slices_that_share_columns_are_refused(ra):
     # vectors between a matrix's rows
     assert ra.lib().ra_layernorm_forward(BASE, 200, BASE + 2 * MB, None, BASE + 4 * MB, 200, BASE + 128, None, 16, 64, 1e-5, 2, 0,
                                          None) == ra.RA_ERR_ALIAS
+
+
+def strided(rows, cols, dtype, pad, shift, values=None):
+    """A [rows, cols] view with `pad` elements between its rows, `shift` elements past an allocation's start."""
+    base = torch.full((rows * (cols + pad) + shift,), 7.0, dtype=dtype, device="cuda")
+    view = base[shift:].as_strided((rows, cols), (cols + pad, 1))
+    if values is not None:
+        view.copy_(values)
+    return view
+
+
+def assert_gaps_untouched(view):
+    rows, cols = view.shape
+    stride, start = view.stride(0), view.storage_offset()
+    assert (view.as_strided((start,), (1,), 0) == 7).all()
+    if rows > 1 and stride > cols:
+        assert (view.as_strided((rows - 1, stride - cols), (stride, 1), start + cols) == 7).all()
+
+
+# enough rows that every CTA, group of threads and place in shared memory comes to a second row, for each number of
+# columns a thread, on the 16-byte grid and off it, and rows shared by several CTAs
+MANY = [(20003, 200), (20003, 203), (6001, 501), (8001, 1024), (8001, 1003), (5001, 1536), (5001, 4095), (2501, 6000), (1001, 9001),
+        (501, 12001), (501, 14000), (501, 14001), (701, 20000), (401, 20001), (501, 32768)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", MANY)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("pads,shift", [((0, 0, 0), 0), ((16, 48, 32), 0), ((48, 0, 16), 3)])
+def test_every_row_and_stride(ra, dtype, rows, cols, pads, shift):
+    # the matrices are in step (a pad is whole 16-byte lines) and have a stride each
+    gpu()
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+
+    x = strided(rows, cols, dtype, pads[0], shift, normal(rows, cols) * 2 + 0.7)
+    y = strided(rows, cols, dtype, pads[1], shift)
+    w, b = normal(cols) * 0.3 + 1, normal(cols) * 0.3
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ra.ra_layernorm_forward(x, w, b, y, mean, rstd)
+    x64 = x.double()
+    m = x64.mean(1, keepdim=True)
+    r = ((x64 - m).square().mean(1, keepdim=True) + EPS).rsqrt()
+    h = (x64 - m) * r
+    k, top = (cols / 32 + 32) * U, x64.abs().amax(1, keepdim=True)
+    want = h * w.double() + b.double()
+    tol = w.double().abs() * k * (3 * h.abs() + 3 * top * r) + 2 * U * want.abs()
+    within(y, want, ROUND[dtype] * want.abs() + STEP[dtype] + 1.01 * tol, "y")
+    within(mean, m[:, 0], k * top[:, 0] + U * m[:, 0].abs(), "mean")
+    within(rstd, r[:, 0], r[:, 0] * k * (3 + 3 * (top * r)[:, 0]), "rstd")
+    assert_gaps_untouched(y)
+    del x64, h, want, tol, y
+    dy = strided(rows, cols, dtype, pads[2], shift, normal(rows, cols) * 0.1)
+    dx = strided(rows, cols, dtype, pads[1], shift)
+    check_backward(ra, dy, x, w, mean, rstd, dx)
+    assert_gaps_untouched(dx)

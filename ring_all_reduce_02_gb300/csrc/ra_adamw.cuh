@@ -149,9 +149,6 @@ __device__ __forceinline__ void widen8_e4m3(const uint2& q, float* f) {
     f[2 * k] = p.x, f[2 * k + 1] = p.y;
   }
 }
-__device__ __forceinline__ float e4m3_byte(uint32_t w, int k) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(w >> (8 * k)), __NV_E4M3)));
-}
 __device__ __forceinline__ uint32_t pack4_e4m3(const float* f) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);

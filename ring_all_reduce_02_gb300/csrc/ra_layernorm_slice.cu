@@ -46,14 +46,20 @@ cudaError_t with_second(uint64_t cols, F launch) {
   else return second_mean<DT>(cols) ? launch(std::true_type{}) : launch(std::false_type{});
 }
 
-// E columns a thread: rows of LEAST columns or more.
+// E columns a thread: a row to each warp of a CTA, or rows of LEAST columns or more to a CTA of `group` threads.
+template <int E>
+cudaError_t forward_warps(const LnForward& a, cudaStream_t s) {
+  constexpr uint64_t per_cta = kLnWarpThreads / 32;
+  return with_second<0, E * 32>(a.cols, [&](auto second) {
+    return launch_programmatic(ln_forward_registers<DT, WDT, E, true, decltype(second)::value>,
+                               dim3((unsigned)((a.rows + per_cta - 1) / per_cta)), kLnWarpThreads, 0, s, a);
+  });
+}
 template <int E, uint64_t LEAST>
 cudaError_t forward_registers(const LnForward& a, uint32_t group, cudaStream_t s) {
-  const uint64_t per_cta = group == 32 ? kLnWarpThreads / 32 : 1, ctas = (a.rows + per_cta - 1) / per_cta;
   return with_second<LEAST, E * kLnMaxThreads>(a.cols, [&](auto second) {
-    constexpr bool S = decltype(second)::value;
-    return group == 32 ? launch_programmatic(ln_forward_registers<DT, WDT, E, true, S>, dim3((unsigned)ctas), kLnWarpThreads, 0, s, a)
-                       : launch_programmatic(ln_forward_registers<DT, WDT, E, false, S>, dim3((unsigned)ctas), group, 0, s, a);
+    return launch_programmatic(ln_forward_registers<DT, WDT, E, false, decltype(second)::value>, dim3((unsigned)a.rows), group, 0, s,
+                               a);
   });
 }
 // CTAs, each with a row of `reach` columns, that an SM holds at `per` columns a thread: by registers (64, 85 or 128 a
@@ -139,12 +145,12 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
   const bool aligned = a.cols % V == 0 && !phase(a.x) && !phase(a.y) && !line(a.x_stride) && !line(a.y_stride) &&
                        !phase(a.w) && !phase(a.b);
   if (aligned && a.cols <= (uint64_t)kLnMaxThreads * 64 && a.rows <= 0x7fffffffull) {  // a CTA for every row, or for 4
-    if (a.cols <= 256) return forward_registers<8, 0>(a, 32, s);
-    if (a.cols <= 512) return forward_registers<16, 0>(a, 32, s);
+    if (a.cols <= 256) return forward_warps<8>(a, s);
+    if (a.cols <= 512) return forward_warps<16>(a, s);
     // few rows leave SMs idle: more threads to a row, fewer columns each (1 x 1024: 1.6 us against 2.1, 512 x 1024: 2.4
     // against 2.8); many rows want the row's fixed cost on few threads (8192 x 4096: 24 us against 36)
-    if (a.rows <= 608 && a.cols <= 4096) return forward_registers<8, 0>(a, group_for(a.cols, 8), s);
-    if (a.cols <= 16384) return forward_registers<32, 0>(a, group_for(a.cols, 32), s);
+    if (a.rows <= 608 && a.cols <= 4096) return forward_registers<8, 513>(a, group_for(a.cols, 8), s);
+    if (a.cols <= 16384) return forward_registers<32, 513>(a, group_for(a.cols, 32), s);
     return forward_registers<64, 16385>(a, group_for(a.cols, 64), s);
   }
   // x and y in step: every row of both at the same place in its 16-byte line
@@ -200,14 +206,14 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
       if (groups == 0 || weights + 2 * groups * row > kLnSmem) return 0.0;
       return groups * group * (per == 16 ? 1.0 : per == 24 ? 0.8 : 0.5);
     };
-    const double s16 = score(16), s24 = score(24), s32 = score(32);
+    const double s16 = score(16), s24 = score(24), s32 = es == 2 ? score(32) : 0.0;  // of 4 bytes it is never the best
     const uint32_t per = reach <= 256 ? 8 : s16 >= s24 && s16 >= s32 ? 16 : s24 >= s32 ? 24 : 32;
     if (s16 + s24 + s32 > 0.0) {
       a.group = group_for(reach, per);
       if (per == 8) err = backward_fused<8, true>(&a, !aligned, weights, row, s);
       else if (per == 16) err = backward_fused<16, true>(&a, !aligned, weights, row, s);
-      else if (per == 24) err = backward_fused<24, false>(&a, !aligned, weights, row, s);
-      else err = backward_fused<32, false>(&a, !aligned, weights, row, s);
+      else if (es == 4 || per == 24) err = backward_fused<24, false>(&a, !aligned, weights, row, s);
+      else if constexpr (es == 2) err = backward_fused<32, false>(&a, !aligned, weights, row, s);
       return err != cudaSuccess ? err : finish();
     }
   }

@@ -51,7 +51,7 @@ def check_backward(ra, dy, x, w, mean, rstd, dx=None):
 
 # columns of every way through the backward pass: 8, 16, 24, 32 a thread, on the 16-byte grid and off it, rows
 # shared by 2 and 4 CTAs, and rows of any length
-COLUMNS = [200, 203, 1024, 1537, 5120, 6001, 14000, 14001, 20000, 17001, 32768, 40000]
+COLUMNS = [200, 203, 1024, 1537, 5120, 6001, 14000, 14001, 20000, 17001, 32768, 40000, 50001]
 
 
 @pytest.mark.gpu

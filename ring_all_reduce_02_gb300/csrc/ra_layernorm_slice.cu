@@ -150,7 +150,8 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
     // few rows leave SMs idle: more threads to a row, fewer columns each (1 x 1024: 1.6 us against 2.1, 512 x 1024: 2.4
     // against 2.8); many rows want the row's fixed cost on few threads (8192 x 4096: 24 us against 36)
     if (a.rows <= 608 && a.cols <= 4096) return forward_registers<8, 513>(a, group_for(a.cols, 8), s);
-    if (a.cols <= 16384) return forward_registers<32, 513>(a, group_for(a.cols, 32), s);
+    if (a.cols <= 1024) return forward_warps<32>(a, s);
+    if (a.cols <= 16384) return forward_registers<32, 1025>(a, group_for(a.cols, 32), s);
     return forward_registers<64, 16385>(a, group_for(a.cols, 64), s);
   }
   // x and y in step: every row of both at the same place in its 16-byte line

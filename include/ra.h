@@ -472,7 +472,9 @@ typedef struct {
  *
  * Written buffers must not overlap each other or a gradient (RA_ERR_ALIAS);
  * gradients may overlap each other. RA_ERR_INVALID_ARG: step < 1, betas
- * outside [0, 1), eps or lr or weight_decay negative or not finite.
+ * outside [0, 1), eps or lr or weight_decay negative or not finite, eps
+ * positive but below 2^-126 (with eps 0 an element that never had a gradient
+ * becomes 0/0 = NaN).
  * RA_ERR_UNSUPPORTED: no host memory for the check of a long list. Lists of
  * more than 384 tensors go out as several launches.
  * HBM traffic per element: param and moments read and written, grad read.

@@ -143,6 +143,8 @@ extern "C" ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, 
   if (st != RA_SUCCESS) return st;
   if (o.state != RA_STATE_F32 && o.state != RA_STATE_E4M3) return RA_ERR_INVALID_ARG;
   if (o.step < 1 || !unit(o.beta1) || !unit(o.beta2) || !sound(o.lr) || !sound(o.eps)) return RA_ERR_INVALID_ARG;
+  // the kernel's reciprocal of a denormal is infinite, and an element without a gradient would become 0 * infinity
+  if (o.eps > 0.0 && o.eps < 0x1p-126) return RA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(o.grad_scale) % 4) return RA_ERR_INVALID_ARG;
   Sizes z{(uint64_t)ra::float_size(param_dtype), (uint64_t)ra::float_size(grad_dtype), 4, 0, o.state == RA_STATE_E4M3};
   if (z.s8) z.moment = 1;

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_adamw import BF16, BLOCK, F8, F16, F32, HYPER, Case, gpu, random_bits
+from test_adamw import BF16, BLOCK, F8, F16, F32, HYPER, Case, gpu, random_bits, refuse
 
 f32 = np.float32
 
@@ -125,3 +125,22 @@ def test_gradients_may_overlap_each_other(ra, eight):
     for name in ("p", "m", "v", "ms", "vs"):
         for x, y in zip(getattr(shared, name) or [], getattr(apart, name) or []):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30])
+def test_the_smallest_eps_leaves_elements_without_a_gradient(ra, eight, eps):
+    gpu()
+    c = Case([3000, 100], F32, F32, eight, seed=1, zeros=True)
+    for t in c.g + c.m + c.v + (c.ms or []) + (c.vs or []):
+        t.view(torch.uint8).zero_()
+    c.p[0].fill_(3.0), c.p[1].fill_(-2.0)
+    c.wd = [0.0, 0.0]
+    ra.ra_adamw(c.table(ra), step=1, **{**HYPER, "eps": eps})
+    assert (c.p[0] == 3.0).all() and (c.p[1] == -2.0).all()
+
+
+def test_an_eps_whose_reciprocal_is_infinite_is_refused(ra):
+    for eps in (2.0 ** -127, 1e-40, 1e-60, 5e-324):
+        assert refuse(ra, options={"eps": eps}) == ra.RA_ERR_INVALID_ARG

@@ -231,3 +231,33 @@ def test_every_row_and_stride(ra, dtype, rows, cols, pads, shift):
     dx = strided(rows, cols, dtype, pads[1], shift)
     check_backward(ra, dy, x, w, mean, rstd, dx)
     assert_gaps_untouched(dx)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(40, 6001), (700, 1537), (40, 20000), (40, 17001), (5, 60000)])
+def test_in_a_graph(ra, rows, cols):
+    # kernels with raised shared-memory limits, clusters, and several launches
+    gpu()
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x, dy = (torch.randn(rows, cols, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    w = torch.randn(cols, generator=gen, device="cuda")
+    ws = torch.empty(ra.ra_layernorm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return [torch.zeros_like(x), torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda"), torch.zeros_like(x),
+                torch.zeros_like(w), torch.zeros_like(w)]
+
+    def both(o):
+        ra.ra_layernorm_forward(x, w, w, o[0], o[1], o[2])
+        ra.ra_layernorm_backward(dy, x, w, o[1], o[2], o[3], o[4], o[5], workspace=ws)
+
+    want, got = outputs(), outputs()
+    both(want)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        both(got)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

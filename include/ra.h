@@ -354,7 +354,8 @@ ra_status_t ra_allreduce_bulk_noalloc(const void* const* sendbufs, void* const* 
  * default stream) as programmatic dependent launches and can be captured in a
  * graph. Buffers are device memory; scratch comes from the caller. dtypes: RA_FLOAT32, RA_FLOAT16,
  * RA_BFLOAT16 (RA_INT32: RA_ERR_UNSUPPORTED). All arithmetic is fp32, rounded
- * to nearest even once where a result is stored. Results do not depend on
+ * to nearest even once where a result is stored; quotients and square roots
+ * inside a formula may be off by a few ulp of fp32. Results do not depend on
  * timing: no sum is taken in an order that varies from run to run on a device.
  * Pointers must be aligned to their element size; wider alignment is faster.
  */
@@ -404,8 +405,9 @@ size_t ra_layernorm_workspace(size_t rows, size_t cols);
  *   out[1] = scale = prescale * min(1, max_norm / (norm + 1e-6)),
  * or NaN in out[1] if the norm is not finite, which makes ra_adamw leave
  * everything as it is. prescale undoes a loss scale (1 otherwise); max_norm
- * may be infinity (no clipping). Squares and sums are fp32 (a |prescale * g|
- * above 1.8e19 overflows to an infinite norm). out: 2 device floats.
+ * may be infinity (no clipping). Squares and sums are fp32: a norm above
+ * 1.8e19 may come out infinite, and a |prescale * g| below 1e-19 loses digits
+ * or counts as 0. out: 2 device floats.
  * workspace: ra_grad_norm_workspace() bytes of device memory, 16-byte aligned,
  * set to zero before its first use; every call leaves it ready for the next.
  * Two calls that may run at once need one each. Tensors of count 0 may be
@@ -451,7 +453,8 @@ typedef struct {
 } ra_adamw_options_t;
 
 /*
- * One AdamW step over `ntensors` tensors. Per element, every operation fp32:
+ * One AdamW step over `ntensors` tensors. Per element, every operation fp32
+ * (the moments' products and sums rounded one by one):
  *   g = grad * grad_scale
  *   m = beta1 * m + (1 - beta1) * g,   v = beta2 * v + (1 - beta2) * g * g
  *   param = param * (1 - lr * weight_decay)
@@ -466,8 +469,8 @@ typedef struct {
  * leave its 8-bit value. The random bits are a hash of (seed, step, place of
  * the tensor in the list, place of the element in the tensor), 16 for each
  * moment, so a step can be repeated exactly. Below e4m3's normal range (2^-15
- * of the block's amax) rounding is to nearest, and a v that is not zero is not
- * stored as zero. A NaN or infinity in a block's moments makes the whole block
+ * of the block's amax) the value so rounded is rounded once more, to nearest,
+ * and a v that is not zero is not stored as zero. A NaN or infinity in a block's moments makes the whole block
  * NaN (nearest what fp32 moments would do; grad_scale avoids it).
  *
  * Written buffers must not overlap each other or a gradient (RA_ERR_ALIAS);

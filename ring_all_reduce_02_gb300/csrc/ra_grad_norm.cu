@@ -20,8 +20,9 @@ namespace ra {
 
 constexpr int kNormThreads = 256;
 // 456 CTAs (3 on each of 152 SMs) of 256 threads with four 32-byte vectors in flight each. Measured, 354.8 M fp32
-// gradients / one layer's 12.6 M bf16 (back to back): 200 us (7.1 TB/s, 105% of the copy bandwidth) / 7.9 us; two
-// vectors 265 / 8.9, one 445 / 11.7; 1216 CTAs 198 / 11.4 (the last CTA waits for more tickets), 304 CTAs 213 / 7.8.
+// gradients / one layer's 12.6 M bf16 (back to back): 199 us (7.1 TB/s, 105% of the copy bandwidth) / 6.9 us.
+// When they were chosen, at 200 / 7.9: two vectors 265 / 8.9, one 445 / 11.7; 1216 CTAs 198 / 11.4 (the last CTA waits
+// for more tickets), 304 CTAs 213 / 7.8.
 constexpr int kNormUnroll = 4;
 constexpr int kNormCtas = 456;
 constexpr int kNormSmall = 32;  // tensors in the small and the large table: kernel parameters hold 32,764 bytes

@@ -121,7 +121,7 @@ __device__ __forceinline__ float weight_at(const void* base, uint32_t i) {
 }
 // Where element i of a row's lines has its weight in shared memory: four of a line's values stand together, a
 // line's second four `half` floats on, so that a warp's 16-byte reads touch every bank equally often (a thread's
-// eight in a row cost two passes: 6001 x 4095 fp16 30.5 us, not 26.9; backward, 4096 x 12288 bf16 71 us, not 66).
+// eight in a row cost two passes: 13% of 6001 x 4095 fp16; backward, 8% of 4096 x 12288 bf16).
 template <uint32_t V>
 __device__ __forceinline__ uint32_t weight_slot(uint32_t i, uint32_t half) {
   return V == 4 ? i : (i & 4 ? half : 0) + i / 8 * 4 + (i & 3);
@@ -195,10 +195,11 @@ __device__ __forceinline__ float mean_rest(float rest) { return fabsf(rest) < IN
 // barriers for several groups would hold 16 of an SM's 64 barriers per CTA and
 // so allow only 4 CTAs on it).
 //
-// Measured (back to back, inputs larger than L2): 8192 x 1024 bf16 7.8 us (floor
-// 4.9), 8192 x 4096 bf16 23.3 us (85% of the copy bandwidth), 4096 x 8192 fp32
-// 41.6 us (95%), 32768 x 8192 bf16 171 us (92%). About 16 instructions an element
-// at 16-bit types, and a launch's 2 us where rows are few, keep it off the floor.
+// Measured (back to back, inputs larger than L2): 8192 x 1024 bf16 7.1 us (floor
+// 4.9), 8192 x 4096 bf16 23.7 us (83% of the copy bandwidth), 4096 x 8192 fp32
+// 41.9 us (94%), 32768 x 8192 bf16 173 us (91%). Short launches spend 2 us on their
+// start; at 8192 x 1024 the warps wait for their rows (long_scoreboard) at 52% of
+// the issue slots, 16 instructions an element.
 template <int DT, int WDT, int E, bool WARP, bool SECOND>
 __global__ void __launch_bounds__(WARP ? kLnWarpThreads : kLnMaxThreads) ln_forward_registers(const __grid_constant__ LnForward a) {
   pdl_enter();
@@ -324,8 +325,8 @@ __device__ __forceinline__ void store_part(char* at, const uint4& q, int from, i
 }
 
 // Persistent CTAs, one row at a time; the next row's lines are read while a row is worked on. The grid is a
-// multiple of 8 (or has a CTA for every row). 6001 x 4095 fp16: 23.2 us (floor 14.5; element by element 75), 2047 x
-// 1537 fp32: 7.5 us (3.7). Issue slots, 60% of them in use, and the two exchanges of a row among its warps on 24 to 32
+// multiple of 8 (or has a CTA for every row). 6001 x 4095 fp16: 22.8 us (floor 14.5; element by element 75), 2047 x
+// 1537 fp32: 8.2 us (3.7). The chain of weights from shared memory and the two or three exchanges of a row on 24 to 32
 // resident warps bound it: 2 to 8 rows ahead in shared memory instead of one in registers, or two rows to an
 // exchange, made it slower.
 template <int DT, int WDT, int E, bool SECOND>
@@ -462,14 +463,14 @@ __global__ void __launch_bounds__(E == 24 ? 384 : kLnMaxThreads, E <= 24 ? 2 : 1
 // LATE: a row too long for one CTA's registers or shared memory is shared by the
 // 2 or 4 CTAs of a cluster, each with a run of its lines; their sums meet in
 // each other's shared memory, and a row's dx waits until the next row's sums are
-// on their way. 4096 x 20000 bf16: 136 us (53% of the copy bandwidth), 4096 x
-// 16384 fp32: 139 us (85%), against 500 and 459 us in separate passes for dx and
+// on their way. 4096 x 20000 bf16: 132 us (55% of the copy bandwidth), 4096 x
+// 16384 fp32: 141 us (84%), against 500 and 459 us in separate passes for dx and
 // the column sums; without the delay 233 and 171.
 //
 // Measured (back to back, inputs larger than L2, of the copy bandwidth's floor):
-// 8192 x 1024 bf16 15.8 us (7.4), of which about 3 are the first rows' way, 9 the
+// 8192 x 1024 bf16 15.7 us (7.4), of which about 3 are the first rows' way, 9 the
 // loop at 80% of the copy bandwidth, 1 the fold and 2 ln_backward_finish; 32768 x
-// 8192 bf16 286 us (237); 2047 x 1537 fp32 15.3 us (5.6); 6001 x 4095 fp16 58 us
+// 8192 bf16 286 us (237); 2047 x 1537 fp32 14.3 us (5.6); 6001 x 4095 fp16 59 us
 // (21.7). In the loop 16 warps (accumulators and the row's values fill the
 // registers) keep 40 to 45% of the issue slots busy: the chain from the row's
 // sums through the exchange to dx bounds it as much as HBM does.

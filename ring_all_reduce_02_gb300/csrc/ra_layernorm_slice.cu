@@ -174,7 +174,7 @@ cudaError_t RA_CAT3(ln_forward, RA_SLICE_DT, RA_SLICE_W)(const LnForward& a, cud
                      : forward_shifted<16, 0>(a, group_for(reach, 16), smem, s);
       }
       if (reach <= 16384) return forward_shifted<32, 9217 - V>(a, group_for(reach, 32), smem, s);
-      // 64 columns a thread spill; at 4 bytes a column the general kernel is faster (3000 x 23001 fp32: 230 us, not 405)
+      // 64 columns a thread spill; at 4 bytes a column the general kernel is faster (3000 x 23001 fp32, one mean: 230 us, not 405)
       if constexpr (es == 2) return forward_shifted<64, 16385 - V>(a, group_for(reach, 64), smem, s);
     }
   }
@@ -200,8 +200,8 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
     const size_t weights = elems * 4, row = 2 * elems * es;
     // 16 columns a thread keep xhat and dy w in registers; 24 and 32 take them from shared memory again and are
     // worth about 0.8 and 0.5 of a thread of 16, but win where they put more of the CTA's 512 threads to work (a
-    // group is whole warps): 4096 x 5120 fp32 48 us with 24 against 53 with 16, 4096 x 6001 bf16 51 against 56,
-    // 6001 x 4095 fp16 58 against 67 (72 with 32), 8192 x 4096 bf16 45 with 16
+    // group is whole warps): 4096 x 5120 fp32 and 4096 x 6001 bf16 take 9% less with 24 than with 16,
+    // 6001 x 4095 fp16 13% (19% less than with 32)
     const auto score = [&](uint32_t per) {
       const uint32_t group = group_for(reach, per), groups = group ? kLnMaxThreads / group : 0;
       if (groups == 0 || weights + 2 * groups * row > kLnSmem) return 0.0;
@@ -218,8 +218,8 @@ cudaError_t RA_CAT3(ln_backward, RA_SLICE_DT, RA_SLICE_W)(LnBackward a, cudaStre
       return err != cudaSuccess ? err : finish();
     }
   }
-  // else a row shared by the fewest CTAs that hold it (where one CTA does, sharing is slower: 4096 x 12288 bf16 107 us
-  // against 70, 4096 x 10000 fp32 111 against 85)
+  // else a row shared by the fewest CTAs that hold it (where one CTA does, sharing takes longer: half as long again
+  // at 4096 x 12288 bf16, 30% at 4096 x 10000 fp32)
   for (uint32_t split = 2; a.rows > 0 && in_step && split <= kLnMaxSplit; split *= 2) {
     if (a.cols > (uint64_t)kLnMaxThreads * 24 * split) continue;
     const uint32_t share = ln_share_elems((uint32_t)a.cols, es, !aligned, split), per = share <= kLnMaxThreads * 16 ? 16 : 24;

@@ -485,6 +485,106 @@ typedef struct {
 ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, ra_dtype_t param_dtype, ra_dtype_t grad_dtype,
                      const ra_adamw_options_t* options, void* stream);
 
+/* ==== the two ends of a language model ========================================
+ *
+ * The embedding lookup and the loss, with their gradients: they share the
+ * vocabulary's table, the largest tensor of the gradient buffer (with tied
+ * weights ra_cross_entropy_backward writes its gradient there and
+ * ra_embedding_backward adds the lookup's). Common rules as above.
+ * tokens and targets: `rows` integers of index_size bytes (4: int32, 8:
+ * int64), aligned to that. rows and vocab are at most 2^31 - 1024. Matrices
+ * have a stride in elements (>= cols) from row to row and may start anywhere;
+ * column slices of one matrix do not overlap. Two calls that may run at once
+ * need a workspace each; its contents are irrelevant before and after.
+ */
+
+/*
+ * Embedding lookup: out[t] = scale * table[tokens[t]], with accumulate != 0
+ * out[t] = out[t] + scale * table[tokens[t]] (position embeddings on top of
+ * token embeddings, for one). fp32, rounded once. A token outside [0, vocab)
+ * makes its row NaN. out must not overlap the table or the tokens.
+ * HBM traffic: reads the distinct rows, writes rows*cols*e.
+ */
+ra_status_t ra_embedding_forward(const void* table, size_t table_stride, const void* tokens, size_t index_size,
+                                 void* out, size_t out_stride, int accumulate, size_t rows, size_t cols, size_t vocab,
+                                 double scale, ra_dtype_t dtype, void* stream);
+
+/*
+ * Its gradient: dtable[v] = scale * sum over the t with tokens[t] == v of dy[t]
+ * for every v in [0, vocab) (zero where there is none), with accumulate != 0
+ * added to what dtable holds (rows without a token are then not touched).
+ * Sums are fp32 in an order that depends on the tokens alone, rounded once.
+ * Tokens equal to `padding` and tokens outside [0, vocab) contribute nothing
+ * (a padding outside [0, vocab), such as -1, is none). dy: dtype; dtable:
+ * table_dtype (dtype itself or RA_FLOAT32). workspace:
+ * ra_embedding_workspace(rows, cols, vocab) bytes, 16-byte aligned.
+ * HBM traffic: reads rows*cols*e, writes vocab*cols*e (accumulate: reads and
+ * writes the distinct rows).
+ */
+ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* tokens, size_t index_size,
+                                  int64_t padding, void* dtable, size_t dtable_stride, int accumulate, size_t rows,
+                                  size_t cols, size_t vocab, double scale, ra_dtype_t dtype, ra_dtype_t table_dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ra_embedding_backward needs (0: a size it does not take). Host only. */
+size_t ra_embedding_workspace(size_t rows, size_t cols, size_t vocab);
+
+/*
+ * Softmax cross entropy over the vocabulary, from the hidden states and the
+ * head's weight; the logits are not stored. With logit[t][v] = sum over the
+ * columns of hidden[t] * weight[v]:
+ *   lse[t]  = log(sum over v of exp(logit[t][v])),
+ *   loss[t] = lse[t] - logit[t][targets[t]].
+ * hidden [rows, cols] and weight [vocab, cols]: RA_FLOAT16 or RA_BFLOAT16 (the
+ * products run on the tensor cores, products exact, sums fp32; RA_FLOAT32:
+ * RA_ERR_UNSUPPORTED). loss, lse: `rows` floats; lse is kept for the backward
+ * pass. A row whose target is `ignore` has loss 0 and lse 0, costs no products,
+ * and its hidden states are not read as numbers (they may be NaN). Any other
+ * target outside [0, vocab) makes its row's loss and lse NaN. No output may overlap
+ * another buffer. cols == 0 and vocab == 0 are RA_ERR_INVALID_ARG (rows == 0
+ * enqueues nothing). workspace: as ra_cross_entropy_workspace says, 16-byte
+ * aligned.
+ * Work: 2*rows*cols*vocab operations; HBM traffic: hidden and weight.
+ */
+ra_status_t ra_cross_entropy_forward(const void* hidden, size_t hidden_stride, const void* weight,
+                                     size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                                     float* loss, float* lse, size_t rows, size_t cols, size_t vocab,
+                                     ra_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients. With g[t][v] = dloss[t] * (exp(logit[t][v] - lse[t]) -
+ * [v == targets[t]]), the logits computed again, a piece of the vocabulary at
+ * a time:
+ *   dhidden[t] = sum over v of g[t][v] * weight[v],
+ *   dweight[v] = sum over t of g[t][v] * hidden[t].
+ * g divided by the largest finite |dloss| is rounded to dtype for these
+ * products (an error of half a step of dtype relative to each g); sums are
+ * fp32, rounded once. targets, ignore, lse: as of the forward pass; rows with
+ * target `ignore` have dhidden 0 and add nothing; another target outside
+ * [0, vocab) makes dhidden's row and dweight NaN. dloss: `rows` floats (NULL:
+ * ones). dhidden: dtype; dweight: dweight_dtype (dtype itself or RA_FLOAT32), with
+ * accumulate != 0 added to what it holds. Either may be NULL. No output may
+ * overlap another buffer. rows == 0 gives a zero dweight.
+ * Work: 6*rows*cols*vocab operations.
+ */
+ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, const void* weight,
+                                      size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                                      const float* lse, const float* dloss, void* dhidden, size_t dhidden_stride,
+                                      void* dweight, size_t dweight_stride, int accumulate, size_t rows, size_t cols,
+                                      size_t vocab, ra_dtype_t dtype, ra_dtype_t dweight_dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace the two calls need for these sizes (0: sizes they do not
+ * take). backward: 0 for the forward pass, 1 for the backward pass. The weight
+ * is read in place where it starts on a 16-byte boundary and its stride is a
+ * multiple of 16 bytes; otherwise the workspace holds a copy of it, so the
+ * answer depends on weight and weight_stride (the address alone is looked at).
+ * The backward pass holds one piece of g, 256 MiB at most or 1024 columns. Host only.
+ */
+size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
+                                  ra_dtype_t dtype, int backward);
+
 #ifdef __cplusplus
 }
 #endif

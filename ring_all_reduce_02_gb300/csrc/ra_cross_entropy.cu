@@ -1,0 +1,189 @@
+// ra_cross_entropy_forward / _backward: argument checks, scratch, launches.
+#include <math.h>
+
+#include "ra_cross_entropy.cuh"
+#include "ra_cross_entropy_plan.h"
+#include "ra_host.h"
+
+namespace {
+
+using ra::Buffer;
+using ra::CeArgs;
+using ra::CePlan;
+
+constexpr uint64_t kMostRows = (1ull << 31) - 1024;
+
+unsigned at_most(uint64_t n, uint64_t most) { return (unsigned)(n < most ? n : most); }
+
+bool in_place(const void* weight, uint64_t stride) {
+  return reinterpret_cast<uintptr_t>(weight) % 16 == 0 && stride * 2 % 16 == 0;
+}
+
+bool sizes_ok(uint64_t rows, uint64_t cols, uint64_t vocab) {
+  return rows <= kMostRows && vocab <= kMostRows && cols <= kMostRows && ra::shape_ok(rows, cols) && ra::shape_ok(vocab, cols);
+}
+
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t s, A... args) {
+  return ra::launch_programmatic(kernel, grid, threads, 0, s, args...);
+}
+
+// The rows that count, and the operands in the form that the products take.
+template <bool BACKWARD>
+cudaError_t rows_and_operands(const CeArgs& a, cudaStream_t s) {
+  cudaError_t err = launch(ra::ce_rows_kernel<BACKWARD>, dim3(1), ra::kCeRowsThreads, s, a);
+  if (err == cudaSuccess) err = launch(ra::ce_hidden_kernel, dim3(at_most(a.rows_pad, 152 * 8)), 256, s, a);
+  if (err == cudaSuccess && a.w != a.weight) err = launch(ra::ce_weight_kernel, dim3(at_most(a.vocab, 152 * 8)), 256, s, a);
+  return err;
+}
+
+template <int DT>
+cudaError_t forward(const CeArgs& a, cudaStream_t s) {
+  cudaError_t err = rows_and_operands<false>(a, s);
+  if (err == cudaSuccess)
+    err = launch(ra::ce_logits_kernel<DT>, dim3((unsigned)a.slots, (unsigned)((a.rows + 63) / 64)), 256, s, a);
+  if (err == cudaSuccess) err = launch(ra::ce_join_kernel, dim3((unsigned)((a.rows + 7) / 8)), 256, s, a);
+  return err;
+}
+
+template <int DT, int WDT>
+cudaError_t backward(const CeArgs& a, cudaStream_t s) {
+  cudaError_t err = rows_and_operands<true>(a, s);
+  for (uint64_t v0 = 0; v0 < a.vocab && err == cudaSuccess; v0 += a.piece) {
+    const uint64_t width = a.vocab - v0 < a.piece ? a.vocab - v0 : a.piece;
+    const unsigned across = (unsigned)((a.cols + 63) / 64);
+    err = launch(ra::ce_g_kernel<DT>, dim3((unsigned)(ra::round_up(width, 256) / 64), (unsigned)(a.rows_pad / 64)), 256, s, a, v0);
+    if (a.dhidden && err == cudaSuccess)
+      err = launch(ra::ce_dhidden_kernel<DT>, dim3(across, (unsigned)(a.rows_pad / 64)), 256, s, a, v0, width);
+    if (a.dweight && err == cudaSuccess)
+      err = launch(ra::ce_dweight_kernel<DT, WDT>, dim3(across, (unsigned)((width + 63) / 64)), 256, s, a, v0, width);
+  }
+  if (a.dhidden && a.rows && err == cudaSuccess)
+    err = launch(ra::ce_finish_kernel<DT>, dim3(at_most(a.rows, 152 * 8)), 256, s, a);
+  return err;
+}
+
+void place(CeArgs& a, const CePlan& p, void* workspace, bool packed) {
+  char* w = static_cast<char*>(workspace);
+  a.rows_pad = p.rows_pad, a.cols_pad = p.cols_pad, a.slots = p.slots, a.piece = p.piece;
+  a.head = reinterpret_cast<ra::CeHeader*>(w);
+  a.index = reinterpret_cast<int32_t*>(w + p.index);
+  a.where = reinterpret_cast<int32_t*>(w + p.where);
+  a.target = reinterpret_cast<int32_t*>(w + p.target);
+  a.h = w + p.hidden;
+  a.w = packed ? w + p.weight : a.weight;
+  a.w_stride = packed ? p.cols_pad : a.weight_stride;
+  a.lse_kept = reinterpret_cast<float*>(w + p.lse);
+  a.dloss_kept = reinterpret_cast<float*>(w + p.dloss);
+  a.g = w + p.g;
+  a.dh = reinterpret_cast<float*>(w + p.dhidden);
+  a.logit = reinterpret_cast<float*>(w + p.logit);
+  a.partial = reinterpret_cast<float2*>(w + p.partial);
+}
+
+ra_status_t check_type(int dtype) {
+  const ra_status_t st = ra::check_float(dtype);
+  return st == RA_SUCCESS && dtype == RA_FLOAT32 ? RA_ERR_UNSUPPORTED : st;
+}
+
+// RA_SUCCESS if every buffer is sound and no output overlaps another buffer.
+template <int IN, int OUT>
+ra_status_t check_buffers(Buffer (&in)[IN], Buffer (&out)[OUT], uint64_t width) {
+  for (Buffer& b : in)
+    if (!ra::sound(b)) return RA_ERR_INVALID_ARG;
+  for (Buffer& b : out)
+    if (!ra::sound(b)) return RA_ERR_INVALID_ARG;
+  for (int o = 0; o < OUT; ++o) {
+    for (const Buffer& b : in)
+      if (ra::shares(out[o], b, width)) return RA_ERR_ALIAS;
+    for (int q = 0; q < o; ++q)
+      if (ra::shares(out[o], out[q], width)) return RA_ERR_ALIAS;
+  }
+  return RA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
+                                  ra_dtype_t dtype, int backward) {
+  if (check_type(dtype) != RA_SUCCESS || !sizes_ok(rows, cols, vocab)) return 0;
+  return (size_t)ra::ce_plan(rows, cols, vocab, !in_place(weight, weight_stride), backward != 0).bytes;
+}
+
+ra_status_t ra_cross_entropy_forward(const void* hidden, size_t hidden_stride, const void* weight,
+                                     size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                                     float* loss, float* lse, size_t rows, size_t cols, size_t vocab,
+                                     ra_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  ra_status_t st = check_type(dtype);
+  if (st != RA_SUCCESS) return st;
+  if ((index_size != 4 && index_size != 8) || cols == 0 || vocab == 0 || !sizes_ok(rows, cols, vocab) ||
+      !ra::stride_ok(rows, cols, hidden_stride) || !ra::stride_ok(vocab, cols, weight_stride))
+    return RA_ERR_INVALID_ARG;
+  if (rows == 0) return RA_SUCCESS;
+  const bool packed = !in_place(weight, weight_stride);
+  const CePlan p = ra::ce_plan(rows, cols, vocab, packed, false);
+  if (workspace_bytes < p.bytes) return RA_ERR_INVALID_ARG;
+  Buffer in[3] = {{hidden, ra::extent(rows, cols, hidden_stride, 2), 2, true, {}, hidden_stride * 2},
+                  {weight, ra::extent(vocab, cols, weight_stride, 2), 2, true, {}, weight_stride * 2},
+                  {targets, rows * index_size, index_size, true, {}}};
+  Buffer out[3] = {{loss, rows * 4, 4, true, {}}, {lse, rows * 4, 4, true, {}}, {workspace, p.bytes, 16, true, {}}};
+  st = check_buffers(in, out, cols * 2);
+  if (st != RA_SUCCESS) return st;
+  CeArgs a = {};
+  a.hidden = hidden, a.weight = weight, a.hidden_stride = hidden_stride, a.weight_stride = weight_stride;
+  a.targets = {targets, (int)index_size}, a.ignore = ignore, a.rows = rows, a.cols = cols, a.vocab = vocab;
+  a.loss = loss, a.lse = lse;
+  place(a, p, workspace, packed);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return ra::launched(dtype == RA_FLOAT16 ? forward<ra::DT_F16>(a, s) : forward<ra::DT_BF16>(a, s));
+}
+
+ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, const void* weight,
+                                      size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                                      const float* lse, const float* dloss, void* dhidden, size_t dhidden_stride,
+                                      void* dweight, size_t dweight_stride, int accumulate, size_t rows, size_t cols,
+                                      size_t vocab, ra_dtype_t dtype, ra_dtype_t dweight_dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  ra_status_t st = check_type(dtype);
+  if (st == RA_SUCCESS) st = ra::check_float(dweight_dtype);
+  if (st == RA_SUCCESS && dweight_dtype != dtype && dweight_dtype != RA_FLOAT32) st = RA_ERR_UNSUPPORTED;
+  if (st != RA_SUCCESS) return st;
+  if ((index_size != 4 && index_size != 8) || cols == 0 || vocab == 0 || !sizes_ok(rows, cols, vocab) ||
+      !ra::stride_ok(rows, cols, hidden_stride) || !ra::stride_ok(vocab, cols, weight_stride) ||
+      (dhidden && !ra::stride_ok(rows, cols, dhidden_stride)) || (dweight && !ra::stride_ok(vocab, cols, dweight_stride)))
+    return RA_ERR_INVALID_ARG;
+  if ((!dhidden && !dweight) || (rows == 0 && (!dweight || accumulate))) return RA_SUCCESS;
+  const uint64_t ws = ra::float_size(dweight_dtype);
+  const bool packed = !in_place(weight, weight_stride);
+  const CePlan p = ra::ce_plan(rows, cols, vocab, packed, true);
+  if (workspace_bytes < p.bytes) return RA_ERR_INVALID_ARG;
+  const auto full = [&](size_t stride) { return rows ? ra::extent(rows, cols, stride, 2) : 0; };
+  Buffer in[5] = {{hidden, full(hidden_stride), 2, rows > 0, {}, hidden_stride * 2},
+                  {weight, ra::extent(vocab, cols, weight_stride, 2), 2, true, {}, weight_stride * 2},
+                  {targets, rows * index_size, index_size, rows > 0, {}},
+                  {lse, rows * 4, 4, rows > 0, {}},
+                  {dloss, rows * 4, 4, false, {}}};
+  Buffer out[3] = {{dhidden, full(dhidden_stride), 2, false, {}, dhidden_stride * 2},
+                   {dweight, ra::extent(vocab, cols, dweight_stride, ws), ws, false, {}, dweight_stride * ws},
+                   {workspace, p.bytes, 16, true, {}}};
+  st = check_buffers(in, out, cols * (ws > 2 ? ws : 2));
+  if (st != RA_SUCCESS) return st;
+  CeArgs a = {};
+  a.hidden = hidden, a.weight = weight, a.hidden_stride = hidden_stride, a.weight_stride = weight_stride;
+  a.targets = {targets, (int)index_size}, a.ignore = ignore, a.rows = rows, a.cols = cols, a.vocab = vocab;
+  a.lse = const_cast<float*>(lse), a.dloss = dloss;
+  a.dhidden = dhidden, a.dweight = dweight, a.dhidden_stride = dhidden_stride, a.dweight_stride = dweight_stride;
+  a.accumulate = accumulate != 0;
+  place(a, p, workspace, packed);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if (dtype == RA_FLOAT16)
+    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, s) : backward<ra::DT_F16, ra::DT_F16>(a, s);
+  else
+    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, s);
+  return ra::launched(err);
+}
+
+}  // extern "C"

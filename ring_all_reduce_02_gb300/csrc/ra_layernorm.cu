@@ -17,46 +17,13 @@ RA_DECLARE_LN(2, 2)
 
 namespace {
 
-using ra::Range;
-
+using ra::Buffer;
+using ra::extent;
+using ra::shape_ok;
+using ra::shares;
+using ra::sound;
+using ra::stride_ok;
 using ra::kLnMaxParts;
-
-// Bytes from a matrix's first element to past its last.
-uint64_t extent(uint64_t rows, uint64_t cols, uint64_t stride, uint64_t es) { return ((rows - 1) * stride + cols) * es; }
-
-// One buffer of a call.
-struct Buffer {
-  const void* p;
-  uint64_t bytes;
-  uintptr_t align;
-  bool needed;
-  Range at;
-  uint64_t stride = 0;  // of a matrix, in bytes
-};
-
-// A span of 2^57 elements at most, not null (unless it may be), aligned, inside the address space.
-bool sound(Buffer& b) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(b.p);
-  b.at = {};
-  if (lo == 0) return !b.needed;
-  if (lo % b.align || lo + b.bytes < lo) return false;
-  b.at = {lo, lo + (uintptr_t)b.bytes};
-  return true;
-}
-// Whether two buffers share a byte. Matrices of one stride whose rows (of `width` bytes) lie side by side do not, as
-// column slices of one matrix.
-bool shares(const Buffer& a, const Buffer& b, uint64_t width) {
-  if (!ra::overlaps(a.at, b.at)) return false;
-  if (a.stride == 0 || a.stride != b.stride) return true;
-  const uint64_t apart = (a.at.lo < b.at.lo ? b.at.lo - a.at.lo : a.at.lo - b.at.lo) % a.stride;
-  return apart < width || apart + width > a.stride;
-}
-bool shape_ok(uint64_t rows, uint64_t cols) {
-  return rows <= RA_MAX_COUNT && cols <= RA_MAX_COUNT && (cols == 0 || rows <= RA_MAX_COUNT / cols);
-}
-bool stride_ok(uint64_t rows, uint64_t cols, uint64_t stride) {
-  return stride >= cols && stride <= RA_MAX_COUNT && (stride == 0 || rows <= RA_MAX_COUNT / stride);
-}
 ra_status_t check_types(int dtype, int weight_dtype) {
   ra_status_t st = ra::check_float(dtype);
   if (st == RA_SUCCESS) st = ra::check_float(weight_dtype);

@@ -29,7 +29,9 @@ EXPORTS = ("ra_allreduce", "ra_reduce_scatter", "ra_allgather", "ra_allreduce_ex
            "ra_bucket_plan", "ra_allreduce_buckets", "ra_allreduce_ringsteps", "ra_chunk_range", "ra_plan_chunk",
            "ra_status_string", "ra_last_cuda_error", "ra_vector_bytes", "ra_selftest_bulk_timeout",
            "ra_allreduce_bulk_noalloc", "ra_layernorm_forward", "ra_layernorm_backward", "ra_layernorm_workspace",
-           "ra_grad_norm", "ra_grad_norm_workspace", "ra_adamw")
+           "ra_grad_norm", "ra_grad_norm_workspace", "ra_adamw", "ra_embedding_forward", "ra_embedding_backward",
+           "ra_embedding_workspace", "ra_cross_entropy_forward", "ra_cross_entropy_backward",
+           "ra_cross_entropy_workspace")
 ENGINE_CODES = {"registers": 0, "bulk": 1}
 RA_STATE_F32, RA_STATE_E4M3 = 0, 1
 RA_ADAMW_BLOCK = 256  # elements per scale of an 8-bit moment
@@ -132,6 +134,20 @@ def lib() -> ctypes.CDLL:
             L.ra_grad_norm_workspace.restype = SZ
             L.ra_adamw.argtypes = [ctypes.POINTER(AdamwTensor), I, I, I, ctypes.POINTER(AdamwOptions), VP]
             L.ra_adamw.restype = I
+            D, I64 = ctypes.c_double, ctypes.c_int64
+            L.ra_embedding_forward.argtypes = [VP, SZ, VP, SZ, VP, SZ, I, SZ, SZ, SZ, D, I, VP]
+            L.ra_embedding_forward.restype = I
+            L.ra_embedding_backward.argtypes = [VP, SZ, VP, SZ, I64, VP, SZ, I, SZ, SZ, SZ, D, I, I, VP, SZ, VP]
+            L.ra_embedding_backward.restype = I
+            L.ra_embedding_workspace.argtypes = [SZ, SZ, SZ]
+            L.ra_embedding_workspace.restype = SZ
+            L.ra_cross_entropy_forward.argtypes = [VP, SZ, VP, SZ, VP, SZ, I64, VP, VP, SZ, SZ, SZ, I, VP, SZ, VP]
+            L.ra_cross_entropy_forward.restype = I
+            L.ra_cross_entropy_backward.argtypes = [VP, SZ, VP, SZ, VP, SZ, I64, VP, VP, VP, SZ, VP, SZ, I, SZ, SZ, SZ,
+                                                    I, I, VP, SZ, VP]
+            L.ra_cross_entropy_backward.restype = I
+            L.ra_cross_entropy_workspace.argtypes = [VP, SZ, SZ, SZ, SZ, I, I]
+            L.ra_cross_entropy_workspace.restype = SZ
             _lib = L
     return _lib
 
@@ -378,6 +394,7 @@ class _Torch:
     torch, and looking names up again would cost a call more than its checks."""
 
     codes: dict = {}  # torch dtype -> ra_dtype_t
+    index_bytes: dict = {}  # torch dtype of tokens and targets -> bytes
     f32 = None
     current_stream = None  # device index -> handle of torch's current stream there
     current_device = None  # () -> index of torch's current device
@@ -389,6 +406,7 @@ class _Torch:
         cls.f32 = torch.float32
         cls.current_stream = torch._C._cuda_getCurrentRawStream
         cls.current_device = torch._C._cuda_getDevice
+        cls.index_bytes = {torch.int32: 4, torch.int64: 8}
         cls.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
         return cls
 
@@ -643,3 +661,144 @@ def ra_adamw(tensors: AdamwTensors, lr: float, step: int, beta1: float = 0.9, be
                                   ctypes.byref(opts), _stream_on(tensors.device, stream, "ra_adamw"))
     if st:
         raise RaError(st, "ra_adamw")
+
+
+# ---- embedding, cross entropy -----------------------------------------------
+
+
+def _check_matrices(what: str, device: int, cols: int, **matrices) -> None:
+    """Raises for the first of ``name=(tensor, rows, dtype)`` that is not a matrix of those rows on ``device``, with
+    contiguous rows of ``cols`` (None: there is none)."""
+    for name, (t, rows, dtype) in matrices.items():
+        if t is None:
+            continue
+        if not (t.get_device() == device and device >= 0 and len(t.shape) == 2 and tuple(t.shape) == (rows, cols)
+                and t.dtype is dtype and _rows_contiguous(t)):
+            raise ValueError(f"{what}: {name} must be a CUDA tensor [{rows}, {cols}] of {dtype} with contiguous rows, "
+                             f"on cuda:{device}")
+
+
+def _index_bytes(t, rows: int, device: int, what: str, name: str) -> int:
+    """Bytes of each of the ``rows`` tokens or targets in t."""
+    size = (_Torch.index_bytes or _Torch.load().index_bytes).get(t.dtype)
+    if size is None:
+        raise TypeError(f"{what}: {name} must be int32 or int64, not {t.dtype}")
+    if not (t.get_device() == device and t.numel() == rows and t.is_contiguous()):
+        raise ValueError(f"{what}: {name} must be a contiguous CUDA tensor of {rows} elements, on cuda:{device}")
+    return size
+
+
+def _scratch(t, device: int, what: str):
+    """(address, bytes) of a workspace."""
+    if t is None or not (t.get_device() == device and t.is_contiguous()):
+        raise ValueError(f"{what}: workspace must be a contiguous CUDA tensor, on cuda:{device}")
+    return t.data_ptr(), t.nbytes
+
+
+def _shape2(t, what: str, name: str):
+    if len(t.shape) != 2:
+        raise ValueError(f"{what}: {name} must be a CUDA tensor of two dimensions")
+    return t.shape
+
+
+def ra_embedding_forward(table, tokens, out, scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """out[t] = scale * table[tokens[t]] (added to what out holds with ``accumulate``): table [vocab, cols], tokens
+    [rows] int32 or int64, out [rows, cols] of the table's type. A token outside the vocabulary makes its row NaN."""
+    what = "ra_embedding_forward"
+    vocab, cols = _shape2(table, what, "table")
+    rows, device = tokens.numel(), table.get_device()
+    dtype = _float_code(table, what)
+    _check_matrices(what, device, cols, table=(table, vocab, table.dtype), out=(out, rows, table.dtype))
+    size = _index_bytes(tokens, rows, device, what, "tokens")
+    st = (_lib or lib()).ra_embedding_forward(
+        table.data_ptr(), _row_stride(table, cols), tokens.data_ptr(), size, out.data_ptr(), _row_stride(out, cols),
+        accumulate, rows, cols, vocab, scale, dtype, _stream_on(device, stream, what))
+    if st:
+        raise RaError(st, what)
+
+
+def ra_embedding_workspace(rows: int, cols: int, vocab: int) -> int:
+    """Bytes of workspace ra_embedding_backward needs."""
+    return lib().ra_embedding_workspace(rows, cols, vocab)
+
+
+def ra_embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool = False, padding=None,
+                          workspace=None, stream=None) -> None:
+    """dtable[v] = scale * the sum of dy[t] over the t with tokens[t] == v (added to what dtable holds with
+    ``accumulate``): dy [rows, cols], dtable [vocab, cols] of dy's type or float32. Tokens equal to ``padding`` add
+    nothing. ``workspace``: a contiguous CUDA tensor of ra_embedding_workspace(rows, cols, vocab) bytes."""
+    what = "ra_embedding_backward"
+    vocab, cols = _shape2(dtable, what, "dtable")
+    rows, device = tokens.numel(), dtable.get_device()
+    dtype, table_dtype = _float_code(dy, what), _float_code(dtable, what)
+    _check_matrices(what, device, cols, dy=(dy, rows, dy.dtype), dtable=(dtable, vocab, dtable.dtype))
+    size = _index_bytes(tokens, rows, device, what, "tokens")
+    scratch, scratch_bytes = _scratch(workspace, device, what)
+    st = (_lib or lib()).ra_embedding_backward(
+        dy.data_ptr(), _row_stride(dy, cols), tokens.data_ptr(), size, -1 if padding is None else padding,
+        dtable.data_ptr(), _row_stride(dtable, cols), accumulate, rows, cols, vocab, scale, dtype, table_dtype, scratch,
+        scratch_bytes, _stream_on(device, stream, what))
+    if st:
+        raise RaError(st, what)
+
+
+def ra_cross_entropy_workspace(hidden, weight, backward: bool = False) -> int:
+    """Bytes of workspace ra_cross_entropy_forward (or ra_cross_entropy_backward) needs for these tensors."""
+    vocab, cols = _shape2(weight, "ra_cross_entropy_workspace", "weight")
+    rows = _shape2(hidden, "ra_cross_entropy_workspace", "hidden")[0]
+    return lib().ra_cross_entropy_workspace(weight.data_ptr(), _row_stride(weight, cols), rows, cols, vocab,
+                                            _float_code(weight, "ra_cross_entropy_workspace"), backward)
+
+
+def ra_cross_entropy_forward(hidden, weight, targets, loss, lse, ignore: int = -100, workspace=None,
+                             stream=None) -> None:
+    """Softmax cross entropy of hidden [rows, cols] against the head's weight [vocab, cols] (both float16 or
+    bfloat16): loss and lse [rows] float32, 0 where the target (int32 or int64) is ``ignore``; lse is kept for the
+    backward pass. ``workspace``: a contiguous CUDA tensor of ra_cross_entropy_workspace(hidden, weight) bytes."""
+    what = "ra_cross_entropy_forward"
+    rows, cols = _shape2(hidden, what, "hidden")
+    vocab = _shape2(weight, what, "weight")[0]
+    device, dtype = hidden.get_device(), _float_code(hidden, what)
+    _check_matrices(what, device, cols, hidden=(hidden, rows, hidden.dtype), weight=(weight, vocab, hidden.dtype))
+    size = _index_bytes(targets, rows, device, what, "targets")
+    if loss is None or lse is None:
+        raise ValueError(f"{what}: loss and lse are needed")
+    f32 = _Torch.f32
+    _check_vectors(what, device, loss=(loss, rows, f32), lse=(lse, rows, f32))
+    scratch, scratch_bytes = _scratch(workspace, device, what)
+    st = (_lib or lib()).ra_cross_entropy_forward(
+        hidden.data_ptr(), _row_stride(hidden, cols), weight.data_ptr(), _row_stride(weight, cols), targets.data_ptr(),
+        size, ignore, loss.data_ptr(), lse.data_ptr(), rows, cols, vocab, dtype, scratch, scratch_bytes,
+        _stream_on(device, stream, what))
+    if st:
+        raise RaError(st, what)
+
+
+def ra_cross_entropy_backward(hidden, weight, targets, lse, dloss=None, dhidden=None, dweight=None, ignore: int = -100,
+                              accumulate: bool = False, workspace=None, stream=None) -> None:
+    """Gradients of ra_cross_entropy_forward: dhidden [rows, cols], and dweight [vocab, cols] (of the weight's type or
+    float32), added to what it holds with ``accumulate``; either may be None. lse: as the forward pass stored it.
+    dloss: [rows] float32, the gradient of each row's loss (None: ones). ``workspace``: a contiguous CUDA tensor of
+    ra_cross_entropy_workspace(hidden, weight, backward=True) bytes."""
+    what = "ra_cross_entropy_backward"
+    rows, cols = _shape2(hidden, what, "hidden")
+    vocab = _shape2(weight, what, "weight")[0]
+    device, dtype = hidden.get_device(), _float_code(hidden, what)
+    wdtype = hidden.dtype if dweight is None else dweight.dtype
+    wcode = dtype if dweight is None else _float_code(dweight, what)
+    _check_matrices(what, device, cols, hidden=(hidden, rows, hidden.dtype), weight=(weight, vocab, hidden.dtype),
+                    dhidden=(dhidden, rows, hidden.dtype), dweight=(dweight, vocab, wdtype))
+    size = _index_bytes(targets, rows, device, what, "targets")
+    if lse is None:
+        raise ValueError(f"{what}: lse is needed, as ra_cross_entropy_forward stored it")
+    f32 = _Torch.f32
+    _check_vectors(what, device, lse=(lse, rows, f32), dloss=(dloss, rows, f32))
+    scratch, scratch_bytes = _scratch(workspace, device, what)
+    st = (_lib or lib()).ra_cross_entropy_backward(
+        hidden.data_ptr(), _row_stride(hidden, cols), weight.data_ptr(), _row_stride(weight, cols), targets.data_ptr(),
+        size, ignore, lse.data_ptr(), _address(dloss), _address(dhidden),
+        cols if dhidden is None else _row_stride(dhidden, cols), _address(dweight),
+        cols if dweight is None else _row_stride(dweight, cols), accumulate, rows, cols, vocab, dtype, wcode, scratch,
+        scratch_bytes, _stream_on(device, stream, what))
+    if st:
+        raise RaError(st, what)

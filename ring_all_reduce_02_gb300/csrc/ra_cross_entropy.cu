@@ -1,4 +1,5 @@
 // ra_cross_entropy_forward / _backward: argument checks, scratch, launches.
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include "ra_cross_entropy.cuh"
@@ -16,7 +17,7 @@ constexpr uint64_t kMostRows = (1ull << 31) - 1024;
 unsigned at_most(uint64_t n, uint64_t most) { return (unsigned)(n < most ? n : most); }
 
 bool in_place(const void* weight, uint64_t stride) {
-  return reinterpret_cast<uintptr_t>(weight) % 16 == 0 && stride * 2 % 16 == 0;
+  return reinterpret_cast<uintptr_t>(weight) % 16 == 0 && stride % 8 == 0 && stride < 1ull << 38;
 }
 
 bool sizes_ok(uint64_t rows, uint64_t cols, uint64_t vocab) {
@@ -37,26 +38,62 @@ cudaError_t rows_and_operands(const CeArgs& a, cudaStream_t s) {
   return err;
 }
 
+// A tensor map of a [rows][cols] matrix of 16-bit elements, in boxes of 64 x 64 with swizzled rows.
+cudaError_t encode(CUtensorMap* map, int dtype, const void* p, uint64_t cols, uint64_t rows, uint64_t stride) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+    return err == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+  }();
+  if (fn == nullptr) return cudaErrorInitializationError;
+  const cuuint64_t size[2] = {cols, rows}, strides[1] = {stride * 2};
+  const cuuint32_t box[2] = {64, 64}, steps[2] = {1, 1};
+  const CUresult r = fn(map, dtype == RA_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                        const_cast<void*>(p), size, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t maps(ra::CeTiles& t, int dtype) {
+  const CeArgs& a = t.a;
+  cudaError_t err = encode(&t.h, dtype, a.h, a.cols_pad, a.rows_pad, a.cols_pad);
+  if (err == cudaSuccess) err = encode(&t.w, dtype, a.w, a.cols, a.vocab, a.w_stride);
+  if (err == cudaSuccess && a.g) err = encode(&t.g, dtype, a.g, a.piece, a.rows_pad, a.piece);
+  return err;
+}
+
+// Every SM has a CTA at most; all rows are taken to count.
+template <int DT, int WDT, int KIND>
+cudaError_t launch_tiles(const ra::CeTiles& t, uint64_t tiles, cudaStream_t s) {
+  const auto kernel = ra::ce_tiles_kernel<DT, WDT, KIND>;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ra::kCeSmem);
+  return err != cudaSuccess ? err : ra::launch_programmatic(kernel, dim3(2 * at_most(tiles, 76)), ra::kCeThreads, ra::kCeSmem, s, t);
+}
+
 template <int DT>
 cudaError_t forward(const CeArgs& a, cudaStream_t s) {
-  cudaError_t err = rows_and_operands<false>(a, s);
-  if (err == cudaSuccess)
-    err = launch(ra::ce_logits_kernel<DT>, dim3((unsigned)a.slots, (unsigned)((a.rows + 63) / 64)), 256, s, a);
+  ra::CeTiles t;
+  t.a = a, t.v0 = 0, t.width = a.vocab;
+  cudaError_t err = maps(t, DT);
+  if (err == cudaSuccess) err = rows_and_operands<false>(a, s);
+  if (err == cudaSuccess) err = launch_tiles<DT, DT, ra::CE_LOGITS>(t, a.rows_pad / 256 * (a.slots / 2), s);
   if (err == cudaSuccess) err = launch(ra::ce_join_kernel, dim3((unsigned)((a.rows + 7) / 8)), 256, s, a);
   return err;
 }
 
 template <int DT, int WDT>
 cudaError_t backward(const CeArgs& a, cudaStream_t s) {
-  cudaError_t err = rows_and_operands<true>(a, s);
+  ra::CeTiles t;
+  t.a = a;
+  cudaError_t err = maps(t, DT);
+  if (err == cudaSuccess) err = rows_and_operands<true>(a, s);
   for (uint64_t v0 = 0; v0 < a.vocab && err == cudaSuccess; v0 += a.piece) {
-    const uint64_t width = a.vocab - v0 < a.piece ? a.vocab - v0 : a.piece;
-    const unsigned across = (unsigned)((a.cols + 63) / 64);
-    err = launch(ra::ce_g_kernel<DT>, dim3((unsigned)(ra::round_up(width, 256) / 64), (unsigned)(a.rows_pad / 64)), 256, s, a, v0);
-    if (a.dhidden && err == cudaSuccess)
-      err = launch(ra::ce_dhidden_kernel<DT>, dim3(across, (unsigned)(a.rows_pad / 64)), 256, s, a, v0, width);
-    if (a.dweight && err == cudaSuccess)
-      err = launch(ra::ce_dweight_kernel<DT, WDT>, dim3(across, (unsigned)((width + 63) / 64)), 256, s, a, v0, width);
+    t.v0 = v0, t.width = a.vocab - v0 < a.piece ? a.vocab - v0 : a.piece;
+    const uint64_t words = (t.width + 255) / 256, rows = a.rows_pad / 256, across = (a.cols + 255) / 256;
+    err = launch_tiles<DT, DT, ra::CE_G>(t, rows * words, s);
+    if (err == cudaSuccess)
+      err = launch_tiles<DT, WDT, ra::CE_GRADIENTS>(t, ((a.dweight ? words : 0) + (a.dhidden ? rows : 0)) * across, s);
   }
   if (a.dhidden && a.rows && err == cudaSuccess)
     err = launch(ra::ce_finish_kernel<DT>, dim3(at_most(a.rows, 152 * 8)), 256, s, a);
@@ -75,7 +112,7 @@ void place(CeArgs& a, const CePlan& p, void* workspace, bool packed) {
   a.w_stride = packed ? p.cols_pad : a.weight_stride;
   a.lse_kept = reinterpret_cast<float*>(w + p.lse);
   a.dloss_kept = reinterpret_cast<float*>(w + p.dloss);
-  a.g = w + p.g;
+  a.g = p.g ? w + p.g : nullptr;
   a.dh = reinterpret_cast<float*>(w + p.dhidden);
   a.logit = reinterpret_cast<float*>(w + p.logit);
   a.partial = reinterpret_cast<float2*>(w + p.partial);

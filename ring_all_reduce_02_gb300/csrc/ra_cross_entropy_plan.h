@@ -28,7 +28,7 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
   CePlan p = {};
   p.rows_pad = round_up(rows ? rows : 1, kCeTile);
   p.cols_pad = round_up(cols, 8);
-  p.slots = (vocab + 63) / 64;
+  p.slots = (vocab + 255) / 256 * 2;
   const uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile * kCeTile;
   p.piece = most < kCeLeastPiece ? kCeLeastPiece : most;
   if (p.piece > round_up(vocab, kCeTile)) p.piece = round_up(vocab, kCeTile);

@@ -1,0 +1,121 @@
+// The instructions of a tensor-core product on sm_103a: tiles brought in by the
+// Tensor Memory Accelerator, tcgen05.mma over a pair of CTAs, accumulators in
+// tensor memory. Thin wrappers; every wait is bounded.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "ra_bulk.cuh"
+
+namespace ra {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared memory p in the pair's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+constexpr uint64_t kPairWaitNs = 10000000000ull;  // 10 s: more than any tile takes
+// As mbar_wait, for arrivals from both CTAs of a pair; gives up at once where the CTA already has (*dead).
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  uint64_t start = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*dead) return false;
+    const uint64_t now = global_ns();
+    if (start == 0) start = now;
+    if (now - start > kPairWaitNs) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+
+// A box of a two-dimensional tensor map into this CTA's shared memory; its bytes are counted by the barrier at
+// `cluster_bar`, in either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ---- tensor memory ---------------------------------------------------------------
+// One warp of each CTA of the pair; the address is written to *slot.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t address, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(address), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 columns of the warp's 32 lanes: lane l's into its x[0..31].
+__device__ __forceinline__ void tmem_load32(uint32_t address, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]),
+        "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]), "=r"(x[18]),
+        "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]),
+        "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
+      : "r"(address));
+}
+
+// ---- products ----------------------------------------------------------------------
+// Operand tiles lie in shared memory as boxes of 64 x 64 16-bit elements, rows of 128 bytes with their 16-byte lines
+// swizzled (line l of row r at l ^ (r % 8)), 8192 bytes a box. An operand whose rows run along the summed dimension
+// ("summed inner") has its boxes one below the other: 8-row groups are 1024 bytes apart. One whose rows run along its
+// own dimension ("own inner") has a box for every 64 of them: boxes are 8192 bytes apart, groups of 8 summed
+// elements 1024.
+constexpr uint32_t kBoxBytes = 8192;
+__device__ __forceinline__ uint64_t umma_descriptor(uint32_t smem_addr, bool own_inner) {
+  const uint64_t groups = 1024 >> 4, boxes = own_inner ? kBoxBytes >> 4 : 1;
+  return (uint64_t)((smem_addr & 0x3ffffu) >> 4) | boxes << 16 | groups << 32 | 1ull << 46 | 2ull << 61;
+}
+// How far 16 summed elements lie apart, in the descriptor's units of 16 bytes.
+__device__ __forceinline__ uint32_t umma_step(bool own_inner) { return own_inner ? 16 * 128 / 16 : 32 / 16; }
+// fp32 accumulators, 16-bit operands (bf16 or fp16), 256 x n.
+__device__ __forceinline__ uint32_t umma_instruction(bool bf16, bool a_own_inner, bool b_own_inner, uint32_t n) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (a_own_inner ? 1u << 15 : 0u) | (b_own_inner ? 1u << 16 : 0u) | (n >> 3) << 17 |
+         (256u >> 4) << 24;
+}
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b),
+      "r"(instruction), "r"(add ? 1u : 0u)
+      : "memory");
+}
+// Arrives at the barrier at `bar`'s place in both CTAs once every product issued so far is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+
+}  // namespace ra

@@ -580,7 +580,7 @@ ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, 
  * is read in place where it starts on a 16-byte boundary and its stride is a
  * multiple of 16 bytes; otherwise the workspace holds a copy of it, so the
  * answer depends on weight and weight_stride (the address alone is looked at).
- * The backward pass holds one piece of g, 256 MiB at most or 1024 columns. Host only.
+ * The backward pass holds two pieces of g, each 192 MiB at most or 1024 columns. Host only.
  */
 size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
                                   ra_dtype_t dtype, int backward);

@@ -32,9 +32,8 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream
 // The rows that count, and the operands in the form that the products take.
 template <bool BACKWARD>
 cudaError_t rows_and_operands(const CeArgs& a, cudaStream_t s) {
-  cudaError_t err = launch(ra::ce_rows_kernel<BACKWARD>, dim3(1), ra::kCeRowsThreads, s, a);
-  if (err == cudaSuccess) err = launch(ra::ce_hidden_kernel, dim3(at_most(a.rows_pad, 152 * 8)), 256, s, a);
-  if (err == cudaSuccess && a.w != a.weight) err = launch(ra::ce_weight_kernel, dim3(at_most(a.vocab, 152 * 8)), 256, s, a);
+  cudaError_t err = launch(ra::ce_rows_kernel<BACKWARD>, dim3((unsigned)a.parts), ra::kCeRowsThreads, s, a);
+  if (err == cudaSuccess && a.w != a.weight) err = launch(ra::ce_weight_kernel, dim3(at_most((a.vocab + 7) / 8, 152 * 8)), 256, s, a);
   return err;
 }
 
@@ -55,55 +54,62 @@ cudaError_t encode(CUtensorMap* map, int dtype, const void* p, uint64_t cols, ui
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t maps(ra::CeTiles& t, int dtype) {
-  const CeArgs& a = t.a;
-  cudaError_t err = encode(&t.h, dtype, a.h, a.cols_pad, a.rows_pad, a.cols_pad);
-  if (err == cudaSuccess) err = encode(&t.w, dtype, a.w, a.cols, a.vocab, a.w_stride);
-  if (err == cudaSuccess && a.g) err = encode(&t.g, dtype, a.g, a.piece, a.rows_pad, a.piece);
-  return err;
-}
-
 // Every SM has a CTA at most; all rows are taken to count.
-template <int DT, int WDT, int KIND>
+template <int DT, int WDT, bool BACKWARD>
 cudaError_t launch_tiles(const ra::CeTiles& t, uint64_t tiles, cudaStream_t s) {
-  const auto kernel = ra::ce_tiles_kernel<DT, WDT, KIND>;
+  const auto kernel = ra::ce_tiles_kernel<DT, WDT, BACKWARD>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ra::kCeSmem);
-  return err != cudaSuccess ? err : ra::launch_programmatic(kernel, dim3(2 * at_most(tiles, 76)), ra::kCeThreads, ra::kCeSmem, s, t);
+  return err != cudaSuccess ? err
+                            : ra::launch_programmatic(kernel, dim3(2 * at_most(tiles, ra::kCePairs)), ra::kCeThreads, ra::kCeSmem, s, t);
 }
 
 template <int DT>
 cudaError_t forward(const CeArgs& a, cudaStream_t s) {
-  ra::CeTiles t;
-  t.a = a, t.v0 = 0, t.width = a.vocab;
-  cudaError_t err = maps(t, DT);
+  ra::CeTiles t = {};
+  t.a = a, t.w_out = a.vocab, t.counter = a.counters;
+  cudaError_t err = encode(&t.h, DT, a.h, a.cols_pad, a.rows_pad, a.cols_pad);
+  if (err == cudaSuccess) err = encode(&t.w, DT, a.w, a.cols, a.vocab, a.w_stride);
   if (err == cudaSuccess) err = rows_and_operands<false>(a, s);
-  if (err == cudaSuccess) err = launch_tiles<DT, DT, ra::CE_LOGITS>(t, a.rows_pad / 256 * (a.slots / 2), s);
-  if (err == cudaSuccess) err = launch(ra::ce_join_kernel, dim3((unsigned)((a.rows + 7) / 8)), 256, s, a);
-  return err;
+  if (err == cudaSuccess) err = launch_tiles<DT, DT, false>(t, a.rows_pad / 256 * (a.slots / 2), s);
+  if (err != cudaSuccess) return err;
+  // few rows: a CTA to each
+  return a.rows <= 512 ? launch(ra::ce_join_kernel<8>, dim3((unsigned)a.rows), 256, s, a)
+                       : launch(ra::ce_join_kernel<1>, dim3((unsigned)((a.rows + 7) / 8)), 256, s, a);
 }
 
 template <int DT, int WDT>
-cudaError_t backward(const CeArgs& a, cudaStream_t s) {
-  ra::CeTiles t;
+cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream_t s) {
+  ra::CeTiles t = {};
   t.a = a;
-  cudaError_t err = maps(t, DT);
+  CUtensorMap g[2];
+  cudaError_t err = encode(&t.h, DT, a.h, a.cols_pad, a.rows_pad, a.cols_pad);
+  if (err == cudaSuccess) err = encode(&t.w, DT, a.w, a.cols, a.vocab, a.w_stride);
+  for (int i = 0; i < 2 && err == cudaSuccess; ++i) err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece);
   if (err == cudaSuccess) err = rows_and_operands<true>(a, s);
-  for (uint64_t v0 = 0; v0 < a.vocab && err == cudaSuccess; v0 += a.piece) {
-    t.v0 = v0, t.width = a.vocab - v0 < a.piece ? a.vocab - v0 : a.piece;
-    const uint64_t words = (t.width + 255) / 256, rows = a.rows_pad / 256, across = (a.cols + 255) / 256;
-    err = launch_tiles<DT, DT, ra::CE_G>(t, rows * words, s);
-    if (err == cudaSuccess)
-      err = launch_tiles<DT, WDT, ra::CE_GRADIENTS>(t, ((a.dweight ? words : 0) + (a.dhidden ? rows : 0)) * across, s);
+  const auto width = [&](uint64_t piece) { return piece >= a.pieces ? 0 : a.vocab - piece * a.piece < a.piece ? a.vocab - piece * a.piece : a.piece; };
+  for (uint64_t i = 0; i <= a.pieces && err == cudaSuccess; ++i) {  // piece i of g, and the gradients of the one before
+    t.v_out = i * a.piece, t.w_out = width(i), t.g_out = scratch + p.g[i % 2];
+    t.v_sum = i ? (i - 1) * a.piece : 0, t.w_sum = i ? width(i - 1) : 0, t.g = g[(i + 1) % 2];
+    t.counter = a.counters + i;
+    const uint64_t rows = a.rows_pad / 256, across = (a.cols + 255) / 256;
+    const uint64_t tiles = rows * ((t.w_out + 255) / 256) + (a.dhidden && t.w_sum ? rows * across * a.splits : 0) +
+                           (a.dweight ? (t.w_sum + 255) / 256 * across : 0);
+    err = launch_tiles<DT, WDT, true>(t, tiles, s);
   }
   if (a.dhidden && a.rows && err == cudaSuccess)
-    err = launch(ra::ce_finish_kernel<DT>, dim3(at_most(a.rows, 152 * 8)), 256, s, a);
+    err = launch(ra::ce_finish_kernel<DT>, dim3(at_most((a.rows * ((a.cols + 3) / 4) + 255) / 256, 152 * 64)), 256, s, a);
   return err;
 }
 
+char* first_place(void* workspace) { return reinterpret_cast<char*>(ra::round_up(reinterpret_cast<uintptr_t>(workspace), 256)); }
+
 void place(CeArgs& a, const CePlan& p, void* workspace, bool packed) {
-  char* w = static_cast<char*>(workspace);
-  a.rows_pad = p.rows_pad, a.cols_pad = p.cols_pad, a.slots = p.slots, a.piece = p.piece;
+  char* w = first_place(workspace);
+  a.rows_pad = p.rows_pad, a.cols_pad = p.cols_pad, a.part_rows = p.part_rows, a.parts = p.parts;
+  a.slots = p.slots, a.piece = p.piece, a.pieces = p.pieces, a.splits = p.splits;
   a.head = reinterpret_cast<ra::CeHeader*>(w);
+  a.counters = reinterpret_cast<uint32_t*>(w + p.counters);
+  a.tops = reinterpret_cast<float*>(w + p.tops);
   a.index = reinterpret_cast<int32_t*>(w + p.index);
   a.where = reinterpret_cast<int32_t*>(w + p.where);
   a.target = reinterpret_cast<int32_t*>(w + p.target);
@@ -112,7 +118,6 @@ void place(CeArgs& a, const CePlan& p, void* workspace, bool packed) {
   a.w_stride = packed ? p.cols_pad : a.weight_stride;
   a.lse_kept = reinterpret_cast<float*>(w + p.lse);
   a.dloss_kept = reinterpret_cast<float*>(w + p.dloss);
-  a.g = p.g ? w + p.g : nullptr;
   a.dh = reinterpret_cast<float*>(w + p.dhidden);
   a.logit = reinterpret_cast<float*>(w + p.logit);
   a.partial = reinterpret_cast<float2*>(w + p.partial);
@@ -215,11 +220,12 @@ ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, 
   a.accumulate = accumulate != 0;
   place(a, p, workspace, packed);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* const w = first_place(workspace);
   cudaError_t err;
   if (dtype == RA_FLOAT16)
-    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, s) : backward<ra::DT_F16, ra::DT_F16>(a, s);
+    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, p, w, s) : backward<ra::DT_F16, ra::DT_F16>(a, p, w, s);
   else
-    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, s);
+    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, p, w, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, p, w, s);
   return ra::launched(err);
 }
 

@@ -3,10 +3,10 @@
 //   forward    logit = h w^T, lse = log sum exp(logit), loss = lse - logit[target]
 //   backward   g = dloss (exp(logit - lse) - onehot),  dh = g w,  dw = g^T h
 //
-// Rows without a loss are left out: a first kernel numbers the others, a second copies their hidden states side by side
-// (which also makes them whole 16-byte lines), and every product runs over the rows that count alone. The logits are
-// not stored: the forward pass folds every tile of them into a partial maximum and sum per row, which a last kernel
-// joins; the backward pass computes them again, a piece of the vocabulary at a time, and stores that piece of g.
+// Rows without a loss are left out: a first kernel copies the hidden states of the others side by side (which also
+// makes them whole 16-byte lines), and every product runs over the rows that count alone. The logits are not stored:
+// the forward pass folds every tile of them into a partial maximum and sum per row, which a last kernel joins; the
+// backward pass computes them again, a piece of the vocabulary at a time, and stores that piece of g.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,12 +19,12 @@
 
 namespace ra {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct CeHeader {
-  int32_t rows;  // that count
-  int32_t failed; // a wait inside a kernel gave up: every result is NaN
-  float scale;   // the largest finite |dloss| (1 if that is 0)
+  int32_t rows;    // that count
+  int32_t failed;  // a wait inside a kernel gave up: every result is NaN
+  float scale;     // what g is held relative to (from the first launch on)
 };
 
 // Everything that the kernels need.
@@ -34,14 +34,15 @@ struct CeArgs {
   uint64_t hidden_stride, weight_stride, w_stride;
   Indices targets;
   int64_t ignore;
-  uint64_t rows, cols, vocab, rows_pad, cols_pad, slots, piece;
+  uint64_t rows, cols, vocab, rows_pad, cols_pad, part_rows, parts, slots, piece, pieces, splits;
   CeHeader* head;
-  int32_t *index, *where, *target;  // row of a counted row; counted row of a row or -1; its target or -1 (no number of the vocabulary)
+  uint32_t* counters;  // of the tiles that a launch's pairs have taken
+  float* tops;         // the first kernel's CTAs' largest finite |dloss|
+  int32_t *index, *where, *target;  // row of a counted row; counted row of a row or -1; its target or -1 (no word)
   float *lse_kept, *dloss_kept;     // backward: of the counted rows
   float* logit;                     // forward: the target's logit of a counted row
   float2* partial;                  // forward: [rows_pad][slots]
-  void* g;                          // backward: [rows_pad][piece]
-  float* dh;                        // backward: [rows_pad][cols_pad]
+  float* dh;                        // backward: [splits][rows][cols_pad]
   float *loss, *lse;                // forward: outputs; backward: lse is an input
   const float* dloss;
   void *dhidden, *dweight;
@@ -57,159 +58,208 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // ---- rows that count ---------------------------------------------------------------
 
-constexpr int kCeRowsThreads = 1024;
+constexpr int kCeRowsThreads = 256;
 
-// One CTA: numbers the rows that count in their order.
+// `cols` 16-bit elements from anywhere to a 16-byte boundary by a warp, zeros up to a whole line. A line that starts
+// off a 4-byte boundary is put together from 5 words, none of which lies wholly outside the row.
+__device__ __forceinline__ void ce_copy_row(void* to, const void* from, uint64_t cols, int lane) {
+  const uint64_t lines = (cols + 7) / 8;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(from);
+  if (p % 16 == 0 && cols % 8 == 0) {
+    for (uint64_t i = lane; i < lines; i += 32) static_cast<uint4*>(to)[i] = static_cast<const uint4*>(from)[i];
+    return;
+  }
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(p & ~(uintptr_t)3);
+  const uint32_t shift = p % 4 * 8;
+  const uint64_t reach = (p % 4 + cols * 2 + 3) / 4;  // words that hold elements of the row
+  for (uint64_t i = lane; i < lines; i += 32) {
+    uint32_t w[5], v[4];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = 4 * i + k < reach ? words[4 * i + k] : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = __funnelshift_r(w[k], w[k + 1], shift);
+      const uint64_t c = 8 * i + 2 * k;
+      if (c + 2 > cols) v[k] &= c < cols ? 0xffffu : 0u;
+    }
+    static_cast<uint4*>(to)[i] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// Numbers the rows that count in their order. Every CTA has part_rows rows and counts those before them itself.
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kCeRowsThreads) ce_rows_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
-  __shared__ int32_t sums[32];
-  __shared__ float tops[32];
+  constexpr int kWarps = kCeRowsThreads / 32;
+  __shared__ int32_t sums[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint64_t t0 = blockIdx.x * a.part_rows, t1 = t0 + a.part_rows < a.rows ? t0 + a.part_rows : a.rows;
   int32_t before = 0;
+#pragma unroll 8
+  for (uint64_t t = threadIdx.x; t < t0; t += kCeRowsThreads) before += load_index(a.targets, t) != a.ignore;
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) sums[warp] = before;
+  __syncthreads();
+  before = 0;
+  for (int i = 0; i < kWarps; ++i) before += sums[i];
   float top = 0.0f;
-  for (uint64_t t0 = 0; t0 < a.rows; t0 += kCeRowsThreads) {
-    const uint64_t t = t0 + threadIdx.x;
-    const int64_t v = t < a.rows ? load_index(a.targets, t) : a.ignore;
+  for (uint64_t u = t0; u < t1; u += 32) {  // every warp numbers all rows, and copies each eighth
+    const uint64_t t = u + lane;
+    const int64_t v = t < t1 ? load_index(a.targets, t) : a.ignore;
     const bool counts = v != a.ignore;
     const uint32_t votes = __ballot_sync(0xffffffffu, counts);
-    if (lane == 0) sums[warp] = __popc(votes);
-    __syncthreads();
-    int32_t sum = sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int32_t left = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += left;
-    }
-    const int32_t all = __shfl_sync(0xffffffffu, sum, 31);
-    const int32_t mine = before + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0) + __popc(votes & ((1u << lane) - 1));
-    if (counts) {
-      a.index[mine] = (int32_t)t;
-      a.target[mine] = v >= 0 && v < (int64_t)a.vocab ? (int32_t)v : -1;
-      if constexpr (BACKWARD) {
-        const float d = a.dloss ? a.dloss[t] : 1.0f;
-        a.lse_kept[mine] = a.lse[t];
-        a.dloss_kept[mine] = d;
-        if (fabsf(d) < __int_as_float(0x7f800000)) top = fmaxf(top, fabsf(d));
+    if (warp == 0) {
+      const int32_t mine = before + __popc(votes & ((1u << lane) - 1));
+      if (counts) {
+        a.index[mine] = (int32_t)t;
+        a.target[mine] = v >= 0 && v < (int64_t)a.vocab ? (int32_t)v : -1;
+        if constexpr (BACKWARD) {
+          const float d = a.dloss ? a.dloss[t] : 1.0f;
+          a.lse_kept[mine] = a.lse[t];
+          a.dloss_kept[mine] = d;
+          if (fabsf(d) < __int_as_float(0x7f800000)) top = fmaxf(top, fabsf(d));
+        }
+      } else if (!BACKWARD && t < t1) {
+        a.loss[t] = 0.0f;
+        a.lse[t] = 0.0f;
       }
-    } else if (!BACKWARD && t < a.rows) {
-      a.loss[t] = 0.0f;
-      a.lse[t] = 0.0f;
+      if (t < t1) a.where[t] = counts ? mine : -1;
     }
-    if (t < a.rows) a.where[t] = counts ? mine : -1;
-    before += all;
-    __syncthreads();
+    int32_t to = before;
+    for (uint32_t left = votes; left; left &= left - 1, ++to)
+      if (to % kWarps == warp)
+        ce_copy_row(static_cast<uint16_t*>(const_cast<void*>(a.h)) + (uint64_t)to * a.cols_pad,
+                    static_cast<const uint16_t*>(a.hidden) + (u + __ffs(left) - 1) * a.hidden_stride, a.cols, lane);
+    before += __popc(votes);
   }
-  if constexpr (BACKWARD) {
+  if (BACKWARD && blockIdx.x == gridDim.x - 1) {  // the products sum over whole blocks of 64 rows
+    const int32_t up = before ? (before + 63) / 64 * 64 : 64;
+    for (int32_t i = before + warp; i < up; i += kWarps)
+      for (uint64_t c = lane; c < a.cols_pad / 8; c += 32)
+        static_cast<uint4*>(const_cast<void*>(a.h))[(uint64_t)i * (a.cols_pad / 8) + c] = make_uint4(0, 0, 0, 0);
+  }
+  if (warp == 0) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    top = tops[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) {
+      a.tops[blockIdx.x] = top;
+      if (blockIdx.x == gridDim.x - 1) {
+        a.head->rows = before;
+        a.head->failed = 0;
+      }
+    }
   }
-  if (threadIdx.x == 0) {
-    a.head->rows = before;
-    a.head->failed = 0;
-    a.head->scale = top > 0.0f ? top : 1.0f;
-  }
+  if (blockIdx.x == 0)
+    for (uint64_t i = threadIdx.x; i <= a.pieces; i += kCeRowsThreads) a.counters[i] = 0;
 }
 
-// The counted rows' hidden states side by side, zeros behind them.
-__global__ void __launch_bounds__(256) ce_hidden_kernel(const __grid_constant__ CeArgs a) {
-  pdl_enter();
-  const uint64_t rows = (uint64_t)a.head->rows, up = rows ? (rows + 255) / 256 * 256 : 256;
-  for (uint64_t i = blockIdx.x; i < up; i += gridDim.x) {
-    uint16_t* to = static_cast<uint16_t*>(const_cast<void*>(a.h)) + i * a.cols_pad;
-    const uint16_t* from = i < rows ? static_cast<const uint16_t*>(a.hidden) + (uint64_t)a.index[i] * a.hidden_stride : nullptr;
-    for (uint64_t c = threadIdx.x; c < a.cols_pad; c += 256) to[c] = from && c < a.cols ? from[c] : (uint16_t)0;
-  }
-}
-
-// The weight in rows of whole 16-byte lines.
+// The weight in rows of whole 16-byte lines: a warp per row.
 __global__ void __launch_bounds__(256) ce_weight_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
-  for (uint64_t v = blockIdx.x; v < a.vocab; v += gridDim.x) {
-    uint16_t* to = static_cast<uint16_t*>(const_cast<void*>(a.w)) + v * a.w_stride;
-    const uint16_t* from = static_cast<const uint16_t*>(a.weight) + v * a.weight_stride;
-    for (uint64_t c = threadIdx.x; c < a.cols_pad; c += 256) to[c] = c < a.cols ? from[c] : (uint16_t)0;
-  }
+  for (uint64_t v = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32; v < a.vocab; v += (uint64_t)gridDim.x * 8)
+    ce_copy_row(static_cast<uint16_t*>(const_cast<void*>(a.w)) + v * a.w_stride,
+                static_cast<const uint16_t*>(a.weight) + v * a.weight_stride, a.cols, threadIdx.x & 31);
 }
+
+// g is held relative to the largest finite |dloss| (1 if that is 0), by a whole warp.
+__device__ __forceinline__ float ce_scale(const CeArgs& a) {
+  float top = 0.0f;
+  for (uint32_t i = threadIdx.x & 31; i < a.parts; i += 32) top = fmaxf(top, a.tops[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top > 0.0f ? top : 1.0f;
+}
+// fp16 holds g times 2^14, where it keeps its digits down to 2^-28 and its multiples of 2^-38.
+template <int DT>
+constexpr float kCeShift = DT == DT_F16 ? 16384.0f : 1.0f;
 
 // ---- products ------------------------------------------------------------------------
 //
 // All three products run in one kernel, 256 x 256 elements of the result to a pair of CTAs at a time: a warp brings
 // tiles of the operands in by the Tensor Memory Accelerator, a thread issues the products, and 8 warps take the results
 // out of tensor memory, which holds two tiles, so that a tile's results are worked on while the next one's products
-// run. Every pair takes each so manyth tile.
+// run. A pair's first tile is its own number's; it takes the others from a counter, the longest first.
 //   logits  rows x words, summed over the columns     both operands summed-inner
 //   dh      rows x columns, summed over the words     g summed-inner, w own-inner
 //   dw      words x columns, summed over the rows     g and h own-inner
+// A launch of the backward pass has the gradients' tiles of one piece of g and the tiles of the next piece, in
+// another buffer: the short ones fill the gaps that the long ones leave at the end.
 
-enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_GRADIENTS = 2 };
+enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_DHIDDEN = 2, CE_DWEIGHT = 3 };
 
-constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6;
+constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6, kCeRing = 4;
 constexpr uint32_t kCeStageBytes = 4 * kBoxBytes;  // 128 x 64 of the one operand, 128 x 64 of the other
-constexpr uint32_t kCeSmem = kCeStages * kCeStageBytes + 1024;
+constexpr uint32_t kCeTurn = 32 * 33 * 4;          // a warp's 32 x 32 results on their way to other lanes
+constexpr uint32_t kCeSmem = kCeStages * kCeStageBytes + kCeOutWarps * kCeTurn + 1024;
 constexpr uint32_t kCeGroup = 8;  // tiles of rows that are worked on together, so that the pairs share words and rows
 
 struct CeTiles {
-  CUtensorMap h, w, g;
+  CUtensorMap h, w, g;      // g: the piece whose gradients are summed
   CeArgs a;
-  uint64_t v0, width;  // the words of this launch
+  void* g_out;              // the piece that is computed (forward: none)
+  uint64_t v_sum, w_sum;    // first word and words of the one piece (none: 0 words)
+  uint64_t v_out, w_out;    // of the other; the forward pass's words
+  uint32_t* counter;
 };
 
 struct CeTile {
-  uint32_t m0, n0;  // first row and column
-  uint32_t n;       // columns: 256, or 128 where there are no more
-  uint32_t blocks;  // of 64 summed elements
-  bool dw;
+  int kind;
+  uint32_t m0, n0;      // first row and column
+  uint32_t n;           // columns: 256, or 128 where there are no more
+  uint32_t b0, blocks;  // first of the blocks of 64 summed elements, and how many
+  uint32_t split;       // dh: the share of the words
 };
 
-// Tiles of a launch, from the rows that count.
+// Tiles of a launch, from the rows that count: dh's and dw's, the longer ones first, then those of logits.
 struct CeWork {
-  uint32_t rows, row_tiles, col_tiles, words, tiles, dw_tiles, dw_blocks, dh_blocks;
+  uint32_t rows, row_tiles, across, dh_tiles, dw_tiles, tiles, dh_blocks, dh_share, dw_blocks, out_blocks, out_tiles;
+  bool dw_first;
 };
-template <int KIND>
 __device__ __forceinline__ CeWork ce_work(const CeTiles& t) {
   CeWork k;
   k.rows = (uint32_t)t.a.head->rows;
   const uint32_t rows = k.rows ? k.rows : 1;
-  k.words = (uint32_t)t.width;
   k.row_tiles = (rows + 255) / 256;
-  if constexpr (KIND == CE_GRADIENTS) {
-    k.col_tiles = (uint32_t)((t.a.cols + 255) / 256);
-    k.dw_blocks = (rows + 63) / 64;
-    k.dh_blocks = (k.words + 63) / 64;
-    k.dw_tiles = t.a.dweight ? (k.words + 255) / 256 * k.col_tiles : 0;
-    k.tiles = k.dw_tiles + (t.a.dhidden ? k.row_tiles * k.col_tiles : 0);
-  } else {
-    k.col_tiles = (k.words + 255) / 256;
-    k.dw_blocks = 0;
-    k.dh_blocks = (uint32_t)((t.a.cols + 63) / 64);
-    k.dw_tiles = 0;
-    k.tiles = k.row_tiles * k.col_tiles;
-  }
+  k.across = (uint32_t)((t.a.cols + 255) / 256);
+  k.dh_blocks = (uint32_t)((t.w_sum + 63) / 64);
+  k.dh_share = (k.dh_blocks + (uint32_t)t.a.splits - 1) / (uint32_t)t.a.splits;
+  k.dw_blocks = (rows + 63) / 64;
+  k.out_blocks = (uint32_t)((t.a.cols + 63) / 64);
+  k.dh_tiles = t.a.dhidden && t.w_sum ? k.row_tiles * k.across * (uint32_t)t.a.splits : 0;
+  k.dw_tiles = t.a.dweight && t.w_sum ? (uint32_t)((t.w_sum + 255) / 256) * k.across : 0;
+  k.out_tiles = (uint32_t)((t.w_out + 255) / 256);
+  k.tiles = k.dh_tiles + k.dw_tiles + k.row_tiles * k.out_tiles;
+  k.dw_first = k.dw_blocks > k.dh_share;
   return k;
 }
-template <int KIND>
+template <bool BACKWARD>
 __device__ __forceinline__ CeTile ce_tile(const CeTiles& t, const CeWork& k, uint32_t i) {
   CeTile o;
-  uint32_t m, c, across;
-  if constexpr (KIND == CE_GRADIENTS) {
-    o.dw = i < k.dw_tiles;
-    if (!o.dw) i -= k.dw_tiles;
-    m = i / k.col_tiles, c = i % k.col_tiles, across = (uint32_t)t.a.cols;
+  uint32_t m, c, across = (uint32_t)t.a.cols;
+  o.b0 = o.split = 0;
+  if (BACKWARD && i < k.dh_tiles + k.dw_tiles) {
+    const uint32_t first = k.dw_first ? k.dw_tiles : k.dh_tiles;
+    o.kind = (i < first) == k.dw_first ? CE_DWEIGHT : CE_DHIDDEN;
+    if (i >= first) i -= first;
+    m = i / k.across, c = i % k.across;
+    if (o.kind == CE_DWEIGHT) {
+      o.blocks = k.dw_blocks;
+    } else {
+      o.split = m / k.row_tiles, m %= k.row_tiles;
+      o.b0 = o.split * k.dh_share;
+      const uint32_t left = k.dh_blocks > o.b0 ? k.dh_blocks - o.b0 : 0;
+      o.blocks = left < k.dh_share ? left : k.dh_share;
+    }
   } else {
-    o.dw = false;
-    const uint32_t group = i / (kCeGroup * k.col_tiles), r = i - group * kCeGroup * k.col_tiles;
+    o.kind = BACKWARD ? CE_G : CE_LOGITS;
+    if constexpr (BACKWARD) i -= k.dh_tiles + k.dw_tiles;
+    const uint32_t group = i / (kCeGroup * k.out_tiles), r = i - group * kCeGroup * k.out_tiles;
     const uint32_t left = k.row_tiles - group * kCeGroup, high = left < kCeGroup ? left : kCeGroup;
-    m = group * kCeGroup + r % high, c = r / high, across = k.words;
+    m = group * kCeGroup + r % high, c = r / high, across = (uint32_t)t.w_out;
+    o.blocks = k.out_blocks;
   }
   o.m0 = m * 256, o.n0 = c * 256;
   o.n = across - o.n0 <= 128 ? 128 : 256;
-  o.blocks = o.dw ? k.dw_blocks : k.dh_blocks;
   return o;
 }
 
@@ -223,10 +273,6 @@ __device__ __forceinline__ float ce_load(const void* p, uint64_t i) {
   if constexpr (DT == DT_F32) return static_cast<const float*>(p)[i];
   else return widen16<DT>(static_cast<const uint16_t*>(p)[i]);
 }
-// g is held relative to the largest |dloss|, in fp16 times 2^14, where it keeps its digits down to 2^-28 and its
-// multiples of 2^-38; both are undone where g has been used.
-template <int DT>
-__device__ __forceinline__ float ce_unscale(const CeArgs& a) { return a.head->scale * (DT == DT_F16 ? 1.0f / 16384.0f : 1.0f); }
 template <int DT>
 __device__ __forceinline__ uint32_t ce_pack(float low, float high) {
   uint32_t r;
@@ -234,17 +280,28 @@ __device__ __forceinline__ uint32_t ce_pack(float low, float high) {
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
   return r;
 }
+// 32 bytes at a multiple of 32: whole sectors.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_sector(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
 
-// ---- what becomes of a tile's results: a thread has `n` columns (from `col` on) of row `m` in x ----
+// ---- what becomes of a tile's results: a thread has the 128 columns from `col` on of row `m` in x ----
 
 // The maximum and the sum of exponentials of a row's 128 logits, and the target's logit.
-template <int DT>
 __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k, uint32_t m, uint32_t col, float (&x)[128]) {
   const float low = __int_as_float(0xff800000);
-  if (col + 128 > k.words)
+  const uint32_t words = (uint32_t)t.w_out;
+  if (col + 128 > words)
 #pragma unroll
     for (int j = 0; j < 128; ++j)
-      if (col + j >= k.words) x[j] = low;
+      if (col + j >= words) x[j] = low;
   float top = low;
 #pragma unroll
   for (int j = 0; j < 128; ++j) top = fmaxf(top, x[j]);
@@ -268,92 +325,151 @@ __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k,
   }
 }
 
-// g = d (exp(logit - lse) - [target]); zero in rows and words behind the last.
+// g = d (exp(logit - lse) - [target]), d = dloss / scale; zero in words behind the last and in rows behind the counted
+// ones, as far as the products go.
 template <int DT>
-__device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, uint32_t m, uint32_t col, float (&x)[128]) {
+__device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, float scale, uint32_t m, uint32_t col, float (&x)[128]) {
   const bool counts = m < k.rows;
+  if (m >= k.dw_blocks * 64) return;
   const int32_t target = counts ? t.a.target[m] : 0;
-  float d = counts ? __fdiv_rn(t.a.dloss_kept[m], t.a.head->scale) * (DT == DT_F16 ? 16384.0f : 1.0f) : 0.0f;
+  float d = counts ? __fdiv_rn(t.a.dloss_kept[m], scale) * kCeShift<DT> : 0.0f;
   if (target < 0) d = __int_as_float(0x7fffffff);
   const float shift = counts ? -t.a.lse_kept[m] * kLog2e : 0.0f;
   const F2 slope = twice(kLog2e), both = twice(shift), dd = twice(d);
-  const uint32_t at = counts ? (uint32_t)(target - (int32_t)(t.v0 + col)) : 128u;
+  const uint32_t at = counts ? (uint32_t)(target - (int32_t)(t.v_out + col)) : 128u;
   float y = 0.0f;
   if (at < 128) {
 #pragma unroll
     for (int j = 0; j < 128; ++j) y = at == j ? x[j] : y;
     y = (exp2_approx(__fmaf_rn(y, kLog2e, shift)) - 1.0f) * d;
   }
-  uint16_t* to = static_cast<uint16_t*>(t.a.g) + (uint64_t)m * t.a.piece + col;
-  const bool ragged = col + 128 > k.words;
+  uint16_t* to = static_cast<uint16_t*>(t.g_out) + (uint64_t)m * t.a.piece + col;
+  const uint32_t words = (uint32_t)t.w_out, there = !counts || col >= words ? 0 : words - col;
 #pragma unroll
   for (int j = 0; j < 128; j += 16) {
-    VecT<8> v;
+    uint32_t w[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       float e, f;
       split(fma2(pair(x[j + 2 * q], x[j + 2 * q + 1]), slope, both), e, f);
       split(mul2(pair(exp2_approx(e), exp2_approx(f)), dd), e, f);
-      if (ragged) {
-        e = col + j + 2 * q < k.words ? e : 0.0f;
-        f = col + j + 2 * q + 1 < k.words ? f : 0.0f;
-      }
-      v.w[q] = ce_pack<DT>(e, f);
+      w[q] = ce_pack<DT>(e, f);
     }
-    *reinterpret_cast<uint4*>(to + j) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-    *reinterpret_cast<uint4*>(to + j + 8) = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+    if (there < 128) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] &= j + 2 * q + 1 < there ? 0xffffffffu : j + 2 * q < there ? 0xffffu : 0u;
+    }
+    st_sector(to + j, w);
   }
   if (at < 128) to[at] = (uint16_t)round16<DT>(y);
 }
 
-template <int DT>
-__device__ __forceinline__ void ce_out_dhidden(const CeTiles& t, const CeWork& k, uint32_t m, uint32_t col, float (&x)[128]) {
+// A share of dh, added to what the piece before left.
+__device__ __forceinline__ void ce_out_dhidden(const CeTiles& t, const CeWork& k, const CeTile& o, uint32_t m, uint32_t col,
+                                               float (&x)[128]) {
   if (m >= k.rows) return;
-  float* to = t.a.dh + (uint64_t)m * t.a.cols_pad + col;
+  float* to = t.a.dh + (o.split * t.a.rows + m) * t.a.cols_pad + col;
 #pragma unroll
-  for (int j = 0; j < 128; j += 4) {
+  for (int j = 0; j < 128; j += 8) {
     if (col + j >= t.a.cols_pad) break;
-    float4 v = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-    if (t.v0) {
-      const float4 old = *reinterpret_cast<const float4*>(to + j);
-      v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
-    }
-    *reinterpret_cast<float4*>(to + j) = v;
-  }
-}
-
-template <int DT, int WDT>
-__device__ __forceinline__ void ce_out_dweight(const CeTiles& t, const CeWork& k, uint32_t m, uint32_t col, float (&x)[128]) {
-  if (m >= k.words) return;
-  const float scale = ce_unscale<DT>(t.a);
-  const uint64_t to = (t.v0 + m) * t.a.dweight_stride + col;
+    uint32_t w[8];
+    if (t.v_sum) {
+      ld_sector(to + j, w);
 #pragma unroll
-  for (int j = 0; j < 128; ++j) {
-    if (col + j >= t.a.cols) break;
-    float v = x[j] * scale;
-    if (t.a.accumulate) v += ce_load<WDT>(t.a.dweight, to + j);
-    ce_store<WDT>(t.a.dweight, to + j, v);
+      for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(__uint_as_float(w[q]) + x[j + q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(x[j + q]);
+    }
+    st_sector(to + j, w);
   }
 }
 
-template <int DT, int WDT, int KIND>
+// dw (+)= scale * x. Rows of whole sectors are stored as the threads hold them; others are turned in shared memory, so
+// that a warp stores 32 columns of a row at a time.
+template <int DT, int WDT>
+__device__ __forceinline__ void ce_out_dweight(const CeTiles& t, float scale, uint32_t m, uint32_t col, float (&x)[128], float* turn) {
+  constexpr uint32_t es = Elem<WDT>::kSize, V = 32 / es;
+  const uint32_t cols = (uint32_t)t.a.cols, words = (uint32_t)t.w_sum, lane = threadIdx.x & 31;
+  const float f = scale / kCeShift<DT>;
+  char* const base = static_cast<char*>(t.a.dweight);
+  if ((reinterpret_cast<uintptr_t>(base) | t.a.dweight_stride * es | cols * es) % 32 == 0) {
+    if (m >= words) return;
+    char* const to = base + ((t.v_sum + m) * t.a.dweight_stride + col) * es;
+#pragma unroll
+    for (uint32_t j = 0; j < 128; j += V) {
+      if (col + j >= cols) break;
+      uint32_t w[8];
+      if (t.a.accumulate) ld_sector(to + j * es, w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if constexpr (WDT == DT_F32) {
+          const float v = x[j + q] * f;
+          w[q] = __float_as_uint(t.a.accumulate ? v + __uint_as_float(w[q]) : v);
+        } else {
+          float u = x[j + 2 * q] * f, v = x[j + 2 * q + 1] * f;
+          if (t.a.accumulate) u += widen16<WDT>(w[q] & 0xffffu), v += widen16<WDT>(w[q] >> 16);
+          w[q] = ce_pack<WDT>(u, v);
+        }
+      }
+      st_sector(to + j * es, w);
+    }
+    return;
+  }
+  const uint32_t m0 = m - lane;
+#pragma unroll
+  for (uint32_t j = 0; j < 128; j += 32) {
+    if (col + j >= cols) break;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) turn[lane * 33 + q] = x[j + q] * f;
+    __syncwarp();
+    const uint32_t c = col + j + lane;
+#pragma unroll
+    for (uint32_t r0 = 0; r0 < 32; r0 += 16) {
+      const uint64_t at = (t.v_sum + m0 + r0) * t.a.dweight_stride + c;
+      const uint32_t high = c >= cols || m0 + r0 >= words ? 0 : words - m0 - r0;
+      float old[16];
+      if (t.a.accumulate) {
+#pragma unroll
+        for (uint32_t r = 0; r < 16; ++r) old[r] = r < high ? ce_load<WDT>(base, at + r * t.a.dweight_stride) : 0.0f;
+      }
+#pragma unroll
+      for (uint32_t r = 0; r < 16; ++r) {
+        float v = turn[(r0 + r) * 33 + lane];
+        if (t.a.accumulate) v += old[r];
+        if (r < high) ce_store<WDT>(base, at + r * t.a.dweight_stride, v);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// The numbers of a pair's tiles, handed to its warps through a small ring in both CTAs.
+struct CeTurns {
+  uint64_t full[kCeRing], empty[kCeRing];
+  uint32_t tile[kCeRing];
+};
+
+template <int DT, int WDT, bool BACKWARD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_tiles_kernel(const __grid_constant__ CeTiles t) {
   extern __shared__ uint8_t dynamic[];
   __shared__ uint64_t full[kCeStages], empty[kCeStages], ready[2], taken[2];
+  __shared__ CeTurns turns;
   __shared__ uint32_t tmem_slot;
   __shared__ int dead;
   uint8_t* const stages = dynamic + (1024u - (smem_u32(dynamic) & 1023u)) % 1024u;  // the swizzle goes by the address
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31, rank = cluster_rank();
-  const bool own = KIND == CE_GRADIENTS;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCeStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ready[i], 1), mbar_init(&taken[i], 2 * kCeOutWarps);
+    // a tile's number is read by two loading threads, one that issues products, and both CTAs' warps for the results
+    for (int i = 0; i < kCeRing; ++i) mbar_init(&turns.full[i], 1), mbar_init(&turns.empty[i], 3 + 2 * kCeOutWarps);
     dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tma_prefetch_map(&t.h);
     tma_prefetch_map(&t.w);
-    if (own) tma_prefetch_map(&t.g);
+    if (BACKWARD) tma_prefetch_map(&t.g);
   }
   if (warp == 2) tmem_alloc_pair(&tmem_slot, 512);
   tmem_fence_before();
@@ -362,14 +478,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_enter();
-  const CeWork k = ce_work<KIND>(t);
-  const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
+  const CeWork k = ce_work(t);
+
+  uint32_t turn = 0;
+  // the number of the next tile; k.tiles or more: there is none
+  const auto next = [&]() -> uint32_t {
+    const uint32_t slot = turn % kCeRing;
+    if (!mbar_wait_pair(&turns.full[slot], turn / kCeRing & 1, &dead)) return 0xffffffffu;
+    return *static_cast<volatile uint32_t*>(&turns.tile[slot]);
+  };
+  const auto have_read = [&] { mbar_arrive_at(cluster_address(&turns.empty[turn++ % kCeRing], 0)); };
 
   if (warp == 0 && lane == 0) {
     // the tiles of both operands, each CTA of the pair its half; both count at the even CTA's barrier
     uint32_t s = 0, phase = 0;
-    for (uint32_t i = first; i < k.tiles && !dead; i += step) {
-      const CeTile o = ce_tile<KIND>(t, k, i);
+    while (!dead) {
+      const uint32_t i = next();
+      if (i >= k.tiles) break;
+      const CeTile o = ce_tile<BACKWARD>(t, k, i);
+      have_read();
       const uint32_t half = o.n / 2, boxes = half / 64;
       const int32_t am = (int32_t)(o.m0 + rank * 128), bn = (int32_t)(o.n0 + rank * half);
       for (uint32_t b = 0; b < o.blocks; ++b) {
@@ -377,19 +504,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
         uint8_t* const at = stages + s * kCeStageBytes;
         const uint32_t bar = cluster_address(&full[s], 0);
         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (2 + boxes) * kBoxBytes);
-        const int32_t sum = (int32_t)(b * 64);
+        const int32_t sum = (int32_t)((o.b0 + b) * 64);
         for (uint32_t q = 0; q < 2; ++q) {
           uint8_t* const to = at + q * kBoxBytes;
-          if (KIND != CE_GRADIENTS) tma_load_pair(to, &t.h, sum, am + (int32_t)q * 64, bar);
-          else if (o.dw) tma_load_pair(to, &t.g, am + (int32_t)q * 64, sum, bar);
-          else tma_load_pair(to, &t.g, sum, am + (int32_t)q * 64, bar);
+          const int32_t row = am + (int32_t)q * 64;
+          if (!BACKWARD || o.kind == CE_G) tma_load_pair(to, &t.h, sum, row, bar);
+          else if (o.kind == CE_DWEIGHT) tma_load_pair(to, &t.g, row, sum, bar);
+          else tma_load_pair(to, &t.g, sum, row, bar);
         }
         for (uint32_t q = 0; q < boxes; ++q) {
           uint8_t* const to = at + (2 + q) * kBoxBytes;
           const int32_t col = bn + (int32_t)q * 64;
-          if (KIND != CE_GRADIENTS) tma_load_pair(to, &t.w, sum, (int32_t)t.v0 + col, bar);
-          else if (o.dw) tma_load_pair(to, &t.h, col, sum, bar);
-          else tma_load_pair(to, &t.w, col, (int32_t)t.v0 + sum, bar);
+          if (!BACKWARD || o.kind == CE_G) tma_load_pair(to, &t.w, sum, (int32_t)t.v_out + col, bar);
+          else if (o.kind == CE_DWEIGHT) tma_load_pair(to, &t.h, col, sum, bar);
+          else tma_load_pair(to, &t.w, col, (int32_t)t.v_sum + sum, bar);
         }
         if (++s == kCeStages) s = 0, phase ^= 1;
       }
@@ -397,12 +525,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // the products of both CTAs
     uint32_t s = 0, phase = 0, n = 0;
-    for (uint32_t i = first; i < k.tiles && !dead; i += step, ++n) {
-      const CeTile o = ce_tile<KIND>(t, k, i);
+    for (; !dead; ++n) {
+      const uint32_t i = next();
+      if (i >= k.tiles) break;
+      const CeTile o = ce_tile<BACKWARD>(t, k, i);
+      have_read();
       const uint32_t buffer = n & 1, d = tmem + buffer * 256;
       if (!mbar_wait_pair(&taken[buffer], (n >> 1 & 1) ^ 1, &dead)) break;
       tmem_fence_after();
-      const bool a_own = o.dw, b_own = own;
+      const bool a_own = BACKWARD && o.kind == CE_DWEIGHT, b_own = BACKWARD && o.kind != CE_G;
       const uint32_t instruction = umma_instruction(DT == DT_BF16, a_own, b_own, o.n);
       const uint32_t a_step = umma_step(a_own), b_step = umma_step(b_own);
       for (uint32_t b = 0; b < o.blocks; ++b) {
@@ -417,12 +548,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       }
       umma_commit_pair(&ready[buffer]);
     }
+  } else if (warp == 3 && lane == 0 && rank == 0) {
+    // the tiles' numbers
+    const uint32_t pairs = gridDim.x / 2;
+    for (uint32_t n = 0; !dead; ++n) {
+      const uint32_t slot = n % kCeRing;
+      if (n >= kCeRing && !mbar_wait_pair(&turns.empty[slot], (n / kCeRing - 1) & 1, &dead)) break;
+      const uint32_t i = n == 0 ? blockIdx.x / 2 : pairs + atomicAdd(t.counter, 1u);
+      turns.tile[slot] = i;
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(&turns.tile[slot], 1)), "r"(i) : "memory");
+      mbar_arrive_at(cluster_address(&turns.full[slot], 0));
+      mbar_arrive_at(cluster_address(&turns.full[slot], 1));
+      if (i >= k.tiles) break;
+    }
   } else if (warp >= 4) {
     // the results: warp w has lanes 32 (w % 4) on of tensor memory, the first four warps columns 0 to 127
     const uint32_t part = (warp & 3) * 32, col = (warp - 4) / 4 * 128;
-    uint32_t n = 0;
-    for (uint32_t i = first; i < k.tiles && !dead; i += step, ++n) {
-      const CeTile o = ce_tile<KIND>(t, k, i);
+    float* const mine = reinterpret_cast<float*>(stages + kCeStages * kCeStageBytes + (warp - 4) * kCeTurn);
+    float scale = 1.0f;
+    if (BACKWARD) {
+      scale = t.w_sum ? t.a.head->scale : ce_scale(t.a);
+      if (!t.w_sum && blockIdx.x == 0 && warp == 4 && lane == 0) t.a.head->scale = scale;
+    }
+    for (uint32_t n = 0; !dead; ++n) {
+      const uint32_t i = next();
+      if (i >= k.tiles) break;
+      const CeTile o = ce_tile<BACKWARD>(t, k, i);
+      __syncwarp();
+      if (lane == 0) have_read();
+      else ++turn;
       const uint32_t buffer = n & 1;
       if (!mbar_wait_pair(&ready[buffer], n >> 1 & 1, &dead)) break;
       __syncwarp();
@@ -437,11 +591,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       __syncwarp();
       if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
       const uint32_t m = o.m0 + rank * 128 + part + lane;
-      if constexpr (KIND == CE_LOGITS) ce_out_logits<DT>(t, k, m, o.n0 + col, x);
-      else if (col < o.n) {
-        if constexpr (KIND == CE_G) ce_out_g<DT>(t, k, m, o.n0 + col, x);
-        else if (o.dw) ce_out_dweight<DT, WDT>(t, k, m, o.n0 + col, x);
-        else ce_out_dhidden<DT>(t, k, m, o.n0 + col, x);
+      if constexpr (!BACKWARD) {
+        ce_out_logits(t, k, m, o.n0 + col, x);
+      } else if (col < o.n) {
+        if (o.blocks == 0)  // a share without words
+#pragma unroll
+          for (int j = 0; j < 128; ++j) x[j] = 0.0f;
+        if (o.kind == CE_G) ce_out_g<DT>(t, k, scale, m, o.n0 + col, x);
+        else if (o.kind == CE_DHIDDEN) ce_out_dhidden(t, k, o, m, o.n0 + col, x);
+        else ce_out_dweight<DT, WDT>(t, scale, m, o.n0 + col, x, mine);
       }
     }
   }
@@ -458,46 +616,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   if (warp == 2) tmem_free_pair(tmem, 512);
 }
 
-// Joins a row's partial sums: a warp per counted row.
+// A maximum and a sum relative to it, of two.
+__device__ __forceinline__ void ce_join(float& top, float& sum, float other, float osum) {
+  const float both = fmaxf(top, other), base = both == __int_as_float(0xff800000) ? 0.0f : both;
+  sum = sum * exp2_approx((top - base) * kLog2e) + osum * exp2_approx((other - base) * kLog2e);
+  top = both;
+}
+
+// Joins the rows' partial sums: WARPS warps to a counted row.
+template <int WARPS>
 __global__ void __launch_bounds__(256) ce_join_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
-  const uint64_t i = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  if (i >= (uint64_t)a.head->rows) return;
-  const int lane = threadIdx.x & 31;
-  const float low = __int_as_float(0xff800000);
-  float top = low, sum = 0.0f;
-  for (uint64_t s = lane; s < a.slots; s += 32) {
-    const float2 p = a.partial[i * a.slots + s];
-    const float both = fmaxf(top, p.x), base = both == low ? 0.0f : both;
-    sum = sum * exp2_approx((top - base) * kLog2e) + p.y * exp2_approx((p.x - base) * kLog2e);
-    top = both;
+  __shared__ float2 joined[8];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint64_t i = (uint64_t)blockIdx.x * (8 / WARPS) + warp / WARPS;
+  const bool there = i < (uint64_t)a.head->rows;
+  float top = __int_as_float(0xff800000), sum = 0.0f;
+  if (there) {
+#pragma unroll 4
+    for (uint64_t s = threadIdx.x % (32 * WARPS); s < a.slots; s += 32 * WARPS) {
+      const float2 p = a.partial[i * a.slots + s];
+      ce_join(top, sum, p.x, p.y);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float other = __shfl_xor_sync(0xffffffffu, top, o), osum = __shfl_xor_sync(0xffffffffu, sum, o);
-    const float both = fmaxf(top, other), base = both == low ? 0.0f : both;
-    sum = sum * exp2_approx((top - base) * kLog2e) + osum * exp2_approx((other - base) * kLog2e);
-    top = both;
+    ce_join(top, sum, other, osum);
   }
-  if (lane == 0) {
-    const bool there = a.target[i] >= 0 && !a.head->failed;
+  if constexpr (WARPS > 1) {
+    if (lane == 0) joined[warp] = make_float2(top, sum);
+    __syncthreads();
+    if (warp % WARPS == 0)
+      for (int w = 1; w < WARPS; ++w) ce_join(top, sum, joined[warp + w].x, joined[warp + w].y);
+  }
+  if (there && lane == 0 && warp % WARPS == 0) {
+    const bool word = a.target[i] >= 0 && !a.head->failed;
     const float nan = __int_as_float(0x7fffffff);
-    const float lse = there ? top + logf(sum) : nan;
+    const float lse = word ? top + logf(sum) : nan;
     const uint64_t t = (uint64_t)a.index[i];
     a.lse[t] = lse;
-    a.loss[t] = there ? lse - a.logit[i] : nan;
+    a.loss[t] = word ? lse - a.logit[i] : nan;
   }
 }
 
-// dh into the rows it belongs to, zeros into those that do not count.
+// dh's shares added up, into the rows they belong to; zeros into those that do not count. A thread has four columns.
 template <int DT>
 __global__ void __launch_bounds__(256) ce_finish_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
-  const float scale = a.head->failed ? __int_as_float(0x7fffffff) : ce_unscale<DT>(a);
-  for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+  const float scale = a.head->failed ? __int_as_float(0x7fffffff) : a.head->scale / kCeShift<DT>;
+  const uint32_t across = (uint32_t)((a.cols + 3) / 4);
+  const uint64_t each = a.rows * a.cols_pad;
+  const bool whole = ((reinterpret_cast<uintptr_t>(a.dhidden) | a.dhidden_stride * 2) & 7) == 0;
+  for (uint64_t b = (uint64_t)blockIdx.x * 256 + threadIdx.x; b < a.rows * across; b += (uint64_t)gridDim.x * 256) {
+    const uint64_t t = b / across, c = b % across * 4;
     const int32_t i = a.where[t];
-    for (uint64_t c = threadIdx.x; c < a.cols; c += 256)
-      ce_store<DT>(a.dhidden, t * a.dhidden_stride + c, i < 0 ? 0.0f : a.dh[(uint64_t)i * a.cols_pad + c] * scale);
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i >= 0) {
+      const float* at = a.dh + (uint64_t)i * a.cols_pad + c;
+#pragma unroll 8
+      for (uint32_t s = 0; s < a.splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4*>(at + s * each);
+        sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+      }
+      sum = make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
+    }
+    uint16_t* const to = static_cast<uint16_t*>(a.dhidden) + t * a.dhidden_stride + c;
+    const uint2 w = make_uint2(ce_pack<DT>(sum.x, sum.y), ce_pack<DT>(sum.z, sum.w));
+    if (whole && c + 4 <= a.cols) {
+      *reinterpret_cast<uint2*>(to) = w;
+    } else {
+      to[0] = (uint16_t)w.x;
+      if (c + 1 < a.cols) to[1] = (uint16_t)(w.x >> 16);
+      if (c + 2 < a.cols) to[2] = (uint16_t)w.y;
+      if (c + 3 < a.cols) to[3] = (uint16_t)(w.y >> 16);
+    }
   }
 }
 

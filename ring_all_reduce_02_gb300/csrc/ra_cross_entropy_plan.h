@@ -5,21 +5,26 @@
 
 namespace ra {
 
-constexpr uint64_t kCeTile = 256;                  // rows and columns of the logits that a tile has
-constexpr uint64_t kCePieceBytes = 256ull << 20;   // of g, at most (but kCeLeastPiece columns)
+constexpr uint64_t kCeTile = 256;                  // rows and columns of a result that a tile has
+constexpr uint64_t kCePieceBytes = 192ull << 20;   // of g, at most (but kCeLeastPiece columns)
 constexpr uint64_t kCeLeastPiece = 1024;
+constexpr uint64_t kCePairs = 76;                  // pairs of CTAs: one on each two of the 152 SMs
+constexpr uint64_t kCeMostParts = 1216;            // CTAs of the first kernel
+constexpr uint64_t kCeMostSplits = 64;             // of the words that dh sums over
 
 inline uint64_t round_up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
-// Where the scratch's parts start, in bytes from its own start.
+// Where the scratch's parts start, in bytes from its first multiple of 256.
 struct CePlan {
   uint64_t rows_pad, cols_pad;  // hidden's copy: whole tiles of rows, rows of whole 16-byte lines
+  uint64_t part_rows, parts;    // rows of a CTA of the first kernel, and how many there are
   uint64_t slots;               // forward: partial sums per row
   uint64_t piece, pieces;       // backward: columns of a piece of g (whole tiles), and how many there are
-  uint64_t index, where, target, lse, dloss, logit;  // per row
-  uint64_t hidden, weight;                           // copies (weight: only where it is not read in place)
-  uint64_t partial;                                  // forward
-  uint64_t g, dhidden;                               // backward
+  uint64_t splits;              // backward: shares of a piece's words that dh is summed over apart
+  uint64_t counters, tops, index, where, target, lse, dloss, logit;
+  uint64_t hidden, weight;      // copies (weight: only where it is not read in place)
+  uint64_t partial;             // forward
+  uint64_t g[2], dhidden;       // backward
   uint64_t bytes;
 };
 constexpr uint64_t kCeHeader = 256;
@@ -28,17 +33,38 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
   CePlan p = {};
   p.rows_pad = round_up(rows ? rows : 1, kCeTile);
   p.cols_pad = round_up(cols, 8);
+  p.part_rows = round_up((rows + kCeMostParts - 1) / kCeMostParts, 8);
+  if (p.part_rows == 0) p.part_rows = 8;
+  p.parts = rows ? (rows + p.part_rows - 1) / p.part_rows : 1;
   p.slots = (vocab + 255) / 256 * 2;
-  const uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile * kCeTile;
-  p.piece = most < kCeLeastPiece ? kCeLeastPiece : most;
-  if (p.piece > round_up(vocab, kCeTile)) p.piece = round_up(vocab, kCeTile);
-  p.pieces = (vocab + p.piece - 1) / p.piece;
+  // pieces of about one size, so that no launch is a small one
+  uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile;
+  if (most < kCeLeastPiece / kCeTile) most = kCeLeastPiece / kCeTile;
+  const uint64_t tiles = (vocab + kCeTile - 1) / kCeTile;
+  p.pieces = (tiles + most - 1) / most;
+  if (p.pieces) {
+    const uint64_t each = (tiles + p.pieces - 1) / p.pieces;
+    p.piece = each * kCeTile;
+    p.pieces = (tiles + each - 1) / each;
+    // few rows make few tiles of dh, each a sum over all words of a piece: as many shares as keep a tile's work below
+    // half of a pair's, in blocks of 64 summed elements; storing a tile's results counts as 6 of them
+    const uint64_t across = (cols + kCeTile - 1) / kCeTile, words = p.piece / 64;
+    const uint64_t dh = p.rows_pad / kCeTile * across;
+    const uint64_t work = dh * words + (words / 4) * across * ((rows + 63) / 64 + 6) + p.rows_pad / kCeTile * (words / 4) * ((cols + 63) / 64 + 6);
+    const uint64_t most_words = work / (2 * kCePairs) + 1;
+    p.splits = (words + most_words - 1) / most_words;
+    if (p.splits > words / 8) p.splits = words / 8;  // none below 512 words
+    if (p.splits > kCeMostSplits) p.splits = kCeMostSplits;
+    if (p.splits < 1) p.splits = 1;
+  }
   uint64_t at = kCeHeader;
   const auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
     at += round_up(bytes, 256);
     return here;
   };
+  p.counters = take((p.pieces + 1) * 4);
+  p.tops = take(p.parts * 4);
   p.index = take(p.rows_pad * 4);
   p.where = take(p.rows_pad * 4);
   p.target = take(p.rows_pad * 4);
@@ -47,13 +73,14 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
   if (backward) {
     p.lse = take(p.rows_pad * 4);
     p.dloss = take(p.rows_pad * 4);
-    p.g = take(p.rows_pad * p.piece * 2);
-    p.dhidden = take(p.rows_pad * p.cols_pad * 4);
+    p.g[0] = take(p.rows_pad * p.piece * 2);
+    p.g[1] = p.pieces > 1 ? take(p.rows_pad * p.piece * 2) : p.g[0];
+    p.dhidden = take(p.splits * rows * p.cols_pad * 4);
   } else {
     p.logit = take(p.rows_pad * 4);
     p.partial = take(p.rows_pad * p.slots * 8);
   }
-  p.bytes = at;
+  p.bytes = at + 255;
   return p;
 }
 

@@ -1,92 +1,9 @@
-// ra_embedding_forward / _backward: the lookup of a token's row with scaling, and
-// the sum of the rows of dy over the places of each token.
+// ra_embedding_forward / _backward: argument checks, scratch, launch shapes.
 #include <math.h>
 
+#include "ra_embedding.cuh"
+#include "ra_embedding_plan.h"
 #include "ra_host.h"
-#include "ra_kernels.cuh"
-#include "ra_ops.cuh"
-#include "ra_tokens.cuh"
-
-namespace ra {
-
-constexpr int kEmbThreads = 256;
-
-struct EmbForward {
-  const void* table;
-  Indices tokens;
-  void* out;
-  uint64_t rows, cols, table_stride, out_stride;
-  int64_t vocab;
-  float scale;
-  int accumulate;
-};
-
-template <int DT>
-__device__ __forceinline__ float load_float(const void* p, uint64_t i) {
-  const uint32_t v = ld_elem<DT>(p, i);
-  if constexpr (DT == DT_F32) return __uint_as_float(v);
-  else return widen16<DT>(v);
-}
-template <int DT>
-__device__ __forceinline__ void store_float(void* p, uint64_t i, float f) {
-  if constexpr (DT == DT_F32) st_elem<DT>(p, i, __float_as_uint(f));
-  else st_elem<DT>(p, i, round16<DT>(f));
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kEmbThreads) embedding_forward_kernel(const __grid_constant__ EmbForward a) {
-  pdl_enter();
-  const float nan = __int_as_float(0x7fffffff);
-  for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const int64_t v = load_index(a.tokens, t);
-    const bool there = v >= 0 && v < a.vocab;
-    for (uint64_t c = threadIdx.x; c < a.cols; c += kEmbThreads) {
-      const uint64_t at = t * a.out_stride + c;
-      float x = there ? __fmul_rn(a.scale, load_float<DT>(a.table, (uint64_t)v * a.table_stride + c)) : nan;
-      if (a.accumulate) x += load_float<DT>(a.out, at);
-      store_float<DT>(a.out, at, x);
-    }
-  }
-}
-
-struct EmbBackward {
-  const void* dy;
-  Indices tokens;
-  void* dtable;
-  uint64_t rows, cols, dy_stride, table_stride;
-  int64_t vocab, padding;
-  float scale;
-  int accumulate;
-};
-
-// A CTA per row of the table walks over all tokens and adds the rows of dy whose token is its own, in their order.
-template <int DT, int WDT>
-__global__ void __launch_bounds__(kEmbThreads) embedding_backward_kernel(const __grid_constant__ EmbBackward a) {
-  pdl_enter();
-  const int64_t v = blockIdx.x;
-  for (uint64_t c0 = 0; c0 < a.cols; c0 += kEmbThreads) {
-    const uint64_t c = c0 + threadIdx.x;
-    float sum = 0.0f;
-    bool any = false;
-    if (v != a.padding) {
-      for (uint64_t t0 = 0; t0 < a.rows; t0 += 32) {
-        const uint64_t mine = t0 + (threadIdx.x & 31);
-        uint32_t hits = __ballot_sync(0xffffffffu, mine < a.rows && load_index(a.tokens, mine) == v);
-        any |= hits != 0;
-        for (; hits; hits &= hits - 1)
-          if (c < a.cols) sum += load_float<DT>(a.dy, (t0 + __ffs(hits) - 1) * a.dy_stride + c);
-      }
-    }
-    if (c < a.cols && (any || !a.accumulate)) {
-      const uint64_t at = (uint64_t)v * a.table_stride + c;
-      float x = __fmul_rn(a.scale, sum);
-      if (a.accumulate) x += load_float<WDT>(a.dtable, at);
-      store_float<WDT>(a.dtable, at, x);
-    }
-  }
-}
-
-}  // namespace ra
 
 namespace {
 
@@ -94,14 +11,60 @@ using ra::Buffer;
 
 constexpr uint64_t kMostRows = (1ull << 31) - 1024;
 
+bool lines(const void* p, uint64_t stride_bytes) { return (reinterpret_cast<uintptr_t>(p) | stride_bytes) % 16 == 0; }
+unsigned ctas(uint64_t units) { return (unsigned)((units + ra::kEmbThreads / 32 - 1) / (ra::kEmbThreads / 32)); }
+
 template <int DT>
-cudaError_t forward(const ra::EmbForward& a, cudaStream_t s) {
-  const unsigned ctas = (unsigned)(a.rows < 152 * 64 ? a.rows : 152 * 64);
-  return ra::launch_programmatic(ra::embedding_forward_kernel<DT>, dim3(ctas), ra::kEmbThreads, 0, s, a);
+cudaError_t forward(ra::EmbForward a, cudaStream_t s) {
+  constexpr uint64_t es = ra::Elem<DT>::kSize;
+  constexpr int N = 16 / es;
+  if (lines(a.table, a.table_stride * es) && lines(a.out, a.out_stride * es) && a.cols % N == 0) {
+    constexpr int U = 4;
+    a.across = (a.cols + 32 * N * U - 1) / (32 * N * U);
+    return ra::launch_programmatic(ra::embedding_forward_kernel<DT, N, U, true>, dim3(ctas(a.rows * a.across)), ra::kEmbThreads, 0, s, a);
+  }
+  a.across = (a.cols + 255) / 256;
+  return ra::launch_programmatic(ra::embedding_forward_kernel<DT, 8, 1, false>, dim3(ctas(a.rows * a.across)), ra::kEmbThreads, 0, s, a);
 }
+
+constexpr int kPerLane(int dtype) { return dtype == RA_FLOAT32 ? 4 : 8; }
+
+template <int THREADS, int ITEMS>
+cudaError_t sort_one(const ra::EmbBackward& a, unsigned zeros, cudaStream_t s) {
+  const auto kernel = ra::embedding_sort_kernel<THREADS, ITEMS>;
+  constexpr size_t smem = (size_t)THREADS * ITEMS * 4;
+  // the limit is the function's, not the call's: the same for all calls
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return err != cudaSuccess ? err : ra::launch_programmatic(kernel, dim3(1 + zeros), THREADS, smem, s, a);
+}
+
+// Sorts the tokens, and clears the table beside that.
+cudaError_t sort(ra::EmbBackward& a, const ra::EmbPlan& p, bool clear, cudaStream_t s) {
+  const unsigned zeros = clear ? 304 : 0;  // two CTAs an SM
+  if (p.one) {
+    a.zero_from = 1;
+    return a.rows <= 2048 ? sort_one<256, 8>(a, zeros, s) : a.rows <= 8192 ? sort_one<1024, 8>(a, zeros, s) : sort_one<1024, 32>(a, zeros, s);
+  }
+  cudaError_t err = cudaSuccess;
+  a.zero_from = a.tiles;
+  for (uint32_t pass = 0; pass < a.passes && err == cudaSuccess; ++pass) {
+    err = ra::launch_programmatic(ra::embedding_count_kernel, dim3(a.tiles + (pass == 0 ? zeros : 0)), ra::kEmbThreads, 0, s, a, pass);
+    if (err == cudaSuccess) err = ra::launch_programmatic(ra::embedding_scatter_kernel, dim3(a.tiles), ra::kEmbThreads, 0, s, a, pass);
+  }
+  return err;
+}
+
 template <int DT, int WDT>
-cudaError_t backward(const ra::EmbBackward& a, cudaStream_t s) {
-  return ra::launch_programmatic(ra::embedding_backward_kernel<DT, WDT>, dim3((unsigned)a.vocab), ra::kEmbThreads, 0, s, a);
+cudaError_t backward(ra::EmbBackward& a, const ra::EmbPlan& p, bool add, cudaStream_t s) {
+  constexpr int N = kPerLane(DT);
+  const cudaError_t err = sort(a, p, !add, s);
+  if (err != cudaSuccess || a.rows == 0) return err;
+  const int last = p.one ? 0 : (int)(p.passes - 1) % 2;
+  const bool vec = lines(a.dy, a.dy_stride * ra::Elem<DT>::kSize) && lines(a.dtable, a.table_stride * ra::Elem<WDT>::kSize) && a.cols % N == 0;
+  const auto kernel = vec ? add ? ra::embedding_sum_kernel<DT, WDT, N, true, true> : ra::embedding_sum_kernel<DT, WDT, N, true, false>
+                      : add ? ra::embedding_sum_kernel<DT, WDT, N, false, true>
+                            : ra::embedding_sum_kernel<DT, WDT, N, false, false>;
+  return ra::launch_programmatic(kernel, dim3(ctas((uint64_t)a.spans * a.across)), ra::kEmbThreads, 0, s, a, a.keys[last], a.places[last]);
 }
 
 }  // namespace
@@ -124,8 +87,8 @@ ra_status_t ra_embedding_forward(const void* table, size_t table_stride, const v
   Buffer o{out, ra::extent(rows, cols, out_stride, es), es, true, {}, out_stride * es};
   if (!ra::sound(t) || !ra::sound(i) || !ra::sound(o)) return RA_ERR_INVALID_ARG;
   if (ra::shares(o, t, cols * es) || ra::shares(o, i, cols * es)) return RA_ERR_ALIAS;
-  const ra::EmbForward a{table, {tokens, (int)index_size}, out, rows, cols, table_stride, out_stride, (int64_t)vocab,
-                         (float)scale, accumulate != 0};
+  const ra::EmbForward a{table, {tokens, (int)index_size}, out, rows, cols, table_stride, out_stride, 1,
+                         (int64_t)vocab, (float)scale, accumulate != 0};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return ra::launched(dtype == RA_FLOAT32   ? forward<ra::DT_F32>(a, s)
                       : dtype == RA_FLOAT16 ? forward<ra::DT_F16>(a, s)
@@ -134,7 +97,9 @@ ra_status_t ra_embedding_forward(const void* table, size_t table_stride, const v
 
 size_t ra_embedding_workspace(size_t rows, size_t cols, size_t vocab) {
   if (rows > kMostRows || vocab > kMostRows || !ra::shape_ok(rows, cols) || !ra::shape_ok(vocab, cols)) return 0;
-  return 16;
+  // of the two shapes that a call may take by its type, the larger
+  const uint64_t four = ra::emb_plan(rows, cols, vocab, 4).bytes, eight = ra::emb_plan(rows, cols, vocab, 8).bytes;
+  return (size_t)(four > eight ? four : eight);
 }
 
 ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* tokens, size_t index_size,
@@ -162,15 +127,27 @@ ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* 
   for (Buffer& o : out)
     if (ra::shares(o, in[0], width) || ra::shares(o, in[1], width)) return RA_ERR_ALIAS;
   if (ra::shares(out[0], out[1], width)) return RA_ERR_ALIAS;
-  const ra::EmbBackward a{dy, {tokens, (int)index_size}, dtable, rows, cols, dy_stride, dtable_stride, (int64_t)vocab,
-                          padding, (float)scale, accumulate != 0};
+  const ra::EmbPlan p = ra::emb_plan(rows, cols, vocab, kPerLane(dtype));
+  char* const w = static_cast<char*>(workspace);
+  const auto at = [&](uint64_t offset) { return reinterpret_cast<uint32_t*>(w + offset); };
+  ra::EmbBackward a = {};
+  a.dy = dy, a.tokens = {tokens, (int)index_size}, a.dtable = dtable, a.rows = rows, a.cols = cols;
+  a.dy_stride = dy_stride, a.table_stride = dtable_stride, a.vocab = (int64_t)vocab, a.padding = padding, a.scale = (float)scale;
+  a.bits = p.bits, a.passes = p.passes, a.tiles = (uint32_t)p.tiles, a.span = (uint32_t)p.span, a.spans = (uint32_t)p.spans;
+  a.across = (uint32_t)p.across;
+  for (int i = 0; i < 2; ++i) a.keys[i] = at(p.keys[i]), a.places[i] = at(p.places[i]);
+  a.counts = at(p.counts), a.tickets = at(p.tickets), a.partial = reinterpret_cast<float*>(w + p.partial);
+  // Looking up whether a row has a token costs every clearing CTA a walk over the tokens, about 1 us for 8192 of them;
+  // writing the rows with a token twice costs their bytes. So it is looked up for rows of 2 KiB and more.
+  a.zero_bytes = (int)ws, a.zero_known = cols * ws >= 2048;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool add = accumulate != 0;
   cudaError_t err;
-  if (dtype == RA_FLOAT32) err = backward<ra::DT_F32, ra::DT_F32>(a, s);
+  if (dtype == RA_FLOAT32) err = backward<ra::DT_F32, ra::DT_F32>(a, p, add, s);
   else if (dtype == RA_FLOAT16)
-    err = table_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, s) : backward<ra::DT_F16, ra::DT_F16>(a, s);
+    err = table_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, p, add, s) : backward<ra::DT_F16, ra::DT_F16>(a, p, add, s);
   else
-    err = table_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, s);
+    err = table_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, p, add, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, p, add, s);
   return ra::launched(err);
 }
 

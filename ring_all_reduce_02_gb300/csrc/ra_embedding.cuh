@@ -1,0 +1,520 @@
+// The embedding lookup with scaling, and its gradient: the sum of the rows of dy over the places of each token.
+//
+// The gradient's sums go by sorted tokens. A stable radix sort gives the places of every token side by side, in their
+// order; warps add up spans of sorted places, each a slice of the columns, and write a token's row where its places end
+// inside the span. Places that reach over a span's ends leave a partial sum in scratch; the warp that is last to leave
+// one of a token's adds them up in the places' order, so that no sum depends on timing.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "ra_kernels.cuh"
+#include "ra_ops.cuh"
+#include "ra_tokens.cuh"
+
+namespace ra {
+
+template <int DT>
+__device__ __forceinline__ float load_float(const void* p, uint64_t i) {
+  if constexpr (DT == DT_F32) return static_cast<const float*>(p)[i];
+  else return widen16<DT>(static_cast<const uint16_t*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void store_float(void* p, uint64_t i, float f) {
+  if constexpr (DT == DT_F32) static_cast<float*>(p)[i] = f;
+  else static_cast<uint16_t*>(p)[i] = (uint16_t)round16<DT>(f);
+}
+
+// A lane's N columns of a row: with VEC side by side in whole 16-byte lines, else every 32nd, one by one. The first is
+// column c0 + emb_first, columns from `cols` on are left out.
+template <int N, bool VEC>
+__device__ __forceinline__ uint32_t emb_first() { return (threadIdx.x & 31) * (VEC ? N : 1); }
+
+template <int DT, int N, bool VEC>
+__device__ __forceinline__ void emb_load(const void* row, uint64_t c, uint64_t cols, float (&x)[N]) {
+  if constexpr (VEC) {
+    constexpr int kLines = N * Elem<DT>::kSize / 16, V = 16 / Elem<DT>::kSize;
+#pragma unroll
+    for (int l = 0; l < kLines; ++l) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (c < cols) v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * Elem<DT>::kSize + l * 16);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if constexpr (DT == DT_F32) x[l * V + k] = __uint_as_float(w[k]);
+        else x[l * V + k] = widen16<DT>(k % 2 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = c + 32 * k < cols ? load_float<DT>(row, c + 32 * k) : 0.0f;
+  }
+}
+template <int DT, int N, bool VEC>
+__device__ __forceinline__ void emb_store(void* row, uint64_t c, uint64_t cols, const float (&x)[N]) {
+  if constexpr (VEC) {
+    constexpr int kLines = N * Elem<DT>::kSize / 16, V = 16 / Elem<DT>::kSize;
+#pragma unroll
+    for (int l = 0; l < kLines; ++l) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == DT_F32) w[k] = __float_as_uint(x[l * V + k]);
+        else w[k] = round16<DT>(x[l * V + 2 * k]) | round16<DT>(x[l * V + 2 * k + 1]) << 16;
+      }
+      if (c < cols) *reinterpret_cast<uint4*>(static_cast<char*>(row) + c * Elem<DT>::kSize + l * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (c + 32 * k < cols) store_float<DT>(row, c + 32 * k, x[k]);
+  }
+}
+
+// Which row, and which of the `across` warps side by side on it.
+__device__ __forceinline__ void emb_unit(uint64_t unit, uint64_t across, uint64_t& row, uint64_t& slice) {
+  if (across == 1) row = unit, slice = 0;
+  else if ((unit | across) >> 32 == 0) row = (uint32_t)unit / (uint32_t)across, slice = (uint32_t)unit % (uint32_t)across;
+  else row = unit / across, slice = unit % across;
+}
+
+// ---- lookup --------------------------------------------------------------------------
+
+constexpr int kEmbThreads = 256;
+
+struct EmbForward {
+  const void* table;
+  Indices tokens;
+  void* out;
+  uint64_t rows, cols, table_stride, out_stride, across;
+  int64_t vocab;
+  float scale;
+  int accumulate;
+};
+
+// A warp per row and slice of columns; lanes have U times N columns of it.
+template <int DT, int N, int U, bool VEC>
+__global__ void __launch_bounds__(kEmbThreads) embedding_forward_kernel(const __grid_constant__ EmbForward a) {
+  pdl_enter();
+  constexpr uint64_t es = Elem<DT>::kSize;
+  const uint64_t unit = (uint64_t)blockIdx.x * (kEmbThreads / 32) + threadIdx.x / 32;
+  uint64_t t, slice;
+  emb_unit(unit, a.across, t, slice);
+  if (t >= a.rows) return;
+  const uint64_t c0 = slice * (32 * N * U) + emb_first<N, VEC>();
+  const int64_t v = load_index(a.tokens, t);
+  const bool there = v >= 0 && v < a.vocab;
+  const char* from = static_cast<const char*>(a.table) + (there ? v : 0) * a.table_stride * es;
+  char* to = static_cast<char*>(a.out) + t * a.out_stride * es;
+  float x[U][N], old[U][N];
+#pragma unroll
+  for (int u = 0; u < U; ++u) emb_load<DT, N, VEC>(from, c0 + u * 32 * N, there ? a.cols : 0, x[u]);
+  if (a.accumulate) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) emb_load<DT, N, VEC>(to, c0 + u * 32 * N, a.cols, old[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      x[u][k] = there ? __fmul_rn(x[u][k], a.scale) : __int_as_float(0x7fffffff);
+      if (a.accumulate) x[u][k] += old[u][k];
+    }
+    emb_store<DT, N, VEC>(to, c0 + u * 32 * N, a.cols, x[u]);
+  }
+}
+
+// ---- gradient: what all its kernels get -------------------------------------------------
+
+struct EmbBackward {
+  const void* dy;
+  Indices tokens;
+  void* dtable;
+  uint64_t rows, cols, dy_stride, table_stride;
+  int64_t vocab, padding;
+  float scale;
+  uint32_t bits, passes, tiles, span, spans, across;
+  uint32_t *keys[2], *places[2], *counts, *tickets;
+  float* partial;  // [spans][2][across][32 * N]: of the places that come from the span before, and that go on into the next
+  uint32_t zero_from;  // CTAs from this one on clear the table
+  int zero_bytes, zero_known;  // bytes of its elements; whether only rows without a token are cleared
+};
+
+// The number that a token is sorted by: `vocab` where it does not count.
+__device__ __forceinline__ uint32_t emb_key(const EmbBackward& a, uint64_t t) {
+  const int64_t v = load_index(a.tokens, t);
+  return v < 0 || v >= a.vocab || v == a.padding ? (uint32_t)a.vocab : (uint32_t)v;
+}
+
+// Clears the table (CTA `part` of `parts`, any number of threads), or of it the rows that no token has: those with a
+// token are written by the sums. `seen`: 4096 words of shared memory.
+__device__ __forceinline__ void emb_clear(const EmbBackward& a, uint32_t part, uint32_t parts, uint32_t* seen) {
+  constexpr uint32_t kSlice = 4096 * 32;  // rows whose presence the words hold
+  const uint64_t es = (uint64_t)a.zero_bytes, width = a.cols * es, pitch = a.table_stride * es;
+  const uint64_t v0 = (uint64_t)a.vocab * part / parts, v1 = (uint64_t)a.vocab * (part + 1) / parts;
+  char* const table = static_cast<char*>(a.dtable);
+  const bool lines = ((reinterpret_cast<uintptr_t>(table) | pitch | width) & 15) == 0;
+  if (!a.zero_known && pitch == width) {  // one run of bytes
+    char* const from = table + v0 * pitch;
+    char* const to = table + v1 * pitch;
+    char* const lo = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(from) + 15) / 16 * 16);
+    char* const hi = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(to) / 16 * 16);
+    for (char* b = lo + threadIdx.x * 16; b < hi; b += blockDim.x * 16) *reinterpret_cast<uint4*>(b) = make_uint4(0, 0, 0, 0);
+    char* const end = lo < to ? lo : to;
+    for (char* b = from + threadIdx.x * 2; b < end; b += blockDim.x * 2) *reinterpret_cast<uint16_t*>(b) = 0;
+    for (char* b = (hi > end ? hi : end) + threadIdx.x * 2; b < to; b += blockDim.x * 2) *reinterpret_cast<uint16_t*>(b) = 0;
+    return;
+  }
+  for (uint64_t u = v0; u < v1; u += kSlice) {
+    const uint32_t rows = (uint32_t)(v1 - u < kSlice ? v1 - u : kSlice);
+    if (a.zero_known) {
+      for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) seen[i] = 0;
+      __syncthreads();
+#pragma unroll 8
+      for (uint64_t t = threadIdx.x; t < a.rows; t += blockDim.x) {
+        const uint64_t r = (uint64_t)emb_key(a, t) - u;
+        if (r < rows) atomicOr(&seen[r / 32], 1u << r % 32);
+      }
+      __syncthreads();
+    }
+    for (uint32_t r = threadIdx.x / 32; r < rows; r += blockDim.x / 32) {  // a warp per row
+      if (a.zero_known && (seen[r / 32] >> r % 32 & 1)) continue;
+      char* const row = table + (u + r) * pitch;
+      const uint64_t step = lines ? 16 : es;
+      for (uint64_t b = (threadIdx.x & 31) * step; b < width; b += 32 * step) {
+        if (lines) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
+        else if (es == 4) *reinterpret_cast<uint32_t*>(row + b) = 0;
+        else *reinterpret_cast<uint16_t*>(row + b) = 0;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- sort -----------------------------------------------------------------------------
+//
+// Stable, by digits of `bits` bits from the lowest. A CTA's items stand in the order (warp, round, lane). Within a warp
+// an item's rank among those of its digit is what the warp has counted of the digit plus the lanes before it that hold
+// it too; the counts of digits and warps, summed up in that order, give each warp's first place for each digit.
+
+template <int THREADS>
+struct EmbSort {
+  static constexpr int kWarps = THREADS / 32;
+  uint32_t counts[kWarps][256];
+  uint32_t parts[THREADS / 256][256];
+  uint32_t sums[8];
+};
+
+// Ranks of a thread's items among the warp's of the same digit (below 1024: two to a word); the warp's counts of digits
+// in s.counts. digit(i): of item i.
+template <int THREADS, int ITEMS, class D>
+__device__ __forceinline__ void emb_rank(EmbSort<THREADS>& s, D digit, uint32_t (&ranks)[(ITEMS + 1) / 2]) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  for (uint32_t d = lane; d < 256; d += 32) s.counts[warp][d] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t d = digit(i), same = __match_any_sync(0xffffffffu, d), before = __popc(same & ((1u << lane) - 1));
+    const uint32_t old = s.counts[warp][d];
+    __syncwarp();
+    if (before == 0) s.counts[warp][d] = old + __popc(same);
+    __syncwarp();
+    if (i % 2 == 0) ranks[i / 2] = old + before;
+    else ranks[i / 2] |= (old + before) << 16;
+  }
+}
+template <int N>
+__device__ __forceinline__ uint32_t emb_rank_of(const uint32_t (&ranks)[N], int i) { return i % 2 ? ranks[i / 2] >> 16 : ranks[i / 2] & 0xffffu; }
+// Counts into first places: s.counts[w][d] becomes the CTA's items of smaller digits, and those of d in warps before w.
+template <int THREADS>
+__device__ __forceinline__ void emb_first_places(EmbSort<THREADS>& s) {
+  constexpr int kParts = THREADS / 256, kEach = EmbSort<THREADS>::kWarps / kParts;
+  const uint32_t d = threadIdx.x % 256, part = threadIdx.x / 256, lane = threadIdx.x & 31;
+  __syncthreads();
+  uint32_t mine = 0;
+#pragma unroll
+  for (int w = 0; w < kEach; ++w) mine += s.counts[part * kEach + w][d];
+  s.parts[part][d] = mine;
+  __syncthreads();
+  uint32_t all = 0, before = 0;
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) {
+    const uint32_t n = s.parts[q][d];
+    if (q < (int)part) before += n;
+    all += n;
+  }
+  uint32_t sum = all;  // over the digits up to d
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t left = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += left;
+  }
+  if (threadIdx.x < 256 && lane == 31) s.sums[threadIdx.x / 32] = sum;
+  __syncthreads();
+  uint32_t at = sum - all + before;
+  for (uint32_t w = 0; w < d / 32; ++w) at += s.sums[w];
+#pragma unroll
+  for (int w = 0; w < kEach; ++w) {
+    const uint32_t n = s.counts[part * kEach + w][d];
+    s.counts[part * kEach + w][d] = at;
+    at += n;
+  }
+  __syncthreads();
+}
+
+constexpr uint32_t kEmbPlaceBits = 15;
+
+// CTA 0 sorts all tokens, as words of number and place; the others clear the table.
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) embedding_sort_kernel(const __grid_constant__ EmbBackward a) {
+  pdl_enter();
+  extern __shared__ uint32_t words[];  // THREADS * ITEMS
+  __shared__ union {
+    EmbSort<THREADS> sort;
+    uint32_t seen[4096];
+  } s;
+  if (blockIdx.x >= a.zero_from) {
+    emb_clear(a, blockIdx.x - a.zero_from, gridDim.x - a.zero_from, s.seen);
+    return;
+  }
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, first = warp * 32 * ITEMS + lane;
+  for (uint32_t i = threadIdx.x; i < a.spans * a.across; i += THREADS) a.tickets[i] = 0;
+  uint32_t word[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t t = first + i * 32;
+    word[i] = t < a.rows ? emb_key(a, t) << kEmbPlaceBits | t : 0xffffffffu;
+  }
+  for (uint32_t pass = 0; pass < a.passes; ++pass) {
+    const uint32_t shift = kEmbPlaceBits + pass * a.bits, mask = (1u << a.bits) - 1;
+    uint32_t ranks[(ITEMS + 1) / 2];
+    const auto digit = [&](int i) { return word[i] >> shift & mask; };
+    emb_rank<THREADS, ITEMS>(s.sort, digit, ranks);
+    emb_first_places<THREADS>(s.sort);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) words[s.sort.counts[warp][digit(i)] + emb_rank_of(ranks, i)] = word[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) word[i] = words[first + i * 32];
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t at = first + i * 32;
+    if (at < a.rows) {
+      a.keys[0][at] = word[i] >> kEmbPlaceBits;
+      a.places[0][at] = word[i] & ((1u << kEmbPlaceBits) - 1);
+    }
+  }
+}
+
+// More tokens than that: a pass is a count of every CTA's digits, and a CTA's items to their places. Pass 0 reads the
+// tokens themselves.
+constexpr int kEmbTileItems = 16;
+static_assert(kEmbThreads * kEmbTileItems == 4096, "a tile of the plan");
+
+__device__ __forceinline__ void emb_item(const EmbBackward& a, uint32_t pass, uint64_t t, uint32_t& key, uint32_t& place) {
+  key = 0xffffffffu, place = 0;
+  if (t >= a.rows) return;
+  key = pass ? a.keys[(pass - 1) % 2][t] : emb_key(a, t);
+  place = pass ? a.places[(pass - 1) % 2][t] : (uint32_t)t;
+}
+
+__global__ void __launch_bounds__(kEmbThreads) embedding_count_kernel(const __grid_constant__ EmbBackward a, uint32_t pass) {
+  pdl_enter();
+  __shared__ uint32_t seen[4096];  // the first 256: counts of digits
+  if (blockIdx.x >= a.zero_from) {
+    emb_clear(a, blockIdx.x - a.zero_from, gridDim.x - a.zero_from, seen);
+    return;
+  }
+  if (pass == 0)
+    for (uint64_t i = (uint64_t)blockIdx.x * kEmbThreads + threadIdx.x; i < (uint64_t)a.spans * a.across; i += (uint64_t)a.tiles * kEmbThreads)
+      a.tickets[i] = 0;
+  seen[threadIdx.x] = 0;
+  __syncthreads();
+  const uint64_t first = (uint64_t)blockIdx.x * 4096 + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kEmbTileItems; ++i) {
+    uint32_t key, place;
+    emb_item(a, pass, first + i * kEmbThreads, key, place);
+    if (first + i * kEmbThreads < a.rows) atomicAdd(&seen[key >> pass * a.bits & ((1u << a.bits) - 1)], 1u);
+  }
+  __syncthreads();
+  a.counts[(uint64_t)blockIdx.x * 256 + threadIdx.x] = seen[threadIdx.x];
+}
+
+__global__ void __launch_bounds__(kEmbThreads) embedding_scatter_kernel(const __grid_constant__ EmbBackward a, uint32_t pass) {
+  pdl_enter();
+  __shared__ EmbSort<kEmbThreads> s;
+  __shared__ uint32_t base[256], sums[8];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  // this CTA's first place for the thread's digit: items of smaller digits, and of this one in CTAs before
+  uint32_t all = 0, before = 0;
+#pragma unroll 8
+  for (uint32_t c = 0; c < a.tiles; ++c) {
+    const uint32_t n = a.counts[(uint64_t)c * 256 + threadIdx.x];
+    if (c < blockIdx.x) before += n;
+    all += n;
+  }
+  uint32_t sum = all;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t left = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += left;
+  }
+  if (lane == 31) sums[warp] = sum;
+  __syncthreads();
+  uint32_t at = sum - all + before;
+  for (uint32_t w = 0; w < warp; ++w) at += sums[w];
+  base[threadIdx.x] = at;
+  const uint64_t first = (uint64_t)blockIdx.x * 4096 + warp * 32 * kEmbTileItems + lane;
+  uint32_t key[kEmbTileItems], place[kEmbTileItems], ranks[kEmbTileItems / 2];
+#pragma unroll
+  for (int i = 0; i < kEmbTileItems; ++i) emb_item(a, pass, first + i * 32, key[i], place[i]);
+  const auto digit = [&](int i) { return key[i] >> pass * a.bits & ((1u << a.bits) - 1); };
+  emb_rank<kEmbThreads, kEmbTileItems>(s, digit, ranks);
+  __syncthreads();
+  // items of the digit in the warps before this one
+  uint32_t run = 0;
+  for (int w = 0; w < kEmbThreads / 32; ++w) {
+    const uint32_t n = s.counts[w][threadIdx.x];
+    s.counts[w][threadIdx.x] = run;
+    run += n;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEmbTileItems; ++i)
+    if (first + i * 32 < a.rows) {
+      const uint32_t to = base[digit(i)] + s.counts[warp][digit(i)] + emb_rank_of(ranks, i);
+      a.keys[pass % 2][to] = key[i];
+      a.places[pass % 2][to] = place[i];
+    }
+}
+
+// ---- sums -----------------------------------------------------------------------------
+
+// dtable's row of a token: scale * sum, with ADD on top of what it holds (`old`).
+template <int WDT, int N, bool VEC, bool ADD>
+__device__ __forceinline__ void emb_finish(const EmbBackward& a, uint32_t key, uint64_t c, const float (&sum)[N], const float (&old)[N]) {
+  float x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    x[k] = __fmul_rn(sum[k], a.scale);
+    if (ADD) x[k] += old[k];
+  }
+  emb_store<WDT, N, VEC>(static_cast<char*>(a.dtable) + (uint64_t)key * a.table_stride * Elem<WDT>::kSize, c, a.cols, x);
+}
+template <int WDT, int N, bool VEC>
+__device__ __forceinline__ void emb_old(const EmbBackward& a, uint32_t key, uint64_t c, bool wanted, float (&old)[N]) {
+  emb_load<WDT, N, VEC>(static_cast<const char*>(a.dtable) + (uint64_t)key * a.table_stride * Elem<WDT>::kSize, c, wanted ? a.cols : 0, old);
+}
+
+// A token's places reach over the ends of spans `first` to `last`: adds up what they left, if this warp is the last of
+// them to have left something.
+template <int WDT, int N, bool VEC, bool ADD>
+__device__ __forceinline__ void emb_join(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t across, uint32_t key, uint64_t c) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t first = span, last = span;
+  // 32 spans at a time: span f goes on from the one before where the places at its start and before it have the key
+  for (bool more = true; more;) {
+    const uint32_t f = first - lane;  // wraps below 0
+    const bool from = f <= first && f > 0 && keys[(uint64_t)f * a.span - 1] == key;
+    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, from)) - 1;
+    more = run == 0xffffffffu;
+    first -= more ? 32 : run;
+  }
+  for (bool more = true; more;) {
+    const uint64_t next = (uint64_t)(last + lane + 1) * a.span;
+    const bool on = next < a.rows && keys[next] == key;
+    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, on)) - 1;
+    more = run == 0xffffffffu;
+    last += more ? 32 : run;
+  }
+  __threadfence();
+  __syncwarp();
+  uint32_t ticket = 0;
+  if (lane == 0) ticket = atomicAdd(&a.tickets[(uint64_t)first * a.across + across], 1u);
+  if (__shfl_sync(0xffffffffu, ticket, 0) != last - first) return;
+  __threadfence();
+  float sum[N], old[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum[k] = old[k] = 0.0f;
+  if (ADD) emb_old<WDT, N, VEC>(a, key, c, true, old);
+  const uint64_t slot = (uint64_t)a.across * 32 * N;  // floats of a partial sum
+  const float4* at = reinterpret_cast<const float4*>(a.partial + ((uint64_t)first * 2 + 1) * slot + (uint64_t)across * 32 * N + lane * N);
+#pragma unroll 4
+  for (uint32_t f = first; f <= last; ++f) {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const float4 v = __ldcg(at + q);
+      sum[4 * q] += v.x, sum[4 * q + 1] += v.y, sum[4 * q + 2] += v.z, sum[4 * q + 3] += v.w;
+    }
+    at += (f == first ? 1 : 2) * (slot / 4);  // the first span's last places, then each one's first
+  }
+  emb_finish<WDT, N, VEC, ADD>(a, key, c, sum, old);
+}
+
+// A warp per span of sorted places and slice of the columns. Rows of dy are asked for a batch at a time, and with
+// accumulate the rows of dtable that the batch ends, so that a token costs no wait of its own.
+template <int DT, int WDT, int N, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kEmbThreads) embedding_sum_kernel(const __grid_constant__ EmbBackward a, const uint32_t* keys, const uint32_t* places) {
+  pdl_enter();
+  constexpr int kBatch = ADD ? 4 : 8;
+  uint64_t row, slice;
+  emb_unit((uint64_t)blockIdx.x * (kEmbThreads / 32) + threadIdx.x / 32, a.across, row, slice);
+  const uint32_t span = (uint32_t)row, across = (uint32_t)slice, lane = threadIdx.x & 31;
+  if (row >= a.spans) return;
+  const uint64_t c = slice * 32 * N + emb_first<N, VEC>();
+  const uint64_t p0 = (uint64_t)span * a.span, p1 = p0 + a.span < a.rows ? p0 + a.span : a.rows;
+  const uint32_t none = (uint32_t)a.vocab;  // of the tokens that do not count, behind all others
+  // lane l has place p + l - 1 of the batch that starts at p
+  uint32_t key = none, place = 0;
+  const auto ask = [&](uint64_t p) {
+    const uint64_t mine = p + lane - 1;  // wraps for lane 0 at place 0
+    key = lane < kBatch + 2 && mine < a.rows ? keys[mine] : none;
+    place = lane > 0 && lane <= kBatch && mine < p1 ? places[mine] : 0;
+  };
+  ask(p0);
+  float sum[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+  // whether the places summed now start in this span
+  bool inside = p0 == 0 || __shfl_sync(0xffffffffu, key, 0) != __shfl_sync(0xffffffffu, key, 1);
+  uint32_t head = none, tail = none;
+  for (uint64_t p = p0; p < p1; p += kBatch) {
+    float x[kBatch][N], old[ADD ? kBatch : 1][N];
+    uint32_t k[kBatch + 1];
+#pragma unroll
+    for (int i = 0; i <= kBatch; ++i) k[i] = __shfl_sync(0xffffffffu, key, i + 1);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint64_t from = __shfl_sync(0xffffffffu, place, i + 1);
+      const bool counts = p + i < p1 && k[i] != none;
+      emb_load<DT, N, VEC>(static_cast<const char*>(a.dy) + from * a.dy_stride * Elem<DT>::kSize, c, counts ? a.cols : 0, x[i]);
+      if constexpr (ADD) emb_old<WDT, N, VEC>(a, counts ? k[i] : 0, c, counts && k[i + 1] != k[i], old[i]);
+    }
+    ask(p + kBatch);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (p + i >= p1 || k[i] == none) break;
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum[j] += x[i][j];
+      const bool ends = k[i + 1] != k[i];
+      if (!ends && p + i + 1 < p1) continue;
+      if (ends && inside) {
+        emb_finish<WDT, N, VEC, ADD>(a, k[i], c, sum, old[ADD ? i : 0]);
+      } else {
+        float4* to = reinterpret_cast<float4*>(a.partial + (((uint64_t)span * 2 + (inside ? 1 : 0)) * a.across + across) * 32 * N + lane * N);
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) to[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
+        (inside ? tail : head) = k[i];
+      }
+      inside = true;
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+    }
+  }
+  if (head != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, across, head, c);
+  if (tail != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, across, tail, c);
+}
+
+}  // namespace ra

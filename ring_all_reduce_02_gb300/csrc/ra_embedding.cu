@@ -31,27 +31,30 @@ constexpr int kPerLane(int dtype) { return dtype == RA_FLOAT32 ? 4 : 8; }
 
 template <int THREADS, int ITEMS>
 cudaError_t sort_one(const ra::EmbBackward& a, unsigned zeros, cudaStream_t s) {
-  const auto kernel = ra::embedding_sort_kernel<THREADS, ITEMS>;
-  constexpr size_t smem = (size_t)THREADS * ITEMS * 4;
-  // the limit is the function's, not the call's: the same for all calls
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return err != cudaSuccess ? err : ra::launch_programmatic(kernel, dim3(1 + zeros), THREADS, smem, s, a);
+  return ra::launch_programmatic(ra::embedding_sort_kernel<THREADS, ITEMS>, dim3(ra::kEmbCluster + zeros), THREADS, 0, s, a);
 }
 
 // Sorts the tokens, and clears the table beside that.
 cudaError_t sort(ra::EmbBackward& a, const ra::EmbPlan& p, bool clear, cudaStream_t s) {
   const unsigned zeros = clear ? 304 : 0;  // two CTAs an SM
-  if (p.one) {
-    a.zero_from = 1;
-    return a.rows <= 2048 ? sort_one<256, 8>(a, zeros, s) : a.rows <= 8192 ? sort_one<1024, 8>(a, zeros, s) : sort_one<1024, 32>(a, zeros, s);
-  }
+  if (p.one) return a.rows <= 2048 ? sort_one<256, 1>(a, zeros, s) : a.rows <= 8192 ? sort_one<256, 4>(a, zeros, s) : sort_one<512, 8>(a, zeros, s);
   cudaError_t err = cudaSuccess;
-  a.zero_from = a.tiles;
   for (uint32_t pass = 0; pass < a.passes && err == cudaSuccess; ++pass) {
     err = ra::launch_programmatic(ra::embedding_count_kernel, dim3(a.tiles + (pass == 0 ? zeros : 0)), ra::kEmbThreads, 0, s, a, pass);
     if (err == cudaSuccess) err = ra::launch_programmatic(ra::embedding_scatter_kernel, dim3(a.tiles), ra::kEmbThreads, 0, s, a, pass);
   }
   return err;
+}
+
+template <int DT, int WDT, int N, bool VEC, bool ADD>
+cudaError_t sums(const ra::EmbBackward& a, int last, cudaStream_t s) {
+  const auto kernel = ra::embedding_sum_kernel<DT, WDT, N, VEC, ADD>;
+  constexpr size_t smem = ra::kEmbSumSmem<DT, WDT, N, VEC, ADD>;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+  }
+  return ra::launch_programmatic(kernel, dim3(ctas((uint64_t)a.spans * a.across)), ra::kEmbThreads, smem, s, a, a.keys[last], a.places[last]);
 }
 
 template <int DT, int WDT>
@@ -61,10 +64,9 @@ cudaError_t backward(ra::EmbBackward& a, const ra::EmbPlan& p, bool add, cudaStr
   if (err != cudaSuccess || a.rows == 0) return err;
   const int last = p.one ? 0 : (int)(p.passes - 1) % 2;
   const bool vec = lines(a.dy, a.dy_stride * ra::Elem<DT>::kSize) && lines(a.dtable, a.table_stride * ra::Elem<WDT>::kSize) && a.cols % N == 0;
-  const auto kernel = vec ? add ? ra::embedding_sum_kernel<DT, WDT, N, true, true> : ra::embedding_sum_kernel<DT, WDT, N, true, false>
-                      : add ? ra::embedding_sum_kernel<DT, WDT, N, false, true>
-                            : ra::embedding_sum_kernel<DT, WDT, N, false, false>;
-  return ra::launch_programmatic(kernel, dim3(ctas((uint64_t)a.spans * a.across)), ra::kEmbThreads, 0, s, a, a.keys[last], a.places[last]);
+  return vec ? add ? sums<DT, WDT, N, true, true>(a, last, s) : sums<DT, WDT, N, true, false>(a, last, s)
+             : add ? sums<DT, WDT, N, false, true>(a, last, s)
+                   : sums<DT, WDT, N, false, false>(a, last, s);
 }
 
 }  // namespace

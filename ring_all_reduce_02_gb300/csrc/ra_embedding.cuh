@@ -11,6 +11,7 @@
 #include "ra_kernels.cuh"
 #include "ra_ops.cuh"
 #include "ra_tokens.cuh"
+#include "ra_umma.cuh"
 
 namespace ra {
 
@@ -30,26 +31,35 @@ __device__ __forceinline__ void store_float(void* p, uint64_t i, float f) {
 template <int N, bool VEC>
 __device__ __forceinline__ uint32_t emb_first() { return (threadIdx.x & 31) * (VEC ? N : 1); }
 
+// As they lie in memory, to be widened where they are used: rows in flight take half the registers.
 template <int DT, int N, bool VEC>
-__device__ __forceinline__ void emb_load(const void* row, uint64_t c, uint64_t cols, float (&x)[N]) {
-  if constexpr (VEC) {
-    constexpr int kLines = N * Elem<DT>::kSize / 16, V = 16 / Elem<DT>::kSize;
+struct EmbRaw {
+  uint32_t w[VEC ? N * Elem<DT>::kSize / 4 : N];
+  __device__ __forceinline__ void load(const void* row, uint64_t c, uint64_t cols) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int l = 0; l < kLines; ++l) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c < cols) v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * Elem<DT>::kSize + l * 16);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int l = 0; l < N * Elem<DT>::kSize / 16; ++l) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c < cols) v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * Elem<DT>::kSize + l * 16);
+        w[4 * l] = v.x, w[4 * l + 1] = v.y, w[4 * l + 2] = v.z, w[4 * l + 3] = v.w;
+      }
+    } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if constexpr (DT == DT_F32) x[l * V + k] = __uint_as_float(w[k]);
-        else x[l * V + k] = widen16<DT>(k % 2 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+      for (int k = 0; k < N; ++k) {
+        w[k] = 0;
+        if (c + 32 * k < cols) {
+          if constexpr (DT == DT_F32) w[k] = static_cast<const uint32_t*>(row)[c + 32 * k];
+          else w[k] = static_cast<const uint16_t*>(row)[c + 32 * k];
+        }
       }
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = c + 32 * k < cols ? load_float<DT>(row, c + 32 * k) : 0.0f;
   }
-}
+  __device__ __forceinline__ float at(int k) const {
+    if constexpr (DT == DT_F32) return __uint_as_float(w[k]);
+    else if constexpr (VEC) return widen16<DT>(k % 2 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+    else return widen16<DT>(w[k]);
+  }
+};
 template <int DT, int N, bool VEC>
 __device__ __forceinline__ void emb_store(void* row, uint64_t c, uint64_t cols, const float (&x)[N]) {
   if constexpr (VEC) {
@@ -106,21 +116,22 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_forward_kernel(const __
   const bool there = v >= 0 && v < a.vocab;
   const char* from = static_cast<const char*>(a.table) + (there ? v : 0) * a.table_stride * es;
   char* to = static_cast<char*>(a.out) + t * a.out_stride * es;
-  float x[U][N], old[U][N];
+  EmbRaw<DT, N, VEC> raw[U], old[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) emb_load<DT, N, VEC>(from, c0 + u * 32 * N, there ? a.cols : 0, x[u]);
+  for (int u = 0; u < U; ++u) raw[u].load(from, c0 + u * 32 * N, there ? a.cols : 0);
   if (a.accumulate) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) emb_load<DT, N, VEC>(to, c0 + u * 32 * N, a.cols, old[u]);
+    for (int u = 0; u < U; ++u) old[u].load(to, c0 + u * 32 * N, a.cols);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    float x[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      x[u][k] = there ? __fmul_rn(x[u][k], a.scale) : __int_as_float(0x7fffffff);
-      if (a.accumulate) x[u][k] += old[u][k];
+      x[k] = there ? __fmul_rn(raw[u].at(k), a.scale) : __int_as_float(0x7fffffff);
+      if (a.accumulate) x[k] += old[u].at(k);
     }
-    emb_store<DT, N, VEC>(to, c0 + u * 32 * N, a.cols, x[u]);
+    emb_store<DT, N, VEC>(to, c0 + u * 32 * N, a.cols, x);
   }
 }
 
@@ -136,7 +147,6 @@ struct EmbBackward {
   uint32_t bits, passes, tiles, span, spans, across;
   uint32_t *keys[2], *places[2], *counts, *tickets;
   float* partial;  // [spans][2][across][32 * N]: of the places that come from the span before, and that go on into the next
-  uint32_t zero_from;  // CTAs from this one on clear the table
   int zero_bytes, zero_known;  // bytes of its elements; whether only rows without a token are cleared
 };
 
@@ -195,26 +205,35 @@ __device__ __forceinline__ void emb_clear(const EmbBackward& a, uint32_t part, u
 //
 // Stable, by digits of `bits` bits from the lowest. A CTA's items stand in the order (warp, round, lane). Within a warp
 // an item's rank among those of its digit is what the warp has counted of the digit plus the lanes before it that hold
-// it too; the counts of digits and warps, summed up in that order, give each warp's first place for each digit.
+// it too; the counts of digits, CTAs and warps, summed up in that order, give each warp's first place for each digit.
 
 template <int THREADS>
 struct EmbSort {
   static constexpr int kWarps = THREADS / 32;
   uint32_t counts[kWarps][256];
-  uint32_t parts[THREADS / 256][256];
   uint32_t sums[8];
 };
 
 // Ranks of a thread's items among the warp's of the same digit (below 1024: two to a word); the warp's counts of digits
-// in s.counts. digit(i): of item i.
+// in s.counts. digit(i): of item i, `bits` bits. The lanes with an item's digit come from a ballot a bit (match.any takes
+// as long); ballots are what bounds a CTA with many warps, 8192 tokens in one CTA of 1024 threads take 14 us, in 8 CTAs
+// of 256 threads less than 4.
 template <int THREADS, int ITEMS, class D>
-__device__ __forceinline__ void emb_rank(EmbSort<THREADS>& s, D digit, uint32_t (&ranks)[(ITEMS + 1) / 2]) {
+__device__ __forceinline__ void emb_rank(EmbSort<THREADS>& s, uint32_t bits, D digit, uint32_t (&ranks)[(ITEMS + 1) / 2]) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   for (uint32_t d = lane; d < 256; d += 32) s.counts[warp][d] = 0;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const uint32_t d = digit(i), same = __match_any_sync(0xffffffffu, d), before = __popc(same & ((1u << lane) - 1));
+    const uint32_t d = digit(i);
+    uint32_t same = 0xffffffffu;
+#pragma unroll
+    for (uint32_t b = 0; b < 8; ++b) {
+      const bool one = d >> b & 1;
+      const uint32_t ones = __ballot_sync(0xffffffffu, one);
+      if (b < bits) same &= one ? ones : ~ones;
+    }
+    const uint32_t before = __popc(same & ((1u << lane) - 1));
     const uint32_t old = s.counts[warp][d];
     __syncwarp();
     if (before == 0) s.counts[warp][d] = old + __popc(same);
@@ -225,81 +244,107 @@ __device__ __forceinline__ void emb_rank(EmbSort<THREADS>& s, D digit, uint32_t 
 }
 template <int N>
 __device__ __forceinline__ uint32_t emb_rank_of(const uint32_t (&ranks)[N], int i) { return i % 2 ? ranks[i / 2] >> 16 : ranks[i / 2] & 0xffffu; }
-// Counts into first places: s.counts[w][d] becomes the CTA's items of smaller digits, and those of d in warps before w.
+
+// Thread d < 256: the items of the digits below d in all CTAs, `all` of d. Every thread of the CTA has to come here.
 template <int THREADS>
-__device__ __forceinline__ void emb_first_places(EmbSort<THREADS>& s) {
-  constexpr int kParts = THREADS / 256, kEach = EmbSort<THREADS>::kWarps / kParts;
-  const uint32_t d = threadIdx.x % 256, part = threadIdx.x / 256, lane = threadIdx.x & 31;
-  __syncthreads();
-  uint32_t mine = 0;
-#pragma unroll
-  for (int w = 0; w < kEach; ++w) mine += s.counts[part * kEach + w][d];
-  s.parts[part][d] = mine;
-  __syncthreads();
-  uint32_t all = 0, before = 0;
-#pragma unroll
-  for (int q = 0; q < kParts; ++q) {
-    const uint32_t n = s.parts[q][d];
-    if (q < (int)part) before += n;
-    all += n;
-  }
-  uint32_t sum = all;  // over the digits up to d
+__device__ __forceinline__ uint32_t emb_digits_below(EmbSort<THREADS>& s, uint32_t all) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  uint32_t sum = all;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const uint32_t left = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += left;
   }
-  if (threadIdx.x < 256 && lane == 31) s.sums[threadIdx.x / 32] = sum;
+  if (warp < 8 && lane == 31) s.sums[warp] = sum;
   __syncthreads();
-  uint32_t at = sum - all + before;
-  for (uint32_t w = 0; w < d / 32; ++w) at += s.sums[w];
-#pragma unroll
-  for (int w = 0; w < kEach; ++w) {
-    const uint32_t n = s.counts[part * kEach + w][d];
-    s.counts[part * kEach + w][d] = at;
-    at += n;
-  }
-  __syncthreads();
+  uint32_t at = sum - all;
+  for (uint32_t w = 0; w < warp && w < 8; ++w) at += s.sums[w];
+  return at;
 }
 
-constexpr uint32_t kEmbPlaceBits = 15;
+__device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_address(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_store(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(p, rank)), "r"(v) : "memory");
+}
 
-// CTA 0 sorts all tokens, as words of number and place; the others clear the table.
+constexpr uint32_t kEmbPlaceBits = 15, kEmbCluster = 8;
+
+// The first cluster sorts all tokens, as words of number and place, a share to each CTA; the others clear the table.
 template <int THREADS, int ITEMS>
-__global__ void __launch_bounds__(THREADS) embedding_sort_kernel(const __grid_constant__ EmbBackward a) {
+__global__ void __cluster_dims__(kEmbCluster, 1, 1) __launch_bounds__(THREADS) embedding_sort_kernel(const __grid_constant__ EmbBackward a) {
   pdl_enter();
-  extern __shared__ uint32_t words[];  // THREADS * ITEMS
+  constexpr uint32_t kShare = THREADS * ITEMS;
   __shared__ union {
-    EmbSort<THREADS> sort;
+    struct {
+      EmbSort<THREADS> sort;
+      uint32_t total[256];
+      uint32_t words[kShare];
+    };
     uint32_t seen[4096];
   } s;
-  if (blockIdx.x >= a.zero_from) {
-    emb_clear(a, blockIdx.x - a.zero_from, gridDim.x - a.zero_from, s.seen);
+  if (blockIdx.x >= kEmbCluster) {
+    emb_clear(a, blockIdx.x - kEmbCluster, gridDim.x - kEmbCluster, s.seen);
     return;
   }
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, first = warp * 32 * ITEMS + lane;
-  for (uint32_t i = threadIdx.x; i < a.spans * a.across; i += THREADS) a.tickets[i] = 0;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, rank = blockIdx.x, first = warp * 32 * ITEMS + lane;
+  for (uint32_t i = rank * THREADS + threadIdx.x; i < a.spans * a.across; i += kEmbCluster * THREADS) a.tickets[i] = 0;
   uint32_t word[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const uint32_t t = first + i * 32;
+    const uint32_t t = rank * kShare + first + i * 32;
     word[i] = t < a.rows ? emb_key(a, t) << kEmbPlaceBits | t : 0xffffffffu;
   }
   for (uint32_t pass = 0; pass < a.passes; ++pass) {
     const uint32_t shift = kEmbPlaceBits + pass * a.bits, mask = (1u << a.bits) - 1;
     uint32_t ranks[(ITEMS + 1) / 2];
     const auto digit = [&](int i) { return word[i] >> shift & mask; };
-    emb_rank<THREADS, ITEMS>(s.sort, digit, ranks);
-    emb_first_places<THREADS>(s.sort);
+    emb_rank<THREADS, ITEMS>(s.sort, a.bits, digit, ranks);
+    __syncthreads();
+    const uint32_t d = threadIdx.x;
+    if (d < 256) {
+      uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) words[s.sort.counts[warp][digit(i)] + emb_rank_of(ranks, i)] = word[i];
+      for (int w = 0; w < THREADS / 32; ++w) mine += s.sort.counts[w][d];
+      s.total[d] = mine;
+    }
+    cluster_sync();
+    uint32_t all = 0, before = 0;
+    if (d < 256) {
+      uint32_t n[kEmbCluster];
+#pragma unroll
+      for (uint32_t c = 0; c < kEmbCluster; ++c) n[c] = peer_load(&s.total[d], c);
+#pragma unroll
+      for (uint32_t c = 0; c < kEmbCluster; ++c) {
+        if (c < rank) before += n[c];
+        all += n[c];
+      }
+    }
+    uint32_t at = emb_digits_below(s.sort, all) + before;
+    if (d < 256) {
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        const uint32_t n = s.sort.counts[w][d];
+        s.sort.counts[w][d] = at;
+        at += n;
+      }
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) word[i] = words[first + i * 32];
+    for (int i = 0; i < ITEMS; ++i) {
+      const uint32_t to = s.sort.counts[warp][digit(i)] + emb_rank_of(ranks, i);
+      peer_store(&s.words[to % kShare], to / kShare, word[i]);
+    }
+    cluster_sync();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) word[i] = s.words[first + i * 32];
   }
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const uint32_t at = first + i * 32;
+    const uint32_t at = rank * kShare + first + i * 32;
     if (at < a.rows) {
       a.keys[0][at] = word[i] >> kEmbPlaceBits;
       a.places[0][at] = word[i] & ((1u << kEmbPlaceBits) - 1);
@@ -322,8 +367,8 @@ __device__ __forceinline__ void emb_item(const EmbBackward& a, uint32_t pass, ui
 __global__ void __launch_bounds__(kEmbThreads) embedding_count_kernel(const __grid_constant__ EmbBackward a, uint32_t pass) {
   pdl_enter();
   __shared__ uint32_t seen[4096];  // the first 256: counts of digits
-  if (blockIdx.x >= a.zero_from) {
-    emb_clear(a, blockIdx.x - a.zero_from, gridDim.x - a.zero_from, seen);
+  if (blockIdx.x >= a.tiles) {
+    emb_clear(a, blockIdx.x - a.tiles, gridDim.x - a.tiles, seen);
     return;
   }
   if (pass == 0)
@@ -345,7 +390,7 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_count_kernel(const __gr
 __global__ void __launch_bounds__(kEmbThreads) embedding_scatter_kernel(const __grid_constant__ EmbBackward a, uint32_t pass) {
   pdl_enter();
   __shared__ EmbSort<kEmbThreads> s;
-  __shared__ uint32_t base[256], sums[8];
+  __shared__ uint32_t base[256];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   // this CTA's first place for the thread's digit: items of smaller digits, and of this one in CTAs before
   uint32_t all = 0, before = 0;
@@ -355,23 +400,14 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_scatter_kernel(const __
     if (c < blockIdx.x) before += n;
     all += n;
   }
-  uint32_t sum = all;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const uint32_t left = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += left;
-  }
-  if (lane == 31) sums[warp] = sum;
-  __syncthreads();
-  uint32_t at = sum - all + before;
-  for (uint32_t w = 0; w < warp; ++w) at += sums[w];
+  const uint32_t at = emb_digits_below(s, all) + before;
   base[threadIdx.x] = at;
   const uint64_t first = (uint64_t)blockIdx.x * 4096 + warp * 32 * kEmbTileItems + lane;
   uint32_t key[kEmbTileItems], place[kEmbTileItems], ranks[kEmbTileItems / 2];
 #pragma unroll
   for (int i = 0; i < kEmbTileItems; ++i) emb_item(a, pass, first + i * 32, key[i], place[i]);
   const auto digit = [&](int i) { return key[i] >> pass * a.bits & ((1u << a.bits) - 1); };
-  emb_rank<kEmbThreads, kEmbTileItems>(s, digit, ranks);
+  emb_rank<kEmbThreads, kEmbTileItems>(s, a.bits, digit, ranks);
   __syncthreads();
   // items of the digit in the warps before this one
   uint32_t run = 0;
@@ -392,26 +428,71 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_scatter_kernel(const __
 
 // ---- sums -----------------------------------------------------------------------------
 
+// A warp's slice of a row (32 N columns from c0 on) on its way through shared memory, which holds as many rows in flight
+// as the memory's latency asks for without a register for them. With VEC a lane copies and reads its own 16-byte lines;
+// else lanes copy every 32nd word that holds some of the slice, and read every 32nd element.
+template <int DT, int N, bool VEC>
+struct EmbSlice {
+  static constexpr uint32_t es = Elem<DT>::kSize, kBytes = 32 * N * es + (VEC ? 0 : 16);
+  static __device__ __forceinline__ void copy(uint8_t* slot, const void* row, uint64_t c0, uint64_t cols) {
+    const uint32_t lane = threadIdx.x & 31, to = (uint32_t)__cvta_generic_to_shared(slot);
+    if constexpr (VEC) {
+#pragma unroll
+      for (uint32_t l = 0; l < N * es / 16; ++l) {
+        const uint64_t c = c0 + lane * N;
+        if (c < cols)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + lane * N * es + l * 16),
+                       "l"(static_cast<const char*>(row) + c * es + l * 16)
+                       : "memory");
+      }
+    } else {
+      const uintptr_t first = reinterpret_cast<uintptr_t>(row) + c0 * es, word = first & ~(uintptr_t)3;
+      const uint64_t left = cols - c0 < 32 * N ? cols - c0 : 32 * N;
+      const uint32_t words = (uint32_t)((first - word + left * es + 3) / 4);
+#pragma unroll
+      for (uint32_t j = 0; j <= N * es / 4; ++j)
+        if (lane + 32 * j < words)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + (lane + 32 * j) * 4), "l"(word + (lane + 32 * j) * 4) : "memory");
+    }
+  }
+  // The lane's columns; those from `cols` on hold anything.
+  static __device__ __forceinline__ void read(const uint8_t* slot, const void* row, uint64_t c0, float (&x)[N]) {
+    const uint32_t lane = threadIdx.x & 31;
+    if constexpr (VEC) {
+#pragma unroll
+      for (uint32_t l = 0; l < N * es / 16; ++l) {
+        const uint4 v = *reinterpret_cast<const uint4*>(slot + lane * N * es + l * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (uint32_t k = 0; k < 16 / es; ++k) {
+          if constexpr (DT == DT_F32) x[l * 4 + k] = __uint_as_float(w[k]);
+          else x[l * 8 + k] = widen16<DT>(k % 2 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+        }
+      }
+    } else {
+      const uint32_t phase = (uint32_t)((reinterpret_cast<uintptr_t>(row) + c0 * es) & 3);
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = load_float<DT>(slot + phase, lane + 32 * k);
+    }
+  }
+};
+
 // dtable's row of a token: scale * sum, with ADD on top of what it holds (`old`).
 template <int WDT, int N, bool VEC, bool ADD>
-__device__ __forceinline__ void emb_finish(const EmbBackward& a, uint32_t key, uint64_t c, const float (&sum)[N], const float (&old)[N]) {
+__device__ __forceinline__ void emb_finish(const EmbBackward& a, char* row, uint64_t c, const float (&sum)[N], const float (&old)[N]) {
   float x[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     x[k] = __fmul_rn(sum[k], a.scale);
     if (ADD) x[k] += old[k];
   }
-  emb_store<WDT, N, VEC>(static_cast<char*>(a.dtable) + (uint64_t)key * a.table_stride * Elem<WDT>::kSize, c, a.cols, x);
-}
-template <int WDT, int N, bool VEC>
-__device__ __forceinline__ void emb_old(const EmbBackward& a, uint32_t key, uint64_t c, bool wanted, float (&old)[N]) {
-  emb_load<WDT, N, VEC>(static_cast<const char*>(a.dtable) + (uint64_t)key * a.table_stride * Elem<WDT>::kSize, c, wanted ? a.cols : 0, old);
+  emb_store<WDT, N, VEC>(row, c, a.cols, x);
 }
 
 // A token's places reach over the ends of spans `first` to `last`: adds up what they left, if this warp is the last of
 // them to have left something.
 template <int WDT, int N, bool VEC, bool ADD>
-__device__ __forceinline__ void emb_join(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t across, uint32_t key, uint64_t c) {
+__device__ __noinline__ void emb_join(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t across, uint32_t key) {
   const uint32_t lane = threadIdx.x & 31;
   uint32_t first = span, last = span;
   // 32 spans at a time: span f goes on from the one before where the places at its start and before it have the key
@@ -435,86 +516,119 @@ __device__ __forceinline__ void emb_join(const EmbBackward& a, const uint32_t* k
   if (lane == 0) ticket = atomicAdd(&a.tickets[(uint64_t)first * a.across + across], 1u);
   if (__shfl_sync(0xffffffffu, ticket, 0) != last - first) return;
   __threadfence();
+  const uint64_t c = (uint64_t)across * 32 * N + emb_first<N, VEC>();
+  char* const row = static_cast<char*>(a.dtable) + (uint64_t)key * a.table_stride * Elem<WDT>::kSize;
   float sum[N], old[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) sum[k] = old[k] = 0.0f;
-  if (ADD) emb_old<WDT, N, VEC>(a, key, c, true, old);
+  if (ADD) {
+    EmbRaw<WDT, N, VEC> raw;
+    raw.load(row, c, a.cols);
+#pragma unroll
+    for (int k = 0; k < N; ++k) old[k] = raw.at(k);
+  }
   const uint64_t slot = (uint64_t)a.across * 32 * N;  // floats of a partial sum
   const float4* at = reinterpret_cast<const float4*>(a.partial + ((uint64_t)first * 2 + 1) * slot + (uint64_t)across * 32 * N + lane * N);
-#pragma unroll 4
-  for (uint32_t f = first; f <= last; ++f) {
+  // the first span's last places, then each one's first, 8 at a time
+  for (uint32_t f = first; f <= last; f += 8) {
+    float4 v[8][N / 4];
 #pragma unroll
-    for (int q = 0; q < N / 4; ++q) {
-      const float4 v = __ldcg(at + q);
-      sum[4 * q] += v.x, sum[4 * q + 1] += v.y, sum[4 * q + 2] += v.z, sum[4 * q + 3] += v.w;
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint64_t on = (f + i <= last ? f + i : last) - first;
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) v[i][q] = __ldcg(at + (on ? 2 * on - 1 : 0) * (slot / 4) + q);
     }
-    at += (f == first ? 1 : 2) * (slot / 4);  // the first span's last places, then each one's first
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q)
+        if (f + i <= last) sum[4 * q] += v[i][q].x, sum[4 * q + 1] += v[i][q].y, sum[4 * q + 2] += v[i][q].z, sum[4 * q + 3] += v[i][q].w;
   }
-  emb_finish<WDT, N, VEC, ADD>(a, key, c, sum, old);
+  emb_finish<WDT, N, VEC, ADD>(a, row, c, sum, old);
 }
 
-// A warp per span of sorted places and slice of the columns. Rows of dy are asked for a batch at a time, and with
-// accumulate the rows of dtable that the batch ends, so that a token costs no wait of its own.
+#ifndef EMB_FLIGHT
+#define EMB_FLIGHT 8
+#endif
+constexpr uint32_t kEmbFlight = EMB_FLIGHT;  // rows that a warp has in flight
+template <int DT, int WDT, int N, bool VEC, bool ADD>
+constexpr uint32_t kEmbSumSmem = kEmbThreads / 32 * kEmbFlight * (EmbSlice<DT, N, VEC>::kBytes + (ADD ? EmbSlice<WDT, N, VEC>::kBytes : 0));
+
+// A warp per span of sorted places and slice of the columns: adds the places' rows up in their order, and writes a
+// token's row where its places end. With ADD dtable's row comes along with the token's last place.
 template <int DT, int WDT, int N, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kEmbThreads) embedding_sum_kernel(const __grid_constant__ EmbBackward a, const uint32_t* keys, const uint32_t* places) {
   pdl_enter();
-  constexpr int kBatch = ADD ? 4 : 8;
+  extern __shared__ __align__(16) uint8_t flight[];
+  using From = EmbSlice<DT, N, VEC>;
+  using To = EmbSlice<WDT, N, VEC>;
+  constexpr uint32_t kSlot = From::kBytes + (ADD ? To::kBytes : 0);
   uint64_t row, slice;
   emb_unit((uint64_t)blockIdx.x * (kEmbThreads / 32) + threadIdx.x / 32, a.across, row, slice);
-  const uint32_t span = (uint32_t)row, across = (uint32_t)slice, lane = threadIdx.x & 31;
   if (row >= a.spans) return;
-  const uint64_t c = slice * 32 * N + emb_first<N, VEC>();
-  const uint64_t p0 = (uint64_t)span * a.span, p1 = p0 + a.span < a.rows ? p0 + a.span : a.rows;
+  const uint32_t span = (uint32_t)row, lane = threadIdx.x & 31;
+  const uint64_t c0 = slice * 32 * N, c = c0 + emb_first<N, VEC>();
+  uint8_t* const mine = flight + threadIdx.x / 32 * (kEmbFlight * kSlot);
+  const uint64_t p0 = (uint64_t)span * a.span;
   const uint32_t none = (uint32_t)a.vocab;  // of the tokens that do not count, behind all others
-  // lane l has place p + l - 1 of the batch that starts at p
-  uint32_t key = none, place = 0;
-  const auto ask = [&](uint64_t p) {
-    const uint64_t mine = p + lane - 1;  // wraps for lane 0 at place 0
-    key = lane < kBatch + 2 && mine < a.rows ? keys[mine] : none;
-    place = lane > 0 && lane <= kBatch && mine < p1 ? places[mine] : 0;
+  // lane l has place p0 + l, at most 32 of them
+  const uint64_t p = p0 + lane;
+  const bool here = lane < a.span && p < a.rows;
+  const uint32_t key = here ? keys[p] : none, next = here && p + 1 < a.rows ? keys[p + 1] : none, place = here ? places[p] : 0;
+  const uint32_t before = p0 ? keys[p0 - 1] : none;
+  const uint32_t count = __popc(__ballot_sync(0xffffffffu, key != none)), ends = __ballot_sync(0xffffffffu, next != key);
+  const auto source = [&](uint32_t i) {
+    return static_cast<const char*>(a.dy) + (uint64_t)__shfl_sync(0xffffffffu, place, i) * a.dy_stride * From::es;
   };
-  ask(p0);
+  const auto target = [&](uint32_t i) {
+    return static_cast<char*>(a.dtable) + (uint64_t)__shfl_sync(0xffffffffu, key, i) * a.table_stride * To::es;
+  };
+  const auto ask = [&](uint32_t i) {
+    if (i < count) {
+      uint8_t* const slot = mine + i % kEmbFlight * kSlot;
+      From::copy(slot, source(i), c0, a.cols);
+      if (ADD && (ends >> i & 1)) To::copy(slot + From::kBytes, target(i), c0, a.cols);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (uint32_t i = 0; i < kEmbFlight; ++i) ask(i);
+  // whether the places summed now start in this span
+  bool inside = p0 == 0 || before != __shfl_sync(0xffffffffu, key, 0);
+  uint32_t head = none, tail = none;
   float sum[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) sum[k] = 0.0f;
-  // whether the places summed now start in this span
-  bool inside = p0 == 0 || __shfl_sync(0xffffffffu, key, 0) != __shfl_sync(0xffffffffu, key, 1);
-  uint32_t head = none, tail = none;
-  for (uint64_t p = p0; p < p1; p += kBatch) {
-    float x[kBatch][N], old[ADD ? kBatch : 1][N];
-    uint32_t k[kBatch + 1];
+#pragma unroll 1
+  for (uint32_t i = 0; i < count; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kEmbFlight - 1) : "memory");
+    if (!VEC) __syncwarp();
+    const uint8_t* const slot = mine + i % kEmbFlight * kSlot;
+    float x[N];
+    From::read(slot, source(i), c0, x);
 #pragma unroll
-    for (int i = 0; i <= kBatch; ++i) k[i] = __shfl_sync(0xffffffffu, key, i + 1);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint64_t from = __shfl_sync(0xffffffffu, place, i + 1);
-      const bool counts = p + i < p1 && k[i] != none;
-      emb_load<DT, N, VEC>(static_cast<const char*>(a.dy) + from * a.dy_stride * Elem<DT>::kSize, c, counts ? a.cols : 0, x[i]);
-      if constexpr (ADD) emb_old<WDT, N, VEC>(a, counts ? k[i] : 0, c, counts && k[i + 1] != k[i], old[i]);
-    }
-    ask(p + kBatch);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (p + i >= p1 || k[i] == none) break;
-#pragma unroll
-      for (int j = 0; j < N; ++j) sum[j] += x[i][j];
-      const bool ends = k[i + 1] != k[i];
-      if (!ends && p + i + 1 < p1) continue;
-      if (ends && inside) {
-        emb_finish<WDT, N, VEC, ADD>(a, k[i], c, sum, old[ADD ? i : 0]);
+    for (int k = 0; k < N; ++k) sum[k] += x[k];
+    const bool end = ends >> i & 1;
+    if (end || i + 1 == count) {
+      char* const to = target(i);
+      if (end && inside) {
+        if (ADD) To::read(slot + From::kBytes, to, c0, x);
+        emb_finish<WDT, N, VEC, ADD>(a, to, c, sum, x);
       } else {
-        float4* to = reinterpret_cast<float4*>(a.partial + (((uint64_t)span * 2 + (inside ? 1 : 0)) * a.across + across) * 32 * N + lane * N);
+        float4* left = reinterpret_cast<float4*>(a.partial + (((uint64_t)span * 2 + (inside ? 1 : 0)) * a.across + slice) * 32 * N + lane * N);
 #pragma unroll
-        for (int q = 0; q < N / 4; ++q) to[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
-        (inside ? tail : head) = k[i];
+        for (int q = 0; q < N / 4; ++q) left[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
+        (inside ? tail : head) = __shfl_sync(0xffffffffu, key, i);
       }
       inside = true;
 #pragma unroll
-      for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+      for (int k = 0; k < N; ++k) sum[k] = 0.0f;
     }
+    if (!VEC) __syncwarp();
+    ask(i + kEmbFlight);
   }
-  if (head != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, across, head, c);
-  if (tail != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, across, tail, c);
+  if (head != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, (uint32_t)slice, head);
+  if (tail != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, (uint32_t)slice, tail);
 }
 
 }  // namespace ra

@@ -90,6 +90,7 @@ __device__ __forceinline__ void ce_copy_row(void* to, const void* from, uint64_t
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kCeRowsThreads) ce_rows_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
+  pdl_next();
   constexpr int kWarps = kCeRowsThreads / 32;
   __shared__ int32_t sums[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kCeRowsThreads) ce_rows_kernel(const __grid_co
 // The weight in rows of whole 16-byte lines: a warp per row.
 __global__ void __launch_bounds__(256) ce_weight_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
+  pdl_next();
   for (uint64_t v = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32; v < a.vocab; v += (uint64_t)gridDim.x * 8)
     ce_copy_row(static_cast<uint16_t*>(const_cast<void*>(a.w)) + v * a.w_stride,
                 static_cast<const uint16_t*>(a.weight) + v * a.weight_stride, a.cols, threadIdx.x & 31);
@@ -273,13 +275,6 @@ __device__ __forceinline__ float ce_load(const void* p, uint64_t i) {
   if constexpr (DT == DT_F32) return static_cast<const float*>(p)[i];
   else return widen16<DT>(static_cast<const uint16_t*>(p)[i]);
 }
-template <int DT>
-__device__ __forceinline__ uint32_t ce_pack(float low, float high) {
-  uint32_t r;
-  if constexpr (DT == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
-  return r;
-}
 // 32 bytes at a multiple of 32: whole sectors.
 __device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
@@ -353,7 +348,7 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, floa
       float e, f;
       split(fma2(pair(x[j + 2 * q], x[j + 2 * q + 1]), slope, both), e, f);
       split(mul2(pair(exp2_approx(e), exp2_approx(f)), dd), e, f);
-      w[q] = ce_pack<DT>(e, f);
+      w[q] = round16x2<DT>(e, f);
     }
     if (there < 128) {
 #pragma unroll
@@ -409,7 +404,7 @@ __device__ __forceinline__ void ce_out_dweight(const CeTiles& t, float scale, ui
         } else {
           float u = x[j + 2 * q] * f, v = x[j + 2 * q + 1] * f;
           if (t.a.accumulate) u += widen16<WDT>(w[q] & 0xffffu), v += widen16<WDT>(w[q] >> 16);
-          w[q] = ce_pack<WDT>(u, v);
+          w[q] = round16x2<WDT>(u, v);
         }
       }
       st_sector(to + j * es, w);
@@ -478,6 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_enter();
+  pdl_next();
   const CeWork k = ce_work(t);
 
   uint32_t turn = 0;
@@ -682,7 +678,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const __grid_constant__ 
       sum = make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
     }
     uint16_t* const to = static_cast<uint16_t*>(a.dhidden) + t * a.dhidden_stride + c;
-    const uint2 w = make_uint2(ce_pack<DT>(sum.x, sum.y), ce_pack<DT>(sum.z, sum.w));
+    const uint2 w = make_uint2(round16x2<DT>(sum.x, sum.y), round16x2<DT>(sum.z, sum.w));
     if (whole && c + 4 <= a.cols) {
       *reinterpret_cast<uint2*>(to) = w;
     } else {

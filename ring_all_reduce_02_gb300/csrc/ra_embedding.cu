@@ -36,7 +36,10 @@ cudaError_t sort_one(const ra::EmbBackward& a, unsigned zeros, cudaStream_t s) {
 
 // Sorts the tokens, and clears the table beside that.
 cudaError_t sort(ra::EmbBackward& a, const ra::EmbPlan& p, bool clear, cudaStream_t s) {
-  const unsigned zeros = clear ? 304 : 0;  // two CTAs an SM
+  #ifndef EMB_ZEROS
+#define EMB_ZEROS 1216
+#endif
+  const unsigned zeros = clear ? EMB_ZEROS : 0;  // two CTAs an SM
   if (p.one) return a.rows <= 2048 ? sort_one<256, 1>(a, zeros, s) : a.rows <= 8192 ? sort_one<256, 4>(a, zeros, s) : sort_one<512, 8>(a, zeros, s);
   cudaError_t err = cudaSuccess;
   for (uint32_t pass = 0; pass < a.passes && err == cudaSuccess; ++pass) {
@@ -50,23 +53,29 @@ template <int DT, int WDT, int N, bool VEC, bool ADD>
 cudaError_t sums(const ra::EmbBackward& a, int last, cudaStream_t s) {
   const auto kernel = ra::embedding_sum_kernel<DT, WDT, N, VEC, ADD>;
   constexpr size_t smem = ra::kEmbSumSmem<DT, WDT, N, VEC, ADD>;
-  if (smem > 48 * 1024) {
+  if (smem + 1024 > 48 * 1024) {  // beside the static
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
   }
-  return ra::launch_programmatic(kernel, dim3(ctas((uint64_t)a.spans * a.across)), ra::kEmbThreads, smem, s, a, a.keys[last], a.places[last]);
+  return ra::launch_programmatic(kernel, dim3((unsigned)((uint64_t)a.spans * a.across)), ra::kEmbThreads, smem, s, a, a.keys[last], a.places[last]);
+}
+
+template <int DT, int WDT, bool VEC>
+cudaError_t backward_lanes(ra::EmbBackward& a, const ra::EmbPlan& p, bool add, cudaStream_t s) {
+  constexpr int N = kPerLane(DT);
+  if (add && a.rows <= ra::kEmbFew)
+    return ra::launch_programmatic(ra::embedding_few_kernel<DT, WDT, N, VEC>, dim3((unsigned)(a.rows * a.across)), ra::kEmbThreads, 0, s, a);
+  const cudaError_t err = sort(a, p, !add, s);
+  if (err != cudaSuccess || a.rows == 0) return err;
+  const int last = p.one ? 0 : (int)(p.passes - 1) % 2;
+  return add ? sums<DT, WDT, N, VEC, true>(a, last, s) : sums<DT, WDT, N, VEC, false>(a, last, s);
 }
 
 template <int DT, int WDT>
 cudaError_t backward(ra::EmbBackward& a, const ra::EmbPlan& p, bool add, cudaStream_t s) {
-  constexpr int N = kPerLane(DT);
-  const cudaError_t err = sort(a, p, !add, s);
-  if (err != cudaSuccess || a.rows == 0) return err;
-  const int last = p.one ? 0 : (int)(p.passes - 1) % 2;
-  const bool vec = lines(a.dy, a.dy_stride * ra::Elem<DT>::kSize) && lines(a.dtable, a.table_stride * ra::Elem<WDT>::kSize) && a.cols % N == 0;
-  return vec ? add ? sums<DT, WDT, N, true, true>(a, last, s) : sums<DT, WDT, N, true, false>(a, last, s)
-             : add ? sums<DT, WDT, N, false, true>(a, last, s)
-                   : sums<DT, WDT, N, false, false>(a, last, s);
+  const bool vec = lines(a.dy, a.dy_stride * ra::Elem<DT>::kSize) && lines(a.dtable, a.table_stride * ra::Elem<WDT>::kSize) &&
+                   a.cols % kPerLane(DT) == 0;
+  return vec ? backward_lanes<DT, WDT, true>(a, p, add, s) : backward_lanes<DT, WDT, false>(a, p, add, s);
 }
 
 }  // namespace
@@ -139,9 +148,7 @@ ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* 
   a.across = (uint32_t)p.across;
   for (int i = 0; i < 2; ++i) a.keys[i] = at(p.keys[i]), a.places[i] = at(p.places[i]);
   a.counts = at(p.counts), a.tickets = at(p.tickets), a.partial = reinterpret_cast<float*>(w + p.partial);
-  // Looking up whether a row has a token costs every clearing CTA a walk over the tokens, about 1 us for 8192 of them;
-  // writing the rows with a token twice costs their bytes. So it is looked up for rows of 2 KiB and more.
-  a.zero_bytes = (int)ws, a.zero_known = cols * ws >= 2048;
+  a.table_bytes = (int)ws;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool add = accumulate != 0;
   cudaError_t err;

@@ -70,7 +70,7 @@ __device__ __forceinline__ void emb_store(void* row, uint64_t c, uint64_t cols, 
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if constexpr (DT == DT_F32) w[k] = __float_as_uint(x[l * V + k]);
-        else w[k] = round16<DT>(x[l * V + 2 * k]) | round16<DT>(x[l * V + 2 * k + 1]) << 16;
+        else w[k] = round16x2<DT>(x[l * V + 2 * k], x[l * V + 2 * k + 1]);
       }
       if (c < cols) *reinterpret_cast<uint4*>(static_cast<char*>(row) + c * Elem<DT>::kSize + l * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -147,7 +147,7 @@ struct EmbBackward {
   uint32_t bits, passes, tiles, span, spans, across;
   uint32_t *keys[2], *places[2], *counts, *tickets;
   float* partial;  // [spans][2][across][32 * N]: of the places that come from the span before, and that go on into the next
-  int zero_bytes, zero_known;  // bytes of its elements; whether only rows without a token are cleared
+  int table_bytes;  // of dtable's elements
 };
 
 // The number that a token is sorted by: `vocab` where it does not count.
@@ -156,15 +156,12 @@ __device__ __forceinline__ uint32_t emb_key(const EmbBackward& a, uint64_t t) {
   return v < 0 || v >= a.vocab || v == a.padding ? (uint32_t)a.vocab : (uint32_t)v;
 }
 
-// Clears the table (CTA `part` of `parts`, any number of threads), or of it the rows that no token has: those with a
-// token are written by the sums. `seen`: 4096 words of shared memory.
-__device__ __forceinline__ void emb_clear(const EmbBackward& a, uint32_t part, uint32_t parts, uint32_t* seen) {
-  constexpr uint32_t kSlice = 4096 * 32;  // rows whose presence the words hold
-  const uint64_t es = (uint64_t)a.zero_bytes, width = a.cols * es, pitch = a.table_stride * es;
+// Clears the table: CTA `part` of `parts`, any number of threads.
+__device__ __forceinline__ void emb_clear(const EmbBackward& a, uint32_t part, uint32_t parts) {
+  const uint64_t es = (uint64_t)a.table_bytes, width = a.cols * es, pitch = a.table_stride * es;
   const uint64_t v0 = (uint64_t)a.vocab * part / parts, v1 = (uint64_t)a.vocab * (part + 1) / parts;
   char* const table = static_cast<char*>(a.dtable);
-  const bool lines = ((reinterpret_cast<uintptr_t>(table) | pitch | width) & 15) == 0;
-  if (!a.zero_known && pitch == width) {  // one run of bytes
+  if (pitch == width) {  // one run of bytes
     char* const from = table + v0 * pitch;
     char* const to = table + v1 * pitch;
     char* const lo = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(from) + 15) / 16 * 16);
@@ -175,29 +172,15 @@ __device__ __forceinline__ void emb_clear(const EmbBackward& a, uint32_t part, u
     for (char* b = (hi > end ? hi : end) + threadIdx.x * 2; b < to; b += blockDim.x * 2) *reinterpret_cast<uint16_t*>(b) = 0;
     return;
   }
-  for (uint64_t u = v0; u < v1; u += kSlice) {
-    const uint32_t rows = (uint32_t)(v1 - u < kSlice ? v1 - u : kSlice);
-    if (a.zero_known) {
-      for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) seen[i] = 0;
-      __syncthreads();
-#pragma unroll 8
-      for (uint64_t t = threadIdx.x; t < a.rows; t += blockDim.x) {
-        const uint64_t r = (uint64_t)emb_key(a, t) - u;
-        if (r < rows) atomicOr(&seen[r / 32], 1u << r % 32);
-      }
-      __syncthreads();
+  const bool lines = ((reinterpret_cast<uintptr_t>(table) | pitch | width) & 15) == 0;
+  const uint64_t step = lines ? 16 : es;
+  for (uint64_t v = v0 + threadIdx.x / 32; v < v1; v += blockDim.x / 32) {  // a warp per row
+    char* const row = table + v * pitch;
+    for (uint64_t b = (threadIdx.x & 31) * step; b < width; b += 32 * step) {
+      if (lines) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
+      else if (es == 4) *reinterpret_cast<uint32_t*>(row + b) = 0;
+      else *reinterpret_cast<uint16_t*>(row + b) = 0;
     }
-    for (uint32_t r = threadIdx.x / 32; r < rows; r += blockDim.x / 32) {  // a warp per row
-      if (a.zero_known && (seen[r / 32] >> r % 32 & 1)) continue;
-      char* const row = table + (u + r) * pitch;
-      const uint64_t step = lines ? 16 : es;
-      for (uint64_t b = (threadIdx.x & 31) * step; b < width; b += 32 * step) {
-        if (lines) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
-        else if (es == 4) *reinterpret_cast<uint32_t*>(row + b) = 0;
-        else *reinterpret_cast<uint16_t*>(row + b) = 0;
-      }
-    }
-    __syncthreads();
   }
 }
 
@@ -277,17 +260,15 @@ constexpr uint32_t kEmbPlaceBits = 15, kEmbCluster = 8;
 template <int THREADS, int ITEMS>
 __global__ void __cluster_dims__(kEmbCluster, 1, 1) __launch_bounds__(THREADS) embedding_sort_kernel(const __grid_constant__ EmbBackward a) {
   pdl_enter();
+  pdl_next();
   constexpr uint32_t kShare = THREADS * ITEMS;
-  __shared__ union {
-    struct {
-      EmbSort<THREADS> sort;
-      uint32_t total[256];
-      uint32_t words[kShare];
-    };
-    uint32_t seen[4096];
+  __shared__ struct {
+    EmbSort<THREADS> sort;
+    uint32_t total[256];
+    uint32_t words[kShare];
   } s;
   if (blockIdx.x >= kEmbCluster) {
-    emb_clear(a, blockIdx.x - kEmbCluster, gridDim.x - kEmbCluster, s.seen);
+    emb_clear(a, blockIdx.x - kEmbCluster, gridDim.x - kEmbCluster);
     return;
   }
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, rank = blockIdx.x, first = warp * 32 * ITEMS + lane;
@@ -366,9 +347,10 @@ __device__ __forceinline__ void emb_item(const EmbBackward& a, uint32_t pass, ui
 
 __global__ void __launch_bounds__(kEmbThreads) embedding_count_kernel(const __grid_constant__ EmbBackward a, uint32_t pass) {
   pdl_enter();
-  __shared__ uint32_t seen[4096];  // the first 256: counts of digits
+  pdl_next();
+  __shared__ uint32_t seen[256];  // of each digit
   if (blockIdx.x >= a.tiles) {
-    emb_clear(a, blockIdx.x - a.tiles, gridDim.x - a.tiles, seen);
+    emb_clear(a, blockIdx.x - a.tiles, gridDim.x - a.tiles);
     return;
   }
   if (pass == 0)
@@ -389,6 +371,7 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_count_kernel(const __gr
 
 __global__ void __launch_bounds__(kEmbThreads) embedding_scatter_kernel(const __grid_constant__ EmbBackward a, uint32_t pass) {
   pdl_enter();
+  pdl_next();
   __shared__ EmbSort<kEmbThreads> s;
   __shared__ uint32_t base[256];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -489,27 +472,30 @@ __device__ __forceinline__ void emb_finish(const EmbBackward& a, char* row, uint
   emb_store<WDT, N, VEC>(row, c, a.cols, x);
 }
 
+// The first span that holds places of the token whose places reach from before into `span`, and the last one that holds
+// some of the token whose places go on behind `span`; 32 spans at a time.
+__device__ __forceinline__ uint32_t emb_first_span(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t key) {
+  for (uint32_t first = span;; first -= 32) {
+    const uint32_t f = first - (threadIdx.x & 31);  // wraps below 0
+    const bool from = f <= first && f > 0 && keys[(uint64_t)f * a.span - 1] == key;
+    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, from));
+    if (run) return first - (run - 1);
+  }
+}
+__device__ __forceinline__ uint32_t emb_last_span(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t key) {
+  for (uint32_t last = span;; last += 32) {
+    const uint64_t next = (uint64_t)(last + (threadIdx.x & 31) + 1) * a.span;
+    const bool on = next < a.rows && keys[next] == key;
+    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, on));
+    if (run) return last + (run - 1);
+  }
+}
+
 // A token's places reach over the ends of spans `first` to `last`: adds up what they left, if this warp is the last of
 // them to have left something.
 template <int WDT, int N, bool VEC, bool ADD>
-__device__ __noinline__ void emb_join(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t across, uint32_t key) {
+__device__ __noinline__ void emb_join(const EmbBackward& a, uint32_t first, uint32_t last, uint32_t across, uint32_t key) {
   const uint32_t lane = threadIdx.x & 31;
-  uint32_t first = span, last = span;
-  // 32 spans at a time: span f goes on from the one before where the places at its start and before it have the key
-  for (bool more = true; more;) {
-    const uint32_t f = first - lane;  // wraps below 0
-    const bool from = f <= first && f > 0 && keys[(uint64_t)f * a.span - 1] == key;
-    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, from)) - 1;
-    more = run == 0xffffffffu;
-    first -= more ? 32 : run;
-  }
-  for (bool more = true; more;) {
-    const uint64_t next = (uint64_t)(last + lane + 1) * a.span;
-    const bool on = next < a.rows && keys[next] == key;
-    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, on)) - 1;
-    more = run == 0xffffffffu;
-    last += more ? 32 : run;
-  }
   __threadfence();
   __syncwarp();
   uint32_t ticket = 0;
@@ -547,88 +533,203 @@ __device__ __noinline__ void emb_join(const EmbBackward& a, const uint32_t* keys
   emb_finish<WDT, N, VEC, ADD>(a, row, c, sum, old);
 }
 
-#ifndef EMB_FLIGHT
-#define EMB_FLIGHT 8
-#endif
-constexpr uint32_t kEmbFlight = EMB_FLIGHT;  // rows that a warp has in flight
-template <int DT, int WDT, int N, bool VEC, bool ADD>
-constexpr uint32_t kEmbSumSmem = kEmbThreads / 32 * kEmbFlight * (EmbSlice<DT, N, VEC>::kBytes + (ADD ? EmbSlice<WDT, N, VEC>::kBytes : 0));
+// A few rows added to the table, in one launch without a sort: a CTA per row and slice of the columns. The first row of
+// its token has the sum of all of them, a share to each warp; the others leave. Adding the shares up goes by the warps'
+// order.
+constexpr uint32_t kEmbFew = 256;
+template <int DT, int WDT, int N, bool VEC>
+__global__ void __launch_bounds__(kEmbThreads) embedding_few_kernel(const __grid_constant__ EmbBackward a) {
+  pdl_enter();
+  constexpr uint32_t kWarps = kEmbThreads / 32;
+  static_assert(kEmbThreads == kEmbFew, "a token to each thread");
+  __shared__ uint32_t counts[kWarps], list[kEmbFew];
+  __shared__ float sums[kWarps][N][32];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, i = threadIdx.x;
+  uint64_t t, slice;
+  emb_unit(blockIdx.x, a.across, t, slice);
+  const uint32_t none = (uint32_t)a.vocab, own = emb_key(a, t), key = i < a.rows ? emb_key(a, i) : none;
+  if (own == none || __syncthreads_or(i < t && key == own)) return;
+  const uint32_t votes = __ballot_sync(0xffffffffu, key == own);
+  if (lane == 0) counts[warp] = __popc(votes);
+  __syncthreads();
+  uint32_t at = __popc(votes & ((1u << lane) - 1)), n = 0;
+  for (uint32_t w = 0; w < kWarps; ++w) {
+    if (w < warp) at += counts[w];
+    n += counts[w];
+  }
+  if (key == own) list[at] = i;
+  __syncthreads();
+  if (warp >= n) return;  // no barrier of the whole CTA below: the warps that stay are counted
+  const uint64_t c = slice * 32 * N + emb_first<N, VEC>();
+  char* const row = static_cast<char*>(a.dtable) + (uint64_t)own * a.table_stride * Elem<WDT>::kSize;
+  EmbRaw<WDT, N, VEC> old;
+  if (warp == 0) old.load(row, c, a.cols);
+  float sum[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+#pragma unroll 4
+  for (uint32_t j = warp; j < n; j += kWarps) {
+    EmbRaw<DT, N, VEC> x;
+    x.load(static_cast<const char*>(a.dy) + (uint64_t)list[j] * a.dy_stride * Elem<DT>::kSize, c, a.cols);
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum[k] += x.at(k);
+  }
+  const uint32_t warps = n < kWarps ? n : kWarps;
+  if (warp > 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) sums[warp][k][lane] = sum[k];
+  }
+  if (warps > 1) asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory");
+  if (warp > 0) return;
+  for (uint32_t w = 1; w < warps; ++w) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum[k] += sums[w][k][lane];
+  }
+  float before[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) before[k] = old.at(k);
+  emb_finish<WDT, N, VEC, true>(a, row, c, sum, before);
+}
 
-// A warp per span of sorted places and slice of the columns: adds the places' rows up in their order, and writes a
-// token's row where its places end. With ADD dtable's row comes along with the token's last place.
+// Rows that a warp has in flight, as many as let an SM hold 4 CTAs; and a partial sum of each warp beside them.
+template <bool ADD>
+constexpr uint32_t kEmbFlight = ADD ? 5 : 8;
 template <int DT, int WDT, int N, bool VEC, bool ADD>
-__global__ void __launch_bounds__(kEmbThreads) embedding_sum_kernel(const __grid_constant__ EmbBackward a, const uint32_t* keys, const uint32_t* places) {
+constexpr uint32_t kEmbSumSmem =
+    kEmbThreads / 32 * (32 * N * 4 + kEmbFlight<ADD> * (EmbSlice<DT, N, VEC>::kBytes + (ADD ? EmbSlice<WDT, N, VEC>::kBytes : 0)));
+
+// A CTA per span of sorted places and slice of the columns, a share of the span to each warp. A warp adds its places'
+// rows up in their order, and writes a token's row where its places end; with ADD dtable's row comes along with the
+// token's last place. Places that reach over the end of a warp's share are joined by the warp in whose share they start,
+// and those that reach over the span's ends by the last CTA that has some of them.
+template <int DT, int WDT, int N, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kEmbThreads, 4) embedding_sum_kernel(const __grid_constant__ EmbBackward a, const uint32_t* keys, const uint32_t* places) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t flight[];
   using From = EmbSlice<DT, N, VEC>;
   using To = EmbSlice<WDT, N, VEC>;
-  constexpr uint32_t kSlot = From::kBytes + (ADD ? To::kBytes : 0);
+  constexpr uint32_t kWarps = kEmbThreads / 32, kFlight = kEmbFlight<ADD>, kSlot = From::kBytes + (ADD ? To::kBytes : 0);
+  static_assert(kFlight * kSlot >= 32 * N * 4, "the rows' place takes a partial sum when they are through");
+  enum { HEAD = 1, HEAD_ENDS = 2, TAIL = 4 };  // places that come from the share before, and end here; that go on
+  __shared__ uint32_t left[kWarps], keys_left[kWarps], first_span, last_span;
   uint64_t row, slice;
-  emb_unit((uint64_t)blockIdx.x * (kEmbThreads / 32) + threadIdx.x / 32, a.across, row, slice);
-  if (row >= a.spans) return;
-  const uint32_t span = (uint32_t)row, lane = threadIdx.x & 31;
+  emb_unit(blockIdx.x, a.across, row, slice);
+  const uint32_t span = (uint32_t)row, lane = threadIdx.x & 31, warp = threadIdx.x / 32, share = a.span / kWarps;
   const uint64_t c0 = slice * 32 * N, c = c0 + emb_first<N, VEC>();
-  uint8_t* const mine = flight + threadIdx.x / 32 * (kEmbFlight * kSlot);
-  const uint64_t p0 = (uint64_t)span * a.span;
+  float4* const heads = reinterpret_cast<float4*>(flight) + lane * (N / 4);  // of warp w: + w * 8 N float4s
+  uint8_t* const rows = flight + kWarps * 32 * N * 4;
+  uint8_t* const mine = rows + warp * (kFlight * kSlot);
+  const auto tails = [&](uint32_t w) { return reinterpret_cast<float4*>(rows + w * (kFlight * kSlot)) + lane * (N / 4); };
+  const auto put = [&](float4* to, const float (&x)[N]) {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) to[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+  };
+  const auto add = [&](const float4* from, float (&x)[N]) {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) x[4 * q] += from[q].x, x[4 * q + 1] += from[q].y, x[4 * q + 2] += from[q].z, x[4 * q + 3] += from[q].w;
+  };
+  const uint64_t p0 = (uint64_t)span * a.span + warp * share;
   const uint32_t none = (uint32_t)a.vocab;  // of the tokens that do not count, behind all others
   // lane l has place p0 + l, at most 32 of them
   const uint64_t p = p0 + lane;
-  const bool here = lane < a.span && p < a.rows;
+  const bool here = lane < share && p < a.rows;
   const uint32_t key = here ? keys[p] : none, next = here && p + 1 < a.rows ? keys[p + 1] : none, place = here ? places[p] : 0;
-  const uint32_t before = p0 ? keys[p0 - 1] : none;
+  const uint32_t before = p0 && p0 <= a.rows ? keys[p0 - 1] : none;
   const uint32_t count = __popc(__ballot_sync(0xffffffffu, key != none)), ends = __ballot_sync(0xffffffffu, next != key);
-  const auto source = [&](uint32_t i) {
-    return static_cast<const char*>(a.dy) + (uint64_t)__shfl_sync(0xffffffffu, place, i) * a.dy_stride * From::es;
-  };
-  const auto target = [&](uint32_t i) {
-    return static_cast<char*>(a.dtable) + (uint64_t)__shfl_sync(0xffffffffu, key, i) * a.table_stride * To::es;
-  };
+  // the lane's place's rows, handed to all lanes when it is their turn
+  const uint64_t my_source = reinterpret_cast<uint64_t>(a.dy) + (uint64_t)place * a.dy_stride * From::es;
+  const uint64_t my_target = reinterpret_cast<uint64_t>(a.dtable) + (uint64_t)key * a.table_stride * To::es;
+  const auto source = [&](uint32_t i) { return reinterpret_cast<const void*>(__shfl_sync(0xffffffffu, my_source, i)); };
+  const auto target = [&](uint32_t i) { return reinterpret_cast<char*>(__shfl_sync(0xffffffffu, my_target, i)); };
   const auto ask = [&](uint32_t i) {
     if (i < count) {
-      uint8_t* const slot = mine + i % kEmbFlight * kSlot;
+      uint8_t* const slot = mine + i % kFlight * kSlot;
       From::copy(slot, source(i), c0, a.cols);
       if (ADD && (ends >> i & 1)) To::copy(slot + From::kBytes, target(i), c0, a.cols);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll 1
-  for (uint32_t i = 0; i < kEmbFlight; ++i) ask(i);
-  // whether the places summed now start in this span
-  bool inside = p0 == 0 || before != __shfl_sync(0xffffffffu, key, 0);
-  uint32_t head = none, tail = none;
-  float sum[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) sum[k] = 0.0f;
-#pragma unroll 1
-  for (uint32_t i = 0; i < count; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kEmbFlight - 1) : "memory");
-    if (!VEC) __syncwarp();
-    const uint8_t* const slot = mine + i % kEmbFlight * kSlot;
-    float x[N];
-    From::read(slot, source(i), c0, x);
-#pragma unroll
-    for (int k = 0; k < N; ++k) sum[k] += x[k];
-    const bool end = ends >> i & 1;
-    if (end || i + 1 == count) {
-      char* const to = target(i);
-      if (end && inside) {
-        if (ADD) To::read(slot + From::kBytes, to, c0, x);
-        emb_finish<WDT, N, VEC, ADD>(a, to, c, sum, x);
-      } else {
-        float4* left = reinterpret_cast<float4*>(a.partial + (((uint64_t)span * 2 + (inside ? 1 : 0)) * a.across + slice) * 32 * N + lane * N);
-#pragma unroll
-        for (int q = 0; q < N / 4; ++q) left[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
-        (inside ? tail : head) = __shfl_sync(0xffffffffu, key, i);
-      }
-      inside = true;
-#pragma unroll
-      for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+  for (uint32_t i = 0; i < kFlight; ++i) ask(i);
+  uint32_t what = 0;
+  if (count) {
+    const uint32_t key0 = __shfl_sync(0xffffffffu, key, 0), key1 = __shfl_sync(0xffffffffu, key, count - 1);
+    bool inside = p0 == 0 || before != key0;  // whether the places summed now start in this share
+    // the spans over which the first and the last places reach, asked for while the rows are on their way
+    if (warp == 0 && !inside) {
+      const uint32_t f = emb_first_span(a, keys, span, key0);
+      if (lane == 0) first_span = f;
     }
-    if (!VEC) __syncwarp();
-    ask(i + kEmbFlight);
+    if (warp == kWarps - 1 && count == share && !(ends >> (count - 1) & 1)) {
+      const uint32_t l = emb_last_span(a, keys, span, key1);
+      if (lane == 0) last_span = l;
+    }
+    float sum[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+#pragma unroll 1
+    for (uint32_t i = 0; i < count; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kFlight - 1) : "memory");
+      if (!VEC) __syncwarp();
+      const uint8_t* const slot = mine + i % kFlight * kSlot;
+      float x[N];
+      From::read(slot, VEC ? nullptr : source(i), c0, x);
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum[k] += x[k];
+      if (ends >> i & 1) {
+        if (inside) {
+          char* const to = target(i);
+          if (ADD) To::read(slot + From::kBytes, to, c0, x);
+          emb_finish<WDT, N, VEC, ADD>(a, to, c, sum, x);
+        } else {
+          put(heads + warp * (8 * N), sum);
+          what = HEAD | HEAD_ENDS;
+        }
+        inside = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+      }
+      if (!VEC) __syncwarp();
+      ask(i + kFlight);
+    }
+    if (!(ends >> (count - 1) & 1)) {  // the last places go on
+      put(inside ? tails(warp) : heads + warp * (8 * N), sum);
+      what |= inside ? TAIL : HEAD;
+    }
+    if (lane == 0) keys_left[warp] = what & TAIL ? key1 : key0;
   }
-  if (head != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, (uint32_t)slice, head);
-  if (tail != none) emb_join<WDT, N, VEC, ADD>(a, keys, span, (uint32_t)slice, tail);
+  if (lane == 0) left[warp] = what;
+  __syncthreads();
+  // from share to share: what starts in this one, and in the first also what comes from the span before
+  for (uint32_t from_before = 0; from_before < 2; ++from_before) {
+    if (from_before ? warp != 0 || !(left[0] & HEAD) : !(what & TAIL)) continue;
+    float sum[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+    uint32_t w = from_before ? 0 : warp + 1, token = keys_left[warp];
+    if (from_before) {
+      if (what & TAIL) token = __shfl_sync(0xffffffffu, key, 0);
+    } else {
+      add(tails(warp), sum);
+    }
+    bool end = false;
+    for (; w < kWarps && !end; ++w) {
+      add(heads + w * (8 * N), sum);
+      end = left[w] & HEAD_ENDS;
+    }
+    if (end && !from_before) {
+      char* const to = static_cast<char*>(a.dtable) + (uint64_t)token * a.table_stride * To::es;
+      float old[N];
+      EmbRaw<WDT, N, VEC> raw;
+      if (ADD) raw.load(to, c, a.cols);
+#pragma unroll
+      for (int k = 0; k < N; ++k) old[k] = ADD ? raw.at(k) : 0.0f;
+      emb_finish<WDT, N, VEC, ADD>(a, to, c, sum, old);
+    } else {
+      put(reinterpret_cast<float4*>(a.partial + (((uint64_t)span * 2 + (from_before ? 0 : 1)) * a.across + slice) * 32 * N + lane * N), sum);
+      emb_join<WDT, N, VEC, ADD>(a, from_before ? first_span : span, end ? span : last_span, (uint32_t)slice, token);
+    }
+  }
 }
 
 }  // namespace ra

@@ -8,14 +8,14 @@ namespace ra {
 constexpr uint64_t kEmbOneSort = 32768;      // tokens that a cluster sorts, at most: their places take 15 bits of a word
 constexpr uint64_t kEmbOneVocab = 1u << 17;  // and their numbers, or `vocab` for none, the other 17
 constexpr uint64_t kEmbSortTile = 4096;      // tokens of a CTA where there are more
-constexpr uint64_t kEmbColumns = 256;        // of a warp's sums, at most
+constexpr uint64_t kEmbSumWarps = 8;         // of a CTA that adds up
 
 struct EmbPlan {
   bool one;              // a cluster sorts
   uint32_t bits, passes; // of a digit, and digits of a number
   uint64_t tiles;        // CTAs of a sorting pass (not one)
-  uint64_t span, spans;  // sorted places that a warp adds up, and how many such spans there are
-  uint64_t across;       // warps side by side on a row
+  uint64_t span, spans;  // sorted places that a CTA adds up, a share to each warp, and how many such spans there are
+  uint64_t across;       // CTAs side by side on a row
   uint64_t keys[2], places[2], counts, tickets, partial;  // in bytes from the scratch's start
   uint64_t bytes;
 };
@@ -30,15 +30,10 @@ inline EmbPlan emb_plan(uint64_t rows, uint64_t cols, uint64_t vocab, uint64_t p
   p.bits = (bits + p.passes - 1) / p.passes;
   p.tiles = (rows + kEmbSortTile - 1) / kEmbSortTile;
   p.across = (cols + 32 * per_lane - 1) / (32 * per_lane);
-  // short spans where they fill the device once, longer ones where there are more: a span's ends cost it a partial sum
-#ifndef EMB_LEAST
-#define EMB_LEAST 8
-#endif
-#ifndef EMB_FILL
-#define EMB_FILL 64
-#endif
-  p.span = EMB_LEAST;
-  while (p.span < 32 && (rows + p.span - 1) / p.span * p.across > 152 * EMB_FILL) p.span *= 2;
+  // short spans where they fill the device once (4 CTAs an SM), longer ones where there are more: a span's ends cost it
+  // a partial sum
+  p.span = kEmbSumWarps * 8;
+  while (p.span < kEmbSumWarps * 32 && (rows + p.span - 1) / p.span * p.across > 152 * 4) p.span *= 2;
   p.spans = (rows + p.span - 1) / p.span;
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes_) {

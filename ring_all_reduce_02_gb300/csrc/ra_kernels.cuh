@@ -84,6 +84,14 @@ __device__ __forceinline__ void pdl_enter() {
 #endif
 }
 
+// Lets the next launch on the stream be placed as soon as every CTA of this one has come here. For the short first
+// kernels of a call, whose successor is the call's own and finds room beside them.
+__device__ __forceinline__ void pdl_next() {
+#if RA_PDL
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#endif
+}
+
 // Launch `kernel` on `s`, as a programmatic dependent launch when RA_PDL is
 // set; returns the launch error (and consumes it).
 template <typename... P, typename... A>

@@ -67,6 +67,15 @@ __device__ __forceinline__ uint32_t round16(float f) {
   }
 }
 
+// Two at once: `low` into the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t round16x2(float low, float high) {
+  uint32_t r;
+  if constexpr (DT == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
+  return r;
+}
+
 template <int DT, bool IS_MAX>
 __device__ __forceinline__ uint32_t minmax16(uint32_t a, uint32_t b) {
   const float fa = widen16<DT>(a), fb = widen16<DT>(b);

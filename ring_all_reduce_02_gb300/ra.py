@@ -666,55 +666,61 @@ def ra_adamw(tensors: AdamwTensors, lr: float, step: int, beta1: float = 0.9, be
 # ---- embedding, cross entropy -----------------------------------------------
 
 
-def _check_matrices(what: str, device: int, cols: int, **matrices) -> None:
-    """Raises for the first of ``name=(tensor, rows, dtype)`` that is not a matrix of those rows on ``device``, with
-    contiguous rows of ``cols`` (None: there is none)."""
+def _is_matrix(t, shape, dtype, device: int) -> bool:
+    """A matrix of that shape with contiguous rows on CUDA device ``device``, or None."""
+    return t is None or (t.get_device() == device and t.dtype is dtype and t.shape == shape
+                         and (t.is_contiguous() or _rows_contiguous(t)))
+
+
+def _is_index(t, rows: int, device: int) -> bool:
+    return t.get_device() == device and t.numel() == rows and t.is_contiguous()
+
+
+def _pitch(t, cols: int) -> int:
+    """Elements from row to row of a matrix that _is_matrix has passed."""
+    return cols if t.is_contiguous() else _row_stride(t, cols)
+
+
+def _refuse_matrices(what: str, device: int, cols: int, index=None, workspace=None, **matrices) -> None:
+    """Raises for the first argument that the checks above did not pass: ``name=(tensor, rows, dtype)``, ``index`` =
+    (name, tensor, rows), ``workspace``."""
     for name, (t, rows, dtype) in matrices.items():
-        if t is None:
-            continue
-        if not (t.get_device() == device and device >= 0 and len(t.shape) == 2 and tuple(t.shape) == (rows, cols)
-                and t.dtype is dtype and _rows_contiguous(t)):
+        if t is not None and (device < 0 or len(t.shape) != 2 or not _is_matrix(t, (rows, cols), dtype, device)):
             raise ValueError(f"{what}: {name} must be a CUDA tensor [{rows}, {cols}] of {dtype} with contiguous rows, "
                              f"on cuda:{device}")
-
-
-def _index_bytes(t, rows: int, device: int, what: str, name: str) -> int:
-    """Bytes of each of the ``rows`` tokens or targets in t."""
-    size = (_Torch.index_bytes or _Torch.load().index_bytes).get(t.dtype)
-    if size is None:
-        raise TypeError(f"{what}: {name} must be int32 or int64, not {t.dtype}")
-    if not (t.get_device() == device and t.numel() == rows and t.is_contiguous()):
+    name, t, rows = index
+    if not _is_index(t, rows, device):
         raise ValueError(f"{what}: {name} must be a contiguous CUDA tensor of {rows} elements, on cuda:{device}")
-    return size
-
-
-def _scratch(t, device: int, what: str):
-    """(address, bytes) of a workspace."""
-    if t is None or not (t.get_device() == device and t.is_contiguous()):
+    if workspace is None or not (workspace.get_device() == device and workspace.is_contiguous()):
         raise ValueError(f"{what}: workspace must be a contiguous CUDA tensor, on cuda:{device}")
-    return t.data_ptr(), t.nbytes
 
 
-def _shape2(t, what: str, name: str):
-    if len(t.shape) != 2:
-        raise ValueError(f"{what}: {name} must be a CUDA tensor of two dimensions")
-    return t.shape
+def _refuse_types(what: str, index_name: str, index, *tensors) -> None:
+    if index.dtype not in _Torch.index_bytes:
+        raise TypeError(f"{what}: {index_name} must be int32 or int64, not {index.dtype}")
+    raise TypeError(f"{what}: unsupported dtype {', '.join(str(t.dtype) for t in tensors if t is not None)}")
 
 
 def ra_embedding_forward(table, tokens, out, scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
     """out[t] = scale * table[tokens[t]] (added to what out holds with ``accumulate``): table [vocab, cols], tokens
     [rows] int32 or int64, out [rows, cols] of the table's type. A token outside the vocabulary makes its row NaN."""
-    what = "ra_embedding_forward"
-    vocab, cols = _shape2(table, what, "table")
-    rows, device = tokens.numel(), table.get_device()
-    dtype = _float_code(table, what)
-    _check_matrices(what, device, cols, table=(table, vocab, table.dtype), out=(out, rows, table.dtype))
-    size = _index_bytes(tokens, rows, device, what, "tokens")
+    codes = _Torch.codes or _Torch.load().codes
+    if len(table.shape) != 2:
+        raise ValueError("ra_embedding_forward: table must be a CUDA tensor of two dimensions")
+    vocab, cols = table.shape
+    rows, device, dtype = tokens.numel(), table.get_device(), table.dtype
+    code, size = codes.get(dtype), _Torch.index_bytes.get(tokens.dtype)
+    if code is None or size is None:
+        _refuse_types("ra_embedding_forward", "tokens", tokens, table)
+    if not (device >= 0 and _is_matrix(table, (vocab, cols), dtype, device) and _is_matrix(out, (rows, cols), dtype, device)
+            and _is_index(tokens, rows, device)):
+        _refuse_matrices("ra_embedding_forward", device, cols, index=("tokens", tokens, rows), workspace=table,
+                         table=(table, vocab, dtype), out=(out, rows, dtype))
     st = (_lib or lib()).ra_embedding_forward(
-        table.data_ptr(), _row_stride(table, cols), tokens.data_ptr(), size, out.data_ptr(), _row_stride(out, cols),
-        accumulate, rows, cols, vocab, scale, dtype, _stream_on(device, stream, what))
+        table.data_ptr(), _pitch(table, cols), tokens.data_ptr(), size, out.data_ptr(), _pitch(out, cols), accumulate, rows,
+        cols, vocab, scale, code, _stream_on(device, stream, "ra_embedding_forward"))
     if st:
-        raise RaError(st, what)
+        raise RaError(st, "ra_embedding_forward")
 
 
 def ra_embedding_workspace(rows: int, cols: int, vocab: int) -> int:
@@ -727,26 +733,33 @@ def ra_embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bo
     """dtable[v] = scale * the sum of dy[t] over the t with tokens[t] == v (added to what dtable holds with
     ``accumulate``): dy [rows, cols], dtable [vocab, cols] of dy's type or float32. Tokens equal to ``padding`` add
     nothing. ``workspace``: a contiguous CUDA tensor of ra_embedding_workspace(rows, cols, vocab) bytes."""
-    what = "ra_embedding_backward"
-    vocab, cols = _shape2(dtable, what, "dtable")
-    rows, device = tokens.numel(), dtable.get_device()
-    dtype, table_dtype = _float_code(dy, what), _float_code(dtable, what)
-    _check_matrices(what, device, cols, dy=(dy, rows, dy.dtype), dtable=(dtable, vocab, dtable.dtype))
-    size = _index_bytes(tokens, rows, device, what, "tokens")
-    scratch, scratch_bytes = _scratch(workspace, device, what)
+    codes = _Torch.codes or _Torch.load().codes
+    if len(dtable.shape) != 2:
+        raise ValueError("ra_embedding_backward: dtable must be a CUDA tensor of two dimensions")
+    vocab, cols = dtable.shape
+    rows, device, dtype, tdtype = tokens.numel(), dtable.get_device(), dy.dtype, dtable.dtype
+    code, tcode, size = codes.get(dtype), codes.get(tdtype), _Torch.index_bytes.get(tokens.dtype)
+    if code is None or tcode is None or size is None:
+        _refuse_types("ra_embedding_backward", "tokens", tokens, dy, dtable)
+    if not (device >= 0 and _is_matrix(dy, (rows, cols), dtype, device) and _is_matrix(dtable, (vocab, cols), tdtype, device)
+            and _is_index(tokens, rows, device) and workspace is not None and workspace.get_device() == device
+            and workspace.is_contiguous()):
+        _refuse_matrices("ra_embedding_backward", device, cols, index=("tokens", tokens, rows), workspace=workspace,
+                         dy=(dy, rows, dtype), dtable=(dtable, vocab, tdtype))
     st = (_lib or lib()).ra_embedding_backward(
-        dy.data_ptr(), _row_stride(dy, cols), tokens.data_ptr(), size, -1 if padding is None else padding,
-        dtable.data_ptr(), _row_stride(dtable, cols), accumulate, rows, cols, vocab, scale, dtype, table_dtype, scratch,
-        scratch_bytes, _stream_on(device, stream, what))
+        dy.data_ptr(), _pitch(dy, cols), tokens.data_ptr(), size, -1 if padding is None else padding, dtable.data_ptr(),
+        _pitch(dtable, cols), accumulate, rows, cols, vocab, scale, code, tcode, workspace.data_ptr(), workspace.nbytes,
+        _stream_on(device, stream, "ra_embedding_backward"))
     if st:
-        raise RaError(st, what)
+        raise RaError(st, "ra_embedding_backward")
 
 
 def ra_cross_entropy_workspace(hidden, weight, backward: bool = False) -> int:
     """Bytes of workspace ra_cross_entropy_forward (or ra_cross_entropy_backward) needs for these tensors."""
-    vocab, cols = _shape2(weight, "ra_cross_entropy_workspace", "weight")
-    rows = _shape2(hidden, "ra_cross_entropy_workspace", "hidden")[0]
-    return lib().ra_cross_entropy_workspace(weight.data_ptr(), _row_stride(weight, cols), rows, cols, vocab,
+    if len(hidden.shape) != 2 or len(weight.shape) != 2:
+        raise ValueError("ra_cross_entropy_workspace: hidden and weight must be tensors of two dimensions")
+    vocab, cols = weight.shape
+    return lib().ra_cross_entropy_workspace(weight.data_ptr(), _row_stride(weight, cols), hidden.shape[0], cols, vocab,
                                             _float_code(weight, "ra_cross_entropy_workspace"), backward)
 
 
@@ -756,19 +769,26 @@ def ra_cross_entropy_forward(hidden, weight, targets, loss, lse, ignore: int = -
     bfloat16): loss and lse [rows] float32, 0 where the target (int32 or int64) is ``ignore``; lse is kept for the
     backward pass. ``workspace``: a contiguous CUDA tensor of ra_cross_entropy_workspace(hidden, weight) bytes."""
     what = "ra_cross_entropy_forward"
-    rows, cols = _shape2(hidden, what, "hidden")
-    vocab = _shape2(weight, what, "weight")[0]
-    device, dtype = hidden.get_device(), _float_code(hidden, what)
-    _check_matrices(what, device, cols, hidden=(hidden, rows, hidden.dtype), weight=(weight, vocab, hidden.dtype))
-    size = _index_bytes(targets, rows, device, what, "targets")
-    if loss is None or lse is None:
-        raise ValueError(f"{what}: loss and lse are needed")
-    f32 = _Torch.f32
-    _check_vectors(what, device, loss=(loss, rows, f32), lse=(lse, rows, f32))
-    scratch, scratch_bytes = _scratch(workspace, device, what)
+    codes = _Torch.codes or _Torch.load().codes
+    if len(hidden.shape) != 2 or len(weight.shape) != 2:
+        raise ValueError(f"{what}: hidden and weight must be CUDA tensors of two dimensions")
+    rows, cols = hidden.shape
+    vocab, device, dtype, f32 = weight.shape[0], hidden.get_device(), hidden.dtype, _Torch.f32
+    code, size = codes.get(dtype), _Torch.index_bytes.get(targets.dtype)
+    if code is None or size is None:
+        _refuse_types(what, "targets", targets, hidden)
+    if not (device >= 0 and _is_matrix(hidden, (rows, cols), dtype, device) and _is_matrix(weight, (vocab, cols), dtype, device)
+            and _is_index(targets, rows, device) and loss is not None and lse is not None and workspace is not None
+            and _is_vector(loss, rows, f32, device) and _is_vector(lse, rows, f32, device)
+            and workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse_matrices(what, device, cols, index=("targets", targets, rows), workspace=workspace,
+                         hidden=(hidden, rows, dtype), weight=(weight, vocab, dtype))
+        if loss is None or lse is None:
+            raise ValueError(f"{what}: loss and lse are needed")
+        _check_vectors(what, device, loss=(loss, rows, f32), lse=(lse, rows, f32))
     st = (_lib or lib()).ra_cross_entropy_forward(
-        hidden.data_ptr(), _row_stride(hidden, cols), weight.data_ptr(), _row_stride(weight, cols), targets.data_ptr(),
-        size, ignore, loss.data_ptr(), lse.data_ptr(), rows, cols, vocab, dtype, scratch, scratch_bytes,
+        hidden.data_ptr(), _pitch(hidden, cols), weight.data_ptr(), _pitch(weight, cols), targets.data_ptr(), size, ignore,
+        loss.data_ptr(), lse.data_ptr(), rows, cols, vocab, code, workspace.data_ptr(), workspace.nbytes,
         _stream_on(device, stream, what))
     if st:
         raise RaError(st, what)
@@ -781,24 +801,30 @@ def ra_cross_entropy_backward(hidden, weight, targets, lse, dloss=None, dhidden=
     dloss: [rows] float32, the gradient of each row's loss (None: ones). ``workspace``: a contiguous CUDA tensor of
     ra_cross_entropy_workspace(hidden, weight, backward=True) bytes."""
     what = "ra_cross_entropy_backward"
-    rows, cols = _shape2(hidden, what, "hidden")
-    vocab = _shape2(weight, what, "weight")[0]
-    device, dtype = hidden.get_device(), _float_code(hidden, what)
-    wdtype = hidden.dtype if dweight is None else dweight.dtype
-    wcode = dtype if dweight is None else _float_code(dweight, what)
-    _check_matrices(what, device, cols, hidden=(hidden, rows, hidden.dtype), weight=(weight, vocab, hidden.dtype),
-                    dhidden=(dhidden, rows, hidden.dtype), dweight=(dweight, vocab, wdtype))
-    size = _index_bytes(targets, rows, device, what, "targets")
-    if lse is None:
-        raise ValueError(f"{what}: lse is needed, as ra_cross_entropy_forward stored it")
-    f32 = _Torch.f32
-    _check_vectors(what, device, lse=(lse, rows, f32), dloss=(dloss, rows, f32))
-    scratch, scratch_bytes = _scratch(workspace, device, what)
+    codes = _Torch.codes or _Torch.load().codes
+    if len(hidden.shape) != 2 or len(weight.shape) != 2:
+        raise ValueError(f"{what}: hidden and weight must be CUDA tensors of two dimensions")
+    rows, cols = hidden.shape
+    vocab, device, dtype, f32 = weight.shape[0], hidden.get_device(), hidden.dtype, _Torch.f32
+    wdtype = dtype if dweight is None else dweight.dtype
+    code, wcode, size = codes.get(dtype), codes.get(wdtype), _Torch.index_bytes.get(targets.dtype)
+    if code is None or wcode is None or size is None:
+        _refuse_types(what, "targets", targets, hidden, dweight)
+    if not (device >= 0 and _is_matrix(hidden, (rows, cols), dtype, device) and _is_matrix(weight, (vocab, cols), dtype, device)
+            and _is_matrix(dhidden, (rows, cols), dtype, device) and _is_matrix(dweight, (vocab, cols), wdtype, device)
+            and _is_index(targets, rows, device) and lse is not None and workspace is not None
+            and _is_vector(lse, rows, f32, device) and _is_vector(dloss, rows, f32, device)
+            and workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse_matrices(what, device, cols, index=("targets", targets, rows), workspace=workspace,
+                         hidden=(hidden, rows, dtype), weight=(weight, vocab, dtype), dhidden=(dhidden, rows, dtype),
+                         dweight=(dweight, vocab, wdtype))
+        if lse is None:
+            raise ValueError(f"{what}: lse is needed, as ra_cross_entropy_forward stored it")
+        _check_vectors(what, device, lse=(lse, rows, f32), dloss=(dloss, rows, f32))
     st = (_lib or lib()).ra_cross_entropy_backward(
-        hidden.data_ptr(), _row_stride(hidden, cols), weight.data_ptr(), _row_stride(weight, cols), targets.data_ptr(),
-        size, ignore, lse.data_ptr(), _address(dloss), _address(dhidden),
-        cols if dhidden is None else _row_stride(dhidden, cols), _address(dweight),
-        cols if dweight is None else _row_stride(dweight, cols), accumulate, rows, cols, vocab, dtype, wcode, scratch,
-        scratch_bytes, _stream_on(device, stream, what))
+        hidden.data_ptr(), _pitch(hidden, cols), weight.data_ptr(), _pitch(weight, cols), targets.data_ptr(), size, ignore,
+        lse.data_ptr(), _address(dloss), _address(dhidden), cols if dhidden is None else _pitch(dhidden, cols),
+        _address(dweight), cols if dweight is None else _pitch(dweight, cols), accumulate, rows, cols, vocab, code, wcode,
+        workspace.data_ptr(), workspace.nbytes, _stream_on(device, stream, what))
     if st:
         raise RaError(st, what)

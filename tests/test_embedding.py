@@ -95,7 +95,7 @@ def check_backward(ra, dy, tokens, dtable, scale, accumulate, padding=None, work
         assert torch.equal(dtable.double()[untouched], old[untouched])
 
 
-SHAPES = [(1, 1, 1), (1, 1024, 50), (2, 3, 2), (5, 31, 7), (33, 64, 100), (64, 33, 3), (100, 100, 1000), (257, 128, 64),
+SHAPES = [(1, 1, 1), (1, 1024, 50), (2, 3, 2), (5, 31, 7), (33, 64, 100), (64, 33, 3), (100, 100, 1000), (255, 72, 40), (256, 264, 30), (257, 128, 64),
           (1000, 72, 5000), (1025, 257, 300), (3000, 8, 40), (4099, 96, 700), (9001, 40, 50257), (20000, 16, 11)]
 
 
@@ -114,7 +114,7 @@ def test_forward_and_backward(ra, rows, cols, vocab, dtype, index):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["one", "ends", "descending"])
-@pytest.mark.parametrize("rows,cols,vocab", [(1, 64, 9), (31, 40, 1), (300, 65, 2), (5000, 64, 333), (40000, 24, 50257), (70001, 17, 9)])
+@pytest.mark.parametrize("rows,cols,vocab", [(1, 64, 9), (31, 40, 1), (256, 72, 3), (300, 65, 2), (5000, 64, 333), (40000, 24, 50257), (70001, 17, 9)])
 def test_orders_and_repeats(ra, rows, cols, vocab, kind):
     gpu()
     gen = torch.Generator().manual_seed(rows + cols)

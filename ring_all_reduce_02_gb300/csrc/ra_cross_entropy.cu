@@ -37,8 +37,10 @@ cudaError_t rows_and_operands(const CeArgs& a, cudaStream_t s) {
   return err;
 }
 
-// A tensor map of a [rows][cols] matrix of 16-bit elements, in boxes of 64 x 64 with swizzled rows.
-cudaError_t encode(CUtensorMap* map, int dtype, const void* p, uint64_t cols, uint64_t rows, uint64_t stride) {
+// Tensor maps of a [rows][cols] matrix of 16-bit elements with swizzled rows of 64: in boxes of 64 columns and `high`
+// rows, or (groups) of 64 rows and two groups of 64 columns, one behind the other. Columns are whole groups then.
+cudaError_t encode(CUtensorMap* map, int dtype, const void* p, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t high,
+                   bool groups = false) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -46,12 +48,18 @@ cudaError_t encode(CUtensorMap* map, int dtype, const void* p, uint64_t cols, ui
     return err == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
   }();
   if (fn == nullptr) return cudaErrorInitializationError;
-  const cuuint64_t size[2] = {cols, rows}, strides[1] = {stride * 2};
-  const cuuint32_t box[2] = {64, 64}, steps[2] = {1, 1};
-  const CUresult r = fn(map, dtype == RA_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+  const cuuint64_t size[3] = {groups ? 64 : cols, rows, cols / 64}, strides[2] = {stride * 2, 128};
+  const cuuint32_t box[3] = {64, high, 2}, steps[3] = {1, 1, 1};
+  const CUresult r = fn(map, dtype == RA_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 3 : 2,
                         const_cast<void*>(p), size, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// The maps of both passes.
+cudaError_t encode_logits(ra::CeTiles& t, int dtype) {
+  const CeArgs& a = t.a;
+  const cudaError_t err = encode(&t.h, dtype, a.h, a.cols_pad, a.rows_pad, a.cols_pad, a.rows <= ra::kCeFew ? 64 : 128);
+  return err != cudaSuccess ? err : encode(&t.w, dtype, a.w, a.cols, a.vocab, a.w_stride, 128);
 }
 
 // Every SM has a CTA at most; all rows are taken to count.
@@ -67,9 +75,9 @@ template <int DT>
 cudaError_t forward(const CeArgs& a, cudaStream_t s) {
   ra::CeTiles t = {};
   t.a = a, t.w_out = a.vocab, t.counter = a.counters;
-  cudaError_t err = encode(&t.h, DT, a.h, a.cols_pad, a.rows_pad, a.cols_pad);
-  if (err == cudaSuccess) err = encode(&t.w, DT, a.w, a.cols, a.vocab, a.w_stride);
+  cudaError_t err = encode_logits(t, DT);
   if (err == cudaSuccess) err = rows_and_operands<false>(a, s);
+  t.early = a.rows <= ra::kCeFew && a.w == a.weight;
   if (err == cudaSuccess) err = launch_tiles<DT, DT, false>(t, a.rows_pad / 256 * (a.slots / 2), s);
   if (err != cudaSuccess) return err;
   // few rows: a CTA to each
@@ -81,16 +89,25 @@ template <int DT, int WDT>
 cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream_t s) {
   ra::CeTiles t = {};
   t.a = a;
-  CUtensorMap g[2];
-  cudaError_t err = encode(&t.h, DT, a.h, a.cols_pad, a.rows_pad, a.cols_pad);
-  if (err == cudaSuccess) err = encode(&t.w, DT, a.w, a.cols, a.vocab, a.w_stride);
-  for (int i = 0; i < 2 && err == cudaSuccess; ++i) err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece);
+  CUtensorMap g[2], g_own[2];
+  t.w_groups = a.w != a.weight || a.cols % 64 == 0;
+  cudaError_t err = encode_logits(t, DT);
+  if (err == cudaSuccess) err = encode(&t.h_own, DT, a.h, a.cols_pad, a.rows_pad, a.cols_pad, 64, true);
+  if (err == cudaSuccess)
+    err = t.w_groups ? encode(&t.w_own, DT, a.w, (a.cols + 63) / 64 * 64, a.vocab, a.w_stride, 64, true)
+                     : encode(&t.w_own, DT, a.w, a.cols, a.vocab, a.w_stride, 64);
+  for (uint64_t i = 0; i < 2 && i < a.pieces && err == cudaSuccess; ++i) {
+    err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 128);
+    if (err == cudaSuccess) err = encode(&g_own[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 64, true);
+  }
   if (err == cudaSuccess) err = rows_and_operands<true>(a, s);
   const auto width = [&](uint64_t piece) { return piece >= a.pieces ? 0 : a.vocab - piece * a.piece < a.piece ? a.vocab - piece * a.piece : a.piece; };
   for (uint64_t i = 0; i <= a.pieces && err == cudaSuccess; ++i) {  // piece i of g, and the gradients of the one before
     t.v_out = i * a.piece, t.w_out = width(i), t.g_out = scratch + p.g[i % 2];
-    t.v_sum = i ? (i - 1) * a.piece : 0, t.w_sum = i ? width(i - 1) : 0, t.g = g[(i + 1) % 2];
+    t.v_sum = i ? (i - 1) * a.piece : 0, t.w_sum = i ? width(i - 1) : 0;
+    if (i) t.g = g[(i + 1) % 2], t.g_own = g_own[(i + 1) % 2];
     t.counter = a.counters + i;
+    t.early = i == 0 && a.rows <= ra::kCeFew && a.w == a.weight;
     const uint64_t rows = a.rows_pad / 256, across = (a.cols + 255) / 256;
     const uint64_t tiles = rows * ((t.w_out + 255) / 256) + (a.dhidden && t.w_sum ? rows * across * a.splits : 0) +
                            (a.dweight ? (t.w_sum + 255) / 256 * across : 0);

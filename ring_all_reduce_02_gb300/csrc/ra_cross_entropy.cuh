@@ -23,7 +23,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct CeHeader {
   int32_t rows;    // that count
-  int32_t failed;  // a wait inside a kernel gave up: every result is NaN
+  int32_t failed;  // not 0: a wait inside a kernel gave up (CeWait, and where), and every result is NaN
   float scale;     // what g is held relative to (from the first launch on)
 };
 
@@ -60,10 +60,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 constexpr int kCeRowsThreads = 256;
 
-// `cols` 16-bit elements from anywhere to a 16-byte boundary by a warp, zeros up to a whole line. A line that starts
-// off a 4-byte boundary is put together from 5 words, none of which lies wholly outside the row.
-__device__ __forceinline__ void ce_copy_row(void* to, const void* from, uint64_t cols, int lane) {
+// `cols` 16-bit elements from anywhere to a 16-byte boundary by a warp, zeros up to `padded` (whole lines). A line that
+// starts off a 16-byte boundary is put together from 5 words, none of which lies wholly outside the row.
+__device__ __forceinline__ void ce_copy_row(void* to, const void* from, uint64_t cols, uint64_t padded, int lane) {
   const uint64_t lines = (cols + 7) / 8;
+  for (uint64_t i = lines + lane; i < padded / 8; i += 32) static_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
   const uintptr_t p = reinterpret_cast<uintptr_t>(from);
   if (p % 16 == 0 && cols % 8 == 0) {
     for (uint64_t i = lane; i < lines; i += 32) static_cast<uint4*>(to)[i] = static_cast<const uint4*>(from)[i];
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kCeRowsThreads) ce_rows_kernel(const __grid_co
     for (uint32_t left = votes; left; left &= left - 1, ++to)
       if (to % kWarps == warp)
         ce_copy_row(static_cast<uint16_t*>(const_cast<void*>(a.h)) + (uint64_t)to * a.cols_pad,
-                    static_cast<const uint16_t*>(a.hidden) + (u + __ffs(left) - 1) * a.hidden_stride, a.cols, lane);
+                    static_cast<const uint16_t*>(a.hidden) + (u + __ffs(left) - 1) * a.hidden_stride, a.cols, a.cols_pad, lane);
     before += __popc(votes);
   }
   if (BACKWARD && blockIdx.x == gridDim.x - 1) {  // the products sum over whole blocks of 64 rows
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(256) ce_weight_kernel(const __grid_constant__ 
   pdl_next();
   for (uint64_t v = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32; v < a.vocab; v += (uint64_t)gridDim.x * 8)
     ce_copy_row(static_cast<uint16_t*>(const_cast<void*>(a.w)) + v * a.w_stride,
-                static_cast<const uint16_t*>(a.weight) + v * a.weight_stride, a.cols, threadIdx.x & 31);
+                static_cast<const uint16_t*>(a.weight) + v * a.weight_stride, a.cols, a.cols_pad, threadIdx.x & 31);
 }
 
 // g is held relative to the largest finite |dloss| (1 if that is 0), by a whole warp.
@@ -187,21 +188,29 @@ constexpr float kCeShift = DT == DT_F16 ? 16384.0f : 1.0f;
 // A launch of the backward pass has the gradients' tiles of one piece of g and the tiles of the next piece, in
 // another buffer: the short ones fill the gaps that the long ones leave at the end.
 
+// A wait that gave up.
+enum CeWait { CE_WAIT_EMPTY = 1, CE_WAIT_TILE, CE_WAIT_TAKEN, CE_WAIT_FULL, CE_WAIT_READ, CE_WAIT_READY };
 enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_DHIDDEN = 2, CE_DWEIGHT = 3 };
 
 constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6, kCeRing = 4;
 constexpr uint32_t kCeStageBytes = 4 * kBoxBytes;  // 128 x 64 of the one operand, 128 x 64 of the other
 constexpr uint32_t kCeTurn = 32 * 33 * 4;          // a warp's 32 x 32 results on their way to other lanes
 constexpr uint32_t kCeSmem = kCeStages * kCeStageBytes + kCeOutWarps * kCeTurn + 1024;
+constexpr uint32_t kCeFew = 256;  // rows, at most, that one tile has all of
 constexpr uint32_t kCeGroup = 8;  // tiles of rows that are worked on together, so that the pairs share words and rows
 
 struct CeTiles {
-  CUtensorMap h, w, g;      // g: the piece whose gradients are summed
+  // Boxes of 128 x 64 with rows along the summed dimension (h, w, g: the piece whose gradients are summed; with few rows
+  // h's are of 64 rows), and of two groups of 64 with rows along their own (h_own, w_own, g_own). Where w's
+  // rows are no whole groups, w_own's boxes are of one.
+  CUtensorMap h, w, g, h_own, w_own, g_own;
   CeArgs a;
   void* g_out;              // the piece that is computed (forward: none)
   uint64_t v_sum, w_sum;    // first word and words of the one piece (none: 0 words)
   uint64_t v_out, w_out;    // of the other; the forward pass's words
   uint32_t* counter;
+  int early;                // the first tiles' words may be asked for before the launch before this one has ended
+  int w_groups;             // w_own's boxes are of two groups
 };
 
 struct CeTile {
@@ -230,7 +239,7 @@ __device__ __forceinline__ CeWork ce_work(const CeTiles& t) {
   k.dh_tiles = t.a.dhidden && t.w_sum ? k.row_tiles * k.across * (uint32_t)t.a.splits : 0;
   k.dw_tiles = t.a.dweight && t.w_sum ? (uint32_t)((t.w_sum + 255) / 256) * k.across : 0;
   k.out_tiles = (uint32_t)((t.w_out + 255) / 256);
-  k.tiles = k.dh_tiles + k.dw_tiles + k.row_tiles * k.out_tiles;
+  k.tiles = t.a.head->failed ? 0 : k.dh_tiles + k.dw_tiles + k.row_tiles * k.out_tiles;
   k.dw_first = k.dw_blocks > k.dh_share;
   return k;
 }
@@ -264,7 +273,6 @@ __device__ __forceinline__ CeTile ce_tile(const CeTiles& t, const CeWork& k, uin
   o.n = across - o.n0 <= 128 ? 128 : 256;
   return o;
 }
-
 template <int DT>
 __device__ __forceinline__ void ce_store(void* p, uint64_t i, float f) {
   if constexpr (DT == DT_F32) static_cast<float*>(p)[i] = f;
@@ -457,14 +465,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCeStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ready[i], 1), mbar_init(&taken[i], 2 * kCeOutWarps);
-    // a tile's number is read by two loading threads, one that issues products, and both CTAs' warps for the results
-    for (int i = 0; i < kCeRing; ++i) mbar_init(&turns.full[i], 1), mbar_init(&turns.empty[i], 3 + 2 * kCeOutWarps);
+    // a tile's number is read by four loading threads, one that issues products, and both CTAs' warps for the results
+    for (int i = 0; i < kCeRing; ++i) mbar_init(&turns.full[i], 1), mbar_init(&turns.empty[i], 5 + 2 * kCeOutWarps);
     dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tma_prefetch_map(&t.h);
     tma_prefetch_map(&t.w);
-    if (BACKWARD) tma_prefetch_map(&t.g);
+    if (BACKWARD) tma_prefetch_map(&t.g), tma_prefetch_map(&t.g_own), tma_prefetch_map(&t.h_own), tma_prefetch_map(&t.w_own);
   }
   if (warp == 2) tmem_alloc_pair(&tmem_slot, 512);
   tmem_fence_before();
@@ -472,6 +480,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
+  const bool few = t.a.rows <= kCeFew;
+  // With few rows the first tile's words do not depend on how many rows count. Nothing in this call writes them, and
+  // what did before it has ended: the launch before this one waited for that before it let this one start.
+  uint32_t early = 0;
+  if (t.early && warp == 2 && lane == 0 && blockIdx.x / 2 * 256 < t.w_out) {
+    const uint32_t all = (uint32_t)((t.a.cols + 63) / 64);
+    const uint32_t n0 = blockIdx.x / 2 * 256, half = t.w_out - n0 <= 128 ? 64 : 128;
+    for (; early < all && early < kCeStages; ++early)
+      tma_load_pair(stages + early * kCeStageBytes + 2 * kBoxBytes, &t.w, (int32_t)early * 64, (int32_t)(t.v_out + n0 + rank * half),
+                    cluster_address(&full[early], 0));
+  }
   pdl_enter();
   pdl_next();
   const CeWork k = ce_work(t);
@@ -480,43 +499,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   // the number of the next tile; k.tiles or more: there is none
   const auto next = [&]() -> uint32_t {
     const uint32_t slot = turn % kCeRing;
-    if (!mbar_wait_pair(&turns.full[slot], turn / kCeRing & 1, &dead)) return 0xffffffffu;
+    if (!mbar_wait_pair(&turns.full[slot], turn / kCeRing & 1, &dead, CE_WAIT_TILE)) return 0xffffffffu;
     return *static_cast<volatile uint32_t*>(&turns.tile[slot]);
   };
   const auto have_read = [&] { mbar_arrive_at(cluster_address(&turns.empty[turn++ % kCeRing], 0)); };
 
   if (warp == 0 && lane == 0) {
-    // the tiles of both operands, each CTA of the pair its half; both count at the even CTA's barrier
+    // The first operand, 128 rows of each block to each CTA of the pair. What both CTAs bring in counts at the even one's
+    // barrier, and its bytes are announced here: those of the first operand that have to come, and all of the second.
     uint32_t s = 0, phase = 0;
     while (!dead) {
       const uint32_t i = next();
       if (i >= k.tiles) break;
       const CeTile o = ce_tile<BACKWARD>(t, k, i);
       have_read();
-      const uint32_t half = o.n / 2, boxes = half / 64;
-      const int32_t am = (int32_t)(o.m0 + rank * 128), bn = (int32_t)(o.n0 + rank * half);
+      const bool logits = !BACKWARD || o.kind == CE_G;
+      // boxes of each CTA; with few rows, of 64 rows and those alone that hold any
+      uint32_t boxes = 1, all = 2;
+      if (few && logits) {
+        const uint32_t mine = rank * 128 < k.rows ? k.rows - rank * 128 : 0;
+        boxes = mine > 64 ? 2 : mine > 0;
+        all = k.rows > 192 ? 4 : (k.rows + 63) / 64;
+      }
+      const uint32_t bytes = (few && logits ? all + 4 : 8) * kBoxBytes;
+      const int32_t own = (int32_t)(o.m0 + rank * 128);
       for (uint32_t b = 0; b < o.blocks; ++b) {
-        if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead)) break;
-        uint8_t* const at = stages + s * kCeStageBytes;
-        const uint32_t bar = cluster_address(&full[s], 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (2 + boxes) * kBoxBytes);
-        const int32_t sum = (int32_t)((o.b0 + b) * 64);
-        for (uint32_t q = 0; q < 2; ++q) {
-          uint8_t* const to = at + q * kBoxBytes;
-          const int32_t row = am + (int32_t)q * 64;
-          if (!BACKWARD || o.kind == CE_G) tma_load_pair(to, &t.h, sum, row, bar);
-          else if (o.kind == CE_DWEIGHT) tma_load_pair(to, &t.g, row, sum, bar);
-          else tma_load_pair(to, &t.g, sum, row, bar);
-        }
-        for (uint32_t q = 0; q < boxes; ++q) {
-          uint8_t* const to = at + (2 + q) * kBoxBytes;
-          const int32_t col = bn + (int32_t)q * 64;
-          if (!BACKWARD || o.kind == CE_G) tma_load_pair(to, &t.w, sum, (int32_t)t.v_out + col, bar);
-          else if (o.kind == CE_DWEIGHT) tma_load_pair(to, &t.h, col, sum, bar);
-          else tma_load_pair(to, &t.w, col, (int32_t)t.v_sum + sum, bar);
+        // a CTA that brings nothing in does not wait either: its stage may be used up by then
+        if (boxes || rank == 0) {
+          if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          uint8_t* const at = stages + s * kCeStageBytes;
+          const uint32_t bar = cluster_address(&full[s], 0);
+          const int32_t sum = (int32_t)((o.b0 + b) * 64);
+          if (BACKWARD && o.kind == CE_DWEIGHT) {
+            tma_load_pair(at, &t.g_own, 0, sum, own / 64, bar);
+          } else if (BACKWARD && o.kind == CE_DHIDDEN) {
+            tma_load_pair(at, &t.g, sum, own, bar);
+          } else {
+            if (boxes) tma_load_pair(at, &t.h, sum, own, bar);
+            if (boxes > 1) tma_load_pair(at + kBoxBytes, &t.h, sum, own + 64, bar);
+          }
         }
         if (++s == kCeStages) s = 0, phase ^= 1;
       }
+    }
+  } else if (warp == 2 && lane == 0) {
+    // the second operand
+    uint32_t s = 0, phase = 0;
+    while (!dead) {
+      const uint32_t i = next();
+      if (i >= k.tiles) break;
+      const CeTile o = ce_tile<BACKWARD>(t, k, i);
+      have_read();
+      const int32_t own = (int32_t)(o.n0 + rank * (o.n / 2));
+      for (uint32_t b = 0; b < o.blocks; ++b) {
+        if (b >= early) {
+          if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
+          uint8_t* const at = stages + s * kCeStageBytes + 2 * kBoxBytes;
+          const uint32_t bar = cluster_address(&full[s], 0);
+          const int32_t sum = (int32_t)((o.b0 + b) * 64);
+          if (BACKWARD && o.kind == CE_DWEIGHT) {
+            tma_load_pair(at, &t.h_own, 0, sum, own / 64, bar);
+          } else if (BACKWARD && o.kind == CE_DHIDDEN) {
+            if (t.w_groups) {
+              tma_load_pair(at, &t.w_own, 0, (int32_t)t.v_sum + sum, own / 64, bar);
+            } else {
+              tma_load_pair(at, &t.w_own, own, (int32_t)t.v_sum + sum, bar);
+              tma_load_pair(at + kBoxBytes, &t.w_own, own + 64, (int32_t)t.v_sum + sum, bar);
+            }
+          } else {
+            tma_load_pair(at, &t.w, sum, (int32_t)t.v_out + own, bar);
+          }
+        }
+        if (++s == kCeStages) s = 0, phase ^= 1;
+      }
+      early = 0;
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // the products of both CTAs
@@ -527,13 +584,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       const CeTile o = ce_tile<BACKWARD>(t, k, i);
       have_read();
       const uint32_t buffer = n & 1, d = tmem + buffer * 256;
-      if (!mbar_wait_pair(&taken[buffer], (n >> 1 & 1) ^ 1, &dead)) break;
+      if (!mbar_wait_pair(&taken[buffer], (n >> 1 & 1) ^ 1, &dead, CE_WAIT_TAKEN)) break;
       tmem_fence_after();
       const bool a_own = BACKWARD && o.kind == CE_DWEIGHT, b_own = BACKWARD && o.kind != CE_G;
       const uint32_t instruction = umma_instruction(DT == DT_BF16, a_own, b_own, o.n);
       const uint32_t a_step = umma_step(a_own), b_step = umma_step(b_own);
       for (uint32_t b = 0; b < o.blocks; ++b) {
-        if (!mbar_wait_pair(&full[s], phase, &dead)) break;
+        if (!mbar_wait_pair(&full[s], phase, &dead, CE_WAIT_FULL)) break;
         tmem_fence_after();
         const uint32_t at = smem_u32(stages + s * kCeStageBytes);
         const uint64_t da = umma_descriptor(at, a_own), db = umma_descriptor(at + 2 * kBoxBytes, b_own);
@@ -549,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
     const uint32_t pairs = gridDim.x / 2;
     for (uint32_t n = 0; !dead; ++n) {
       const uint32_t slot = n % kCeRing;
-      if (n >= kCeRing && !mbar_wait_pair(&turns.empty[slot], (n / kCeRing - 1) & 1, &dead)) break;
+      if (n >= kCeRing && !mbar_wait_pair(&turns.empty[slot], (n / kCeRing - 1) & 1, &dead, CE_WAIT_READ)) break;
       const uint32_t i = n == 0 ? blockIdx.x / 2 : pairs + atomicAdd(t.counter, 1u);
       turns.tile[slot] = i;
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(&turns.tile[slot], 1)), "r"(i) : "memory");
@@ -574,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       if (lane == 0) have_read();
       else ++turn;
       const uint32_t buffer = n & 1;
-      if (!mbar_wait_pair(&ready[buffer], n >> 1 & 1, &dead)) break;
+      if (!mbar_wait_pair(&ready[buffer], n >> 1 & 1, &dead, CE_WAIT_READY)) break;
       __syncwarp();
       tmem_fence_after();
       float x[128];
@@ -604,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   if (dead) {  // a wait gave up: the copies and products in flight end first, and the caller sees NaN
     const uint64_t start = global_ns();
     while (global_ns() - start < 10000000ull) {}
-    if (threadIdx.x == 0) atomicExch(&t.a.head->failed, 1);
+    if (threadIdx.x == 0) atomicCAS(&t.a.head->failed, 0, dead + 16 * (int)rank + 256 * (int)(blockIdx.x / 2));
   }
   tmem_fence_before();
   cluster_sync();

@@ -16,7 +16,7 @@ inline uint64_t round_up(uint64_t x, uint64_t to) { return (x + to - 1) / to * t
 
 // Where the scratch's parts start, in bytes from its first multiple of 256.
 struct CePlan {
-  uint64_t rows_pad, cols_pad;  // hidden's copy: whole tiles of rows, rows of whole 16-byte lines
+  uint64_t rows_pad, cols_pad;  // hidden's copy: whole tiles of rows, rows of whole blocks of 64
   uint64_t part_rows, parts;    // rows of a CTA of the first kernel, and how many there are
   uint64_t slots;               // forward: partial sums per row
   uint64_t piece, pieces;       // backward: columns of a piece of g (whole tiles), and how many there are
@@ -32,11 +32,11 @@ constexpr uint64_t kCeHeader = 256;
 inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed, bool backward) {
   CePlan p = {};
   p.rows_pad = round_up(rows ? rows : 1, kCeTile);
-  p.cols_pad = round_up(cols, 8);
+  p.cols_pad = round_up(cols, 64);
   p.part_rows = round_up((rows + kCeMostParts - 1) / kCeMostParts, 8);
   if (p.part_rows == 0) p.part_rows = 8;
   p.parts = rows ? (rows + p.part_rows - 1) / p.part_rows : 1;
-  p.slots = (vocab + 255) / 256 * 2;
+  p.slots = (vocab + kCeTile - 1) / kCeTile * 2;
   // pieces of about one size, so that no launch is a small one
   uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile;
   if (most < kCeLeastPiece / kCeTile) most = kCeLeastPiece / kCeTile;

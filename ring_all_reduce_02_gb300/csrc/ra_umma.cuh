@@ -28,9 +28,15 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-constexpr uint64_t kPairWaitNs = 10000000000ull;  // 10 s: more than any tile takes
-// As mbar_wait, for arrivals from both CTAs of a pair; gives up at once where the CTA already has (*dead).
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead) {
+// More bytes for the phase that the barrier is in.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+constexpr uint64_t kPairWaitNs = 4000000000ull;  // 4 s: more than any tile takes
+// As mbar_wait, for arrivals from both CTAs of a pair. Where it gives up, `what` says in *dead which wait did; where the
+// CTA already has, it gives up at once.
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead, int what) {
   uint64_t start = 0;
   while (true) {
     uint32_t done;
@@ -44,7 +50,7 @@ __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, v
     const uint64_t now = global_ns();
     if (start == 0) start = now;
     if (now - start > kPairWaitNs) {
-      *dead = 1;
+      *dead = what;
       return false;
     }
   }
@@ -57,6 +63,14 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+// The same of a three-dimensional one.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {

@@ -502,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
     if (!mbar_wait_pair(&turns.full[slot], turn / kCeRing & 1, &dead, CE_WAIT_TILE)) return 0xffffffffu;
     return *static_cast<volatile uint32_t*>(&turns.tile[slot]);
   };
-  const auto have_read = [&] { mbar_arrive_at(cluster_address(&turns.empty[turn++ % kCeRing], 0)); };
+  const auto have_read = [&] { mbar_arrive_at<false>(cluster_address(&turns.empty[turn++ % kCeRing], 0)); };
 
   if (warp == 0 && lane == 0) {
     // The first operand, 128 rows of each block to each CTA of the pair. What both CTAs bring in counts at the even one's
@@ -610,8 +610,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       const uint32_t i = n == 0 ? blockIdx.x / 2 : pairs + atomicAdd(t.counter, 1u);
       turns.tile[slot] = i;
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(&turns.tile[slot], 1)), "r"(i) : "memory");
-      mbar_arrive_at(cluster_address(&turns.full[slot], 0));
-      mbar_arrive_at(cluster_address(&turns.full[slot], 1));
+      mbar_arrive_at<true>(cluster_address(&turns.full[slot], 0));
+      mbar_arrive_at<true>(cluster_address(&turns.full[slot], 1));
       if (i >= k.tiles) break;
     }
   } else if (warp >= 4) {
@@ -642,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       tmem_wait_loads();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
+      if (lane == 0) mbar_arrive_at<false>(cluster_address(&taken[buffer], 0));
       const uint32_t m = o.m0 + rank * 128 + part + lane;
       if constexpr (!BACKWARD) {
         ce_out_logits(t, k, m, o.n0 + col, x);

@@ -24,8 +24,13 @@ __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
+// An arrival at a barrier of either CTA of a pair: with release what this thread has written before it is seen by who
+// waits there. That makes it wait for its stores to global memory too, half a microsecond and more, so an arrival that
+// only says that something has been read comes without.
+template <bool RELEASE>
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  if constexpr (RELEASE) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  else asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // More bytes for the phase that the barrier is in.
@@ -34,14 +39,15 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 }
 
 constexpr uint64_t kPairWaitNs = 4000000000ull;  // 4 s: more than any tile takes
-// As mbar_wait, for arrivals from both CTAs of a pair. Where it gives up, `what` says in *dead which wait did; where the
+// As mbar_wait. An acquire of the CTA's scope does for arrivals from the other one: what is read behind it lies in this
+// CTA's shared memory or in tensor memory (one of the cluster's scope also empties the L1 cache, at 0.3 us). Where it gives up, `what` says in *dead which wait did; where the
 // CTA already has, it gives up at once.
 __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead, int what) {
   uint64_t start = 0;
   while (true) {
     uint32_t done;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(done)
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");

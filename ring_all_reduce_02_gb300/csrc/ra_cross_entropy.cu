@@ -59,7 +59,7 @@ cudaError_t encode(CUtensorMap* map, int dtype, const void* p, uint64_t cols, ui
 cudaError_t encode_logits(ra::CeTiles& t, int dtype) {
   const CeArgs& a = t.a;
   const cudaError_t err = encode(&t.h, dtype, a.h, a.cols_pad, a.rows_pad, a.cols_pad, a.rows <= ra::kCeFew ? 64 : 128);
-  return err != cudaSuccess ? err : encode(&t.w, dtype, a.w, a.cols, a.vocab, a.w_stride, 128);
+  return err != cudaSuccess ? err : encode(&t.w, dtype, a.w, a.cols, a.vocab, a.w_stride, (uint32_t)a.words / 2);
 }
 
 // Every SM has a CTA at most; all rows are taken to count.
@@ -97,7 +97,7 @@ cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream
     err = t.w_groups ? encode(&t.w_own, DT, a.w, (a.cols + 63) / 64 * 64, a.vocab, a.w_stride, 64, true)
                      : encode(&t.w_own, DT, a.w, a.cols, a.vocab, a.w_stride, 64);
   for (uint64_t i = 0; i < 2 && i < a.pieces && err == cudaSuccess; ++i) {
-    err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 128);
+    err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, a.rows <= ra::kCeFew ? 64 : 128);
     if (err == cudaSuccess) err = encode(&g_own[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 64, true);
   }
   if (err == cudaSuccess) err = rows_and_operands<true>(a, s);
@@ -109,7 +109,7 @@ cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream
     t.counter = a.counters + i;
     t.early = i == 0 && a.rows <= ra::kCeFew && a.w == a.weight;
     const uint64_t rows = a.rows_pad / 256, across = (a.cols + 255) / 256;
-    const uint64_t tiles = rows * ((t.w_out + 255) / 256) + (a.dhidden && t.w_sum ? rows * across * a.splits : 0) +
+    const uint64_t tiles = rows * ((t.w_out + a.words - 1) / a.words) + (a.dhidden && t.w_sum ? rows * across * a.splits : 0) +
                            (a.dweight ? (t.w_sum + 255) / 256 * across : 0);
     err = launch_tiles<DT, WDT, true>(t, tiles, s);
   }
@@ -123,7 +123,7 @@ char* first_place(void* workspace) { return reinterpret_cast<char*>(ra::round_up
 void place(CeArgs& a, const CePlan& p, void* workspace, bool packed) {
   char* w = first_place(workspace);
   a.rows_pad = p.rows_pad, a.cols_pad = p.cols_pad, a.part_rows = p.part_rows, a.parts = p.parts;
-  a.slots = p.slots, a.piece = p.piece, a.pieces = p.pieces, a.splits = p.splits;
+  a.words = p.words, a.slots = p.slots, a.piece = p.piece, a.pieces = p.pieces, a.splits = p.splits;
   a.head = reinterpret_cast<ra::CeHeader*>(w);
   a.counters = reinterpret_cast<uint32_t*>(w + p.counters);
   a.tops = reinterpret_cast<float*>(w + p.tops);

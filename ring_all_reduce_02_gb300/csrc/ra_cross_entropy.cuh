@@ -34,7 +34,7 @@ struct CeArgs {
   uint64_t hidden_stride, weight_stride, w_stride;
   Indices targets;
   int64_t ignore;
-  uint64_t rows, cols, vocab, rows_pad, cols_pad, part_rows, parts, slots, piece, pieces, splits;
+  uint64_t rows, cols, vocab, rows_pad, cols_pad, part_rows, parts, words, slots, piece, pieces, splits;
   CeHeader* head;
   uint32_t* counters;  // of the tiles that a launch's pairs have taken
   float* tops;         // the first kernel's CTAs' largest finite |dloss|
@@ -96,6 +96,10 @@ __global__ void __launch_bounds__(kCeRowsThreads) ce_rows_kernel(const __grid_co
   __shared__ int32_t sums[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const uint64_t t0 = blockIdx.x * a.part_rows, t1 = t0 + a.part_rows < a.rows ? t0 + a.part_rows : a.rows;
+  // the rows on their way while the targets are looked at
+  for (uint64_t t = t0 + warp; t < t1; t += kWarps)
+    for (uint64_t b = lane * 128; b < a.cols * 2; b += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.hidden) + t * a.hidden_stride * 2 + b));
   int32_t before = 0;
 #pragma unroll 8
   for (uint64_t t = threadIdx.x; t < t0; t += kCeRowsThreads) before += load_index(a.targets, t) != a.ignore;
@@ -190,7 +194,7 @@ constexpr float kCeShift = DT == DT_F16 ? 16384.0f : 1.0f;
 
 // A wait that gave up.
 enum CeWait { CE_WAIT_EMPTY = 1, CE_WAIT_TILE, CE_WAIT_TAKEN, CE_WAIT_FULL, CE_WAIT_READ, CE_WAIT_READY };
-enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_DHIDDEN = 2, CE_DWEIGHT = 3 };
+enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_DHIDDEN = 2, CE_DWEIGHT = 3, CE_END = 4 };
 
 constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6, kCeRing = 4;
 constexpr uint32_t kCeStageBytes = 4 * kBoxBytes;  // 128 x 64 of the one operand, 128 x 64 of the other
@@ -201,7 +205,7 @@ constexpr uint32_t kCeGroup = 8;  // tiles of rows that are worked on together, 
 
 struct CeTiles {
   // Boxes of 128 x 64 with rows along the summed dimension (h, w, g: the piece whose gradients are summed; with few rows
-  // h's are of 64 rows), and of two groups of 64 with rows along their own (h_own, w_own, g_own). Where w's
+  // h's and g's are of 64 rows), and of two groups of 64 with rows along their own (h_own, w_own, g_own). Where w's
   // rows are no whole groups, w_own's boxes are of one.
   CUtensorMap h, w, g, h_own, w_own, g_own;
   CeArgs a;
@@ -213,13 +217,17 @@ struct CeTiles {
   int w_groups;             // w_own's boxes are of two groups
 };
 
-struct CeTile {
-  int kind;
+// A tile as it is handed to the warps that work on it.
+struct __align__(16) CeTile {
   uint32_t m0, n0;      // first row and column
-  uint32_t n;           // columns: 256, or 128 where there are no more
-  uint32_t b0, blocks;  // first of the blocks of 64 summed elements, and how many
-  uint32_t split;       // dh: the share of the words
+  uint32_t blocks, b0;  // blocks of 64 summed elements, and the first of them
+  uint32_t slot;        // logits: its place in a row of partial sums; dh: the share of the words
+  uint16_t kind, n;     // n: columns
+  uint32_t pad[2];
 };
+
+// Columns of a tile with `left` to go: a half where there are no more.
+__device__ __forceinline__ uint32_t ce_width(uint32_t wide, uint32_t left) { return wide == 256 && left <= 128 ? 128 : wide; }
 
 // Tiles of a launch, from the rows that count: dh's and dw's, the longer ones first, then those of logits.
 struct CeWork {
@@ -238,16 +246,19 @@ __device__ __forceinline__ CeWork ce_work(const CeTiles& t) {
   k.out_blocks = (uint32_t)((t.a.cols + 63) / 64);
   k.dh_tiles = t.a.dhidden && t.w_sum ? k.row_tiles * k.across * (uint32_t)t.a.splits : 0;
   k.dw_tiles = t.a.dweight && t.w_sum ? (uint32_t)((t.w_sum + 255) / 256) * k.across : 0;
-  k.out_tiles = (uint32_t)((t.w_out + 255) / 256);
+  k.out_tiles = (uint32_t)((t.w_out + t.a.words - 1) / t.a.words);
   k.tiles = t.a.head->failed ? 0 : k.dh_tiles + k.dw_tiles + k.row_tiles * k.out_tiles;
   k.dw_first = k.dw_blocks > k.dh_share;
   return k;
 }
 template <bool BACKWARD>
 __device__ __forceinline__ CeTile ce_tile(const CeTiles& t, const CeWork& k, uint32_t i) {
-  CeTile o;
-  uint32_t m, c, across = (uint32_t)t.a.cols;
-  o.b0 = o.split = 0;
+  CeTile o = {};
+  if (i >= k.tiles) {
+    o.kind = CE_END;
+    return o;
+  }
+  uint32_t m, c, wide = 256, across = (uint32_t)t.a.cols;
   if (BACKWARD && i < k.dh_tiles + k.dw_tiles) {
     const uint32_t first = k.dw_first ? k.dw_tiles : k.dh_tiles;
     o.kind = (i < first) == k.dw_first ? CE_DWEIGHT : CE_DHIDDEN;
@@ -256,8 +267,8 @@ __device__ __forceinline__ CeTile ce_tile(const CeTiles& t, const CeWork& k, uin
     if (o.kind == CE_DWEIGHT) {
       o.blocks = k.dw_blocks;
     } else {
-      o.split = m / k.row_tiles, m %= k.row_tiles;
-      o.b0 = o.split * k.dh_share;
+      o.slot = m / k.row_tiles, m %= k.row_tiles;
+      o.b0 = o.slot * k.dh_share;
       const uint32_t left = k.dh_blocks > o.b0 ? k.dh_blocks - o.b0 : 0;
       o.blocks = left < k.dh_share ? left : k.dh_share;
     }
@@ -266,13 +277,15 @@ __device__ __forceinline__ CeTile ce_tile(const CeTiles& t, const CeWork& k, uin
     if constexpr (BACKWARD) i -= k.dh_tiles + k.dw_tiles;
     const uint32_t group = i / (kCeGroup * k.out_tiles), r = i - group * kCeGroup * k.out_tiles;
     const uint32_t left = k.row_tiles - group * kCeGroup, high = left < kCeGroup ? left : kCeGroup;
-    m = group * kCeGroup + r % high, c = r / high, across = (uint32_t)t.w_out;
+    m = group * kCeGroup + r % high, c = r / high, across = (uint32_t)t.w_out, wide = (uint32_t)t.a.words;
+    o.slot = 2 * c;
     o.blocks = k.out_blocks;
   }
-  o.m0 = m * 256, o.n0 = c * 256;
-  o.n = across - o.n0 <= 128 ? 128 : 256;
+  o.m0 = m * 256, o.n0 = c * wide;
+  o.n = (uint16_t)ce_width(wide, across - o.n0);
   return o;
 }
+
 template <int DT>
 __device__ __forceinline__ void ce_store(void* p, uint64_t i, float f) {
   if constexpr (DT == DT_F32) static_cast<float*>(p)[i] = f;
@@ -298,9 +311,10 @@ __device__ __forceinline__ void ld_sector(const void* p, uint32_t (&w)[8]) {
 // ---- what becomes of a tile's results: a thread has the 128 columns from `col` on of row `m` in x ----
 
 // The maximum and the sum of exponentials of a row's 128 logits, and the target's logit.
-__device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k, uint32_t m, uint32_t col, float (&x)[128]) {
+__device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k, const CeTile& o, uint32_t m, uint32_t col,
+                                              float (&x)[128]) {
   const float low = __int_as_float(0xff800000);
-  const uint32_t words = (uint32_t)t.w_out;
+  const uint32_t words = o.n0 + o.n < (uint32_t)t.w_out ? o.n0 + o.n : (uint32_t)t.w_out;
   if (col + 128 > words)
 #pragma unroll
     for (int j = 0; j < 128; ++j)
@@ -318,9 +332,9 @@ __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k,
     sums[j / 2 % 4] = add2(sums[j / 2 % 4], pair(exp2_approx(p), exp2_approx(q)));
   }
   if (m >= k.rows) return;
-  t.a.partial[(uint64_t)m * t.a.slots + col / 128] = make_float2(top, fold2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]))));
+  t.a.partial[(uint64_t)m * t.a.slots + o.slot + (col > o.n0)] = make_float2(top, fold2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]))));
   const uint32_t at = (uint32_t)(t.a.target[m] - (int32_t)col);
-  if (at < 128) {
+  if (at < 128 && col + at < words) {
     float y = 0.0f;
 #pragma unroll
     for (int j = 0; j < 128; ++j) y = at == j ? x[j] : y;
@@ -331,7 +345,8 @@ __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k,
 // g = d (exp(logit - lse) - [target]), d = dloss / scale; zero in words behind the last and in rows behind the counted
 // ones, as far as the products go.
 template <int DT>
-__device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, float scale, uint32_t m, uint32_t col, float (&x)[128]) {
+__device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, const CeTile& o, float scale, uint32_t m, uint32_t col,
+                                         float (&x)[128]) {
   const bool counts = m < k.rows;
   if (m >= k.dw_blocks * 64) return;
   const int32_t target = counts ? t.a.target[m] : 0;
@@ -339,7 +354,10 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, floa
   if (target < 0) d = __int_as_float(0x7fffffff);
   const float shift = counts ? -t.a.lse_kept[m] * kLog2e : 0.0f;
   const F2 slope = twice(kLog2e), both = twice(shift), dd = twice(d);
-  const uint32_t at = counts ? (uint32_t)(target - (int32_t)(t.v_out + col)) : 128u;
+  // the last tile goes on to a whole block of 64
+  const uint32_t words = (uint32_t)t.w_out, end = o.n0 + o.n < words ? o.n0 + o.n : (words + 63) / 64 * 64;
+  uint32_t at = counts ? (uint32_t)(target - (int32_t)(t.v_out + col)) : 128u;
+  if (at < 128 && col + at >= o.n0 + o.n) at = 128;
   float y = 0.0f;
   if (at < 128) {
 #pragma unroll
@@ -347,9 +365,10 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, floa
     y = (exp2_approx(__fmaf_rn(y, kLog2e, shift)) - 1.0f) * d;
   }
   uint16_t* to = static_cast<uint16_t*>(t.g_out) + (uint64_t)m * t.a.piece + col;
-  const uint32_t words = (uint32_t)t.w_out, there = !counts || col >= words ? 0 : words - col;
+  const uint32_t there = !counts || col >= words ? 0 : words - col;
 #pragma unroll
   for (int j = 0; j < 128; j += 16) {
+    if (col + j >= end) break;
     uint32_t w[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -371,7 +390,7 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, floa
 __device__ __forceinline__ void ce_out_dhidden(const CeTiles& t, const CeWork& k, const CeTile& o, uint32_t m, uint32_t col,
                                                float (&x)[128]) {
   if (m >= k.rows) return;
-  float* to = t.a.dh + (o.split * t.a.rows + m) * t.a.cols_pad + col;
+  float* to = t.a.dh + (o.slot * t.a.rows + m) * t.a.cols_pad + col;
 #pragma unroll
   for (int j = 0; j < 128; j += 8) {
     if (col + j >= t.a.cols_pad) break;
@@ -388,69 +407,76 @@ __device__ __forceinline__ void ce_out_dhidden(const CeTiles& t, const CeWork& k
   }
 }
 
-// dw (+)= scale * x. Rows of whole sectors are stored as the threads hold them; others are turned in shared memory, so
-// that a warp stores 32 columns of a row at a time.
+// Whether dw's rows are whole sectors.
+template <int WDT>
+__device__ __forceinline__ bool ce_sectors(const CeArgs& a) {
+  constexpr uint64_t es = Elem<WDT>::kSize;
+  return (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 32 == 0;
+}
+// dw (+)= scale * x, rows of whole sectors.
 template <int DT, int WDT>
-__device__ __forceinline__ void ce_out_dweight(const CeTiles& t, float scale, uint32_t m, uint32_t col, float (&x)[128], float* turn) {
+__device__ __forceinline__ void ce_out_dweight(const CeTiles& t, float scale, uint32_t m, uint32_t col, float (&x)[128]) {
   constexpr uint32_t es = Elem<WDT>::kSize, V = 32 / es;
-  const uint32_t cols = (uint32_t)t.a.cols, words = (uint32_t)t.w_sum, lane = threadIdx.x & 31;
+  const uint32_t cols = (uint32_t)t.a.cols;
   const float f = scale / kCeShift<DT>;
-  char* const base = static_cast<char*>(t.a.dweight);
-  if ((reinterpret_cast<uintptr_t>(base) | t.a.dweight_stride * es | cols * es) % 32 == 0) {
-    if (m >= words) return;
-    char* const to = base + ((t.v_sum + m) * t.a.dweight_stride + col) * es;
+  if (m >= (uint32_t)t.w_sum) return;
+  char* const to = static_cast<char*>(t.a.dweight) + ((t.v_sum + m) * t.a.dweight_stride + col) * es;
 #pragma unroll
-    for (uint32_t j = 0; j < 128; j += V) {
-      if (col + j >= cols) break;
-      uint32_t w[8];
-      if (t.a.accumulate) ld_sector(to + j * es, w);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if constexpr (WDT == DT_F32) {
-          const float v = x[j + q] * f;
-          w[q] = __float_as_uint(t.a.accumulate ? v + __uint_as_float(w[q]) : v);
-        } else {
-          float u = x[j + 2 * q] * f, v = x[j + 2 * q + 1] * f;
-          if (t.a.accumulate) u += widen16<WDT>(w[q] & 0xffffu), v += widen16<WDT>(w[q] >> 16);
-          w[q] = round16x2<WDT>(u, v);
-        }
-      }
-      st_sector(to + j * es, w);
-    }
-    return;
-  }
-  const uint32_t m0 = m - lane;
-#pragma unroll
-  for (uint32_t j = 0; j < 128; j += 32) {
+  for (uint32_t j = 0; j < 128; j += V) {
     if (col + j >= cols) break;
+    uint32_t w[8];
+    if (t.a.accumulate) ld_sector(to + j * es, w);
 #pragma unroll
-    for (int q = 0; q < 32; ++q) turn[lane * 33 + q] = x[j + q] * f;
+    for (int q = 0; q < 8; ++q) {
+      if constexpr (WDT == DT_F32) {
+        const float v = x[j + q] * f;
+        w[q] = __float_as_uint(t.a.accumulate ? v + __uint_as_float(w[q]) : v);
+      } else {
+        float u = x[j + 2 * q] * f, v = x[j + 2 * q + 1] * f;
+        if (t.a.accumulate) u += widen16<WDT>(w[q] & 0xffffu), v += widen16<WDT>(w[q] >> 16);
+        w[q] = round16x2<WDT>(u, v);
+      }
+    }
+    st_sector(to + j * es, w);
+  }
+}
+// The same for rows that start anywhere, by a warp and from tensor memory (`at`: its 128 columns; rows m0 on): 32 columns
+// at a time are turned in shared memory, so that the warp reads and stores 32 columns of a row together, all 32 rows' in
+// flight at once.
+template <int DT, int WDT>
+__device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float scale, uint32_t m0, uint32_t col, uint32_t at, float* turn) {
+  const uint32_t cols = (uint32_t)t.a.cols, words = (uint32_t)t.w_sum, lane = threadIdx.x & 31;
+  const uint32_t high = m0 >= words ? 0 : words - m0 < 32 ? words - m0 : 32;
+  const float f = scale / kCeShift<DT>;
+#pragma unroll 1
+  for (uint32_t j = 0; j < 128 && col + j < cols; j += 32) {
+    uint32_t x[32];
+    tmem_load32(at + j, x);
+    tmem_wait_loads();
+    const uint32_t c = col + j + lane, rows = c < cols ? high : 0;
+    const uint64_t first = (t.v_sum + m0) * t.a.dweight_stride + c;
+    float old[32];
+    if (t.a.accumulate) {
+#pragma unroll
+      for (uint32_t r = 0; r < 32; ++r) old[r] = r < rows ? ce_load<WDT>(t.a.dweight, first + r * t.a.dweight_stride) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < 32; ++q) turn[lane * 33 + q] = __uint_as_float(x[q]) * f;
     __syncwarp();
-    const uint32_t c = col + j + lane;
 #pragma unroll
-    for (uint32_t r0 = 0; r0 < 32; r0 += 16) {
-      const uint64_t at = (t.v_sum + m0 + r0) * t.a.dweight_stride + c;
-      const uint32_t high = c >= cols || m0 + r0 >= words ? 0 : words - m0 - r0;
-      float old[16];
-      if (t.a.accumulate) {
-#pragma unroll
-        for (uint32_t r = 0; r < 16; ++r) old[r] = r < high ? ce_load<WDT>(base, at + r * t.a.dweight_stride) : 0.0f;
-      }
-#pragma unroll
-      for (uint32_t r = 0; r < 16; ++r) {
-        float v = turn[(r0 + r) * 33 + lane];
-        if (t.a.accumulate) v += old[r];
-        if (r < high) ce_store<WDT>(base, at + r * t.a.dweight_stride, v);
-      }
+    for (uint32_t r = 0; r < 32; ++r) {
+      float v = turn[r * 33 + lane];
+      if (t.a.accumulate) v += old[r];
+      if (r < rows) ce_store<WDT>(t.a.dweight, first + r * t.a.dweight_stride, v);
     }
     __syncwarp();
   }
 }
 
-// The numbers of a pair's tiles, handed to its warps through a small ring in both CTAs.
+// A pair's tiles, handed to its warps through a small ring in both CTAs.
 struct CeTurns {
+  CeTile tile[kCeRing];
   uint64_t full[kCeRing], empty[kCeRing];
-  uint32_t tile[kCeRing];
 };
 
 template <int DT, int WDT, bool BACKWARD>
@@ -461,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   __shared__ uint32_t tmem_slot;
   __shared__ int dead;
   uint8_t* const stages = dynamic + (1024u - (smem_u32(dynamic) & 1023u)) % 1024u;  // the swizzle goes by the address
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31, rank = cluster_rank();
+  const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x & 31, rank = uniform(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCeStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ready[i], 1), mbar_init(&taken[i], 2 * kCeOutWarps);
@@ -479,16 +505,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   __syncthreads();
   cluster_sync();
   tmem_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = uniform(tmem_slot);
   const bool few = t.a.rows <= kCeFew;
   // With few rows the first tile's words do not depend on how many rows count. Nothing in this call writes them, and
   // what did before it has ended: the launch before this one waited for that before it let this one start.
   uint32_t early = 0;
-  if (t.early && warp == 2 && lane == 0 && blockIdx.x / 2 * 256 < t.w_out) {
+  if (t.early && warp == 2 && blockIdx.x / 2 * t.a.words < t.w_out) {
     const uint32_t all = (uint32_t)((t.a.cols + 63) / 64);
-    const uint32_t n0 = blockIdx.x / 2 * 256, half = t.w_out - n0 <= 128 ? 64 : 128;
+    const uint32_t n0 = blockIdx.x / 2 * (uint32_t)t.a.words, half = ce_width((uint32_t)t.a.words, (uint32_t)t.w_out - n0) / 2;
     for (; early < all && early < kCeStages; ++early)
-      tma_load_pair(stages + early * kCeStageBytes + 2 * kBoxBytes, &t.w, (int32_t)early * 64, (int32_t)(t.v_out + n0 + rank * half),
+      if (elected()) tma_load_pair(stages + early * kCeStageBytes + 2 * kBoxBytes, &t.w, (int32_t)early * 64, (int32_t)(t.v_out + n0 + rank * half),
                     cluster_address(&full[early], 0));
   }
   pdl_enter();
@@ -496,93 +522,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   const CeWork k = ce_work(t);
 
   uint32_t turn = 0;
-  // the number of the next tile; k.tiles or more: there is none
-  const auto next = [&]() -> uint32_t {
-    const uint32_t slot = turn % kCeRing;
-    if (!mbar_wait_pair(&turns.full[slot], turn / kCeRing & 1, &dead, CE_WAIT_TILE)) return 0xffffffffu;
-    return *static_cast<volatile uint32_t*>(&turns.tile[slot]);
+  // The next tile, by a whole warp. The loading warps and the one of the products ask for it before they work on the one
+  // before, so that they do not wait for it. What it says is the same in all lanes, as what these warps count: one lane
+  // issues, and finds all it needs in uniform registers (from a branch of one lane each product waits for its operands
+  // to be moved there, 75 cycles of the 128 that it takes).
+  const auto next = [&] {
+    CeTile o;
+    const uint32_t slot = turn % kCeRing, round = turn / kCeRing;
+    ++turn;
+    o.kind = CE_END;
+    if (!mbar_wait_pair(&turns.full[slot], round & 1, &dead, CE_WAIT_TILE)) return o;
+    const volatile uint32_t* from = reinterpret_cast<const volatile uint32_t*>(&turns.tile[slot]);
+    o.m0 = uniform(from[0]), o.n0 = uniform(from[1]), o.blocks = uniform(from[2]), o.b0 = uniform(from[3]), o.slot = uniform(from[4]);
+    const uint32_t both = uniform(from[5]);
+    o.kind = (uint16_t)both, o.n = (uint16_t)(both >> 16);
+    if (lane == 0) mbar_arrive_at(cluster_address(&turns.empty[slot], 0));
+    return o;
   };
-  const auto have_read = [&] { mbar_arrive_at<false>(cluster_address(&turns.empty[turn++ % kCeRing], 0)); };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // The first operand, 128 rows of each block to each CTA of the pair. What both CTAs bring in counts at the even one's
     // barrier, and its bytes are announced here: those of the first operand that have to come, and all of the second.
     uint32_t s = 0, phase = 0;
-    while (!dead) {
-      const uint32_t i = next();
-      if (i >= k.tiles) break;
-      const CeTile o = ce_tile<BACKWARD>(t, k, i);
-      have_read();
+    for (CeTile o = next(), after; o.kind != CE_END && !dead; o = after) {
       const bool logits = !BACKWARD || o.kind == CE_G;
-      // boxes of each CTA; with few rows, of 64 rows and those alone that hold any
-      uint32_t boxes = 1, all = 2;
-      if (few && logits) {
-        const uint32_t mine = rank * 128 < k.rows ? k.rows - rank * 128 : 0;
-        boxes = mine > 64 ? 2 : mine > 0;
-        all = k.rows > 192 ? 4 : (k.rows + 63) / 64;
+      // Boxes of this CTA, and of both. With few rows they are of 64 rows, and those that hold none are left out, but for
+      // one of each CTA: one that brings nothing in could not tell a stage that is free from one that is used again.
+      uint32_t boxes = 1, bytes = 4 * kBoxBytes;
+      if (few && (logits || o.kind == CE_DHIDDEN)) {
+        const uint32_t other = k.rows > 192 ? 2 : 1, first = k.rows > 64 ? 2 : 1;
+        boxes = rank ? other : first;
+        bytes = (first + other) * kBoxBytes;
       }
-      const uint32_t bytes = (few && logits ? all + 4 : 8) * kBoxBytes;
+      bytes += logits ? (uint32_t)t.a.words * 128 : 4 * kBoxBytes;
       const int32_t own = (int32_t)(o.m0 + rank * 128);
+      after = next();
       for (uint32_t b = 0; b < o.blocks; ++b) {
-        // a CTA that brings nothing in does not wait either: its stage may be used up by then
-        if (boxes || rank == 0) {
-          if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
+        if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
+        if (elected()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           uint8_t* const at = stages + s * kCeStageBytes;
           const uint32_t bar = cluster_address(&full[s], 0);
           const int32_t sum = (int32_t)((o.b0 + b) * 64);
           if (BACKWARD && o.kind == CE_DWEIGHT) {
             tma_load_pair(at, &t.g_own, 0, sum, own / 64, bar);
-          } else if (BACKWARD && o.kind == CE_DHIDDEN) {
-            tma_load_pair(at, &t.g, sum, own, bar);
           } else {
-            if (boxes) tma_load_pair(at, &t.h, sum, own, bar);
-            if (boxes > 1) tma_load_pair(at + kBoxBytes, &t.h, sum, own + 64, bar);
+            const CUtensorMap* const map = BACKWARD && o.kind == CE_DHIDDEN ? &t.g : &t.h;
+            tma_load_pair(at, map, sum, own, bar);
+            if (boxes > 1) tma_load_pair(at + kBoxBytes, map, sum, own + 64, bar);
           }
         }
         if (++s == kCeStages) s = 0, phase ^= 1;
       }
     }
-  } else if (warp == 2 && lane == 0) {
+  } else if (warp == 2) {
     // the second operand
     uint32_t s = 0, phase = 0;
-    while (!dead) {
-      const uint32_t i = next();
-      if (i >= k.tiles) break;
-      const CeTile o = ce_tile<BACKWARD>(t, k, i);
-      have_read();
+    for (CeTile o = next(), after; o.kind != CE_END && !dead; o = after) {
       const int32_t own = (int32_t)(o.n0 + rank * (o.n / 2));
+      after = next();
       for (uint32_t b = 0; b < o.blocks; ++b) {
         if (b >= early) {
           if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
-          uint8_t* const at = stages + s * kCeStageBytes + 2 * kBoxBytes;
-          const uint32_t bar = cluster_address(&full[s], 0);
-          const int32_t sum = (int32_t)((o.b0 + b) * 64);
-          if (BACKWARD && o.kind == CE_DWEIGHT) {
-            tma_load_pair(at, &t.h_own, 0, sum, own / 64, bar);
-          } else if (BACKWARD && o.kind == CE_DHIDDEN) {
-            if (t.w_groups) {
-              tma_load_pair(at, &t.w_own, 0, (int32_t)t.v_sum + sum, own / 64, bar);
+          if (elected()) {
+            uint8_t* const at = stages + s * kCeStageBytes + 2 * kBoxBytes;
+            const uint32_t bar = cluster_address(&full[s], 0);
+            const int32_t sum = (int32_t)((o.b0 + b) * 64);
+            if (BACKWARD && o.kind == CE_DWEIGHT) {
+              tma_load_pair(at, &t.h_own, 0, sum, own / 64, bar);
+            } else if (BACKWARD && o.kind == CE_DHIDDEN) {
+              if (t.w_groups) {
+                tma_load_pair(at, &t.w_own, 0, (int32_t)t.v_sum + sum, own / 64, bar);
+              } else {
+                tma_load_pair(at, &t.w_own, own, (int32_t)t.v_sum + sum, bar);
+                tma_load_pair(at + kBoxBytes, &t.w_own, own + 64, (int32_t)t.v_sum + sum, bar);
+              }
             } else {
-              tma_load_pair(at, &t.w_own, own, (int32_t)t.v_sum + sum, bar);
-              tma_load_pair(at + kBoxBytes, &t.w_own, own + 64, (int32_t)t.v_sum + sum, bar);
+              tma_load_pair(at, &t.w, sum, (int32_t)t.v_out + own, bar);
             }
-          } else {
-            tma_load_pair(at, &t.w, sum, (int32_t)t.v_out + own, bar);
           }
         }
         if (++s == kCeStages) s = 0, phase ^= 1;
       }
       early = 0;
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // the products of both CTAs
     uint32_t s = 0, phase = 0, n = 0;
-    for (; !dead; ++n) {
-      const uint32_t i = next();
-      if (i >= k.tiles) break;
-      const CeTile o = ce_tile<BACKWARD>(t, k, i);
-      have_read();
+    for (CeTile o = next(), after; o.kind != CE_END && !dead; o = after, ++n) {
+      after = next();
       const uint32_t buffer = n & 1, d = tmem + buffer * 256;
       if (!mbar_wait_pair(&taken[buffer], (n >> 1 & 1) ^ 1, &dead, CE_WAIT_TAKEN)) break;
       tmem_fence_after();
@@ -592,27 +620,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       for (uint32_t b = 0; b < o.blocks; ++b) {
         if (!mbar_wait_pair(&full[s], phase, &dead, CE_WAIT_FULL)) break;
         tmem_fence_after();
-        const uint32_t at = smem_u32(stages + s * kCeStageBytes);
-        const uint64_t da = umma_descriptor(at, a_own), db = umma_descriptor(at + 2 * kBoxBytes, b_own);
+        if (elected()) {
+          const uint32_t at = smem_u32(stages + s * kCeStageBytes);
+          const uint64_t da = umma_descriptor(at, a_own), db = umma_descriptor(at + 2 * kBoxBytes, b_own);
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) umma_pair(d, da + q * a_step, db + q * b_step, instruction, b > 0 || q > 0);
-        umma_commit_pair(&empty[s]);
+          for (uint32_t q = 0; q < 4; ++q) umma_pair(d, da + q * a_step, db + q * b_step, instruction, b > 0 || q > 0);
+          umma_commit_pair(&empty[s]);
+        }
         if (++s == kCeStages) s = 0, phase ^= 1;
       }
-      umma_commit_pair(&ready[buffer]);
+      if (elected()) umma_commit_pair(&ready[buffer]);
     }
   } else if (warp == 3 && lane == 0 && rank == 0) {
-    // the tiles' numbers
+    // the tiles; the counter is asked for the next one before this one is handed out
     const uint32_t pairs = gridDim.x / 2;
+    uint32_t i = blockIdx.x / 2, following = atomicAdd(t.counter, 1u);
     for (uint32_t n = 0; !dead; ++n) {
       const uint32_t slot = n % kCeRing;
       if (n >= kCeRing && !mbar_wait_pair(&turns.empty[slot], (n / kCeRing - 1) & 1, &dead, CE_WAIT_READ)) break;
-      const uint32_t i = n == 0 ? blockIdx.x / 2 : pairs + atomicAdd(t.counter, 1u);
-      turns.tile[slot] = i;
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(&turns.tile[slot], 1)), "r"(i) : "memory");
-      mbar_arrive_at<true>(cluster_address(&turns.full[slot], 0));
-      mbar_arrive_at<true>(cluster_address(&turns.full[slot], 1));
-      if (i >= k.tiles) break;
+      const CeTile o = ce_tile<BACKWARD>(t, k, i);
+      const uint32_t w[8] = {o.m0, o.n0, o.blocks, o.b0, o.slot, (uint32_t)o.kind | (uint32_t)o.n << 16, 0, 0};
+      for (uint32_t to = 0; to < 2; ++to) store_pair(cluster_address(&turns.tile[slot], to), w, cluster_address(&turns.full[slot], to));
+      if (o.kind == CE_END) break;
+      i = pairs + following;
+      following = atomicAdd(t.counter, 1u);
     }
   } else if (warp >= 4) {
     // the results: warp w has lanes 32 (w % 4) on of tensor memory, the first four warps columns 0 to 127
@@ -623,36 +654,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       scale = t.w_sum ? t.a.head->scale : ce_scale(t.a);
       if (!t.w_sum && blockIdx.x == 0 && warp == 4 && lane == 0) t.a.head->scale = scale;
     }
-    for (uint32_t n = 0; !dead; ++n) {
-      const uint32_t i = next();
-      if (i >= k.tiles) break;
-      const CeTile o = ce_tile<BACKWARD>(t, k, i);
-      __syncwarp();
-      if (lane == 0) have_read();
-      else ++turn;
-      const uint32_t buffer = n & 1;
+    const bool sectors = BACKWARD && ce_sectors<WDT>(t.a);
+    uint32_t n = 0;
+    for (CeTile o = next(); o.kind != CE_END && !dead; o = next(), ++n) {
+      const uint32_t buffer = n & 1, m = o.m0 + rank * 128 + part + lane;
+      if (BACKWARD && o.kind == CE_DWEIGHT && t.a.accumulate && m < t.w_sum && o.n0 + col < t.a.cols) {
+        // what the tile is added to, on its way while the products run
+        constexpr uint32_t es = Elem<WDT>::kSize;
+        const uint32_t left = ((uint32_t)t.a.cols - o.n0 - col < 128 ? (uint32_t)t.a.cols - o.n0 - col : 128) * es;
+        const char* at = static_cast<const char*>(t.a.dweight) + ((t.v_sum + m) * t.a.dweight_stride + o.n0 + col) * es;
+        for (uint32_t b = 0; b < left; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
+      }
       if (!mbar_wait_pair(&ready[buffer], n >> 1 & 1, &dead, CE_WAIT_READY)) break;
       __syncwarp();
       tmem_fence_after();
+      const uint32_t at = tmem + buffer * 256 + col + (part << 16);
+      if (BACKWARD && !sectors && o.kind == CE_DWEIGHT) {
+        if (col < o.n) ce_out_dweight_turned<DT, WDT>(t, scale, m - lane, o.n0 + col, at, mine);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
+        continue;
+      }
       float x[128];
       uint32_t* const raw = reinterpret_cast<uint32_t*>(x);
-      const uint32_t at = tmem + buffer * 256 + col + (part << 16);
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_load32(at + q * 32, raw + q * 32);
       tmem_wait_loads();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at<false>(cluster_address(&taken[buffer], 0));
-      const uint32_t m = o.m0 + rank * 128 + part + lane;
+      if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
       if constexpr (!BACKWARD) {
-        ce_out_logits(t, k, m, o.n0 + col, x);
+        ce_out_logits(t, k, o, m, o.n0 + col, x);
+      } else if (o.kind == CE_G) {
+        ce_out_g<DT>(t, k, o, scale, m, o.n0 + col, x);
       } else if (col < o.n) {
         if (o.blocks == 0)  // a share without words
 #pragma unroll
           for (int j = 0; j < 128; ++j) x[j] = 0.0f;
-        if (o.kind == CE_G) ce_out_g<DT>(t, k, scale, m, o.n0 + col, x);
-        else if (o.kind == CE_DHIDDEN) ce_out_dhidden(t, k, o, m, o.n0 + col, x);
-        else ce_out_dweight<DT, WDT>(t, scale, m, o.n0 + col, x, mine);
+        if (o.kind == CE_DHIDDEN) ce_out_dhidden(t, k, o, m, o.n0 + col, x);
+        else ce_out_dweight<DT, WDT>(t, scale, m, o.n0 + col, x);
       }
     }
   }

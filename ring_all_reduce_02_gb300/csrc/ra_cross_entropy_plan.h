@@ -18,6 +18,7 @@ inline uint64_t round_up(uint64_t x, uint64_t to) { return (x + to - 1) / to * t
 struct CePlan {
   uint64_t rows_pad, cols_pad;  // hidden's copy: whole tiles of rows, rows of whole blocks of 64
   uint64_t part_rows, parts;    // rows of a CTA of the first kernel, and how many there are
+  uint64_t words;               // of a tile of logits: 256, or as many less as share them out evenly
   uint64_t slots;               // forward: partial sums per row
   uint64_t piece, pieces;       // backward: columns of a piece of g (whole tiles), and how many there are
   uint64_t splits;              // backward: shares of a piece's words that dh is summed over apart
@@ -36,7 +37,6 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
   p.part_rows = round_up((rows + kCeMostParts - 1) / kCeMostParts, 8);
   if (p.part_rows == 0) p.part_rows = 8;
   p.parts = rows ? (rows + p.part_rows - 1) / p.part_rows : 1;
-  p.slots = (vocab + kCeTile - 1) / kCeTile * 2;
   // pieces of about one size, so that no launch is a small one
   uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile;
   if (most < kCeLeastPiece / kCeTile) most = kCeLeastPiece / kCeTile;
@@ -57,6 +57,16 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
     if (p.splits > kCeMostSplits) p.splits = kCeMostSplits;
     if (p.splits < 1) p.splits = 1;
   }
+  p.words = kCeTile;
+  if (!backward || p.pieces == 1) {
+    // where the pairs take few tiles each, narrower ones that make a whole number for every pair
+    const uint64_t high = p.rows_pad / kCeTile, turns = (high * tiles + kCePairs - 1) / kCePairs;
+    const uint64_t most_tiles = turns * kCePairs / high;
+    if (turns && turns <= 8) p.words = round_up((vocab + most_tiles - 1) / most_tiles, 32);
+    if (p.words > kCeTile) p.words = kCeTile;
+    if (p.words < 64) p.words = 64;
+  }
+  p.slots = (vocab + p.words - 1) / p.words * 2;
   uint64_t at = kCeHeader;
   const auto take = [&](uint64_t bytes) {
     const uint64_t here = at;

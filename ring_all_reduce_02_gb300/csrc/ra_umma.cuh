@@ -15,6 +15,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// True in one lane, the same one each time, of a warp that comes here together.
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
+// A value that is the same in all lanes, so that the compiler keeps what follows from it in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -24,18 +32,19 @@ __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-// An arrival at a barrier of either CTA of a pair: with release what this thread has written before it is seen by who
-// waits there. That makes it wait for its stores to global memory too, half a microsecond and more, so an arrival that
-// only says that something has been read comes without.
-template <bool RELEASE>
+// An arrival at a barrier of either CTA of a pair that only says that something has been read. (One with release of the
+// cluster's scope waits for the thread's stores to global memory, half a microsecond and more.)
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
-  if constexpr (RELEASE) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-  else asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-
-// More bytes for the phase that the barrier is in.
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+// 32 bytes to either CTA of a pair, and the arrival at its barrier that says so.
+__device__ __forceinline__ void store_pair(uint32_t cluster_addr, const uint32_t (&w)[8], uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 32;" ::"r"(cluster_bar) : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; i += 4)
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr + 4 * i),
+                 "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(cluster_bar)
+                 : "memory");
 }
 
 constexpr uint64_t kPairWaitNs = 4000000000ull;  // 4 s: more than any tile takes

@@ -198,7 +198,7 @@ enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_DHIDDEN = 2, CE_DWEIGHT = 3, CE_END = 
 
 constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6, kCeRing = 4;
 constexpr uint32_t kCeStageBytes = 4 * kBoxBytes;  // 128 x 64 of the one operand, 128 x 64 of the other
-constexpr uint32_t kCeTurn = 32 * 33 * 4;          // a warp's 32 x 32 results on their way to other lanes
+constexpr uint32_t kCeTurn = 32 * 128;             // a warp's results on their way to other lanes
 constexpr uint32_t kCeSmem = kCeStages * kCeStageBytes + kCeOutWarps * kCeTurn + 1024;
 constexpr uint32_t kCeFew = 256;  // rows, at most, that one tile has all of
 constexpr uint32_t kCeGroup = 8;  // tiles of rows that are worked on together, so that the pairs share words and rows
@@ -296,17 +296,19 @@ __device__ __forceinline__ float ce_load(const void* p, uint64_t i) {
   if constexpr (DT == DT_F32) return static_cast<const float*>(p)[i];
   else return widen16<DT>(static_cast<const uint16_t*>(p)[i]);
 }
-// 32 bytes at a multiple of 32: whole sectors.
-__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-               "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// Results on their way from a lane that holds a row of them to lanes that store 16 bytes each of a few rows: 32 rows of
+// 128 bytes in shared memory, 16-byte chunk c of row r at c ^ r % 8. A lane that stored its own row's sectors one by one
+// (32 lines an instruction) would keep the SM at 9 bytes a cycle.
+__device__ __forceinline__ uint4* ce_chunk(uint8_t* turn, uint32_t row, uint32_t chunk) {
+  return reinterpret_cast<uint4*>(turn + row * 128 + (chunk ^ (row & 7)) * 16);
 }
-__device__ __forceinline__ void ld_sector(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
+// The lane's row: 32 words.
+__device__ __forceinline__ void ce_put(uint8_t* turn, const uint32_t* w) {
+#pragma unroll
+  for (uint32_t c = 0; c < 8; ++c) *ce_chunk(turn, threadIdx.x & 31, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
+// What of it the lane stores in round i: chunk lane % 8 of row 4 i + lane / 8.
+__device__ __forceinline__ uint32_t ce_row_of(uint32_t i) { return 4 * i + (threadIdx.x & 31) / 8; }
 
 // ---- what becomes of a tile's results: a thread has the 128 columns from `col` on of row `m` in x ----
 
@@ -346,9 +348,10 @@ __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k,
 // ones, as far as the products go.
 template <int DT>
 __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, const CeTile& o, float scale, uint32_t m, uint32_t col,
-                                         float (&x)[128]) {
+                                         float (&x)[64], uint8_t* turn) {
+  const uint32_t lane = threadIdx.x & 31, m0 = m - lane, rows = k.dw_blocks * 64;
+  if (m0 >= rows) return;
   const bool counts = m < k.rows;
-  if (m >= k.dw_blocks * 64) return;
   const int32_t target = counts ? t.a.target[m] : 0;
   float d = counts ? __fdiv_rn(t.a.dloss_kept[m], scale) * kCeShift<DT> : 0.0f;
   if (target < 0) d = __int_as_float(0x7fffffff);
@@ -356,95 +359,125 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, cons
   const F2 slope = twice(kLog2e), both = twice(shift), dd = twice(d);
   // the last tile goes on to a whole block of 64
   const uint32_t words = (uint32_t)t.w_out, end = o.n0 + o.n < words ? o.n0 + o.n : (words + 63) / 64 * 64;
-  uint32_t at = counts ? (uint32_t)(target - (int32_t)(t.v_out + col)) : 128u;
-  if (at < 128 && col + at >= o.n0 + o.n) at = 128;
+  if (col >= end) return;
+  uint32_t at = counts ? (uint32_t)(target - (int32_t)(t.v_out + col)) : 64u;
+  if (at < 64 && col + at >= o.n0 + o.n) at = 64;
   float y = 0.0f;
-  if (at < 128) {
+  if (at < 64) {
 #pragma unroll
-    for (int j = 0; j < 128; ++j) y = at == j ? x[j] : y;
+    for (int j = 0; j < 64; ++j) y = at == j ? x[j] : y;
     y = (exp2_approx(__fmaf_rn(y, kLog2e, shift)) - 1.0f) * d;
   }
-  uint16_t* to = static_cast<uint16_t*>(t.g_out) + (uint64_t)m * t.a.piece + col;
   const uint32_t there = !counts || col >= words ? 0 : words - col;
+  char* const to = static_cast<char*>(t.g_out) + ((uint64_t)m0 * t.a.piece + col) * 2;
+  uint32_t w[32];
 #pragma unroll
-  for (int j = 0; j < 128; j += 16) {
-    if (col + j >= end) break;
-    uint32_t w[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      float e, f;
-      split(fma2(pair(x[j + 2 * q], x[j + 2 * q + 1]), slope, both), e, f);
-      split(mul2(pair(exp2_approx(e), exp2_approx(f)), dd), e, f);
-      w[q] = round16x2<DT>(e, f);
-    }
-    if (there < 128) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] &= j + 2 * q + 1 < there ? 0xffffffffu : j + 2 * q < there ? 0xffffu : 0u;
-    }
-    st_sector(to + j, w);
+  for (int q = 0; q < 32; ++q) {
+    float e, f;
+    split(fma2(pair(x[2 * q], x[2 * q + 1]), slope, both), e, f);
+    split(mul2(pair(exp2_approx(e), exp2_approx(f)), dd), e, f);
+    w[q] = round16x2<DT>(e, f);
   }
-  if (at < 128) to[at] = (uint16_t)round16<DT>(y);
+  if (there < 64) {
+#pragma unroll
+    for (int q = 0; q < 32; ++q) w[q] &= 2 * q + 1 < there ? 0xffffffffu : 2 * q < there ? 0xffffu : 0u;
+  }
+  ce_put(turn, w);
+  if (at < 64) reinterpret_cast<uint16_t*>(ce_chunk(turn, lane, at / 8))[at % 8] = (uint16_t)round16<DT>(y);
+  __syncwarp();
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i) {
+    const uint32_t r = ce_row_of(i), c = lane % 8 * 8;
+    if (m0 + r < rows && col + c < end) *reinterpret_cast<uint4*>(to + (r * t.a.piece + c) * 2) = *ce_chunk(turn, r, lane % 8);
+  }
+  __syncwarp();
 }
 
-// A share of dh, added to what the piece before left.
-__device__ __forceinline__ void ce_out_dhidden(const CeTiles& t, const CeWork& k, const CeTile& o, uint32_t m, uint32_t col,
-                                               float (&x)[128]) {
-  if (m >= k.rows) return;
-  float* to = t.a.dh + (o.slot * t.a.rows + m) * t.a.cols_pad + col;
-#pragma unroll
-  for (int j = 0; j < 128; j += 8) {
-    if (col + j >= t.a.cols_pad) break;
-    uint32_t w[8];
-    if (t.v_sum) {
-      ld_sector(to + j, w);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(__uint_as_float(w[q]) + x[j + q]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(x[j + q]);
-    }
-    st_sector(to + j, w);
-  }
-}
-
-// Whether dw's rows are whole sectors.
+// to[m][col] (+)= x f for the warp's rows from m0 to `rows` and its columns up to `cols`: rows of whole 16-byte chunks.
+// The sums that are added are in flight together.
 template <int WDT>
-__device__ __forceinline__ bool ce_sectors(const CeArgs& a) {
-  constexpr uint64_t es = Elem<WDT>::kSize;
-  return (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 32 == 0;
-}
-// dw (+)= scale * x, rows of whole sectors.
-template <int DT, int WDT>
-__device__ __forceinline__ void ce_out_dweight(const CeTiles& t, float scale, uint32_t m, uint32_t col, float (&x)[128]) {
-  constexpr uint32_t es = Elem<WDT>::kSize, V = 32 / es;
-  const uint32_t cols = (uint32_t)t.a.cols;
-  const float f = scale / kCeShift<DT>;
-  if (m >= (uint32_t)t.w_sum) return;
-  char* const to = static_cast<char*>(t.a.dweight) + ((t.v_sum + m) * t.a.dweight_stride + col) * es;
+__device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t m0, uint32_t rows, uint32_t col, uint32_t cols, float f,
+                                            bool add, float (&x)[64], uint8_t* turn) {
+  constexpr uint32_t es = Elem<WDT>::kSize;
+  const uint32_t lane = threadIdx.x & 31;
+  if (m0 >= rows || col >= cols) return;
+  char* const base = static_cast<char*>(to) + (m0 * stride + col) * es;
+  if constexpr (WDT != DT_F32) {
+    if (!add) {  // all 64 columns, rounded
+      uint32_t w[32];
 #pragma unroll
-  for (uint32_t j = 0; j < 128; j += V) {
+      for (int q = 0; q < 32; ++q) w[q] = round16x2<WDT>(x[2 * q] * f, x[2 * q + 1] * f);
+      ce_put(turn, w);
+      __syncwarp();
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t r = ce_row_of(i), c = lane % 8 * 8;
+        if (m0 + r < rows && col + c < cols) *reinterpret_cast<uint4*>(base + (r * stride + c) * es) = *ce_chunk(turn, r, lane % 8);
+      }
+      __syncwarp();
+      return;
+    }
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < 64; j += 32) {
     if (col + j >= cols) break;
-    uint32_t w[8];
-    if (t.a.accumulate) ld_sector(to + j * es, w);
+    const uint32_t c = j + lane % 8 * 4;
+    uint4 old[8];
+    if (add) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if constexpr (WDT == DT_F32) {
-        const float v = x[j + q] * f;
-        w[q] = __float_as_uint(t.a.accumulate ? v + __uint_as_float(w[q]) : v);
-      } else {
-        float u = x[j + 2 * q] * f, v = x[j + 2 * q + 1] * f;
-        if (t.a.accumulate) u += widen16<WDT>(w[q] & 0xffffu), v += widen16<WDT>(w[q] >> 16);
-        w[q] = round16x2<WDT>(u, v);
+      for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t r = ce_row_of(i);
+        old[i] = make_uint4(0, 0, 0, 0);
+        if (m0 + r < rows && col + c < cols) {
+          const char* at = base + (r * stride + c) * es;
+          if constexpr (WDT == DT_F32) {
+            old[i] = *reinterpret_cast<const uint4*>(at);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
+            old[i].x = v.x, old[i].y = v.y;
+          }
+        }
       }
     }
-    st_sector(to + j * es, w);
+    uint32_t w[32];
+#pragma unroll
+    for (int q = 0; q < 32; ++q) w[q] = __float_as_uint(x[j + q] * f);
+    ce_put(turn, w);
+    __syncwarp();
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t r = ce_row_of(i);
+      const uint4 v = *ce_chunk(turn, r, lane % 8);
+      float4 y = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+      if (m0 + r < rows && col + c < cols) {
+        char* at = base + (r * stride + c) * es;
+        if constexpr (WDT == DT_F32) {
+          if (add)
+            y = make_float4(y.x + __uint_as_float(old[i].x), y.y + __uint_as_float(old[i].y), y.z + __uint_as_float(old[i].z),
+                            y.w + __uint_as_float(old[i].w));
+          *reinterpret_cast<float4*>(at) = y;
+        } else {
+          y = make_float4(y.x + widen16<WDT>(old[i].x & 0xffffu), y.y + widen16<WDT>(old[i].x >> 16),
+                          y.z + widen16<WDT>(old[i].y & 0xffffu), y.w + widen16<WDT>(old[i].y >> 16));
+          *reinterpret_cast<uint2*>(at) = make_uint2(round16x2<WDT>(y.x, y.y), round16x2<WDT>(y.z, y.w));
+        }
+      }
+    }
+    __syncwarp();
   }
 }
-// The same for rows that start anywhere, by a warp and from tensor memory (`at`: its 128 columns; rows m0 on): 32 columns
+
+// Whether dw's rows are whole 16-byte chunks.
+template <int WDT>
+__device__ __forceinline__ bool ce_chunks(const CeArgs& a) {
+  constexpr uint64_t es = Elem<WDT>::kSize;
+  return (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 16 == 0;
+}
+// dw (+)= scale * x for rows that start anywhere, by a warp and from tensor memory (`at`: its 128 columns; rows m0 on): 32 columns
 // at a time are turned in shared memory, so that the warp reads and stores 32 columns of a row together, all 32 rows' in
 // flight at once.
 template <int DT, int WDT>
-__device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float scale, uint32_t m0, uint32_t col, uint32_t at, float* turn) {
+__device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float scale, uint32_t m0, uint32_t col, uint32_t at, uint8_t* turn) {
   const uint32_t cols = (uint32_t)t.a.cols, words = (uint32_t)t.w_sum, lane = threadIdx.x & 31;
   const uint32_t high = m0 >= words ? 0 : words - m0 < 32 ? words - m0 : 32;
   const float f = scale / kCeShift<DT>;
@@ -461,11 +494,12 @@ __device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float sc
       for (uint32_t r = 0; r < 32; ++r) old[r] = r < rows ? ce_load<WDT>(t.a.dweight, first + r * t.a.dweight_stride) : 0.0f;
     }
 #pragma unroll
-    for (int q = 0; q < 32; ++q) turn[lane * 33 + q] = __uint_as_float(x[q]) * f;
+    for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * f);
+    ce_put(turn, x);
     __syncwarp();
 #pragma unroll
     for (uint32_t r = 0; r < 32; ++r) {
-      float v = turn[r * 33 + lane];
+      float v = reinterpret_cast<const float*>(ce_chunk(turn, r, lane / 4))[lane % 4];
       if (t.a.accumulate) v += old[r];
       if (r < rows) ce_store<WDT>(t.a.dweight, first + r * t.a.dweight_stride, v);
     }
@@ -648,13 +682,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   } else if (warp >= 4) {
     // the results: warp w has lanes 32 (w % 4) on of tensor memory, the first four warps columns 0 to 127
     const uint32_t part = (warp & 3) * 32, col = (warp - 4) / 4 * 128;
-    float* const mine = reinterpret_cast<float*>(stages + kCeStages * kCeStageBytes + (warp - 4) * kCeTurn);
+    uint8_t* const mine = stages + kCeStages * kCeStageBytes + (warp - 4) * kCeTurn;
     float scale = 1.0f;
     if (BACKWARD) {
       scale = t.w_sum ? t.a.head->scale : ce_scale(t.a);
       if (!t.w_sum && blockIdx.x == 0 && warp == 4 && lane == 0) t.a.head->scale = scale;
     }
-    const bool sectors = BACKWARD && ce_sectors<WDT>(t.a);
+    const bool chunks = BACKWARD && ce_chunks<WDT>(t.a);
     uint32_t n = 0;
     for (CeTile o = next(); o.kind != CE_END && !dead; o = next(), ++n) {
       const uint32_t buffer = n & 1, m = o.m0 + rank * 128 + part + lane;
@@ -669,31 +703,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       __syncwarp();
       tmem_fence_after();
       const uint32_t at = tmem + buffer * 256 + col + (part << 16);
-      if (BACKWARD && !sectors && o.kind == CE_DWEIGHT) {
+      if (BACKWARD && !chunks && o.kind == CE_DWEIGHT) {
         if (col < o.n) ce_out_dweight_turned<DT, WDT>(t, scale, m - lane, o.n0 + col, at, mine);
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
         continue;
       }
-      float x[128];
-      uint32_t* const raw = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_load32(at + q * 32, raw + q * 32);
-      tmem_wait_loads();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
+      const auto release = [&] {
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(cluster_address(&taken[buffer], 0));
+      };
       if constexpr (!BACKWARD) {
-        ce_out_logits(t, k, o, m, o.n0 + col, x);
-      } else if (o.kind == CE_G) {
-        ce_out_g<DT>(t, k, o, scale, m, o.n0 + col, x);
-      } else if (col < o.n) {
-        if (o.blocks == 0)  // a share without words
+        float x[128];
 #pragma unroll
-          for (int j = 0; j < 128; ++j) x[j] = 0.0f;
-        if (o.kind == CE_DHIDDEN) ce_out_dhidden(t, k, o, m, o.n0 + col, x);
-        else ce_out_dweight<DT, WDT>(t, scale, m, o.n0 + col, x);
+        for (int q = 0; q < 4; ++q) tmem_load32(at + q * 32, reinterpret_cast<uint32_t*>(x) + q * 32);
+        tmem_wait_loads();
+        release();
+        ce_out_logits(t, k, o, m, o.n0 + col, x);
+      } else {
+#pragma unroll 1
+        for (uint32_t j = 0; j < 128; j += 64) {
+          float x[64];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) tmem_load32(at + j + q * 32, reinterpret_cast<uint32_t*>(x) + q * 32);
+          tmem_wait_loads();
+          if (j) release();
+          const uint32_t c = o.n0 + col + j;
+          if (o.kind == CE_G) {
+            ce_out_g<DT>(t, k, o, scale, m, c, x, mine);
+          } else if (col + j < o.n) {
+            if (o.blocks == 0)  // a share without words
+#pragma unroll
+              for (int q = 0; q < 64; ++q) x[q] = 0.0f;
+            if (o.kind == CE_DHIDDEN)  // a share of dh, on top of what the piece before left
+              ce_out_rows<DT_F32>(t.a.dh + o.slot * t.a.rows * t.a.cols_pad, t.a.cols_pad, m - lane, k.rows, c, (uint32_t)t.a.cols_pad, 1.0f,
+                                  t.v_sum > 0, x, mine);
+            else
+              ce_out_rows<WDT>(static_cast<char*>(t.a.dweight) + t.v_sum * t.a.dweight_stride * Elem<WDT>::kSize, t.a.dweight_stride,
+                               m - lane, (uint32_t)t.w_sum, c, (uint32_t)t.a.cols, scale / kCeShift<DT>, t.a.accumulate, x, mine);
+          }
+        }
       }
     }
   }

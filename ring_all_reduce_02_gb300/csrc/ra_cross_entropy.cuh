@@ -200,6 +200,7 @@ constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6, kCeRing = 4;
 constexpr uint32_t kCeStageBytes = 4 * kBoxBytes;  // 128 x 64 of the one operand, 128 x 64 of the other
 constexpr uint32_t kCeTurn = 32 * 128;             // a warp's results on their way to other lanes
 constexpr uint32_t kCeSmem = kCeStages * kCeStageBytes + kCeOutWarps * kCeTurn + 1024;
+constexpr uint32_t kCeLong = 8;   // blocks of a tile that the next one is not taken ahead of
 constexpr uint32_t kCeFew = 256;  // rows, at most, that one tile has all of
 constexpr uint32_t kCeGroup = 8;  // tiles of rows that are worked on together, so that the pairs share words and rows
 
@@ -550,6 +551,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
     for (; early < all && early < kCeStages; ++early)
       if (elected()) tma_load_pair(stages + early * kCeStageBytes + 2 * kBoxBytes, &t.w, (int32_t)early * 64, (int32_t)(t.v_out + n0 + rank * half),
                     cluster_address(&full[early], 0));
+    // the rest of the tile as far as L2 (1 x 1024 x 50257: 30.4 us a call without, 29.1 with; the tiles after it as well:
+    // 32.6)
+    for (uint32_t b = early; b < all; ++b)
+      if (elected()) tma_prefetch(&t.w, (int32_t)b * 64, (int32_t)(t.v_out + n0 + rank * half));
   }
   pdl_enter();
   pdl_next();
@@ -666,18 +671,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       if (elected()) umma_commit_pair(&ready[buffer]);
     }
   } else if (warp == 3 && lane == 0 && rank == 0) {
-    // the tiles; the counter is asked for the next one before this one is handed out
+    // The tiles. One is taken as late as keeps the others from waiting for it, so that no pair takes tiles that another
+    // would get to earlier: after a long one as soon as all warps know the one before, after a short one three ahead.
     const uint32_t pairs = gridDim.x / 2;
-    uint32_t i = blockIdx.x / 2, following = atomicAdd(t.counter, 1u);
+    uint32_t ahead = kCeRing;
     for (uint32_t n = 0; !dead; ++n) {
       const uint32_t slot = n % kCeRing;
-      if (n >= kCeRing && !mbar_wait_pair(&turns.empty[slot], (n / kCeRing - 1) & 1, &dead, CE_WAIT_READ)) break;
-      const CeTile o = ce_tile<BACKWARD>(t, k, i);
+      if (n >= ahead && !mbar_wait_pair(&turns.empty[(n - ahead) % kCeRing], (n - ahead) / kCeRing & 1, &dead, CE_WAIT_READ)) break;
+      const CeTile o = ce_tile<BACKWARD>(t, k, n == 0 ? blockIdx.x / 2 : pairs + atomicAdd(t.counter, 1u));
       const uint32_t w[8] = {o.m0, o.n0, o.blocks, o.b0, o.slot, (uint32_t)o.kind | (uint32_t)o.n << 16, 0, 0};
       for (uint32_t to = 0; to < 2; ++to) store_pair(cluster_address(&turns.tile[slot], to), w, cluster_address(&turns.full[slot], to));
       if (o.kind == CE_END) break;
-      i = pairs + following;
-      following = atomicAdd(t.counter, 1u);
+      ahead = o.blocks >= kCeLong ? 2 : kCeRing;
     }
   } else if (warp >= 4) {
     // the results: warp w has lanes 32 (w % 4) on of tensor memory, the first four warps columns 0 to 127

@@ -501,8 +501,8 @@ ra_status_t ra_adamw(const ra_adamw_tensor_t* tensors, int ntensors, ra_dtype_t 
 /*
  * Embedding lookup: out[t] = scale * table[tokens[t]], with accumulate != 0
  * out[t] = out[t] + scale * table[tokens[t]] (position embeddings on top of
- * token embeddings, for one). fp32, rounded once. A token outside [0, vocab)
- * makes its row NaN. out must not overlap the table or the tokens.
+ * token embeddings, for one). fp32, rounded once; a scale that fp32 does not
+ * hold is refused. A token outside [0, vocab) makes its row NaN. out must not overlap the table or the tokens.
  * HBM traffic: reads the distinct rows, writes rows*cols*e.
  */
 ra_status_t ra_embedding_forward(const void* table, size_t table_stride, const void* tokens, size_t index_size,

@@ -1,4 +1,5 @@
 // ra_embedding_forward / _backward: argument checks, scratch, launch shapes.
+#include <float.h>
 #include <math.h>
 
 #include "ra_embedding.cuh"
@@ -12,6 +13,7 @@ using ra::Buffer;
 constexpr uint64_t kMostRows = (1ull << 31) - 1024;
 
 bool lines(const void* p, uint64_t stride_bytes) { return (reinterpret_cast<uintptr_t>(p) | stride_bytes) % 16 == 0; }
+bool scale_ok(double scale) { return fabs(scale) <= FLT_MAX; }  // what fp32 holds
 unsigned ctas(uint64_t units) { return (unsigned)((units + ra::kEmbThreads / 32 - 1) / (ra::kEmbThreads / 32)); }
 
 template <int DT>
@@ -88,7 +90,7 @@ ra_status_t ra_embedding_forward(const void* table, size_t table_stride, const v
   if (st != RA_SUCCESS) return st;
   if ((index_size != 4 && index_size != 8) || rows > kMostRows || vocab > kMostRows || !ra::shape_ok(rows, cols) ||
       !ra::shape_ok(vocab, cols) || !ra::stride_ok(vocab, cols, table_stride) || !ra::stride_ok(rows, cols, out_stride) ||
-      !(fabs(scale) < INFINITY))
+      !scale_ok(scale))
     return RA_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return RA_SUCCESS;
   const uint64_t es = ra::float_size(dtype);
@@ -122,7 +124,7 @@ ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* 
   if (st != RA_SUCCESS) return st;
   if ((index_size != 4 && index_size != 8) || rows > kMostRows || vocab > kMostRows || !ra::shape_ok(rows, cols) ||
       !ra::shape_ok(vocab, cols) || !ra::stride_ok(rows, cols, dy_stride) || !ra::stride_ok(vocab, cols, dtable_stride) ||
-      !(fabs(scale) < INFINITY))
+      !scale_ok(scale))
     return RA_ERR_INVALID_ARG;
   if (vocab == 0 || cols == 0 || (rows == 0 && accumulate)) return RA_SUCCESS;
   const uint64_t es = ra::float_size(dtype), ws = ra::float_size(table_dtype);

@@ -274,7 +274,7 @@ def test_forward_refusals(ra):
     assert call(size=2) == call(size=0) == call(ts=63) == call(os=63) == bad
     assert call(table=0) == call(tokens=0) == call(out=0) == bad
     assert call(table=BASE + 1) == call(tokens=BASE + 4 * MB + 4) == call(out=BASE + 8 * MB + 1) == bad
-    assert call(scale=float("inf")) == call(scale=float("nan")) == bad
+    assert call(scale=float("inf")) == call(scale=float("nan")) == call(scale=1e39) == call(scale=-1e39) == bad
     assert call(rows=1 << 31) == call(vocab=1 << 31) == call(cols=1 << 57, ts=1 << 57, os=1 << 57) == bad
     assert call(out=BASE + 2) == call(out=BASE, os=65) == call(out=BASE + 4 * MB) == alias
     assert call(rows=0) == call(cols=0, ts=0, os=0) == ra.RA_SUCCESS
@@ -291,7 +291,7 @@ def test_backward_refusals(ra):
     assert need > 0 and ra.ra_embedding_workspace(1 << 31, 1, 1) == ra.ra_embedding_workspace(1, 1, 1 << 31) == 0
     assert call(dtype=3) == call(dtype=2, tdtype=1) == call(dtype=0, tdtype=2) == ra.RA_ERR_UNSUPPORTED
     assert call(dtype=5) == call(tdtype=-1) == bad
-    assert call(size=3) == call(ds=63) == call(ts=63) == call(scale=float("nan")) == bad
+    assert call(size=3) == call(ds=63) == call(ts=63) == call(scale=float("nan")) == call(scale=-1e39) == bad
     assert call(dy=0) == call(tokens=0) == call(dt=0) == call(ws=0) == call(nws=need - 1) == call(ws=BASE + 16 * MB + 8) == bad
     assert call(rows=1 << 31) == call(vocab=1 << 31) == bad
     assert call(dt=BASE + 2) == call(dt=BASE, ts=65) == call(ws=BASE) == call(ws=BASE + 8 * MB) == call(dt=BASE + 4 * MB) == alias

@@ -541,8 +541,8 @@ size_t ra_embedding_workspace(size_t rows, size_t cols, size_t vocab);
  * pass. A row whose target is `ignore` has loss 0 and lse 0, costs no products,
  * and its hidden states are not read as numbers (they may be NaN). Any other
  * target outside [0, vocab) makes its row's loss and lse NaN. No output may overlap
- * another buffer. cols == 0 and vocab == 0 are RA_ERR_INVALID_ARG (rows == 0
- * enqueues nothing). workspace: as ra_cross_entropy_workspace says, 16-byte
+ * another buffer. cols == 0, cols above 2^24 and vocab == 0 are
+ * RA_ERR_INVALID_ARG (rows == 0 enqueues nothing). workspace: as ra_cross_entropy_workspace says, 16-byte
  * aligned.
  * Work: 2*rows*cols*vocab operations; HBM traffic: hidden and weight.
  */

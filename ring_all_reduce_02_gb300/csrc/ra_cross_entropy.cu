@@ -13,6 +13,9 @@ using ra::CeArgs;
 using ra::CePlan;
 
 constexpr uint64_t kMostRows = (1ull << 31) - 1024;
+// A tile of logits sums over all columns, by one pair of CTAs: 2^18 blocks take it under a second, and no wait for it
+// comes near its limit.
+constexpr uint64_t kMostCols = 1ull << 24;
 
 unsigned at_most(uint64_t n, uint64_t most) { return (unsigned)(n < most ? n : most); }
 
@@ -21,7 +24,7 @@ bool in_place(const void* weight, uint64_t stride) {
 }
 
 bool sizes_ok(uint64_t rows, uint64_t cols, uint64_t vocab) {
-  return rows <= kMostRows && vocab <= kMostRows && cols <= kMostRows && ra::shape_ok(rows, cols) && ra::shape_ok(vocab, cols);
+  return rows <= kMostRows && vocab <= kMostRows && cols <= kMostCols && ra::shape_ok(rows, cols) && ra::shape_ok(vocab, cols);
 }
 
 template <class... P, class... A>

@@ -451,6 +451,9 @@ def test_forward_refusals(ra):
     assert call(h=0) == call(w=0) == call(t=0) == call(loss=0) == call(lse=0) == call(scratch=0) == bad
     assert call(h=BASE + 1) == call(t=BASE + 4 * MB + 4) == call(loss=BASE + 5 * MB + 2) == call(scratch=BASE + 8 * MB + 8) == bad
     assert call(n=need - 1) == call(rows=1 << 31) == call(vocab=1 << 31) == call(rows=1 << 30, cols=1 << 30, hs=1 << 30, ws=1 << 30) == bad
+    wide = (1 << 24) + 1
+    assert call(rows=1, vocab=1, cols=wide, hs=wide, ws=wide, w=BASE + 64 * MB, t=BASE + 128 * MB, loss=BASE + 129 * MB, lse=BASE + 130 * MB,
+                scratch=BASE + 256 * MB, n=1 << 40) == bad
     assert call(loss=BASE) == call(lse=BASE + 5 * MB + 4) == call(scratch=BASE + 2 * MB) == call(loss=BASE + 4 * MB) == alias
     assert call(rows=0) == ra.RA_SUCCESS
 
@@ -477,7 +480,8 @@ def test_workspace_sizes(ra):
     def size(rows, cols, vocab, backward=0, w=BASE, stride=None, dt=2):
         return ra.lib().ra_cross_entropy_workspace(w, cols if stride is None else stride, rows, cols, vocab, dt, backward)
 
-    assert size(1 << 31, 8, 8) == size(8, 8, 1 << 31) == size(8, 8, 8, dt=0) == size(8, 8, 8, dt=3) == 0
+    assert size(8, 1 << 24, 8) > 0
+    assert size(1 << 31, 8, 8) == size(8, 8, 1 << 31) == size(8, (1 << 24) + 1, 8) == size(8, 8, 8, dt=0) == size(8, 8, 8, dt=3) == 0
     copy = 50257 * 1024 * 2
     assert size(64, 1024, 50257, w=BASE + 2) - size(64, 1024, 50257) >= copy  # not on a 16-byte boundary: a copy of the weight
     assert size(64, 1024, 50257, stride=1025) - size(64, 1024, 50257) >= copy

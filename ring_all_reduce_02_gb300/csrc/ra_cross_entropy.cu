@@ -116,8 +116,10 @@ cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream
                            (a.dweight ? (t.w_sum + 255) / 256 * across : 0);
     err = launch_tiles<DT, WDT, true>(t, tiles, s);
   }
-  if (a.dhidden && a.rows && err == cudaSuccess)
-    err = launch(ra::ce_finish_kernel<DT>, dim3(at_most((a.rows * ((a.cols + 3) / 4) + 255) / 256, 152 * 64)), 256, s, a);
+  if (err == cudaSuccess) {
+    const uint64_t units = a.dhidden && a.rows ? a.rows * ((a.cols + 3) / 4) : 1;
+    err = launch(ra::ce_finish_kernel<DT, WDT>, dim3(at_most((units + 255) / 256, 152 * 64)), 256, s, a);
+  }
   return err;
 }
 

@@ -811,10 +811,16 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const __grid_constant__ Ce
 }
 
 // dh's shares added up, into the rows they belong to; zeros into those that do not count. A thread has four columns.
-template <int DT>
+// dw is stored by then, but for a launch that failed: then it is NaN too.
+template <int DT, int WDT>
 __global__ void __launch_bounds__(256) ce_finish_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
-  const float scale = a.head->failed ? __int_as_float(0x7fffffff) : a.head->scale / kCeShift<DT>;
+  const bool failed = a.head->failed != 0;
+  if (failed && a.dweight)
+    for (uint64_t v = blockIdx.x; v < a.vocab; v += gridDim.x)
+      for (uint64_t c = threadIdx.x; c < a.cols; c += 256) ce_store<WDT>(a.dweight, v * a.dweight_stride + c, __int_as_float(0x7fffffff));
+  if (a.dhidden == nullptr) return;
+  const float scale = failed ? __int_as_float(0x7fffffff) : a.head->scale / kCeShift<DT>;
   const uint32_t across = (uint32_t)((a.cols + 3) / 4);
   const uint64_t each = a.rows * a.cols_pad;
   const bool whole = ((reinterpret_cast<uintptr_t>(a.dhidden) | a.dhidden_stride * 2) & 7) == 0;

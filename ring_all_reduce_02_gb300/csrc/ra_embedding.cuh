@@ -693,6 +693,7 @@ __global__ void __launch_bounds__(kEmbThreads, 4) embedding_sum_kernel(const __g
       if (!VEC) __syncwarp();
       ask(i + kFlight);
     }
+    __syncwarp();  // a tail takes the place of rows that other lanes have read
     if (!(ends >> (count - 1) & 1)) {  // the last places go on
       put(inside ? tails(warp) : heads + warp * (8 * N), sum);
       what |= inside ? TAIL : HEAD;

@@ -70,7 +70,7 @@ namespace ra {
 // are visible before any global load or store, so the stream order is kept.
 // On GB300, 16-32 MiB all-reduces launched back to back gained 2-4 points of
 // the copy bandwidth, and the 33 DDP buckets of a GPT-2-medium gradient ran
-// 1.6% faster. The kernels do not signal their dependents early
+// 1.6% faster. The collective kernels do not signal their dependents early
 // (griddepcontrol.launch_dependents): CTAs of the next launch then sat on the
 // SMs beside a running kernel that left registers free, and the fp32
 // reduce-scatter at N = 3 ran at half speed.

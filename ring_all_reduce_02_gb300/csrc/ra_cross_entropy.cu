@@ -92,16 +92,20 @@ template <int DT, int WDT>
 cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream_t s) {
   ra::CeTiles t = {};
   t.a = a;
-  CUtensorMap g[2], g_own[2];
+  CUtensorMap g[2], g_own[2], g_store[2];
   t.w_groups = a.w != a.weight || a.cols % 64 == 0;
   cudaError_t err = encode_logits(t, DT);
   if (err == cudaSuccess) err = encode(&t.h_own, DT, a.h, a.cols_pad, a.rows_pad, a.cols_pad, 64, true);
   if (err == cudaSuccess)
     err = t.w_groups ? encode(&t.w_own, DT, a.w, (a.cols + 63) / 64 * 64, a.vocab, a.w_stride, 64, true)
                      : encode(&t.w_own, DT, a.w, a.cols, a.vocab, a.w_stride, 64);
+  constexpr uint64_t es = ra::Elem<WDT>::kSize;
+  t.chunks = a.dweight && (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 16 == 0 && a.dweight_stride < 1ull << 38;
+  if (t.chunks && es == 2 && !a.accumulate && err == cudaSuccess) err = encode(&t.dw_store, DT, a.dweight, a.cols, a.vocab, a.dweight_stride, 32);
   for (uint64_t i = 0; i < 2 && i < a.pieces && err == cudaSuccess; ++i) {
     err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, a.rows <= ra::kCeFew ? 64 : 128);
     if (err == cudaSuccess) err = encode(&g_own[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 64, true);
+    if (err == cudaSuccess) err = encode(&g_store[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 32);
   }
   if (err == cudaSuccess) err = rows_and_operands<true>(a, s);
   const auto width = [&](uint64_t piece) { return piece >= a.pieces ? 0 : a.vocab - piece * a.piece < a.piece ? a.vocab - piece * a.piece : a.piece; };
@@ -109,6 +113,7 @@ cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream
     t.v_out = i * a.piece, t.w_out = width(i), t.g_out = scratch + p.g[i % 2];
     t.v_sum = i ? (i - 1) * a.piece : 0, t.w_sum = i ? width(i - 1) : 0;
     if (i) t.g = g[(i + 1) % 2], t.g_own = g_own[(i + 1) % 2];
+    if (i < a.pieces) t.g_store = g_store[i % 2];
     t.counter = a.counters + i;
     t.early = i == 0 && a.rows <= ra::kCeFew && a.w == a.weight;
     const uint64_t rows = a.rows_pad / 256, across = (a.cols + 255) / 256;

@@ -209,6 +209,7 @@ struct CeTiles {
   // h's and g's are of 64 rows), and of two groups of 64 with rows along their own (h_own, w_own, g_own). Where w's
   // rows are no whole groups, w_own's boxes are of one.
   CUtensorMap h, w, g, h_own, w_own, g_own;
+  CUtensorMap g_store, dw_store;  // boxes of 32 rows of 64 columns
   CeArgs a;
   void* g_out;              // the piece that is computed (forward: none)
   uint64_t v_sum, w_sum;    // first word and words of the one piece (none: 0 words)
@@ -216,6 +217,7 @@ struct CeTiles {
   uint32_t* counter;
   int early;                // the first tiles' words may be asked for before the launch before this one has ended
   int w_groups;             // w_own's boxes are of two groups
+  int chunks;               // dw's rows are whole 16-byte chunks
 };
 
 // A tile as it is handed to the warps that work on it.
@@ -303,10 +305,22 @@ __device__ __forceinline__ float ce_load(const void* p, uint64_t i) {
 __device__ __forceinline__ uint4* ce_chunk(uint8_t* turn, uint32_t row, uint32_t chunk) {
   return reinterpret_cast<uint4*>(turn + row * 128 + (chunk ^ (row & 7)) * 16);
 }
+// What ce_send sent has left, before the warp puts anything there.
+__device__ __forceinline__ void ce_free() {
+  if ((threadIdx.x & 31) == 0) tma_stores_read();
+  __syncwarp();
+}
 // The lane's row: 32 words.
 __device__ __forceinline__ void ce_put(uint8_t* turn, const uint32_t* w) {
 #pragma unroll
   for (uint32_t c = 0; c < 8; ++c) *ce_chunk(turn, threadIdx.x & 31, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
+// The 32 rows on their way to box (x, y), while the warp goes on (61 x 1024 x 50257 bf16: 103 us with 16 bytes from each
+// lane, 86 so).
+__device__ __forceinline__ void ce_send(const CUtensorMap* map, const uint8_t* turn, uint32_t x, uint64_t y) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tma_store(map, turn, (int32_t)x, (int32_t)y);
 }
 // What of it the lane stores in round i: chunk lane % 8 of row 4 i + lane / 8.
 __device__ __forceinline__ uint32_t ce_row_of(uint32_t i) { return 4 * i + (threadIdx.x & 31) / 8; }
@@ -383,9 +397,14 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, cons
 #pragma unroll
     for (int q = 0; q < 32; ++q) w[q] &= 2 * q + 1 < there ? 0xffffffffu : 2 * q < there ? 0xffffu : 0u;
   }
+  ce_free();
   ce_put(turn, w);
   if (at < 64) reinterpret_cast<uint16_t*>(ce_chunk(turn, lane, at / 8))[at % 8] = (uint16_t)round16<DT>(y);
-  __syncwarp();
+  if (col + 64 <= end) {
+    ce_send(&t.g_store, turn, col, m0);
+    return;
+  }
+  __syncwarp();  // the columns behind are another tile's
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i) {
     const uint32_t r = ce_row_of(i), c = lane % 8 * 8;
@@ -395,10 +414,11 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, cons
 }
 
 // to[m][col] (+)= x f for the warp's rows from m0 to `rows` and its columns up to `cols`: rows of whole 16-byte chunks.
-// The sums that are added are in flight together.
+// The sums that are added are in flight together. 16-bit results that are not added go through `map`, whose row y0 is
+// row 0 here.
 template <int WDT>
 __device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t m0, uint32_t rows, uint32_t col, uint32_t cols, float f,
-                                            bool add, float (&x)[64], uint8_t* turn) {
+                                            bool add, float (&x)[64], uint8_t* turn, const CUtensorMap* map, uint64_t y0) {
   constexpr uint32_t es = Elem<WDT>::kSize;
   const uint32_t lane = threadIdx.x & 31;
   if (m0 >= rows || col >= cols) return;
@@ -408,17 +428,13 @@ __device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t 
       uint32_t w[32];
 #pragma unroll
       for (int q = 0; q < 32; ++q) w[q] = round16x2<WDT>(x[2 * q] * f, x[2 * q + 1] * f);
+      ce_free();
       ce_put(turn, w);
-      __syncwarp();
-#pragma unroll
-      for (uint32_t i = 0; i < 8; ++i) {
-        const uint32_t r = ce_row_of(i), c = lane % 8 * 8;
-        if (m0 + r < rows && col + c < cols) *reinterpret_cast<uint4*>(base + (r * stride + c) * es) = *ce_chunk(turn, r, lane % 8);
-      }
-      __syncwarp();
+      ce_send(map, turn, col, y0 + m0);
       return;
     }
   }
+  ce_free();
 #pragma unroll
   for (uint32_t j = 0; j < 64; j += 32) {
     if (col + j >= cols) break;
@@ -468,12 +484,6 @@ __device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t 
   }
 }
 
-// Whether dw's rows are whole 16-byte chunks.
-template <int WDT>
-__device__ __forceinline__ bool ce_chunks(const CeArgs& a) {
-  constexpr uint64_t es = Elem<WDT>::kSize;
-  return (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 16 == 0;
-}
 // dw (+)= scale * x for rows that start anywhere, by a warp and from tensor memory (`at`: its 128 columns; rows m0 on): 32 columns
 // at a time are turned in shared memory, so that the warp reads and stores 32 columns of a row together, all 32 rows' in
 // flight at once.
@@ -482,6 +492,7 @@ __device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float sc
   const uint32_t cols = (uint32_t)t.a.cols, words = (uint32_t)t.w_sum, lane = threadIdx.x & 31;
   const uint32_t high = m0 >= words ? 0 : words - m0 < 32 ? words - m0 : 32;
   const float f = scale / kCeShift<DT>;
+  ce_free();
 #pragma unroll 1
   for (uint32_t j = 0; j < 128 && col + j < cols; j += 32) {
     uint32_t x[32];
@@ -693,7 +704,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       scale = t.w_sum ? t.a.head->scale : ce_scale(t.a);
       if (!t.w_sum && blockIdx.x == 0 && warp == 4 && lane == 0) t.a.head->scale = scale;
     }
-    const bool chunks = BACKWARD && ce_chunks<WDT>(t.a);
     uint32_t n = 0;
     for (CeTile o = next(); o.kind != CE_END && !dead; o = next(), ++n) {
       const uint32_t buffer = n & 1, m = o.m0 + rank * 128 + part + lane;
@@ -708,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       __syncwarp();
       tmem_fence_after();
       const uint32_t at = tmem + buffer * 256 + col + (part << 16);
-      if (BACKWARD && !chunks && o.kind == CE_DWEIGHT) {
+      if (BACKWARD && !t.chunks && o.kind == CE_DWEIGHT) {
         if (col < o.n) ce_out_dweight_turned<DT, WDT>(t, scale, m - lane, o.n0 + col, at, mine);
         tmem_fence_before();
         __syncwarp();
@@ -744,14 +754,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
               for (int q = 0; q < 64; ++q) x[q] = 0.0f;
             if (o.kind == CE_DHIDDEN)  // a share of dh, on top of what the piece before left
               ce_out_rows<DT_F32>(t.a.dh + o.slot * t.a.rows * t.a.cols_pad, t.a.cols_pad, m - lane, k.rows, c, (uint32_t)t.a.cols_pad, 1.0f,
-                                  t.v_sum > 0, x, mine);
+                                  t.v_sum > 0, x, mine, nullptr, 0);
             else
               ce_out_rows<WDT>(static_cast<char*>(t.a.dweight) + t.v_sum * t.a.dweight_stride * Elem<WDT>::kSize, t.a.dweight_stride,
-                               m - lane, (uint32_t)t.w_sum, c, (uint32_t)t.a.cols, scale / kCeShift<DT>, t.a.accumulate, x, mine);
+                               m - lane, (uint32_t)t.w_sum, c, (uint32_t)t.a.cols, scale / kCeShift<DT>, t.a.accumulate, x, mine,
+                               &t.dw_store, t.v_sum);
           }
         }
       }
     }
+    if (lane == 0) tma_stores_written();
   }
   __syncwarp();
   __syncthreads();

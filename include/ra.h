@@ -526,7 +526,8 @@ ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* 
                                   size_t cols, size_t vocab, double scale, ra_dtype_t dtype, ra_dtype_t table_dtype,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace ra_embedding_backward needs (0: a size it does not take). Host only. */
+/* Bytes of workspace ra_embedding_backward needs (0: a size it does not take). Fewer rows may need more than many: ask
+ * for each size that is called. Host only. */
 size_t ra_embedding_workspace(size_t rows, size_t cols, size_t vocab);
 
 /*
@@ -580,7 +581,9 @@ ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, 
  * is read in place where it starts on a 16-byte boundary and its stride is a
  * multiple of 16 bytes; otherwise the workspace holds a copy of it, so the
  * answer depends on weight and weight_stride (the address alone is looked at).
- * The backward pass holds two pieces of g, each 192 MiB at most or 1024 columns. Host only.
+ * The backward pass holds two pieces of g, each 192 MiB at most or 1024 columns;
+ * the forward pass 16 bytes a row for each 256 words or less. Fewer rows may need
+ * more than many: ask for each size that is called. Host only.
  */
 size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
                                   ra_dtype_t dtype, int backward);

@@ -755,7 +755,8 @@ def ra_embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bo
 
 
 def ra_cross_entropy_workspace(hidden, weight, backward: bool = False) -> int:
-    """Bytes of workspace ra_cross_entropy_forward (or ra_cross_entropy_backward) needs for these tensors."""
+    """Bytes of workspace ra_cross_entropy_forward (or ra_cross_entropy_backward) needs for these tensors (fewer rows may
+    need more)."""
     if len(hidden.shape) != 2 or len(weight.shape) != 2:
         raise ValueError("ra_cross_entropy_workspace: hidden and weight must be tensors of two dimensions")
     vocab, cols = weight.shape

@@ -38,10 +38,19 @@ cudaError_t sort_one(const ra::EmbBackward& a, unsigned zeros, cudaStream_t s) {
 
 // Sorts the tokens, and clears the table beside that.
 cudaError_t sort(ra::EmbBackward& a, const ra::EmbPlan& p, bool clear, cudaStream_t s) {
-    // 32768 x 8192 bf16 into 50257 rows: 270 us a call with 304 CTAs that clear, 243 with 1216. Leaving out the rows that
+  // 32768 x 8192 bf16 into 50257 rows: 270 us a call with 304 CTAs that clear, 243 with 1216. Leaving out the rows that
   // have a token, which the sums write again, cost more in looking for them than their bytes (290).
   const unsigned zeros = clear ? 1216 : 0;
-  if (p.one) return a.rows <= 2048 ? sort_one<256, 1>(a, zeros, s) : a.rows <= 8192 ? sort_one<256, 4>(a, zeros, s) : sort_one<512, 8>(a, zeros, s);
+  // As few tokens to a thread as hold them all (12000 / 16384 / 20011 tokens, us a call: 8 to each of 512 threads 25.3 / 30.9 /
+  // 32.3; 4, 4 and 6 22.0 / 27.3 / 30.2; twice as many to each of 256 22.3 / 27.5 / 30.7). 4096: 4 to each of 256 15.0, 2 14.0.
+  // More threads wait longer at the barriers (8192: 1 to each of 1024 19.4, 4 to each of 256 18.6).
+  if (p.one) {
+    if (a.rows <= 2048) return sort_one<256, 1>(a, zeros, s);
+    if (a.rows <= 4096) return sort_one<256, 2>(a, zeros, s);
+    if (a.rows <= 8192) return sort_one<256, 4>(a, zeros, s);
+    if (a.rows <= 16384) return sort_one<512, 4>(a, zeros, s);
+    return a.rows <= 24576 ? sort_one<512, 6>(a, zeros, s) : sort_one<512, 8>(a, zeros, s);
+  }
   cudaError_t err = cudaSuccess;
   for (uint32_t pass = 0; pass < a.passes && err == cudaSuccess; ++pass) {
     err = ra::launch_programmatic(ra::embedding_count_kernel, dim3(a.tiles + (pass == 0 ? zeros : 0)), ra::kEmbThreads, 0, s, a, pass);

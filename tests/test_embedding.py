@@ -113,6 +113,18 @@ def test_forward_and_backward(ra, rows, cols, vocab, dtype, index):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("vocab", [300, 2 ** 17 - 1, 2 ** 17])
+@pytest.mark.parametrize("rows", [2048, 2049, 4096, 4097, 8192, 8193, 16384, 16385, 24576, 24577, 32768, 32769])
+def test_ends_of_the_sorts_ranges(ra, rows, vocab):
+    gpu()
+    gen = torch.Generator().manual_seed(rows + vocab)
+    for kind in ("any", "descending"):
+        tokens = draw_tokens(kind, rows, vocab, gen, I64)
+        tokens[::97] = vocab - 1
+        check_backward(ra, matrix(rows, 8, BF16, gen), tokens, matrix(vocab, 8, F32, gen), 1.0, True, padding=7)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["one", "ends", "descending"])
 @pytest.mark.parametrize("rows,cols,vocab", [(1, 64, 9), (31, 40, 1), (256, 72, 3), (300, 65, 2), (5000, 64, 333), (40000, 24, 50257), (70001, 17, 9)])
 def test_orders_and_repeats(ra, rows, cols, vocab, kind):

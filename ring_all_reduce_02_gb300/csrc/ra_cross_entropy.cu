@@ -66,9 +66,9 @@ cudaError_t encode_logits(ra::CeTiles& t, int dtype) {
 }
 
 // Every SM has a CTA at most; all rows are taken to count.
-template <int DT, int WDT, bool BACKWARD>
+template <int DT, int WDT, bool BACKWARD, bool CHUNKS>
 cudaError_t launch_tiles(const ra::CeTiles& t, uint64_t tiles, cudaStream_t s) {
-  const auto kernel = ra::ce_tiles_kernel<DT, WDT, BACKWARD>;
+  const auto kernel = ra::ce_tiles_kernel<DT, WDT, BACKWARD, CHUNKS>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ra::kCeSmem);
   return err != cudaSuccess ? err
                             : ra::launch_programmatic(kernel, dim3(2 * at_most(tiles, ra::kCePairs)), ra::kCeThreads, ra::kCeSmem, s, t);
@@ -81,7 +81,7 @@ cudaError_t forward(const CeArgs& a, cudaStream_t s) {
   cudaError_t err = encode_logits(t, DT);
   if (err == cudaSuccess) err = rows_and_operands<false>(a, s);
   t.early = a.rows <= ra::kCeFew && a.w == a.weight;
-  if (err == cudaSuccess) err = launch_tiles<DT, DT, false>(t, a.rows_pad / 256 * (a.slots / 2), s);
+  if (err == cudaSuccess) err = launch_tiles<DT, DT, false, true>(t, a.rows_pad / 256 * (a.slots / 2), s);
   if (err != cudaSuccess) return err;
   // few rows: a CTA to each
   return a.rows <= 512 ? launch(ra::ce_join_kernel<8>, dim3((unsigned)a.rows), 256, s, a)
@@ -100,8 +100,8 @@ cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream
     err = t.w_groups ? encode(&t.w_own, DT, a.w, (a.cols + 63) / 64 * 64, a.vocab, a.w_stride, 64, true)
                      : encode(&t.w_own, DT, a.w, a.cols, a.vocab, a.w_stride, 64);
   constexpr uint64_t es = ra::Elem<WDT>::kSize;
-  t.chunks = a.dweight && (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 16 == 0 && a.dweight_stride < 1ull << 38;
-  if (t.chunks && es == 2 && !a.accumulate && err == cudaSuccess) err = encode(&t.dw_store, DT, a.dweight, a.cols, a.vocab, a.dweight_stride, 32);
+  const bool chunks = (reinterpret_cast<uintptr_t>(a.dweight) | a.dweight_stride * es | a.cols * es) % 16 == 0 && a.dweight_stride < 1ull << 38;
+  if (chunks && a.dweight && es == 2 && !a.accumulate && err == cudaSuccess) err = encode(&t.dw_store, DT, a.dweight, a.cols, a.vocab, a.dweight_stride, 32);
   for (uint64_t i = 0; i < 2 && i < a.pieces && err == cudaSuccess; ++i) {
     err = encode(&g[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, a.rows <= ra::kCeFew ? 64 : 128);
     if (err == cudaSuccess) err = encode(&g_own[i], DT, scratch + p.g[i], a.piece, a.rows_pad, a.piece, 64, true);
@@ -119,7 +119,7 @@ cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream
     const uint64_t rows = a.rows_pad / 256, across = (a.cols + 255) / 256;
     const uint64_t tiles = rows * ((t.w_out + a.words - 1) / a.words) + (a.dhidden && t.w_sum ? rows * across * a.splits : 0) +
                            (a.dweight ? (t.w_sum + 255) / 256 * across : 0);
-    err = launch_tiles<DT, WDT, true>(t, tiles, s);
+    err = chunks || !a.dweight ? launch_tiles<DT, WDT, true, true>(t, tiles, s) : launch_tiles<DT, WDT, true, false>(t, tiles, s);
   }
   if (err == cudaSuccess) {
     const uint64_t units = a.dhidden && a.rows ? a.rows * ((a.cols + 3) / 4) : 1;

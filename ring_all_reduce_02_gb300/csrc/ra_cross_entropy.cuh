@@ -197,7 +197,7 @@ constexpr float kCeShift = DT == DT_F16 ? 16384.0f : 1.0f;
 // PFLOP/s; back to back the board's power holds the clock lower, 487 us a call, 1.73 PFLOP/s (a library product of such
 // sizes, columns whole 16 bytes, burst / long loop: 1.90 / 1.71). Its backward pass: 1570 us for 2.53 PFLOP, 1.61 PFLOP/s;
 // the launches' ends, where pairs run out of tiles, are most of the rest. Few rows are bound by the words' stream: 1 row, 103
-// MB in 25 us of a call's 29, with products of which 255 rows of 256 are empty (43% of the pipe); of 61 rows' gradients 86 us,
+// MB in 25 us of a call's 29, with products of which 255 rows of 256 are empty (43% of the pipe); of 61 rows' gradients 79 us,
 // the words read twice and dw written once, 309 MB in all.
 
 // A wait that gave up.
@@ -225,7 +225,6 @@ struct CeTiles {
   uint32_t* counter;
   int early;                // the first tiles' words may be asked for before the launch before this one has ended
   int w_groups;             // w_own's boxes are of two groups
-  int chunks;               // dw's rows are whole 16-byte chunks
 };
 
 // A tile as it is handed to the warps that work on it.
@@ -323,8 +322,8 @@ __device__ __forceinline__ void ce_put(uint8_t* turn, const uint32_t* w) {
 #pragma unroll
   for (uint32_t c = 0; c < 8; ++c) *ce_chunk(turn, threadIdx.x & 31, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
-// The 32 rows on their way to box (x, y), while the warp goes on (61 x 1024 x 50257 bf16: 103 us with 16 bytes from each
-// lane, 86 so).
+// The 32 rows on their way to box (x, y), while the warp goes on (16 bytes from each lane instead: 17 us more a call of 61 x
+// 1024 x 50257 bf16).
 __device__ __forceinline__ void ce_send(const CUtensorMap* map, const uint8_t* turn, uint32_t x, uint64_t y) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
@@ -533,7 +532,9 @@ struct CeTurns {
   uint64_t full[kCeRing], empty[kCeRing];
 };
 
-template <int DT, int WDT, bool BACKWARD>
+// CHUNKS: dw's rows are whole 16-byte chunks. The two ways to store it are kernels of their own: in one, registers run out (61 x
+// 1024 x 50257 bf16 85 us a call against 79, 1537 x 768 x 10007 fp16 added 74 against 69).
+template <int DT, int WDT, bool BACKWARD, bool CHUNKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_tiles_kernel(const __grid_constant__ CeTiles t) {
   extern __shared__ uint8_t dynamic[];
   __shared__ uint64_t full[kCeStages], empty[kCeStages], ready[2], taken[2];
@@ -726,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       __syncwarp();
       tmem_fence_after();
       const uint32_t at = tmem + buffer * 256 + col + (part << 16);
-      if (BACKWARD && !t.chunks && o.kind == CE_DWEIGHT) {
+      if (BACKWARD && !CHUNKS && o.kind == CE_DWEIGHT) {
         if (col < o.n) ce_out_dweight_turned<DT, WDT>(t, scale, m - lane, o.n0 + col, at, mine);
         tmem_fence_before();
         __syncwarp();
@@ -763,7 +764,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
             if (o.kind == CE_DHIDDEN)  // a share of dh, on top of what the piece before left
               ce_out_rows<DT_F32>(t.a.dh + o.slot * t.a.rows * t.a.cols_pad, t.a.cols_pad, m - lane, k.rows, c, (uint32_t)t.a.cols_pad, 1.0f,
                                   t.v_sum > 0, x, mine, nullptr, 0);
-            else
+            else if constexpr (CHUNKS)
               ce_out_rows<WDT>(static_cast<char*>(t.a.dweight) + t.v_sum * t.a.dweight_stride * Elem<WDT>::kSize, t.a.dweight_stride,
                                m - lane, (uint32_t)t.w_sum, c, (uint32_t)t.a.cols, scale / kCeShift<DT>, t.a.accumulate, x, mine,
                                &t.dw_store, t.v_sum);

@@ -37,7 +37,9 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
   p.part_rows = round_up((rows + kCeMostParts - 1) / kCeMostParts, 8);
   if (p.part_rows == 0) p.part_rows = 8;
   p.parts = rows ? (rows + p.part_rows - 1) / p.part_rows : 1;
-  // pieces of about one size, so that no launch is a small one
+  // Pieces of about one size, so that no launch is a small one. With few rows all words are one piece, although they are read
+  // a second time from HBM then: pieces whose words stay in L2 (61 x 1024 x 50257 bf16: 2 pieces 105 us a call, 4 132, one 85)
+  // pay more for their launches' ends.
   uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile;
   if (most < kCeLeastPiece / kCeTile) most = kCeLeastPiece / kCeTile;
   const uint64_t tiles = (vocab + kCeTile - 1) / kCeTile;
@@ -47,10 +49,10 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
     p.piece = each * kCeTile;
     p.pieces = (tiles + each - 1) / each;
     // few rows make few tiles of dh, each a sum over all words of a piece: as many shares as keep a tile's work below
-    // half of a pair's, in blocks of 64 summed elements. Storing a tile's results counts as 4 of them (61 x 1024 x 50257 /
-    // 200 x 1024 x 50257 / 500 x 768 x 32000 bf16, us a call: 2: 88.0 / 90.5 / 76.7, 4: 84.3 / 93.9 / 76.4, 6: 85.4 / 97.2 /
-    // 79.4, 14: 96.8 / 103 / 82.9).
-    constexpr uint64_t kCeStore = 4;
+    // half of a pair's, in blocks of 64 summed elements. Storing a tile's results counts as 3 of them (61 x 1024 x 50257 /
+    // 200 x 1024 x 50257 / 500 x 768 x 32000 bf16, us a call: 1: 82.8 / 86.3 / 73.2, 2: 81.0 / 85.1 / 73.2, 3: 78.5 / 86.9 /
+    // 72.7, 4: 78.2 / 89.2 / 72.7, 6: 80.6 / 91.7 / 75.5).
+    constexpr uint64_t kCeStore = 3;
     const uint64_t across = (cols + kCeTile - 1) / kCeTile, words = p.piece / 64;
     const uint64_t dh = p.rows_pad / kCeTile * across;
     const uint64_t work = dh * words + (words / 4) * across * ((rows + 63) / 64 + kCeStore) + p.rows_pad / kCeTile * (words / 4) * ((cols + 63) / 64 + kCeStore);

@@ -49,8 +49,8 @@ __device__ __forceinline__ void store_pair(uint32_t cluster_addr, const uint32_t
 
 constexpr uint64_t kPairWaitNs = 4000000000ull;  // 4 s: more than any tile takes
 // As mbar_wait. An acquire of the CTA's scope does for arrivals from the other one: what is read behind it lies in this
-// CTA's shared memory or in tensor memory (one of the cluster's scope also empties the L1 cache, at 0.3 us). Where it gives up, `what` says in *dead which wait did; where the
-// CTA already has, it gives up at once.
+// CTA's shared memory or in tensor memory (one of the cluster's scope also empties the L1 cache, at 0.3 us). Where it gives
+// up, `what` says in *dead which wait did; where the CTA already has, it gives up at once.
 __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead, int what) {
   uint64_t start = 0;
   while (true) {

@@ -203,6 +203,25 @@ def test_strides_and_alignment(ra, dtype, cols, pad, shift):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows,cols,pad,vocab", [(70, 64, 64, 300), (70, 72, 8, 33), (300, 200, 56, 601), (9, 264, 248, 1025), (300, 65, 1, 290),
+                                                 (40, 8, 8, 31)])
+def test_columns_between_others(ra, dtype, accumulate, rows, cols, pad, vocab):
+    # the gradients of a slice of a wider matrix's columns, of both types: its other columns and the rows behind it stay
+    gpu()
+    gen = generator(rows + cols)
+    h, w = matrix(rows, cols, dtype, gen), matrix(vocab, cols, dtype, gen, std=0.1)
+    targets = draw_targets(rows, vocab, gen, I64, [1])
+    lse = check_forward(ra, h, w, targets)
+    for wdtype in (dtype, F32):
+        for first in (0, pad):
+            wide = torch.full((vocab + 2, cols + pad), 7.0, dtype=wdtype, device="cuda")
+            check_backward(ra, h, w, targets, lse, None, torch.full_like(h, 7.0), wide[:vocab, first:first + cols], accumulate)
+            assert (wide[vocab:] == 7).all() and (wide[:, :first] == 7).all() and (wide[:, first + cols:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
 def test_one_gradient_alone(ra, dtype):
     gpu()
     rows, cols, vocab = 300, 96, 900

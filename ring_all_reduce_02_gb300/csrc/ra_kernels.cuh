@@ -84,8 +84,9 @@ __device__ __forceinline__ void pdl_enter() {
 #endif
 }
 
-// Lets the next launch on the stream be placed as soon as every CTA of this one has come here. For the short first
-// kernels of a call, whose successor is the call's own and finds room beside them.
+// Lets the next launch on the stream be placed as soon as every CTA of this one has come here. For kernels whose successor
+// is the call's own: the short first ones, beside which it finds room, and those whose CTAs fill an SM's shared memory, where
+// it moves in as they leave.
 __device__ __forceinline__ void pdl_next() {
 #if RA_PDL
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

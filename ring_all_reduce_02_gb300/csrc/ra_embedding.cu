@@ -41,6 +41,8 @@ cudaError_t sort(ra::EmbBackward& a, const ra::EmbPlan& p, bool clear, cudaStrea
   // 32768 x 8192 bf16 into 50257 rows: 270 us a call with 304 CTAs that clear, 243 with 1216. Leaving out the rows that
   // have a token, which the sums write again, cost more in looking for them than their bytes (290).
   const unsigned zeros = clear ? 1216 : 0;
+  // no tokens: a table that is cleared, whatever its size, and no launch of no CTAs
+  if (a.rows == 0) return ra::launch_programmatic(ra::embedding_count_kernel, dim3(zeros), ra::kEmbThreads, 0, s, a, 0u);
   // As few tokens to a thread as hold them all (12000 / 16384 / 20011 tokens, us a call: 8 to each of 512 threads 25.3 / 30.9 /
   // 32.3; 4, 4 and 6 22.0 / 27.3 / 30.2; twice as many to each of 256 22.3 / 27.5 / 30.7). 4096: 4 to each of 256 15.0, 2 14.0.
   // More threads wait longer at the barriers (8192: 1 to each of 1024 19.4, 4 to each of 256 18.6).

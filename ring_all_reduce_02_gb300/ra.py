@@ -760,7 +760,7 @@ def ra_cross_entropy_workspace(hidden, weight, backward: bool = False) -> int:
     if len(hidden.shape) != 2 or len(weight.shape) != 2:
         raise ValueError("ra_cross_entropy_workspace: hidden and weight must be tensors of two dimensions")
     vocab, cols = weight.shape
-    return lib().ra_cross_entropy_workspace(weight.data_ptr(), _row_stride(weight, cols), hidden.shape[0], cols, vocab,
+    return lib().ra_cross_entropy_workspace(weight.data_ptr(), _pitch(weight, cols), hidden.shape[0], cols, vocab,
                                             _float_code(weight, "ra_cross_entropy_workspace"), backward)
 
 

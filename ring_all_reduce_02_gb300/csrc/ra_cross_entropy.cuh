@@ -179,6 +179,10 @@ __device__ __forceinline__ float ce_scale(const CeArgs& a) {
 // fp16 holds g times 2^14, where it keeps its digits down to 2^-28 and its multiples of 2^-38.
 template <int DT>
 constexpr float kCeShift = DT == DT_F16 ? 16384.0f : 1.0f;
+// A sum of such values as the gradient that it is. The power of two goes from the sum, which keeps all its digits, and not
+// from the scale: one below 2^-112 would be subnormal after it.
+template <int DT>
+__device__ __forceinline__ float ce_unscaled(float x, float scale) { return x * (1.0f / kCeShift<DT>) * scale; }
 
 // ---- products ------------------------------------------------------------------------
 //
@@ -420,12 +424,12 @@ __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, cons
   __syncwarp();
 }
 
-// to[m][col] (+)= x f for the warp's rows from m0 to `rows` and its columns up to `cols`: rows of whole 16-byte chunks.
-// The sums that are added are in flight together. 16-bit results that are not added go through `map`, whose row y0 is
-// row 0 here.
-template <int WDT>
-__device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t m0, uint32_t rows, uint32_t col, uint32_t cols, float f,
-                                            bool add, float (&x)[64], uint8_t* turn, const CUtensorMap* map, uint64_t y0) {
+// to[m][col] (+)= x, unscaled as of type DT, for the warp's rows from m0 to `rows` and its columns up to `cols`: rows of
+// whole 16-byte chunks. The sums that are added are in flight together. 16-bit results that are not added go through
+// `map`, whose row y0 is row 0 here.
+template <int DT, int WDT>
+__device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t m0, uint32_t rows, uint32_t col, uint32_t cols,
+                                            float scale, bool add, float (&x)[64], uint8_t* turn, const CUtensorMap* map, uint64_t y0) {
   constexpr uint32_t es = Elem<WDT>::kSize;
   const uint32_t lane = threadIdx.x & 31;
   if (m0 >= rows || col >= cols) return;
@@ -434,7 +438,7 @@ __device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t 
     if (!add) {  // all 64 columns, rounded
       uint32_t w[32];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) w[q] = round16x2<WDT>(x[2 * q] * f, x[2 * q + 1] * f);
+      for (int q = 0; q < 32; ++q) w[q] = round16x2<WDT>(ce_unscaled<DT>(x[2 * q], scale), ce_unscaled<DT>(x[2 * q + 1], scale));
       ce_free();
       ce_put(turn, w);
       ce_send(map, turn, col, y0 + m0);
@@ -465,7 +469,7 @@ __device__ __forceinline__ void ce_out_rows(void* to, uint64_t stride, uint32_t 
     }
     uint32_t w[32];
 #pragma unroll
-    for (int q = 0; q < 32; ++q) w[q] = __float_as_uint(x[j + q] * f);
+    for (int q = 0; q < 32; ++q) w[q] = __float_as_uint(ce_unscaled<DT>(x[j + q], scale));
     ce_put(turn, w);
     __syncwarp();
 #pragma unroll
@@ -498,7 +502,6 @@ template <int DT, int WDT>
 __device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float scale, uint32_t m0, uint32_t col, uint32_t at, uint8_t* turn) {
   const uint32_t cols = (uint32_t)t.a.cols, words = (uint32_t)t.w_sum, lane = threadIdx.x & 31;
   const uint32_t high = m0 >= words ? 0 : words - m0 < 32 ? words - m0 : 32;
-  const float f = scale / kCeShift<DT>;
   ce_free();
 #pragma unroll 1
   for (uint32_t j = 0; j < 128 && col + j < cols; j += 32) {
@@ -513,7 +516,7 @@ __device__ __forceinline__ void ce_out_dweight_turned(const CeTiles& t, float sc
       for (uint32_t r = 0; r < 32; ++r) old[r] = r < rows ? ce_load<WDT>(t.a.dweight, first + r * t.a.dweight_stride) : 0.0f;
     }
 #pragma unroll
-    for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * f);
+    for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(ce_unscaled<DT>(__uint_as_float(x[q]), scale));
     ce_put(turn, x);
     __syncwarp();
 #pragma unroll
@@ -762,11 +765,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
 #pragma unroll
               for (int q = 0; q < 64; ++q) x[q] = 0.0f;
             if (o.kind == CE_DHIDDEN)  // a share of dh, on top of what the piece before left
-              ce_out_rows<DT_F32>(t.a.dh + o.slot * t.a.rows * t.a.cols_pad, t.a.cols_pad, m - lane, k.rows, c, (uint32_t)t.a.cols_pad, 1.0f,
+              ce_out_rows<DT_F32, DT_F32>(t.a.dh + o.slot * t.a.rows * t.a.cols_pad, t.a.cols_pad, m - lane, k.rows, c, (uint32_t)t.a.cols_pad, 1.0f,
                                   t.v_sum > 0, x, mine, nullptr, 0);
             else if constexpr (CHUNKS)
-              ce_out_rows<WDT>(static_cast<char*>(t.a.dweight) + t.v_sum * t.a.dweight_stride * Elem<WDT>::kSize, t.a.dweight_stride,
-                               m - lane, (uint32_t)t.w_sum, c, (uint32_t)t.a.cols, scale / kCeShift<DT>, t.a.accumulate, x, mine,
+              ce_out_rows<DT, WDT>(static_cast<char*>(t.a.dweight) + t.v_sum * t.a.dweight_stride * Elem<WDT>::kSize, t.a.dweight_stride,
+                               m - lane, (uint32_t)t.w_sum, c, (uint32_t)t.a.cols, scale, t.a.accumulate, x, mine,
                                &t.dw_store, t.v_sum);
           }
         }
@@ -841,7 +844,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const __grid_constant__ 
     for (uint64_t v = blockIdx.x; v < a.vocab; v += gridDim.x)
       for (uint64_t c = threadIdx.x; c < a.cols; c += 256) ce_store<WDT>(a.dweight, v * a.dweight_stride + c, __int_as_float(0x7fffffff));
   if (a.dhidden == nullptr) return;
-  const float scale = failed ? __int_as_float(0x7fffffff) : a.head->scale / kCeShift<DT>;
+  const float scale = failed ? __int_as_float(0x7fffffff) : a.head->scale;
   const uint32_t across = (uint32_t)((a.cols + 3) / 4);
   const uint64_t each = a.rows * a.cols_pad;
   const bool whole = ((reinterpret_cast<uintptr_t>(a.dhidden) | a.dhidden_stride * 2) & 7) == 0;
@@ -856,7 +859,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const __grid_constant__ 
         const float4 v = *reinterpret_cast<const float4*>(at + s * each);
         sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
       }
-      sum = make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
+      sum = make_float4(ce_unscaled<DT>(sum.x, scale), ce_unscaled<DT>(sum.y, scale), ce_unscaled<DT>(sum.z, scale), ce_unscaled<DT>(sum.w, scale));
     }
     uint16_t* const to = static_cast<uint16_t*>(a.dhidden) + t * a.dhidden_stride + c;
     const uint2 w = make_uint2(round16x2<DT>(sum.x, sum.y), round16x2<DT>(sum.z, sum.w));

@@ -588,6 +588,22 @@ ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, 
 size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
                                   ra_dtype_t dtype, int backward);
 
+/*
+ * Self-test of the bounded waits inside the two calls' kernels. No wait takes
+ * more than 4 s there; one that does gives up, its launch ends, and every
+ * result of a row that counts, and dweight, is NaN (the call itself has
+ * returned RA_SUCCESS long before). This runs the forward pass (dhidden and
+ * dweight NULL) or the backward pass of dense operands, targets of 64 bits,
+ * ignore -100 and dloss 1, with waits of 1 ms and a part of the work withheld
+ * from the others, so that they run out. withhold: 1 the numbers of the tiles,
+ * 2 the second operand, 3 the products, 4 the reading of the results (as far
+ * as a pair of SMs has more than two tiles). workspace: as for the call.
+ */
+ra_status_t ra_selftest_cross_entropy_timeout(const void* hidden, const void* weight, const int64_t* targets,
+                                              float* loss, float* lse, void* dhidden, void* dweight, size_t rows,
+                                              size_t cols, size_t vocab, ra_dtype_t dtype, int withhold,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -74,10 +74,16 @@ cudaError_t launch_tiles(const ra::CeTiles& t, uint64_t tiles, cudaStream_t s) {
                             : ra::launch_programmatic(kernel, dim3(2 * at_most(tiles, ra::kCePairs)), ra::kCeThreads, ra::kCeSmem, s, t);
 }
 
+// How long a wait inside a kernel may take, and what the self-test withholds from it.
+struct Limits {
+  uint64_t wait_ns = ra::kPairWaitNs;
+  int withheld = ra::CE_NOTHING;
+};
+
 template <int DT>
-cudaError_t forward(const CeArgs& a, cudaStream_t s) {
+cudaError_t forward(const CeArgs& a, const Limits& limits, cudaStream_t s) {
   ra::CeTiles t = {};
-  t.a = a, t.w_out = a.vocab, t.counter = a.counters;
+  t.a = a, t.w_out = a.vocab, t.counter = a.counters, t.wait_ns = limits.wait_ns, t.withheld = limits.withheld;
   cudaError_t err = encode_logits(t, DT);
   if (err == cudaSuccess) err = rows_and_operands<false>(a, s);
   t.early = a.rows <= ra::kCeFew && a.w == a.weight;
@@ -89,9 +95,9 @@ cudaError_t forward(const CeArgs& a, cudaStream_t s) {
 }
 
 template <int DT, int WDT>
-cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, cudaStream_t s) {
+cudaError_t backward(const CeArgs& a, const CePlan& p, char* scratch, const Limits& limits, cudaStream_t s) {
   ra::CeTiles t = {};
-  t.a = a;
+  t.a = a, t.wait_ns = limits.wait_ns, t.withheld = limits.withheld;
   CUtensorMap g[2], g_own[2], g_store[2];
   t.w_groups = a.w != a.weight || a.cols % 64 == 0;
   cudaError_t err = encode_logits(t, DT);
@@ -171,20 +177,10 @@ ra_status_t check_buffers(Buffer (&in)[IN], Buffer (&out)[OUT], uint64_t width) 
   return RA_SUCCESS;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
-                                  ra_dtype_t dtype, int backward) {
-  if (check_type(dtype) != RA_SUCCESS || !sizes_ok(rows, cols, vocab)) return 0;
-  return (size_t)ra::ce_plan(rows, cols, vocab, !in_place(weight, weight_stride), backward != 0).bytes;
-}
-
-ra_status_t ra_cross_entropy_forward(const void* hidden, size_t hidden_stride, const void* weight,
-                                     size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
-                                     float* loss, float* lse, size_t rows, size_t cols, size_t vocab,
-                                     ra_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+ra_status_t call_forward(const void* hidden, size_t hidden_stride, const void* weight,
+                         size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                         float* loss, float* lse, size_t rows, size_t cols, size_t vocab,
+                         ra_dtype_t dtype, void* workspace, size_t workspace_bytes, const Limits& limits, void* stream) {
   ra_status_t st = check_type(dtype);
   if (st != RA_SUCCESS) return st;
   if ((index_size != 4 && index_size != 8) || cols == 0 || vocab == 0 || !sizes_ok(rows, cols, vocab) ||
@@ -206,15 +202,15 @@ ra_status_t ra_cross_entropy_forward(const void* hidden, size_t hidden_stride, c
   a.loss = loss, a.lse = lse;
   place(a, p, workspace, packed);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return ra::launched(dtype == RA_FLOAT16 ? forward<ra::DT_F16>(a, s) : forward<ra::DT_BF16>(a, s));
+  return ra::launched(dtype == RA_FLOAT16 ? forward<ra::DT_F16>(a, limits, s) : forward<ra::DT_BF16>(a, limits, s));
 }
 
-ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, const void* weight,
-                                      size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
-                                      const float* lse, const float* dloss, void* dhidden, size_t dhidden_stride,
-                                      void* dweight, size_t dweight_stride, int accumulate, size_t rows, size_t cols,
-                                      size_t vocab, ra_dtype_t dtype, ra_dtype_t dweight_dtype, void* workspace,
-                                      size_t workspace_bytes, void* stream) {
+ra_status_t call_backward(const void* hidden, size_t hidden_stride, const void* weight,
+                          size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                          const float* lse, const float* dloss, void* dhidden, size_t dhidden_stride,
+                          void* dweight, size_t dweight_stride, int accumulate, size_t rows, size_t cols,
+                          size_t vocab, ra_dtype_t dtype, ra_dtype_t dweight_dtype, void* workspace,
+                          size_t workspace_bytes, const Limits& limits, void* stream) {
   ra_status_t st = check_type(dtype);
   if (st == RA_SUCCESS) st = ra::check_float(dweight_dtype);
   if (st == RA_SUCCESS && dweight_dtype != dtype && dweight_dtype != RA_FLOAT32) st = RA_ERR_UNSUPPORTED;
@@ -250,10 +246,52 @@ ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, 
   char* const w = first_place(workspace);
   cudaError_t err;
   if (dtype == RA_FLOAT16)
-    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, p, w, s) : backward<ra::DT_F16, ra::DT_F16>(a, p, w, s);
+    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_F16, ra::DT_F32>(a, p, w, limits, s) : backward<ra::DT_F16, ra::DT_F16>(a, p, w, limits, s);
   else
-    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, p, w, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, p, w, s);
+    err = dweight_dtype == RA_FLOAT32 ? backward<ra::DT_BF16, ra::DT_F32>(a, p, w, limits, s) : backward<ra::DT_BF16, ra::DT_BF16>(a, p, w, limits, s);
   return ra::launched(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ra_cross_entropy_workspace(const void* weight, size_t weight_stride, size_t rows, size_t cols, size_t vocab,
+                                  ra_dtype_t dtype, int backward) {
+  if (check_type(dtype) != RA_SUCCESS || !sizes_ok(rows, cols, vocab)) return 0;
+  return (size_t)ra::ce_plan(rows, cols, vocab, !in_place(weight, weight_stride), backward != 0).bytes;
+}
+
+ra_status_t ra_cross_entropy_forward(const void* hidden, size_t hidden_stride, const void* weight,
+                                     size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                                     float* loss, float* lse, size_t rows, size_t cols, size_t vocab,
+                                     ra_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return call_forward(hidden, hidden_stride, weight, weight_stride, targets, index_size, ignore, loss, lse, rows, cols, vocab,
+                      dtype, workspace, workspace_bytes, Limits{}, stream);
+}
+
+ra_status_t ra_cross_entropy_backward(const void* hidden, size_t hidden_stride, const void* weight,
+                                      size_t weight_stride, const void* targets, size_t index_size, int64_t ignore,
+                                      const float* lse, const float* dloss, void* dhidden, size_t dhidden_stride,
+                                      void* dweight, size_t dweight_stride, int accumulate, size_t rows, size_t cols,
+                                      size_t vocab, ra_dtype_t dtype, ra_dtype_t dweight_dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  return call_backward(hidden, hidden_stride, weight, weight_stride, targets, index_size, ignore, lse, dloss, dhidden,
+                       dhidden_stride, dweight, dweight_stride, accumulate, rows, cols, vocab, dtype, dweight_dtype,
+                       workspace, workspace_bytes, Limits{}, stream);
+}
+
+ra_status_t ra_selftest_cross_entropy_timeout(const void* hidden, const void* weight, const int64_t* targets, float* loss,
+                                              float* lse, void* dhidden, void* dweight, size_t rows, size_t cols,
+                                              size_t vocab, ra_dtype_t dtype, int withhold, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  if (withhold < ra::CE_TILES || withhold > ra::CE_RESULTS) return RA_ERR_INVALID_ARG;
+  const Limits limits{1000000, withhold};  // a millisecond
+  if (!dhidden && !dweight)
+    return call_forward(hidden, cols, weight, cols, targets, 8, -100, loss, lse, rows, cols, vocab, dtype, workspace,
+                        workspace_bytes, limits, stream);
+  return call_backward(hidden, cols, weight, cols, targets, 8, -100, lse, nullptr, dhidden, cols, dweight, cols, 0, rows, cols,
+                       vocab, dtype, dtype, workspace, workspace_bytes, limits, stream);
 }
 
 }  // extern "C"

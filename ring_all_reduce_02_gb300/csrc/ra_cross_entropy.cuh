@@ -206,6 +206,9 @@ __device__ __forceinline__ float ce_unscaled(float x, float scale) { return x * 
 
 // A wait that gave up.
 enum CeWait { CE_WAIT_EMPTY = 1, CE_WAIT_TILE, CE_WAIT_TAKEN, CE_WAIT_FULL, CE_WAIT_READ, CE_WAIT_READY };
+// What the self-test withholds from the other warps: the tiles' numbers, the second operand, the products, or the reading
+// of the results.
+enum CeWithheld { CE_NOTHING = 0, CE_TILES, CE_OPERAND, CE_PRODUCTS, CE_RESULTS };
 enum CeKind { CE_LOGITS = 0, CE_G = 1, CE_DHIDDEN = 2, CE_DWEIGHT = 3, CE_END = 4 };
 
 constexpr int kCeThreads = 384, kCeOutWarps = 8, kCeStages = 6, kCeRing = 4;
@@ -229,6 +232,8 @@ struct CeTiles {
   uint32_t* counter;
   int early;                // the first tiles' words may be asked for before the launch before this one has ended
   int w_groups;             // w_own's boxes are of two groups
+  int withheld;             // CeWithheld
+  uint64_t wait_ns;         // that a wait takes at most
 };
 
 // A tile as it is handed to the warps that work on it.
@@ -583,6 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
   pdl_next();
   const CeWork k = ce_work(t);
 
+  // Both by a whole warp, with the same answer in all lanes.
+  const auto wait = [&](uint64_t* bar, uint32_t parity, int what) { return mbar_wait_warp(bar, parity, &dead, what, t.wait_ns); };
+  const auto gave_up = [&] { return uniform((uint32_t)*const_cast<volatile int*>(&dead)) != 0; };
   uint32_t turn = 0;
   // The next tile, by a whole warp. The loading warps and the one of the products ask for it before they work on the one
   // before, so that they do not wait for it. What it says is the same in all lanes, as what these warps count: one lane
@@ -593,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
     const uint32_t slot = turn % kCeRing, round = turn / kCeRing;
     ++turn;
     o.kind = CE_END;
-    if (!mbar_wait_pair(&turns.full[slot], round & 1, &dead, CE_WAIT_TILE)) return o;
+    if (!wait(&turns.full[slot], round & 1, CE_WAIT_TILE)) return o;
     const volatile uint32_t* from = reinterpret_cast<const volatile uint32_t*>(&turns.tile[slot]);
     o.m0 = uniform(from[0]), o.n0 = uniform(from[1]), o.blocks = uniform(from[2]), o.b0 = uniform(from[3]), o.slot = uniform(from[4]);
     const uint32_t both = uniform(from[5]);
@@ -606,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
     // The first operand, 128 rows of each block to each CTA of the pair. What both CTAs bring in counts at the even one's
     // barrier, and its bytes are announced here: those of the first operand that have to come, and all of the second.
     uint32_t s = 0, phase = 0;
-    for (CeTile o = next(), after; o.kind != CE_END && !dead; o = after) {
+    for (CeTile o = next(), after; o.kind != CE_END && !gave_up(); o = after) {
       const bool logits = !BACKWARD || o.kind == CE_G;
       // Boxes of this CTA, and of both. With few rows they are of 64 rows, and those that hold none are left out, but for
       // one of each CTA: one that brings nothing in could not tell a stage that is free from one that is used again.
@@ -620,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       const int32_t own = (int32_t)(o.m0 + rank * 128);
       after = next();
       for (uint32_t b = 0; b < o.blocks; ++b) {
-        if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
+        if (!wait(&empty[s], phase ^ 1, CE_WAIT_EMPTY)) break;
         if (elected()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           uint8_t* const at = stages + s * kCeStageBytes;
@@ -637,15 +645,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
         if (++s == kCeStages) s = 0, phase ^= 1;
       }
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 && t.withheld != CE_OPERAND) {
     // the second operand
     uint32_t s = 0, phase = 0;
-    for (CeTile o = next(), after; o.kind != CE_END && !dead; o = after) {
+    for (CeTile o = next(), after; o.kind != CE_END && !gave_up(); o = after) {
       const int32_t own = (int32_t)(o.n0 + rank * (o.n / 2));
       after = next();
       for (uint32_t b = 0; b < o.blocks; ++b) {
         if (b >= early) {
-          if (!mbar_wait_pair(&empty[s], phase ^ 1, &dead, CE_WAIT_EMPTY)) break;
+          if (!wait(&empty[s], phase ^ 1, CE_WAIT_EMPTY)) break;
           if (elected()) {
             uint8_t* const at = stages + s * kCeStageBytes + 2 * kBoxBytes;
             const uint32_t bar = cluster_address(&full[s], 0);
@@ -668,19 +676,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       }
       early = 0;
     }
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == 1 && rank == 0 && t.withheld != CE_PRODUCTS) {
     // the products of both CTAs
     uint32_t s = 0, phase = 0, n = 0;
-    for (CeTile o = next(), after; o.kind != CE_END && !dead; o = after, ++n) {
+    for (CeTile o = next(), after; o.kind != CE_END && !gave_up(); o = after, ++n) {
       after = next();
       const uint32_t buffer = n & 1, d = tmem + buffer * 256;
-      if (!mbar_wait_pair(&taken[buffer], (n >> 1 & 1) ^ 1, &dead, CE_WAIT_TAKEN)) break;
+      if (!wait(&taken[buffer], (n >> 1 & 1) ^ 1, CE_WAIT_TAKEN)) break;
       tmem_fence_after();
       const bool a_own = BACKWARD && o.kind == CE_DWEIGHT, b_own = BACKWARD && o.kind != CE_G;
       const uint32_t instruction = umma_instruction(DT == DT_BF16, a_own, b_own, o.n);
       const uint32_t a_step = umma_step(a_own), b_step = umma_step(b_own);
       for (uint32_t b = 0; b < o.blocks; ++b) {
-        if (!mbar_wait_pair(&full[s], phase, &dead, CE_WAIT_FULL)) break;
+        if (!wait(&full[s], phase, CE_WAIT_FULL)) break;
         tmem_fence_after();
         if (elected()) {
           const uint32_t at = smem_u32(stages + s * kCeStageBytes);
@@ -693,21 +701,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       }
       if (elected()) umma_commit_pair(&ready[buffer]);
     }
-  } else if (warp == 3 && lane == 0 && rank == 0) {
+  } else if (warp == 3 && lane == 0 && rank == 0 && t.withheld != CE_TILES) {
     // The tiles. One is taken as late as keeps the others from waiting for it, so that no pair takes tiles that another
     // would get to earlier: after a long one as soon as all warps know the one before, after a short one three ahead.
     const uint32_t pairs = gridDim.x / 2;
     uint32_t ahead = kCeRing;
-    for (uint32_t n = 0; !dead; ++n) {
+    for (uint32_t n = 0; !*const_cast<volatile int*>(&dead); ++n) {
       const uint32_t slot = n % kCeRing;
-      if (n >= ahead && !mbar_wait_pair(&turns.empty[(n - ahead) % kCeRing], (n - ahead) / kCeRing & 1, &dead, CE_WAIT_READ)) break;
+      if (n >= ahead && !mbar_wait_pair(&turns.empty[(n - ahead) % kCeRing], (n - ahead) / kCeRing & 1, &dead, CE_WAIT_READ, t.wait_ns)) break;
       const CeTile o = ce_tile<BACKWARD>(t, k, n == 0 ? blockIdx.x / 2 : pairs + atomicAdd(t.counter, 1u));
       const uint32_t w[8] = {o.m0, o.n0, o.blocks, o.b0, o.slot, (uint32_t)o.kind | (uint32_t)o.n << 16, 0, 0};
       for (uint32_t to = 0; to < 2; ++to) store_pair(cluster_address(&turns.tile[slot], to), w, cluster_address(&turns.full[slot], to));
       if (o.kind == CE_END) break;
       ahead = o.blocks >= kCeLong ? 2 : kCeRing;
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && t.withheld != CE_RESULTS) {
     // the results: warp w has lanes 32 (w % 4) on of tensor memory, the first four warps columns 0 to 127
     const uint32_t part = (warp & 3) * 32, col = (warp - 4) / 4 * 128;
     uint8_t* const mine = stages + kCeStages * kCeStageBytes + (warp - 4) * kCeTurn;
@@ -717,7 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
       if (!t.w_sum && blockIdx.x == 0 && warp == 4 && lane == 0) t.a.head->scale = scale;
     }
     uint32_t n = 0;
-    for (CeTile o = next(); o.kind != CE_END && !dead; o = next(), ++n) {
+    for (CeTile o = next(); o.kind != CE_END && !gave_up(); o = next(), ++n) {
       const uint32_t buffer = n & 1, m = o.m0 + rank * 128 + part + lane;
       if (BACKWARD && o.kind == CE_DWEIGHT && t.a.accumulate && m < t.w_sum && o.n0 + col < t.a.cols) {
         // what the tile is added to, on its way while the products run
@@ -726,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
         const char* at = static_cast<const char*>(t.a.dweight) + ((t.v_sum + m) * t.a.dweight_stride + o.n0 + col) * es;
         for (uint32_t b = 0; b < left; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
       }
-      if (!mbar_wait_pair(&ready[buffer], n >> 1 & 1, &dead, CE_WAIT_READY)) break;
+      if (!wait(&ready[buffer], n >> 1 & 1, CE_WAIT_READY)) break;
       __syncwarp();
       tmem_fence_after();
       const uint32_t at = tmem + buffer * 256 + col + (part << 16);
@@ -783,6 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_ti
     const uint64_t start = global_ns();
     while (global_ns() - start < 10000000ull) {}
     if (threadIdx.x == 0) atomicCAS(&t.a.head->failed, 0, dead + 16 * (int)rank + 256 * (int)(blockIdx.x / 2));
+    __syncwarp();
   }
   tmem_fence_before();
   cluster_sync();

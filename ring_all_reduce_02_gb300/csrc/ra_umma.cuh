@@ -48,27 +48,47 @@ __device__ __forceinline__ void store_pair(uint32_t cluster_addr, const uint32_t
 }
 
 constexpr uint64_t kPairWaitNs = 4000000000ull;  // 4 s: more than any tile takes
-// As mbar_wait. An acquire of the CTA's scope does for arrivals from the other one: what is read behind it lies in this
-// CTA's shared memory or in tensor memory (one of the cluster's scope also empties the L1 cache, at 0.3 us). Where it gives
-// up, `what` says in *dead which wait did; where the CTA already has, it gives up at once.
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead, int what) {
+// Whether the phase of a barrier has ended. An acquire of the CTA's scope does for arrivals from the other one: what is read
+// behind it lies in this CTA's shared memory or in tensor memory (one of the cluster's scope also empties the L1 cache, at
+// 0.3 us).
+__device__ __forceinline__ bool mbar_try_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// As mbar_wait, for `limit` ns at most, by one thread. Where it gives up, `what` says in *dead which wait did; where the CTA
+// already has, it gives up at once.
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* dead, int what, uint64_t limit) {
   uint64_t start = 0;
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
+  while (!mbar_try_pair(bar, parity)) {
     if (*dead) return false;
     const uint64_t now = global_ns();
     if (start == 0) start = now;
-    if (now - start > kPairWaitNs) {
+    if (now - start > limit) {
       *dead = what;
       return false;
     }
   }
+  return true;
+}
+// The same by a whole warp, whose lanes all have the same answer: a lane may see the phase end when another one sees that
+// the CTA has given up, and what follows a wait (shuffles, tensor memory) takes all 32.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* dead, int what, uint64_t limit) {
+  uint64_t start = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_pair(bar, parity))) {
+    const uint64_t now = global_ns();
+    if (start == 0) start = now;
+    if (__any_sync(0xffffffffu, *dead != 0 || now - start > limit)) {
+      if ((threadIdx.x & 31) == 0 && *dead == 0) *dead = what;
+      __syncwarp();
+      return false;
+    }
+  }
+  return true;
 }
 
 // A box of a two-dimensional tensor map into this CTA's shared memory; its bytes are counted by the barrier at

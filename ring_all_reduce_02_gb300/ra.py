@@ -31,7 +31,7 @@ EXPORTS = ("ra_allreduce", "ra_reduce_scatter", "ra_allgather", "ra_allreduce_ex
            "ra_allreduce_bulk_noalloc", "ra_layernorm_forward", "ra_layernorm_backward", "ra_layernorm_workspace",
            "ra_grad_norm", "ra_grad_norm_workspace", "ra_adamw", "ra_embedding_forward", "ra_embedding_backward",
            "ra_embedding_workspace", "ra_cross_entropy_forward", "ra_cross_entropy_backward",
-           "ra_cross_entropy_workspace")
+           "ra_cross_entropy_workspace", "ra_selftest_cross_entropy_timeout")
 ENGINE_CODES = {"registers": 0, "bulk": 1}
 RA_STATE_F32, RA_STATE_E4M3 = 0, 1
 RA_ADAMW_BLOCK = 256  # elements per scale of an 8-bit moment
@@ -148,6 +148,8 @@ def lib() -> ctypes.CDLL:
             L.ra_cross_entropy_backward.restype = I
             L.ra_cross_entropy_workspace.argtypes = [VP, SZ, SZ, SZ, SZ, I, I]
             L.ra_cross_entropy_workspace.restype = SZ
+            L.ra_selftest_cross_entropy_timeout.argtypes = [VP, VP, VP, VP, VP, VP, VP, SZ, SZ, SZ, I, I, VP, SZ, VP]
+            L.ra_selftest_cross_entropy_timeout.restype = I
             _lib = L
     return _lib
 
@@ -827,5 +829,22 @@ def ra_cross_entropy_backward(hidden, weight, targets, lse, dloss=None, dhidden=
         lse.data_ptr(), _address(dloss), _address(dhidden), cols if dhidden is None else _pitch(dhidden, cols),
         _address(dweight), cols if dweight is None else _pitch(dweight, cols), accumulate, rows, cols, vocab, code, wcode,
         workspace.data_ptr(), workspace.nbytes, _stream_on(device, stream, what))
+    if st:
+        raise RaError(st, what)
+
+
+def ra_selftest_cross_entropy_timeout(hidden, weight, targets, loss=None, lse=None, dhidden=None, dweight=None, withhold: int = 1,
+                                      workspace=None, stream=None) -> None:
+    """The cross entropy (the backward pass where dhidden or dweight is given) of dense operands and int64 targets, with waits
+    of a millisecond and the part ``withhold`` of its work left out: its waits must give up, and its results be NaN."""
+    what = "ra_selftest_cross_entropy_timeout"
+    rows, cols = hidden.shape
+    tensors = [t for t in (hidden, weight, targets, loss, lse, dhidden, dweight, workspace) if t is not None]
+    if workspace is None or not all(t.is_cuda and t.is_contiguous() and t.get_device() == hidden.get_device() for t in tensors):
+        raise ValueError(f"{what}: contiguous CUDA tensors of one device and a workspace are needed")
+    st = lib().ra_selftest_cross_entropy_timeout(
+        hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(), _address(loss), _address(lse), _address(dhidden), _address(dweight),
+        rows, cols, weight.shape[0], _float_code(hidden, what), withhold, workspace.data_ptr(), workspace.nbytes,
+        _stream_on(hidden.get_device(), stream, what))
     if st:
         raise RaError(st, what)

@@ -477,23 +477,30 @@ __device__ __forceinline__ void emb_finish(const EmbBackward& a, char* row, uint
   emb_store<WDT, N, VEC>(row, c, a.cols, x);
 }
 
-// The first span that holds places of the token whose places reach from before into `span`, and the last one that holds
-// some of the token whose places go on behind `span`; 32 spans at a time.
-__device__ __forceinline__ uint32_t emb_first_span(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t key) {
-  for (uint32_t first = span;; first -= 32) {
-    const uint32_t f = first - (threadIdx.x & 31);  // wraps below 0
-    const bool from = f <= first && f > 0 && keys[(uint64_t)f * a.span - 1] == key;
-    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, from));
-    if (run) return first - (run - 1);
+// How far a condition holds from the warp's n = 0, where it does: the least n > 0 where it no longer holds. It does not come
+// back behind that. 32 numbers at a time, side by side, and where all 32 hold in strides 32 times as long, which come down
+// again: a token that has all of 2^23 places took 21.7 ms a call by steps of 32 alone (2^20: 1.1), and 7.7 with this (0.75).
+template <class C>
+__device__ __forceinline__ uint32_t emb_reach(C holds) {
+  uint32_t at = 0, stride = 1;
+  while (true) {
+    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, holds((uint64_t)at + (uint64_t)((threadIdx.x & 31) + 1) * stride)));
+    if (run == 0) {  // all 32
+      at += 32 * stride, stride *= 32;
+    } else {
+      at += (run - 1) * stride;
+      if (stride == 1) return at + 1;
+      stride /= 32;
+    }
   }
 }
+// The first span that holds places of the token whose places reach from before into `span`, and the last one that holds
+// some of the token whose places go on behind `span`.
+__device__ __forceinline__ uint32_t emb_first_span(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t key) {
+  return span - emb_reach([&](uint64_t n) { return n < span && keys[(span - n) * a.span - 1] == key; });
+}
 __device__ __forceinline__ uint32_t emb_last_span(const EmbBackward& a, const uint32_t* keys, uint32_t span, uint32_t key) {
-  for (uint32_t last = span;; last += 32) {
-    const uint64_t next = (uint64_t)(last + (threadIdx.x & 31) + 1) * a.span;
-    const bool on = next < a.rows && keys[next] == key;
-    const uint32_t run = __ffs(~__ballot_sync(0xffffffffu, on));
-    if (run) return last + (run - 1);
-  }
+  return span + emb_reach([&](uint64_t n) { return (span + n + 1) * a.span < a.rows && keys[(span + n + 1) * a.span] == key; });
 }
 
 // A token's places reach over the ends of spans `first` to `last`: adds up what they left, if this warp is the last of

@@ -55,8 +55,8 @@ cudaError_t sort(ra::EmbBackward& a, const ra::EmbPlan& p, bool clear, cudaStrea
   }
   cudaError_t err = cudaSuccess;
   for (uint32_t pass = 0; pass < a.passes && err == cudaSuccess; ++pass) {
-    err = ra::launch_programmatic(ra::embedding_count_kernel, dim3(a.tiles + (pass == 0 ? zeros : 0)), ra::kEmbThreads, 0, s, a, pass);
-    if (err == cudaSuccess) err = ra::launch_programmatic(ra::embedding_scatter_kernel, dim3(a.tiles), ra::kEmbThreads, 0, s, a, pass);
+    err = ra::launch_programmatic(ra::embedding_count_kernel, dim3(a.ctas + (pass == 0 ? zeros : 0)), ra::kEmbThreads, 0, s, a, pass);
+    if (err == cudaSuccess) err = ra::launch_programmatic(ra::embedding_scatter_kernel, dim3(a.ctas), ra::kEmbThreads, 0, s, a, pass);
   }
   return err;
 }
@@ -156,7 +156,7 @@ ra_status_t ra_embedding_backward(const void* dy, size_t dy_stride, const void* 
   ra::EmbBackward a = {};
   a.dy = dy, a.tokens = {tokens, (int)index_size}, a.dtable = dtable, a.rows = rows, a.cols = cols;
   a.dy_stride = dy_stride, a.table_stride = dtable_stride, a.vocab = (int64_t)vocab, a.padding = padding, a.scale = (float)scale;
-  a.bits = p.bits, a.passes = p.passes, a.tiles = (uint32_t)p.tiles, a.span = (uint32_t)p.span, a.spans = (uint32_t)p.spans;
+  a.bits = p.bits, a.passes = p.passes, a.tiles = (uint32_t)p.tiles, a.ctas = (uint32_t)p.ctas, a.span = (uint32_t)p.span, a.spans = (uint32_t)p.spans;
   a.across = (uint32_t)p.across;
   for (int i = 0; i < 2; ++i) a.keys[i] = at(p.keys[i]), a.places[i] = at(p.places[i]);
   a.counts = at(p.counts), a.tickets = at(p.tickets), a.partial = reinterpret_cast<float*>(w + p.partial);

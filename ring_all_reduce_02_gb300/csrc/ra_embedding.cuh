@@ -145,7 +145,7 @@ struct EmbBackward {
   uint64_t rows, cols, dy_stride, table_stride;
   int64_t vocab, padding;
   float scale;
-  uint32_t bits, passes, tiles, span, spans, across;
+  uint32_t bits, passes, tiles, ctas, span, spans, across;
   uint32_t *keys[2], *places[2], *counts, *tickets;
   float* partial;  // [spans][2][across][32 * N]: of the places that come from the span before, and that go on into the next
   int table_bytes;  // of dtable's elements
@@ -339,7 +339,9 @@ __global__ void __cluster_dims__(kEmbCluster, 1, 1) __launch_bounds__(THREADS) e
 }
 
 // More tokens than that: a pass is a count of every CTA's digits, and a CTA's items to their places. Pass 0 reads the
-// tokens themselves.
+// tokens themselves. A CTA finds its first places from the counts of all, 1 KB of each, so that there are 304 of them at most,
+// as many as the device holds, which take tiles in a row (into 50257 x 8 fp32, ms a call: a CTA to each tile 0.62 for 2^22 tokens,
+// 37.9 for 2^26; 1216 CTAs 0.67 and 8.5, 608 0.53 for 2^22, 304 0.51 and 9.1).
 constexpr int kEmbTileItems = 16;
 static_assert(kEmbThreads * kEmbTileItems == 4096, "a tile of the plan");
 
@@ -354,21 +356,24 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_count_kernel(const __gr
   pdl_enter();
   pdl_next();
   __shared__ uint32_t seen[256];  // of each digit
-  if (blockIdx.x >= a.tiles) {
-    emb_clear(a, blockIdx.x - a.tiles, gridDim.x - a.tiles);
+  if (blockIdx.x >= a.ctas) {
+    emb_clear(a, blockIdx.x - a.ctas, gridDim.x - a.ctas);
     return;
   }
   if (pass == 0)
-    for (uint64_t i = (uint64_t)blockIdx.x * kEmbThreads + threadIdx.x; i < (uint64_t)a.spans * a.across; i += (uint64_t)a.tiles * kEmbThreads)
+    for (uint64_t i = (uint64_t)blockIdx.x * kEmbThreads + threadIdx.x; i < (uint64_t)a.spans * a.across; i += (uint64_t)a.ctas * kEmbThreads)
       a.tickets[i] = 0;
   seen[threadIdx.x] = 0;
   __syncthreads();
-  const uint64_t first = (uint64_t)blockIdx.x * 4096 + threadIdx.x;
+#pragma unroll 1
+  for (uint32_t tile = 0; tile < a.tiles; ++tile) {
+    const uint64_t first = ((uint64_t)blockIdx.x * a.tiles + tile) * 4096 + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < kEmbTileItems; ++i) {
-    uint32_t key, place;
-    emb_item(a, pass, first + i * kEmbThreads, key, place);
-    if (first + i * kEmbThreads < a.rows) atomicAdd(&seen[key >> pass * a.bits & ((1u << a.bits) - 1)], 1u);
+    for (int i = 0; i < kEmbTileItems; ++i) {
+      uint32_t key, place;
+      emb_item(a, pass, first + i * kEmbThreads, key, place);
+      if (first + i * kEmbThreads < a.rows) atomicAdd(&seen[key >> pass * a.bits & ((1u << a.bits) - 1)], 1u);
+    }
   }
   __syncthreads();
   a.counts[(uint64_t)blockIdx.x * 256 + threadIdx.x] = seen[threadIdx.x];
@@ -383,35 +388,42 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_scatter_kernel(const __
   // this CTA's first place for the thread's digit: items of smaller digits, and of this one in CTAs before
   uint32_t all = 0, before = 0;
 #pragma unroll 8
-  for (uint32_t c = 0; c < a.tiles; ++c) {
+  for (uint32_t c = 0; c < a.ctas; ++c) {
     const uint32_t n = a.counts[(uint64_t)c * 256 + threadIdx.x];
     if (c < blockIdx.x) before += n;
     all += n;
   }
   const uint32_t at = emb_digits_below(s, all) + before;
   base[threadIdx.x] = at;
-  const uint64_t first = (uint64_t)blockIdx.x * 4096 + warp * 32 * kEmbTileItems + lane;
-  uint32_t key[kEmbTileItems], place[kEmbTileItems], ranks[kEmbTileItems / 2];
+#pragma unroll 1
+  for (uint32_t tile = 0; tile < a.tiles; ++tile) {
+    const uint64_t first = ((uint64_t)blockIdx.x * a.tiles + tile) * 4096 + warp * 32 * kEmbTileItems + lane;
+    uint32_t key[kEmbTileItems], place[kEmbTileItems], ranks[kEmbTileItems / 2];
 #pragma unroll
-  for (int i = 0; i < kEmbTileItems; ++i) emb_item(a, pass, first + i * 32, key[i], place[i]);
-  const auto digit = [&](int i) { return key[i] >> pass * a.bits & ((1u << a.bits) - 1); };
-  emb_rank<kEmbThreads, kEmbTileItems>(s, digit, ranks);
-  __syncthreads();
-  // items of the digit in the warps before this one
-  uint32_t run = 0;
-  for (int w = 0; w < kEmbThreads / 32; ++w) {
-    const uint32_t n = s.counts[w][threadIdx.x];
-    s.counts[w][threadIdx.x] = (uint16_t)run;
-    run += n;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kEmbTileItems; ++i)
-    if (first + i * 32 < a.rows) {
-      const uint32_t to = base[digit(i)] + s.counts[warp][digit(i)] + emb_rank_of(ranks, i);
-      a.keys[pass % 2][to] = key[i];
-      a.places[pass % 2][to] = place[i];
+    for (int i = 0; i < kEmbTileItems; ++i) emb_item(a, pass, first + i * 32, key[i], place[i]);
+    const auto digit = [&](int i) { return key[i] >> pass * a.bits & ((1u << a.bits) - 1); };
+    emb_rank<kEmbThreads, kEmbTileItems>(s, digit, ranks);
+    __syncthreads();
+    // items of the digit in the warps before this one
+    uint32_t run = 0;
+    for (int w = 0; w < kEmbThreads / 32; ++w) {
+      const uint32_t n = s.counts[w][threadIdx.x];
+      s.counts[w][threadIdx.x] = (uint16_t)run;
+      run += n;
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEmbTileItems; ++i)
+      if (first + i * 32 < a.rows) {
+        const uint32_t to = base[digit(i)] + s.counts[warp][digit(i)] + emb_rank_of(ranks, i);
+        a.keys[pass % 2][to] = key[i];
+        a.places[pass % 2][to] = place[i];
+      }
+    if (tile + 1 < a.tiles) {  // the next tile's come behind these
+      __syncthreads();
+      base[threadIdx.x] += run;
+    }
+  }
 }
 
 // ---- sums -----------------------------------------------------------------------------

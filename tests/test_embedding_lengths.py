@@ -88,3 +88,28 @@ def test_one_tokens_time_grows_with_its_places(ra):  # noqa: F811
         times.append(fastest(lambda: ra.ra_embedding_backward(dy, tokens, dtable, workspace=ws)))
         assert (dtable[77] == rows).all() and float(dtable.sum()) == rows * cols
     assert times[1] <= 14 * times[0], times
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab", [40, 50257, 200_003])
+@pytest.mark.parametrize("rows", [304 * 4096 - 1, 304 * 4096, 304 * 4096 + 1, 2 * 304 * 4096 + 1, 10_100_003])
+def test_more_tiles_than_a_pass_has_ctas(ra, rows, vocab):  # noqa: F811
+    gpu()
+    gen = torch.Generator(device="cuda").manual_seed(rows + vocab)
+    u = torch.rand(rows, generator=gen, device="cuda", dtype=torch.float64)
+    check_exactly(ra, whole_numbers(rows, 5, gen), (u * u * vocab).long(), vocab)
+
+
+@pytest.mark.gpu
+def test_the_sorts_time_grows_with_the_tokens(ra):  # noqa: F811
+    # 8 times the tokens in at most 12 times the time. Were each tile a CTA's, which reads the counts of all, it would be 18 times
+    gpu()
+    cols, vocab, times = 8, 50257, []
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for rows in (1 << 22, 1 << 25):
+        dy, tokens = torch.ones(rows, cols, dtype=BF16, device="cuda"), torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+        dtable = torch.empty(vocab, cols, device="cuda")
+        ws = torch.empty(ra.ra_embedding_workspace(rows, cols, vocab), dtype=torch.uint8, device="cuda")
+        times.append(fastest(lambda: ra.ra_embedding_backward(dy, tokens, dtable, workspace=ws)))
+        assert torch.equal(dtable[:, 0].long(), torch.bincount(tokens, minlength=vocab))
+    assert times[1] <= 12 * times[0], times

@@ -697,6 +697,10 @@ def _refuse_matrices(what: str, device: int, cols: int, index=None, workspace=No
         raise ValueError(f"{what}: workspace must be a contiguous CUDA tensor, on cuda:{device}")
 
 
+def _refuse_ignore(what: str, ignore: int) -> None:
+    raise ValueError(f"{what}: ignore must be a number of 64 bits, not {ignore}")
+
+
 def _refuse_types(what: str, index_name: str, index, *tensors) -> None:
     if index.dtype not in _Torch.index_bytes:
         raise TypeError(f"{what}: {index_name} must be int32 or int64, not {index.dtype}")
@@ -749,7 +753,8 @@ def ra_embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bo
         _refuse_matrices("ra_embedding_backward", device, cols, index=("tokens", tokens, rows), workspace=workspace,
                          dy=(dy, rows, dtype), dtable=(dtable, vocab, tdtype))
     st = (_lib or lib()).ra_embedding_backward(
-        dy.data_ptr(), _pitch(dy, cols), tokens.data_ptr(), size, -1 if padding is None else padding, dtable.data_ptr(),
+        dy.data_ptr(), _pitch(dy, cols), tokens.data_ptr(), size,
+        padding if padding is not None and 0 <= padding < vocab else -1, dtable.data_ptr(),
         _pitch(dtable, cols), accumulate, rows, cols, vocab, scale, code, tcode, workspace.data_ptr(), workspace.nbytes,
         _stream_on(device, stream, "ra_embedding_backward"))
     if st:
@@ -780,6 +785,8 @@ def ra_cross_entropy_forward(hidden, weight, targets, loss, lse, ignore: int = -
     code, size = codes.get(dtype), _Torch.index_bytes.get(targets.dtype)
     if code is None or size is None:
         _refuse_types(what, "targets", targets, hidden)
+    if not -(1 << 63) <= ignore < 1 << 63:  # ctypes would cut it off
+        _refuse_ignore(what, ignore)
     if not (device >= 0 and _is_matrix(hidden, (rows, cols), dtype, device) and _is_matrix(weight, (vocab, cols), dtype, device)
             and _is_index(targets, rows, device) and loss is not None and lse is not None and workspace is not None
             and _is_vector(loss, rows, f32, device) and _is_vector(lse, rows, f32, device)
@@ -813,6 +820,8 @@ def ra_cross_entropy_backward(hidden, weight, targets, lse, dloss=None, dhidden=
     code, wcode, size = codes.get(dtype), codes.get(wdtype), _Torch.index_bytes.get(targets.dtype)
     if code is None or wcode is None or size is None:
         _refuse_types(what, "targets", targets, hidden, dweight)
+    if not -(1 << 63) <= ignore < 1 << 63:
+        _refuse_ignore(what, ignore)
     if not (device >= 0 and _is_matrix(hidden, (rows, cols), dtype, device) and _is_matrix(weight, (vocab, cols), dtype, device)
             and _is_matrix(dhidden, (rows, cols), dtype, device) and _is_matrix(dweight, (vocab, cols), wdtype, device)
             and _is_index(targets, rows, device) and lse is not None and workspace is not None

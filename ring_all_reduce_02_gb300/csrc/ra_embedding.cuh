@@ -615,12 +615,14 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_few_kernel(const __grid
   emb_finish<WDT, N, VEC, true>(a, row, c, sum, before);
 }
 
-// Rows that a warp has in flight, as many as let an SM hold 4 CTAs; and a partial sum of each warp beside them.
-template <bool ADD>
-constexpr uint32_t kEmbFlight = ADD ? 5 : 8;
+// Rows that a warp has in flight, as many as let an SM hold 4 CTAs, which is also what their registers are limited for; and a
+// partial sum of each warp beside them. 16-bit rows added to an fp32 table, whose slots are half as large again: 8192 x 1024
+// bf16 21.5 us a call with 3 rows and 4 CTAs, 23.9 with 5 and 3; 20011 x 515 fp16 33.1 and 33.9; 32768 x 8192 bf16 239 and 241.
+template <int DT, int WDT, bool ADD>
+constexpr uint32_t kEmbFlight = !ADD ? 8 : DT == WDT ? 5 : 3;
 template <int DT, int WDT, int N, bool VEC, bool ADD>
 constexpr uint32_t kEmbSumSmem =
-    kEmbThreads / 32 * (32 * N * 4 + kEmbFlight<ADD> * (EmbSlice<DT, N, VEC>::kBytes + (ADD ? EmbSlice<WDT, N, VEC>::kBytes : 0)));
+    kEmbThreads / 32 * (32 * N * 4 + kEmbFlight<DT, WDT, ADD> * (EmbSlice<DT, N, VEC>::kBytes + (ADD ? EmbSlice<WDT, N, VEC>::kBytes : 0)));
 
 // A CTA per span of sorted places and slice of the columns, a share of the span to each warp. A warp adds its places'
 // rows up in their order, and writes a token's row where its places end; with ADD dtable's row comes along with the
@@ -635,7 +637,9 @@ __global__ void __launch_bounds__(kEmbThreads, 4) embedding_sum_kernel(const __g
   extern __shared__ __align__(16) uint8_t flight[];
   using From = EmbSlice<DT, N, VEC>;
   using To = EmbSlice<WDT, N, VEC>;
-  constexpr uint32_t kWarps = kEmbThreads / 32, kFlight = kEmbFlight<ADD>, kSlot = From::kBytes + (ADD ? To::kBytes : 0);
+  constexpr uint32_t kWarps = kEmbThreads / 32, kFlight = kEmbFlight<DT, WDT, ADD>, kSlot = From::kBytes + (ADD ? To::kBytes : 0);
+  // 228 KB of an SM, of which each CTA takes 1 KB and its variables of a known size
+  static_assert(4 * (kEmbSumSmem<DT, WDT, N, VEC, ADD> + 1024 + 128) <= 228 * 1024, "4 CTAs to an SM");
   static_assert(kFlight * kSlot >= 32 * N * 4, "the rows' place takes a partial sum when they are through");
   enum { HEAD = 1, HEAD_ENDS = 2, TAIL = 4 };  // places that come from the share before, and end here; that go on
   __shared__ uint32_t left[kWarps], keys_left[kWarps], first_span, last_span;

@@ -847,13 +847,19 @@ def ra_selftest_cross_entropy_timeout(hidden, weight, targets, loss=None, lse=No
     """The cross entropy (the backward pass where dhidden or dweight is given) of dense operands and int64 targets, with waits
     of a millisecond and the part ``withhold`` of its work left out: its waits must give up, and its results be NaN."""
     what = "ra_selftest_cross_entropy_timeout"
-    rows, cols = hidden.shape
-    tensors = [t for t in (hidden, weight, targets, loss, lse, dhidden, dweight, workspace) if t is not None]
-    if workspace is None or not all(t.is_cuda and t.is_contiguous() and t.get_device() == hidden.get_device() for t in tensors):
-        raise ValueError(f"{what}: contiguous CUDA tensors of one device and a workspace are needed")
+    if len(hidden.shape) != 2 or len(weight.shape) != 2:
+        raise ValueError(f"{what}: hidden and weight must be CUDA tensors of two dimensions")
+    code = _float_code(hidden, what)
+    (rows, cols), vocab, device, dtype, f32 = hidden.shape, weight.shape[0], hidden.get_device(), hidden.dtype, _Torch.f32
+    if _Torch.index_bytes.get(targets.dtype) != 8:
+        raise TypeError(f"{what}: targets must be int64, not {targets.dtype}")
+    matrices = dict(hidden=(hidden, rows, dtype), weight=(weight, vocab, dtype), dhidden=(dhidden, rows, dtype), dweight=(dweight, vocab, dtype))
+    _refuse_matrices(what, device, cols, index=("targets", targets, rows), workspace=workspace, **matrices)
+    if not all(t is None or t.is_contiguous() for t, _, _ in matrices.values()):
+        raise ValueError(f"{what}: the matrices must be contiguous")
+    _check_vectors(what, device, loss=(loss, rows, f32), lse=(lse, rows, f32))
     st = lib().ra_selftest_cross_entropy_timeout(
         hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(), _address(loss), _address(lse), _address(dhidden), _address(dweight),
-        rows, cols, weight.shape[0], _float_code(hidden, what), withhold, workspace.data_ptr(), workspace.nbytes,
-        _stream_on(hidden.get_device(), stream, what))
+        rows, cols, vocab, code, withhold, workspace.data_ptr(), workspace.nbytes, _stream_on(device, stream, what))
     if st:
         raise RaError(st, what)

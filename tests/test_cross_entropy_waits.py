@@ -4,6 +4,7 @@ next call is as any other."""
 import pytest
 import torch
 
+from test_binding_devices import OnDevice
 from test_cross_entropy import BF16, F16, I64, check_backward, check_forward, draw_targets, generator, gpu, matrix, ra  # noqa: F401
 
 WITHHELD = {"tiles": 1, "operand": 2, "products": 3, "results": 4}
@@ -67,3 +68,35 @@ def test_refusals(ra):  # noqa: F811
     h = torch.zeros(4, 8, dtype=BF16)
     with pytest.raises(ValueError, match="CUDA"):
         ra.ra_selftest_cross_entropy_timeout(h, h, torch.zeros(4, dtype=I64), workspace=h)
+
+
+def test_binding_refusals(monkeypatch):
+    from ring_all_reduce_02_gb300 import ra as binding
+
+    calls = []
+
+    class Fake:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or 0
+
+    binding._Torch.load()
+    monkeypatch.setattr(binding, "_lib", Fake())
+    monkeypatch.setattr(binding._Torch, "current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(binding._Torch, "current_stream", lambda device: 0)
+
+    def call(h=(4, 8), w=(9, 8), t=4, tdtype=I64, n=4, dh=(4, 8), dw=(9, 8), wdtype=BF16, ws=64, device=0):
+        def on(*shape, dtype=torch.float32, at=0):
+            return OnDevice(at, *shape, dtype=dtype)
+
+        binding.ra_selftest_cross_entropy_timeout(
+            on(*h, dtype=BF16), on(*w, dtype=wdtype, at=device), on(t, dtype=tdtype), on(n), on(n), on(*dh, dtype=BF16), on(*dw, dtype=BF16),
+            workspace=None if ws is None else on(ws))
+
+    call()
+    assert calls == ["ra_selftest_cross_entropy_timeout"]
+    with pytest.raises(TypeError, match="int64"):
+        call(tdtype=torch.int32)
+    for wrong in (dict(h=(4,)), dict(w=(9, 7)), dict(t=3), dict(n=3), dict(dh=(3, 8)), dict(dw=(8, 8)), dict(wdtype=F16), dict(ws=None), dict(device=1)):
+        with pytest.raises(ValueError):
+            call(**wrong)
+    assert len(calls) == 1

@@ -513,7 +513,8 @@ ra_status_t ra_embedding_forward(const void* table, size_t table_stride, const v
  * Its gradient: dtable[v] = scale * sum over the t with tokens[t] == v of dy[t]
  * for every v in [0, vocab) (zero where there is none), with accumulate != 0
  * added to what dtable holds (rows without a token are then not touched).
- * Sums are fp32 in an order that depends on the tokens alone, rounded once.
+ * Sums are fp32, rounded once, in an order that the call's arguments alone
+ * decide (its sizes, tokens and whether it adds), never timing.
  * Tokens equal to `padding` and tokens outside [0, vocab) contribute nothing
  * (a padding outside [0, vocab), such as -1, is none). dy: dtype; dtable:
  * table_dtype (dtype itself or RA_FLOAT32). workspace:
@@ -541,7 +542,8 @@ size_t ra_embedding_workspace(size_t rows, size_t cols, size_t vocab);
  * RA_ERR_UNSUPPORTED). loss, lse: `rows` floats; lse is kept for the backward
  * pass. A row whose target is `ignore` has loss 0 and lse 0, costs no products,
  * and its hidden states are not read as numbers (they may be NaN). Any other
- * target outside [0, vocab) makes its row's loss and lse NaN. No output may overlap
+ * target outside [0, vocab) makes its row's loss and lse NaN, as does a logit
+ * of +infinity or NaN. No output may overlap
  * another buffer. cols == 0, cols above 2^24 and vocab == 0 are
  * RA_ERR_INVALID_ARG (rows == 0 enqueues nothing). workspace: as ra_cross_entropy_workspace says, 16-byte
  * aligned.
@@ -558,9 +560,15 @@ ra_status_t ra_cross_entropy_forward(const void* hidden, size_t hidden_stride, c
  * a time:
  *   dhidden[t] = sum over v of g[t][v] * weight[v],
  *   dweight[v] = sum over t of g[t][v] * hidden[t].
- * g divided by the largest finite |dloss| is rounded to dtype for these
- * products (an error of half a step of dtype relative to each g); sums are
- * fp32, rounded once. targets, ignore, lse: as of the forward pass; rows with
+ * For these products g is rounded to dtype, which the products' operands have
+ * (sums are fp32, rounded once): each g is off by half a step of dtype, 2^-8
+ * of itself at most in bf16 and 2^-11 in fp16, and so is each term of a sum, whether
+ * the sum is stored in 16 bits, where its own rounding hides that, or in an
+ * fp32 dweight, where it does not. g is held relative to the largest finite
+ * |dloss| of the call: bf16 loses nothing by that; fp16 rounds a g below 2^-28
+ * of it to a multiple of 2^-38 of it, so that a row whose dloss is 2^-k of the
+ * largest has k bits less of range for its small probabilities.
+ * targets, ignore, lse: as of the forward pass; rows with
  * target `ignore` have dhidden 0 and add nothing; another target outside
  * [0, vocab) makes dhidden's row and dweight NaN. dloss: `rows` floats (NULL:
  * ones). dhidden: dtype; dweight: dweight_dtype (dtype itself or RA_FLOAT32), with

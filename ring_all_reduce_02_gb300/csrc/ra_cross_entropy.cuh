@@ -376,7 +376,11 @@ __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k,
 }
 
 // g = d (exp(logit - lse) - [target]), d = dloss / scale; zero in words behind the last and in rows behind the counted
-// ones, as far as the products go.
+// ones, as far as the products go. The products' operands have 16 bits, so g is rounded to them, once: half a step of the
+// operands' type of each g, which is what the gradients differ by from those of an fp32 g (3e-4 of their 2-norm at the
+// batch, where bf16's own rounding of them is 2e-3). A second product with what the rounding leaves would double the work of dh
+// and dw for digits that a 16-bit result cannot hold; with an fp32 dweight it is this rounding that bounds the result. One
+// scale for all rows, as dw sums over them: what a row of fp16 has of its range goes by the largest |dloss|.
 template <int DT>
 __device__ __forceinline__ void ce_out_g(const CeTiles& t, const CeWork& k, const CeTile& o, float scale, uint32_t m, uint32_t col,
                                          float (&x)[64], uint8_t* turn) {
@@ -540,8 +544,9 @@ struct CeTurns {
   uint64_t full[kCeRing], empty[kCeRing];
 };
 
-// CHUNKS: dw's rows are whole 16-byte chunks. The two ways to store it are kernels of their own: in one, registers run out (61 x
-// 1024 x 50257 bf16 85 us a call against 79, 1537 x 768 x 10007 fp16 added 74 against 69).
+// CHUNKS: dw's rows are whole 16-byte chunks. The two ways to store it are kernels of their own, so that 16-bit chunks need no
+// register more than there are (61 x 1024 x 50257 bf16 85 us a call by one kernel for both, 79 so; 1537 x 768 x 10007 fp16 added
+// 74 and 67). The other three still spill: an fp32 dw in chunks 64 bytes a thread, dw off the grid 70 of either type.
 template <int DT, int WDT, bool BACKWARD, bool CHUNKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) ce_tiles_kernel(const __grid_constant__ CeTiles t) {
   extern __shared__ uint8_t dynamic[];

@@ -38,7 +38,7 @@ inline CePlan ce_plan(uint64_t rows, uint64_t cols, uint64_t vocab, bool packed,
   if (p.part_rows == 0) p.part_rows = 8;
   p.parts = rows ? (rows + p.part_rows - 1) / p.part_rows : 1;
   // Pieces of about one size, so that no launch is a small one. With few rows all words are one piece, although they are read
-  // a second time from HBM then: pieces whose words stay in L2 (61 x 1024 x 50257 bf16: 2 pieces 105 us a call, 4 132, one 85)
+  // a second time from HBM then: pieces whose words stay in L2 (61 x 1024 x 50257 bf16: 2 pieces 97 us a call, 4 121, one 79)
   // pay more for their launches' ends.
   uint64_t most = kCePieceBytes / (2 * p.rows_pad) / kCeTile;
   if (most < kCeLeastPiece / kCeTile) most = kCeLeastPiece / kCeTile;

@@ -32,8 +32,11 @@ __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-// An arrival at a barrier of either CTA of a pair that only says that something has been read. (One with release of the
-// cluster's scope waits for the thread's stores to global memory, half a microsecond and more.)
+// An arrival at a barrier of either CTA of a pair that only says that something has been read. It is relaxed, and by itself
+// would not stay behind a read of shared memory that has been issued but not answered. What has been read has to have reached
+// registers, in all lanes whose reading it speaks for: a tile's words have gone through shuffles of the whole warp by then
+// (which take the values, not the addresses), and accumulators are waited for by tcgen05.wait::ld and handed over by a tcgen05
+// fence. (One with release of the cluster's scope waits for the thread's stores to global memory, half a microsecond and more.)
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -378,7 +378,7 @@ __device__ __forceinline__ void ce_out_logits(const CeTiles& t, const CeWork& k,
 // g = d (exp(logit - lse) - [target]), d = dloss / scale; zero in words behind the last and in rows behind the counted
 // ones, as far as the products go. The products' operands have 16 bits, so g is rounded to them, once: half a step of the
 // operands' type of each g, which is what the gradients differ by from those of an fp32 g (3e-4 of their 2-norm at the
-// batch, where bf16's own rounding of them is 2e-3). A second product with what the rounding leaves would double the work of dh
+// batch, where bf16's own rounding of them is 1.7e-3). A second product with what the rounding leaves would double the work of dh
 // and dw for digits that a 16-bit result cannot hold; with an fp32 dweight it is this rounding that bounds the result. One
 // scale for all rows, as dw sums over them: what a row of fp16 has of its range goes by the largest |dloss|.
 template <int DT>

@@ -629,7 +629,7 @@ constexpr uint32_t kEmbSumSmem =
 // token's last place. Places that reach over the end of a warp's share are joined by the warp in whose share they start,
 // and those that reach over the span's ends by the last CTA that has some of them. Spans of sorted places, not a CTA per
 // token: text has tokens that come up in a tenth of all places, which would be one CTA's work (8192 x 1024 bf16 14106 us a
-// call by the thread that owns a token's column, 18 by spans). 32768 x 8192 bf16: 125 us, 661 MB at 5.3 TB/s, HBM; 8192 x
+// call by the thread that owns a token's column, 18 by spans). 32768 x 8192 bf16: 121 us, 661 MB at 5.5 TB/s, HBM; 8192 x
 // 1024 added: 10 us for 50 MB, a chain of keys, rows and two joins with 30% of the warps an SM holds.
 template <int DT, int WDT, int N, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kEmbThreads, 4) embedding_sum_kernel(const __grid_constant__ EmbBackward a, const uint32_t* keys, const uint32_t* places) {

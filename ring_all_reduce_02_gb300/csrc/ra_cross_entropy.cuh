@@ -87,7 +87,9 @@ __device__ __forceinline__ void ce_copy_row(void* to, const void* from, uint64_t
   }
 }
 
-// Numbers the rows that count in their order. Every CTA has part_rows rows and counts those before them itself.
+// Numbers the rows that count in their order. Every CTA has part_rows rows and counts those before them itself: there are 1216
+// CTAs at most, so that this grows with the rows alone (a loss of which no row counts, 2^17 x 64 53 us, 2^20 474, 2^22 1930; at
+// 1024 columns and 50257 words 2^20 rows' products take over 60 ms).
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kCeRowsThreads) ce_rows_kernel(const __grid_constant__ CeArgs a) {
   pdl_enter();
